@@ -275,6 +275,137 @@ ssm_status ssm_conv1d_update(int64_t batch, int64_t dim, int64_t width, int32_t 
                              void* conv_state, const void* x, const float* weight,
                              const float* bias, void* u, struct ihipStream_t* stream);
 
+/* ------------------------------------------------------------------ training operators
+ *
+ * What a training step needs next to the scan and its gradients: the gradients of the conv,
+ * the embedding of the tokens with its gradient, and the optimizer.  Conventions as above:
+ * device pointers, 16-byte aligned bases, host-side checks before any launch, asynchronous on
+ * `stream`, no allocation, fixed-order sums (bitwise reproducible). */
+
+/* Bytes of device workspace ssm_conv1d_bwd needs (0 for invalid sizes): one partial sum of
+ * dweight and dbias per row and segment of the sequence. */
+size_t ssm_conv1d_bwd_workspace_size(int64_t batch, int64_t dim, int64_t seqlen, int64_t width,
+                                     int32_t io_dtype);
+
+/* Gradients of ssm_conv1d_fwd, from its inputs alone.  With a the pre-activation,
+ * g = dout * silu'(a), H = width - 1 and x extended to the left by the initial state:
+ *   dx[b,d,t]    = sum_k weight[d,k] * g[b,d,t+H-k]   (g is zero past the last step)
+ *   dweight[d,k] = sum_{b,t} g[b,d,t] * x[b,d,t-H+k];   dbias[d] = sum_{b,t} g[b,d,t]
+ * and the gradient of the initial state is dx's formula at the steps before 0.
+ *   x, dout, dx               : [B, D, L] io_dtype
+ *   weight, dweight           : [D, width] fp32;  bias (NULL means zero), dbias : [D] fp32
+ *   initial_conv_state        : [B, D, H] io_dtype, NULL means zeros
+ *   dfinal_conv_state         : [B, D, H] io_dtype gradient of final_conv_state, NULL means zero
+ *   dinitial_conv_state       : [B, D, H] io_dtype, NULL means not written
+ *   dbias                     : NULL means not computed (written even when bias is NULL)
+ *   workspace                 : required, at least ssm_conv1d_bwd_workspace_size() bytes
+ * width in [1, 4]; with width 1 the state pointers are ignored.  No output may overlap an
+ * input, another output or the workspace. */
+ssm_status ssm_conv1d_bwd(int64_t batch, int64_t dim, int64_t seqlen, int64_t width, int32_t io_dtype,
+                          const void* x, const float* weight, const float* bias,
+                          const void* initial_conv_state, const void* dout,
+                          const void* dfinal_conv_state, void* dx, float* dweight, float* dbias,
+                          void* dinitial_conv_state, void* workspace, size_t workspace_bytes,
+                          struct ihipStream_t* stream);
+
+typedef enum ssm_index_dtype { SSM_I32 = 0, SSM_I64 = 1 } ssm_index_dtype;
+
+/* flag bits for ssm_embed_shape.flags */
+#define SSM_FLAG_CHANNELS_FIRST 1u /* out and dout are [B, E, L], the layout of the conv and the scan */
+#define SSM_FLAG_ACCUMULATE 2u     /* the gradient is added to dweight, whose other rows stay untouched */
+
+typedef struct ssm_embed_shape {
+  int64_t batch;        /* B >= 1 */
+  int64_t seqlen;       /* L >= 1; B * L below 2^31 */
+  int64_t rows;         /* V >= 1, below 2^31 - 1: rows of the table */
+  int64_t dim;          /* E >= 1 */
+  int32_t index_dtype;  /* ssm_index_dtype of tokens */
+  int32_t table_dtype;  /* ssm_dtype of weight (forward) or dweight (backward) */
+  int32_t io_dtype;     /* ssm_dtype of out or dout */
+  uint32_t flags;       /* SSM_FLAG_CHANNELS_FIRST; backward: SSM_FLAG_ACCUMULATE */
+} ssm_embed_shape;
+
+/* Embedding: out[b,t,:] = scale * weight[tokens[b,t],:], rounded once to io_dtype.
+ *   tokens : [B, L];  weight : [V, E];  out : [B, L, E], or [B, E, L] with SSM_FLAG_CHANNELS_FIRST
+ * A token outside [0, V) (a padding mark such as -1) gives zeros. */
+ssm_status ssm_embedding_fwd(const ssm_embed_shape* shape, const void* tokens, const void* weight,
+                             float scale, void* out, struct ihipStream_t* stream);
+
+/* Bytes of device workspace ssm_embedding_bwd needs for this shape (0 for an invalid one). */
+size_t ssm_embedding_bwd_workspace_size(const ssm_embed_shape* shape);
+
+/* Gradient of ssm_embedding_fwd: dweight[v,:] = scale * sum of dout over the positions whose
+ * token is v.  The positions are sorted by token (equal tokens in order of position) and each
+ * token's rows are summed in fp32 in a fixed order.  Tokens outside [0, V) take no part.
+ *   dout    : [B, L, E] or [B, E, L], io_dtype
+ *   dweight : [V, E] table_dtype, fully written (zeros for tokens that do not occur), or with
+ *             SSM_FLAG_ACCUMULATE added to: then only the rows of tokens that occur are touched
+ *   workspace : required, at least ssm_embedding_bwd_workspace_size() bytes */
+ssm_status ssm_embedding_bwd(const ssm_embed_shape* shape, const void* tokens, const void* dout,
+                             float scale, void* dweight, void* workspace, size_t workspace_bytes,
+                             struct ihipStream_t* stream);
+
+/* One parameter tensor of an optimizer step (dense, any shape). */
+typedef struct ssm_adamw_tensor {
+  void* param;          /* read and written */
+  const void* grad;
+  int64_t numel;        /* >= 1 */
+  int64_t offset;       /* where its states begin in the state buffers, in elements: a multiple of
+                           SSM_ADAMW_BLOCK; they take numel rounded up to whole blocks, and the
+                           next tensor's begin behind them */
+  int32_t param_dtype;  /* ssm_dtype */
+  int32_t grad_dtype;   /* ssm_dtype */
+} ssm_adamw_tensor;
+
+#define SSM_ADAMW_BLOCK 128 /* elements that share a base of the 8-bit states */
+
+typedef struct ssm_adamw_config {
+  double lr, beta1, beta2, eps, weight_decay; /* finite; betas in [0, 1); eps in [1e-30, 1e30] */
+  int64_t step;        /* number of this step, from 1 */
+  uint64_t seed;       /* of the stochastic rounding */
+  int32_t state_bits;  /* 32: fp32 states; 8: one byte per element and one base per block */
+  uint32_t flags;      /* 0 */
+} ssm_adamw_config;
+
+/* Norm of all gradients together and the factor that clips it to max_norm:
+ *   result[0] = sqrt(sum of squares) (summed in fp64, in a fixed order; fp32)
+ *   result[1] = max_norm / norm where norm > max_norm, else 1; NaN where the norm is not finite
+ * tensors is a host array of `count` descriptors (only grad, numel and grad_dtype are read); it is
+ * not needed after the call returns.  result: 2 floats on the device.  workspace: required, at
+ * least ssm_grad_norm_workspace_size() bytes. */
+size_t ssm_grad_norm_workspace_size(const ssm_adamw_tensor* tensors, int64_t count);
+ssm_status ssm_grad_norm(const ssm_adamw_tensor* tensors, int64_t count, double max_norm, float* result,
+                         void* workspace, size_t workspace_bytes, struct ihipStream_t* stream);
+
+/* One AdamW step over all tensors (decoupled weight decay, bias-corrected moments):
+ *   g = clip * grad;  m = beta1 m + (1 - beta1) g;  v = beta2 v + (1 - beta2) g g
+ *   p = p (1 - lr weight_decay) - lr / (1 - beta1^step) * m / (sqrt(v / (1 - beta2^step)) + eps)
+ * in fp32.  tensors: a host array, not needed after the call returns; params must not overlap one
+ * another, the gradients or the states.
+ *   exp_avg, exp_avg_sq : m and v of all tensors, tensor k's at its offset: fp32 (state_bits 32) or
+ *       codes of one byte (state_bits 8).  8-bit: with the bits of a positive fp32 number read as an
+ *       integer, an element of code c >= 1 in a block of base K stands for the number whose bits are
+ *       (c + K) << 20 (a sign bit, 8 exponent bits and 3 mantissa bits); code 0 stands for zero.  m has a
+ *       sign in bit 7 and c in bits 0-6, v has c in 8 bits.  A block's base puts its largest
+ *       element at the largest code, the others are rounded stochastically, and a v that is not zero
+ *       is not rounded to zero.
+ *   exp_avg_base, exp_avg_sq_base : the blocks' K, int16, element offset / 128 onwards; 8-bit only
+ *   master : fp32 weights of all bf16 tensors at their offsets (the step works on these and writes
+ *       their rounded values to param), or NULL: then a bf16 param is itself rounded stochastically.
+ *       Not used for fp32 tensors.
+ *   clip : result of ssm_grad_norm on the device, or NULL for no clipping.  Where result[1] is
+ *       NaN the step changes nothing.
+ * The random numbers are a hash of (seed, step, index of the tensor, index of the element). */
+ssm_status ssm_adamw_step(const ssm_adamw_config* config, const ssm_adamw_tensor* tensors, int64_t count,
+                          void* exp_avg, void* exp_avg_sq, int16_t* exp_avg_base, int16_t* exp_avg_sq_base,
+                          float* master, const float* clip, struct ihipStream_t* stream);
+
+/* The values that 8-bit states stand for, exactly, in bf16: `numel` codes (a multiple of
+ * SSM_ADAMW_BLOCK), numel / 128 bases each.  m_values and v_values : [numel] bf16; NULL means not wanted. */
+ssm_status ssm_adamw_state_values(int64_t numel, const void* exp_avg, const void* exp_avg_sq,
+                                  const int16_t* exp_avg_base, const int16_t* exp_avg_sq_base,
+                                  void* m_values, void* v_values, struct ihipStream_t* stream);
+
 #ifdef __cplusplus
 }
 #endif

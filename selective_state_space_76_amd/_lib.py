@@ -35,11 +35,26 @@ class ssm_shape(ctypes.Structure):
                 ("seqlen", ctypes.c_int64), ("io_dtype", ctypes.c_int32), ("flags", ctypes.c_uint32)]
 
 
+class ssm_embed_shape(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int64), ("seqlen", ctypes.c_int64), ("rows", ctypes.c_int64),
+                ("dim", ctypes.c_int64), ("index_dtype", ctypes.c_int32), ("table_dtype", ctypes.c_int32),
+                ("io_dtype", ctypes.c_int32), ("flags", ctypes.c_uint32)]
+
+
+class ssm_adamw_config(ctypes.Structure):
+    _fields_ = [("lr", ctypes.c_double), ("beta1", ctypes.c_double), ("beta2", ctypes.c_double),
+                ("eps", ctypes.c_double), ("weight_decay", ctypes.c_double), ("step", ctypes.c_int64),
+                ("seed", ctypes.c_uint64), ("state_bits", ctypes.c_int32), ("flags", ctypes.c_uint32)]
+
+
 _lib = None
 EXPORTS = ("ssm_abi_version", "ssm_status_str", "ssm_scan_workspace_size", "ssm_scan_fwd", "ssm_scan_fwd_save",
            "ssm_scan_fwd_noalloc",
            "ssm_state_update", "ssm_scan_bwd_workspace_size", "ssm_scan_bwd", "ssm_scan_bwd_saved_workspace_size",
-           "ssm_scan_bwd_saved", "ssm_conv1d_fwd", "ssm_conv1d_update")
+           "ssm_scan_bwd_saved", "ssm_conv1d_fwd", "ssm_conv1d_update",
+           "ssm_conv1d_bwd_workspace_size", "ssm_conv1d_bwd", "ssm_embedding_fwd", "ssm_embedding_bwd_workspace_size",
+           "ssm_embedding_bwd", "ssm_grad_norm_workspace_size", "ssm_grad_norm", "ssm_adamw_step",
+           "ssm_adamw_state_values")
 
 
 def load() -> ctypes.CDLL:
@@ -78,6 +93,25 @@ def load() -> ctypes.CDLL:
     lib.ssm_conv1d_fwd.restype = ctypes.c_int
     lib.ssm_conv1d_update.argtypes = [i64, i64, i64, i32] + [vp] * 5 + [vp]
     lib.ssm_conv1d_update.restype = ctypes.c_int
+    lib.ssm_conv1d_bwd_workspace_size.argtypes = [i64, i64, i64, i64, i32]
+    lib.ssm_conv1d_bwd_workspace_size.restype = ctypes.c_size_t
+    lib.ssm_conv1d_bwd.argtypes = [i64, i64, i64, i64, i32] + [vp] * 11 + [ctypes.c_size_t, vp]
+    lib.ssm_conv1d_bwd.restype = ctypes.c_int
+    lib.ssm_embedding_fwd.argtypes = [ctypes.POINTER(ssm_embed_shape), vp, vp, ctypes.c_float, vp, vp]
+    lib.ssm_embedding_fwd.restype = ctypes.c_int
+    lib.ssm_embedding_bwd_workspace_size.argtypes = [ctypes.POINTER(ssm_embed_shape)]
+    lib.ssm_embedding_bwd_workspace_size.restype = ctypes.c_size_t
+    lib.ssm_embedding_bwd.argtypes = [ctypes.POINTER(ssm_embed_shape), vp, vp, ctypes.c_float, vp, vp,
+                                      ctypes.c_size_t, vp]
+    lib.ssm_embedding_bwd.restype = ctypes.c_int
+    lib.ssm_grad_norm_workspace_size.argtypes = [vp, i64]
+    lib.ssm_grad_norm_workspace_size.restype = ctypes.c_size_t
+    lib.ssm_grad_norm.argtypes = [vp, i64, ctypes.c_double, vp, vp, ctypes.c_size_t, vp]
+    lib.ssm_grad_norm.restype = ctypes.c_int
+    lib.ssm_adamw_step.argtypes = [ctypes.POINTER(ssm_adamw_config), vp, i64] + [vp] * 7
+    lib.ssm_adamw_step.restype = ctypes.c_int
+    lib.ssm_adamw_state_values.argtypes = [i64] + [vp] * 7
+    lib.ssm_adamw_state_values.restype = ctypes.c_int
     if lib.ssm_abi_version() != ABI_VERSION:
         raise ImportError("libssmscan.so ABI version %d, binding expects %d" % (lib.ssm_abi_version(), ABI_VERSION))
     _lib = lib

@@ -1,4 +1,4 @@
-"""torch.autograd binding of the scan: forward through ssm_scan_fwd_save (the outputs plus the block
+"""torch.autograd binding of the scan, the conv and the embedding.  The scan: forward through ssm_scan_fwd_save (the outputs plus the block
 checkpoints), backward through ssm_scan_bwd_saved.
 
     from selective_state_space_76_amd import selective_scan
@@ -15,7 +15,8 @@ from __future__ import annotations
 
 import torch
 
-from ._lib import checkpoints_shape, scan_bwd, scan_fwd
+from ._lib import checkpoints_shape, conv1d_fwd, scan_bwd, scan_fwd
+from .training import conv1d_bwd, embedding_bwd, embedding_fwd
 
 
 class SelectiveScanFn(torch.autograd.Function):
@@ -55,3 +56,48 @@ def selective_scan(u, delta, A, B, C, D=None, z=None, delta_bias=None, initial_s
     """Differentiable selective scan.  Same arguments and layouts as scan_fwd; returns
     (out [B,D,L] in u's dtype, final_state [B,D,N] fp32)."""
     return SelectiveScanFn.apply(u, delta, A, B, C, D, z, delta_bias, initial_state, zoh, reverse)
+
+
+class CausalConv1dFn(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, weight, bias, initial_state):
+        u, final_state = conv1d_fwd(x, weight, bias, initial_state)
+        ctx.save_for_backward(x, weight, bias, initial_state)
+        return u, final_state
+
+    @staticmethod
+    def backward(ctx, dout, dfinal):
+        x, weight, bias, initial_state = ctx.saved_tensors
+        dout = torch.zeros_like(x) if dout is None else dout.to(x.dtype).contiguous()
+        dfinal = None if dfinal is None else dfinal.to(x.dtype).contiguous()
+        g = conv1d_bwd(x, weight, bias, initial_state, dout=dout, dfinal_state=dfinal)
+        need = ctx.needs_input_grad
+        return (g["dx"] if need[0] else None, g["dweight"] if need[1] else None,
+                g["dbias"] if need[2] and bias is not None else None,
+                g["dinitial_state"] if need[3] and initial_state is not None else None)
+
+
+def causal_conv1d(x, weight, bias=None, initial_state=None):
+    """Differentiable conv1d_fwd: (u [B,D,L], final_state [B,D,K-1]), with gradients of x, weight, bias and
+    initial_state through conv1d_bwd."""
+    return CausalConv1dFn.apply(x, weight, bias, initial_state)
+
+
+class EmbeddingFn(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, tokens, weight, scale, dtype, channels_first):
+        ctx.save_for_backward(tokens)
+        ctx.table = (weight.shape[0], weight.dtype, scale, channels_first)
+        return embedding_fwd(tokens, weight, scale=scale, dtype=dtype, channels_first=channels_first)
+
+    @staticmethod
+    def backward(ctx, dout):
+        (tokens,) = ctx.saved_tensors
+        rows, dtype, scale, channels_first = ctx.table
+        dw = embedding_bwd(tokens, dout.contiguous(), rows, scale=scale, channels_first=channels_first, dtype=dtype)
+        return None, dw, None, None, None
+
+
+def embedding(tokens, weight, *, scale=1.0, dtype=None, channels_first=False):
+    """Differentiable embedding_fwd; the gradient comes in weight's dtype, summed in fp32 and rounded once."""
+    return EmbeddingFn.apply(tokens, weight, scale, dtype, channels_first)

@@ -1,0 +1,384 @@
+// adamw.hip -- one AdamW step over many tensors, the gradients' norm, and the 8-bit states.
+//
+//   g = clip * grad;  m = b1 m + (1 - b1) g;  v = b2 v + (1 - b2) g g
+//   p = p (1 - lr wd) - lr / (1 - b1^t) * m / (sqrt(v) / sqrt(1 - b2^t) + eps)
+//
+// Layout: a launch covers up to kAdamTensors tensors whose addresses travel in the kernel arguments (no
+// table in memory to fill, keep or wait for).  A workgroup owns one chunk of kAdamChunk elements of one
+// tensor, found by bisection over the first workgroup of each tensor; a lane owns V consecutive elements
+// (4 with fp32 states, 8 with 8-bit ones, so that every stream is read in 8- or 16-byte pieces).
+// The step is bound by HBM: every byte of weights, gradients and states is touched once.
+//
+// 8-bit states.  A positive float's bit pattern is an increasing integer, and its top 12 bits a number
+// of 4 significant bits.  A block of 128 elements (16 lanes of 8) keeps K, the largest element's top
+// bits (rounded up) less the largest code, and an element the code c with (c + K) << 20 its bits; c = 0 is
+// zero.  The scale of a code is thus its own exponent: 7 bits span 16 octaves (m, with a sign), 8 bits 32
+// (v).  With b2 = 0.999 an average moves by a thousandth per step, a code by a sixteenth to an
+// eighth, so rounding to nearest would never let it move; adding 16 random bits below the kept ones
+// rounds up with the odds of the part cut off, which keeps the expected state exact.  A v > 0 is
+// never rounded to zero: a zero under a nonzero m would divide by eps alone.  m below its smallest code
+// becomes that code with the odds that keep its mean, else zero.
+#include "../ssm_device.h"
+#include "train_launch.h"
+
+namespace ssm {
+
+namespace {
+
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+
+// 32 bits mixed by xor-shifts and products with the fractions of sqrt(2) and sqrt(3)
+__host__ __device__ __forceinline__ uint32_t mix32(uint32_t x) {
+  x ^= x >> 16;
+  x *= 0x6A09E667u;
+  x ^= x >> 15;
+  x *= 0xBB67AE85u;
+  return x ^ (x >> 16);
+}
+
+// V consecutive floats or bf16 numbers as floats; c of them are there, the others read as zero
+template <int V>
+__device__ __forceinline__ void load(const float* p, int c, float (&x)[V]) {
+  if (c == V) {
+#pragma unroll
+    for (int i = 0; i < V; i += 4) {
+      const f32x4 q = __builtin_nontemporal_load(reinterpret_cast<const f32x4*>(p + i));
+#pragma unroll
+      for (int e = 0; e < 4; ++e) x[i + e] = q[e];
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i) x[i] = i < c ? p[i] : 0.0f;
+  }
+}
+template <int V>
+__device__ __forceinline__ void load(const bf16_t* p, int c, float (&x)[V]) {
+  if (c == V) {
+    uint32_t w[V / 2];
+    if constexpr (V == 8) {
+      const u32x4 q = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(p));
+#pragma unroll
+      for (int i = 0; i < 4; ++i) w[i] = q[i];
+    } else {
+      const u32x2 q = __builtin_nontemporal_load(reinterpret_cast<const u32x2*>(p));
+      w[0] = q[0]; w[1] = q[1];
+    }
+#pragma unroll
+    for (int i = 0; i < V / 2; ++i) {
+      x[2 * i] = __uint_as_float(w[i] << 16);
+      x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i) x[i] = i < c ? to_f32(p[i]) : 0.0f;
+  }
+}
+template <int V>
+__device__ __forceinline__ void store(float* p, int c, const float (&x)[V]) {
+  if (c == V) {
+#pragma unroll
+    for (int i = 0; i < V; i += 4)
+      __builtin_nontemporal_store(f32x4{x[i], x[i + 1], x[i + 2], x[i + 3]}, reinterpret_cast<f32x4*>(p + i));
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+      if (i < c) p[i] = x[i];
+  }
+}
+// the upper halves of V words
+template <int V>
+__device__ __forceinline__ void store_high(bf16_t* p, int c, const uint32_t (&x)[V]) {
+  if (c == V) {
+    uint32_t w[V / 2];
+#pragma unroll
+    for (int i = 0; i < V / 2; ++i) w[i] = (x[2 * i] >> 16) | (x[2 * i + 1] & 0xffff0000u);
+    if constexpr (V == 8)
+      __builtin_nontemporal_store(u32x4{w[0], w[1], w[2], w[3]}, reinterpret_cast<u32x4*>(p));
+    else
+      __builtin_nontemporal_store(u32x2{w[0], w[1]}, reinterpret_cast<u32x2*>(p));
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+      if (i < c) p[i] = (bf16_t)(x[i] >> 16);
+  }
+}
+__device__ __forceinline__ void load_codes(const uint8_t* p, int c, uint32_t (&x)[8]) {
+  if (c > 0) {  // a block's room is there even where its tensor ends inside it
+    const u32x2 q = __builtin_nontemporal_load(reinterpret_cast<const u32x2*>(p));
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = i < c ? (q[i >> 2] >> (8 * (i & 3))) & 255u : 0u;
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = 0u;
+  }
+}
+__device__ __forceinline__ void store_codes(uint8_t* p, int c, const uint32_t (&x)[8]) {
+  if (c > 0) {  // codes past the tensor's end are zero
+    u32x2 q = {0u, 0u};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) q[i >> 2] |= x[i] << (8 * (i & 3));
+    __builtin_nontemporal_store(q, reinterpret_cast<u32x2*>(p));
+  }
+}
+
+// largest of a 16-lane row, in every lane of it
+__device__ __forceinline__ uint32_t row_max(uint32_t v) {
+  auto step = [&](auto ctrl) {
+    const uint32_t o = (uint32_t)__builtin_amdgcn_mov_dpp((int)v, decltype(ctrl)::value, 0xf, 0xf, true);
+    v = v > o ? v : o;
+  };
+  step(IC<0x128>{});  // row_ror:8
+  step(IC<0x124>{});
+  step(IC<0x122>{});
+  step(IC<0x121>{});
+  return v;
+}
+
+// the tensor that workgroup `block` works on
+__device__ __forceinline__ int find(const AdamTable& t, uint32_t block) {
+  int lo = 0, hi = t.count - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (t.first[mid] <= block) lo = mid;
+    else hi = mid - 1;
+  }
+  return lo;
+}
+
+__device__ __forceinline__ float code_value(uint32_t c, uint32_t K) { return __uint_as_float(c ? (c + K) << 20 : 0u); }
+
+// base of a block from the bits of its largest magnitude: that element, rounded up, gets code `top`
+__device__ __forceinline__ uint32_t block_base(uint32_t amax, uint32_t top) {
+  const uint32_t q = (amax + 0xfffffu) >> 20;
+  return q > top ? q - top : 0u;
+}
+
+}  // namespace
+
+template <bool PB, bool GB, bool MW, bool S8>
+__global__ __launch_bounds__(256) void adamw_kernel(AdamTable t, AdamParams a) {
+#pragma clang fp contract(off)  // every product and sum of the states rounds once: the codes depend on their bits
+  constexpr int V = S8 ? 8 : 4;
+  float clip = 1.0f;
+  if (a.clip) {
+    clip = a.clip[1];
+    if (clip != clip) return;  // the gradients' norm is not finite: nothing changes
+  }
+  const int k = find(t, blockIdx.x);
+  const int64_t n = t.n[k], off = t.off[k];
+  const int64_t base = (int64_t)(blockIdx.x - t.first[k]) * kAdamChunk;
+  const uint32_t key = t.key[k];
+  const int lane0 = (threadIdx.x & ~63) * V;
+#pragma unroll 1
+  for (int it = 0; it < kAdamChunk / (256 * V); ++it) {
+    const int64_t w0 = base + it * (256 * V) + lane0;  // the wave's first element
+    if (w0 >= n) break;
+    const int64_t i = w0 + (threadIdx.x & 63) * V;
+    const int64_t left = n - i;
+    const int c = left >= V ? V : left > 0 ? (int)left : 0;
+    float p[V], g[V], m[V], v[V];
+    if constexpr (GB) load<V>(static_cast<const bf16_t*>(t.g[k]) + i, c, g);
+    else load<V>(static_cast<const float*>(t.g[k]) + i, c, g);
+    if constexpr (MW) load<V>(a.master + off + i, c, p);
+    else if constexpr (PB) load<V>(static_cast<const bf16_t*>(t.p[k]) + i, c, p);
+    else load<V>(static_cast<const float*>(t.p[k]) + i, c, p);
+    const int64_t blk = (off + i) / kAdamBlock;
+    if constexpr (S8) {
+      uint32_t mc[8], vc[8], mk = 0, vk = 0;
+      load_codes(static_cast<const uint8_t*>(a.m) + off + i, c, mc);
+      load_codes(static_cast<const uint8_t*>(a.v) + off + i, c, vc);
+      if (c > 0) {
+        mk = (uint32_t)(int32_t)a.mb[blk];
+        vk = (uint32_t)(int32_t)a.vb[blk];
+      }
+#pragma unroll
+      for (int e = 0; e < V; ++e) {
+        const float x = code_value(mc[e] & 127u, mk);
+        m[e] = mc[e] & 128u ? -x : x;
+        v[e] = code_value(vc[e], vk);
+      }
+    } else {
+      load<V>(static_cast<const float*>(a.m) + off + i, c, m);
+      load<V>(static_cast<const float*>(a.v) + off + i, c, v);
+    }
+    uint32_t h[V];
+    if constexpr (S8 || (PB && !MW)) {
+#pragma unroll
+      for (int e = 0; e < V; ++e) h[e] = mix32(((uint32_t)i + e) * 0x9E3779B9u + key);
+    }
+    uint32_t pb[V];
+#pragma unroll
+    for (int e = 0; e < V; ++e) {
+      const float ge = g[e] * clip;
+      m[e] = m[e] * a.b1 + ge * a.c1;
+      v[e] = v[e] * a.b2 + ge * a.c2 * ge;
+      const float den = __builtin_amdgcn_sqrtf(v[e]) * a.isb + a.eps;
+      p[e] = p[e] * a.decay - m[e] * a.step * rcp_(den);
+      if constexpr (PB) {
+        if constexpr (MW) {
+          pb[e] = (uint32_t)__builtin_bit_cast(uint16_t, (__bf16)p[e]) << 16;
+        } else {
+          const uint32_t b = __float_as_uint(p[e]);
+          const bool finite = (b & 0x7f800000u) != 0x7f800000u;
+          pb[e] = finite ? b + ((h[e] * 0x3C6EF373u) >> 16) : b | (b & 0xffffu ? 0x10000u : 0u);
+        }
+      }
+    }
+    if constexpr (MW) store<V>(a.master + off + i, c, p);
+    if constexpr (PB) store_high<V>(static_cast<bf16_t*>(t.p[k]) + i, c, pb);
+    else store<V>(static_cast<float*>(t.p[k]) + i, c, p);
+    if constexpr (S8) {
+      uint32_t am = 0, av = 0;
+#pragma unroll
+      for (int e = 0; e < V; ++e) {
+        const uint32_t x = e < c ? __float_as_uint(m[e]) & 0x7fffffffu : 0u, y = e < c ? __float_as_uint(v[e]) : 0u;
+        am = am > x ? am : x;
+        av = av > y ? av : y;
+      }
+      const uint32_t mk = block_base(row_max(am), 127u), vk = block_base(row_max(av), 255u);
+      const uint32_t least = (mk + 1) << 20;
+      uint32_t mc[8], vc[8];
+#pragma unroll
+      for (int e = 0; e < V; ++e) {
+        const uint32_t x = __float_as_uint(m[e]) & 0x7fffffffu, rm = h[e] & 0xffffu;
+        const uint32_t q = ((x + (rm << 4) + 8u) >> 20) - mk;
+        const bool up = __uint_as_float(x) > __uint_as_float(least) * ((float)rm * 0x1p-16f + 0x1p-17f);
+        mc[e] = (x < least ? (uint32_t)up : q < 127u ? q : 127u) | (m[e] < 0.0f ? 128u : 0u);
+        const uint32_t y = __float_as_uint(v[e]), rv = h[e] >> 16;
+        const int32_t r = (int32_t)((y + (rv << 4) + 8u) >> 20) - (int32_t)vk;
+        vc[e] = y == 0u ? 0u : (uint32_t)(r < 1 ? 1 : r > 255 ? 255 : r);
+        if (e >= c) mc[e] = vc[e] = 0u;
+      }
+      store_codes(static_cast<uint8_t*>(a.m) + off + i, c, mc);
+      store_codes(static_cast<uint8_t*>(a.v) + off + i, c, vc);
+      if (c > 0 && (threadIdx.x & 15) == 0) {
+        a.mb[blk] = (int16_t)mk;
+        a.vb[blk] = (int16_t)vk;
+      }
+    } else {
+      store<V>(static_cast<float*>(a.m) + off + i, c, m);
+      store<V>(static_cast<float*>(a.v) + off + i, c, v);
+    }
+  }
+}
+
+// Sum of the squares of one chunk, in fp64 (no overflow below fp32's largest squares, and no loss over
+// many elements); the workgroup's 256 lanes are added in a fixed tree.
+template <bool GB>
+__global__ __launch_bounds__(256) void norm_part_kernel(AdamTable t, double* part) {
+  constexpr int V = GB ? 8 : 4;
+  const int k = find(t, blockIdx.x);
+  const int64_t n = t.n[k];
+  const int64_t base = (int64_t)(blockIdx.x - t.first[k]) * kNormChunk;
+  double s = 0.0;
+#pragma unroll 4
+  for (int it = 0; it < kNormChunk / (256 * V); ++it) {
+    const int64_t i = base + it * (256 * V) + threadIdx.x * V;
+    const int64_t left = n - i;
+    const int c = left >= V ? V : left > 0 ? (int)left : 0;
+    float g[V];
+    if constexpr (GB) load<V>(static_cast<const bf16_t*>(t.g[k]) + i, c, g);
+    else load<V>(static_cast<const float*>(t.g[k]) + i, c, g);
+#pragma unroll
+    for (int e = 0; e < V; ++e) s = __builtin_fma((double)g[e], (double)g[e], s);
+  }
+  __shared__ double sm[256];
+  sm[threadIdx.x] = s;
+  __syncthreads();
+#pragma unroll
+  for (int h = 128; h > 0; h >>= 1) {
+    if ((int)threadIdx.x < h) sm[threadIdx.x] += sm[threadIdx.x + h];
+    __syncthreads();
+  }
+  if (threadIdx.x == 0) part[blockIdx.x] = sm[0];
+}
+
+__global__ __launch_bounds__(1024) void norm_join_kernel(const double* part, int64_t n, double max_norm, float* result) {
+  __shared__ double sm[1024];
+  double s = 0.0;
+  for (int64_t i = threadIdx.x; i < n; i += 1024) s += part[i];
+  sm[threadIdx.x] = s;
+  __syncthreads();
+  for (int h = 512; h > 0; h >>= 1) {
+    if ((int)threadIdx.x < h) sm[threadIdx.x] += sm[threadIdx.x + h];
+    __syncthreads();
+  }
+  if (threadIdx.x == 0) {
+    const double norm = sqrt(sm[0]);
+    const float out = (float)norm;
+    const bool finite = (__float_as_uint(out) & 0x7f800000u) != 0x7f800000u;
+    result[0] = out;
+    result[1] = !finite ? __uint_as_float(0x7fc00000u) : norm > max_norm ? (float)(max_norm / norm) : 1.0f;
+  }
+}
+
+// (c + K) << 20 has its set bits in the upper half: the value in bf16 is (c + K) << 4, exactly
+__global__ __launch_bounds__(256) void state_values_kernel(int64_t n, const uint8_t* m, const uint8_t* v,
+                                                           const int16_t* mb, const int16_t* vb, bf16_t* mo, bf16_t* vo) {
+  const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 8;
+  if (i >= n) return;
+  uint32_t c[8], w[8];
+  if (mo) {
+    load_codes(m + i, 8, c);
+    const uint32_t K = (uint32_t)(int32_t)mb[i / kAdamBlock];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) w[e] = (c[e] & 127u ? ((c[e] & 127u) + K) << 20 : 0u) | (c[e] & 128u) << 24;
+    store_high<8>(mo + i, 8, w);
+  }
+  if (vo) {
+    load_codes(v + i, 8, c);
+    const uint32_t K = (uint32_t)(int32_t)vb[i / kAdamBlock];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) w[e] = c[e] ? (c[e] + K) << 20 : 0u;
+    store_high<8>(vo + i, 8, w);
+  }
+}
+
+uint32_t adam_key(uint64_t seed, int64_t step, int64_t tensor) {
+  uint32_t x = mix32((uint32_t)seed);
+  if (seed >> 32) x = mix32(x + (uint32_t)(seed >> 32));
+  x = mix32(x + (uint32_t)step);
+  return mix32(x + (uint32_t)tensor);
+}
+
+hipError_t launch_adamw(const AdamTable& t, const AdamParams& p, int kind, uint32_t blocks, hipStream_t s) {
+  auto go = [&](auto fn) { hipLaunchKernelGGL(fn, dim3(blocks), dim3(256), 0, s, t, p); };
+  switch (kind) {
+    case 0: go(adamw_kernel<false, false, false, false>); break;
+    case 1: go(adamw_kernel<true, false, false, false>); break;
+    case 2: go(adamw_kernel<false, true, false, false>); break;
+    case 3: go(adamw_kernel<true, true, false, false>); break;
+    case 5: go(adamw_kernel<true, false, true, false>); break;
+    case 7: go(adamw_kernel<true, true, true, false>); break;
+    case 8: go(adamw_kernel<false, false, false, true>); break;
+    case 9: go(adamw_kernel<true, false, false, true>); break;
+    case 10: go(adamw_kernel<false, true, false, true>); break;
+    case 11: go(adamw_kernel<true, true, false, true>); break;
+    case 13: go(adamw_kernel<true, false, true, true>); break;
+    case 15: go(adamw_kernel<true, true, true, true>); break;
+    default: return hipErrorInvalidValue;
+  }
+  return hipGetLastError();
+}
+
+hipError_t launch_norm_part(const AdamTable& t, double* part, bool bf16, uint32_t blocks, hipStream_t s) {
+  if (bf16) hipLaunchKernelGGL(norm_part_kernel<true>, dim3(blocks), dim3(256), 0, s, t, part);
+  else hipLaunchKernelGGL(norm_part_kernel<false>, dim3(blocks), dim3(256), 0, s, t, part);
+  return hipGetLastError();
+}
+
+hipError_t launch_norm_join(const double* part, int64_t n, double max_norm, float* result, hipStream_t s) {
+  hipLaunchKernelGGL(norm_join_kernel, dim3(1), dim3(1024), 0, s, part, n, max_norm, result);
+  return hipGetLastError();
+}
+
+hipError_t launch_state_values(int64_t n, const void* m, const void* v, const int16_t* mb, const int16_t* vb,
+                               void* mo, void* vo, hipStream_t s) {
+  hipLaunchKernelGGL(state_values_kernel, dim3((unsigned)((n / 8 + 255) / 256)), dim3(256), 0, s, n,
+                     static_cast<const uint8_t*>(m), static_cast<const uint8_t*>(v), mb, vb,
+                     static_cast<bf16_t*>(mo), static_cast<bf16_t*>(vo));
+  return hipGetLastError();
+}
+
+}  // namespace ssm

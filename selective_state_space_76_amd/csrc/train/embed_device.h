@@ -1,0 +1,83 @@
+// embed_device.h -- what the embedding's kernels share: tokens, and pieces of rows at any alignment.
+#pragma once
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "../ssm_device.h"
+
+namespace ssm {
+
+typedef uint32_t u32x4a __attribute__((ext_vector_type(4)));
+
+// 16 bytes that begin at any element
+template <typename IO> struct Unaligned;
+template <> struct Unaligned<float> { typedef uint32_t type __attribute__((ext_vector_type(4), aligned(4))); };
+template <> struct Unaligned<bf16_t> { typedef uint32_t type __attribute__((ext_vector_type(4), aligned(2))); };
+
+// the row that position t names, or V (no row) for a token outside the table
+__device__ __forceinline__ int64_t token_at(const void* tokens, int i64, int64_t t, int64_t V) {
+  const int64_t k = i64 ? static_cast<const int64_t*>(tokens)[t] : (int64_t)static_cast<const int32_t*>(tokens)[t];
+  return k >= 0 && k < V ? k : V;
+}
+
+// N elements from p, of which the first n exist (the others are zero); nt: they are not needed again
+template <typename IO, int N, bool NT = false>
+__device__ __forceinline__ void load_n(const IO* p, int n, float (&x)[N]) {
+  constexpr int V = 16 / (int)sizeof(IO);
+  if (n == N && N % V == 0) {
+#pragma unroll
+    for (int k = 0; k < N / V; ++k) {
+      const auto* a = reinterpret_cast<const typename Unaligned<IO>::type*>(p + k * V);
+      const auto q = NT ? __builtin_nontemporal_load(a) : *a;
+      if constexpr (V == 8) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          x[k * V + 2 * i] = __uint_as_float(q[i] << 16);
+          x[k * V + 2 * i + 1] = __uint_as_float(q[i] & 0xffff0000u);
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[k * V + i] = __uint_as_float(q[i]);
+      }
+    }
+  } else if (n == N && N == 4 && V == 8) {
+    typedef uint32_t u32x2u __attribute__((ext_vector_type(2), aligned(2)));
+    const auto* a = reinterpret_cast<const u32x2u*>(p);
+    const auto q = NT ? __builtin_nontemporal_load(a) : *a;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      x[2 * i] = __uint_as_float(q[i] << 16);
+      x[2 * i + 1] = __uint_as_float(q[i] & 0xffff0000u);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i) x[i] = i < n ? to_f32(p[i]) : 0.0f;
+  }
+}
+
+template <typename IO, int N>
+__device__ __forceinline__ void store_n(IO* p, int n, const float (&x)[N]) {
+  constexpr int V = 16 / (int)sizeof(IO);
+  if (n == N && N % V == 0) {
+#pragma unroll
+    for (int k = 0; k < N / V; ++k) {
+      typename Unaligned<IO>::type q;
+      if constexpr (V == 8) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          q[i] = (uint32_t)__builtin_bit_cast(uint16_t, (__bf16)x[k * V + 2 * i]) |
+                 ((uint32_t)__builtin_bit_cast(uint16_t, (__bf16)x[k * V + 2 * i + 1]) << 16);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) q[i] = __float_as_uint(x[k * V + i]);
+      }
+      __builtin_nontemporal_store(q, reinterpret_cast<typename Unaligned<IO>::type*>(p + k * V));
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      if (i < n) store_io(p + i, x[i]);
+  }
+}
+
+}  // namespace ssm

@@ -1,0 +1,92 @@
+// train_launch.h -- internal interface between the training operators' C entry points
+// (train_abi.cpp) and their gfx950 kernels.  Not installed; not part of the public ABI.
+#pragma once
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+namespace ssm {
+
+// ---- gradients of conv1d + SiLU (conv_bwd.hip)
+struct ConvBwdParams {
+  const void* x;        // [B,D,L]
+  const float* w;       // [D,K]
+  const float* bias;    // [D] or null
+  const void* init;     // [B,D,K-1] or null (zeros)
+  const void* dout;     // [B,D,L]
+  const void* dfinal;   // [B,D,K-1] or null (zeros)
+  void* dx;             // [B,D,L]
+  void* dinit;          // [B,D,K-1] or null
+  float* dw;            // [D,K]
+  float* db;            // [D] or null
+  float* part;          // [B*S][D][K+1]: dweight and dbias summed over one segment of one row
+  int64_t Bsz, Dm, L;
+  int64_t S;            // segments per row
+  int K;
+  int lanes;            // lanes per row segment, 16 or 64
+};
+int64_t conv_bwd_segments(int64_t L, bool bf16, int* lanes);
+hipError_t launch_conv_bwd(const ConvBwdParams& p, bool bf16, hipStream_t s);
+
+// ---- AdamW (adamw.hip)
+constexpr int kAdamBlock = 128;
+constexpr int kAdamTensors = 80;  // tensors per launch: their table travels in the kernel arguments (3.3 KB)
+constexpr int64_t kAdamChunk = 8192;  // elements per workgroup
+constexpr int64_t kNormChunk = 32768;
+
+struct AdamTable {
+  void* p[kAdamTensors];
+  const void* g[kAdamTensors];
+  int64_t n[kAdamTensors];
+  int64_t off[kAdamTensors];
+  uint32_t first[kAdamTensors];  // workgroup that a tensor begins with
+  uint32_t key[kAdamTensors];    // of its random numbers
+  int count;
+};
+
+struct AdamParams {
+  void* m;
+  void* v;
+  int16_t* mb;
+  int16_t* vb;
+  float* master;
+  const float* clip;   // {norm, factor} or null
+  float b1, c1, b2, c2, eps, isb, step, decay;
+};
+
+// of a tensor: a hash of the seed, the step and its place in the list
+uint32_t adam_key(uint64_t seed, int64_t step, int64_t tensor);
+// kind: bit 0 bf16 params, bit 1 bf16 gradients, bit 2 master weights, bit 3 8-bit states
+hipError_t launch_adamw(const AdamTable& t, const AdamParams& p, int kind, uint32_t blocks, hipStream_t s);
+hipError_t launch_norm_part(const AdamTable& t, double* part, bool bf16, uint32_t blocks, hipStream_t s);
+hipError_t launch_norm_join(const double* part, int64_t n, double max_norm, float* result, hipStream_t s);
+hipError_t launch_state_values(int64_t n, const void* m, const void* v, const int16_t* mb, const int16_t* vb,
+                               void* mo, void* vo, hipStream_t s);
+
+// ---- embedding (embed_fwd.hip, embed_bwd.hip)
+struct EmbedParams {
+  const void* tokens;
+  const void* table;   // weight (forward)
+  void* out;           // out (forward), dweight (backward)
+  const void* dout;
+  int64_t Bsz, L, V, E, T;
+  float scale;
+  int i64;             // tokens are int64
+  int cf;              // [B,E,L]
+  int add;
+};
+hipError_t launch_embed_fwd(const EmbedParams& p, bool table_bf16, bool io_bf16, hipStream_t s);
+
+struct EmbedBwdPlan {
+  bool onehot = false;            // few rows, [B,E,L]: one-hot products on the matrix cores
+  bool transpose = false;         // [B,E,L]: dout is brought to [B,L,E] first
+  int bits = 0, passes = 0, digit_bits = 0;
+  int64_t tile = 0, tiles = 0;    // of the sort
+  int64_t run = 0, chunks = 0;    // sorted rows per chunk of the sums
+  int64_t segs = 0;               // onehot: segments of the positions
+  size_t rows = 0, key[2] = {0, 0}, pos[2] = {0, 0}, hist[2] = {0, 0}, part = 0, total = 0;  // offsets, bytes
+};
+void plan_embed_bwd(int64_t Bsz, int64_t L, int64_t V, int64_t E, bool io_bf16, bool cf, EmbedBwdPlan* pl);
+hipError_t launch_embed_bwd(const EmbedParams& p, const EmbedBwdPlan& pl, bool table_bf16, bool io_bf16, void* ws,
+                            hipStream_t s);
+
+}  // namespace ssm

@@ -1,0 +1,289 @@
+"""The training operators next to the scan: the conv's gradients, the embedding with its gradient, AdamW.
+
+    x = embedding_fwd(tokens, table, scale=s, channels_first=True)       # [B,E,L], what the conv reads
+    g = conv1d_bwd(x, weight, bias, dout=du)                             # dx, dweight, dbias, dinitial_state
+    dtable = embedding_bwd(tokens, g["dx"], table.shape[0], scale=s, channels_first=True)
+    opt = AdamW(params, lr=1e-4, weight_decay=0.1, state_bits=8, max_grad_norm=1.0)
+    opt.step()
+
+As in _lib.py this is argument marshalling: the arithmetic runs in the library's HIP kernels (see
+include/ssm_scan.h for the formulas and layouts), and nothing falls back to anything else.
+"""
+from __future__ import annotations
+
+import ctypes
+
+import numpy as np
+import torch
+
+from ._lib import (SSM_BF16, SSM_F32, _check, _expect, _io_dtype, _nonempty, _on_stream, _ptr, _stream, load,
+                   ssm_adamw_config, ssm_embed_shape)
+
+SSM_I32 = 0
+SSM_I64 = 1
+SSM_FLAG_CHANNELS_FIRST = 1
+SSM_FLAG_ACCUMULATE = 2
+ADAMW_BLOCK = 128
+
+
+def _workspace(workspace, need, device, made):
+    """The caller's workspace, or one made here."""
+    if workspace is None:
+        workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=device)
+        made.append(workspace)
+    elif workspace.device != device:
+        raise ValueError("workspace: expected a tensor on %s, got %s" % (device, workspace.device))
+    return workspace, workspace.numel() * workspace.element_size()
+
+
+def conv1d_bwd_workspace_size(batch, dim, seqlen, width, io_dtype=SSM_BF16) -> int:
+    """Workspace bytes of conv1d_bwd."""
+    return int(load().ssm_conv1d_bwd_workspace_size(batch, dim, seqlen, width, io_dtype))
+
+
+def conv1d_bwd(x, weight, bias=None, initial_state=None, *, dout, dfinal_state=None, grads=None, workspace=None,
+               stream=None):
+    """Gradients of conv1d_fwd for the gradient dout [B,D,L] of u and, optionally, dfinal_state [B,D,K-1] of
+    the final state (both in x's dtype).  Returns a dict: dx [B,D,L] and dinitial_state [B,D,K-1] in
+    x's dtype, dweight [D,K] and dbias [D] in fp32 (dbias also without a bias: the gradient at zero).
+    grads: optional dict of preallocated outputs with those names."""
+    lib = load()
+    Bsz, Dm, L = x.shape
+    K = weight.shape[1]
+    _nonempty(batch=Bsz, dim=Dm, seqlen=L, width=K)
+    io, device, f32 = _io_dtype(x), x.device, torch.float32
+    state = (Bsz, Dm, K - 1)
+    for t, shp, dt, name in ((weight, (Dm, K), f32, "weight"), (bias, (Dm,), f32, "bias"),
+                             (initial_state, state, x.dtype, "initial_state"), (dout, (Bsz, Dm, L), x.dtype, "dout"),
+                             (dfinal_state, state, x.dtype, "dfinal_state")):
+        _expect(t, shp, dt, name, device)
+    g, made = dict(grads or {}), []
+    for k, (shp, dt) in dict(dx=((Bsz, Dm, L), x.dtype), dweight=((Dm, K), f32), dbias=((Dm,), f32),
+                             dinitial_state=(state, x.dtype)).items():
+        if g.get(k) is None:
+            g[k] = torch.empty(shp, dtype=dt, device=device)
+            made.append(g[k])
+        _expect(g[k], shp, dt, k, device)
+    workspace, ws_bytes = _workspace(workspace, conv1d_bwd_workspace_size(Bsz, Dm, L, K, io), device, made)
+    _check(lib.ssm_conv1d_bwd(Bsz, Dm, L, K, io, _ptr(x), _ptr(weight), _ptr(bias), _ptr(initial_state), _ptr(dout),
+                              _ptr(dfinal_state), _ptr(g["dx"]), _ptr(g["dweight"]), _ptr(g["dbias"]),
+                              _ptr(g["dinitial_state"]), _ptr(workspace), ws_bytes, _stream(stream, device)))
+    _on_stream(stream, *made)
+    return g
+
+
+def _embed_shape(tokens, rows, dim, table_dtype, io_dtype, channels_first, accumulate=False):
+    if tokens.dtype not in (torch.int32, torch.int64):
+        raise TypeError("tokens must be int32 or int64, got %s" % tokens.dtype)
+    if tokens.dim() not in (1, 2):
+        raise ValueError("tokens: expected [B, L] or [T], got %d dimensions" % tokens.dim())
+    if channels_first and tokens.dim() != 2:
+        raise ValueError("channels_first needs tokens of shape [B, L]")
+    Bsz, L = tokens.shape if tokens.dim() == 2 else (1, tokens.shape[0])
+    _nonempty(batch=Bsz, seqlen=L, rows=rows, dim=dim)
+    kind = {torch.float32: SSM_F32, torch.bfloat16: SSM_BF16}
+    for dt in (table_dtype, io_dtype):
+        if dt not in kind:
+            raise TypeError("tables and embeddings must be float32 or bfloat16, got %s" % dt)
+    flags = (SSM_FLAG_CHANNELS_FIRST if channels_first else 0) | (SSM_FLAG_ACCUMULATE if accumulate else 0)
+    shape = (Bsz, dim, L) if channels_first else tuple(tokens.shape) + (dim,)
+    return ssm_embed_shape(Bsz, L, int(rows), int(dim), SSM_I64 if tokens.dtype == torch.int64 else SSM_I32,
+                           kind[table_dtype], kind[io_dtype], flags), shape
+
+
+def embedding_fwd(tokens, weight, *, scale=1.0, dtype=None, channels_first=False, out=None, stream=None):
+    """scale * weight[tokens].  tokens: int32 or int64, [B,L], or [T] (the single tokens of a generation step);
+    weight: [V,E] fp32 or bf16; a token outside [0, V) gives zeros.  Returns [B,L,E] (or [T,E]), with channels_first
+    [B,E,L], in `dtype` (default: weight's), rounded once."""
+    lib = load()
+    dtype = out.dtype if out is not None and dtype is None else dtype or weight.dtype
+    if weight.dim() != 2:
+        raise ValueError("weight: expected [V, E], got %d dimensions" % weight.dim())
+    sh, shape = _embed_shape(tokens, weight.shape[0], weight.shape[1], weight.dtype, dtype, channels_first)
+    device, made = tokens.device, []
+    if out is None:
+        out = torch.empty(shape, dtype=dtype, device=device)
+        made.append(out)
+    _expect(weight, weight.shape, weight.dtype, "weight", device)
+    _expect(out, shape, dtype, "out", device)
+    _check(lib.ssm_embedding_fwd(ctypes.byref(sh), _ptr(tokens), _ptr(weight), float(scale), _ptr(out),
+                                 _stream(stream, device)))
+    _on_stream(stream, *made)
+    return out
+
+
+def embedding_bwd_workspace_size(tokens, dout, rows, *, dtype=torch.float32, channels_first=False) -> int:
+    """Workspace bytes of embedding_bwd for these arguments."""
+    dim = dout.shape[1 if channels_first else -1]
+    sh, _ = _embed_shape(tokens, rows, dim, dtype, dout.dtype, channels_first)
+    return int(load().ssm_embedding_bwd_workspace_size(ctypes.byref(sh)))
+
+
+def embedding_bwd(tokens, dout, rows, *, scale=1.0, channels_first=False, dtype=None, dweight=None, accumulate=False,
+                  workspace=None, stream=None):
+    """Gradient of embedding_fwd with respect to a table of `rows` rows: for every token, scale times the sum of its
+    positions' rows of dout ([B,L,E], [T,E] or with channels_first [B,E,L]; fp32 or bf16), summed in fp32 in a fixed
+    order.  Returns dweight [rows,E] in `dtype` (default fp32); accumulate=True adds to the dweight given, of which
+    only the rows of tokens that occur are touched."""
+    lib = load()
+    if accumulate and dweight is None:
+        raise ValueError("accumulate needs the dweight to add to")
+    dtype = dweight.dtype if dweight is not None and dtype is None else dtype or torch.float32
+    want = 3 if channels_first else tokens.dim() + 1
+    if dout.dim() != want:
+        raise ValueError("dout: expected %d dimensions, got %d" % (want, dout.dim()))
+    dim = dout.shape[1 if channels_first else -1]
+    sh, shape = _embed_shape(tokens, rows, dim, dtype, dout.dtype, channels_first, accumulate)
+    device, made = tokens.device, []
+    _expect(dout, shape, dout.dtype, "dout", device)
+    if dweight is None:
+        dweight = torch.empty((rows, dim), dtype=dtype, device=device)
+        made.append(dweight)
+    _expect(dweight, (rows, dim), dtype, "dweight", device)
+    need = int(lib.ssm_embedding_bwd_workspace_size(ctypes.byref(sh)))
+    workspace, ws_bytes = _workspace(workspace, need, device, made)
+    _check(lib.ssm_embedding_bwd(ctypes.byref(sh), _ptr(tokens), _ptr(dout), float(scale), _ptr(dweight),
+                                 _ptr(workspace), ws_bytes, _stream(stream, device)))
+    _on_stream(stream, *made)
+    return dweight
+
+
+# struct ssm_adamw_tensor
+_TENSOR = np.dtype([("param", "u8"), ("grad", "u8"), ("numel", "i8"), ("offset", "i8"), ("param_dtype", "i4"),
+                    ("grad_dtype", "i4")])
+
+
+class AdamW:
+    """AdamW over many tensors at once, in place, with decoupled weight decay and bias-corrected moments.
+
+    params: fp32 or bf16 tensors on one GPU, contiguous.  lr, betas, eps, weight_decay and max_grad_norm are
+    attributes that may be changed between steps.
+    state_bits: 32 (fp32 moments) or 8 (one byte per element and an int16 per 128; see include/ssm_scan.h).
+    master_weights: fp32 copies of the bf16 parameters, on which the step works; without them a bf16 parameter is
+        rounded stochastically (to nearest, updates under half a unit would be lost).
+    max_grad_norm: scale the gradients so that their norm over all tensors is at most this; a step whose
+        norm is not finite changes nothing.
+    seed: of the stochastic rounding (a hash of seed, step, tensor and element: the same on every run).
+    state, step: state_dict()'s tensors to go on from (taken over, not copied), and the steps already made.
+
+    The states of all tensors are flat buffers: tensor k's begin at offsets[k], a multiple of 128."""
+
+    def __init__(self, params, *, lr=1e-3, betas=(0.9, 0.999), eps=1e-8, weight_decay=0.01, state_bits=32,
+                 master_weights=True, max_grad_norm=None, seed=0, state=None, step=0):
+        self.params = list(params)
+        if not self.params:
+            raise ValueError("no parameters")
+        if state_bits not in (8, 32):
+            raise ValueError("state_bits must be 8 or 32, got %r" % (state_bits,))
+        self.lr, self.betas, self.eps, self.weight_decay = lr, tuple(betas), eps, weight_decay
+        self.state_bits, self.max_grad_norm, self.seed, self.step_count = state_bits, max_grad_norm, int(seed), int(step)
+        self.device = self.params[0].device
+        for p in self.params:
+            _io_dtype(p)
+            _ptr(p)
+            if p.numel() < 1:
+                raise ValueError("empty parameter")
+            if p.device != self.device:
+                raise ValueError("parameters on %s and %s" % (self.device, p.device))
+        spans = sorted((p.data_ptr(), p.data_ptr() + p.numel() * p.element_size()) for p in self.params)
+        if any(a[1] > b[0] for a, b in zip(spans, spans[1:])):
+            raise ValueError("parameters overlap")
+        self._shapes = [p.shape for p in self.params]
+        self._dtypes = [p.dtype for p in self.params]
+        n = np.array([p.numel() for p in self.params], np.int64)
+        room = -(-n // ADAMW_BLOCK) * ADAMW_BLOCK
+        self.offsets = (np.cumsum(room) - room).tolist()
+        self.numel = int(room.sum())
+        self._table = np.zeros(len(n), _TENSOR)
+        self._table["numel"], self._table["offset"] = n, self.offsets
+        self._table["param_dtype"] = [_io_dtype(p) for p in self.params]
+        want = {"exp_avg": (self.numel, torch.float32 if state_bits == 32 else torch.uint8)}
+        want["exp_avg_sq"] = want["exp_avg"]
+        if state_bits == 8:
+            want["exp_avg_base"] = want["exp_avg_sq_base"] = (self.numel // ADAMW_BLOCK, torch.int16)
+        if master_weights and torch.bfloat16 in self._dtypes:
+            want["master"] = (self.numel, torch.float32)
+        given = {k: v for k, v in (state or {}).items() if v is not None}
+        if set(given) - set(want):
+            raise ValueError("state: %s not expected here" % ", ".join(sorted(set(given) - set(want))))
+        self.state = {}
+        for k, (size, dt) in want.items():
+            t = given.get(k)
+            if t is None:
+                t = torch.zeros(size, dtype=dt, device=self.device)
+                if k == "master":
+                    for p, o in zip(self.params, self.offsets):
+                        t[o:o + p.numel()].copy_(p.detach().reshape(-1))
+            _expect(t, (size,), dt, k, self.device)
+            _ptr(t)
+            self.state[k] = t
+
+    def state_dict(self):
+        """The state tensors and the number of steps made: AdamW(params, **settings, **state_dict) goes on from here."""
+        return {"state": dict(self.state), "step": self.step_count}
+
+    def _checked(self, tensors, what):
+        """Their addresses; every call looks at shape, type, device and layout anew."""
+        if [t.shape for t in tensors] != self._shapes:
+            raise ValueError("%s: shapes differ from the parameters' at construction" % what)
+        if any(t.device != self.device for t in tensors):
+            raise ValueError("%s: expected tensors on %s" % (what, self.device))
+        if not all([t.is_contiguous() for t in tensors]):
+            raise ValueError("%s: tensors must be contiguous" % what)
+        return [t.data_ptr() for t in tensors]
+
+    def step(self, grads=None, *, stream=None):
+        """One step with the gradients given (fp32 or bf16, the parameters' shapes), by default each parameter's
+        .grad; a parameter whose gradient is None is left out.  Returns the gradients' norm before clipping (a
+        0-dim fp32 tensor on the device), or None without max_grad_norm."""
+        lib = load()
+        grads = [p.grad for p in self.params] if grads is None else list(grads)
+        if len(grads) != len(self.params):
+            raise ValueError("%d gradients for %d parameters" % (len(grads), len(self.params)))
+        table = self._table
+        if [p.dtype for p in self.params] != self._dtypes:
+            raise TypeError("a parameter's dtype has changed")
+        table["param"] = self._checked(self.params, "params")
+        have = [g is not None for g in grads]
+        if all(have):
+            table["grad"] = self._checked(grads, "grads")
+            table["grad_dtype"] = [_io_dtype(g) for g in grads]
+        else:
+            if not any(have):
+                return None
+            table = table[have].copy()
+            grads = [p if g is None else g for p, g in zip(self.params, grads)]
+            table["grad"] = np.array(self._checked(grads, "grads"), np.uint64)[have]
+            table["grad_dtype"] = np.array([_io_dtype(g) for g in grads])[have]
+        rows, count = table.ctypes.data, len(table)
+        s, made, norm, clip = _stream(stream, self.device), [], None, None
+        if self.max_grad_norm is not None:
+            need = int(lib.ssm_grad_norm_workspace_size(rows, count))
+            clip = torch.empty(2, dtype=torch.float32, device=self.device)
+            workspace = torch.empty(need, dtype=torch.uint8, device=self.device)
+            made = [clip, workspace]
+            _check(lib.ssm_grad_norm(rows, count, float(self.max_grad_norm), _ptr(clip), _ptr(workspace), need, s))
+            norm = clip[0]
+        cfg = ssm_adamw_config(self.lr, self.betas[0], self.betas[1], self.eps, self.weight_decay, self.step_count + 1,
+                               self.seed & (2 ** 64 - 1), self.state_bits, 0)
+        st = self.state
+        _check(lib.ssm_adamw_step(ctypes.byref(cfg), rows, count, _ptr(st["exp_avg"]), _ptr(st["exp_avg_sq"]),
+                                  _ptr(st.get("exp_avg_base")), _ptr(st.get("exp_avg_sq_base")),
+                                  _ptr(st.get("master")), _ptr(clip), s))
+        self.step_count += 1
+        _on_stream(stream, *made)
+        return norm
+
+    def state_values(self, *, stream=None):
+        """(m, v) of all tensors, flat, at their offsets: fp32 buffers as they are, 8-bit states as the values they
+        stand for, in bf16 (exact)."""
+        st = self.state
+        if self.state_bits == 32:
+            return st["exp_avg"], st["exp_avg_sq"]
+        m = torch.empty(self.numel, dtype=torch.bfloat16, device=self.device)
+        v = torch.empty_like(m)
+        _check(load().ssm_adamw_state_values(self.numel, _ptr(st["exp_avg"]), _ptr(st["exp_avg_sq"]),
+                                             _ptr(st["exp_avg_base"]), _ptr(st["exp_avg_sq_base"]), _ptr(m), _ptr(v),
+                                             _stream(stream, self.device)))
+        _on_stream(stream, m, v)
+        return m, v
