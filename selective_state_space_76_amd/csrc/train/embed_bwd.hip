@@ -2,14 +2,16 @@
 //
 // The positions are sorted by token, equal tokens in order of position, and each token's rows are summed in
 // that order: no atomics on the sums, so the result is the same bits on every run.
-//   1. Sort: a stable radix sort of (token, position), digits of up to 8 bits, the lowest first.  Per digit a
-//      counting pass and a moving pass; in the latter every workgroup adds up the counts of the tiles
-//      before its own.  A wave ranks 64 keys at a time by ballots over the digit's bits.
+//   1. Sort: a stable radix sort of (token, position), digits of up to 8 bits, the lowest first.  Up to 4096
+//      positions are sorted by one workgroup in LDS (12.7 us, where the launches below take 17; 16384
+//      would take 41 against 18); more of them take, per digit, a counting pass and a
+//      moving pass, in which every workgroup adds up the counts of the tiles before its own.  A wave
+//      ranks 64 keys at a time by ballots over the digit's bits.  The sort is short and narrow: the
+//      other workgroups of its launches clear dweight meanwhile (not when the gradient is added to).
 //   2. Sums: the sorted list is cut into chunks of `run` rows.  A wave owns a chunk and 64 * VC columns; it
 //      keeps 8 rows in flight and adds them to the running token's sum.  Sums of tokens that lie within
 //      the chunk go to dweight; one that reaches over an end goes to memory as a partial sum.
 //   3. Join: where a token's rows begin in a chunk and go on in the next, its partial sums are added, in order.
-//   4. Rows of tokens that do not occur are set to zero (not when the gradient is added to).
 // Bound by HBM: dout is read once in whole rows, dweight is written once.
 // Tokens outside the table sort as V, behind all others, and are left out.
 #include "../ssm_device.h"
@@ -20,32 +22,145 @@ namespace ssm {
 
 namespace {
 
-constexpr int kRounds = 8;  // keys per lane of a sort tile
-
 struct SortParams {
   const void* tokens;     // first pass: the keys are the tokens; else null
   const uint32_t* key_in;
   const uint32_t* pos_in;
   uint32_t* key_out;
   uint32_t* pos_out;
-  uint32_t* hist;         // [tiles][digits], or null for a single tile
+  uint32_t* hist;         // [tiles][digits]
+  char* fill;             // bytes to clear meanwhile (the sort leaves most of the chip idle)
+  int64_t fill_bytes;
   int64_t n, V, tiles;
-  int i64, shift, bits;
+  int i64, shift, bits, passes;
 };
 
 __device__ __forceinline__ uint32_t key_at(const SortParams& p, int64_t i) {
   return p.tokens ? (uint32_t)token_at(p.tokens, p.i64, i, p.V) : p.key_in[i];
 }
 
-template <int NW>
+constexpr int64_t kFill = 65536;  // bytes per workgroup
+
+// clears piece `block` of the bytes to fill
+__device__ __forceinline__ void fill_piece(const SortParams& p, int64_t block, int threads) {
+  const int64_t lo = block * kFill;
+  const int64_t hi = lo + kFill < p.fill_bytes ? lo + kFill : p.fill_bytes;
+  int64_t i = lo + threadIdx.x * 16;
+  for (; i + 16 <= hi; i += threads * 16)
+    __builtin_nontemporal_store(u32x4a{0u, 0u, 0u, 0u}, reinterpret_cast<u32x4a*>(p.fill + i));
+  if (i < hi)  // the last elements, fewer than 16 bytes
+    for (; i < hi; i += 2) *reinterpret_cast<uint16_t*>(p.fill + i) = 0;
+}
+
+// Exclusive sum over up to 256 digits, by one wave: 4 per lane.
+__device__ __forceinline__ void scan_digits(uint32_t* tot, int digits, int lane) {
+  uint32_t v[4], s = 0;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    v[e] = s;
+    if (lane * 4 + e < digits) s += tot[lane * 4 + e];
+  }
+  uint32_t inc = s;
+  for (int o = 1; o < 64; o <<= 1) {
+    const uint32_t up = __shfl_up(inc, o, 64);
+    if (lane >= o) inc += up;
+  }
+#pragma unroll
+  for (int e = 0; e < 4; ++e)
+    if (lane * 4 + e < digits) tot[lane * 4 + e] = inc - s + v[e];
+}
+
+// Place of this lane's key among the wave's keys of one round: at[d] is where the digit's keys go next.
+__device__ __forceinline__ uint32_t place(uint32_t* at, uint32_t d, bool valid, int bits, int lane) {
+  uint64_t same = __ballot(valid);  // lanes with the same digit
+  for (int b = 0; b < bits; ++b) {
+    const uint64_t set = __ballot((d >> b) & 1u);
+    same &= (d >> b) & 1u ? set : ~set;
+  }
+  const uint64_t below = same & ((1ull << lane) - 1);
+  uint32_t dst = 0;
+  if (valid) dst = at[d] + (uint32_t)__popcll(below);
+  wave_sync();  // every lane has read its place before the digit's first lane moves it on
+  if (valid && below == 0) at[d] = dst + (uint32_t)__popcll(same);
+  wave_sync();
+  return dst;
+}
+
+// Up to 1024 R keys in one workgroup, all digits: between the passes only the positions move, through LDS
+// (16 bits each), and the keys are looked up again.  The other workgroups fill.
+template <int R>
+__global__ __launch_bounds__(1024) void sort_small_kernel(SortParams p) {
+  if (blockIdx.x > 0) return fill_piece(p, blockIdx.x - 1, 1024);
+  __shared__ uint32_t at[16][256];
+  __shared__ uint32_t tot[256];
+  __shared__ uint16_t moved[1024 * R];
+  const int digits = 1 << p.bits;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int base = wave * (64 * R) + lane, n = (int)p.n;
+  uint32_t key[R], pos[R];
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    pos[r] = base + r * 64;
+    key[r] = (int)pos[r] < n ? key_at(p, pos[r]) : 0u;
+  }
+  for (int pass = 0; pass < p.passes; ++pass) {
+    const int shift = pass * p.bits;
+    for (int i = tid; i < 16 * 256; i += 1024) (&at[0][0])[i] = 0;
+    __syncthreads();
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+      if (base + r * 64 < n) atomicAdd(&at[wave][(key[r] >> shift) & (digits - 1)], 1u);
+    __syncthreads();
+    if (tid < digits) {
+      uint32_t all = 0;
+      for (int w = 0; w < 16; ++w) all += at[w][tid];
+      tot[tid] = all;
+    }
+    __syncthreads();
+    if (wave == 0) scan_digits(tot, digits, lane);
+    __syncthreads();
+    if (tid < digits) {
+      uint32_t a = tot[tid];
+      for (int w = 0; w < 16; ++w) {
+        const uint32_t c = at[w][tid];
+        at[w][tid] = a;
+        a += c;
+      }
+    }
+    __syncthreads();
+    const bool last = pass + 1 == p.passes;
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const bool valid = base + r * 64 < n;
+      const uint32_t dst = place(at[wave], (key[r] >> shift) & (digits - 1), valid, p.bits, lane);
+      if (valid && last) {
+        p.key_out[dst] = key[r];
+        p.pos_out[dst] = pos[r];
+      } else if (valid) {
+        moved[dst] = (uint16_t)pos[r];
+      }
+    }
+    if (last) break;
+    __syncthreads();
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+      if (base + r * 64 < n) {
+        pos[r] = moved[base + r * 64];
+        key[r] = key_at(p, pos[r]);
+      }
+  }
+}
+
+template <int NW, int R>
 __global__ __launch_bounds__(NW * 64) void sort_count_kernel(SortParams p) {
+  if (blockIdx.x >= p.tiles) return fill_piece(p, blockIdx.x - p.tiles, NW * 64);
   __shared__ uint32_t cnt[256];
   const int digits = 1 << p.bits;
   for (int i = threadIdx.x; i < digits; i += NW * 64) cnt[i] = 0;
   __syncthreads();
-  const int64_t base = (int64_t)blockIdx.x * (NW * 64 * kRounds);
+  const int64_t base = (int64_t)blockIdx.x * (NW * 64 * R);
 #pragma unroll
-  for (int r = 0; r < kRounds; ++r) {
+  for (int r = 0; r < R; ++r) {
     const int64_t i = base + r * (NW * 64) + threadIdx.x;
     if (i < p.n) atomicAdd(&cnt[(key_at(p, i) >> p.shift) & (digits - 1)], 1u);
   }
@@ -53,20 +168,21 @@ __global__ __launch_bounds__(NW * 64) void sort_count_kernel(SortParams p) {
   for (int i = threadIdx.x; i < digits; i += NW * 64) p.hist[blockIdx.x * digits + i] = cnt[i];
 }
 
-template <int NW>
+template <int NW, int R>
 __global__ __launch_bounds__(NW * 64) void sort_move_kernel(SortParams p) {
+  if (blockIdx.x >= p.tiles) return fill_piece(p, blockIdx.x - p.tiles, NW * 64);
   __shared__ uint32_t at[NW][256];  // next place of a digit's keys, per wave
-  __shared__ uint32_t tot[256], pre[256];
+  __shared__ uint32_t tot[256];
   const int digits = 1 << p.bits;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   for (int i = tid; i < NW * 256; i += NW * 64) (&at[0][0])[i] = 0;
   __syncthreads();
-  // a wave's keys: 64 * kRounds consecutive ones
-  const int64_t base = ((int64_t)blockIdx.x * NW + wave) * (64 * kRounds);
-  uint32_t key[kRounds], pos[kRounds];
+  // a wave's keys: 64 R consecutive ones
+  const int64_t base = ((int64_t)blockIdx.x * NW + wave) * (64 * R) + lane;
+  uint32_t key[R], pos[R];
 #pragma unroll
-  for (int r = 0; r < kRounds; ++r) {
-    const int64_t i = base + r * 64 + lane;
+  for (int r = 0; r < R; ++r) {
+    const int64_t i = base + r * 64;
     key[r] = pos[r] = 0;
     if (i < p.n) {
       key[r] = key_at(p, i);
@@ -74,58 +190,34 @@ __global__ __launch_bounds__(NW * 64) void sort_move_kernel(SortParams p) {
     }
   }
 #pragma unroll
-  for (int r = 0; r < kRounds; ++r)
-    if (base + r * 64 + lane < p.n) atomicAdd(&at[wave][(key[r] >> p.shift) & (digits - 1)], 1u);
-  if (tid < digits) {  // a digit's keys in all tiles, and in those before this one
-    uint32_t all = 0, mine = 0;
-    if (p.hist) {
-      int64_t j = 0;
-      for (; j + 8 <= p.tiles; j += 8) {
-        uint32_t c[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) c[e] = p.hist[(j + e) * digits + tid];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          all += c[e];
-          if (j + e < blockIdx.x) mine += c[e];
-        }
-      }
-      for (; j < p.tiles; ++j) {
-        const uint32_t c = p.hist[j * digits + tid];
-        all += c;
-        if (j < blockIdx.x) mine += c;
-      }
-    }
-    tot[tid] = all;
-    pre[tid] = mine;
-  }
-  __syncthreads();
-  if (!p.hist && tid < digits) {
+  for (int r = 0; r < R; ++r)
+    if (base + r * 64 < p.n) atomicAdd(&at[wave][(key[r] >> p.shift) & (digits - 1)], 1u);
+  uint32_t mine = 0;  // a digit's keys in the tiles before this one
+  if (tid < digits) {
     uint32_t all = 0;
-    for (int w = 0; w < NW; ++w) all += at[w][tid];
+    int64_t j = 0;
+    for (; j + 16 <= p.tiles; j += 16) {
+      uint32_t c[16];
+#pragma unroll
+      for (int e = 0; e < 16; ++e) c[e] = p.hist[(j + e) * digits + tid];
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        all += c[e];
+        if (j + e < blockIdx.x) mine += c[e];
+      }
+    }
+    for (; j < p.tiles; ++j) {
+      const uint32_t c = p.hist[j * digits + tid];
+      all += c;
+      if (j < blockIdx.x) mine += c;
+    }
     tot[tid] = all;
   }
   __syncthreads();
-  // exclusive sum of the totals over the digits, by one wave (4 digits per lane)
-  if (wave == 0) {
-    uint32_t v[4], s = 0;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      v[e] = s;
-      if (lane * 4 + e < digits) s += tot[lane * 4 + e];
-    }
-    uint32_t inc = s;
-    for (int o = 1; o < 64; o <<= 1) {
-      const uint32_t up = __shfl_up(inc, o, 64);
-      if (lane >= o) inc += up;
-    }
-#pragma unroll
-    for (int e = 0; e < 4; ++e)
-      if (lane * 4 + e < digits) tot[lane * 4 + e] = inc - s + v[e];
-  }
+  if (wave == 0) scan_digits(tot, digits, lane);
   __syncthreads();
   if (tid < digits) {
-    uint32_t a = tot[tid] + pre[tid];
+    uint32_t a = tot[tid] + mine;
     for (int w = 0; w < NW; ++w) {
       const uint32_t c = at[w][tid];
       at[w][tid] = a;
@@ -133,28 +225,13 @@ __global__ __launch_bounds__(NW * 64) void sort_move_kernel(SortParams p) {
     }
   }
   __syncthreads();
-#pragma unroll 1
-  for (int r = 0; r < kRounds; ++r) {
-    uint32_t k = 0, q = 0;
 #pragma unroll
-    for (int e = 0; e < kRounds; ++e)
-      if (e == r) { k = key[e]; q = pos[e]; }
-    const bool valid = base + r * 64 + lane < p.n;
-    const uint32_t d = (k >> p.shift) & (digits - 1);
-    uint64_t same = __ballot(valid);
-    for (int b = 0; b < p.bits; ++b) {
-      const uint64_t set = __ballot((d >> b) & 1u);
-      same &= (d >> b) & 1u ? set : ~set;
-    }
-    const uint64_t below = same & ((1ull << lane) - 1);
-    uint32_t dst = 0;
-    if (valid) dst = at[wave][d] + (uint32_t)__popcll(below);
-    wave_sync();  // every lane has read its place before the digit's first lane moves it on
-    if (valid && below == 0) at[wave][d] = dst + (uint32_t)__popcll(same);
-    wave_sync();
+  for (int r = 0; r < R; ++r) {
+    const bool valid = base + r * 64 < p.n;
+    const uint32_t dst = place(at[wave], (key[r] >> p.shift) & (digits - 1), valid, p.bits, lane);
     if (valid) {
-      p.key_out[dst] = k;
-      p.pos_out[dst] = q;
+      p.key_out[dst] = key[r];
+      p.pos_out[dst] = pos[r];
     }
   }
 }
@@ -171,21 +248,13 @@ struct SumParams {
 };
 
 template <typename OT, int VC>
-__device__ __forceinline__ void put_row(const SumParams& p, uint32_t k, int64_t col, int nc, const float (&acc)[VC]) {
-  OT* o = static_cast<OT*>(p.dweight) + (int64_t)k * p.E + col;
-  float x[VC];
-  if (p.add) {
-    load_n<OT, VC>(o, nc, x);
-#pragma unroll
-    for (int e = 0; e < VC; ++e) x[e] += acc[e] * p.scale;
-  } else {
-#pragma unroll
-    for (int e = 0; e < VC; ++e) x[e] = acc[e] * p.scale;
-  }
-  store_n<OT, VC>(o, nc, x);
+__device__ __forceinline__ OT* row_at(const SumParams& p, uint32_t k, int64_t col) {
+  return static_cast<OT*>(p.dweight) + (int64_t)k * p.E + col;
 }
 
-template <typename IO, typename OT, int VC>
+// With ADD the rows of dweight that a group of 8 will add to are loaded with the group, not one by one as the
+// tokens change (41 -> 27 us per call for 509 tokens of width 768 into a table of 50000 rows).
+template <typename IO, typename OT, int VC, bool ADD>
 __global__ __launch_bounds__(256) void embed_sum_kernel(SumParams p) {
   const int lane = threadIdx.x & 63;
   const int64_t unit = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
@@ -203,12 +272,6 @@ __global__ __launch_bounds__(256) void embed_sum_kernel(SumParams p) {
   for (int e = 0; e < VC; ++e) acc[e] = 0.0f;
   uint32_t cur = V;     // token whose rows are being added; V: none yet
   bool head = true;     // its rows began with the chunk
-  auto flush = [&](bool at_end) {
-    if (cur == V) return;
-    if (head && prev == cur) store_n<float, VC>(p.part + (chunk * 2) * p.E + col, nc, acc);
-    else if (at_end && next == cur) store_n<float, VC>(p.part + (chunk * 2 + 1) * p.E + col, nc, acc);
-    else put_row<OT, VC>(p, cur, col, nc, acc);
-  };
   for (int64_t s = i0; s < i1; s += 64) {
     const int m = i1 - s < 64 ? (int)(i1 - s) : 64;
     uint32_t kv = V, pv = 0;
@@ -216,32 +279,49 @@ __global__ __launch_bounds__(256) void embed_sum_kernel(SumParams p) {
       kv = p.key[s + lane];
       pv = p.pos[s + lane];
     }
+    const uint32_t after = s + 64 < i1 ? p.key[s + 64] : next;  // the key behind these
     for (int r = 0; r < m; r += 8) {
-      float x[8][VC];
-      uint32_t k[8];
+      Raw<IO, VC> x[8];
+      Raw<OT, VC> old[ADD ? 8 : 1];
+      uint32_t k[9];
+#pragma unroll
+      for (int q = 0; q < 9; ++q)
+        k[q] = r + q < m ? (uint32_t)__builtin_amdgcn_readlane((int)kv, r + q < 64 ? r + q : 63) : r + q == m ? after : V;
 #pragma unroll
       for (int q = 0; q < 8; ++q) {
-        k[q] = r + q < m ? (uint32_t)__builtin_amdgcn_readlane((int)kv, r + q) : V;
-        const uint32_t t = (uint32_t)__builtin_amdgcn_readlane((int)pv, r + q < m ? r + q : 0);
-        if (k[q] != V) load_n<IO, VC, true>(rows + (int64_t)t * p.E, nc, x[q]);
+        if (r + q >= m || k[q] == V) continue;  // past the chunk, or outside the table as all that follow
+        const uint32_t t = (uint32_t)__builtin_amdgcn_readlane((int)pv, r + q);
+        x[q].load(rows + (int64_t)t * p.E, nc);
+        if constexpr (ADD)
+          if (k[q] != k[q + 1]) old[q].load(row_at<OT, VC>(p, k[q], col), nc);
       }
 #pragma unroll
       for (int q = 0; q < 8; ++q) {
-        if (k[q] == V) continue;  // past the chunk, or outside the table: all that follow are, too
+        if (r + q >= m || k[q] == V) continue;
         if (k[q] != cur) {
-          flush(false);
           head = s + r + q == i0;
           cur = k[q];
 #pragma unroll
-          for (int e = 0; e < VC; ++e) acc[e] = x[q][e];
+          for (int e = 0; e < VC; ++e) acc[e] = x[q].at(e);
         } else {
 #pragma unroll
-          for (int e = 0; e < VC; ++e) acc[e] += x[q][e];
+          for (int e = 0; e < VC; ++e) acc[e] += x[q].at(e);
+        }
+        const bool end = s + r + q + 1 == i1;
+        if (!end && k[q] == k[q + 1]) continue;
+        if (head && prev == cur) {
+          store_n<float, VC>(p.part + (chunk * 2) * p.E + col, nc, acc);
+        } else if (end && next == cur) {
+          store_n<float, VC>(p.part + (chunk * 2 + 1) * p.E + col, nc, acc);
+        } else {
+          float y[VC];
+#pragma unroll
+          for (int e = 0; e < VC; ++e) y[e] = ADD ? old[ADD ? q : 0].at(e) + acc[e] * p.scale : acc[e] * p.scale;
+          store_n<OT, VC>(row_at<OT, VC>(p, cur, col), nc, y);
         }
       }
     }
   }
-  flush(true);
 }
 
 // A workgroup per chunk and column tile: where a token begins in the chunk and goes on, the sums of the chunks
@@ -251,26 +331,32 @@ __global__ __launch_bounds__(256) void embed_join_kernel(SumParams p) {
   const int64_t chunk = blockIdx.x / p.col_tiles, ct = blockIdx.x - chunk * p.col_tiles;
   const int64_t i0 = chunk * p.run, i1 = i0 + p.run;
   if (i1 >= p.n) return;
-  const uint32_t k = p.key[i1 - 1];
+  const uint32_t k = p.key[i1 - 1], first = p.key[i0], before = i0 > 0 ? p.key[i0 - 1] : (uint32_t)p.V;
   if (k == (uint32_t)p.V || p.key[i1] != k) return;
-  if (i0 > 0 && p.key[i0] == k && p.key[i0 - 1] == k) return;  // it begins in an earlier chunk
-  int64_t lo = i1 + 1, hi = p.n;  // the first place behind the token's rows
-  while (lo < hi) {
-    const int64_t mid = (lo + hi) >> 1;
-    if (p.key[mid] <= k) lo = mid + 1;
-    else hi = mid;
-  }
-  const int64_t last = (lo - 1) / p.run;
+  if (first == k && before == k) return;  // it begins in an earlier chunk
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  int64_t last = chunk + 1;  // the chunk that the token's rows end in: the next one begins with another
+  for (;;) {
+    const int64_t i = (last + 1 + lane) * p.run;
+    const uint64_t goes_on = __ballot(i < p.n && p.key[i < p.n ? i : 0] == k);
+    if (~goes_on) {
+      last += __builtin_ctzll(~goes_on);
+      break;
+    }
+    last += 64;
+  }
   const int64_t col = (ct * 64 + lane) * VC;
   const int nc = p.E - col >= VC ? VC : p.E - col > 0 ? (int)(p.E - col) : 0;
   const int64_t per = (last - chunk + 3) / 4;
   int64_t c = chunk + 1 + wave * per;
   const int64_t c1 = c + per < last + 1 ? c + per : last + 1;
-  float acc[VC];
+  float acc[VC], old[VC];
 #pragma unroll
-  for (int e = 0; e < VC; ++e) acc[e] = 0.0f;
-  if (wave == 0) load_n<float, VC>(p.part + (chunk * 2 + 1) * p.E + col, nc, acc);
+  for (int e = 0; e < VC; ++e) acc[e] = old[e] = 0.0f;
+  if (wave == 0) {
+    load_n<float, VC>(p.part + (chunk * 2 + 1) * p.E + col, nc, acc);
+    if (p.add) load_n<OT, VC>(row_at<OT, VC>(p, k, col), nc, old);
+  }
   for (; c + 8 <= c1; c += 8) {
     float x[8][VC];
 #pragma unroll
@@ -292,38 +378,11 @@ __global__ __launch_bounds__(256) void embed_join_kernel(SumParams p) {
   __syncthreads();
   if (wave == 0) {
 #pragma unroll
-    for (int e = 0; e < VC; ++e) acc[e] += sm[1][e][lane] + (sm[2][e][lane] + sm[3][e][lane]);
-    put_row<OT, VC>(p, k, col, nc, acc);
-  }
-}
-
-// A wave looks 16 rows of the table up in the sorted tokens and clears those that are not there.
-template <typename OT>
-__global__ __launch_bounds__(256) void embed_zero_kernel(SumParams p) {
-  constexpr int VO = 16 / (int)sizeof(OT);
-  const int lane = threadIdx.x & 63;
-  const int64_t v0 = ((int64_t)blockIdx.x * 4 + (threadIdx.x >> 6)) * 16;
-  const int64_t v = v0 + (lane & 15);
-  bool absent = false;
-  if (lane < 16 && v < p.V) {
-    int64_t lo = 0, hi = p.n;
-    while (lo < hi) {
-      const int64_t mid = (lo + hi) >> 1;
-      if (p.key[mid] < (uint32_t)v) lo = mid + 1;
-      else hi = mid;
+    for (int e = 0; e < VC; ++e) {
+      acc[e] = (acc[e] + (sm[1][e][lane] + (sm[2][e][lane] + sm[3][e][lane]))) * p.scale;
+      if (p.add) acc[e] += old[e];
     }
-    absent = lo == p.n || p.key[lo] != (uint32_t)v;
-  }
-  uint64_t todo = __ballot(absent);
-  float zero[VO];
-#pragma unroll
-  for (int e = 0; e < VO; ++e) zero[e] = 0.0f;
-  while (todo) {
-    const int b = __builtin_ctzll(todo);
-    todo &= todo - 1;
-    OT* o = static_cast<OT*>(p.dweight) + (v0 + b) * p.E;
-    for (int64_t c = lane * VO; c < p.E; c += 64 * VO)
-      store_n<OT, VO>(o + c, p.E - c >= VO ? VO : (int)(p.E - c), zero);
+    store_n<OT, VC>(row_at<OT, VC>(p, k, col), nc, acc);
   }
 }
 
@@ -374,11 +433,16 @@ __global__ __launch_bounds__(256) void embed_turn_kernel(const IO* in, IO* out, 
   }
 }
 
+// columns per lane of the sums: 8 (16 bytes) where that covers a row with no more idle lanes than 4
+int columns(int64_t E, bool io_bf16) { return io_bf16 && (E + 511) / 512 * 2 == (E + 255) / 256 ? 8 : 4; }
+
 template <typename IO, typename OT, int VC>
 hipError_t launch_sums(SumParams p, hipStream_t s) {
   p.col_tiles = (p.E + 64 * VC - 1) / (64 * VC);
   const int64_t units = p.chunks * p.col_tiles;
-  hipLaunchKernelGGL((embed_sum_kernel<IO, OT, VC>), dim3((unsigned)((units + 3) / 4)), dim3(256), 0, s, p);
+  const dim3 grid((unsigned)((units + 3) / 4));
+  if (p.add) hipLaunchKernelGGL((embed_sum_kernel<IO, OT, VC, true>), grid, dim3(256), 0, s, p);
+  else hipLaunchKernelGGL((embed_sum_kernel<IO, OT, VC, false>), grid, dim3(256), 0, s, p);
   if (p.chunks > 1) hipLaunchKernelGGL((embed_join_kernel<OT, VC>), dim3((unsigned)units), dim3(256), 0, s, p);
   return hipGetLastError();
 }
@@ -392,21 +456,33 @@ hipError_t launch_io(const EmbedParams& e, const EmbedBwdPlan& pl, SumParams p, 
                        static_cast<const IO*>(e.dout), rows, e.E, e.L);
     p.dout = rows;
   }
-  if (!e.add)
-    hipLaunchKernelGGL((embed_zero_kernel<OT>), dim3((unsigned)((e.V + 63) / 64)), dim3(256), 0, s, p);
-  // 8 columns per lane where that covers the row with no more idle lanes than 4
-  if (sizeof(IO) == 2 && (e.E + 511) / 512 * 2 == (e.E + 255) / 256) return launch_sums<IO, OT, 8>(p, s);
+  if constexpr (sizeof(IO) == 2)
+    if (columns(e.E, true) == 8) return launch_sums<IO, OT, 8>(p, s);
   return launch_sums<IO, OT, 4>(p, s);
 }
 
-template <int NW>
-hipError_t launch_sort(SortParams sp, hipStream_t s) {
-  if (sp.tiles > 1)
-    hipLaunchKernelGGL((sort_count_kernel<NW>), dim3((unsigned)sp.tiles), dim3(NW * 64), 0, s, sp);
-  else
-    sp.hist = nullptr;
-  hipLaunchKernelGGL((sort_move_kernel<NW>), dim3((unsigned)sp.tiles), dim3(NW * 64), 0, s, sp);
+// A launch of a sort kernel whose workgroups behind the sort's clear `share` of the bytes left to fill.
+template <typename F>
+hipError_t with_fill(SortParams& sp, int64_t* left, double share, F&& go) {
+  int64_t bytes = (int64_t)(*left * share) / kFill * kFill;
+  if (share >= 1.0) bytes = *left;
+  sp.fill_bytes = bytes;
+  go((unsigned)((bytes + kFill - 1) / kFill));
+  sp.fill += bytes;
+  *left -= bytes;
   return hipGetLastError();
+}
+
+template <int NW, int R>
+hipError_t launch_pass(SortParams& sp, int64_t* left, int passes_left, hipStream_t s) {
+  const unsigned tiles = (unsigned)sp.tiles;
+  hipError_t e = with_fill(sp, left, 1.0 / (2 * passes_left), [&](unsigned more) {
+    hipLaunchKernelGGL((sort_count_kernel<NW, R>), dim3(tiles + more), dim3(NW * 64), 0, s, sp);
+  });
+  if (e != hipSuccess) return e;
+  return with_fill(sp, left, 1.0 / (2 * passes_left - 1), [&](unsigned more) {
+    hipLaunchKernelGGL((sort_move_kernel<NW, R>), dim3(tiles + more), dim3(NW * 64), 0, s, sp);
+  });
 }
 
 size_t round256(size_t x) { return (x + 255) & ~size_t(255); }
@@ -419,19 +495,23 @@ void plan_embed_bwd(int64_t Bsz, int64_t L, int64_t V, int64_t E, bool io_bf16, 
   while ((V >> pl->bits) != 0) ++pl->bits;  // keys 0 .. V
   pl->passes = (pl->bits + 7) / 8;
   pl->digit_bits = (pl->bits + pl->passes - 1) / pl->passes;
-  pl->tile = n <= 8192 || n > 262144 ? 16 * 64 * kRounds : 4 * 64 * kRounds;
+  pl->tile = n <= 4096 ? 4096 : n <= 65536 ? 512 : n <= 524288 ? 4096 : 8192;
   pl->tiles = (n + pl->tile - 1) / pl->tile;
-  pl->run = n <= 65536 ? 32 : n <= 524288 ? 64 : 256;
+  // rows per chunk of the sums: about 8192 waves, so that short lists spread over the chip and long ones
+  // leave few partial sums
+  const int64_t tiles_e = (E + 64 * columns(E, io_bf16) - 1) / (64 * columns(E, io_bf16));
+  pl->run = 8;
+  while (pl->run < 256 && n * tiles_e > pl->run * 8192) pl->run *= 2;
   pl->chunks = (n + pl->run - 1) / pl->run;
   pl->transpose = cf && L > 1;
   size_t off = 0;
   auto take = [&](size_t bytes) { const size_t o = off; off += round256(bytes); return o; };
   if (pl->transpose) pl->rows = take((size_t)n * E * (io_bf16 ? 2 : 4));
-  for (int i = 0; i < 2; ++i) {
+  for (int i = 0; i < (pl->tiles > 1 ? 2 : 1); ++i) {
     pl->key[i] = take((size_t)n * 4);
     pl->pos[i] = take((size_t)n * 4);
   }
-  pl->hist[0] = take((size_t)pl->tiles * 4 << pl->digit_bits);
+  if (pl->tiles > 1) pl->hist = take((size_t)pl->tiles * 4 << pl->digit_bits);
   pl->part = take((size_t)pl->chunks * 2 * E * 4);
   pl->total = off;
 }
@@ -441,19 +521,32 @@ hipError_t launch_embed_bwd(const EmbedParams& e, const EmbedBwdPlan& pl, bool t
   char* w = static_cast<char*>(ws);
   SortParams sp{};
   sp.tokens = e.tokens;
-  sp.hist = reinterpret_cast<uint32_t*>(w + pl.hist[0]);
-  sp.n = e.T; sp.V = e.V; sp.tiles = pl.tiles; sp.i64 = e.i64; sp.bits = pl.digit_bits;
-  int to = 0;
-  for (int k = 0; k < pl.passes; ++k) {
-    sp.key_out = reinterpret_cast<uint32_t*>(w + pl.key[to]);
-    sp.pos_out = reinterpret_cast<uint32_t*>(w + pl.pos[to]);
+  sp.hist = reinterpret_cast<uint32_t*>(w + pl.hist);
+  sp.n = e.T; sp.V = e.V; sp.tiles = pl.tiles; sp.i64 = e.i64; sp.bits = pl.digit_bits; sp.passes = pl.passes;
+  sp.fill = static_cast<char*>(e.out);
+  int64_t left = e.add ? 0 : e.V * e.E * (table_bf16 ? 2 : 4);
+  hipError_t rc = hipSuccess;
+  if (pl.tiles == 1) {
+    sp.key_out = reinterpret_cast<uint32_t*>(w + pl.key[0]);
+    sp.pos_out = reinterpret_cast<uint32_t*>(w + pl.pos[0]);
+    rc = with_fill(sp, &left, 1.0, [&](unsigned more) {
+      const dim3 grid(1 + more), block(1024);
+      if (e.T <= 1024) hipLaunchKernelGGL(sort_small_kernel<1>, grid, block, 0, s, sp);
+      else hipLaunchKernelGGL(sort_small_kernel<4>, grid, block, 0, s, sp);
+    });
+    if (rc != hipSuccess) return rc;
+  }
+  for (int k = 0; pl.tiles > 1 && k < pl.passes; ++k) {
+    sp.key_out = reinterpret_cast<uint32_t*>(w + pl.key[k & 1]);
+    sp.pos_out = reinterpret_cast<uint32_t*>(w + pl.pos[k & 1]);
     sp.shift = k * pl.digit_bits;
-    const hipError_t rc = pl.tile == 4 * 64 * kRounds ? launch_sort<4>(sp, s) : launch_sort<16>(sp, s);
+    rc = pl.tile == 512    ? launch_pass<4, 2>(sp, &left, pl.passes - k, s)
+         : pl.tile == 4096 ? launch_pass<8, 8>(sp, &left, pl.passes - k, s)
+                           : launch_pass<16, 8>(sp, &left, pl.passes - k, s);
     if (rc != hipSuccess) return rc;
     sp.tokens = nullptr;
     sp.key_in = sp.key_out;
     sp.pos_in = sp.pos_out;
-    to ^= 1;
   }
   SumParams p{};
   p.key = sp.key_out; p.pos = sp.pos_out; p.dout = e.dout; p.dweight = e.out;

@@ -55,6 +55,34 @@ __device__ __forceinline__ void load_n(const IO* p, int n, float (&x)[N]) {
   }
 }
 
+// The same, kept as they are in memory (half the registers of floats for bf16) until unpack().
+template <typename IO, int N>
+struct Raw {
+  static constexpr int W = N * (int)sizeof(IO) / 4, C = W < 4 ? W : 4;  // words, and of one piece
+  uint32_t w[W];
+  __device__ __forceinline__ void load(const IO* p, int n) {
+    typedef uint32_t piece __attribute__((ext_vector_type(C), aligned(sizeof(IO))));
+    if (n == N) {
+#pragma unroll
+      for (int k = 0; k < W / C; ++k) {
+        const piece q = __builtin_nontemporal_load(reinterpret_cast<const piece*>(p + k * C * 4 / (int)sizeof(IO)));
+#pragma unroll
+        for (int i = 0; i < C; ++i) w[k * C + i] = q[i];
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < W; ++i) {
+        if constexpr (sizeof(IO) == 4) w[i] = i < n ? reinterpret_cast<const uint32_t*>(p)[i] : 0u;
+        else w[i] = (2 * i < n ? (uint32_t)p[2 * i] : 0u) | (2 * i + 1 < n ? (uint32_t)p[2 * i + 1] << 16 : 0u);
+      }
+    }
+  }
+  __device__ __forceinline__ float at(int i) const {
+    if constexpr (sizeof(IO) == 4) return __uint_as_float(w[i]);
+    else return __uint_as_float(i & 1 ? w[i >> 1] & 0xffff0000u : w[i >> 1] << 16);
+  }
+};
+
 template <typename IO, int N>
 __device__ __forceinline__ void store_n(IO* p, int n, const float (&x)[N]) {
   constexpr int V = 16 / (int)sizeof(IO);

@@ -77,13 +77,11 @@ struct EmbedParams {
 hipError_t launch_embed_fwd(const EmbedParams& p, bool table_bf16, bool io_bf16, hipStream_t s);
 
 struct EmbedBwdPlan {
-  bool onehot = false;            // few rows, [B,E,L]: one-hot products on the matrix cores
   bool transpose = false;         // [B,E,L]: dout is brought to [B,L,E] first
   int bits = 0, passes = 0, digit_bits = 0;
-  int64_t tile = 0, tiles = 0;    // of the sort
+  int64_t tile = 0, tiles = 0;    // of the sort; one tile: one launch
   int64_t run = 0, chunks = 0;    // sorted rows per chunk of the sums
-  int64_t segs = 0;               // onehot: segments of the positions
-  size_t rows = 0, key[2] = {0, 0}, pos[2] = {0, 0}, hist[2] = {0, 0}, part = 0, total = 0;  // offsets, bytes
+  size_t rows = 0, key[2] = {0, 0}, pos[2] = {0, 0}, hist = 0, part = 0, total = 0;  // offsets, bytes
 };
 void plan_embed_bwd(int64_t Bsz, int64_t L, int64_t V, int64_t E, bool io_bf16, bool cf, EmbedBwdPlan* pl);
 hipError_t launch_embed_bwd(const EmbedParams& p, const EmbedBwdPlan& pl, bool table_bf16, bool io_bf16, void* ws,
