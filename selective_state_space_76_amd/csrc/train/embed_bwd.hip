@@ -12,6 +12,7 @@
 //      keeps 8 rows in flight and adds them to the running token's sum.  Sums of tokens that lie within
 //      the chunk go to dweight; one that reaches over an end goes to memory as a partial sum.
 //   3. Join: where a token's rows begin in a chunk and go on in the next, its partial sums are added, in order.
+// dout in [B,E,L] is first brought to [B,L,E], unless the table has few rows (embed_bwd_few.hip).
 // Bound by HBM: dout is read once in whole rows, dweight is written once.
 // Tokens outside the table sort as V, behind all others, and are left out.
 #include "../ssm_device.h"
@@ -490,6 +491,7 @@ size_t round256(size_t x) { return (x + 255) & ~size_t(255); }
 }  // namespace
 
 void plan_embed_bwd(int64_t Bsz, int64_t L, int64_t V, int64_t E, bool io_bf16, bool cf, EmbedBwdPlan* pl) {
+  if (cf && embed_few_rows(V, io_bf16)) return plan_embed_few(Bsz, L, V, E, pl);
   const int64_t n = Bsz * L;
   pl->bits = 1;
   while ((V >> pl->bits) != 0) ++pl->bits;  // keys 0 .. V
@@ -497,13 +499,13 @@ void plan_embed_bwd(int64_t Bsz, int64_t L, int64_t V, int64_t E, bool io_bf16, 
   pl->digit_bits = (pl->bits + pl->passes - 1) / pl->passes;
   pl->tile = n <= 4096 ? 4096 : n <= 65536 ? 512 : n <= 524288 ? 4096 : 8192;
   pl->tiles = (n + pl->tile - 1) / pl->tile;
-  // rows per chunk of the sums: about 8192 waves, so that short lists spread over the chip and long ones
+  // rows per chunk of the sums: about 4096 waves, so that short lists spread over the chip and long ones
   // leave few partial sums
   const int64_t tiles_e = (E + 64 * columns(E, io_bf16) - 1) / (64 * columns(E, io_bf16));
   pl->run = 8;
-  while (pl->run < 256 && n * tiles_e > pl->run * 8192) pl->run *= 2;
+  while (pl->run < 256 && n * tiles_e > pl->run * 4096) pl->run *= 2;
   pl->chunks = (n + pl->run - 1) / pl->run;
-  pl->transpose = cf && L > 1;
+  pl->transpose = cf;
   size_t off = 0;
   auto take = [&](size_t bytes) { const size_t o = off; off += round256(bytes); return o; };
   if (pl->transpose) pl->rows = take((size_t)n * E * (io_bf16 ? 2 : 4));
@@ -518,6 +520,7 @@ void plan_embed_bwd(int64_t Bsz, int64_t L, int64_t V, int64_t E, bool io_bf16, 
 
 hipError_t launch_embed_bwd(const EmbedParams& e, const EmbedBwdPlan& pl, bool table_bf16, bool io_bf16, void* ws,
                             hipStream_t s) {
+  if (pl.few) return launch_embed_few(e, pl, table_bf16, io_bf16, ws, s);
   char* w = static_cast<char*>(ws);
   SortParams sp{};
   sp.tokens = e.tokens;

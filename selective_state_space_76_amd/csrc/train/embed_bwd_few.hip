@@ -1,0 +1,281 @@
+// embed_bwd_few.hip -- gradient of the embedding for a table of few rows (letters), dout in the scan's [B,E,L].
+//
+// With few rows the sum over the positions of each token is a product: dweight[v,e] = scale * sum_t [token_t = v]
+// dout[e,t].  The positions are contiguous in dout, as the matrix cores want the summed index of their right
+// operand, so dout goes from memory into v_mfma_f32_16x16x32_bf16 (or 16x16x4 in fp32) as it lies;
+// the left operand, ones and zeros, is made from the tokens in registers.  Products with one and zero and the
+// fp32 sums are exact but for the sums' rounding.  No sort, no transposed copy.
+//
+// A workgroup owns 64 channels and `seg` positions of one batch row, its 4 waves a quarter of these each; a
+// wave takes 64 positions at a time: per 16 channels two (bf16) or four (fp32) 16-byte loads per lane, a whole
+// line of each channel.  The segments' sums are added by a second kernel in order.  Bound by HBM: dout is read
+// once.
+//
+// 0 * x is not 0 where x is infinite or NaN.  What lies at positions whose token is outside the table is cleared
+// on the way; where a workgroup still meets such a value it adds its segment up again by selection.
+#include "../ssm_device.h"
+#include "embed_device.h"
+#include "train_launch.h"
+
+namespace ssm {
+
+namespace {
+
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+
+struct FewParams {
+  const void* tokens;
+  const void* dout;   // [B,E,L]
+  void* dweight;
+  float* part;        // [segs][V][E]
+  int64_t L, V, E, seg, segs_row, segs, groups;
+  float scale;
+  int i64, add;
+};
+
+constexpr int kMaxSeg = 8192;
+
+// 4 words of a channel from element t on; past the row's end zero
+template <typename IO>
+__device__ __forceinline__ u32x4a words(const IO* row, int64_t t, int64_t L, bool live) {
+  constexpr int V = 16 / (int)sizeof(IO);
+  if (live && t + V <= L) {
+    const auto q = __builtin_nontemporal_load(reinterpret_cast<const typename Unaligned<IO>::type*>(row + t));
+    return u32x4a{q[0], q[1], q[2], q[3]};
+  }
+  u32x4a w = {0u, 0u, 0u, 0u};
+  if (live && t < L) {
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+      if (t + i < L) {
+        if constexpr (sizeof(IO) == 2) w[i >> 1] |= (uint32_t)row[t + i] << (16 * (i & 1));
+        else w[i] = __float_as_uint(row[t + i]);
+      }
+  }
+  return w;
+}
+
+}  // namespace
+
+template <typename IO, int MT>
+__global__ __launch_bounds__(256) void embed_few_kernel(FewParams p) {
+  constexpr bool BF = sizeof(IO) == 2;
+  constexpr int NL = BF ? 2 : 4;  // 16-byte loads per lane and tile of 16 channels, for 64 positions
+  constexpr int ROWS = MT * 16;
+  __shared__ __align__(16) uint16_t tok[kMaxSeg];  // 0xffff: no row
+  __shared__ float sums[ROWS * 64];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int n = lane & 15, g = lane >> 4;
+  const int64_t grp = blockIdx.x % p.groups, seg = blockIdx.x / p.groups;
+  const int64_t b = seg / p.segs_row, t0 = (seg - b * p.segs_row) * p.seg;
+  const int64_t e0 = grp * 64;
+  const IO* base = static_cast<const IO*>(p.dout) + (b * p.E + e0) * p.L;
+  for (int i = threadIdx.x; i < p.seg; i += 256) {
+    const int64_t k = t0 + i < p.L ? token_at(p.tokens, p.i64, b * p.L + t0 + i, p.V) : p.V;
+    tok[i] = k < p.V ? (uint16_t)k : 0xffffu;
+  }
+  const IO* row[4];
+  bool live[4];
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    live[q] = e0 + q * 16 + n < p.E;
+    row[q] = base + (live[q] ? (q * 16 + n) * p.L : 0);
+  }
+  f32x4 acc[MT][4];
+#pragma unroll
+  for (int m = 0; m < MT; ++m)
+#pragma unroll
+    for (int q = 0; q < 4; ++q) acc[m][q] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  u16x2 big16 = {0, 0};
+  uint32_t big32 = 0;
+  const int quarter = (int)(p.seg / 4);  // a multiple of 64
+  const int first = wave * quarter;
+  // lane's positions within 64: BF: g * 16 + s * 8 ..+7, s = 0, 1; fp32: g * 16 + s * 4 ..+3, s = 0..3
+  constexpr int V = 16 / (int)sizeof(IO);
+  u32x4a next[4][NL];
+  auto fetch = [&](int i) {
+    const int64_t t = t0 + i + g * 16;
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+#pragma unroll
+      for (int s = 0; s < NL; ++s) next[q][s] = words<IO>(row[q], t + s * V, p.L, live[q]);
+  };
+  const int64_t here = p.L - t0 - first;  // positions of the row that are left for this wave
+  const int steps = here <= 0 ? 0 : (int)((here < quarter ? here : quarter) + 63) / 64;
+  if (steps > 0) fetch(first);
+  __syncthreads();
+#pragma unroll 1
+  for (int it = 0; it < steps; ++it) {
+    const int i = first + it * 64;
+    u32x4a x[4][NL];
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+#pragma unroll
+      for (int s = 0; s < NL; ++s) x[q][s] = next[q][s];
+    if (it + 1 < steps) fetch(i + 64);
+#pragma unroll
+    for (int s = 0; s < NL; ++s) {
+      if constexpr (BF) {
+        const u32x4a tk = *reinterpret_cast<const u32x4a*>(&tok[i + g * 16 + s * 8]);  // 8 tokens
+        u32x4a keep;  // ones where the token has a row
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+          typedef int16_t i16x2 __attribute__((ext_vector_type(2)));
+          const uint32_t two = tk[w];  // (a bit cast of tk[w] itself would read tk[0])
+          const i16x2 neg = __builtin_bit_cast(i16x2, two) >> 15;
+          keep[w] = ~__builtin_bit_cast(uint32_t, neg);
+        }
+        bf16x8 hot[MT];
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+          u32x4a a;
+          const uint32_t mine = (uint32_t)(m * 16 + n) * 0x10001u;
+#pragma unroll
+          for (int w = 0; w < 4; ++w) {
+            const u16x2 d = __builtin_elementwise_min(__builtin_bit_cast(u16x2, tk[w] ^ mine), u16x2{1, 1});
+            a[w] = (__builtin_bit_cast(uint32_t, d) ^ 0x10001u) * 0x3f80u;  // 1.0 in bf16 where they agree
+          }
+          hot[m] = __builtin_bit_cast(bf16x8, a);
+        }
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          u32x4a y;
+#pragma unroll
+          for (int w = 0; w < 4; ++w) {
+            y[w] = x[q][s][w] & keep[w];
+            big16 = __builtin_elementwise_max(big16, __builtin_bit_cast(u16x2, y[w] & 0x7fff7fffu));
+          }
+#pragma unroll
+          for (int m = 0; m < MT; ++m)
+            acc[m][q] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(hot[m], __builtin_bit_cast(bf16x8, y), acc[m][q], 0, 0, 0);
+        }
+      } else {
+        const uint2 tk = *reinterpret_cast<const uint2*>(&tok[i + g * 16 + s * 4]);  // 4 tokens
+        const uint32_t t4[4] = {tk.x & 0xffffu, tk.x >> 16, tk.y & 0xffffu, tk.y >> 16};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const uint32_t keep = t4[j] == 0xffffu ? 0u : 0xffffffffu;
+          float hot[MT];
+#pragma unroll
+          for (int m = 0; m < MT; ++m) hot[m] = t4[j] == (uint32_t)(m * 16 + n) ? 1.0f : 0.0f;
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const uint32_t y = x[q][s][j] & keep, a = y & 0x7fffffffu;
+            big32 = big32 > a ? big32 : a;
+#pragma unroll
+            for (int m = 0; m < MT; ++m)
+              acc[m][q] = __builtin_amdgcn_mfma_f32_16x16x4f32(hot[m], __uint_as_float(y), acc[m][q], 0, 0, 0);
+          }
+        }
+      }
+    }
+  }
+  const int bad = BF ? (big16[0] >= 0x7f80u || big16[1] >= 0x7f80u) : big32 >= 0x7f800000u;
+  float* out = p.part + seg * p.V * p.E;
+  if (__syncthreads_or(bad)) {  // by selection: every token's sum sees its own values only
+    const int64_t e = e0 + lane;
+    if (e >= p.E) return;
+    const int64_t m = p.L - t0 < p.seg ? p.L - t0 : p.seg;
+    for (int v = wave; v < p.V; v += 4) {
+      float s = 0.0f;
+      for (int64_t i = 0; i < m; ++i)
+        if (tok[i] == v) s += to_f32(base[lane * p.L + t0 + i]);
+      out[v * p.E + e] = s;
+    }
+    return;
+  }
+  // the waves' sums in order; lane: row 4 g + i of a tile, channel n
+  for (int w = 0; w < 4; ++w) {
+    if (wave == w) {
+#pragma unroll
+      for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            float* s = &sums[(m * 16 + g * 4 + i) * 64 + q * 16 + n];
+            *s = w == 0 ? acc[m][q][i] : *s + acc[m][q][i];
+          }
+    }
+    __syncthreads();
+  }
+  for (int i = threadIdx.x; i < ROWS * 64; i += 256) {
+    const int v = i >> 6;
+    const int64_t e = e0 + (i & 63);
+    if (v < p.V && e < p.E) out[v * p.E + e] = sums[i];
+  }
+}
+
+// dweight from the segments' sums: 64 elements per workgroup, the segments split over 4 waves, each in order,
+// then the waves' sums in order.
+template <typename OT>
+__global__ __launch_bounds__(256) void embed_few_join_kernel(FewParams p) {
+  const int64_t n = p.V * p.E;
+  const int64_t i = (int64_t)blockIdx.x * 64 + (threadIdx.x & 63);
+  const int64_t per = (p.segs + 3) / 4;
+  const int64_t k0 = (threadIdx.x >> 6) * per, k1 = k0 + per < p.segs ? k0 + per : p.segs;
+  float s = 0.0f;
+  if (i < n) {
+    int64_t k = k0;
+    for (; k + 16 <= k1; k += 16) {
+      float v[16];
+#pragma unroll
+      for (int e = 0; e < 16; ++e) v[e] = p.part[(k + e) * n + i];
+#pragma unroll
+      for (int e = 0; e < 16; ++e) s += v[e];
+    }
+    for (; k < k1; ++k) s += p.part[k * n + i];
+  }
+  __shared__ float sm[256];
+  sm[threadIdx.x] = s;
+  __syncthreads();
+  if (threadIdx.x < 64 && i < n) {
+    s = (sm[threadIdx.x] + sm[threadIdx.x + 64] + sm[threadIdx.x + 128] + sm[threadIdx.x + 192]) * p.scale;
+    OT* o = static_cast<OT*>(p.dweight) + i;
+    store_io(o, p.add ? to_f32(*o) + s : s);
+  }
+}
+
+// Rows up to which the products pay: the matrix cores keep up with HBM through 64 rows in bf16 and 32 in fp32
+// (4 and 2 products per piece of dout).
+bool embed_few_rows(int64_t V, bool io_bf16) { return V <= (io_bf16 ? 64 : 32); }
+
+void plan_embed_few(int64_t Bsz, int64_t L, int64_t V, int64_t E, EmbedBwdPlan* pl) {
+  const int64_t groups = (E + 63) / 64;
+  int64_t seg = (Bsz * L * groups / 2048 + 255) / 256 * 256;  // about 2048 workgroups
+  if (seg > kMaxSeg) seg = kMaxSeg;
+  if (seg < 256) seg = 256;
+  pl->few = true;
+  pl->run = seg;
+  pl->chunks = Bsz * ((L + seg - 1) / seg);
+  pl->total = (size_t)pl->chunks * V * E * 4;
+}
+
+namespace {
+
+template <typename IO>
+hipError_t launch_few(const FewParams& p, bool table_bf16, hipStream_t s) {
+  const dim3 grid((unsigned)(p.segs * p.groups));
+  if (p.V <= 16) hipLaunchKernelGGL((embed_few_kernel<IO, 1>), grid, dim3(256), 0, s, p);
+  else if (p.V <= 32) hipLaunchKernelGGL((embed_few_kernel<IO, 2>), grid, dim3(256), 0, s, p);
+  else if constexpr (sizeof(IO) == 2) hipLaunchKernelGGL((embed_few_kernel<IO, 4>), grid, dim3(256), 0, s, p);
+  const dim3 jgrid((unsigned)((p.V * p.E + 63) / 64));
+  if (table_bf16) hipLaunchKernelGGL(embed_few_join_kernel<bf16_t>, jgrid, dim3(256), 0, s, p);
+  else hipLaunchKernelGGL(embed_few_join_kernel<float>, jgrid, dim3(256), 0, s, p);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_embed_few(const EmbedParams& e, const EmbedBwdPlan& pl, bool table_bf16, bool io_bf16, void* ws,
+                            hipStream_t s) {
+  FewParams p{};
+  p.tokens = e.tokens; p.dout = e.dout; p.dweight = e.out; p.part = static_cast<float*>(ws);
+  p.L = e.L; p.V = e.V; p.E = e.E; p.seg = pl.run; p.segs = pl.chunks; p.segs_row = (e.L + pl.run - 1) / pl.run;
+  p.groups = (e.E + 63) / 64;
+  p.scale = e.scale; p.i64 = e.i64; p.add = e.add;
+  return io_bf16 ? launch_few<bf16_t>(p, table_bf16, s) : launch_few<float>(p, table_bf16, s);
+}
+
+}  // namespace ssm

@@ -77,6 +77,7 @@ struct EmbedParams {
 hipError_t launch_embed_fwd(const EmbedParams& p, bool table_bf16, bool io_bf16, hipStream_t s);
 
 struct EmbedBwdPlan {
+  bool few = false;               // [B,E,L] and few rows: products (embed_bwd_few.hip); run: positions per segment
   bool transpose = false;         // [B,E,L]: dout is brought to [B,L,E] first
   int bits = 0, passes = 0, digit_bits = 0;
   int64_t tile = 0, tiles = 0;    // of the sort; one tile: one launch
@@ -85,6 +86,10 @@ struct EmbedBwdPlan {
 };
 void plan_embed_bwd(int64_t Bsz, int64_t L, int64_t V, int64_t E, bool io_bf16, bool cf, EmbedBwdPlan* pl);
 hipError_t launch_embed_bwd(const EmbedParams& p, const EmbedBwdPlan& pl, bool table_bf16, bool io_bf16, void* ws,
+                            hipStream_t s);
+bool embed_few_rows(int64_t V, bool io_bf16);
+void plan_embed_few(int64_t Bsz, int64_t L, int64_t V, int64_t E, EmbedBwdPlan* pl);
+hipError_t launch_embed_few(const EmbedParams& p, const EmbedBwdPlan& pl, bool table_bf16, bool io_bf16, void* ws,
                             hipStream_t s);
 
 }  // namespace ssm

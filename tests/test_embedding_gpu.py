@@ -111,6 +111,27 @@ def test_backward_few_rows_channels_first(V, ot):
             bwd_check(tokens_of(B, L, V, V + L), V, E, ot, F32, True, 2.5, seed=V, add=add)
 
 
+@pytest.mark.parametrize("V,cf", [(4, True), (40, True), (4, False), (300, True)])
+@pytest.mark.parametrize("ot", [F32, BF16], ids=["f32", "bf16"])
+def test_infinite_and_nan_gradients_stay_with_their_token(V, cf, ot):
+    """A value that is not finite reaches its own token's row and channel and no other."""
+    B, L, E = 2, 1500, 70
+    tok = tokens_of(B, L, V, V)
+    g = torch.Generator().manual_seed(3)
+    rows = torch.randn(B, L, E, generator=g).to(ot)
+    tok[0, 7], tok[1, 1490], tok[1, 1499] = 1, 2, 0
+    rows[(tok < 0) | (tok >= V)] = float("inf")
+    rows[0, 7, 5], rows[1, 1490, 69], rows[1, 1499, 0] = float("nan"), float("inf"), -float("inf")
+    d = rows.transpose(1, 2).contiguous() if cf else rows
+    got = f64(embedding_bwd(tok.to(DEV), d.to(DEV), V, channels_first=cf))
+    with np.errstate(invalid="ignore"):
+        ref, mag, n = embed_grad(tok.reshape(-1).numpy(), f64(rows).reshape(-1, E), V, 1.0)
+    assert np.isnan(got[1, 5]) and got[2, 69] == np.inf and got[0, 0] == -np.inf
+    fine = np.isfinite(ref)
+    assert fine.sum() == fine.size - 3 and np.isfinite(got[fine]).all()
+    assert (np.abs(got - ref)[fine] <= ((n[:, None] + 3) * 2.0 ** -24 * mag)[fine]).all()
+
+
 # more than one tile of the sort, one to three digits, and chunks of every length
 @pytest.mark.parametrize("n,V,E", [(8192, 50000, 8), (8193, 70000, 8), (9000, 255, 24), (20001, 256, 16),
                                    (66000, 3, 8), (66001, 20, 8), (300007, 70001, 4), (600011, 5, 4)])
