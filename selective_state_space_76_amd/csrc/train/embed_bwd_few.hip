@@ -1,15 +1,22 @@
 // embed_bwd_few.hip -- gradient of the embedding for a table of few rows (letters), dout in the scan's [B,E,L].
 //
 // With few rows the sum over the positions of each token is a product: dweight[v,e] = scale * sum_t [token_t = v]
-// dout[e,t].  The positions are contiguous in dout, as the matrix cores want the summed index of their right
-// operand, so dout goes from memory into v_mfma_f32_16x16x32_bf16 (or 16x16x4 in fp32) as it lies;
-// the left operand, ones and zeros, is made from the tokens in registers.  Products with one and zero and the
-// fp32 sums are exact but for the sums' rounding.  No sort, no transposed copy.
+// dout[e,t].  Positions are contiguous in dout, as the matrix cores want the summed index of their right
+// operand; the left operand, ones and zeros, is made from the tokens in registers for
+// v_mfma_f32_16x16x32_bf16 (16x16x4 in fp32).  Products with one and zero are exact, the sums are fp32.  No
+// sort, no transposed copy.
 //
-// A workgroup owns 64 channels and `seg` positions of one batch row, its 4 waves a quarter of these each; a
-// wave takes 64 positions at a time: per 16 channels two (bf16) or four (fp32) 16-byte loads per lane, a whole
-// line of each channel.  The segments' sums are added by a second kernel in order.  Bound by HBM: dout is read
-// once.
+// A workgroup owns 64 channels (16 per wave) and `seg` positions of one batch row.  A wave moves a tile of 1 KB of
+// each of its 16 channels at a time from memory to registers (a load per channel, 1 KB in one piece), from
+// there to its own LDS, and from LDS into the products, while the next tile is on its way; the pieces of 16 bytes
+// lie rotated by xor with the channel, so that the products' reads, 16 channels at one position, meet all
+// banks.  The segments' sums are added by a second kernel in order.
+//
+// Bound by HBM: dout is read once.  For a million letters and 1024 channels in bf16 (2.1 GB): 371 us, 5.8 TB/s, at
+// the rate of a plain sum over as many bytes (6.0 TB/s).  With the products fed straight from memory (each load
+// 64 bytes of 16 channels that lie 2 MB apart) it took 636 us with the loads marked as not needed again, which
+// dropped half-used lines, 532 without, 480 and 442 with 512 and 1024 bytes of a channel per step; through LDS
+// 502 with 8192 positions per workgroup (one workgroup per CU), 377 with 4096, 371 with 2048, 420 with 1024.
 //
 // 0 * x is not 0 where x is infinite or NaN.  What lies at positions whose token is outside the table is cleared
 // on the way; where a workgroup still meets such a value it adds its segment up again by selection.
@@ -34,7 +41,7 @@ struct FewParams {
   int i64, add;
 };
 
-constexpr int kMaxSeg = 8192;
+constexpr int kMaxSeg = 2048;
 
 // 4 words of a channel from element t on; past the row's end zero
 template <typename IO>
@@ -61,10 +68,10 @@ __device__ __forceinline__ u32x4a words(const IO* row, int64_t t, int64_t L, boo
 template <typename IO, int MT>
 __global__ __launch_bounds__(256) void embed_few_kernel(FewParams p) {
   constexpr bool BF = sizeof(IO) == 2;
-  constexpr int NL = BF ? 2 : 4;  // 16-byte loads per lane and tile of 16 channels, for 64 positions
-  constexpr int ROWS = MT * 16;
-  __shared__ __align__(16) uint16_t tok[kMaxSeg];  // 0xffff: no row
-  __shared__ float sums[ROWS * 64];
+  constexpr int V = 16 / (int)sizeof(IO);
+  constexpr int STEP = 64 * V;  // positions at a time: 1 KB of each channel
+  __shared__ __align__(16) uint16_t tok[kMaxSeg];   // 0xffff: no row
+  __shared__ __align__(16) u32x4a tile[4][16][64];  // per wave: 16 channels; piece c of channel k lies at c ^ k
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int n = lane & 15, g = lane >> 4;
   const int64_t grp = blockIdx.x % p.groups, seg = blockIdx.x / p.groups;
@@ -75,101 +82,70 @@ __global__ __launch_bounds__(256) void embed_few_kernel(FewParams p) {
     const int64_t k = t0 + i < p.L ? token_at(p.tokens, p.i64, b * p.L + t0 + i, p.V) : p.V;
     tok[i] = k < p.V ? (uint16_t)k : 0xffffu;
   }
-  const IO* row[4];
-  bool live[4];
+  f32x4 acc[MT];
 #pragma unroll
-  for (int q = 0; q < 4; ++q) {
-    live[q] = e0 + q * 16 + n < p.E;
-    row[q] = base + (live[q] ? (q * 16 + n) * p.L : 0);
-  }
-  f32x4 acc[MT][4];
-#pragma unroll
-  for (int m = 0; m < MT; ++m)
-#pragma unroll
-    for (int q = 0; q < 4; ++q) acc[m][q] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  for (int m = 0; m < MT; ++m) acc[m] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
   u16x2 big16 = {0, 0};
   uint32_t big32 = 0;
-  const int quarter = (int)(p.seg / 4);  // a multiple of 64
-  const int first = wave * quarter;
-  // lane's positions within 64: BF: g * 16 + s * 8 ..+7, s = 0, 1; fp32: g * 16 + s * 4 ..+3, s = 0..3
-  constexpr int V = 16 / (int)sizeof(IO);
-  u32x4a next[4][NL];
+  u32x4a next[16];
+  const IO* mine = base + wave * 16 * p.L;
   auto fetch = [&](int i) {
-    const int64_t t = t0 + i + g * 16;
+    const int64_t t = t0 + i + lane * V;
 #pragma unroll
-    for (int q = 0; q < 4; ++q)
-#pragma unroll
-      for (int s = 0; s < NL; ++s) next[q][s] = words<IO>(row[q], t + s * V, p.L, live[q]);
+    for (int k = 0; k < 16; ++k)
+      next[k] = words<IO>(mine + k * p.L, t, p.L, e0 + wave * 16 + k < p.E);
   };
-  const int64_t here = p.L - t0 - first;  // positions of the row that are left for this wave
-  const int steps = here <= 0 ? 0 : (int)((here < quarter ? here : quarter) + 63) / 64;
-  if (steps > 0) fetch(first);
+  const int64_t here = p.L - t0 < p.seg ? p.L - t0 : p.seg;
+  fetch(0);
   __syncthreads();
 #pragma unroll 1
-  for (int it = 0; it < steps; ++it) {
-    const int i = first + it * 64;
-    u32x4a x[4][NL];
+  for (int i = 0; i < here; i += STEP) {
 #pragma unroll
-    for (int q = 0; q < 4; ++q)
+    for (int k = 0; k < 16; ++k) tile[wave][k][lane ^ k] = next[k];
+    wave_sync();
+    if (i + STEP < here) fetch(i + STEP);
 #pragma unroll
-      for (int s = 0; s < NL; ++s) x[q][s] = next[q][s];
-    if (it + 1 < steps) fetch(i + 64);
-#pragma unroll
-    for (int s = 0; s < NL; ++s) {
+    for (int s = 0; s < 16; ++s) {
+      const int c = s * 4 + g;  // the lane's piece: V positions of channel n
+      const u32x4a x = tile[wave][n][c ^ n];
       if constexpr (BF) {
-        const u32x4a tk = *reinterpret_cast<const u32x4a*>(&tok[i + g * 16 + s * 8]);  // 8 tokens
-        u32x4a keep;  // ones where the token has a row
+        const u32x4a tk = *reinterpret_cast<const u32x4a*>(&tok[i + c * 8]);  // 8 tokens
+        u32x4a y;
 #pragma unroll
         for (int w = 0; w < 4; ++w) {
           typedef int16_t i16x2 __attribute__((ext_vector_type(2)));
           const uint32_t two = tk[w];  // (a bit cast of tk[w] itself would read tk[0])
-          const i16x2 neg = __builtin_bit_cast(i16x2, two) >> 15;
-          keep[w] = ~__builtin_bit_cast(uint32_t, neg);
+          const i16x2 neg = __builtin_bit_cast(i16x2, two) >> 15;  // ones where the token has no row
+          y[w] = x[w] & ~__builtin_bit_cast(uint32_t, neg);
+          big16 = __builtin_elementwise_max(big16, __builtin_bit_cast(u16x2, y[w] & 0x7fff7fffu));
         }
-        bf16x8 hot[MT];
 #pragma unroll
         for (int m = 0; m < MT; ++m) {
           u32x4a a;
-          const uint32_t mine = (uint32_t)(m * 16 + n) * 0x10001u;
+          const uint32_t row = (uint32_t)(m * 16 + n) * 0x10001u;
 #pragma unroll
           for (int w = 0; w < 4; ++w) {
-            const u16x2 d = __builtin_elementwise_min(__builtin_bit_cast(u16x2, tk[w] ^ mine), u16x2{1, 1});
+            const u16x2 d = __builtin_elementwise_min(__builtin_bit_cast(u16x2, tk[w] ^ row), u16x2{1, 1});
             a[w] = (__builtin_bit_cast(uint32_t, d) ^ 0x10001u) * 0x3f80u;  // 1.0 in bf16 where they agree
           }
-          hot[m] = __builtin_bit_cast(bf16x8, a);
-        }
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          u32x4a y;
-#pragma unroll
-          for (int w = 0; w < 4; ++w) {
-            y[w] = x[q][s][w] & keep[w];
-            big16 = __builtin_elementwise_max(big16, __builtin_bit_cast(u16x2, y[w] & 0x7fff7fffu));
-          }
-#pragma unroll
-          for (int m = 0; m < MT; ++m)
-            acc[m][q] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(hot[m], __builtin_bit_cast(bf16x8, y), acc[m][q], 0, 0, 0);
+          acc[m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, y),
+                                                           acc[m], 0, 0, 0);
         }
       } else {
-        const uint2 tk = *reinterpret_cast<const uint2*>(&tok[i + g * 16 + s * 4]);  // 4 tokens
+        const uint2 tk = *reinterpret_cast<const uint2*>(&tok[i + c * 4]);  // 4 tokens
         const uint32_t t4[4] = {tk.x & 0xffffu, tk.x >> 16, tk.y & 0xffffu, tk.y >> 16};
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const uint32_t keep = t4[j] == 0xffffu ? 0u : 0xffffffffu;
-          float hot[MT];
+          const uint32_t y = t4[j] == 0xffffu ? 0u : x[j], a = y & 0x7fffffffu;
+          big32 = big32 > a ? big32 : a;
 #pragma unroll
-          for (int m = 0; m < MT; ++m) hot[m] = t4[j] == (uint32_t)(m * 16 + n) ? 1.0f : 0.0f;
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const uint32_t y = x[q][s][j] & keep, a = y & 0x7fffffffu;
-            big32 = big32 > a ? big32 : a;
-#pragma unroll
-            for (int m = 0; m < MT; ++m)
-              acc[m][q] = __builtin_amdgcn_mfma_f32_16x16x4f32(hot[m], __uint_as_float(y), acc[m][q], 0, 0, 0);
-          }
+          for (int m = 0; m < MT; ++m)
+            acc[m] = __builtin_amdgcn_mfma_f32_16x16x4f32(t4[j] == (uint32_t)(m * 16 + n) ? 1.0f : 0.0f,
+                                                          __uint_as_float(y), acc[m], 0, 0, 0);
         }
       }
     }
+    wave_sync();  // the tile has been read
   }
   const int bad = BF ? (big16[0] >= 0x7f80u || big16[1] >= 0x7f80u) : big32 >= 0x7f800000u;
   float* out = p.part + seg * p.V * p.E;
@@ -185,26 +161,15 @@ __global__ __launch_bounds__(256) void embed_few_kernel(FewParams p) {
     }
     return;
   }
-  // the waves' sums in order; lane: row 4 g + i of a tile, channel n
-  for (int w = 0; w < 4; ++w) {
-    if (wave == w) {
+  // lane: rows 4 g + i of a tile, channel n
+  const int64_t e = e0 + wave * 16 + n;
 #pragma unroll
-      for (int m = 0; m < MT; ++m)
+  for (int m = 0; m < MT; ++m)
 #pragma unroll
-        for (int q = 0; q < 4; ++q)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            float* s = &sums[(m * 16 + g * 4 + i) * 64 + q * 16 + n];
-            *s = w == 0 ? acc[m][q][i] : *s + acc[m][q][i];
-          }
+    for (int i = 0; i < 4; ++i) {
+      const int v = m * 16 + g * 4 + i;
+      if (v < p.V && e < p.E) out[v * p.E + e] = acc[m][i];
     }
-    __syncthreads();
-  }
-  for (int i = threadIdx.x; i < ROWS * 64; i += 256) {
-    const int v = i >> 6;
-    const int64_t e = e0 + (i & 63);
-    if (v < p.V && e < p.E) out[v * p.E + e] = sums[i];
-  }
 }
 
 // dweight from the segments' sums: 64 elements per workgroup, the segments split over 4 waves, each in order,
@@ -243,9 +208,9 @@ bool embed_few_rows(int64_t V, bool io_bf16) { return V <= (io_bf16 ? 64 : 32); 
 
 void plan_embed_few(int64_t Bsz, int64_t L, int64_t V, int64_t E, EmbedBwdPlan* pl) {
   const int64_t groups = (E + 63) / 64;
-  int64_t seg = (Bsz * L * groups / 2048 + 255) / 256 * 256;  // about 2048 workgroups
+  int64_t seg = (Bsz * L * groups / 2048 + 511) / 512 * 512;  // whole tiles; 2048 workgroups or more
   if (seg > kMaxSeg) seg = kMaxSeg;
-  if (seg < 256) seg = 256;
+  if (seg < 512) seg = 512;
   pl->few = true;
   pl->run = seg;
   pl->chunks = Bsz * ((L + seg - 1) / seg);
