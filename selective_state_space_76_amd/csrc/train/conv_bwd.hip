@@ -9,12 +9,12 @@
 //
 // Layout: LN lanes (64, or 16 for short rows) own one segment of LN * V * P steps of one row: a lane holds P pieces
 // of 16 bytes (V steps each, LN * V steps apart) of x and dout, all in flight before any arithmetic.  A piece needs
-// H inputs from its left neighbour and H values of g from its right one; both come by cross-lane
-// moves.  The pieces are walked from right to left, so a pass finds the g that follows its last lane
-// in the first lane of the pass before; the g after the whole segment (the next segment's) is
-// recomputed by the last lane.  Rows may begin at any element: the pieces are loaded at the alignment
-// of one element, so odd lengths take the same path.  Each segment's K + 1 sums go to memory and are added
-// by a second kernel in a fixed order.
+// H inputs from its left neighbour and H values of g from its right one; both come by DPP shifts.  The
+// pieces are walked from right to left, so a pass finds the g that follows its last lane in the first lane of
+// the pass before; the g after the whole segment (the next segment's) is recomputed by the last lane.  Rows may
+// begin at any element: the pieces lie at addresses that are multiples of 16 bytes, so the first one of a row may
+// begin before it and the last one end behind it.  Each segment's K + 1 sums go to memory and are added by a
+// second kernel in a fixed order.
 #include "../ssm_device.h"
 #include "train_launch.h"
 
@@ -22,52 +22,69 @@ namespace ssm {
 
 namespace {
 
-constexpr int kPasses = 4;
+#ifndef PASSES
+#define PASSES 4
+#endif
+constexpr int kPasses = PASSES;
 
-template <typename IO> struct Piece;
-template <> struct Piece<float> { typedef uint32_t type __attribute__((ext_vector_type(4), aligned(4))); };
-template <> struct Piece<bf16_t> { typedef uint32_t type __attribute__((ext_vector_type(4), aligned(2))); };
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
-// V steps from p, of which the first c exist (the others are zero)
-template <typename IO, int V>
-__device__ __forceinline__ void load_piece(const IO* p, int c, float (&x)[V]) {
-  if (c >= V) {
-    const auto q = __builtin_nontemporal_load(reinterpret_cast<const typename Piece<IO>::type*>(p));
-    if constexpr (V == 8) {
+// 16 bytes as V = 8 or 4 floats
+__device__ __forceinline__ void widen(const u32x4& q, float (&x)[8]) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        x[2 * i] = __uint_as_float(q[i] << 16);
-        x[2 * i + 1] = __uint_as_float(q[i] & 0xffff0000u);
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) x[i] = __uint_as_float(q[i]);
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < V; ++i) x[i] = i < c ? to_f32(p[i]) : 0.0f;
+  for (int i = 0; i < 4; ++i) {
+    x[2 * i] = __uint_as_float(q[i] << 16);
+    x[2 * i + 1] = __uint_as_float(q[i] & 0xffff0000u);
   }
 }
+__device__ __forceinline__ void widen(const u32x4& q, float (&x)[4]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) x[i] = __uint_as_float(q[i]);
+}
+__device__ __forceinline__ u32x4 narrow(const float (&x)[8]) {
+  u32x4 q;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    q[i] = (uint32_t)__builtin_bit_cast(uint16_t, (__bf16)x[2 * i]) |
+           ((uint32_t)__builtin_bit_cast(uint16_t, (__bf16)x[2 * i + 1]) << 16);
+  return q;
+}
+__device__ __forceinline__ u32x4 narrow(const float (&x)[4]) {
+  return u32x4{__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3])};
+}
+__device__ __forceinline__ uint32_t bits_of(bf16_t v) { return v; }
+__device__ __forceinline__ uint32_t bits_of(float v) { return __float_as_uint(v); }
 
-template <typename IO, int V>
-__device__ __forceinline__ void store_piece(IO* p, int c, const float (&x)[V]) {
-  if (c >= V) {
-    typename Piece<IO>::type q;
-    if constexpr (V == 8) {
+// The piece at p; where it is not whole, its elements lo..hi-1 (the others are zero).
+template <typename IO>
+__device__ __forceinline__ u32x4 load_piece(const IO* p, int lo, int hi) {
+  constexpr int V = 16 / (int)sizeof(IO);
+  if (lo == 0 && hi == V) return __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(p));
+  u32x4 q = {0u, 0u, 0u, 0u};
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        q[i] = (uint32_t)__builtin_bit_cast(uint16_t, (__bf16)x[2 * i]) |
-               ((uint32_t)__builtin_bit_cast(uint16_t, (__bf16)x[2 * i + 1]) << 16);
-    } else {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) q[i] = __float_as_uint(x[i]);
+  for (int i = 0; i < V; ++i)
+    if (i >= lo && i < hi) {
+      if constexpr (V == 8) q[i >> 1] |= bits_of(p[i]) << (16 * (i & 1));
+      else q[i] = bits_of(p[i]);
     }
-    __builtin_nontemporal_store(q, reinterpret_cast<typename Piece<IO>::type*>(p));
-  } else {
-#pragma unroll
-    for (int i = 0; i < V; ++i)
-      if (i < c) store_io(p + i, x[i]);
-  }
+  return q;
+}
+
+// The value of the lane to the left (right) in the group of LN lanes; its first (last) lane gets `end`.
+template <int LN>
+__device__ __forceinline__ uint32_t from_left(uint32_t v, uint32_t end) {
+  return (uint32_t)__builtin_amdgcn_update_dpp((int)end, (int)v, LN == 64 ? 0x138 : 0x111, 0xf, 0xf, false);
+}
+template <int LN>
+__device__ __forceinline__ float from_right(float v, float end) {
+  return __uint_as_float((uint32_t)__builtin_amdgcn_update_dpp((int)__float_as_uint(end), (int)__float_as_uint(v),
+                                                               LN == 64 ? 0x130 : 0x101, 0xf, 0xf, false));
+}
+// the group's first or last lane's value, in all of its lanes
+template <int LN, bool LAST>
+__device__ __forceinline__ uint32_t of_lane(uint32_t v) {
+  if constexpr (LN == 64) return (uint32_t)__builtin_amdgcn_readlane((int)v, LAST ? 63 : 0);
+  else return (uint32_t)__builtin_amdgcn_mov_dpp((int)v, LAST ? 0x15f : 0x150, 0xf, 0xf, true);
 }
 
 __device__ __forceinline__ float silu_slope(float a) {
@@ -82,61 +99,97 @@ __global__ __launch_bounds__(256) void conv_bwd_kernel(ConvBwdParams p) {
   constexpr int V = 16 / (int)sizeof(IO);
   constexpr int H = K - 1, HA = H > 0 ? H : 1;
   constexpr int P = kPasses;
-  const int64_t rows = p.Bsz * p.Dm;
-  const int64_t unit = (int64_t)blockIdx.x * (256 / LN) + threadIdx.x / LN;  // row segment
+  constexpr int W = (H * (int)sizeof(IO) + 3) / 4;  // words that hold a piece's last H steps
+  constexpr int SEG = LN * V * P;
   const int lane = threadIdx.x % LN;
-  const bool live = unit < rows * p.S;
-  const int64_t row = live ? unit / p.S : 0, seg = live ? unit - row * p.S : 0;
-  const int64_t d = row % p.Dm;
+  // row segment; their number fits 31 bits, so the divisions take 32
+  uint32_t unit = blockIdx.x * (256 / LN) + threadIdx.x / LN;
+  const bool live = unit < p.units;
+  unit = live ? unit : 0;
+  const uint32_t r32 = unit / (uint32_t)p.S, s32 = unit - r32 * (uint32_t)p.S;
+  const uint32_t b32 = r32 / (uint32_t)p.Dm, d32 = r32 - b32 * (uint32_t)p.Dm;
+  const int64_t row = r32, seg = s32, d = d32;
   const IO* x = static_cast<const IO*>(p.x) + row * p.L;
   const IO* dout = static_cast<const IO*>(p.dout) + row * p.L;
-  IO* dx = static_cast<IO*>(p.dx) + row * p.L;
-  const IO* init = p.init ? static_cast<const IO*>(p.init) + row * H : nullptr;
-  const IO* dfin = p.dfinal ? static_cast<const IO*>(p.dfinal) + row * H : nullptr;
-  const int64_t t0 = seg * (LN * V * P);  // the segment's first step
+  const IO* init = p.init && live ? static_cast<const IO*>(p.init) + row * H : nullptr;
+  const IO* dfin = p.dfinal && live ? static_cast<const IO*>(p.dfinal) + row * H : nullptr;
   const int64_t L = live ? p.L : 0;
+  // the segment's first step: the row's first piece begins up to V - 1 steps before the row
+  const int64_t t0 = seg * SEG - (row * p.L) % V;
+  const int begin = t0 < 0 ? (int)-t0 : 0;                     // of the row within the segment
+  const int end = L - t0 < SEG + 8 ? (int)(L - t0) : SEG + 8;  // where it lies within the segment or close behind
+  x += t0;
+  dout += t0;
 
-  float xs[P][V], go[P][V];
-  int cnt[P];
+  u32x4 xq[P], gq[P];
 #pragma unroll
   for (int j = 0; j < P; ++j) {
-    const int64_t t = t0 + (j * LN + lane) * V;
-    const int64_t left = L - t;
-    cnt[j] = left >= V ? V : left > 0 ? (int)left : 0;
-    load_piece<IO, V>(x + t, cnt[j], xs[j]);
-    load_piece<IO, V>(dout + t, cnt[j], go[j]);
+    const int i = (j * LN + lane) * V;
+    const int lo = begin - i > 0 ? begin - i : 0, hi = end - i < V ? end - i : V;
+    xq[j] = load_piece(x + i, lo, hi);
+    gq[j] = load_piece(dout + i, lo, hi);
   }
   float w[K];
 #pragma unroll
   for (int k = 0; k < K; ++k) w[k] = p.w[d * K + k];
   const float bias = p.bias ? p.bias[d] : 0.0f;
 
-  // the H inputs before the segment (lane 0 uses them), and g of the H steps after it (last lane)
-  auto input = [&](int64_t t) -> float {
-    if (t >= 0) return t < L ? to_f32(x[t]) : 0.0f;
-    return init && live && t >= -H ? to_f32(init[H + t]) : 0.0f;
+  // single steps, counted from the segment's first, for its ends
+  auto input = [&](int i) -> uint32_t {
+    if (t0 + i >= 0) return i < end ? bits_of(x[i]) : 0u;
+    return init && t0 + i >= -H ? bits_of(init[H + t0 + i]) : 0u;
   };
-  float before[HA], after[HA];
-#pragma unroll
-  for (int k = 0; k < HA; ++k) before[k] = after[k] = 0.0f;
-  if constexpr (H > 0) {
-    if (lane == 0) {
-#pragma unroll
-      for (int k = 0; k < H; ++k) before[k] = input(t0 - H + k);
-    }
-    const int64_t te = t0 + LN * V * P;
-    if (lane == LN - 1 && te < L) {
+  auto value = [](uint32_t v) -> float { return __uint_as_float(sizeof(IO) == 2 ? v << 16 : v); };
+  auto gradient = [&](int i, float (&g)[HA]) {  // g of the H steps from i on
+    if constexpr (H > 0) {
       float xv[2 * H];
 #pragma unroll
-      for (int k = 0; k < 2 * H; ++k) xv[k] = input(te - H + k);
+      for (int k = 0; k < 2 * H; ++k) xv[k] = value(input(i - H + k));
 #pragma unroll
       for (int e = 0; e < H; ++e) {
         float a = bias;
 #pragma unroll
         for (int k = 0; k < K; ++k) a = __builtin_fmaf(w[k], xv[e + k], a);
-        after[e] = te + e < L ? to_f32(dout[te + e]) * silu_slope(a) : 0.0f;
+        g[e] = i + e < end ? to_f32(dout[i + e]) * silu_slope(a) : 0.0f;
       }
     }
+  };
+  uint32_t before[W > 0 ? W : 1];  // the words before the segment (first lane)
+  float after[HA];                 // g behind it (last lane)
+#pragma unroll
+  for (int k = 0; k < (W > 0 ? W : 1); ++k) before[k] = 0u;
+#pragma unroll
+  for (int k = 0; k < HA; ++k) after[k] = 0.0f;
+  if constexpr (H > 0) {
+    if (lane == 0 && live) {
+#pragma unroll
+      for (int k = 0; k < W; ++k) {
+        if constexpr (V == 8) before[k] = input(-2 * (W - k)) | input(-2 * (W - k) + 1) << 16;
+        else before[k] = input(k - W);
+      }
+      if (begin > 0) {  // the steps before the row in its first piece are the initial state
+#pragma unroll
+        for (int e = 0; e < V; ++e)
+          if (e < begin) {
+            if constexpr (V == 8) xq[0][e >> 1] |= input(e) << (16 * (e & 1));
+            else xq[0][e] = input(e);
+          }
+      }
+      if (seg == 0 && p.dinit) {
+        float g[HA];
+        gradient(begin, g);
+        IO* di = static_cast<IO*>(p.dinit) + row * H;
+#pragma unroll
+        for (int i = 0; i < H; ++i) {  // dx at step i - H
+          float s = 0.0f;
+#pragma unroll
+          for (int k = 0; k <= i; ++k) s = __builtin_fmaf(w[k], g[i - k], s);
+          if (dfin && i >= L) s += to_f32(dfin[i - L]);  // L < H: the final state still holds it
+          store_io(di + i, s);
+        }
+      }
+    }
+    if (lane == LN - 1 && end > SEG) gradient(SEG, after);
   }
 
   float sw[K], sb = 0.0f;
@@ -144,36 +197,40 @@ __global__ __launch_bounds__(256) void conv_bwd_kernel(ConvBwdParams p) {
   for (int k = 0; k < K; ++k) sw[k] = 0.0f;
 #pragma unroll
   for (int j = P - 1; j >= 0; --j) {
-    float xe[H + V];  // the piece and the H inputs before it
+    float xe[H + V], xv[V], go[V];  // xe: the piece and the H inputs before it
+    widen(xq[j], xv);
+    widen(gq[j], go);
+    if constexpr (H > 0) {
+      u32x4 left = {0u, 0u, 0u, 0u};
 #pragma unroll
-    for (int k = 0; k < H; ++k) {
-      float left = __shfl_up(xs[j][V - H + k], 1, LN);
-      const float prev = j > 0 ? __shfl(xs[j > 0 ? j - 1 : 0][V - H + k], LN - 1, LN) : before[k];
-      xe[k] = lane == 0 ? prev : left;
+      for (int k = 0; k < W; ++k) {
+        const uint32_t end = j > 0 ? of_lane<LN, true>(xq[j > 0 ? j - 1 : 0][4 - W + k]) : before[k];
+        left[4 - W + k] = from_left<LN>(xq[j][4 - W + k], end);
+      }
+      float lv[V];
+      widen(left, lv);
+#pragma unroll
+      for (int k = 0; k < H; ++k) xe[k] = lv[V - H + k];
     }
 #pragma unroll
-    for (int e = 0; e < V; ++e) xe[H + e] = xs[j][e];
+    for (int e = 0; e < V; ++e) xe[H + e] = xv[e];
     float ge[V + HA];
 #pragma unroll
     for (int e = 0; e < V; ++e) {
       float a = bias;
 #pragma unroll
       for (int k = 0; k < K; ++k) a = __builtin_fmaf(w[k], xe[e + k], a);
-      ge[e] = go[j][e] * silu_slope(a);
+      ge[e] = go[e] * silu_slope(a);
       sb += ge[e];
 #pragma unroll
       for (int k = 0; k < K; ++k) sw[k] = __builtin_fmaf(ge[e], xe[e + k], sw[k]);
     }
-    float first[HA];
 #pragma unroll
     for (int k = 0; k < H; ++k) {
-      const float right = __shfl_down(ge[k], 1, LN);
-      first[k] = __shfl(ge[k], 0, LN);
-      ge[V + k] = lane == LN - 1 ? after[k] : right;
+      ge[V + k] = from_right<LN>(ge[k], after[k]);
+      after[k] = __uint_as_float(of_lane<LN, false>(__float_as_uint(ge[k])));
     }
-#pragma unroll
-    for (int k = 0; k < H; ++k) after[k] = first[k];
-    const int64_t t = t0 + (j * LN + lane) * V;
+    const int i = (j * LN + lane) * V;
     float dxe[V];
 #pragma unroll
     for (int e = 0; e < V; ++e) {
@@ -183,26 +240,22 @@ __global__ __launch_bounds__(256) void conv_bwd_kernel(ConvBwdParams p) {
       dxe[e] = s;
     }
     if constexpr (H > 0) {
-      if (dfin && t + V > L - H) {  // the last H inputs are the final state
+      if (dfin && i + V > end - H) {  // the last H inputs are the final state
 #pragma unroll
         for (int e = 0; e < V; ++e) {
-          const int64_t q = t + e - (L - H);
+          const int q = i + e - (end - H);
           if (q >= 0 && q < H) dxe[e] += to_f32(dfin[q]);
         }
       }
-      if (j == 0 && t == 0 && p.dinit && live) {
-        IO* di = static_cast<IO*>(p.dinit) + row * H;
-#pragma unroll
-        for (int i = 0; i < H; ++i) {  // step i - H
-          float s = 0.0f;
-#pragma unroll
-          for (int k = 0; k <= i; ++k) s = __builtin_fmaf(w[k], ge[i - k], s);
-          if (dfin && i >= L) s += to_f32(dfin[i - L]);  // L < H: the final state still holds it
-          store_io(di + i, s);
-        }
-      }
     }
-    if (cnt[j] > 0) store_piece<IO, V>(dx + t, cnt[j], dxe);
+    IO* dx = static_cast<IO*>(p.dx) + row * p.L + t0 + i;
+    if (i >= begin && i + V <= end) {
+      __builtin_nontemporal_store(narrow(dxe), reinterpret_cast<u32x4*>(dx));
+    } else {
+#pragma unroll
+      for (int e = 0; e < V; ++e)
+        if (i + e >= begin && i + e < end) store_io(dx + e, dxe[e]);
+    }
   }
 
   // the segment's sums over its lanes
@@ -213,8 +266,7 @@ __global__ __launch_bounds__(256) void conv_bwd_kernel(ConvBwdParams p) {
     for (int k = 0; k < K; ++k) sw[k] += __shfl_xor(sw[k], o, LN);
   }
   if (live && lane == 0) {
-    const int64_t b = row / p.Dm;
-    float* o = p.part + ((b * p.S + seg) * p.Dm + d) * (K + 1);
+    float* o = p.part + (((int64_t)b32 * p.S + seg) * p.Dm + d) * (K + 1);
 #pragma unroll
     for (int k = 0; k < K; ++k) o[k] = sw[k];
     o[K] = sb;
@@ -258,18 +310,17 @@ int64_t conv_bwd_segments(int64_t L, bool bf16, int* lanes) {
   const int64_t V = bf16 ? 8 : 4;
   *lanes = L <= 32 * V ? 16 : 64;
   const int64_t seg = *lanes * V * kPasses;
-  return (L + seg - 1) / seg;
+  return (L + (L % V ? V - 1 : 0) + seg - 1) / seg;  // rows of whole pieces all begin with one
 }
 
 namespace {
 
 template <typename IO, int K>
 void launch_k(const ConvBwdParams& p, hipStream_t s) {
-  const int64_t units = p.Bsz * p.Dm * p.S;
   if (p.lanes == 16)
-    hipLaunchKernelGGL((conv_bwd_kernel<IO, K, 16>), dim3((unsigned)((units + 15) / 16)), dim3(256), 0, s, p);
+    hipLaunchKernelGGL((conv_bwd_kernel<IO, K, 16>), dim3((p.units + 15) / 16), dim3(256), 0, s, p);
   else
-    hipLaunchKernelGGL((conv_bwd_kernel<IO, K, 64>), dim3((unsigned)((units + 3) / 4)), dim3(256), 0, s, p);
+    hipLaunchKernelGGL((conv_bwd_kernel<IO, K, 64>), dim3((p.units + 3) / 4), dim3(256), 0, s, p);
 }
 
 template <typename IO>

@@ -104,7 +104,7 @@ ssm_status ssm_conv1d_bwd(int64_t batch, int64_t dim, int64_t seqlen, int64_t wi
   memset(&p, 0, sizeof(p));
   p.x = x; p.w = weight; p.bias = bias; p.init = init; p.dout = dout; p.dfinal = dfinal;
   p.dx = dx; p.dinit = dinit; p.dw = dweight; p.db = dbias; p.part = static_cast<float*>(workspace);
-  p.Bsz = batch; p.Dm = dim; p.L = seqlen; p.S = pl.S; p.K = (int)width; p.lanes = pl.lanes;
+  p.Bsz = batch; p.Dm = dim; p.L = seqlen; p.S = pl.S; p.units = (uint32_t)(pl.bd * pl.S); p.K = (int)width; p.lanes = pl.lanes;
   return launch_status(ssm::launch_conv_bwd(p, io_dtype == SSM_BF16, reinterpret_cast<hipStream_t>(stream)));
 }
 

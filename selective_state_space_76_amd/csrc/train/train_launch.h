@@ -21,6 +21,7 @@ struct ConvBwdParams {
   float* part;          // [B*S][D][K+1]: dweight and dbias summed over one segment of one row
   int64_t Bsz, Dm, L;
   int64_t S;            // segments per row
+  uint32_t units;       // segments of all rows, below 2^31
   int K;
   int lanes;            // lanes per row segment, 16 or 64
 };
