@@ -103,18 +103,20 @@ __device__ __forceinline__ void store_high(bf16_t* p, int c, const uint32_t (&x)
       if (i < c) p[i] = (bf16_t)(x[i] >> 16);
   }
 }
-__device__ __forceinline__ void load_codes(const uint8_t* p, int c, uint32_t (&x)[8]) {
-  if (c > 0) {  // a block's room is there even where its tensor ends inside it
-    const u32x2 q = __builtin_nontemporal_load(reinterpret_cast<const u32x2*>(p));
-#pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = i < c ? (q[i >> 2] >> (8 * (i & 3))) & 255u : 0u;
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = 0u;
+// 8 codes, c of which are the tensor's (a block's room is there even where its tensor ends inside it)
+__device__ __forceinline__ u32x2 load_codes(const uint8_t* p, int c) {
+  u32x2 q = {0u, 0u};
+  if (c > 0) q = __builtin_nontemporal_load(reinterpret_cast<const u32x2*>(p));
+  if (c < 8) {
+    const uint64_t keep = (1ull << (8 * c)) - 1;
+    q[0] &= (uint32_t)keep;
+    q[1] &= (uint32_t)(keep >> 32);
   }
+  return q;
 }
+// codes past the tensor's end are zero
 __device__ __forceinline__ void store_codes(uint8_t* p, int c, const uint32_t (&x)[8]) {
-  if (c > 0) {  // codes past the tensor's end are zero
+  if (c > 0) {
     u32x2 q = {0u, 0u};
 #pragma unroll
     for (int i = 0; i < 8; ++i) q[i >> 2] |= x[i] << (8 * (i & 3));
@@ -146,7 +148,8 @@ __device__ __forceinline__ int find(const AdamTable& t, uint32_t block) {
   return lo;
 }
 
-__device__ __forceinline__ float code_value(uint32_t c, uint32_t K) { return __uint_as_float(c ? (c + K) << 20 : 0u); }
+__device__ __forceinline__ uint32_t code_bits(uint32_t c, uint32_t K) { return c ? (c + K) << 20 : 0u; }
+__device__ __forceinline__ int32_t clamp_code(int32_t q, int32_t lo, int32_t hi) { return q < lo ? lo : q > hi ? hi : q; }
 
 // base of a block from the bits of its largest magnitude: that element, rounded up, gets code `top`
 __device__ __forceinline__ uint32_t block_base(uint32_t amax, uint32_t top) {
@@ -185,18 +188,19 @@ __global__ __launch_bounds__(256) void adamw_kernel(AdamTable t, AdamParams a) {
     else load<V>(static_cast<const float*>(t.p[k]) + i, c, p);
     const int64_t blk = (off + i) / kAdamBlock;
     if constexpr (S8) {
-      uint32_t mc[8], vc[8], mk = 0, vk = 0;
-      load_codes(static_cast<const uint8_t*>(a.m) + off + i, c, mc);
-      load_codes(static_cast<const uint8_t*>(a.v) + off + i, c, vc);
+      const u32x2 mw = load_codes(static_cast<const uint8_t*>(a.m) + off + i, c);
+      const u32x2 vw = load_codes(static_cast<const uint8_t*>(a.v) + off + i, c);
+      uint32_t mk = 0, vk = 0;
       if (c > 0) {
         mk = (uint32_t)(int32_t)a.mb[blk];
         vk = (uint32_t)(int32_t)a.vb[blk];
       }
 #pragma unroll
       for (int e = 0; e < V; ++e) {
-        const float x = code_value(mc[e] & 127u, mk);
-        m[e] = mc[e] & 128u ? -x : x;
-        v[e] = code_value(vc[e], vk);
+        const uint32_t w = mw[e >> 2], z = vw[e >> 2];
+        const uint32_t x = code_bits((w >> (8 * (e & 3))) & 127u, mk);
+        m[e] = __uint_as_float(x | ((w << (24 - 8 * (e & 3))) & 0x80000000u));
+        v[e] = __uint_as_float(code_bits((z >> (8 * (e & 3))) & 255u, vk));
       }
     } else {
       load<V>(static_cast<const float*>(a.m) + off + i, c, m);
@@ -213,15 +217,15 @@ __global__ __launch_bounds__(256) void adamw_kernel(AdamTable t, AdamParams a) {
       const float ge = g[e] * clip;
       m[e] = m[e] * a.b1 + ge * a.c1;
       v[e] = v[e] * a.b2 + ge * a.c2 * ge;
-      const float den = __builtin_amdgcn_sqrtf(v[e]) * a.isb + a.eps;
-      p[e] = p[e] * a.decay - m[e] * a.step * rcp_(den);
+      const float den = __builtin_fmaf(__builtin_amdgcn_sqrtf(v[e]), a.isb, a.eps);
+      p[e] = __builtin_fmaf(-(m[e] * a.step), rcp_(den), p[e] * a.decay);
       if constexpr (PB) {
         if constexpr (MW) {
           pb[e] = (uint32_t)__builtin_bit_cast(uint16_t, (__bf16)p[e]) << 16;
         } else {
           const uint32_t b = __float_as_uint(p[e]);
-          const bool finite = (b & 0x7f800000u) != 0x7f800000u;
-          pb[e] = finite ? b + ((h[e] * 0x3C6EF373u) >> 16) : b | (b & 0xffffu ? 0x10000u : 0u);
+          // what is not finite is kept: a NaN computed here is quiet, its mark is in the upper half
+          pb[e] = b + (__builtin_isfinite(p[e]) ? (h[e] * 0x3C6EF373u) >> 16 : 0u);
         }
       }
     }
@@ -229,27 +233,36 @@ __global__ __launch_bounds__(256) void adamw_kernel(AdamTable t, AdamParams a) {
     if constexpr (PB) store_high<V>(static_cast<bf16_t*>(t.p[k]) + i, c, pb);
     else store<V>(static_cast<float*>(t.p[k]) + i, c, p);
     if constexpr (S8) {
+      // elements that are not there have been zero all along, and stay so
       uint32_t am = 0, av = 0;
 #pragma unroll
       for (int e = 0; e < V; ++e) {
-        const uint32_t x = e < c ? __float_as_uint(m[e]) & 0x7fffffffu : 0u, y = e < c ? __float_as_uint(v[e]) : 0u;
+        const uint32_t x = __float_as_uint(m[e]) & 0x7fffffffu, y = __float_as_uint(v[e]);
         am = am > x ? am : x;
         av = av > y ? av : y;
       }
       const uint32_t mk = block_base(row_max(am), 127u), vk = block_base(row_max(av), 255u);
       const uint32_t least = (mk + 1) << 20;
       uint32_t mc[8], vc[8];
+      bool under = false;
 #pragma unroll
       for (int e = 0; e < V; ++e) {
-        const uint32_t x = __float_as_uint(m[e]) & 0x7fffffffu, rm = h[e] & 0xffffu;
-        const uint32_t q = ((x + (rm << 4) + 8u) >> 20) - mk;
-        const bool up = __uint_as_float(x) > __uint_as_float(least) * ((float)rm * 0x1p-16f + 0x1p-17f);
-        mc[e] = (x < least ? (uint32_t)up : q < 127u ? q : 127u) | (m[e] < 0.0f ? 128u : 0u);
-        const uint32_t y = __float_as_uint(v[e]), rv = h[e] >> 16;
-        const int32_t r = (int32_t)((y + (rv << 4) + 8u) >> 20) - (int32_t)vk;
-        vc[e] = y == 0u ? 0u : (uint32_t)(r < 1 ? 1 : r > 255 ? 255 : r);
-        if (e >= c) mc[e] = vc[e] = 0u;
+        const uint32_t x = __float_as_uint(m[e]) & 0x7fffffffu, y = __float_as_uint(v[e]);
+        const uint32_t rm = ((h[e] << 4) & 0xffff0u) | 8u, rv = ((h[e] >> 12) & 0xffff0u) | 8u;
+        mc[e] = (uint32_t)clamp_code((int32_t)((x + rm) >> 20) - (int32_t)mk, 0, 127);
+        vc[e] = (uint32_t)clamp_code((int32_t)((y + rv) >> 20) - (int32_t)vk, (int32_t)(y < 1u ? y : 1u), 255);
+        under |= x - 1u < least - 1u;  // 0 < x < least
       }
+      if (under) {  // below the smallest code: that code or zero
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+          const uint32_t x = __float_as_uint(m[e]) & 0x7fffffffu;
+          const bool up = __uint_as_float(x) > __uint_as_float(least) * ((float)(h[e] & 0xffffu) * 0x1p-16f + 0x1p-17f);
+          if (x < least) mc[e] = up ? 1u : 0u;
+        }
+      }
+#pragma unroll
+      for (int e = 0; e < V; ++e) mc[e] |= (__float_as_uint(m[e]) >> 24) & 128u;
       store_codes(static_cast<uint8_t*>(a.m) + off + i, c, mc);
       store_codes(static_cast<uint8_t*>(a.v) + off + i, c, vc);
       if (c > 0 && (threadIdx.x & 15) == 0) {
@@ -318,20 +331,23 @@ __global__ __launch_bounds__(256) void state_values_kernel(int64_t n, const uint
                                                            const int16_t* mb, const int16_t* vb, bf16_t* mo, bf16_t* vo) {
   const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 8;
   if (i >= n) return;
-  uint32_t c[8], w[8];
+  uint32_t x[8];
   if (mo) {
-    load_codes(m + i, 8, c);
+    const u32x2 w = load_codes(m + i, 8);
     const uint32_t K = (uint32_t)(int32_t)mb[i / kAdamBlock];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) w[e] = (c[e] & 127u ? ((c[e] & 127u) + K) << 20 : 0u) | (c[e] & 128u) << 24;
-    store_high<8>(mo + i, 8, w);
+    for (int e = 0; e < 8; ++e) {
+      const uint32_t c = w[e >> 2] >> (8 * (e & 3));
+      x[e] = code_bits(c & 127u, K) | ((c << 24) & 0x80000000u);
+    }
+    store_high<8>(mo + i, 8, x);
   }
   if (vo) {
-    load_codes(v + i, 8, c);
+    const u32x2 w = load_codes(v + i, 8);
     const uint32_t K = (uint32_t)(int32_t)vb[i / kAdamBlock];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) w[e] = c[e] ? (c[e] + K) << 20 : 0u;
-    store_high<8>(vo + i, 8, w);
+    for (int e = 0; e < 8; ++e) x[e] = code_bits((w[e >> 2] >> (8 * (e & 3))) & 255u, K);
+    store_high<8>(vo + i, 8, x);
   }
 }
 

@@ -95,7 +95,7 @@ __device__ __forceinline__ float silu_slope(float a) {
 }  // namespace
 
 template <typename IO, int K, int LN>
-__global__ __launch_bounds__(256) void conv_bwd_kernel(ConvBwdParams p) {
+__global__ __launch_bounds__(256, 5) void conv_bwd_kernel(ConvBwdParams p) {
   constexpr int V = 16 / (int)sizeof(IO);
   constexpr int H = K - 1, HA = H > 0 ? H : 1;
   constexpr int P = kPasses;
