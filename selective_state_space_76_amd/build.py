@@ -19,7 +19,7 @@ SOURCES = [os.path.join(CSRC, f) for f in (
     "train/adamw.hip", "train/train_abi.cpp")]
 HEADERS = [os.path.join(CSRC, "ssm_launch.h"), os.path.join(CSRC, "ssm_device.h"),
            os.path.join(CSRC, "scan_bwd_kernel.h"),
-           os.path.join(CSRC, "train", "train_launch.h"), os.path.join(CSRC, "train", "embed_device.h"),
+           os.path.join(CSRC, "train", "train_launch.h"), os.path.join(CSRC, "train", "train_device.h"),
            os.path.join(ROOT, "include", "ssm_scan.h")]
 ARCH = "gfx950"
 

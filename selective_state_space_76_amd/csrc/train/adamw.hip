@@ -7,7 +7,11 @@
 // table in memory to fill, keep or wait for).  A workgroup owns one chunk of kAdamChunk elements of one
 // tensor, found by bisection over the first workgroup of each tensor; a lane owns V consecutive elements
 // (4 with fp32 states, 8 with 8-bit ones, so that every stream is read in 8- or 16-byte pieces).
-// The step is bound by HBM: every byte of weights, gradients and states is touched once.
+// With fp32 states the step is bound by HBM: every byte is touched once, at 5.8 TB/s (a copy reaches 5.2, a plain
+// sum 6.0): 127 M bf16 weights with masters 0.66 ms.  With 8-bit states the instructions (about 70 an
+// element, three of them 32-bit integer products for the random numbers) take nearly as long as the 10 bytes:
+// 305 M bf16 weights 0.61 ms, 4.9 TB/s (0.79 ms with 87 instructions).  Loading the next piece before
+// the present one is worked on gained nothing with either.
 //
 // 8-bit states.  A positive float's bit pattern is an increasing integer, and its top 12 bits a number
 // of 4 significant bits.  A block of 128 elements (16 lanes of 8) keeps K, the largest element's top
@@ -18,7 +22,10 @@
 // rounds up with the odds of the part cut off, which keeps the expected state exact.  A v > 0 is
 // never rounded to zero: a zero under a nonzero m would divide by eps alone.  m below its smallest code
 // becomes that code with the odds that keep its mean, else zero.
+#include <type_traits>
+
 #include "../ssm_device.h"
+#include "train_device.h"
 #include "train_launch.h"
 
 namespace ssm {
@@ -37,43 +44,6 @@ __host__ __device__ __forceinline__ uint32_t mix32(uint32_t x) {
   return x ^ (x >> 16);
 }
 
-// V consecutive floats or bf16 numbers as floats; c of them are there, the others read as zero
-template <int V>
-__device__ __forceinline__ void load(const float* p, int c, float (&x)[V]) {
-  if (c == V) {
-#pragma unroll
-    for (int i = 0; i < V; i += 4) {
-      const f32x4 q = __builtin_nontemporal_load(reinterpret_cast<const f32x4*>(p + i));
-#pragma unroll
-      for (int e = 0; e < 4; ++e) x[i + e] = q[e];
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < V; ++i) x[i] = i < c ? p[i] : 0.0f;
-  }
-}
-template <int V>
-__device__ __forceinline__ void load(const bf16_t* p, int c, float (&x)[V]) {
-  if (c == V) {
-    uint32_t w[V / 2];
-    if constexpr (V == 8) {
-      const u32x4 q = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(p));
-#pragma unroll
-      for (int i = 0; i < 4; ++i) w[i] = q[i];
-    } else {
-      const u32x2 q = __builtin_nontemporal_load(reinterpret_cast<const u32x2*>(p));
-      w[0] = q[0]; w[1] = q[1];
-    }
-#pragma unroll
-    for (int i = 0; i < V / 2; ++i) {
-      x[2 * i] = __uint_as_float(w[i] << 16);
-      x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < V; ++i) x[i] = i < c ? to_f32(p[i]) : 0.0f;
-  }
-}
 template <int V>
 __device__ __forceinline__ void store(float* p, int c, const float (&x)[V]) {
   if (c == V) {
@@ -114,14 +84,11 @@ __device__ __forceinline__ u32x2 load_codes(const uint8_t* p, int c) {
   }
   return q;
 }
-// codes past the tensor's end are zero
-__device__ __forceinline__ void store_codes(uint8_t* p, int c, const uint32_t (&x)[8]) {
-  if (c > 0) {
-    u32x2 q = {0u, 0u};
+__device__ __forceinline__ u32x2 pack_codes(const uint32_t (&x)[8]) {
+  u32x2 q;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) q[i >> 2] |= x[i] << (8 * (i & 3));
-    __builtin_nontemporal_store(q, reinterpret_cast<u32x2*>(p));
-  }
+  for (int i = 0; i < 2; ++i) q[i] = x[4 * i] | x[4 * i + 1] << 8 | x[4 * i + 2] << 16 | x[4 * i + 3] << 24;
+  return q;
 }
 
 // largest of a 16-lane row, in every lane of it
@@ -138,7 +105,8 @@ __device__ __forceinline__ uint32_t row_max(uint32_t v) {
 }
 
 // the tensor that workgroup `block` works on
-__device__ __forceinline__ int find(const AdamTable& t, uint32_t block) {
+template <typename Table>
+__device__ __forceinline__ int find(const Table& t, uint32_t block) {
   int lo = 0, hi = t.count - 1;
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
@@ -149,15 +117,50 @@ __device__ __forceinline__ int find(const AdamTable& t, uint32_t block) {
 }
 
 __device__ __forceinline__ uint32_t code_bits(uint32_t c, uint32_t K) { return c ? (c + K) << 20 : 0u; }
+// bit 7 of each byte is clear where the byte's low 7 bits (8 bits) are zero
+__device__ __forceinline__ uint32_t marks7(uint32_t w) { return (w | 0x80808080u) - 0x01010101u; }
+__device__ __forceinline__ uint32_t marks8(uint32_t w) { return marks7(w & 0x7f7f7f7fu) | w; }
 __device__ __forceinline__ int32_t clamp_code(int32_t q, int32_t lo, int32_t hi) { return q < lo ? lo : q > hi ? hi : q; }
 
 // base of a block from the bits of its largest magnitude: that element, rounded up, gets code `top`
-__device__ __forceinline__ uint32_t block_base(uint32_t amax, uint32_t top) {
-  const uint32_t q = (amax + 0xfffffu) >> 20;
+__device__ __forceinline__ uint32_t block_base(uint32_t largest, uint32_t top) {
+  const uint32_t q = (largest + 0xfffffu) >> 20;
   return q > top ? q - top : 0u;
 }
 
 }  // namespace
+
+// What a lane reads for its V elements, as it lies in memory; c of them are there, the others are zero.
+template <bool PB, bool GB, bool MW, bool S8>
+struct AdamPieces {
+  static constexpr int V = S8 ? 8 : 4;
+  template <bool B> using IO = std::conditional_t<B, bf16_t, float>;
+  Raw<IO<GB>, V> g;
+  Raw<IO<PB && !MW>, V> p;  // the master weights where there are some
+  Raw<float, V> m, v;       // fp32 states
+  u32x2 mc, vc;             // 8-bit states: codes, and the block's bases
+  uint32_t mk, vk;
+  int c;
+  __device__ __forceinline__ void load(const AdamTable& t, const AdamParams& a, int k, int64_t off, int64_t i, int64_t n) {
+    const int64_t left = n - i;
+    c = left >= V ? V : left > 0 ? (int)left : 0;
+    g.load(static_cast<const IO<GB>*>(t.g[k]) + i, c);
+    if constexpr (MW) p.load(a.master + off + i, c);
+    else p.load(static_cast<const IO<PB>*>(t.p[k]) + i, c);
+    if constexpr (S8) {
+      mc = load_codes(static_cast<const uint8_t*>(a.m) + off + i, c);
+      vc = load_codes(static_cast<const uint8_t*>(a.v) + off + i, c);
+      mk = vk = 0;
+      if (c > 0) {
+        mk = (uint32_t)(int32_t)a.mb[(off + i) / kAdamBlock];
+        vk = (uint32_t)(int32_t)a.vb[(off + i) / kAdamBlock];
+      }
+    } else {
+      m.load(static_cast<const float*>(a.m) + off + i, c);
+      v.load(static_cast<const float*>(a.v) + off + i, c);
+    }
+  }
+};
 
 template <bool PB, bool GB, bool MW, bool S8>
 __global__ __launch_bounds__(256) void adamw_kernel(AdamTable t, AdamParams a) {
@@ -170,41 +173,47 @@ __global__ __launch_bounds__(256) void adamw_kernel(AdamTable t, AdamParams a) {
   }
   const int k = find(t, blockIdx.x);
   const int64_t n = t.n[k], off = t.off[k];
-  const int64_t base = (int64_t)(blockIdx.x - t.first[k]) * kAdamChunk;
+  const int64_t base = (int64_t)(blockIdx.x - t.first[k]) * kAdamChunk + (threadIdx.x & ~63) * V;  // the wave's first
   const uint32_t key = t.key[k];
-  const int lane0 = (threadIdx.x & ~63) * V;
 #pragma unroll 1
   for (int it = 0; it < kAdamChunk / (256 * V); ++it) {
-    const int64_t w0 = base + it * (256 * V) + lane0;  // the wave's first element
+    const int64_t w0 = base + it * (256 * V);
     if (w0 >= n) break;
     const int64_t i = w0 + (threadIdx.x & 63) * V;
-    const int64_t left = n - i;
-    const int c = left >= V ? V : left > 0 ? (int)left : 0;
-    float p[V], g[V], m[V], v[V];
-    if constexpr (GB) load<V>(static_cast<const bf16_t*>(t.g[k]) + i, c, g);
-    else load<V>(static_cast<const float*>(t.g[k]) + i, c, g);
-    if constexpr (MW) load<V>(a.master + off + i, c, p);
-    else if constexpr (PB) load<V>(static_cast<const bf16_t*>(t.p[k]) + i, c, p);
-    else load<V>(static_cast<const float*>(t.p[k]) + i, c, p);
+    AdamPieces<PB, GB, MW, S8> x;
+    x.load(t, a, k, off, i, n);
+    const int c = x.c;
     const int64_t blk = (off + i) / kAdamBlock;
+    float p[V], g[V], m[V], v[V];
     if constexpr (S8) {
-      const u32x2 mw = load_codes(static_cast<const uint8_t*>(a.m) + off + i, c);
-      const u32x2 vw = load_codes(static_cast<const uint8_t*>(a.v) + off + i, c);
-      uint32_t mk = 0, vk = 0;
-      if (c > 0) {
-        mk = (uint32_t)(int32_t)a.mb[blk];
-        vk = (uint32_t)(int32_t)a.vb[blk];
+      uint32_t mb[V], vb[V];
+#pragma unroll
+      for (int e = 0; e < V; ++e) {
+        mb[e] = (((x.mc[e >> 2] >> (8 * (e & 3))) & 127u) + x.mk) << 20;
+        vb[e] = (((x.vc[e >> 2] >> (8 * (e & 3))) & 255u) + x.vk) << 20;
+      }
+      const uint32_t all = marks7(x.mc[0]) & marks7(x.mc[1]) & marks8(x.vc[0]) & marks8(x.vc[1]);
+      if (~all & 0x80808080u) {  // codes of zero among them
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+          if (!((x.mc[e >> 2] >> (8 * (e & 3))) & 127u)) mb[e] = 0u;
+          if (!((x.vc[e >> 2] >> (8 * (e & 3))) & 255u)) vb[e] = 0u;
+        }
       }
 #pragma unroll
       for (int e = 0; e < V; ++e) {
-        const uint32_t w = mw[e >> 2], z = vw[e >> 2];
-        const uint32_t x = code_bits((w >> (8 * (e & 3))) & 127u, mk);
-        m[e] = __uint_as_float(x | ((w << (24 - 8 * (e & 3))) & 0x80000000u));
-        v[e] = __uint_as_float(code_bits((z >> (8 * (e & 3))) & 255u, vk));
+        m[e] = __uint_as_float(mb[e] | ((x.mc[e >> 2] << (24 - 8 * (e & 3))) & 0x80000000u));
+        v[e] = __uint_as_float(vb[e]);
       }
-    } else {
-      load<V>(static_cast<const float*>(a.m) + off + i, c, m);
-      load<V>(static_cast<const float*>(a.v) + off + i, c, v);
+    }
+#pragma unroll
+    for (int e = 0; e < V; ++e) {
+      g[e] = x.g.at(e);
+      p[e] = x.p.at(e);
+      if constexpr (!S8) {
+        m[e] = x.m.at(e);
+        v[e] = x.v.at(e);
+      }
     }
     uint32_t h[V];
     if constexpr (S8 || (PB && !MW)) {
@@ -224,8 +233,10 @@ __global__ __launch_bounds__(256) void adamw_kernel(AdamTable t, AdamParams a) {
           pb[e] = (uint32_t)__builtin_bit_cast(uint16_t, (__bf16)p[e]) << 16;
         } else {
           const uint32_t b = __float_as_uint(p[e]);
-          // what is not finite is kept: a NaN computed here is quiet, its mark is in the upper half
-          pb[e] = b + (__builtin_isfinite(p[e]) ? (h[e] * 0x3C6EF373u) >> 16 : 0u);
+          // What is not finite stays so: the lower half of an infinity is zero, and that of a NaN too where
+          // every input came in bf16; with fp32 gradients it may not be.
+          const uint32_t r = (h[e] * 0x3C6EF373u) >> 16;
+          pb[e] = b + (GB || __builtin_isfinite(p[e]) ? r : 0u);
         }
       }
     }
@@ -242,15 +253,15 @@ __global__ __launch_bounds__(256) void adamw_kernel(AdamTable t, AdamParams a) {
         av = av > y ? av : y;
       }
       const uint32_t mk = block_base(row_max(am), 127u), vk = block_base(row_max(av), 255u);
-      const uint32_t least = (mk + 1) << 20;
+      const uint32_t least = (mk + 1) << 20, m0 = 8u - (mk << 20), v0 = 8u - (vk << 20);
       uint32_t mc[8], vc[8];
       bool under = false;
 #pragma unroll
       for (int e = 0; e < V; ++e) {
         const uint32_t x = __float_as_uint(m[e]) & 0x7fffffffu, y = __float_as_uint(v[e]);
-        const uint32_t rm = ((h[e] << 4) & 0xffff0u) | 8u, rv = ((h[e] >> 12) & 0xffff0u) | 8u;
-        mc[e] = (uint32_t)clamp_code((int32_t)((x + rm) >> 20) - (int32_t)mk, 0, 127);
-        vc[e] = (uint32_t)clamp_code((int32_t)((y + rv) >> 20) - (int32_t)vk, (int32_t)(y < 1u ? y : 1u), 255);
+        const uint32_t rm = (h[e] & 0xffffu) << 4, rv = (h[e] >> 16) << 4;
+        mc[e] = (uint32_t)clamp_code((int32_t)(x + rm + m0) >> 20, 0, 127);
+        vc[e] = (uint32_t)clamp_code((int32_t)(y + rv + v0) >> 20, (int32_t)(y < 1u ? y : 1u), 255);
         under |= x - 1u < least - 1u;  // 0 < x < least
       }
       if (under) {  // below the smallest code: that code or zero
@@ -261,13 +272,20 @@ __global__ __launch_bounds__(256) void adamw_kernel(AdamTable t, AdamParams a) {
           if (x < least) mc[e] = up ? 1u : 0u;
         }
       }
+      u32x2 mw = pack_codes(mc);
 #pragma unroll
-      for (int e = 0; e < V; ++e) mc[e] |= (__float_as_uint(m[e]) >> 24) & 128u;
-      store_codes(static_cast<uint8_t*>(a.m) + off + i, c, mc);
-      store_codes(static_cast<uint8_t*>(a.v) + off + i, c, vc);
-      if (c > 0 && (threadIdx.x & 15) == 0) {
-        a.mb[blk] = (int16_t)mk;
-        a.vb[blk] = (int16_t)vk;
+      for (int e = 0; e < 2; ++e) {  // the signs: the upper bytes of 4 floats
+        const uint32_t s01 = __builtin_amdgcn_perm(__float_as_uint(m[4 * e + 1]), __float_as_uint(m[4 * e]), 0x0c0c0703u);
+        const uint32_t s23 = __builtin_amdgcn_perm(__float_as_uint(m[4 * e + 3]), __float_as_uint(m[4 * e + 2]), 0x07030c0cu);
+        mw[e] |= (s01 | s23) & 0x80808080u;
+      }
+      if (c > 0) {
+        __builtin_nontemporal_store(mw, reinterpret_cast<u32x2*>(static_cast<uint8_t*>(a.m) + off + i));
+        __builtin_nontemporal_store(pack_codes(vc), reinterpret_cast<u32x2*>(static_cast<uint8_t*>(a.v) + off + i));
+        if ((threadIdx.x & 15) == 0) {
+          a.mb[blk] = (int16_t)mk;
+          a.vb[blk] = (int16_t)vk;
+        }
       }
     } else {
       store<V>(static_cast<float*>(a.m) + off + i, c, m);
@@ -279,22 +297,26 @@ __global__ __launch_bounds__(256) void adamw_kernel(AdamTable t, AdamParams a) {
 // Sum of the squares of one chunk, in fp64 (no overflow below fp32's largest squares, and no loss over
 // many elements); the workgroup's 256 lanes are added in a fixed tree.
 template <bool GB>
-__global__ __launch_bounds__(256) void norm_part_kernel(AdamTable t, double* part) {
+__global__ __launch_bounds__(256) void norm_part_kernel(NormTable t, double* part) {
   constexpr int V = GB ? 8 : 4;
+  using IO = std::conditional_t<GB, bf16_t, float>;
   const int k = find(t, blockIdx.x);
   const int64_t n = t.n[k];
-  const int64_t base = (int64_t)(blockIdx.x - t.first[k]) * kNormChunk;
+  const int64_t base = (int64_t)(blockIdx.x - t.first[k]) * kNormChunk + threadIdx.x * V;
   double s = 0.0;
-#pragma unroll 4
-  for (int it = 0; it < kNormChunk / (256 * V); ++it) {
-    const int64_t i = base + it * (256 * V) + threadIdx.x * V;
-    const int64_t left = n - i;
-    const int c = left >= V ? V : left > 0 ? (int)left : 0;
-    float g[V];
-    if constexpr (GB) load<V>(static_cast<const bf16_t*>(t.g[k]) + i, c, g);
-    else load<V>(static_cast<const float*>(t.g[k]) + i, c, g);
+#pragma unroll 1
+  for (int it = 0; it < kNormChunk / (256 * V); it += 4) {
+    if (base - threadIdx.x * V + it * (256 * V) >= n) break;
+    Raw<IO, V> g[4];
 #pragma unroll
-    for (int e = 0; e < V; ++e) s = __builtin_fma((double)g[e], (double)g[e], s);
+    for (int q = 0; q < 4; ++q) {
+      const int64_t i = base + (it + q) * (256 * V), left = n - i;
+      g[q].load(static_cast<const IO*>(t.g[k]) + i, left >= V ? V : left > 0 ? (int)left : 0);
+    }
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+#pragma unroll
+      for (int e = 0; e < V; ++e) s = __builtin_fma((double)g[q].at(e), (double)g[q].at(e), s);
   }
   __shared__ double sm[256];
   sm[threadIdx.x] = s;
@@ -310,7 +332,15 @@ __global__ __launch_bounds__(256) void norm_part_kernel(AdamTable t, double* par
 __global__ __launch_bounds__(1024) void norm_join_kernel(const double* part, int64_t n, double max_norm, float* result) {
   __shared__ double sm[1024];
   double s = 0.0;
-  for (int64_t i = threadIdx.x; i < n; i += 1024) s += part[i];
+  int64_t i = threadIdx.x;
+  for (; i + 7 * 1024 < n; i += 8 * 1024) {
+    double x[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[e] = part[i + e * 1024];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) s += x[e];
+  }
+  for (; i < n; i += 1024) s += part[i];
   sm[threadIdx.x] = s;
   __syncthreads();
   for (int h = 512; h > 0; h >>= 1) {
@@ -378,7 +408,7 @@ hipError_t launch_adamw(const AdamTable& t, const AdamParams& p, int kind, uint3
   return hipGetLastError();
 }
 
-hipError_t launch_norm_part(const AdamTable& t, double* part, bool bf16, uint32_t blocks, hipStream_t s) {
+hipError_t launch_norm_part(const NormTable& t, double* part, bool bf16, uint32_t blocks, hipStream_t s) {
   if (bf16) hipLaunchKernelGGL(norm_part_kernel<true>, dim3(blocks), dim3(256), 0, s, t, part);
   else hipLaunchKernelGGL(norm_part_kernel<false>, dim3(blocks), dim3(256), 0, s, t, part);
   return hipGetLastError();

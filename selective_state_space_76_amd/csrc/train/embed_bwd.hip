@@ -16,7 +16,7 @@
 // Bound by HBM: dout is read once in whole rows, dweight is written once.
 // Tokens outside the table sort as V, behind all others, and are left out.
 #include "../ssm_device.h"
-#include "embed_device.h"
+#include "train_device.h"
 #include "train_launch.h"
 
 namespace ssm {

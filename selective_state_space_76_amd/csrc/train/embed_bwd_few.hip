@@ -21,7 +21,7 @@
 // 0 * x is not 0 where x is infinite or NaN.  What lies at positions whose token is outside the table is cleared
 // on the way; where a workgroup still meets such a value it adds its segment up again by selection.
 #include "../ssm_device.h"
-#include "embed_device.h"
+#include "train_device.h"
 #include "train_launch.h"
 
 namespace ssm {

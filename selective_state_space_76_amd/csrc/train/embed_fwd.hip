@@ -7,7 +7,7 @@
 //     consecutive columns of two neighbouring positions, writes them as pairs, and later reads
 //     consecutive positions of one column, so both sides move whole lines.
 #include "../ssm_device.h"
-#include "embed_device.h"
+#include "train_device.h"
 #include "train_launch.h"
 
 namespace ssm {

@@ -206,30 +206,28 @@ ssm_status check_tensors(const ssm_adamw_tensor* t, int64_t count, bool grads_on
   return SSM_OK;
 }
 
-// Calls go(table, workgroups) for the tensors that `take` accepts, up to kAdamTensors of them and a launch's
-// workgroups at a time; `chunk` elements per workgroup.
-template <typename Take, typename Go>
-hipError_t in_tables(const ssm_adamw_tensor* t, int64_t count, int64_t chunk, Take take, Go go) {
-  ssm::AdamTable tab;
+// Calls go(table, workgroups) for the tensors that `take` accepts, as many at a time as a table holds and a
+// launch's workgroups allow, `chunk` elements per workgroup; put(table, slot, place in the list) enters one.
+template <typename Table, int kRoom, typename Take, typename Put, typename Go>
+hipError_t in_tables(const ssm_adamw_tensor* t, int64_t count, int64_t chunk, Take take, Put put, Go go) {
+  Table tab;
   tab.count = 0;
   int64_t blocks = 0;
   for (int64_t k = 0; k <= count; ++k) {
     const bool here = k < count && take(t[k]);
     const int64_t more = here ? chunks_of(t[k].numel, chunk) : 0;
-    if (tab.count && (k == count || tab.count == ssm::kAdamTensors || blocks + more > kMaxGrid)) {
+    if (tab.count && (k == count || (here && (tab.count == kRoom || blocks + more > kMaxGrid)))) {
       const hipError_t e = go(tab, (uint32_t)blocks);
       if (e != hipSuccess) return e;
       tab.count = 0;
       blocks = 0;
     }
     if (!here) continue;
-    const int i = tab.count++;
-    tab.p[i] = t[k].param;
-    tab.g[i] = t[k].grad;
-    tab.n[i] = t[k].numel;
-    tab.off[i] = t[k].offset;
-    tab.first[i] = (uint32_t)blocks;
-    tab.key[i] = (uint32_t)k;  // the caller turns the place into a key
+    tab.g[tab.count] = t[k].grad;
+    tab.n[tab.count] = t[k].numel;
+    tab.first[tab.count] = (uint32_t)blocks;
+    put(tab, tab.count, k);
+    ++tab.count;
     blocks += more;
   }
   return hipSuccess;
@@ -269,10 +267,11 @@ ssm_status ssm_grad_norm(const ssm_adamw_tensor* tensors, int64_t count, double 
   double* part = static_cast<double*>(workspace);
   int64_t done = 0;
   for (int b = 0; b < 2; ++b) {
-    const hipError_t e = in_tables(
+    const hipError_t e = in_tables<ssm::NormTable, ssm::kNormTensors>(
         tensors, count, ssm::kNormChunk,
         [&](const ssm_adamw_tensor& t) { return (t.grad_dtype == SSM_BF16) == (b == 1); },
-        [&](const ssm::AdamTable& tab, uint32_t blocks) {
+        [](ssm::NormTable&, int, int64_t) {},
+        [&](const ssm::NormTable& tab, uint32_t blocks) {
           const hipError_t r = ssm::launch_norm_part(tab, part + done, b == 1, blocks, st);
           done += blocks;
           return r;
@@ -324,14 +323,18 @@ ssm_status ssm_adamw_step(const ssm_adamw_config* c, const ssm_adamw_tensor* ten
   a.decay = (float)(1 - c->lr * c->weight_decay);
   hipStream_t st = reinterpret_cast<hipStream_t>(stream);
   for (int kind = 0; kind < 8; ++kind) {  // bit 0 bf16 params, bit 1 bf16 gradients, bit 2 masters
-    const hipError_t e = in_tables(
+    const hipError_t e = in_tables<ssm::AdamTable, ssm::kAdamTensors>(
         tensors, count, ssm::kAdamChunk,
         [&](const ssm_adamw_tensor& t) {
           const bool pb = t.param_dtype == SSM_BF16;
           return kind == (pb ? 1 : 0) + (t.grad_dtype == SSM_BF16 ? 2 : 0) + (pb && master ? 4 : 0);
         },
-        [&](ssm::AdamTable& tab, uint32_t blocks) {
-          for (int i = 0; i < tab.count; ++i) tab.key[i] = ssm::adam_key(c->seed, c->step, tab.key[i]);
+        [&](ssm::AdamTable& tab, int i, int64_t k) {
+          tab.p[i] = tensors[k].param;
+          tab.off[i] = tensors[k].offset;
+          tab.key[i] = ssm::adam_key(c->seed, c->step, k);
+        },
+        [&](const ssm::AdamTable& tab, uint32_t blocks) {
           return ssm::launch_adamw(tab, a, kind + (s8 ? 8 : 0), blocks, st);
         });
     if (e != hipSuccess) return SSM_ERR_LAUNCH;

@@ -1,4 +1,4 @@
-// embed_device.h -- what the embedding's kernels share: tokens, and pieces of rows at any alignment.
+// train_device.h -- what the training operators' kernels share: pieces of rows at any alignment, and tokens.
 #pragma once
 #include <hip/hip_runtime.h>
 #include <stdint.h>

@@ -32,7 +32,8 @@ hipError_t launch_conv_bwd(const ConvBwdParams& p, bool bf16, hipStream_t s);
 constexpr int kAdamBlock = 128;
 constexpr int kAdamTensors = 80;  // tensors per launch: their table travels in the kernel arguments (3.3 KB)
 constexpr int64_t kAdamChunk = 8192;  // elements per workgroup
-constexpr int64_t kNormChunk = 32768;
+constexpr int kNormTensors = 192;  // as many with less to say of each
+constexpr int64_t kNormChunk = 16384;
 
 struct AdamTable {
   void* p[kAdamTensors];
@@ -41,6 +42,13 @@ struct AdamTable {
   int64_t off[kAdamTensors];
   uint32_t first[kAdamTensors];  // workgroup that a tensor begins with
   uint32_t key[kAdamTensors];    // of its random numbers
+  int count;
+};
+
+struct NormTable {
+  const void* g[kNormTensors];
+  int64_t n[kNormTensors];
+  uint32_t first[kNormTensors];
   int count;
 };
 
@@ -58,7 +66,7 @@ struct AdamParams {
 uint32_t adam_key(uint64_t seed, int64_t step, int64_t tensor);
 // kind: bit 0 bf16 params, bit 1 bf16 gradients, bit 2 master weights, bit 3 8-bit states
 hipError_t launch_adamw(const AdamTable& t, const AdamParams& p, int kind, uint32_t blocks, hipStream_t s);
-hipError_t launch_norm_part(const AdamTable& t, double* part, bool bf16, uint32_t blocks, hipStream_t s);
+hipError_t launch_norm_part(const NormTable& t, double* part, bool bf16, uint32_t blocks, hipStream_t s);
 hipError_t launch_norm_join(const double* part, int64_t n, double max_norm, float* result, hipStream_t s);
 hipError_t launch_state_values(int64_t n, const void* m, const void* v, const int16_t* mb, const int16_t* vb,
                                void* mo, void* vo, hipStream_t s);
