@@ -22,10 +22,7 @@ namespace ssm {
 
 namespace {
 
-#ifndef PASSES
-#define PASSES 4
-#endif
-constexpr int kPasses = PASSES;
+constexpr int kPasses = 4;
 
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
@@ -266,10 +263,12 @@ __global__ __launch_bounds__(256, 5) void conv_bwd_kernel(ConvBwdParams p) {
     for (int k = 0; k < K; ++k) sw[k] += __shfl_xor(sw[k], o, LN);
   }
   if (live && lane == 0) {
-    float* o = p.part + (((int64_t)b32 * p.S + seg) * p.Dm + d) * (K + 1);
+    const bool whole = p.Bsz * p.S == 1;  // the only segment of its channel: these are the results
+    float* o = whole ? p.dw + d * K : p.part + (((int64_t)b32 * p.S + seg) * p.Dm + d) * (K + 1);
 #pragma unroll
     for (int k = 0; k < K; ++k) o[k] = sw[k];
-    o[K] = sb;
+    if (!whole) o[K] = sb;
+    else if (p.db) p.db[d] = sb;
   }
 }
 
@@ -339,7 +338,7 @@ hipError_t launch_conv_bwd(const ConvBwdParams& p, bool bf16, hipStream_t s) {
   if (bf16) launch_io<bf16_t>(p, s);
   else launch_io<float>(p, s);
   hipError_t e = hipGetLastError();
-  if (e != hipSuccess) return e;
+  if (e != hipSuccess || p.Bsz * p.S == 1) return e;
   hipLaunchKernelGGL(conv_bwd_join_kernel, dim3((unsigned)((p.Dm * (p.K + 1) + 63) / 64)), dim3(256), 0, s, p.part,
                      p.Bsz * p.S, p.Dm, p.K, p.dw, p.db);
   return hipGetLastError();

@@ -16,14 +16,36 @@ import ctypes
 import numpy as np
 import torch
 
-from ._lib import (SSM_BF16, SSM_F32, _check, _expect, _io_dtype, _nonempty, _on_stream, _ptr, _stream, load,
-                   ssm_adamw_config, ssm_embed_shape)
+from ._lib import (SSM_BF16, SSM_F32, _check, _expect, _io_dtype, _nonempty, _on_stream, _ptr, load, ssm_adamw_config,
+                   ssm_embed_shape)
 
 SSM_I32 = 0
 SSM_I64 = 1
 SSM_FLAG_CHANNELS_FIRST = 1
 SSM_FLAG_ACCUMULATE = 2
 ADAMW_BLOCK = 128
+
+
+# Small calls are bound by the host, so the checks of _lib.py are made in their cheapest order here: plain numbers
+# for addresses, and _expect() (which says what is wrong) only where something is.
+
+def _address(t):
+    """The tensor's address, None for None; _ptr() refuses what is not on the GPU or not contiguous."""
+    if t is None:
+        return None
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or not t.is_contiguous():
+        _ptr(t)
+    return t.data_ptr()
+
+
+def _want(t, shape, dtype, name, device):
+    if t is not None and (t.shape != shape or t.dtype != dtype or t.device != device):
+        _expect(t, shape, dtype, name, device)
+
+
+def _stream(stream, device):
+    """The caller's stream, by default the current one of the tensors' device, as the number the library takes."""
+    return torch._C._cuda_getCurrentRawStream(device.index) if stream is None else stream.cuda_stream
 
 
 def _workspace(workspace, need, device, made):
@@ -56,18 +78,19 @@ def conv1d_bwd(x, weight, bias=None, initial_state=None, *, dout, dfinal_state=N
     for t, shp, dt, name in ((weight, (Dm, K), f32, "weight"), (bias, (Dm,), f32, "bias"),
                              (initial_state, state, x.dtype, "initial_state"), (dout, (Bsz, Dm, L), x.dtype, "dout"),
                              (dfinal_state, state, x.dtype, "dfinal_state")):
-        _expect(t, shp, dt, name, device)
+        _want(t, shp, dt, name, device)
     g, made = dict(grads or {}), []
     for k, (shp, dt) in dict(dx=((Bsz, Dm, L), x.dtype), dweight=((Dm, K), f32), dbias=((Dm,), f32),
                              dinitial_state=(state, x.dtype)).items():
         if g.get(k) is None:
             g[k] = torch.empty(shp, dtype=dt, device=device)
             made.append(g[k])
-        _expect(g[k], shp, dt, k, device)
+        _want(g[k], shp, dt, k, device)
     workspace, ws_bytes = _workspace(workspace, conv1d_bwd_workspace_size(Bsz, Dm, L, K, io), device, made)
-    _check(lib.ssm_conv1d_bwd(Bsz, Dm, L, K, io, _ptr(x), _ptr(weight), _ptr(bias), _ptr(initial_state), _ptr(dout),
-                              _ptr(dfinal_state), _ptr(g["dx"]), _ptr(g["dweight"]), _ptr(g["dbias"]),
-                              _ptr(g["dinitial_state"]), _ptr(workspace), ws_bytes, _stream(stream, device)))
+    _check(lib.ssm_conv1d_bwd(Bsz, Dm, L, K, io, _address(x), _address(weight), _address(bias),
+                              _address(initial_state), _address(dout), _address(dfinal_state), _address(g["dx"]),
+                              _address(g["dweight"]), _address(g["dbias"]), _address(g["dinitial_state"]),
+                              _address(workspace), ws_bytes, _stream(stream, device)))
     _on_stream(stream, *made)
     return g
 
@@ -104,9 +127,9 @@ def embedding_fwd(tokens, weight, *, scale=1.0, dtype=None, channels_first=False
     if out is None:
         out = torch.empty(shape, dtype=dtype, device=device)
         made.append(out)
-    _expect(weight, weight.shape, weight.dtype, "weight", device)
-    _expect(out, shape, dtype, "out", device)
-    _check(lib.ssm_embedding_fwd(ctypes.byref(sh), _ptr(tokens), _ptr(weight), float(scale), _ptr(out),
+    _want(weight, weight.shape, weight.dtype, "weight", device)
+    _want(out, shape, dtype, "out", device)
+    _check(lib.ssm_embedding_fwd(ctypes.byref(sh), _address(tokens), _address(weight), float(scale), _address(out),
                                  _stream(stream, device)))
     _on_stream(stream, *made)
     return out
@@ -135,15 +158,15 @@ def embedding_bwd(tokens, dout, rows, *, scale=1.0, channels_first=False, dtype=
     dim = dout.shape[1 if channels_first else -1]
     sh, shape = _embed_shape(tokens, rows, dim, dtype, dout.dtype, channels_first, accumulate)
     device, made = tokens.device, []
-    _expect(dout, shape, dout.dtype, "dout", device)
+    _want(dout, shape, dout.dtype, "dout", device)
     if dweight is None:
         dweight = torch.empty((rows, dim), dtype=dtype, device=device)
         made.append(dweight)
-    _expect(dweight, (rows, dim), dtype, "dweight", device)
+    _want(dweight, (rows, dim), dtype, "dweight", device)
     need = int(lib.ssm_embedding_bwd_workspace_size(ctypes.byref(sh)))
     workspace, ws_bytes = _workspace(workspace, need, device, made)
-    _check(lib.ssm_embedding_bwd(ctypes.byref(sh), _ptr(tokens), _ptr(dout), float(scale), _ptr(dweight),
-                                 _ptr(workspace), ws_bytes, _stream(stream, device)))
+    _check(lib.ssm_embedding_bwd(ctypes.byref(sh), _address(tokens), _address(dout), float(scale), _address(dweight),
+                                 _address(workspace), ws_bytes, _stream(stream, device)))
     _on_stream(stream, *made)
     return dweight
 
@@ -190,6 +213,7 @@ class AdamW:
             raise ValueError("parameters overlap")
         self._shapes = [p.shape for p in self.params]
         self._dtypes = [p.dtype for p in self.params]
+        self._grad_dtypes = None  # those that the table says
         n = np.array([p.numel() for p in self.params], np.int64)
         room = -(-n // ADAMW_BLOCK) * ADAMW_BLOCK
         self.offsets = (np.cumsum(room) - room).tolist()
@@ -223,14 +247,14 @@ class AdamW:
         return {"state": dict(self.state), "step": self.step_count}
 
     def _checked(self, tensors, what):
-        """Their addresses; every call looks at shape, type, device and layout anew."""
+        """Their addresses; every call looks at shape, device and layout anew (and the caller at the types)."""
         if [t.shape for t in tensors] != self._shapes:
             raise ValueError("%s: shapes differ from the parameters' at construction" % what)
-        if any(t.device != self.device for t in tensors):
+        if set(map(torch.Tensor.get_device, tensors)) != {self.device.index}:
             raise ValueError("%s: expected tensors on %s" % (what, self.device))
-        if not all([t.is_contiguous() for t in tensors]):
+        if not all(map(torch.Tensor.is_contiguous, tensors)):
             raise ValueError("%s: tensors must be contiguous" % what)
-        return [t.data_ptr() for t in tensors]
+        return list(map(torch.Tensor.data_ptr, tensors))
 
     def step(self, grads=None, *, stream=None):
         """One step with the gradients given (fp32 or bf16, the parameters' shapes), by default each parameter's
@@ -247,7 +271,10 @@ class AdamW:
         have = [g is not None for g in grads]
         if all(have):
             table["grad"] = self._checked(grads, "grads")
-            table["grad_dtype"] = [_io_dtype(g) for g in grads]
+            dtypes = [g.dtype for g in grads]
+            if dtypes != self._grad_dtypes:
+                table["grad_dtype"] = [_io_dtype(g) for g in grads]
+                self._grad_dtypes = dtypes
         else:
             if not any(have):
                 return None
@@ -262,14 +289,14 @@ class AdamW:
             clip = torch.empty(2, dtype=torch.float32, device=self.device)
             workspace = torch.empty(need, dtype=torch.uint8, device=self.device)
             made = [clip, workspace]
-            _check(lib.ssm_grad_norm(rows, count, float(self.max_grad_norm), _ptr(clip), _ptr(workspace), need, s))
+            _check(lib.ssm_grad_norm(rows, count, float(self.max_grad_norm), _address(clip), _address(workspace), need, s))
             norm = clip[0]
         cfg = ssm_adamw_config(self.lr, self.betas[0], self.betas[1], self.eps, self.weight_decay, self.step_count + 1,
                                self.seed & (2 ** 64 - 1), self.state_bits, 0)
         st = self.state
-        _check(lib.ssm_adamw_step(ctypes.byref(cfg), rows, count, _ptr(st["exp_avg"]), _ptr(st["exp_avg_sq"]),
-                                  _ptr(st.get("exp_avg_base")), _ptr(st.get("exp_avg_sq_base")),
-                                  _ptr(st.get("master")), _ptr(clip), s))
+        _check(lib.ssm_adamw_step(ctypes.byref(cfg), rows, count, _address(st["exp_avg"]), _address(st["exp_avg_sq"]),
+                                  _address(st.get("exp_avg_base")), _address(st.get("exp_avg_sq_base")),
+                                  _address(st.get("master")), _address(clip), s))
         self.step_count += 1
         _on_stream(stream, *made)
         return norm
@@ -282,8 +309,8 @@ class AdamW:
             return st["exp_avg"], st["exp_avg_sq"]
         m = torch.empty(self.numel, dtype=torch.bfloat16, device=self.device)
         v = torch.empty_like(m)
-        _check(load().ssm_adamw_state_values(self.numel, _ptr(st["exp_avg"]), _ptr(st["exp_avg_sq"]),
-                                             _ptr(st["exp_avg_base"]), _ptr(st["exp_avg_sq_base"]), _ptr(m), _ptr(v),
+        _check(load().ssm_adamw_state_values(self.numel, _address(st["exp_avg"]), _address(st["exp_avg_sq"]),
+                                             _address(st["exp_avg_base"]), _address(st["exp_avg_sq_base"]), _address(m), _address(v),
                                              _stream(stream, self.device)))
         _on_stream(stream, m, v)
         return m, v
