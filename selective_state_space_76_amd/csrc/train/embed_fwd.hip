@@ -1,8 +1,10 @@
 // embed_fwd.hip -- embedding: out[b,t,:] = scale * weight[tokens[b,t],:], zeros for a token outside the table.
 //
 // Bound by HBM: the output is written once and the named rows are read once (from the caches where they
-// come again).
-//   * [B,L,E]: a lane owns V output elements (16 bytes) of a row; lanes run over the rows' pieces.
+// come again).  A million letters into 1024 channels of bf16 (2.1 GB): 370 us, 5.8 TB/s (a plain fill of as many
+// bytes runs at 6.9; the rows of [B,E,L] lie 2 MB apart, and no other tile, order of tiles or table in LDS came
+// below 367).  The stores are marked as not needed again: through the caches it takes 612 us.
+//   * [B,L,E]: a lane owns 16 aligned bytes of the output, wherever the rows begin.
 //   * [B,E,L]: a workgroup turns a tile of kT positions x kE columns through LDS: a lane reads 8
 //     consecutive columns of two neighbouring positions, writes them as pairs, and later reads
 //     consecutive positions of one column, so both sides move whole lines.
@@ -15,89 +17,129 @@ namespace ssm {
 template <typename WT, typename IO>
 __global__ __launch_bounds__(256) void embed_rows_kernel(EmbedParams p) {
   constexpr int V = 16 / (int)sizeof(IO);
-  const int64_t cpr = (p.E + V - 1) / V;  // pieces per row
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (i >= p.T * cpr) return;
-  int64_t t, c;
-  if (p.T * cpr <= 0xffffffffll) {
-    t = (uint32_t)i / (uint32_t)cpr;
-    c = (uint32_t)i - (uint32_t)t * (uint32_t)cpr;
+  const int64_t total = p.T * p.E;
+  const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * V;  // the piece's first element
+  if (i >= total) return;
+  int64_t t, e;
+  if (total <= 0xffffffffll) {
+    t = (uint32_t)i / (uint32_t)p.E;
+    e = (uint32_t)i - (uint32_t)t * (uint32_t)p.E;
   } else {
-    t = i / cpr;
-    c = i - t * cpr;
+    t = i / p.E;
+    e = i - t * p.E;
   }
-  const int64_t e = c * V;
-  const int n = p.E - e < V ? (int)(p.E - e) : V;
-  const int64_t row = token_at(p.tokens, p.i64, t, p.V);
+  const WT* table = static_cast<const WT*>(p.table);
+  int64_t row = token_at(p.tokens, p.i64, t, p.V);
   float x[V];
-  if (row < p.V) {
-    load_n<WT, V>(static_cast<const WT*>(p.table) + row * p.E + e, n, x);
-  } else {
+  if (e + V <= p.E) {
+    if (row < p.V) {
+      load_n<WT, V>(table + row * p.E + e, V, x);
+    } else {
 #pragma unroll
-    for (int k = 0; k < V; ++k) x[k] = 0.0f;
+      for (int k = 0; k < V; ++k) x[k] = 0.0f;
+    }
+  } else {  // the piece goes on in the next row (or rows, or ends with the last)
+#pragma unroll
+    for (int k = 0; k < V; ++k) {
+      x[k] = row < p.V && i + k < total ? to_f32(table[row * p.E + e]) : 0.0f;
+      if (++e == p.E && i + k + 1 < total) {
+        e = 0;
+        row = token_at(p.tokens, p.i64, ++t, p.V);
+      }
+    }
   }
 #pragma unroll
   for (int k = 0; k < V; ++k) x[k] *= p.scale;
-  store_n<IO, V>(static_cast<IO*>(p.out) + t * p.E + e, n, x);
+  store_n<IO, V>(static_cast<IO*>(p.out) + i, total - i >= V ? V : (int)(total - i), x);
 }
 
-constexpr int kT = 128, kE = 64;  // positions x columns of a tile
+// Rows that begin at a multiple of 128 bytes (SHIFT false) take tiles of 128 positions x 64 columns.  Others would
+// share a line with the next tile at each end of every column; there a column's tile begins up to a line earlier, at
+// a multiple of 128 bytes, so that only a row's own ends are partial lines.  262149 letters into 1000 channels of
+// bf16: 291 us with tiles where they fall, 251 with tiles at 16 bytes, 131 with these (128 x 32: 149, 512 x 32: 146,
+// 256 x 64: 193); at 262144, with the aligned tiles, 102.
+template <typename IO, bool SHIFT> struct Tile {
+  static constexpr int V = 16 / (int)sizeof(IO);
+  static constexpr int line = 128 / (int)sizeof(IO);
+  static constexpr int T = SHIFT ? 256 : 128, E = SHIFT ? 32 : 64;  // positions x columns
+  static constexpr int before = SHIFT ? line : 0;                 // positions kept before the tile
+  static int64_t along(int64_t L) { return (L + (SHIFT ? line - 1 : 0) + T - 1) / T; }
+};
 
-template <typename WT, typename IO>
+template <typename WT, typename IO, bool SHIFT>
 __global__ __launch_bounds__(256) void embed_cols_kernel(EmbedParams p) {
-  constexpr int V = 16 / (int)sizeof(IO);
-  constexpr int LD = kT + 16 / (int)sizeof(IO);  // elements between columns in LDS, whole 16-byte pieces
+  using S = Tile<IO, SHIFT>;
+  constexpr int V = S::V, kT = S::T, kE = S::E, EX = S::before;
+  constexpr int LD = kT + EX + V;  // elements between columns in LDS, whole 16-byte pieces
   __shared__ __align__(16) IO sm[kE * LD];
-  const int64_t tiles_t = (p.L + kT - 1) / kT, tiles_e = (p.E + kE - 1) / kE;
-  const int64_t blk = blockIdx.x;
-  const int64_t te = blk % tiles_e, rest = blk / tiles_e;
+  const int64_t tiles_t = p.tiles, tiles_e = (p.E + kE - 1) / kE;
+  const int64_t te = blockIdx.x % tiles_e, rest = blockIdx.x / tiles_e;
   const int64_t tt = rest % tiles_t, b = rest / tiles_t;
   const int64_t t0 = tt * kT, e0 = te * kE;
-  const int64_t nt = p.L - t0, ne = p.E - e0;
-  {
-    const int c = (threadIdx.x & 7) * 8;  // first column
-    const int n = ne - c >= 8 ? 8 : ne - c > 0 ? (int)(ne - c) : 0;
+  const int64_t ne = p.E - e0;
+  constexpr int CPR = kE / 8, RPP = 256 / CPR * 2;  // pieces of 8 columns, positions per pass
+  const int c = (threadIdx.x % CPR) * 8;
+  const int n = ne - c >= 8 ? 8 : ne - c > 0 ? (int)(ne - c) : 0;
+  auto fetch = [&](int r) {  // positions r and r + 1 of LDS
+    float x[2][8];
 #pragma unroll
-    for (int h = 0; h < kT / 64; ++h) {
-      const int r = h * 64 + (threadIdx.x >> 3) * 2;  // first of two positions
-      float x[2][8];
+    for (int k = 0; k < 2; ++k) {
+      const int64_t t = t0 - EX + r + k;
+      int64_t row = p.V;
+      if (t >= 0 && t < p.L) row = token_at(p.tokens, p.i64, b * p.L + t, p.V);
+      if (row < p.V) {
+        load_n<WT, 8>(static_cast<const WT*>(p.table) + row * p.E + e0 + c, n, x[k]);
+      } else {
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        int64_t row = p.V;
-        if (r + k < nt) row = token_at(p.tokens, p.i64, b * p.L + t0 + r + k, p.V);
-        if (row < p.V) {
-          load_n<WT, 8>(static_cast<const WT*>(p.table) + row * p.E + e0 + c, n, x[k]);
-        } else {
-#pragma unroll
-          for (int q = 0; q < 8; ++q) x[k][q] = 0.0f;
-        }
-      }
-#pragma unroll
-      for (int q = 0; q < 8; ++q) {
-        if constexpr (sizeof(IO) == 2) {
-          const uint32_t lo = __builtin_bit_cast(uint16_t, (__bf16)(x[0][q] * p.scale));
-          const uint32_t hi = __builtin_bit_cast(uint16_t, (__bf16)(x[1][q] * p.scale));
-          *reinterpret_cast<uint32_t*>(&sm[(c + q) * LD + r]) = lo | (hi << 16);
-        } else {
-          *reinterpret_cast<float2*>(&sm[(c + q) * LD + r]) = make_float2(x[0][q] * p.scale, x[1][q] * p.scale);
-        }
+        for (int q = 0; q < 8; ++q) x[k][q] = 0.0f;
       }
     }
+#pragma unroll
+    for (int q = 0; q < 8; ++q) {
+      if constexpr (sizeof(IO) == 2) {
+        const uint32_t lo = __builtin_bit_cast(uint16_t, (__bf16)(x[0][q] * p.scale));
+        const uint32_t hi = __builtin_bit_cast(uint16_t, (__bf16)(x[1][q] * p.scale));
+        *reinterpret_cast<uint32_t*>(&sm[(c + q) * LD + r]) = lo | (hi << 16);
+      } else {
+        *reinterpret_cast<float2*>(&sm[(c + q) * LD + r]) = make_float2(x[0][q] * p.scale, x[1][q] * p.scale);
+      }
+    }
+  };
+#pragma unroll
+  for (int h = 0; h < (kT + EX + RPP - 1) / RPP; ++h) {
+    const int r = h * RPP + (threadIdx.x / CPR) * 2;
+    if ((kT + EX) % RPP == 0 || r < kT + EX) fetch(r);
   }
   __syncthreads();
   constexpr int PPC = kT / V;  // pieces per column
 #pragma unroll
   for (int h = 0; h < kE * PPC / 256; ++h) {
     const int i = h * 256 + threadIdx.x;
-    const int col = i / PPC, r = (i % PPC) * V;
-    if (col >= ne || r >= nt) continue;
-    const int n = nt - r < V ? (int)(nt - r) : V;
-    IO* o = static_cast<IO*>(p.out) + (b * p.E + e0 + col) * p.L + t0 + r;
-    const u32x4a q = *reinterpret_cast<const u32x4a*>(&sm[col * LD + r]);
-    if (n == V) {
-      __builtin_nontemporal_store((typename Unaligned<IO>::type)q, reinterpret_cast<typename Unaligned<IO>::type*>(o));
+    const int col = i / PPC;
+    if (col >= ne) continue;
+    const int64_t first = (b * p.E + e0 + col) * p.L;  // of the row
+    const int m = SHIFT ? (int)((first + t0) % S::line) : 0;
+    const int r = (i % PPC) * V;
+    const int64_t t = t0 - m + r;
+    if (t >= p.L || t + V <= 0) continue;
+    IO* o = static_cast<IO*>(p.out) + first + t;
+    const IO* s = &sm[col * LD + EX - m + r];
+    u32x4a q;
+    if constexpr (!SHIFT) {
+      q = *reinterpret_cast<const u32x4a*>(s);
+    } else if constexpr (V == 4) {
+#pragma unroll
+      for (int w = 0; w < 4; ++w) q[w] = __float_as_uint(s[w]);
     } else {
-      for (int k = 0; k < n; ++k) o[k] = sm[col * LD + r + k];
+      const uint32_t* d = reinterpret_cast<const uint32_t*>(s - (m & 1));
+#pragma unroll
+      for (int w = 0; w < 4; ++w) q[w] = m & 1 ? d[w] >> 16 | d[w + 1] << 16 : d[w];
+    }
+    if (t >= 0 && t + V <= p.L) {
+      __builtin_nontemporal_store(q, reinterpret_cast<u32x4a*>(o));
+    } else {
+      for (int k = 0; k < V; ++k)
+        if (t + k >= 0 && t + k < p.L) o[k] = s[k];
     }
   }
 }
@@ -107,11 +149,18 @@ namespace {
 template <typename WT, typename IO>
 hipError_t launch(const EmbedParams& p, hipStream_t s) {
   constexpr int V = 16 / (int)sizeof(IO);
-  if (p.cf) {
-    const int64_t blocks = p.Bsz * ((p.L + kT - 1) / kT) * ((p.E + kE - 1) / kE);
-    hipLaunchKernelGGL((embed_cols_kernel<WT, IO>), dim3((unsigned)blocks), dim3(256), 0, s, p);
+  if (p.cf && p.L % Tile<IO, false>::line == 0) {
+    EmbedParams q = p;
+    q.tiles = Tile<IO, false>::along(p.L);
+    const int64_t blocks = p.Bsz * q.tiles * ((p.E + Tile<IO, false>::E - 1) / Tile<IO, false>::E);
+    hipLaunchKernelGGL((embed_cols_kernel<WT, IO, false>), dim3((unsigned)blocks), dim3(256), 0, s, q);
+  } else if (p.cf) {
+    EmbedParams q = p;
+    q.tiles = Tile<IO, true>::along(p.L);
+    const int64_t blocks = p.Bsz * q.tiles * ((p.E + Tile<IO, true>::E - 1) / Tile<IO, true>::E);
+    hipLaunchKernelGGL((embed_cols_kernel<WT, IO, true>), dim3((unsigned)blocks), dim3(256), 0, s, q);
   } else {
-    const int64_t pieces = p.T * ((p.E + V - 1) / V);
+    const int64_t pieces = (p.T * p.E + V - 1) / V;
     hipLaunchKernelGGL((embed_rows_kernel<WT, IO>), dim3((unsigned)((pieces + 255) / 256)), dim3(256), 0, s, p);
   }
   return hipGetLastError();

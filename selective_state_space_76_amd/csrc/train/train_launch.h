@@ -82,6 +82,7 @@ struct EmbedParams {
   int i64;             // tokens are int64
   int cf;              // [B,E,L]
   int add;
+  int64_t tiles;       // [B,E,L] forward: tiles along a row
 };
 hipError_t launch_embed_fwd(const EmbedParams& p, bool table_bf16, bool io_bf16, hipStream_t s);
 
