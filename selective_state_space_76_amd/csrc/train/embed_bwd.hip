@@ -255,7 +255,9 @@ __device__ __forceinline__ OT* row_at(const SumParams& p, uint32_t k, int64_t co
 
 // With ADD the rows of dweight that a group of 8 will add to are loaded with the group, not one by one as the
 // tokens change (41 -> 27 us per call for 509 tokens of width 768 into a table of 50000 rows).
-template <typename IO, typename OT, int VC, bool ADD>
+// NT: dout is too large to be found in the Infinity Cache (256 MB), where a backward pass has just left it, and
+// is read as not needed again (16384 x 768: 53 -> 49 us per call without; 262144 x 1024: 165 -> 153 us with).
+template <typename IO, typename OT, int VC, bool ADD, bool NT>
 __global__ __launch_bounds__(256) void embed_sum_kernel(SumParams p) {
   const int lane = threadIdx.x & 63;
   const int64_t unit = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
@@ -282,7 +284,7 @@ __global__ __launch_bounds__(256) void embed_sum_kernel(SumParams p) {
     }
     const uint32_t after = s + 64 < i1 ? p.key[s + 64] : next;  // the key behind these
     for (int r = 0; r < m; r += 8) {
-      Raw<IO, VC> x[8];
+      Raw<IO, VC, NT> x[8];
       Raw<OT, VC> old[ADD ? 8 : 1];
       uint32_t k[9];
 #pragma unroll
@@ -442,8 +444,10 @@ hipError_t launch_sums(SumParams p, hipStream_t s) {
   p.col_tiles = (p.E + 64 * VC - 1) / (64 * VC);
   const int64_t units = p.chunks * p.col_tiles;
   const dim3 grid((unsigned)((units + 3) / 4));
-  if (p.add) hipLaunchKernelGGL((embed_sum_kernel<IO, OT, VC, true>), grid, dim3(256), 0, s, p);
-  else hipLaunchKernelGGL((embed_sum_kernel<IO, OT, VC, false>), grid, dim3(256), 0, s, p);
+  const bool nt = p.n * p.E * (int64_t)sizeof(IO) > (int64_t(128) << 20);
+  auto go = [&](auto fn) { hipLaunchKernelGGL(fn, grid, dim3(256), 0, s, p); };
+  if (p.add) nt ? go(embed_sum_kernel<IO, OT, VC, true, true>) : go(embed_sum_kernel<IO, OT, VC, true, false>);
+  else nt ? go(embed_sum_kernel<IO, OT, VC, false, true>) : go(embed_sum_kernel<IO, OT, VC, false, false>);
   if (p.chunks > 1) hipLaunchKernelGGL((embed_join_kernel<OT, VC>), dim3((unsigned)units), dim3(256), 0, s, p);
   return hipGetLastError();
 }

@@ -55,8 +55,8 @@ __device__ __forceinline__ void load_n(const IO* p, int n, float (&x)[N]) {
   }
 }
 
-// The same, kept as they are in memory (half the registers of floats for bf16) until unpack().
-template <typename IO, int N>
+// The same, kept as they are in memory (half the registers of floats for bf16) until at().
+template <typename IO, int N, bool NT = true>
 struct Raw {
   static constexpr int W = N * (int)sizeof(IO) / 4, C = W < 4 ? W : 4;  // words, and of one piece
   uint32_t w[W];
@@ -65,7 +65,8 @@ struct Raw {
     if (n == N) {
 #pragma unroll
       for (int k = 0; k < W / C; ++k) {
-        const piece q = __builtin_nontemporal_load(reinterpret_cast<const piece*>(p + k * C * 4 / (int)sizeof(IO)));
+        const piece* a = reinterpret_cast<const piece*>(p + k * C * 4 / (int)sizeof(IO));
+        const piece q = NT ? __builtin_nontemporal_load(a) : *a;
 #pragma unroll
         for (int i = 0; i < C; ++i) w[k * C + i] = q[i];
       }
