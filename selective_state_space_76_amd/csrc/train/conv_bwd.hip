@@ -84,6 +84,23 @@ __device__ __forceinline__ uint32_t of_lane(uint32_t v) {
   else return (uint32_t)__builtin_amdgcn_mov_dpp((int)v, LAST ? 0x15f : 0x150, 0xf, 0xf, true);
 }
 
+// sum over the group's lanes: rotations within rows of 16, then the four rows
+template <int LN>
+__device__ __forceinline__ float sum_lanes(float v) {
+  auto step = [&](auto ctrl) {
+    v += __uint_as_float((uint32_t)__builtin_amdgcn_mov_dpp((int)__float_as_uint(v), decltype(ctrl)::value, 0xf, 0xf, true));
+  };
+  step(IC<0x128>{});  // row_ror:8
+  step(IC<0x124>{});
+  step(IC<0x122>{});
+  step(IC<0x121>{});
+  if constexpr (LN == 64) {
+    auto row = [&](int l) { return __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(v), l)); };
+    v = (row(0) + row(16)) + (row(32) + row(48));
+  }
+  return v;
+}
+
 __device__ __forceinline__ float silu_slope(float a) {
   const float s = rcp_(1.0f + exp2_(-a * kLog2e));
   return s * __builtin_fmaf(a, 1.0f - s, 1.0f);
@@ -92,7 +109,7 @@ __device__ __forceinline__ float silu_slope(float a) {
 }  // namespace
 
 template <typename IO, int K, int LN>
-__global__ __launch_bounds__(256, 5) void conv_bwd_kernel(ConvBwdParams p) {
+__global__ __launch_bounds__(256, LN == 64 ? 5 : 4) void conv_bwd_kernel(ConvBwdParams p) {
   constexpr int V = 16 / (int)sizeof(IO);
   constexpr int H = K - 1, HA = H > 0 ? H : 1;
   constexpr int P = kPasses;
@@ -101,6 +118,7 @@ __global__ __launch_bounds__(256, 5) void conv_bwd_kernel(ConvBwdParams p) {
   const int lane = threadIdx.x % LN;
   // row segment; their number fits 31 bits, so the divisions take 32
   uint32_t unit = blockIdx.x * (256 / LN) + threadIdx.x / LN;
+  if constexpr (LN == 64) unit = (uint32_t)__builtin_amdgcn_readfirstlane((int)unit);  // the wave's: scalar from here on
   const bool live = unit < p.units;
   unit = live ? unit : 0;
   const uint32_t r32 = unit / (uint32_t)p.S, s32 = unit - r32 * (uint32_t)p.S;
@@ -256,12 +274,9 @@ __global__ __launch_bounds__(256, 5) void conv_bwd_kernel(ConvBwdParams p) {
   }
 
   // the segment's sums over its lanes
+  sb = sum_lanes<LN>(sb);
 #pragma unroll
-  for (int o = LN / 2; o > 0; o >>= 1) {
-    sb += __shfl_xor(sb, o, LN);
-#pragma unroll
-    for (int k = 0; k < K; ++k) sw[k] += __shfl_xor(sw[k], o, LN);
-  }
+  for (int k = 0; k < K; ++k) sw[k] = sum_lanes<LN>(sw[k]);
   if (live && lane == 0) {
     const bool whole = p.Bsz * p.S == 1;  // the only segment of its channel: these are the results
     float* o = whole ? p.dw + d * K : p.part + (((int64_t)b32 * p.S + seg) * p.Dm + d) * (K + 1);
