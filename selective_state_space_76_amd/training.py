@@ -24,6 +24,8 @@ SSM_I64 = 1
 SSM_FLAG_CHANNELS_FIRST = 1
 SSM_FLAG_ACCUMULATE = 2
 ADAMW_BLOCK = 128
+_KIND = {torch.float32: SSM_F32, torch.bfloat16: SSM_BF16}
+_INDEX = {torch.int32: SSM_I32, torch.int64: SSM_I64}
 
 
 # Small calls are bound by the host, so the checks of _lib.py are made in their cheapest order here: plain numbers
@@ -72,21 +74,24 @@ def conv1d_bwd(x, weight, bias=None, initial_state=None, *, dout, dfinal_state=N
     lib = load()
     Bsz, Dm, L = x.shape
     K = weight.shape[1]
-    _nonempty(batch=Bsz, dim=Dm, seqlen=L, width=K)
-    io, device, f32 = _io_dtype(x), x.device, torch.float32
-    state = (Bsz, Dm, K - 1)
-    for t, shp, dt, name in ((weight, (Dm, K), f32, "weight"), (bias, (Dm,), f32, "bias"),
-                             (initial_state, state, x.dtype, "initial_state"), (dout, (Bsz, Dm, L), x.dtype, "dout"),
-                             (dfinal_state, state, x.dtype, "dfinal_state")):
-        _want(t, shp, dt, name, device)
-    g, made = dict(grads or {}), []
-    for k, (shp, dt) in dict(dx=((Bsz, Dm, L), x.dtype), dweight=((Dm, K), f32), dbias=((Dm,), f32),
-                             dinitial_state=(state, x.dtype)).items():
+    if Bsz < 1 or Dm < 1 or L < 1 or K < 1:
+        _nonempty(batch=Bsz, dim=Dm, seqlen=L, width=K)
+    io, device, xdt, f32 = _io_dtype(x), x.device, x.dtype, torch.float32
+    full, state, taps, channels = (Bsz, Dm, L), (Bsz, Dm, K - 1), (Dm, K), (Dm,)
+    _want(weight, taps, f32, "weight", device)
+    _want(bias, channels, f32, "bias", device)
+    _want(initial_state, state, xdt, "initial_state", device)
+    _want(dout, full, xdt, "dout", device)
+    _want(dfinal_state, state, xdt, "dfinal_state", device)
+    g, made = dict(grads) if grads else {}, []
+    for k, shp, dt in (("dx", full, xdt), ("dweight", taps, f32), ("dbias", channels, f32),
+                       ("dinitial_state", state, xdt)):
         if g.get(k) is None:
             g[k] = torch.empty(shp, dtype=dt, device=device)
             made.append(g[k])
-        _want(g[k], shp, dt, k, device)
-    workspace, ws_bytes = _workspace(workspace, conv1d_bwd_workspace_size(Bsz, Dm, L, K, io), device, made)
+        else:
+            _want(g[k], shp, dt, k, device)
+    workspace, ws_bytes = _workspace(workspace, lib.ssm_conv1d_bwd_workspace_size(Bsz, Dm, L, K, io), device, made)
     _check(lib.ssm_conv1d_bwd(Bsz, Dm, L, K, io, _address(x), _address(weight), _address(bias),
                               _address(initial_state), _address(dout), _address(dfinal_state), _address(g["dx"]),
                               _address(g["dweight"]), _address(g["dbias"]), _address(g["dinitial_state"]),
@@ -96,22 +101,23 @@ def conv1d_bwd(x, weight, bias=None, initial_state=None, *, dout, dfinal_state=N
 
 
 def _embed_shape(tokens, rows, dim, table_dtype, io_dtype, channels_first, accumulate=False):
-    if tokens.dtype not in (torch.int32, torch.int64):
+    index, table, io = _INDEX.get(tokens.dtype), _KIND.get(table_dtype), _KIND.get(io_dtype)
+    if index is None:
         raise TypeError("tokens must be int32 or int64, got %s" % tokens.dtype)
-    if tokens.dim() not in (1, 2):
-        raise ValueError("tokens: expected [B, L] or [T], got %d dimensions" % tokens.dim())
-    if channels_first and tokens.dim() != 2:
+    if table is None or io is None:
+        raise TypeError("tables and embeddings must be float32 or bfloat16, got %s"
+                        % (table_dtype if table is None else io_dtype))
+    size = tokens.shape
+    if len(size) not in (1, 2):
+        raise ValueError("tokens: expected [B, L] or [T], got %d dimensions" % len(size))
+    if channels_first and len(size) != 2:
         raise ValueError("channels_first needs tokens of shape [B, L]")
-    Bsz, L = tokens.shape if tokens.dim() == 2 else (1, tokens.shape[0])
-    _nonempty(batch=Bsz, seqlen=L, rows=rows, dim=dim)
-    kind = {torch.float32: SSM_F32, torch.bfloat16: SSM_BF16}
-    for dt in (table_dtype, io_dtype):
-        if dt not in kind:
-            raise TypeError("tables and embeddings must be float32 or bfloat16, got %s" % dt)
+    Bsz, L = size if len(size) == 2 else (1, size[0])
+    if Bsz < 1 or L < 1 or rows < 1 or dim < 1:
+        _nonempty(batch=Bsz, seqlen=L, rows=rows, dim=dim)
     flags = (SSM_FLAG_CHANNELS_FIRST if channels_first else 0) | (SSM_FLAG_ACCUMULATE if accumulate else 0)
-    shape = (Bsz, dim, L) if channels_first else tuple(tokens.shape) + (dim,)
-    return ssm_embed_shape(Bsz, L, int(rows), int(dim), SSM_I64 if tokens.dtype == torch.int64 else SSM_I32,
-                           kind[table_dtype], kind[io_dtype], flags), shape
+    return (ssm_embed_shape(Bsz, L, rows, dim, index, table, io, flags),
+            (Bsz, dim, L) if channels_first else (*size, dim))
 
 
 def embedding_fwd(tokens, weight, *, scale=1.0, dtype=None, channels_first=False, out=None, stream=None):
@@ -122,16 +128,18 @@ def embedding_fwd(tokens, weight, *, scale=1.0, dtype=None, channels_first=False
     dtype = out.dtype if out is not None and dtype is None else dtype or weight.dtype
     if weight.dim() != 2:
         raise ValueError("weight: expected [V, E], got %d dimensions" % weight.dim())
-    sh, shape = _embed_shape(tokens, weight.shape[0], weight.shape[1], weight.dtype, dtype, channels_first)
-    device, made = tokens.device, []
+    rows, dim = weight.shape
+    sh, shape = _embed_shape(tokens, rows, dim, weight.dtype, dtype, channels_first)
+    device, made = tokens.device, None
     if out is None:
-        out = torch.empty(shape, dtype=dtype, device=device)
-        made.append(out)
-    _want(weight, weight.shape, weight.dtype, "weight", device)
-    _want(out, shape, dtype, "out", device)
-    _check(lib.ssm_embedding_fwd(ctypes.byref(sh), _address(tokens), _address(weight), float(scale), _address(out),
+        out = made = torch.empty(shape, dtype=dtype, device=device)
+    else:
+        _want(out, shape, dtype, "out", device)
+    if weight.device != device:
+        _expect(weight, weight.shape, weight.dtype, "weight", device)
+    _check(lib.ssm_embedding_fwd(ctypes.byref(sh), _address(tokens), _address(weight), scale, _address(out),
                                  _stream(stream, device)))
-    _on_stream(stream, *made)
+    _on_stream(stream, made)
     return out
 
 
@@ -165,7 +173,7 @@ def embedding_bwd(tokens, dout, rows, *, scale=1.0, channels_first=False, dtype=
     _want(dweight, (rows, dim), dtype, "dweight", device)
     need = int(lib.ssm_embedding_bwd_workspace_size(ctypes.byref(sh)))
     workspace, ws_bytes = _workspace(workspace, need, device, made)
-    _check(lib.ssm_embedding_bwd(ctypes.byref(sh), _address(tokens), _address(dout), float(scale), _address(dweight),
+    _check(lib.ssm_embedding_bwd(ctypes.byref(sh), _address(tokens), _address(dout), scale, _address(dweight),
                                  _address(workspace), ws_bytes, _stream(stream, device)))
     _on_stream(stream, *made)
     return dweight
@@ -187,6 +195,8 @@ class AdamW:
     max_grad_norm: scale the gradients so that their norm over all tensors is at most this; a step whose
         norm is not finite changes nothing.
     seed: of the stochastic rounding (a hash of seed, step, tensor and element: the same on every run).
+    (The number of the step is an argument of the kernels: a step captured in a graph repeats its bias correction and
+    random numbers with every replay.)
     state, step: state_dict()'s tensors to go on from (taken over, not copied), and the steps already made.
 
     The states of all tensors are flat buffers: tensor k's begin at offsets[k], a multiple of 128."""
