@@ -280,7 +280,8 @@ ssm_status ssm_conv1d_update(int64_t batch, int64_t dim, int64_t width, int32_t 
  * What a training step needs next to the scan and its gradients: the gradients of the conv,
  * the embedding of the tokens with its gradient, and the optimizer.  Conventions as above:
  * device pointers, 16-byte aligned bases, host-side checks before any launch, asynchronous on
- * `stream`, no allocation, fixed-order sums (bitwise reproducible). */
+ * `stream`, no allocation, fixed-order sums (bitwise reproducible).  A number that is out of its
+ * stated range (a scale that is not finite, a beta of 1) is SSM_ERR_UNSUPPORTED. */
 
 /* Bytes of device workspace ssm_conv1d_bwd needs (0 for invalid sizes): one partial sum of
  * dweight and dbias per row and segment of the sequence. */
@@ -345,7 +346,8 @@ ssm_status ssm_embedding_bwd(const ssm_embed_shape* shape, const void* tokens, c
                              float scale, void* dweight, void* workspace, size_t workspace_bytes,
                              struct ihipStream_t* stream);
 
-/* One parameter tensor of an optimizer step (dense, any shape). */
+/* One parameter tensor of an optimizer step (dense, any shape).  The params, gradients and state
+ * buffers of a step must not overlap (checked but for one tensor's param against another's). */
 typedef struct ssm_adamw_tensor {
   void* param;          /* read and written */
   const void* grad;

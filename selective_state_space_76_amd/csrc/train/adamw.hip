@@ -329,18 +329,8 @@ __global__ __launch_bounds__(256) void norm_part_kernel(NormTable t, double* par
   if (threadIdx.x == 0) part[blockIdx.x] = sm[0];
 }
 
-__global__ __launch_bounds__(1024) void norm_join_kernel(const double* part, int64_t n, double max_norm, float* result) {
-  __shared__ double sm[1024];
-  double s = 0.0;
-  int64_t i = threadIdx.x;
-  for (; i + 7 * 1024 < n; i += 8 * 1024) {
-    double x[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) x[e] = part[i + e * 1024];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) s += x[e];
-  }
-  for (; i < n; i += 1024) s += part[i];
+// The sum of a workgroup's 1024 lanes in a fixed tree, and from it the result.
+__device__ __forceinline__ void finish_norm(double s, double* sm, double max_norm, float* result) {
   sm[threadIdx.x] = s;
   __syncthreads();
   for (int h = 512; h > 0; h >>= 1) {
@@ -354,6 +344,52 @@ __global__ __launch_bounds__(1024) void norm_join_kernel(const double* part, int
     result[0] = out;
     result[1] = !finite ? __uint_as_float(0x7fc00000u) : norm > max_norm ? (float)(max_norm / norm) : 1.0f;
   }
+}
+
+__global__ __launch_bounds__(1024) void norm_join_kernel(const double* part, int64_t n, double max_norm, float* result) {
+  __shared__ double sm[1024];
+  double s = 0.0;
+  int64_t i = threadIdx.x;
+  for (; i + 7 * 1024 < n; i += 8 * 1024) {
+    double x[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[e] = part[i + e * 1024];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) s += x[e];
+  }
+  for (; i < n; i += 1024) s += part[i];
+  finish_norm(s, sm, max_norm, result);
+}
+
+template <bool GB>
+__device__ __forceinline__ double chunk_squares(const void* g, int64_t base, int64_t n) {
+  constexpr int V = GB ? 8 : 4, N = (int)(kSmallChunk / (64 * V));
+  using IO = std::conditional_t<GB, bf16_t, float>;
+  Raw<IO, V> x[N];
+#pragma unroll
+  for (int q = 0; q < N; ++q) {
+    const int64_t i = base + (q * 64 + (threadIdx.x & 63)) * V, left = n - i;
+    x[q].load(static_cast<const IO*>(g) + i, left >= V ? V : left > 0 ? (int)left : 0);
+  }
+  double s = 0.0;
+#pragma unroll
+  for (int q = 0; q < N; ++q)
+#pragma unroll
+    for (int e = 0; e < V; ++e) s = __builtin_fma((double)x[q].at(e), (double)x[q].at(e), s);
+  return s;
+}
+
+// Few and small tensors: one workgroup, a wave per chunk, and no second launch.
+__global__ __launch_bounds__(1024) void norm_small_kernel(SmallNormTable t, uint32_t chunks, double max_norm,
+                                                          float* result) {
+  __shared__ double sm[1024];
+  double s = 0.0;
+  for (uint32_t c = threadIdx.x >> 6; c < chunks; c += 16) {
+    const int k = find(t, c);
+    const int64_t base = (int64_t)(c - t.first[k]) * kSmallChunk;
+    s += t.bf16[k] ? chunk_squares<true>(t.g[k], base, t.n[k]) : chunk_squares<false>(t.g[k], base, t.n[k]);
+  }
+  finish_norm(s, sm, max_norm, result);
 }
 
 // (c + K) << 20 has its set bits in the upper half: the value in bf16 is (c + K) << 4, exactly
@@ -411,6 +447,11 @@ hipError_t launch_adamw(const AdamTable& t, const AdamParams& p, int kind, uint3
 hipError_t launch_norm_part(const NormTable& t, double* part, bool bf16, uint32_t blocks, hipStream_t s) {
   if (bf16) hipLaunchKernelGGL(norm_part_kernel<true>, dim3(blocks), dim3(256), 0, s, t, part);
   else hipLaunchKernelGGL(norm_part_kernel<false>, dim3(blocks), dim3(256), 0, s, t, part);
+  return hipGetLastError();
+}
+
+hipError_t launch_norm_small(const SmallNormTable& t, uint32_t chunks, double max_norm, float* result, hipStream_t s) {
+  hipLaunchKernelGGL(norm_small_kernel, dim3(1), dim3(1024), 0, s, t, chunks, max_norm, result);
   return hipGetLastError();
 }
 

@@ -264,6 +264,21 @@ ssm_status ssm_grad_norm(const ssm_adamw_tensor* tensors, int64_t count, double 
     if (overlaps(outs[0], g) || overlaps(outs[1], g)) return SSM_ERR_OVERLAP;
   }
   hipStream_t st = reinterpret_cast<hipStream_t>(stream);
+  int64_t chunks = 0;
+  for (int64_t k = 0; k < count && chunks <= ssm::kSmallChunks; ++k) chunks += chunks_of(tensors[k].numel, ssm::kSmallChunk);
+  if (count <= ssm::kSmallTensors && chunks <= ssm::kSmallChunks) {
+    ssm::SmallNormTable t;
+    uint32_t first = 0;
+    for (int k = 0; k < (int)count; ++k) {
+      t.g[k] = tensors[k].grad;
+      t.n[k] = tensors[k].numel;
+      t.first[k] = first;
+      t.bf16[k] = tensors[k].grad_dtype == SSM_BF16;
+      first += (uint32_t)chunks_of(tensors[k].numel, ssm::kSmallChunk);
+    }
+    t.count = (int)count;
+    return launch_status(ssm::launch_norm_small(t, first, max_norm, result, st));
+  }
   double* part = static_cast<double*>(workspace);
   int64_t done = 0;
   for (int b = 0; b < 2; ++b) {

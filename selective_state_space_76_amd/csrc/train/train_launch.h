@@ -52,6 +52,16 @@ struct NormTable {
   int count;
 };
 
+constexpr int kSmallTensors = 64, kSmallChunks = 64;  // what one workgroup sums up by itself
+constexpr int64_t kSmallChunk = 2048;
+struct SmallNormTable {
+  const void* g[kSmallTensors];
+  int64_t n[kSmallTensors];
+  uint32_t first[kSmallTensors];
+  uint8_t bf16[kSmallTensors];
+  int count;
+};
+
 struct AdamParams {
   void* m;
   void* v;
@@ -67,6 +77,7 @@ uint32_t adam_key(uint64_t seed, int64_t step, int64_t tensor);
 // kind: bit 0 bf16 params, bit 1 bf16 gradients, bit 2 master weights, bit 3 8-bit states
 hipError_t launch_adamw(const AdamTable& t, const AdamParams& p, int kind, uint32_t blocks, hipStream_t s);
 hipError_t launch_norm_part(const NormTable& t, double* part, bool bf16, uint32_t blocks, hipStream_t s);
+hipError_t launch_norm_small(const SmallNormTable& t, uint32_t chunks, double max_norm, float* result, hipStream_t s);
 hipError_t launch_norm_join(const double* part, int64_t n, double max_norm, float* result, hipStream_t s);
 hipError_t launch_state_values(int64_t n, const void* m, const void* v, const int16_t* mb, const int16_t* vb,
                                void* mo, void* vo, hipStream_t s);

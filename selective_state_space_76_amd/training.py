@@ -12,6 +12,7 @@ include/ssm_scan.h for the formulas and layouts), and nothing falls back to anyt
 from __future__ import annotations
 
 import ctypes
+import math
 
 import numpy as np
 import torch
@@ -100,7 +101,7 @@ def conv1d_bwd(x, weight, bias=None, initial_state=None, *, dout, dfinal_state=N
     return g
 
 
-def _embed_shape(tokens, rows, dim, table_dtype, io_dtype, channels_first, accumulate=False):
+def _embed_shape(tokens, rows, dim, table_dtype, io_dtype, channels_first, accumulate=False, scale=1.0):
     index, table, io = _INDEX.get(tokens.dtype), _KIND.get(table_dtype), _KIND.get(io_dtype)
     if index is None:
         raise TypeError("tokens must be int32 or int64, got %s" % tokens.dtype)
@@ -115,6 +116,8 @@ def _embed_shape(tokens, rows, dim, table_dtype, io_dtype, channels_first, accum
     Bsz, L = size if len(size) == 2 else (1, size[0])
     if Bsz < 1 or L < 1 or rows < 1 or dim < 1:
         _nonempty(batch=Bsz, seqlen=L, rows=rows, dim=dim)
+    if not math.isfinite(scale):
+        raise ValueError("scale must be finite, got %r" % (scale,))
     flags = (SSM_FLAG_CHANNELS_FIRST if channels_first else 0) | (SSM_FLAG_ACCUMULATE if accumulate else 0)
     return (ssm_embed_shape(Bsz, L, rows, dim, index, table, io, flags),
             (Bsz, dim, L) if channels_first else (*size, dim))
@@ -129,7 +132,7 @@ def embedding_fwd(tokens, weight, *, scale=1.0, dtype=None, channels_first=False
     if weight.dim() != 2:
         raise ValueError("weight: expected [V, E], got %d dimensions" % weight.dim())
     rows, dim = weight.shape
-    sh, shape = _embed_shape(tokens, rows, dim, weight.dtype, dtype, channels_first)
+    sh, shape = _embed_shape(tokens, rows, dim, weight.dtype, dtype, channels_first, scale=scale)
     device, made = tokens.device, None
     if out is None:
         out = made = torch.empty(shape, dtype=dtype, device=device)
@@ -164,7 +167,7 @@ def embedding_bwd(tokens, dout, rows, *, scale=1.0, channels_first=False, dtype=
     if dout.dim() != want:
         raise ValueError("dout: expected %d dimensions, got %d" % (want, dout.dim()))
     dim = dout.shape[1 if channels_first else -1]
-    sh, shape = _embed_shape(tokens, rows, dim, dtype, dout.dtype, channels_first, accumulate)
+    sh, shape = _embed_shape(tokens, rows, dim, dtype, dout.dtype, channels_first, accumulate, scale)
     device, made = tokens.device, []
     _want(dout, shape, dout.dtype, "dout", device)
     if dweight is None:
@@ -292,6 +295,11 @@ class AdamW:
             grads = [p if g is None else g for p, g in zip(self.params, grads)]
             table["grad"] = np.array(self._checked(grads, "grads"), np.uint64)[have]
             table["grad_dtype"] = np.array([_io_dtype(g) for g in grads])[have]
+        if not (0 <= self.betas[0] < 1 and 0 <= self.betas[1] < 1 and 1e-30 <= self.eps <= 1e30
+                and math.isfinite(self.lr) and math.isfinite(self.weight_decay)
+                and (self.max_grad_norm is None or self.max_grad_norm > 0)):
+            raise ValueError("lr %r, betas %r, eps %r, weight_decay %r, max_grad_norm %r: out of range"
+                             % (self.lr, self.betas, self.eps, self.weight_decay, self.max_grad_norm))
         rows, count = table.ctypes.data, len(table)
         s, made, norm, clip = _stream(stream, self.device), [], None, None
         if self.max_grad_norm is not None:

@@ -170,6 +170,19 @@ def test_norm_and_clip():
             assert (np.abs(part(opt.state["exp_avg"], opt, k, p.numel()) - m) <= 4 * 2.0 ** -24 * np.abs(m)).all()
 
 
+@pytest.mark.parametrize("sizes", [[(1,)], [(5,), (2047,), (2048,), (2049,), (8,), (3, 5)], [(2048,)] * 64, [(2048,)] * 65,
+                                   [(70,)] * 64, [(70,)] * 65, [(1 + k % 300,) for k in range(410)]],
+                         ids=["one", "few", "64 chunks", "65 chunks", "64 tensors", "65 tensors", "410 tensors"])
+@pytest.mark.parametrize("gt", [[F32], [BF16], [BF16, F32, F32]], ids=["gf32", "gbf16", "gmixed"])
+def test_norm_of_many_sizes(sizes, gt):
+    """Around what one workgroup takes, and more tensors than one launch does."""
+    params = [torch.zeros(s, device=DEV) for s in sizes]
+    grads = [g.to(DEV) for g in grads_of(params, gt, 31, mul=1.0)]
+    norm = math.sqrt(sum(float((f64(g) ** 2).sum()) for g in grads))
+    got = AdamW(params, **HYPER, max_grad_norm=1.0).step(grads).item()
+    assert abs(got - norm) <= 2.0 ** -23 * norm
+
+
 @pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
 def test_step_that_is_not_finite_changes_nothing(bad):
     params = [p.to(DEV) for p in make(SIZES, [F32, BF16], 4)]
@@ -232,6 +245,37 @@ def test_resumes_from_its_state():
         side.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(opt.params, other.params))
         assert all(torch.equal(opt.state[k], other.state[k]) for k in opt.state)
+
+
+def test_refusals():
+    p = torch.zeros(10, 6, device=DEV)
+    g = torch.zeros(10, 6, device=DEV)
+    for bad in (dict(betas=(1.0, 0.9)), dict(betas=(0.9, -0.1)), dict(eps=0.0), dict(lr=float("nan")), dict(max_grad_norm=0.0),
+                dict(weight_decay=float("inf"))):
+        with pytest.raises(ValueError, match="out of range"):
+            AdamW([p], **bad).step([g])
+    opt = AdamW([p])
+    with pytest.raises(ValueError, match="shapes differ"):
+        opt.step([g.t().contiguous()])
+    with pytest.raises(ValueError, match="contiguous"):
+        opt.step([torch.zeros(6, 10, device=DEV).t()])
+    with pytest.raises(ValueError, match="on cuda"):
+        opt.step([g.cpu()])
+    with pytest.raises(TypeError, match="float32 or bfloat16"):
+        opt.step([g.half()])
+    with pytest.raises(ValueError, match="gradients for"):
+        opt.step([g, g])
+    with pytest.raises(ValueError, match="overlap"):
+        AdamW([p, p.view(-1)[4:8]])
+    with pytest.raises(ValueError, match="exp_avg: expected shape"):
+        AdamW([p], state={"exp_avg": g})
+    with pytest.raises(ValueError, match="not expected"):
+        AdamW([p], state={"exp_avg_base": g})
+    with pytest.raises(RuntimeError, match="ALIGN"):
+        AdamW([torch.zeros(100, device=DEV)[1:]]).step([torch.zeros(99, device=DEV)])
+    with pytest.raises(RuntimeError, match="OVERLAP"):
+        opt.step([p])
+    assert opt.step_count == 0
 
 
 def test_more_than_2_31_elements():

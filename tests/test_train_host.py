@@ -153,6 +153,11 @@ def test_binding_refusals():
         embedding_fwd(tok, table.half())
     with pytest.raises(ValueError, match="seqlen=0"):
         embedding_fwd(tok[:, :0], table)
+    for scale in (float("nan"), float("inf")):
+        with pytest.raises(ValueError, match="scale"):
+            embedding_fwd(tok, table, scale=scale)
+        with pytest.raises(ValueError, match="scale"):
+            embedding_bwd(tok, torch.zeros(2, 5, 3), 7, scale=scale)
     with pytest.raises(ValueError, match="GPU"):
         embedding_fwd(tok, table)
     with pytest.raises(ValueError, match="dout: expected shape"):
