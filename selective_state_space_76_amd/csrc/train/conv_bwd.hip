@@ -169,6 +169,17 @@ __global__ __launch_bounds__(256, LN == 64 ? 5 : 4) void conv_bwd_kernel(ConvBwd
       }
     }
   };
+  auto initial = [&](const float* g) {  // dx at the steps before the row, from the row's first g
+    IO* di = static_cast<IO*>(p.dinit) + row * H;
+#pragma unroll
+    for (int i = 0; i < H; ++i) {  // step i - H
+      float s = 0.0f;
+#pragma unroll
+      for (int k = 0; k <= i; ++k) s = __builtin_fmaf(w[k], g[i - k], s);
+      if (dfin && i >= L) s += to_f32(dfin[i - L]);  // L < H: the final state still holds it
+      store_io(di + i, s);
+    }
+  };
   uint32_t before[W > 0 ? W : 1];  // the words before the segment (first lane)
   float after[HA];                 // g behind it (last lane)
 #pragma unroll
@@ -176,7 +187,7 @@ __global__ __launch_bounds__(256, LN == 64 ? 5 : 4) void conv_bwd_kernel(ConvBwd
 #pragma unroll
   for (int k = 0; k < HA; ++k) after[k] = 0.0f;
   if constexpr (H > 0) {
-    if (lane == 0 && live) {
+    if (lane == 0 && (t0 > 0 || init || begin > 0)) {
 #pragma unroll
       for (int k = 0; k < W; ++k) {
         if constexpr (V == 8) before[k] = input(-2 * (W - k)) | input(-2 * (W - k) + 1) << 16;
@@ -190,18 +201,10 @@ __global__ __launch_bounds__(256, LN == 64 ? 5 : 4) void conv_bwd_kernel(ConvBwd
             else xq[0][e] = input(e);
           }
       }
-      if (seg == 0 && p.dinit) {
+      if (begin > 0 && p.dinit) {  // the row's first g may lie in two lanes
         float g[HA];
         gradient(begin, g);
-        IO* di = static_cast<IO*>(p.dinit) + row * H;
-#pragma unroll
-        for (int i = 0; i < H; ++i) {  // dx at step i - H
-          float s = 0.0f;
-#pragma unroll
-          for (int k = 0; k <= i; ++k) s = __builtin_fmaf(w[k], g[i - k], s);
-          if (dfin && i >= L) s += to_f32(dfin[i - L]);  // L < H: the final state still holds it
-          store_io(di + i, s);
-        }
+        initial(g);
       }
     }
     if (lane == LN - 1 && end > SEG) gradient(SEG, after);
@@ -255,6 +258,7 @@ __global__ __launch_bounds__(256, LN == 64 ? 5 : 4) void conv_bwd_kernel(ConvBwd
       dxe[e] = s;
     }
     if constexpr (H > 0) {
+      if (j == 0 && lane == 0 && seg == 0 && begin == 0 && live && p.dinit) initial(ge);
       if (dfin && i + V > end - H) {  // the last H inputs are the final state
 #pragma unroll
         for (int e = 0; e < V; ++e) {
