@@ -48,8 +48,11 @@ template <int V>
 __device__ __forceinline__ void store(float* p, int c, const float (&x)[V]) {
   if (c == V) {
 #pragma unroll
-    for (int i = 0; i < V; i += 4)
-      __builtin_nontemporal_store(f32x4{x[i], x[i + 1], x[i + 2], x[i + 3]}, reinterpret_cast<f32x4*>(p + i));
+    for (int i = 0; i < V; i += 4) {
+      const f32x4 q = {x[i], x[i + 1], x[i + 2], x[i + 3]};
+      if constexpr (V == 4) __builtin_nontemporal_store(q, reinterpret_cast<f32x4*>(p + i));
+      else *reinterpret_cast<f32x4*>(p + i) = q;  // half a line at a time: put together by the cache
+    }
   } else {
 #pragma unroll
     for (int i = 0; i < V; ++i)

@@ -40,7 +40,7 @@ __device__ __forceinline__ uint32_t key_at(const SortParams& p, int64_t i) {
   return p.tokens ? (uint32_t)token_at(p.tokens, p.i64, i, p.V) : p.key_in[i];
 }
 
-constexpr int64_t kFill = 65536;  // bytes per workgroup
+constexpr int64_t kFill = 16384;  // bytes per workgroup
 
 // clears piece `block` of the bytes to fill
 __device__ __forceinline__ void fill_piece(const SortParams& p, int64_t block, int threads) {

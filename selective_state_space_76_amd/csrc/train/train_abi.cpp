@@ -121,7 +121,7 @@ ssm_status embed_check(const ssm_embed_shape* s, uint32_t flags, ssm::EmbedParam
   int64_t n, te, ve;
   if (!mul_ok(s->batch, s->seqlen, &n) || n > kMaxGrid || s->rows >= kMaxGrid || s->dim > kMaxSize) return SSM_ERR_SHAPE;
   if (!mul_ok(n, s->dim, &te) || !mul_ok(s->rows, s->dim, &ve)) return SSM_ERR_SHAPE;
-  if (ve > (int64_t(1) << 44)) return SSM_ERR_SHAPE;  // cleared in pieces of 64 KiB, one workgroup each
+  if (ve > (int64_t(1) << 42)) return SSM_ERR_SHAPE;  // cleared in pieces of 16 KiB, one workgroup each
   // every kernel's grid: at most one workgroup per position and 64 columns, or per 256 pieces of 16 bytes
   int64_t blocks;
   if (!mul_ok(n, (s->dim + 63) / 64, &blocks) || blocks > kMaxGrid) return SSM_ERR_SHAPE;

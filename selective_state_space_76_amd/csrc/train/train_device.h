@@ -66,7 +66,8 @@ struct Raw {
 #pragma unroll
       for (int k = 0; k < W / C; ++k) {
         const piece* a = reinterpret_cast<const piece*>(p + k * C * 4 / (int)sizeof(IO));
-        const piece q = NT ? __builtin_nontemporal_load(a) : *a;
+        // two pieces lie in one line: the first must not drop it
+        const piece q = NT && W == C ? __builtin_nontemporal_load(a) : *a;
 #pragma unroll
         for (int i = 0; i < C; ++i) w[k * C + i] = q[i];
       }
@@ -100,7 +101,9 @@ __device__ __forceinline__ void store_n(IO* p, int n, const float (&x)[N]) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) q[i] = __float_as_uint(x[k * V + i]);
       }
-      __builtin_nontemporal_store(q, reinterpret_cast<typename Unaligned<IO>::type*>(p + k * V));
+      auto* a = reinterpret_cast<typename Unaligned<IO>::type*>(p + k * V);
+      if constexpr (N == V) __builtin_nontemporal_store(q, a);
+      else *a = q;  // half a line at a time: put together by the cache
     }
   } else {
 #pragma unroll
