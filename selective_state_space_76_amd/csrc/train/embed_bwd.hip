@@ -3,18 +3,21 @@
 // The positions are sorted by token, equal tokens in order of position, and each token's rows are summed in
 // that order: no atomics on the sums, so the result is the same bits on every run.
 //   1. Sort: a stable radix sort of (token, position), digits of up to 8 bits, the lowest first.  Up to 4096
-//      positions are sorted by one workgroup in LDS (12.7 us, where the launches below take 17; 16384
-//      would take 41 against 18); more of them take, per digit, a counting pass and a
-//      moving pass, in which every workgroup adds up the counts of the tiles before its own.  A wave
-//      ranks 64 keys at a time by ballots over the digit's bits.  The sort is short and narrow: the
-//      other workgroups of its launches clear dweight meanwhile (not when the gradient is added to).
+//      positions are sorted by one workgroup in LDS (12.7 us, where the launches below take 17; 16384 would
+//      take 41 against 18); more of them take, per digit, a counting pass and a moving pass, in which every
+//      workgroup adds up the counts of the tiles before its own.  A wave ranks 64 keys at a time by
+//      ballots over the digit's bits.  The sort is short and narrow: the other workgroups of its
+//      launches clear dweight meanwhile (not when the gradient is added to).
 //   2. Sums: the sorted list is cut into chunks of `run` rows.  A wave owns a chunk and 64 * VC columns; it
 //      keeps 8 rows in flight and adds them to the running token's sum.  Sums of tokens that lie within
 //      the chunk go to dweight; one that reaches over an end goes to memory as a partial sum.
 //   3. Join: where a token's rows begin in a chunk and go on in the next, its partial sums are added, in order.
 // dout in [B,E,L] is first brought to [B,L,E], unless the table has few rows (embed_bwd_few.hip).
-// Bound by HBM: dout is read once in whole rows, dweight is written once.
 // Tokens outside the table sort as V, behind all others, and are left out.
+//
+// Bound by HBM, which the launches reach in part: 8 x 2048 tokens of width 768 into 50000 rows (25 MB read, 154 MB
+// cleared or written) take 48 us, of which 30 are the sort's four launches with the clearing (5.1 TB/s), 11 the sums
+// and 6 the join.  262144 x 1024 in bf16: 148 us (sort 33, sums 105 at 5.1 TB/s, join 10).
 #include "../ssm_device.h"
 #include "train_device.h"
 #include "train_launch.h"
@@ -254,7 +257,8 @@ __device__ __forceinline__ OT* row_at(const SumParams& p, uint32_t k, int64_t co
 }
 
 // With ADD the rows of dweight that a group of 8 will add to are loaded with the group, not one by one as the
-// tokens change (41 -> 27 us per call for 509 tokens of width 768 into a table of 50000 rows).
+// tokens change: one wait for memory per group and not per token (509 tokens of width 768 into a table of 50000
+// rows: this kernel 18 -> 7 us, with chunks of 8 rows and not 32).
 // NT: dout is too large to be found in the Infinity Cache (256 MB), where a backward pass has just left it, and
 // is read as not needed again (16384 x 768: 53 -> 49 us per call without; 262144 x 1024: 165 -> 153 us with).
 template <typename IO, typename OT, int VC, bool ADD, bool NT>
@@ -289,7 +293,9 @@ __global__ __launch_bounds__(256) void embed_sum_kernel(SumParams p) {
       uint32_t k[9];
 #pragma unroll
       for (int q = 0; q < 9; ++q)
-        k[q] = r + q < m ? (uint32_t)__builtin_amdgcn_readlane((int)kv, r + q < 64 ? r + q : 63) : r + q == m ? after : V;
+        k[q] = r + q < m    ? (uint32_t)__builtin_amdgcn_readlane((int)kv, r + q < 64 ? r + q : 63)
+               : r + q == m ? after
+                            : V;
 #pragma unroll
       for (int q = 0; q < 8; ++q) {
         if (r + q >= m || k[q] == V) continue;  // past the chunk, or outside the table as all that follow
@@ -436,7 +442,8 @@ __global__ __launch_bounds__(256) void embed_turn_kernel(const IO* in, IO* out, 
   }
 }
 
-// columns per lane of the sums: 8 (16 bytes) where that covers a row with no more idle lanes than 4
+// Columns per lane of the sums: 8 (16 bytes) where that covers a row with no more idle lanes than 4
+// (262144 x 1024: 153 us with 8, 159 with 4; 262144 x 1000: 189 and 247).
 int columns(int64_t E, bool io_bf16) { return io_bf16 && (E + 511) / 512 * 2 == (E + 255) / 256 ? 8 : 4; }
 
 template <typename IO, typename OT, int VC>
@@ -501,10 +508,14 @@ void plan_embed_bwd(int64_t Bsz, int64_t L, int64_t V, int64_t E, bool io_bf16, 
   while ((V >> pl->bits) != 0) ++pl->bits;  // keys 0 .. V
   pl->passes = (pl->bits + 7) / 8;
   pl->digit_bits = (pl->bits + pl->passes - 1) / pl->passes;
+  // Small tiles spread a short list over the chip; but each adds up the counts of all tiles, so long lists take
+  // larger ones.  Whole calls of width 4 with tiles of 512 / 4096 / 8192: 29 / 38 / 46 us for 16384 positions,
+  // 52 / 56 / 68 for 65536, 76 / 71 / 78 for 131072, 603 / 322 / 320 for 2^20, 6.0 / 0.96 / 0.90 ms for 2^22.
   pl->tile = n <= 4096 ? 4096 : n <= 65536 ? 512 : n <= 524288 ? 4096 : 8192;
   pl->tiles = (n + pl->tile - 1) / pl->tile;
-  // rows per chunk of the sums: about 4096 waves, so that short lists spread over the chip and long ones
-  // leave few partial sums
+  // Rows per chunk of the sums: about 4096 waves, so that short lists spread over the chip and long ones leave few
+  // partial sums (16384 x 768: 52.1 us with 4096, 53.2 with 8192, 56.6 with 2048; 262144 x 1024: 153 with 128 rows,
+  // 163 with 64, 176 with 32).
   const int64_t tiles_e = (E + 64 * columns(E, io_bf16) - 1) / (64 * columns(E, io_bf16));
   pl->run = 8;
   while (pl->run < 256 && n * tiles_e > pl->run * 4096) pl->run *= 2;

@@ -104,7 +104,8 @@ ssm_status ssm_conv1d_bwd(int64_t batch, int64_t dim, int64_t seqlen, int64_t wi
   memset(&p, 0, sizeof(p));
   p.x = x; p.w = weight; p.bias = bias; p.init = init; p.dout = dout; p.dfinal = dfinal;
   p.dx = dx; p.dinit = dinit; p.dw = dweight; p.db = dbias; p.part = static_cast<float*>(workspace);
-  p.Bsz = batch; p.Dm = dim; p.L = seqlen; p.S = pl.S; p.units = (uint32_t)(pl.bd * pl.S); p.K = (int)width; p.lanes = pl.lanes;
+  p.Bsz = batch; p.Dm = dim; p.L = seqlen; p.K = (int)width;
+  p.S = pl.S; p.units = (uint32_t)(pl.bd * pl.S); p.lanes = pl.lanes;
   return launch_status(ssm::launch_conv_bwd(p, io_dtype == SSM_BF16, reinterpret_cast<hipStream_t>(stream)));
 }
 
@@ -119,7 +120,8 @@ ssm_status embed_check(const ssm_embed_shape* s, uint32_t flags, ssm::EmbedParam
   if (s->flags & ~flags) return SSM_ERR_UNSUPPORTED;
   if (s->batch < 1 || s->seqlen < 1 || s->rows < 1 || s->dim < 1) return SSM_ERR_SHAPE;
   int64_t n, te, ve;
-  if (!mul_ok(s->batch, s->seqlen, &n) || n > kMaxGrid || s->rows >= kMaxGrid || s->dim > kMaxSize) return SSM_ERR_SHAPE;
+  if (!mul_ok(s->batch, s->seqlen, &n) || n > kMaxGrid) return SSM_ERR_SHAPE;
+  if (s->rows >= kMaxGrid || s->dim > kMaxSize) return SSM_ERR_SHAPE;
   if (!mul_ok(n, s->dim, &te) || !mul_ok(s->rows, s->dim, &ve)) return SSM_ERR_SHAPE;
   if (ve > (int64_t(1) << 42)) return SSM_ERR_SHAPE;  // cleared in pieces of 16 KiB, one workgroup each
   // every kernel's grid: at most one workgroup per position and 64 columns, or per 256 pieces of 16 bytes
@@ -145,7 +147,8 @@ ssm_status ssm_embedding_fwd(const ssm_embed_shape* shape, const void* tokens, c
   if (!tokens || !weight || !out) return SSM_ERR_NULL;
   if (!isfinite(scale)) return SSM_ERR_UNSUPPORTED;
   if (misaligned(tokens) || misaligned(weight) || misaligned(out)) return SSM_ERR_ALIGN;
-  const Range ins[] = {span(tokens, p.T * (p.i64 ? 8 : 4)), span(weight, p.V * p.E * dtype_size(shape->table_dtype))};
+  const Range ins[] = {span(tokens, p.T * (p.i64 ? 8 : 4)),
+                       span(weight, p.V * p.E * dtype_size(shape->table_dtype))};
   const Range outs[] = {span(out, p.T * p.E * dtype_size(shape->io_dtype))};
   if (any_overlap(outs, 1, ins, 2)) return SSM_ERR_OVERLAP;
   p.tokens = tokens; p.table = weight; p.out = out; p.scale = scale;
@@ -173,7 +176,8 @@ ssm_status ssm_embedding_bwd(const ssm_embed_shape* shape, const void* tokens, c
   ssm::plan_embed_bwd(p.Bsz, p.L, p.V, p.E, shape->io_dtype == SSM_BF16, p.cf, &pl);
   if (workspace_bytes < pl.total) return SSM_ERR_WORKSPACE;
   const Range ins[] = {span(tokens, p.T * (p.i64 ? 8 : 4)), span(dout, p.T * p.E * dtype_size(shape->io_dtype))};
-  const Range outs[] = {span(dweight, p.V * p.E * dtype_size(shape->table_dtype)), span(workspace, (int64_t)pl.total)};
+  const Range outs[] = {span(dweight, p.V * p.E * dtype_size(shape->table_dtype)),
+                        span(workspace, (int64_t)pl.total)};
   if (any_overlap(outs, 2, ins, 2)) return SSM_ERR_OVERLAP;
   p.tokens = tokens; p.dout = dout; p.out = dweight; p.scale = scale;
   return launch_status(ssm::launch_embed_bwd(p, pl, shape->table_dtype == SSM_BF16, shape->io_dtype == SSM_BF16,
@@ -265,7 +269,8 @@ ssm_status ssm_grad_norm(const ssm_adamw_tensor* tensors, int64_t count, double 
   }
   hipStream_t st = reinterpret_cast<hipStream_t>(stream);
   int64_t chunks = 0;
-  for (int64_t k = 0; k < count && chunks <= ssm::kSmallChunks; ++k) chunks += chunks_of(tensors[k].numel, ssm::kSmallChunk);
+  for (int64_t k = 0; k < count && chunks <= ssm::kSmallChunks; ++k)
+    chunks += chunks_of(tensors[k].numel, ssm::kSmallChunk);
   if (count <= ssm::kSmallTensors && chunks <= ssm::kSmallChunks) {
     ssm::SmallNormTable t;
     uint32_t first = 0;

@@ -20,7 +20,7 @@ __device__ __forceinline__ int64_t token_at(const void* tokens, int i64, int64_t
   return k >= 0 && k < V ? k : V;
 }
 
-// N elements from p, of which the first n exist (the others are zero); nt: they are not needed again
+// N elements from p, of which the first n exist (the others are zero); NT: they are not needed again
 template <typename IO, int N, bool NT = false>
 __device__ __forceinline__ void load_n(const IO* p, int n, float (&x)[N]) {
   constexpr int V = 16 / (int)sizeof(IO);
@@ -28,7 +28,8 @@ __device__ __forceinline__ void load_n(const IO* p, int n, float (&x)[N]) {
 #pragma unroll
     for (int k = 0; k < N / V; ++k) {
       const auto* a = reinterpret_cast<const typename Unaligned<IO>::type*>(p + k * V);
-      const auto q = NT ? __builtin_nontemporal_load(a) : *a;
+      // (of two pieces of one line the first must not drop it)
+      const auto q = NT && N == V ? __builtin_nontemporal_load(a) : *a;
       if constexpr (V == 8) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -105,6 +106,14 @@ __device__ __forceinline__ void store_n(IO* p, int n, const float (&x)[N]) {
       if constexpr (N == V) __builtin_nontemporal_store(q, a);
       else *a = q;  // half a line at a time: put together by the cache
     }
+  } else if (n == N && N == 4 && V == 8) {
+    typedef uint32_t u32x2u __attribute__((ext_vector_type(2), aligned(2)));
+    u32x2u q;
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      q[i] = (uint32_t)__builtin_bit_cast(uint16_t, (__bf16)x[2 * i]) |
+             ((uint32_t)__builtin_bit_cast(uint16_t, (__bf16)x[2 * i + 1]) << 16);
+    __builtin_nontemporal_store(q, reinterpret_cast<u32x2u*>(p));
   } else {
 #pragma unroll
     for (int i = 0; i < N; ++i)

@@ -212,7 +212,8 @@ class AdamW:
         if state_bits not in (8, 32):
             raise ValueError("state_bits must be 8 or 32, got %r" % (state_bits,))
         self.lr, self.betas, self.eps, self.weight_decay = lr, tuple(betas), eps, weight_decay
-        self.state_bits, self.max_grad_norm, self.seed, self.step_count = state_bits, max_grad_norm, int(seed), int(step)
+        self.state_bits, self.max_grad_norm = state_bits, max_grad_norm
+        self.seed, self.step_count = int(seed), int(step)
         self.device = self.params[0].device
         for p in self.params:
             _io_dtype(p)
@@ -307,7 +308,8 @@ class AdamW:
             clip = torch.empty(2, dtype=torch.float32, device=self.device)
             workspace = torch.empty(need, dtype=torch.uint8, device=self.device)
             made = [clip, workspace]
-            _check(lib.ssm_grad_norm(rows, count, float(self.max_grad_norm), _address(clip), _address(workspace), need, s))
+            _check(lib.ssm_grad_norm(rows, count, float(self.max_grad_norm), _address(clip), _address(workspace), need,
+                                     s))
             norm = clip[0]
         cfg = ssm_adamw_config(self.lr, self.betas[0], self.betas[1], self.eps, self.weight_decay, self.step_count + 1,
                                self.seed & (2 ** 64 - 1), self.state_bits, 0)
@@ -328,7 +330,7 @@ class AdamW:
         m = torch.empty(self.numel, dtype=torch.bfloat16, device=self.device)
         v = torch.empty_like(m)
         _check(load().ssm_adamw_state_values(self.numel, _address(st["exp_avg"]), _address(st["exp_avg_sq"]),
-                                             _address(st["exp_avg_base"]), _address(st["exp_avg_sq_base"]), _address(m), _address(v),
-                                             _stream(stream, self.device)))
+                                             _address(st["exp_avg_base"]), _address(st["exp_avg_sq_base"]), _address(m),
+                                             _address(v), _stream(stream, self.device)))
         _on_stream(stream, m, v)
         return m, v
