@@ -3,10 +3,10 @@
 // The positions are sorted by token, equal tokens in order of position, and each token's rows are summed in
 // that order: no atomics on the sums, so the result is the same bits on every run.
 //   1. Sort: a stable radix sort of (token, position), digits of up to 8 bits, the lowest first.  Up to 4096
-//      positions are sorted by one workgroup in LDS (12.7 us, where the launches below take 17; 16384 would
-//      take 41 against 18); more of them take, per digit, a counting pass and a moving pass, in which every
+//      positions are sorted by one workgroup in LDS (whole calls of width 4: 22 us, where the launches below
+//      take 25; 8192 would take 30 against 26); more of them take, per digit, a counting pass and a moving pass, in which every
 //      workgroup adds up the counts of the tiles before its own.  A wave ranks 64 keys at a time by
-//      ballots over the digit's bits.  The sort is short and narrow: the other workgroups of its
+//      ballots over the digit's bits, without a wait between them (4096: 26 -> 22 us per call).  The sort is short and narrow: the other workgroups of its
 //      launches clear dweight meanwhile (not when the gradient is added to).
 //   2. Sums: the sorted list is cut into chunks of `run` rows.  A wave owns a chunk and 64 * VC columns; it
 //      keeps 8 rows in flight and adds them to the running token's sum.  Sums of tokens that lie within
@@ -74,85 +74,106 @@ __device__ __forceinline__ void scan_digits(uint32_t* tot, int digits, int lane)
     if (lane * 4 + e < digits) tot[lane * 4 + e] = inc - s + v[e];
 }
 
-// Place of this lane's key among the wave's keys of one round: at[d] is where the digit's keys go next.
-__device__ __forceinline__ uint32_t place(uint32_t* at, uint32_t d, bool valid, int bits, int lane) {
-  uint64_t same = __ballot(valid);  // lanes with the same digit
-  for (int b = 0; b < bits; ++b) {
-    const uint64_t set = __ballot((d >> b) & 1u);
-    same &= (d >> b) & 1u ? set : ~set;
+// Where the wave's keys go: count[] (zero before, in LDS) gets the wave's number of each digit, rank[r] the number
+// of keys with the same digit before key r of this lane, in rounds of 64 keys.  A round's lanes find their equals
+// by ballots over the digit's 8 bits, read the count, and the first of them moves it on.  The LDS serves a wave in
+// order, so that nothing waits between the rounds.
+template <int R>
+__device__ __forceinline__ void rank_keys(uint32_t* count, const uint32_t (&key)[R], int shift, uint32_t mask,
+                                          int64_t base, int64_t n, int rounds, uint32_t (&rank)[R]) {
+  uint32_t below[R];
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    rank[r] = below[r] = 0;
+    if (r >= rounds) continue;
+    const bool valid = base + r * 64 < n;
+    const uint32_t d = (key[r] >> shift) & mask;
+    const uint64_t in = __ballot(valid);
+    uint32_t lo = (uint32_t)in, hi = (uint32_t)(in >> 32);  // lanes with the same digit
+#pragma unroll
+    for (int b = 0; b < 8; ++b) {
+      const int32_t bit = (int32_t)(d << (31 - b)) >> 31;
+      const uint64_t set = __ballot(bit < 0);
+      lo &= ~((uint32_t)set ^ (uint32_t)bit);
+      hi &= ~((uint32_t)(set >> 32) ^ (uint32_t)bit);
+    }
+    below[r] = __builtin_amdgcn_mbcnt_hi(hi, __builtin_amdgcn_mbcnt_lo(lo, 0u));
+    rank[r] = __hip_atomic_load(&count[d], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
+    __builtin_amdgcn_wave_barrier();
+    if (valid && below[r] == 0)
+      __hip_atomic_fetch_add(&count[d], (uint32_t)(__popc(lo) + __popc(hi)), __ATOMIC_RELAXED,
+                             __HIP_MEMORY_SCOPE_WORKGROUP);
+    __builtin_amdgcn_wave_barrier();
   }
-  const uint64_t below = same & ((1ull << lane) - 1);
-  uint32_t dst = 0;
-  if (valid) dst = at[d] + (uint32_t)__popcll(below);
-  wave_sync();  // every lane has read its place before the digit's first lane moves it on
-  if (valid && below == 0) at[d] = dst + (uint32_t)__popcll(same);
-  wave_sync();
-  return dst;
+#pragma unroll
+  for (int r = 0; r < R; ++r) rank[r] += below[r];
 }
 
-// Up to 1024 R keys in one workgroup, all digits: between the passes only the positions move, through LDS
-// (16 bits each), and the keys are looked up again.  The other workgroups fill.
+// Up to 1024 R keys in one workgroup, all digits.  Keys and positions move through LDS, in the last pass too:
+// stores in their new order would cost a line each (4096: 24 -> 22 us per call).  The other workgroups fill.
 template <int R>
 __global__ __launch_bounds__(1024) void sort_small_kernel(SortParams p) {
   if (blockIdx.x > 0) return fill_piece(p, blockIdx.x - 1, 1024);
-  __shared__ uint32_t at[16][256];
+  __shared__ uint32_t at[16][256];  // a wave's keys of a digit; then where they go
   __shared__ uint32_t tot[256];
+  __shared__ uint32_t keys[1024 * R];
   __shared__ uint16_t moved[1024 * R];
   const int digits = 1 << p.bits;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int base = wave * (64 * R) + lane, n = (int)p.n;
-  uint32_t key[R], pos[R];
+  const int n = (int)p.n, rounds = (n + 1023) / 1024;
+  const int base = wave * (64 * rounds) + lane;
+  uint32_t key[R], pos[R], rank[R];
 #pragma unroll
   for (int r = 0; r < R; ++r) {
     pos[r] = base + r * 64;
-    key[r] = (int)pos[r] < n ? key_at(p, pos[r]) : 0u;
+    key[r] = r < rounds && (int)pos[r] < n ? key_at(p, pos[r]) : 0u;
   }
   for (int pass = 0; pass < p.passes; ++pass) {
     const int shift = pass * p.bits;
     for (int i = tid; i < 16 * 256; i += 1024) (&at[0][0])[i] = 0;
     __syncthreads();
-#pragma unroll
-    for (int r = 0; r < R; ++r)
-      if (base + r * 64 < n) atomicAdd(&at[wave][(key[r] >> shift) & (digits - 1)], 1u);
+    rank_keys<R>(at[wave], key, shift, (uint32_t)digits - 1, base, n, rounds, rank);
     __syncthreads();
+    uint32_t c[16];
     if (tid < digits) {
       uint32_t all = 0;
-      for (int w = 0; w < 16; ++w) all += at[w][tid];
+#pragma unroll
+      for (int w = 0; w < 16; ++w) {
+        c[w] = all;
+        all += at[w][tid];
+      }
       tot[tid] = all;
     }
     __syncthreads();
     if (wave == 0) scan_digits(tot, digits, lane);
     __syncthreads();
     if (tid < digits) {
-      uint32_t a = tot[tid];
-      for (int w = 0; w < 16; ++w) {
-        const uint32_t c = at[w][tid];
-        at[w][tid] = a;
-        a += c;
-      }
+      const uint32_t a = tot[tid];
+#pragma unroll
+      for (int w = 0; w < 16; ++w) at[w][tid] = a + c[w];
     }
     __syncthreads();
-    const bool last = pass + 1 == p.passes;
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      const bool valid = base + r * 64 < n;
-      const uint32_t dst = place(at[wave], (key[r] >> shift) & (digits - 1), valid, p.bits, lane);
-      if (valid && last) {
-        p.key_out[dst] = key[r];
-        p.pos_out[dst] = pos[r];
-      } else if (valid) {
-        moved[dst] = (uint16_t)pos[r];
-      }
+      if (r >= rounds || base + r * 64 >= n) continue;
+      const uint32_t dst = at[wave][(key[r] >> shift) & (digits - 1)] + rank[r];
+      keys[dst] = key[r];
+      moved[dst] = (uint16_t)pos[r];
     }
-    if (last) break;
     __syncthreads();
 #pragma unroll
     for (int r = 0; r < R; ++r)
-      if (base + r * 64 < n) {
+      if (r < rounds && base + r * 64 < n) {
         pos[r] = moved[base + r * 64];
-        key[r] = key_at(p, pos[r]);
+        key[r] = keys[base + r * 64];
       }
   }
+#pragma unroll
+  for (int r = 0; r < R; ++r)
+    if (r < rounds && base + r * 64 < n) {
+      p.key_out[base + r * 64] = key[r];
+      p.pos_out[base + r * 64] = pos[r];
+    }
 }
 
 template <int NW, int R>
@@ -183,7 +204,7 @@ __global__ __launch_bounds__(NW * 64) void sort_move_kernel(SortParams p) {
   __syncthreads();
   // a wave's keys: 64 R consecutive ones
   const int64_t base = ((int64_t)blockIdx.x * NW + wave) * (64 * R) + lane;
-  uint32_t key[R], pos[R];
+  uint32_t key[R], pos[R], rank[R];
 #pragma unroll
   for (int r = 0; r < R; ++r) {
     const int64_t i = base + r * 64;
@@ -193,9 +214,6 @@ __global__ __launch_bounds__(NW * 64) void sort_move_kernel(SortParams p) {
       pos[r] = p.tokens ? (uint32_t)i : p.pos_in[i];
     }
   }
-#pragma unroll
-  for (int r = 0; r < R; ++r)
-    if (base + r * 64 < p.n) atomicAdd(&at[wave][(key[r] >> p.shift) & (digits - 1)], 1u);
   uint32_t mine = 0;  // a digit's keys in the tiles before this one
   if (tid < digits) {
     uint32_t all = 0;
@@ -217,6 +235,7 @@ __global__ __launch_bounds__(NW * 64) void sort_move_kernel(SortParams p) {
     }
     tot[tid] = all;
   }
+  rank_keys<R>(at[wave], key, p.shift, (uint32_t)digits - 1, base, p.n, R, rank);
   __syncthreads();
   if (wave == 0) scan_digits(tot, digits, lane);
   __syncthreads();
@@ -231,12 +250,10 @@ __global__ __launch_bounds__(NW * 64) void sort_move_kernel(SortParams p) {
   __syncthreads();
 #pragma unroll
   for (int r = 0; r < R; ++r) {
-    const bool valid = base + r * 64 < p.n;
-    const uint32_t dst = place(at[wave], (key[r] >> p.shift) & (digits - 1), valid, p.bits, lane);
-    if (valid) {
-      p.key_out[dst] = key[r];
-      p.pos_out[dst] = pos[r];
-    }
+    if (base + r * 64 >= p.n) continue;
+    const uint32_t dst = at[wave][(key[r] >> p.shift) & (digits - 1)] + rank[r];
+    p.key_out[dst] = key[r];
+    p.pos_out[dst] = pos[r];
   }
 }
 
