@@ -4,14 +4,16 @@
 // that order: no atomics on the sums, so the result is the same bits on every run.
 //   1. Sort: a stable radix sort of (token, position), digits of up to 8 bits, the lowest first.  Up to 4096
 //      positions are sorted by one workgroup in LDS (whole calls of width 4: 22 us, where the launches below
-//      take 25; 8192 would take 30 against 26); more of them take, per digit, a counting pass and a moving pass, in which every
-//      workgroup adds up the counts of the tiles before its own.  A wave ranks 64 keys at a time by
-//      ballots over the digit's bits, without a wait between them (4096: 26 -> 22 us per call).  The sort is short and narrow: the other workgroups of its
-//      launches clear dweight meanwhile (not when the gradient is added to).
+//      take 25; 8192 would take 30 against 26); more of them take, per digit, a counting pass and a moving pass,
+//      in which every workgroup adds up the counts of the tiles before its own.  A wave ranks 64 keys at a
+//      time by ballots over the digit's bits, without a wait between them (4096: 26 -> 22 us per call).  The
+//      sort is short and narrow: the other workgroups of its launches clear dweight meanwhile (not when the
+//      gradient is added to).
 //   2. Sums: the sorted list is cut into chunks of `run` rows.  A wave owns a chunk and 64 * VC columns; it
 //      keeps 8 rows in flight and adds them to the running token's sum.  Sums of tokens that lie within
 //      the chunk go to dweight; one that reaches over an end goes to memory as a partial sum.
 //   3. Join: where a token's rows begin in a chunk and go on in the next, its partial sums are added, in order.
+// Up to 1024 positions take all three in one launch where there is little to clear (embed_once_kernel).
 // dout in [B,E,L] is first brought to [B,L,E], unless the table has few rows (embed_bwd_few.hip).
 // Tokens outside the table sort as V, behind all others, and are left out.
 //
@@ -109,15 +111,17 @@ __device__ __forceinline__ void rank_keys(uint32_t* count, const uint32_t (&key)
   for (int r = 0; r < R; ++r) rank[r] += below[r];
 }
 
-// Up to 1024 R keys in one workgroup, all digits.  Keys and positions move through LDS, in the last pass too:
-// stores in their new order would cost a line each (4096: 24 -> 22 us per call).  The other workgroups fill.
+// Up to 1024 R keys sorted by one workgroup of 1024, all digits.  Keys and positions move through LDS and stay there.
 template <int R>
-__global__ __launch_bounds__(1024) void sort_small_kernel(SortParams p) {
-  if (blockIdx.x > 0) return fill_piece(p, blockIdx.x - 1, 1024);
-  __shared__ uint32_t at[16][256];  // a wave's keys of a digit; then where they go
-  __shared__ uint32_t tot[256];
-  __shared__ uint32_t keys[1024 * R];
-  __shared__ uint16_t moved[1024 * R];
+struct SortLds {
+  uint32_t at[16][256];  // a wave's keys of a digit; then where they go
+  uint32_t tot[256];
+  uint32_t key[1024 * R];
+  uint16_t pos[1024 * R];
+};
+
+template <int R>
+__device__ __forceinline__ void sort_lds(const SortParams& p, SortLds<R>& sm) {
   const int digits = 1 << p.bits;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int n = (int)p.n, rounds = (n + 1023) / 1024;
@@ -130,9 +134,17 @@ __global__ __launch_bounds__(1024) void sort_small_kernel(SortParams p) {
   }
   for (int pass = 0; pass < p.passes; ++pass) {
     const int shift = pass * p.bits;
-    for (int i = tid; i < 16 * 256; i += 1024) (&at[0][0])[i] = 0;
+    for (int i = tid; i < 16 * 256; i += 1024) (&sm.at[0][0])[i] = 0;
     __syncthreads();
-    rank_keys<R>(at[wave], key, shift, (uint32_t)digits - 1, base, n, rounds, rank);
+    if (pass > 0) {
+#pragma unroll
+      for (int r = 0; r < R; ++r)
+        if (r < rounds && base + r * 64 < n) {
+          pos[r] = sm.pos[base + r * 64];
+          key[r] = sm.key[base + r * 64];
+        }
+    }
+    rank_keys<R>(sm.at[wave], key, shift, (uint32_t)digits - 1, base, n, rounds, rank);
     __syncthreads();
     uint32_t c[16];
     if (tid < digits) {
@@ -140,40 +152,41 @@ __global__ __launch_bounds__(1024) void sort_small_kernel(SortParams p) {
 #pragma unroll
       for (int w = 0; w < 16; ++w) {
         c[w] = all;
-        all += at[w][tid];
+        all += sm.at[w][tid];
       }
-      tot[tid] = all;
+      sm.tot[tid] = all;
     }
     __syncthreads();
-    if (wave == 0) scan_digits(tot, digits, lane);
+    if (wave == 0) scan_digits(sm.tot, digits, lane);
     __syncthreads();
     if (tid < digits) {
-      const uint32_t a = tot[tid];
+      const uint32_t a = sm.tot[tid];
 #pragma unroll
-      for (int w = 0; w < 16; ++w) at[w][tid] = a + c[w];
+      for (int w = 0; w < 16; ++w) sm.at[w][tid] = a + c[w];
     }
     __syncthreads();
 #pragma unroll
     for (int r = 0; r < R; ++r) {
       if (r >= rounds || base + r * 64 >= n) continue;
-      const uint32_t dst = at[wave][(key[r] >> shift) & (digits - 1)] + rank[r];
-      keys[dst] = key[r];
-      moved[dst] = (uint16_t)pos[r];
+      const uint32_t dst = sm.at[wave][(key[r] >> shift) & (digits - 1)] + rank[r];
+      sm.key[dst] = key[r];
+      sm.pos[dst] = (uint16_t)pos[r];
     }
     __syncthreads();
-#pragma unroll
-    for (int r = 0; r < R; ++r)
-      if (r < rounds && base + r * 64 < n) {
-        pos[r] = moved[base + r * 64];
-        key[r] = keys[base + r * 64];
-      }
   }
-#pragma unroll
-  for (int r = 0; r < R; ++r)
-    if (r < rounds && base + r * 64 < n) {
-      p.key_out[base + r * 64] = key[r];
-      p.pos_out[base + r * 64] = pos[r];
-    }
+}
+
+// The sort in a launch of its own.  The lists leave in order: stores by rank would cost a line each (4096: 24 -> 22 us
+// per call).  The other workgroups fill.
+template <int R>
+__global__ __launch_bounds__(1024) void sort_small_kernel(SortParams p) {
+  if (blockIdx.x > 0) return fill_piece(p, blockIdx.x - 1, 1024);
+  __shared__ SortLds<R> sm;
+  sort_lds<R>(p, sm);
+  for (int i = threadIdx.x; i < (int)p.n; i += 1024) {
+    p.key_out[i] = sm.key[i];
+    p.pos_out[i] = sm.pos[i];
+  }
 }
 
 template <int NW, int R>
@@ -273,24 +286,19 @@ __device__ __forceinline__ OT* row_at(const SumParams& p, uint32_t k, int64_t co
   return static_cast<OT*>(p.dweight) + (int64_t)k * p.E + col;
 }
 
+// The sums of rows i0 .. i1 - 1 of the sorted list; prev and next: the keys beside them (V: none).  Sums of tokens
+// within go to dweight, others to partial(0, ..) where the token's rows began before i0, partial(1, ..) where they
+// go on at i1.
 // With ADD the rows of dweight that a group of 8 will add to are loaded with the group, not one by one as the
 // tokens change: one wait for memory per group and not per token (509 tokens of width 768 into a table of 50000
-// rows: this kernel 18 -> 7 us, with chunks of 8 rows and not 32).
+// rows: 18 -> 7 us, with chunks of 8 rows and not 32).
 // NT: dout is too large to be found in the Infinity Cache (256 MB), where a backward pass has just left it, and
 // is read as not needed again (16384 x 768: 53 -> 49 us per call without; 262144 x 1024: 165 -> 153 us with).
-template <typename IO, typename OT, int VC, bool ADD, bool NT>
-__global__ __launch_bounds__(256) void embed_sum_kernel(SumParams p) {
-  const int lane = threadIdx.x & 63;
-  const int64_t unit = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-  const int64_t chunk = unit / p.col_tiles, ct = unit - chunk * p.col_tiles;
-  if (chunk >= p.chunks) return;
-  const int64_t i0 = chunk * p.run, i1 = i0 + p.run < p.n ? i0 + p.run : p.n;
-  const int64_t col = (ct * 64 + lane) * VC;
-  const int nc = p.E - col >= VC ? VC : p.E - col > 0 ? (int)(p.E - col) : 0;
+template <typename IO, typename OT, int VC, bool ADD, bool NT, typename Key, typename Pos, typename Partial>
+__device__ __forceinline__ void sum_rows(const SumParams& p, int64_t i0, int64_t i1, uint32_t prev, uint32_t next,
+                                         int64_t col, int nc, int lane, Key key, Pos pos, Partial partial) {
   const IO* rows = static_cast<const IO*>(p.dout) + col;
   const uint32_t V = (uint32_t)p.V;
-  const uint32_t prev = i0 > 0 ? p.key[i0 - 1] : V, next = i1 < p.n ? p.key[i1] : V;
-
   float acc[VC];
 #pragma unroll
   for (int e = 0; e < VC; ++e) acc[e] = 0.0f;
@@ -300,10 +308,10 @@ __global__ __launch_bounds__(256) void embed_sum_kernel(SumParams p) {
     const int m = i1 - s < 64 ? (int)(i1 - s) : 64;
     uint32_t kv = V, pv = 0;
     if (lane < m) {
-      kv = p.key[s + lane];
-      pv = p.pos[s + lane];
+      kv = key(s + lane);
+      pv = pos(s + lane);
     }
-    const uint32_t after = s + 64 < i1 ? p.key[s + 64] : next;  // the key behind these
+    const uint32_t after = s + 64 < i1 ? key(s + 64) : next;  // the key behind these
     for (int r = 0; r < m; r += 8) {
       Raw<IO, VC, NT> x[8];
       Raw<OT, VC> old[ADD ? 8 : 1];
@@ -336,9 +344,9 @@ __global__ __launch_bounds__(256) void embed_sum_kernel(SumParams p) {
         const bool end = s + r + q + 1 == i1;
         if (!end && k[q] == k[q + 1]) continue;
         if (head && prev == cur) {
-          store_n<float, VC>(p.part + (chunk * 2) * p.E + col, nc, acc);
+          partial(0, acc);
         } else if (end && next == cur) {
-          store_n<float, VC>(p.part + (chunk * 2 + 1) * p.E + col, nc, acc);
+          partial(1, acc);
         } else {
           float y[VC];
 #pragma unroll
@@ -347,6 +355,96 @@ __global__ __launch_bounds__(256) void embed_sum_kernel(SumParams p) {
         }
       }
     }
+  }
+}
+
+template <typename IO, typename OT, int VC, bool ADD, bool NT>
+__global__ __launch_bounds__(256) void embed_sum_kernel(SumParams p) {
+  const int lane = threadIdx.x & 63;
+  const int64_t unit = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+  const int64_t chunk = unit / p.col_tiles, ct = unit - chunk * p.col_tiles;
+  if (chunk >= p.chunks) return;
+  const int64_t i0 = chunk * p.run, i1 = i0 + p.run < p.n ? i0 + p.run : p.n;
+  const int64_t col = (ct * 64 + lane) * VC;
+  const int nc = p.E - col >= VC ? VC : p.E - col > 0 ? (int)(p.E - col) : 0;
+  const uint32_t prev = i0 > 0 ? p.key[i0 - 1] : (uint32_t)p.V, next = i1 < p.n ? p.key[i1] : (uint32_t)p.V;
+  sum_rows<IO, OT, VC, ADD, NT>(
+      p, i0, i1, prev, next, col, nc, lane, [&](int64_t i) { return p.key[i]; }, [&](int64_t i) { return p.pos[i]; },
+      [&](int which, const float(&acc)[VC]) { store_n<float, VC>(p.part + (chunk * 2 + which) * p.E + col, nc, acc); });
+}
+
+// All steps in one launch, for up to 1024 positions (with 4096, 4096 x 768 took 19 us for 22, but 4096 x 2560 45 for
+// 36, and 4096 positions on one token 101 for 34): every workgroup sorts all of them for itself, which takes as
+// long as for one of them alone, takes the tokens whose first row lies in its `run` rows of the sorted list, and
+// a tile of 64 * VC columns; its 16 waves share the rows, and sums that reach over a wave's end meet in LDS.
+// Without ADD each also clears its share of the rows that no token names.
+template <typename IO, typename OT, int VC, bool ADD>
+__global__ __launch_bounds__(1024) void embed_once_kernel(SortParams sp, SumParams p) {
+  __shared__ SortLds<1> sm;
+  __shared__ float part[16][2][VC][64];
+  const int64_t group = blockIdx.x / p.col_tiles, ct = blockIdx.x - group * p.col_tiles;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int64_t col = (ct * 64 + lane) * VC;
+  const int nc = p.E - col >= VC ? VC : p.E - col > 0 ? (int)(p.E - col) : 0;
+  const int n = (int)p.n;
+  const uint32_t V = (uint32_t)p.V;
+  sort_lds<1>(sp, sm);
+
+  // the first row of the list whose key is not less (not more, with `over`) than k
+  auto bound = [&](uint32_t k, bool over) {
+    int lo = 0, hi = n;
+    while (lo < hi) {
+      const int mid = (lo + hi) / 2;
+      const uint32_t x = sm.key[mid];
+      if (x < k || (over && x == k)) lo = mid + 1;
+      else hi = mid;
+    }
+    return __builtin_amdgcn_readfirstlane(lo);
+  };
+  const int named = bound(V, false);  // rows of tokens of the table
+  const int c0 = (int)(group * p.run), c1 = c0 + (int)p.run;
+  const int a = c0 >= named ? named : c0 > 0 ? bound(sm.key[c0 - 1], true) : 0;
+  const int z = c1 >= named ? named : bound(sm.key[c1 - 1], true);
+  const int per = (z - a + 15) / 16;
+  const int i0 = a + wave * per < z ? a + wave * per : z, i1 = i0 + per < z ? i0 + per : z;
+  const uint32_t prev = i0 > a ? sm.key[i0 - 1] : V, next = i1 < z ? sm.key[i1] : V;
+  sum_rows<IO, OT, VC, ADD, false>(
+      p, i0, i1, prev, next, col, nc, lane, [&](int64_t i) { return sm.key[i]; },
+      [&](int64_t i) { return (uint32_t)sm.pos[i]; },
+      [&](int which, const float(&acc)[VC]) {
+#pragma unroll
+        for (int e = 0; e < VC; ++e) part[wave][which][e][lane] = acc[e];
+      });
+  __syncthreads();
+  if (i0 < i1) {
+    const uint32_t k = sm.key[i1 - 1];
+    if (next == k && !(sm.key[i0] == k && prev == k)) {  // begins here and goes on
+      float acc[VC], old[VC];
+#pragma unroll
+      for (int e = 0; e < VC; ++e) acc[e] = part[wave][1][e][lane];
+      if (ADD) load_n<OT, VC>(row_at<OT, VC>(p, k, col), nc, old);
+      for (int w = wave + 1, j = i1; j < z && sm.key[j] == k; ++w, j += per)
+#pragma unroll
+        for (int e = 0; e < VC; ++e) acc[e] += part[w][0][e][lane];
+#pragma unroll
+      for (int e = 0; e < VC; ++e) acc[e] = ADD ? old[e] + acc[e] * p.scale : acc[e] * p.scale;
+      store_n<OT, VC>(row_at<OT, VC>(p, k, col), nc, acc);
+    }
+  }
+  if (ADD) return;
+  const int64_t share = (p.V + p.chunks * 16 - 1) / (p.chunks * 16);
+  const int64_t r0 = (group * 16 + wave) * share, r1 = r0 + share < p.V ? r0 + share : p.V;
+  if (r0 >= r1) return;
+  int i = bound((uint32_t)r0, false);
+  float zero[VC];
+#pragma unroll
+  for (int e = 0; e < VC; ++e) zero[e] = 0.0f;
+  for (int64_t r = r0; r < r1;) {
+    const int64_t stop = i < named && sm.key[i] < r1 ? sm.key[i] : r1;  // the next row that a token names
+    for (; r < stop; ++r) store_n<OT, VC>(row_at<OT, VC>(p, (uint32_t)r, col), nc, zero);
+    if (r == r1) break;
+    r += 1;
+    if (r < r1) i = bound((uint32_t)r, false);
   }
 }
 
@@ -477,7 +575,17 @@ hipError_t launch_sums(SumParams p, hipStream_t s) {
 }
 
 template <typename IO, typename OT>
-hipError_t launch_io(const EmbedParams& e, const EmbedBwdPlan& pl, SumParams p, char* ws, hipStream_t s) {
+hipError_t launch_once(const SortParams& sp, SumParams p, hipStream_t s) {
+  p.col_tiles = (p.E + 255) / 256;
+  const dim3 grid((unsigned)(p.chunks * p.col_tiles)), block(1024);
+  auto go = [&](auto fn) { hipLaunchKernelGGL(fn, grid, block, 0, s, sp, p); };
+  p.add ? go(embed_once_kernel<IO, OT, 4, true>) : go(embed_once_kernel<IO, OT, 4, false>);
+  return hipGetLastError();
+}
+
+template <typename IO, typename OT>
+hipError_t launch_io(const EmbedParams& e, const EmbedBwdPlan& pl, const SortParams& sp, SumParams p, char* ws,
+                     hipStream_t s) {
   if (pl.transpose) {
     const int64_t blocks = e.Bsz * ((e.L + 127) / 128) * ((e.E + 63) / 64);
     IO* rows = reinterpret_cast<IO*>(ws + pl.rows);
@@ -485,6 +593,7 @@ hipError_t launch_io(const EmbedParams& e, const EmbedBwdPlan& pl, SumParams p, 
                        static_cast<const IO*>(e.dout), rows, e.E, e.L);
     p.dout = rows;
   }
+  if (pl.once) return launch_once<IO, OT>(sp, p, s);
   if constexpr (sizeof(IO) == 2)
     if (columns(e.E, true) == 8) return launch_sums<IO, OT, 8>(p, s);
   return launch_sums<IO, OT, 4>(p, s);
@@ -518,13 +627,35 @@ size_t round256(size_t x) { return (x + 255) & ~size_t(255); }
 
 }  // namespace
 
-void plan_embed_bwd(int64_t Bsz, int64_t L, int64_t V, int64_t E, bool io_bf16, bool cf, EmbedBwdPlan* pl) {
+void plan_embed_bwd(int64_t Bsz, int64_t L, int64_t V, int64_t E, int64_t table_size, bool io_bf16, bool cf, bool add,
+                    EmbedBwdPlan* pl) {
   if (cf && embed_few_rows(V, io_bf16)) return plan_embed_few(Bsz, L, V, E, pl);
   const int64_t n = Bsz * L;
   pl->bits = 1;
   while ((V >> pl->bits) != 0) ++pl->bits;  // keys 0 .. V
   pl->passes = (pl->bits + 7) / 8;
   pl->digit_bits = (pl->bits + pl->passes - 1) / pl->passes;
+  pl->transpose = cf;
+  size_t off = 0;
+  auto take = [&](size_t bytes) { const size_t o = off; off += round256(bytes); return o; };
+  if (pl->transpose) pl->rows = take((size_t)n * E * (io_bf16 ? 2 : 4));
+  // All in one launch: up to 1024 positions, as one workgroup per CU (a row per wave, at most 4) and with little or
+  // nothing to clear.  Calls of 509 x 768, added: 10.1 us, 13.8 with three launches; 1024 x 2560: 14.0 and 15.0,
+  // 1024 x 8192 (512 workgroups): 31 and 24; all positions on one token, 1024 x 768: 31 and 18.  Not added, 509 x 768
+  // into 300 / 2500 / 5000 / 10000 rows: 11.0 / 13.7 / 15.1 / 17.7 and 14.0 / 14.2 / 15.1 / 15.2, 1024 x 4 into 8192:
+  // 15.3 and 14.9.
+  const int64_t tiles = (E + 255) / 256;
+  int64_t run = 16;
+  while (run < 64 && (n + run - 1) / run * tiles > 256) run *= 2;
+  const int64_t chunks = (n + run - 1) / run;
+  pl->once = n <= 1024 && chunks * tiles <= 256 && (add || (V <= 4096 && V * E * table_size <= (int64_t(8) << 20)));
+  if (pl->once) {
+    pl->run = run;
+    pl->chunks = chunks;
+    if (!pl->transpose) take(1);  // (no size of 0 for a call that can be made)
+    pl->total = off;
+    return;
+  }
   // Small tiles spread a short list over the chip; but each adds up the counts of all tiles, so long lists take
   // larger ones.  Whole calls of width 4 with tiles of 512 / 4096 / 8192: 29 / 38 / 46 us for 16384 positions,
   // 52 / 56 / 68 for 65536, 76 / 71 / 78 for 131072, 603 / 322 / 320 for 2^20, 6.0 / 0.96 / 0.90 ms for 2^22.
@@ -537,10 +668,6 @@ void plan_embed_bwd(int64_t Bsz, int64_t L, int64_t V, int64_t E, bool io_bf16, 
   pl->run = 8;
   while (pl->run < 256 && n * tiles_e > pl->run * 4096) pl->run *= 2;
   pl->chunks = (n + pl->run - 1) / pl->run;
-  pl->transpose = cf;
-  size_t off = 0;
-  auto take = [&](size_t bytes) { const size_t o = off; off += round256(bytes); return o; };
-  if (pl->transpose) pl->rows = take((size_t)n * E * (io_bf16 ? 2 : 4));
   for (int i = 0; i < (pl->tiles > 1 ? 2 : 1); ++i) {
     pl->key[i] = take((size_t)n * 4);
     pl->pos[i] = take((size_t)n * 4);
@@ -561,7 +688,7 @@ hipError_t launch_embed_bwd(const EmbedParams& e, const EmbedBwdPlan& pl, bool t
   sp.fill = static_cast<char*>(e.out);
   int64_t left = e.add ? 0 : e.V * e.E * (table_bf16 ? 2 : 4);
   hipError_t rc = hipSuccess;
-  if (pl.tiles == 1) {
+  if (pl.tiles == 1 && !pl.once) {
     sp.key_out = reinterpret_cast<uint32_t*>(w + pl.key[0]);
     sp.pos_out = reinterpret_cast<uint32_t*>(w + pl.pos[0]);
     rc = with_fill(sp, &left, 1.0, [&](unsigned more) {
@@ -589,8 +716,8 @@ hipError_t launch_embed_bwd(const EmbedParams& e, const EmbedBwdPlan& pl, bool t
   p.n = e.T; p.V = e.V; p.E = e.E; p.run = pl.run; p.chunks = pl.chunks;
   p.scale = e.scale; p.add = e.add;
   if (io_bf16)
-    return table_bf16 ? launch_io<bf16_t, bf16_t>(e, pl, p, w, s) : launch_io<bf16_t, float>(e, pl, p, w, s);
-  return table_bf16 ? launch_io<float, bf16_t>(e, pl, p, w, s) : launch_io<float, float>(e, pl, p, w, s);
+    return table_bf16 ? launch_io<bf16_t, bf16_t>(e, pl, sp, p, w, s) : launch_io<bf16_t, float>(e, pl, sp, p, w, s);
+  return table_bf16 ? launch_io<float, bf16_t>(e, pl, sp, p, w, s) : launch_io<float, float>(e, pl, sp, p, w, s);
 }
 
 }  // namespace ssm

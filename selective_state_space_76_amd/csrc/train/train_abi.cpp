@@ -160,7 +160,8 @@ size_t ssm_embedding_bwd_workspace_size(const ssm_embed_shape* shape) {
   ssm::EmbedParams p;
   if (embed_check(shape, SSM_FLAG_CHANNELS_FIRST | SSM_FLAG_ACCUMULATE, &p) != SSM_OK) return 0;
   ssm::EmbedBwdPlan pl;
-  ssm::plan_embed_bwd(p.Bsz, p.L, p.V, p.E, shape->io_dtype == SSM_BF16, p.cf, &pl);
+  ssm::plan_embed_bwd(p.Bsz, p.L, p.V, p.E, dtype_size(shape->table_dtype), shape->io_dtype == SSM_BF16, p.cf, p.add,
+                      &pl);
   return pl.total;
 }
 
@@ -173,7 +174,8 @@ ssm_status ssm_embedding_bwd(const ssm_embed_shape* shape, const void* tokens, c
   if (!isfinite(scale)) return SSM_ERR_UNSUPPORTED;
   if (misaligned(tokens) || misaligned(dout) || misaligned(dweight) || misaligned(workspace)) return SSM_ERR_ALIGN;
   ssm::EmbedBwdPlan pl;
-  ssm::plan_embed_bwd(p.Bsz, p.L, p.V, p.E, shape->io_dtype == SSM_BF16, p.cf, &pl);
+  ssm::plan_embed_bwd(p.Bsz, p.L, p.V, p.E, dtype_size(shape->table_dtype), shape->io_dtype == SSM_BF16, p.cf, p.add,
+                      &pl);
   if (workspace_bytes < pl.total) return SSM_ERR_WORKSPACE;
   const Range ins[] = {span(tokens, p.T * (p.i64 ? 8 : 4)), span(dout, p.T * p.E * dtype_size(shape->io_dtype))};
   const Range outs[] = {span(dweight, p.V * p.E * dtype_size(shape->table_dtype)),

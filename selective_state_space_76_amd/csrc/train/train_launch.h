@@ -100,12 +100,14 @@ hipError_t launch_embed_fwd(const EmbedParams& p, bool table_bf16, bool io_bf16,
 struct EmbedBwdPlan {
   bool few = false;               // [B,E,L] and few rows: products (embed_bwd_few.hip); run: positions per segment
   bool transpose = false;         // [B,E,L]: dout is brought to [B,L,E] first
+  bool once = false;              // short lists: all steps in one launch, no workspace but the turned dout
   int bits = 0, passes = 0, digit_bits = 0;
   int64_t tile = 0, tiles = 0;    // of the sort; one tile: one launch
   int64_t run = 0, chunks = 0;    // sorted rows per chunk of the sums
   size_t rows = 0, key[2] = {0, 0}, pos[2] = {0, 0}, hist = 0, part = 0, total = 0;  // offsets, bytes
 };
-void plan_embed_bwd(int64_t Bsz, int64_t L, int64_t V, int64_t E, bool io_bf16, bool cf, EmbedBwdPlan* pl);
+void plan_embed_bwd(int64_t Bsz, int64_t L, int64_t V, int64_t E, int64_t table_size, bool io_bf16, bool cf, bool add,
+                    EmbedBwdPlan* pl);
 hipError_t launch_embed_bwd(const EmbedParams& p, const EmbedBwdPlan& pl, bool table_bf16, bool io_bf16, void* ws,
                             hipStream_t s);
 bool embed_few_rows(int64_t V, bool io_bf16);

@@ -141,6 +141,19 @@ def test_backward_sort_sizes(n, V, E, kind):
     bwd_check(tokens_of(1, n, V, n, kind), V, E, F32, F32, False, 1.0, seed=n)
 
 
+# short lists: one launch or several by what is to be cleared, how wide the rows are and where 1024 and 4096 end
+@pytest.mark.parametrize("n,V,E", [(17, 50000, 20), (1000, 4096, 260), (1023, 4097, 260), (1024, 1 << 20, 4),
+                                   (1025, 700, 24), (2500, 50000, 24), (4096, 300, 24), (1024, 40, 4096),
+                                   (1024, 40, 4100), (700, 9, 2600)])
+@pytest.mark.parametrize("add", [False, True], ids=["new", "added"])
+def test_backward_short_lists(n, V, E, add):
+    for kind in ("mixed", "same", "even", "none"):
+        print("case: embed grad of", n, V, E, add, kind, flush=True)
+        dw = bwd_check(tokens_of(1, n, V, n + E, kind), V, E, BF16 if E > 24 else F32, F32, False, 1.5, seed=n, add=add)
+        if kind == "none" and not add:
+            assert not dw.any()
+
+
 def test_backward_is_the_transpose():
     """<dout, embed(W + D) - embed(W)> = <gradient, D>: the map is linear, so differences are exact but for rounding."""
     V, E = 90, 50
