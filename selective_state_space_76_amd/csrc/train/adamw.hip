@@ -10,7 +10,7 @@
 // With fp32 states the step is bound by HBM: every byte is touched once, at 5.8 TB/s (a copy reaches 5.2, a plain
 // sum 6.0): 127 M bf16 weights with masters 0.66 ms.  With 8-bit states the instructions (about 70 an
 // element, three of them 32-bit integer products for the random numbers) take nearly as long as the 10 bytes:
-// 305 M bf16 weights 0.62 ms, 4.9 TB/s (0.79 ms with 87 instructions).  Loading the next piece before
+// 311 M bf16 weights 0.59 ms, 5.3 TB/s (0.79 ms with 87 instructions).  Loading the next piece before
 // the present one is worked on gained nothing with either.
 // The gradients' norm comes first and reads them once more: 127 M in bf16 44 us, 5.8 TB/s.
 //
