@@ -13,7 +13,7 @@
 //      keeps 8 rows in flight and adds them to the running token's sum.  Sums of tokens that lie within
 //      the chunk go to dweight; one that reaches over an end goes to memory as a partial sum.
 //   3. Join: where a token's rows begin in a chunk and go on in the next, its partial sums are added, in order.
-// Up to 1024 positions take all three in one launch where there is little to clear (embed_once_kernel).
+// Up to 2048 positions take all three in one launch where there is little to clear (embed_once_kernel).
 // dout in [B,E,L] is first brought to [B,L,E], unless the table has few rows (embed_bwd_few.hip).
 // Tokens outside the table sort as V, behind all others, and are left out.
 //
@@ -111,7 +111,8 @@ __device__ __forceinline__ void rank_keys(uint32_t* count, const uint32_t (&key)
   for (int r = 0; r < R; ++r) rank[r] += below[r];
 }
 
-// Up to 1024 R keys sorted by one workgroup of 1024, all digits.  Keys and positions move through LDS and stay there.
+// Up to 1024 R keys sorted by one workgroup of 1024, all digits: the tokens, or (LISTED) what is in sm.key and sm.pos.
+// Keys and positions move through LDS and stay there.
 template <int R>
 struct SortLds {
   uint32_t at[16][256];  // a wave's keys of a digit; then where they go
@@ -120,23 +121,23 @@ struct SortLds {
   uint16_t pos[1024 * R];
 };
 
-template <int R>
-__device__ __forceinline__ void sort_lds(const SortParams& p, SortLds<R>& sm) {
+template <int R, bool LISTED>
+__device__ __forceinline__ void sort_lds(const SortParams& p, int n, SortLds<R>& sm) {
   const int digits = 1 << p.bits;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int n = (int)p.n, rounds = (n + 1023) / 1024;
+  const int rounds = (n + 1023) / 1024;
   const int base = wave * (64 * rounds) + lane;
   uint32_t key[R], pos[R], rank[R];
 #pragma unroll
   for (int r = 0; r < R; ++r) {
     pos[r] = base + r * 64;
-    key[r] = r < rounds && (int)pos[r] < n ? key_at(p, pos[r]) : 0u;
+    key[r] = !LISTED && r < rounds && (int)pos[r] < n ? key_at(p, pos[r]) : 0u;
   }
   for (int pass = 0; pass < p.passes; ++pass) {
     const int shift = pass * p.bits;
     for (int i = tid; i < 16 * 256; i += 1024) (&sm.at[0][0])[i] = 0;
     __syncthreads();
-    if (pass > 0) {
+    if (LISTED || pass > 0) {
 #pragma unroll
       for (int r = 0; r < R; ++r)
         if (r < rounds && base + r * 64 < n) {
@@ -182,7 +183,7 @@ template <int R>
 __global__ __launch_bounds__(1024) void sort_small_kernel(SortParams p) {
   if (blockIdx.x > 0) return fill_piece(p, blockIdx.x - 1, 1024);
   __shared__ SortLds<R> sm;
-  sort_lds<R>(p, sm);
+  sort_lds<R, false>(p, (int)p.n, sm);
   for (int i = threadIdx.x; i < (int)p.n; i += 1024) {
     p.key_out[i] = sm.key[i];
     p.pos_out[i] = sm.pos[i];
@@ -373,41 +374,79 @@ __global__ __launch_bounds__(256) void embed_sum_kernel(SumParams p) {
       [&](int which, const float(&acc)[VC]) { store_n<float, VC>(p.part + (chunk * 2 + which) * p.E + col, nc, acc); });
 }
 
-// All steps in one launch, for up to 1024 positions (with 4096, 4096 x 768 took 19 us for 22, but 4096 x 2560 45 for
-// 36, and 4096 positions on one token 101 for 34): every workgroup sorts all of them for itself, which takes as
-// long as for one of them alone, takes the tokens whose first row lies in its `run` rows of the sorted list, and
-// a tile of 64 * VC columns; its 16 waves share the rows, and sums that reach over a wave's end meet in LDS.
-// Without ADD each also clears its share of the rows that no token names.
-template <typename IO, typename OT, int VC, bool ADD>
+// All steps in one launch, for up to 1024 R positions: a workgroup takes the tokens v with v % groups == its own number
+// and a tile of 64 * VC columns.  It lists their positions in order, sorts the list, short as a rule, by
+// counting for each entry those that come before it, and by radix where it is long.  Its 16 waves share the list's
+// rows, and sums that reach over a wave's end meet in LDS.  Without ADD it also clears its rows that no token names.
+// (509 x 768, added: 8.9 us per call; 10.7 where every workgroup sorted all positions for itself, 13.8 with a launch
+// for each step.)
+constexpr int kPairs = 128;  // longest list sorted by counting
+
+template <typename IO, typename OT, int VC, int R, bool ADD>
 __global__ __launch_bounds__(1024) void embed_once_kernel(SortParams sp, SumParams p) {
-  __shared__ SortLds<1> sm;
+  __shared__ SortLds<R> sm;
   __shared__ float part[16][2][VC][64];
-  const int64_t group = blockIdx.x / p.col_tiles, ct = blockIdx.x - group * p.col_tiles;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  __shared__ uint32_t listed[16];
+  const uint32_t groups = (uint32_t)p.chunks, group = blockIdx.x / (uint32_t)p.col_tiles;
+  const int64_t ct = blockIdx.x - group * (uint32_t)p.col_tiles;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int64_t col = (ct * 64 + lane) * VC;
   const int nc = p.E - col >= VC ? VC : p.E - col > 0 ? (int)(p.E - col) : 0;
-  const int n = (int)p.n;
   const uint32_t V = (uint32_t)p.V;
-  sort_lds<1>(sp, sm);
-
-  // the first row of the list whose key is not less (not more, with `over`) than k
-  auto bound = [&](uint32_t k, bool over) {
-    int lo = 0, hi = n;
-    while (lo < hi) {
-      const int mid = (lo + hi) / 2;
-      const uint32_t x = sm.key[mid];
-      if (x < k || (over && x == k)) lo = mid + 1;
-      else hi = mid;
+  const int base = wave * (64 * R) + lane;
+  uint32_t mine[R];
+  uint64_t ins[R];
+  uint32_t count = 0;
+#pragma unroll
+  for (int r = 0; r < R; ++r) mine[r] = base + r * 64 < (int)p.n ? key_at(sp, base + r * 64) : V;
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    ins[r] = __ballot(mine[r] != V && mine[r] % groups == group);
+    count += (uint32_t)__popcll(ins[r]);
+  }
+  if (lane == 0) listed[wave] = count;
+  __syncthreads();
+  int z = 0, at = 0;  // entries of the list, and of the waves before this one
+#pragma unroll
+  for (int w = 0; w < 16; ++w) {
+    if (w == wave) at = z;
+    z += (int)listed[w];
+  }
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    const int to = at + (int)__builtin_amdgcn_mbcnt_hi((uint32_t)(ins[r] >> 32),
+                                                       __builtin_amdgcn_mbcnt_lo((uint32_t)ins[r], 0u));
+    if (ins[r] >> lane & 1) {
+      sm.key[to] = mine[r];
+      sm.pos[to] = (uint16_t)(base + r * 64);
     }
-    return __builtin_amdgcn_readfirstlane(lo);
-  };
-  const int named = bound(V, false);  // rows of tokens of the table
-  const int c0 = (int)(group * p.run), c1 = c0 + (int)p.run;
-  const int a = c0 >= named ? named : c0 > 0 ? bound(sm.key[c0 - 1], true) : 0;
-  const int z = c1 >= named ? named : bound(sm.key[c1 - 1], true);
-  const int per = (z - a + 15) / 16;
-  const int i0 = a + wave * per < z ? a + wave * per : z, i1 = i0 + per < z ? i0 + per : z;
-  const uint32_t prev = i0 > a ? sm.key[i0 - 1] : V, next = i1 < z ? sm.key[i1] : V;
+    at += (int)__popcll(ins[r]);
+  }
+  __syncthreads();
+  if (z <= kPairs) {
+    uint32_t key = 0, pos = 0;
+    int rank = 0;
+    if (tid < z) {
+      key = sm.key[tid];
+      pos = sm.pos[tid];
+#pragma unroll 8
+      for (int j = 0; j < z; ++j) {
+        const uint32_t other = sm.key[j];
+        rank += other < key || (other == key && j < tid);
+      }
+    }
+    __syncthreads();
+    if (tid < z) {
+      sm.key[rank] = key;
+      sm.pos[rank] = (uint16_t)pos;
+    }
+    __syncthreads();
+  } else {
+    sort_lds<R, true>(sp, z, sm);
+  }
+  const int per = (z + 15) / 16;
+  const int i0 = wave * per < z ? wave * per : z, i1 = i0 + per < z ? i0 + per : z;
+  const uint32_t prev = i0 > 0 ? sm.key[i0 - 1] : V, next = i1 < z ? sm.key[i1] : V;
   sum_rows<IO, OT, VC, ADD, false>(
       p, i0, i1, prev, next, col, nc, lane, [&](int64_t i) { return sm.key[i]; },
       [&](int64_t i) { return (uint32_t)sm.pos[i]; },
@@ -432,19 +471,26 @@ __global__ __launch_bounds__(1024) void embed_once_kernel(SortParams sp, SumPara
     }
   }
   if (ADD) return;
-  const int64_t share = (p.V + p.chunks * 16 - 1) / (p.chunks * 16);
-  const int64_t r0 = (group * 16 + wave) * share, r1 = r0 + share < p.V ? r0 + share : p.V;
-  if (r0 >= r1) return;
-  int i = bound((uint32_t)r0, false);
+  // the group's rows are v = group + groups * r; a wave clears those of r0 <= r < r1
+  const int64_t rows = group < V ? (p.V - group + groups - 1) / groups : 0, share = (rows + 15) / 16;
+  const int64_t r0 = wave * share, r1 = r0 + share < rows ? r0 + share : rows;
   float zero[VC];
 #pragma unroll
   for (int e = 0; e < VC; ++e) zero[e] = 0.0f;
-  for (int64_t r = r0; r < r1;) {
-    const int64_t stop = i < named && sm.key[i] < r1 ? sm.key[i] : r1;  // the next row that a token names
-    for (; r < stop; ++r) store_n<OT, VC>(row_at<OT, VC>(p, (uint32_t)r, col), nc, zero);
-    if (r == r1) break;
-    r += 1;
-    if (r < r1) i = bound((uint32_t)r, false);
+  auto first_from = [&](uint32_t v) {  // the list's first entry that is not before row v
+    int lo = 0, hi = z;
+    while (lo < hi) {
+      const int mid = (lo + hi) / 2;
+      if (sm.key[mid] < v) lo = mid + 1;
+      else hi = mid;
+    }
+    return lo;
+  };
+  int i = r0 < r1 ? first_from(group + groups * (uint32_t)r0) : z;
+  for (int64_t r = r0; r < r1; ++r) {
+    const uint32_t v = group + groups * (uint32_t)r;
+    if (i < z && sm.key[i] == v) i = first_from(v + 1);
+    else store_n<OT, VC>(row_at<OT, VC>(p, v, col), nc, zero);
   }
 }
 
@@ -579,7 +625,8 @@ hipError_t launch_once(const SortParams& sp, SumParams p, hipStream_t s) {
   p.col_tiles = (p.E + 255) / 256;
   const dim3 grid((unsigned)(p.chunks * p.col_tiles)), block(1024);
   auto go = [&](auto fn) { hipLaunchKernelGGL(fn, grid, block, 0, s, sp, p); };
-  p.add ? go(embed_once_kernel<IO, OT, 4, true>) : go(embed_once_kernel<IO, OT, 4, false>);
+  if (p.n <= 1024) p.add ? go(embed_once_kernel<IO, OT, 4, 1, true>) : go(embed_once_kernel<IO, OT, 4, 1, false>);
+  else p.add ? go(embed_once_kernel<IO, OT, 4, 2, true>) : go(embed_once_kernel<IO, OT, 4, 2, false>);
   return hipGetLastError();
 }
 
@@ -639,16 +686,17 @@ void plan_embed_bwd(int64_t Bsz, int64_t L, int64_t V, int64_t E, int64_t table_
   size_t off = 0;
   auto take = [&](size_t bytes) { const size_t o = off; off += round256(bytes); return o; };
   if (pl->transpose) pl->rows = take((size_t)n * E * (io_bf16 ? 2 : 4));
-  // All in one launch: up to 1024 positions, as one workgroup per CU (a row per wave, at most 4) and with little or
-  // nothing to clear.  Calls of 509 x 768, added: 10.1 us, 13.8 with three launches; 1024 x 2560: 14.0 and 15.0,
-  // 1024 x 8192 (512 workgroups): 31 and 24; all positions on one token, 1024 x 768: 31 and 18.  Not added, 509 x 768
-  // into 300 / 2500 / 5000 / 10000 rows: 11.0 / 13.7 / 15.1 / 17.7 and 14.0 / 14.2 / 15.1 / 15.2, 1024 x 4 into 8192:
-  // 15.3 and 14.9.
+  // All in one launch: up to 2048 positions, at most a workgroup per CU (a row per wave, or up to 4) and with little or
+  // nothing to clear.  Calls of 509 x 768, added: 8.9 us, 13.8 with three launches; 2048 x 768: 8.7 and 17.4; 1024 x
+  // 8192 (512 workgroups): 27 and 24.  What a single token names is one workgroup's work: 1024 and 2048 x 768 on one
+  // token 30 and 53 us, 18 and 23 with three launches, and 98 and 34 for 4096 (else 13 and 22).  Not added: 509 x 768
+  // into 2500 / 10000 / 20000 rows 9.1 / 13.2 / 17.7 and 13.7 / 15.6 / 18.5; 1024 x 64 into 10000 / 40000: 10.6 / 19.3
+  // and 15.6 / 14.6.
   const int64_t tiles = (E + 255) / 256;
   int64_t run = 16;
   while (run < 64 && (n + run - 1) / run * tiles > 256) run *= 2;
   const int64_t chunks = (n + run - 1) / run;
-  pl->once = n <= 1024 && chunks * tiles <= 256 && (add || (V <= 4096 && V * E * table_size <= (int64_t(8) << 20)));
+  pl->once = n <= 2048 && chunks * tiles <= 256 && (add || (V <= 16384 && V * E * table_size <= (int64_t(32) << 20)));
   if (pl->once) {
     pl->run = run;
     pl->chunks = chunks;

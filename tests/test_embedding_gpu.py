@@ -141,9 +141,10 @@ def test_backward_sort_sizes(n, V, E, kind):
     bwd_check(tokens_of(1, n, V, n, kind), V, E, F32, F32, False, 1.0, seed=n)
 
 
-# short lists: one launch or several by what is to be cleared, how wide the rows are and where 1024 and 4096 end
+# short lists: one launch or several by what is to be cleared, how wide the rows are and where 1024, 2048 and 4096 end
 @pytest.mark.parametrize("n,V,E", [(17, 50000, 20), (1000, 4096, 260), (1023, 4097, 260), (1024, 1 << 20, 4),
                                    (1025, 700, 24), (2500, 50000, 24), (4096, 300, 24), (1024, 40, 4096),
+                                   (2047, 16384, 260), (2048, 16385, 24), (2049, 5000, 260), (1500, 50, 2000),
                                    (1024, 40, 4100), (700, 9, 2600)])
 @pytest.mark.parametrize("add", [False, True], ids=["new", "added"])
 def test_backward_short_lists(n, V, E, add):
