@@ -487,10 +487,15 @@ __global__ __launch_bounds__(1024) void embed_once_kernel(SortParams sp, SumPara
     return lo;
   };
   int i = r0 < r1 ? first_from(group + groups * (uint32_t)r0) : z;
+  uint32_t named = i < z ? sm.key[i] : V;  // the next row that is not to be cleared
   for (int64_t r = r0; r < r1; ++r) {
     const uint32_t v = group + groups * (uint32_t)r;
-    if (i < z && sm.key[i] == v) i = first_from(v + 1);
-    else store_n<OT, VC>(row_at<OT, VC>(p, v, col), nc, zero);
+    if (v == named) {
+      i = first_from(v + 1);
+      named = i < z ? sm.key[i] : V;
+    } else {
+      store_n<OT, VC>(row_at<OT, VC>(p, v, col), nc, zero);
+    }
   }
 }
 
@@ -690,13 +695,16 @@ void plan_embed_bwd(int64_t Bsz, int64_t L, int64_t V, int64_t E, int64_t table_
   // nothing to clear.  Calls of 509 x 768, added: 8.9 us, 13.8 with three launches; 2048 x 768: 8.7 and 17.4; 1024 x
   // 8192 (512 workgroups): 27 and 24.  What a single token names is one workgroup's work: 1024 and 2048 x 768 on one
   // token 30 and 53 us, 18 and 23 with three launches, and 98 and 34 for 4096 (else 13 and 22).  Not added: 509 x 768
-  // into 2500 / 10000 / 20000 rows 9.1 / 13.2 / 17.7 and 13.7 / 15.6 / 18.5; 1024 x 64 into 10000 / 40000: 10.6 / 19.3
-  // and 15.6 / 14.6.
+  // into 2500 / 10000 / 20000 rows 9.4 / 10.4 / 15.1 and 13.7 / 15.6 / 18.5; 1 x 1000 into 70000 (280 MB): 79 and 54.
   const int64_t tiles = (E + 255) / 256;
   int64_t run = 16;
   while (run < 64 && (n + run - 1) / run * tiles > 256) run *= 2;
-  const int64_t chunks = (n + run - 1) / run;
-  pl->once = n <= 2048 && chunks * tiles <= 256 && (add || (V <= 16384 && V * E * table_size <= (int64_t(32) << 20)));
+  int64_t chunks = (n + run - 1) / run;
+  pl->once = n <= 2048 && chunks * tiles <= 256 && (add || V * E * table_size <= (int64_t(64) << 20));
+  if (!add) {  // rows to clear: up to a workgroup per CU, where each wave has one
+    const int64_t all = 256 / tiles < V / 16 ? 256 / tiles : V / 16;
+    if (chunks < all) chunks = all;
+  }
   if (pl->once) {
     pl->run = run;
     pl->chunks = chunks;
