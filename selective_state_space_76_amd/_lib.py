@@ -171,15 +171,23 @@ def _stream(stream, device):
     return ctypes.c_void_p(stream.cuda_stream)
 
 
-def _on_stream(stream, *tensors):
-    """Tensors this module allocated are taken from torch's current stream; when the kernels run
-    on another stream, tell the caching allocator so the memory is not handed out again before
-    that stream's work on it is done."""
+def _empty(shape, dtype, device, stream):
+    """An uninitialised tensor for kernels on `stream`, from that stream's own memory: a block that torch's allocator
+    holds for another stream may still be in use by work queued there."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _hand_out(stream, *tensors):
+    """Tensors made by _empty() that the caller gets: used on the caller's stream from now on, which the allocator has
+    to know before it hands their memory out again on `stream`."""
     if stream is None:
         return
     for t in tensors:
         if t is not None:
-            t.record_stream(stream)
+            t.record_stream(torch.cuda.current_stream(t.device))
 
 
 def make_shape(batch, dim, dstate, seqlen, io_dtype, zoh=False, reverse=False) -> ssm_shape:
@@ -215,12 +223,12 @@ def scan_fwd(u, delta, A, B, C, D=None, z=None, delta_bias=None, initial_state=N
     io = _io_dtype(u)
     device = u.device
     sh = make_shape(Bsz, Dm, N, L, io, zoh, reverse)
-    made = []  # tensors allocated here (on torch's current stream)
+    made = []  # tensors allocated here
     if out is None:
-        out = torch.empty_like(u)
+        out = _empty(u.shape, u.dtype, device, stream)
         made.append(out)
     if final_state is True:
-        final_state = torch.empty((Bsz, Dm, N), dtype=torch.float32, device=u.device)
+        final_state = _empty((Bsz, Dm, N), torch.float32, device, stream)
         made.append(final_state)
     elif final_state is False:
         final_state = None
@@ -240,8 +248,7 @@ def scan_fwd(u, delta, A, B, C, D=None, z=None, delta_bias=None, initial_state=N
     if split:
         need = int(lib.ssm_scan_workspace_size(ctypes.byref(sh)))
         if need and workspace is None:
-            workspace = torch.empty(need, dtype=torch.uint8, device=u.device)
-            made.append(workspace)
+            workspace = _empty(need, torch.uint8, device, stream)
         if workspace is not None:
             ws_bytes = workspace.numel() * workspace.element_size()
     else:
@@ -254,7 +261,7 @@ def scan_fwd(u, delta, A, B, C, D=None, z=None, delta_bias=None, initial_state=N
         _check(lib.ssm_scan_fwd_save(ctypes.byref(sh), _ptr(u), _ptr(delta), _ptr(A), _ptr(B), _ptr(C), _ptr(D),
                                      _ptr(z), _ptr(delta_bias), _ptr(initial_state), _ptr(out), _ptr(final_state),
                                      _ptr(checkpoints), _ptr(workspace), ws_bytes, _stream(stream, device)))
-    _on_stream(stream, *made)
+    _hand_out(stream, *made)
     return out, final_state
 
 
@@ -301,7 +308,7 @@ def state_update(state, u, delta, A, B, C, D=None, z=None, delta_bias=None, *, o
     device = u.device
     made = []
     if out is None:
-        out = torch.empty_like(u)
+        out = _empty(u.shape, u.dtype, device, stream)
         made.append(out)
     f32 = torch.float32
     for t, shp, dt, name in ((state, (Bsz, Dm, N), f32, "state"), (delta, (Bsz, Dm), u.dtype, "delta"),
@@ -312,7 +319,7 @@ def state_update(state, u, delta, A, B, C, D=None, z=None, delta_bias=None, *, o
     _check(lib.ssm_state_update(Bsz, Dm, N, io, SSM_FLAG_ZOH if zoh else 0, _ptr(state), _ptr(u), _ptr(delta),
                                 _ptr(A), _ptr(B), _ptr(C), _ptr(D), _ptr(z), _ptr(delta_bias), _ptr(out),
                                 _stream(stream, device)))
-    _on_stream(stream, *made)
+    _hand_out(stream, *made)
     return out
 
 
@@ -359,7 +366,7 @@ def scan_bwd(u, delta, A, B, C, D=None, z=None, delta_bias=None, initial_state=N
             g[k] = None
             continue
         if g.get(k) is None:
-            g[k] = torch.empty(shp, dtype=dt, device=dev)
+            g[k] = _empty(shp, dt, dev, stream)
             made.append(g[k])
         _expect(g[k], shp, dt, k, device)
     size_fn = lib.ssm_scan_bwd_workspace_size if checkpoints is None else lib.ssm_scan_bwd_saved_workspace_size
@@ -367,8 +374,7 @@ def scan_bwd(u, delta, A, B, C, D=None, z=None, delta_bias=None, initial_state=N
     if workspace is not None and workspace.device != device:
         raise ValueError("workspace: expected a tensor on %s, got %s" % (device, workspace.device))
     if workspace is None:
-        workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=dev)
-        made.append(workspace)
+        workspace = _empty(max(need, 1), torch.uint8, dev, stream)
     ws_bytes = workspace.numel() * workspace.element_size()
     outs = (_ptr(g["du"]), _ptr(g["ddelta"]), _ptr(g["dA"]), _ptr(g["dB"]), _ptr(g["dC"]), _ptr(g["dD"]),
             _ptr(g["dz"]), _ptr(g["ddelta_bias"]), _ptr(g["dinitial_state"]))
@@ -379,7 +385,7 @@ def scan_bwd(u, delta, A, B, C, D=None, z=None, delta_bias=None, initial_state=N
     else:
         _check(lib.ssm_scan_bwd_saved(ctypes.byref(sh), *ins, _ptr(checkpoints), *outs, _ptr(workspace), ws_bytes,
                                       _stream(stream, device)))
-    _on_stream(stream, *made)
+    _hand_out(stream, *made)
     return g
 
 
@@ -396,10 +402,10 @@ def conv1d_fwd(x, weight, bias=None, initial_state=None, *, out=None, final_stat
     device = x.device
     made = []
     if out is None:
-        out = torch.empty_like(x)
+        out = _empty(x.shape, x.dtype, device, stream)
         made.append(out)
     if final_state is True:
-        final_state = torch.empty((Bsz, Dm, K - 1), dtype=x.dtype, device=x.device)
+        final_state = _empty((Bsz, Dm, K - 1), x.dtype, device, stream)
         made.append(final_state)
     elif final_state is False:
         final_state = None
@@ -411,7 +417,7 @@ def conv1d_fwd(x, weight, bias=None, initial_state=None, *, out=None, final_stat
         _expect(t, shp, dt, name, device)
     _check(lib.ssm_conv1d_fwd(Bsz, Dm, L, K, io, _ptr(x), _ptr(weight), _ptr(bias), _ptr(initial_state),
                               _ptr(out), _ptr(final_state), _stream(stream, device)))
-    _on_stream(stream, *made)
+    _hand_out(stream, *made)
     return out, final_state
 
 
@@ -426,7 +432,7 @@ def conv1d_update(conv_state, x, weight, bias=None, *, out=None, stream=None):
     device = x.device
     made = []
     if out is None:
-        out = torch.empty_like(x)
+        out = _empty(x.shape, x.dtype, device, stream)
         made.append(out)
     f32 = torch.float32
     for t, shp, dt, name in ((conv_state, (Bsz, Dm, K - 1), x.dtype, "conv_state"),
@@ -435,5 +441,5 @@ def conv1d_update(conv_state, x, weight, bias=None, *, out=None, stream=None):
         _expect(t, shp, dt, name, device)
     _check(lib.ssm_conv1d_update(Bsz, Dm, K, io, _ptr(conv_state), _ptr(x), _ptr(weight), _ptr(bias),
                                  _ptr(out), _stream(stream, device)))
-    _on_stream(stream, *made)
+    _hand_out(stream, *made)
     return out

@@ -17,8 +17,8 @@ import math
 import numpy as np
 import torch
 
-from ._lib import (SSM_BF16, SSM_F32, _check, _expect, _io_dtype, _nonempty, _on_stream, _ptr, load, ssm_adamw_config,
-                   ssm_embed_shape)
+from ._lib import (SSM_BF16, SSM_F32, _check, _empty, _expect, _hand_out, _io_dtype, _nonempty, _ptr, load,
+                   ssm_adamw_config, ssm_embed_shape)
 
 SSM_I32 = 0
 SSM_I64 = 1
@@ -51,11 +51,10 @@ def _stream(stream, device):
     return torch._C._cuda_getCurrentRawStream(device.index) if stream is None else stream.cuda_stream
 
 
-def _workspace(workspace, need, device, made):
+def _workspace(workspace, need, device, stream):
     """The caller's workspace, or one made here."""
     if workspace is None:
-        workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=device)
-        made.append(workspace)
+        workspace = _empty(max(need, 1), torch.uint8, device, stream)
     elif workspace.device != device:
         raise ValueError("workspace: expected a tensor on %s, got %s" % (device, workspace.device))
     return workspace, workspace.numel() * workspace.element_size()
@@ -88,16 +87,16 @@ def conv1d_bwd(x, weight, bias=None, initial_state=None, *, dout, dfinal_state=N
     for k, shp, dt in (("dx", full, xdt), ("dweight", taps, f32), ("dbias", channels, f32),
                        ("dinitial_state", state, xdt)):
         if g.get(k) is None:
-            g[k] = torch.empty(shp, dtype=dt, device=device)
+            g[k] = _empty(shp, dt, device, stream)
             made.append(g[k])
         else:
             _want(g[k], shp, dt, k, device)
-    workspace, ws_bytes = _workspace(workspace, lib.ssm_conv1d_bwd_workspace_size(Bsz, Dm, L, K, io), device, made)
+    workspace, ws_bytes = _workspace(workspace, lib.ssm_conv1d_bwd_workspace_size(Bsz, Dm, L, K, io), device, stream)
     _check(lib.ssm_conv1d_bwd(Bsz, Dm, L, K, io, _address(x), _address(weight), _address(bias),
                               _address(initial_state), _address(dout), _address(dfinal_state), _address(g["dx"]),
                               _address(g["dweight"]), _address(g["dbias"]), _address(g["dinitial_state"]),
                               _address(workspace), ws_bytes, _stream(stream, device)))
-    _on_stream(stream, *made)
+    _hand_out(stream, *made)
     return g
 
 
@@ -135,14 +134,14 @@ def embedding_fwd(tokens, weight, *, scale=1.0, dtype=None, channels_first=False
     sh, shape = _embed_shape(tokens, rows, dim, weight.dtype, dtype, channels_first, scale=scale)
     device, made = tokens.device, None
     if out is None:
-        out = made = torch.empty(shape, dtype=dtype, device=device)
+        out = made = _empty(shape, dtype, device, stream)
     else:
         _want(out, shape, dtype, "out", device)
     if weight.device != device:
         _expect(weight, weight.shape, weight.dtype, "weight", device)
     _check(lib.ssm_embedding_fwd(ctypes.byref(sh), _address(tokens), _address(weight), scale, _address(out),
                                  _stream(stream, device)))
-    _on_stream(stream, made)
+    _hand_out(stream, made)
     return out
 
 
@@ -168,17 +167,16 @@ def embedding_bwd(tokens, dout, rows, *, scale=1.0, channels_first=False, dtype=
         raise ValueError("dout: expected %d dimensions, got %d" % (want, dout.dim()))
     dim = dout.shape[1 if channels_first else -1]
     sh, shape = _embed_shape(tokens, rows, dim, dtype, dout.dtype, channels_first, accumulate, scale)
-    device, made = tokens.device, []
+    device, made = tokens.device, None
     _want(dout, shape, dout.dtype, "dout", device)
     if dweight is None:
-        dweight = torch.empty((rows, dim), dtype=dtype, device=device)
-        made.append(dweight)
+        dweight = made = _empty((rows, dim), dtype, device, stream)
     _want(dweight, (rows, dim), dtype, "dweight", device)
     need = int(lib.ssm_embedding_bwd_workspace_size(ctypes.byref(sh)))
-    workspace, ws_bytes = _workspace(workspace, need, device, made)
+    workspace, ws_bytes = _workspace(workspace, need, device, stream)
     _check(lib.ssm_embedding_bwd(ctypes.byref(sh), _address(tokens), _address(dout), scale, _address(dweight),
                                  _address(workspace), ws_bytes, _stream(stream, device)))
-    _on_stream(stream, *made)
+    _hand_out(stream, made)
     return dweight
 
 
@@ -270,6 +268,12 @@ class AdamW:
             raise ValueError("%s: tensors must be contiguous" % what)
         return list(map(torch.Tensor.data_ptr, tensors))
 
+    def _used_on(self, stream):
+        """The states were made on the stream that was current at construction; the allocator has to know of this one."""
+        if stream is not None:
+            for t in self.state.values():
+                t.record_stream(stream)
+
     def step(self, grads=None, *, stream=None):
         """One step with the gradients given (fp32 or bf16, the parameters' shapes), by default each parameter's
         .grad; a parameter whose gradient is None is left out.  Returns the gradients' norm before clipping (a
@@ -302,12 +306,11 @@ class AdamW:
             raise ValueError("lr %r, betas %r, eps %r, weight_decay %r, max_grad_norm %r: out of range"
                              % (self.lr, self.betas, self.eps, self.weight_decay, self.max_grad_norm))
         rows, count = table.ctypes.data, len(table)
-        s, made, norm, clip = _stream(stream, self.device), [], None, None
+        s, norm, clip = _stream(stream, self.device), None, None
         if self.max_grad_norm is not None:
             need = int(lib.ssm_grad_norm_workspace_size(rows, count))
-            clip = torch.empty(2, dtype=torch.float32, device=self.device)
-            workspace = torch.empty(need, dtype=torch.uint8, device=self.device)
-            made = [clip, workspace]
+            clip = _empty(2, torch.float32, self.device, stream)
+            workspace = _empty(need, torch.uint8, self.device, stream)
             _check(lib.ssm_grad_norm(rows, count, float(self.max_grad_norm), _address(clip), _address(workspace), need,
                                      s))
             norm = clip[0]
@@ -318,7 +321,8 @@ class AdamW:
                                   _address(st.get("exp_avg_base")), _address(st.get("exp_avg_sq_base")),
                                   _address(st.get("master")), _address(clip), s))
         self.step_count += 1
-        _on_stream(stream, *made)
+        self._used_on(stream)
+        _hand_out(stream, clip)
         return norm
 
     def state_values(self, *, stream=None):
@@ -327,10 +331,11 @@ class AdamW:
         st = self.state
         if self.state_bits == 32:
             return st["exp_avg"], st["exp_avg_sq"]
-        m = torch.empty(self.numel, dtype=torch.bfloat16, device=self.device)
-        v = torch.empty_like(m)
+        m = _empty(self.numel, torch.bfloat16, self.device, stream)
+        v = _empty(self.numel, torch.bfloat16, self.device, stream)
         _check(load().ssm_adamw_state_values(self.numel, _address(st["exp_avg"]), _address(st["exp_avg_sq"]),
                                              _address(st["exp_avg_base"]), _address(st["exp_avg_sq_base"]), _address(m),
                                              _address(v), _stream(stream, self.device)))
-        _on_stream(stream, m, v)
+        self._used_on(stream)
+        _hand_out(stream, m, v)
         return m, v
