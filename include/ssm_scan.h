@@ -347,7 +347,7 @@ ssm_status ssm_embedding_bwd(const ssm_embed_shape* shape, const void* tokens, c
                              struct ihipStream_t* stream);
 
 /* One parameter tensor of an optimizer step (dense, any shape).  The params, gradients and state
- * buffers of a step must not overlap (checked but for one tensor's param against another's). */
+ * buffers of a step must not overlap (checked; gradients may overlap one another). */
 typedef struct ssm_adamw_tensor {
   void* param;          /* read and written */
   const void* grad;

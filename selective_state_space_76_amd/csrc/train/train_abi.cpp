@@ -5,6 +5,8 @@
 #include <stdint.h>
 #include <string.h>
 
+#include <algorithm>
+
 #include "../../../include/ssm_scan.h"
 #include "train_launch.h"
 
@@ -212,6 +214,30 @@ ssm_status check_tensors(const ssm_adamw_tensor* t, int64_t count, bool grads_on
   return SSM_OK;
 }
 
+// Whether a tensor's param lies over a gradient, its own or another's, or over another param.  The params are sorted
+// a block at a time on the stack, and all other ranges are looked up among them.
+bool params_clash(const ssm_adamw_tensor* t, int64_t count) {
+  constexpr int64_t kBlock = 2048;
+  Range r[kBlock];
+  auto param = [&](int64_t k) { return span(t[k].param, t[k].numel * dtype_size(t[k].param_dtype)); };
+  for (int64_t b = 0; b < count; b += kBlock) {
+    const int64_t n = count - b < kBlock ? count - b : kBlock;
+    for (int64_t i = 0; i < n; ++i) r[i] = param(b + i);
+    std::sort(r, r + n, [](const Range& x, const Range& y) { return x.lo < y.lo; });
+    for (int64_t i = 1; i < n; ++i)
+      if (overlaps(r[i - 1], r[i])) return true;
+    auto hit = [&](Range q) {  // the first that ends behind q's beginning: the only one before those behind q
+      const Range* f = std::partition_point(r, r + n, [&](const Range& x) { return x.hi <= q.lo; });
+      return f < r + n && overlaps(*f, q);
+    };
+    for (int64_t k = 0; k < count; ++k) {
+      if (hit(span(t[k].grad, t[k].numel * dtype_size(t[k].grad_dtype)))) return true;
+      if (k >= b + n && hit(param(k))) return true;
+    }
+  }
+  return false;
+}
+
 // Calls go(table, workgroups) for the tensors that `take` accepts, as many at a time as a table holds and a
 // launch's workgroups allow, `chunk` elements per workgroup; put(table, slot, place in the list) enters one.
 template <typename Table, int kRoom, typename Take, typename Put, typename Go>
@@ -329,10 +355,11 @@ ssm_status ssm_adamw_step(const ssm_adamw_config* c, const ssm_adamw_tensor* ten
   for (int64_t k = 0; k < count; ++k) {
     const Range p = span(tensors[k].param, tensors[k].numel * dtype_size(tensors[k].param_dtype));
     const Range g = span(tensors[k].grad, tensors[k].numel * dtype_size(tensors[k].grad_dtype));
-    if (overlaps(p, g) || overlaps(p, ins[0])) return SSM_ERR_OVERLAP;
+    if (overlaps(p, ins[0])) return SSM_ERR_OVERLAP;
     for (const Range& o : outs)
       if (overlaps(o, p) || overlaps(o, g)) return SSM_ERR_OVERLAP;
   }
+  if (params_clash(tensors, count)) return SSM_ERR_OVERLAP;
 
   ssm::AdamParams a;
   memset(&a, 0, sizeof(a));

@@ -1,0 +1,42 @@
+"""The training operators without a GPU: what a call must refuse, plan or pass on."""
+import ctypes
+
+import numpy as np
+import pytest
+import torch
+
+from selective_state_space_76_amd import _lib as L
+from tests.test_train_host import cfg, fake, rows
+
+OVERLAP, LAUNCH = 8, 7
+
+
+def step(t):
+    """The status of a step: LAUNCH where every check passed (there is no GPU here)."""
+    return L.load().ssm_adamw_step(ctypes.byref(cfg()), t.ctypes.data, len(t), fake(1), fake(2), None, None, None, None, None)
+
+
+@pytest.mark.skipif(torch.cuda.is_available(), reason="a call that is not refused would run on made-up addresses")
+@pytest.mark.parametrize("count", [2, 3, 100, 2048, 2049, 5000])
+def test_adamw_refuses_a_param_over_any_gradient_or_param(count):
+    """Workgroups of one tensor would write what those of another read."""
+    base = fake(3).value
+    order = np.random.default_rng(count).permutation(2 * count) * 1024  # params and gradients in no order, side by side
+
+    def make(**at):
+        t = rows(*[dict(param=base + int(order[2 * k]), grad=base + int(order[2 * k + 1]), numel=512, offset=512 * k)
+                   for k in range(count)])
+        for k, (name, v) in at.items():
+            t[name][int(k[1:])] = v
+        return t
+
+    good = make()
+    assert step(good) == LAUNCH  # they touch, they do not overlap
+    first, last = 0, count - 1
+    for a, b in ((first, last), (last, first), (last, last)):
+        for off in (0, 1008, -1008):
+            assert step(make(**{"k%d" % a: ("grad", int(good["param"][b]) + off)})) == OVERLAP, (a, b, off)
+    for off in (0, 1008, -1008):
+        assert step(make(**{"k%d" % last: ("param", int(good["param"][first]) + off)})) == OVERLAP
+    # two tensors with one gradient: nothing is written there
+    assert step(make(**{"k%d" % last: ("grad", int(good["grad"][first]))})) == LAUNCH
