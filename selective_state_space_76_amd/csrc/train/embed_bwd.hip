@@ -14,7 +14,8 @@
 //      the chunk go to dweight; one that reaches over an end goes to memory as a partial sum.
 //   3. Join: where a token's rows begin in a chunk and go on in the next, its partial sums are added, in order.
 // Up to 2048 positions take all three in one launch where there is little to clear (embed_once_kernel).
-// dout in [B,E,L] is first brought to [B,L,E], unless the table has few rows (embed_bwd_few.hip).
+// dout in [B,E,L] is first brought to [B,L,E], unless the table has few rows and the batch rows are not too short for
+// products (embed_bwd_few.hip).
 // Tokens outside the table sort as V, behind all others, and are left out.
 //
 // Bound by HBM, which the launches reach in part: 8 x 2048 tokens of width 768 into 50000 rows (25 MB read, 154 MB
@@ -681,7 +682,7 @@ size_t round256(size_t x) { return (x + 255) & ~size_t(255); }
 
 void plan_embed_bwd(int64_t Bsz, int64_t L, int64_t V, int64_t E, int64_t table_size, bool io_bf16, bool cf, bool add,
                     EmbedBwdPlan* pl) {
-  if (cf && embed_few_rows(V, io_bf16)) return plan_embed_few(Bsz, L, V, E, pl);
+  if (cf && embed_few_pays(Bsz, L, V, E, io_bf16)) return plan_embed_few(Bsz, L, V, E, pl);
   const int64_t n = Bsz * L;
   pl->bits = 1;
   while ((V >> pl->bits) != 0) ++pl->bits;  // keys 0 .. V

@@ -202,10 +202,6 @@ __global__ __launch_bounds__(256) void embed_few_join_kernel(FewParams p) {
   }
 }
 
-// Rows up to which the products pay: the matrix cores keep up with HBM through 64 rows in bf16 and 32 in fp32
-// (4 and 2 products per piece of dout).
-bool embed_few_rows(int64_t V, bool io_bf16) { return V <= (io_bf16 ? 64 : 32); }
-
 void plan_embed_few(int64_t Bsz, int64_t L, int64_t V, int64_t E, EmbedBwdPlan* pl) {
   const int64_t groups = (E + 63) / 64;
   int64_t seg = (Bsz * L * groups / 2048 + 511) / 512 * 512;  // whole tiles; 2048 workgroups or more
@@ -215,6 +211,21 @@ void plan_embed_few(int64_t Bsz, int64_t L, int64_t V, int64_t E, EmbedBwdPlan* 
   pl->run = seg;
   pl->chunks = Bsz * ((L + seg - 1) / seg);
   pl->total = (size_t)pl->chunks * V * E * 4;
+}
+
+// Where the products pay.  The matrix cores keep up with HBM through 64 rows in bf16 and 32 in fp32 (4 and 2 products
+// per piece of dout).  A workgroup covers 512 positions of one batch row at least and writes V sums of each of its
+// channels, so short batch rows would be mostly idle work and sums: they are turned and sorted instead.  Calls in bf16
+// with 4 / 16 / 64 rows by products, and sorted: 8192 x 16 positions, 1024 channels: 1.5 / 1.6 / 3.1 ms and 0.52 (at 64
+// rows with 2.1 GB of sums for 0.27 GB of dout); 4096 x 64: 0.82 / 0.84 / 1.6 ms and 0.36; 1024 x 256: 222 / 229 / 386 us
+// and 309; 256 x 640: 92 / 96 / 180 and 202; 64 x 512: 20 / 21 / 34 and 58.  Few workgroups and sums cost little,
+// whatever they cover: 64 x 64: 16 / 17 / 30 us and 31 / 28 / 27; 64 x 16: 17 / 17 / 31 and 23 / 19 / 16.
+bool embed_few_pays(int64_t Bsz, int64_t L, int64_t V, int64_t E, bool io_bf16) {
+  if (V > (io_bf16 ? 64 : 32)) return false;
+  EmbedBwdPlan pl;
+  plan_embed_few(Bsz, L, V, E, &pl);
+  if (pl.chunks * ((E + 63) / 64) <= 1024 && pl.total <= (size_t(4) << 20)) return true;
+  return L >= 256 && 2 * pl.chunks * V * 4 < Bsz * L * (io_bf16 ? 2 : 4);
 }
 
 namespace {

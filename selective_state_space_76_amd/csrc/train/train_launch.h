@@ -98,7 +98,7 @@ struct EmbedParams {
 hipError_t launch_embed_fwd(const EmbedParams& p, bool table_bf16, bool io_bf16, hipStream_t s);
 
 struct EmbedBwdPlan {
-  bool few = false;               // [B,E,L] and few rows: products (embed_bwd_few.hip); run: positions per segment
+  bool few = false;               // [B,E,L], few rows, not too short: products (embed_bwd_few.hip); run: positions per segment
   bool transpose = false;         // [B,E,L]: dout is brought to [B,L,E] first
   bool once = false;              // short lists: all steps in one launch, no workspace but the turned dout
   int bits = 0, passes = 0, digit_bits = 0;
@@ -110,7 +110,7 @@ void plan_embed_bwd(int64_t Bsz, int64_t L, int64_t V, int64_t E, int64_t table_
                     EmbedBwdPlan* pl);
 hipError_t launch_embed_bwd(const EmbedParams& p, const EmbedBwdPlan& pl, bool table_bf16, bool io_bf16, void* ws,
                             hipStream_t s);
-bool embed_few_rows(int64_t V, bool io_bf16);
+bool embed_few_pays(int64_t Bsz, int64_t L, int64_t V, int64_t E, bool io_bf16);
 void plan_embed_few(int64_t Bsz, int64_t L, int64_t V, int64_t E, EmbedBwdPlan* pl);
 hipError_t launch_embed_few(const EmbedParams& p, const EmbedBwdPlan& pl, bool table_bf16, bool io_bf16, void* ws,
                             hipStream_t s);

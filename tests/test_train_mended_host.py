@@ -40,3 +40,15 @@ def test_adamw_refuses_a_param_over_any_gradient_or_param(count):
         assert step(make(**{"k%d" % last: ("param", int(good["param"][first]) + off)})) == OVERLAP
     # two tensors with one gradient: nothing is written there
     assert step(make(**{"k%d" % last: ("grad", int(good["grad"][first]))})) == LAUNCH
+
+
+@pytest.mark.parametrize("B,Ln,V,E", [(8192, 16, 64, 1024), (65536, 2, 64, 1024), (1 << 20, 3, 60, 64), (4096, 64, 4, 1024),
+                                      (100000, 17, 32, 300), (1024, 255, 64, 1024), (64, 2, 64, 256), (1, 1 << 20, 4, 1024)])
+@pytest.mark.parametrize("io", [0, 1], ids=["f32", "bf16"])
+def test_embedding_gradient_workspace_of_many_short_rows(B, Ln, V, E, io):
+    """What is kept beside dout is no more than a turned copy of it, the sorted lists (16 bytes a position and their sums)
+    and a few MB, whatever the lengths of the batch rows."""
+    s = L.ssm_embed_shape(batch=B, seqlen=Ln, rows=V, dim=E, index_dtype=1, table_dtype=0, io_dtype=io, flags=1)
+    dout = B * Ln * E * (2 if io else 4)
+    need = L.load().ssm_embedding_bwd_workspace_size(ctypes.byref(s))
+    assert 0 < need <= 1.5 * dout + 32 * B * Ln + (8 << 20)
