@@ -198,7 +198,9 @@ __global__ __launch_bounds__(256) void embed_few_join_kernel(FewParams p) {
   if (threadIdx.x < 64 && i < n) {
     s = (sm[threadIdx.x] + sm[threadIdx.x + 64] + sm[threadIdx.x + 128] + sm[threadIdx.x + 192]) * p.scale;
     OT* o = static_cast<OT*>(p.dweight) + i;
-    store_io(o, p.add ? to_f32(*o) + s : s);
+    // Adding nothing leaves the element alone: the rows of tokens that do not occur (an exact zero) are not written.
+    if (!p.add) store_io(o, s);
+    else if (s != 0.0f) store_io(o, to_f32(*o) + s);
   }
 }
 
