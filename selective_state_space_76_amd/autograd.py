@@ -9,14 +9,46 @@ Bookkeeping only: the forward and backward arithmetic both run in the library's 
 gradients are the chain rule applied to the pages' forward recurrence, see include/ssm_scan.h).
 Gradients are returned in each input's dtype; the library computes dA, dB, dC, dD and d(delta_bias)
 in fp32 and they are cast to bf16 when those inputs are bf16.  Both discretisations (the default
-dt*B and zero-order hold) and both scan directions have gradients.
+dt*B and zero-order hold) and both scan directions have gradients.  There are no gradients of gradients: asking
+for one (after create_graph=True) is an error.
 """
 from __future__ import annotations
+
+import functools
 
 import torch
 
 from ._lib import checkpoints_shape, conv1d_fwd, scan_bwd, scan_fwd
 from .training import conv1d_bwd, embedding_bwd, embedding_fwd
+
+
+class _NoSecond(torch.autograd.Function):
+    """Passes n gradients on, as functions of the tensors behind them that cannot be differentiated."""
+
+    @staticmethod
+    def forward(ctx, n, *tensors):
+        return tensors[:n]
+
+    @staticmethod
+    def backward(ctx, *grads):
+        raise RuntimeError("the gradients of the scan, the conv and the embedding cannot be differentiated again")
+
+
+def _first_order(backward):
+    """The kernels' results carry no graph.  Where the caller wants one (create_graph=True), the gradients are tied to
+    everything that they depend on, so that a second derivative is refused and no term of it gets lost."""
+    @functools.wraps(backward)
+    def run(ctx, *douts):
+        with torch.no_grad():
+            grads = backward(ctx, *douts)
+        if torch.is_grad_enabled():
+            behind = [t for t in (*ctx.saved_tensors, *douts) if t is not None and t.requires_grad]
+            some = [g for g in grads if g is not None]
+            if behind and some:
+                tied = iter(_NoSecond.apply(len(some), *some, *behind))
+                grads = tuple(None if g is None else next(tied) for g in grads)
+        return grads
+    return run
 
 
 class SelectiveScanFn(torch.autograd.Function):
@@ -35,6 +67,7 @@ class SelectiveScanFn(torch.autograd.Function):
         return out, final_state
 
     @staticmethod
+    @_first_order
     def backward(ctx, dout, dfinal):
         u, delta, A, B, C, D, z, delta_bias, initial_state, ck = ctx.saved_tensors
         dout = torch.zeros_like(u) if dout is None else dout.to(u.dtype).contiguous()
@@ -67,6 +100,7 @@ class CausalConv1dFn(torch.autograd.Function):
         return u, final_state
 
     @staticmethod
+    @_first_order
     def backward(ctx, dout, dfinal):
         x, weight, bias, initial_state = ctx.saved_tensors
         dout = torch.zeros_like(x) if dout is None else dout.to(x.dtype).contiguous()
@@ -93,6 +127,7 @@ class EmbeddingFn(torch.autograd.Function):
         return embedding_fwd(tokens, weight, scale=scale, dtype=dtype, channels_first=channels_first)
 
     @staticmethod
+    @_first_order
     def backward(ctx, dout):
         (tokens,) = ctx.saved_tensors
         rows, dtype, scale, channels_first = ctx.table

@@ -1,0 +1,94 @@
+"""The autograd functions without a GPU: the library's calls are replaced by torch code of the same mathematics, the
+bookkeeping is the package's own."""
+import pytest
+import torch
+
+import selective_state_space_76_amd as ssm
+from selective_state_space_76_amd import autograd as F
+
+
+@pytest.fixture
+def plain(monkeypatch):
+    def rows(tokens, weight, scale=1.0, dtype=None, channels_first=False):
+        out = weight.detach()[tokens] * scale
+        return out.transpose(1, 2).contiguous() if channels_first else out
+
+    def rows_bwd(tokens, dout, n, scale=1.0, channels_first=False, dtype=None):
+        d = dout.transpose(1, 2) if channels_first else dout
+        return torch.zeros(n, d.shape[-1]).index_add_(0, tokens.reshape(-1), d.reshape(-1, d.shape[-1])) * scale
+
+    def conv(x, weight, bias, init):
+        H = weight.shape[1] - 1
+        xs = torch.cat([x.new_zeros(*x.shape[:2], H) if init is None else init, x], -1)
+        y = torch.nn.functional.conv1d(xs, weight[:, None], bias, groups=x.shape[1])
+        return torch.nn.functional.silu(y), xs[..., x.shape[-1]:].contiguous()
+
+    def conv_bwd(x, weight, bias, init, *, dout, dfinal_state):
+        with torch.enable_grad():
+            ins = [t.detach().requires_grad_(True) for t in (x, weight, bias, init)]
+            outs = conv(*ins)
+            g = torch.autograd.grad(outs, ins, [dout, torch.zeros_like(outs[1]) if dfinal_state is None else dfinal_state])
+        return dict(zip(("dx", "dweight", "dbias", "dinitial_state"), g))
+
+    def scan(u, delta, A, B, C, D, z, bias, init, zoh, reverse, checkpoints):
+        return u.detach() * delta.detach(), torch.zeros(u.shape[0], u.shape[1], A.shape[1])
+
+    def scan_bwd(u, delta, *a, dout, **k):
+        return dict({n: None for n in ("dA", "dB", "dC", "dD", "dz", "ddelta_bias", "dinitial_state")}, du=dout * delta,
+                    ddelta=dout * u)
+
+    for name, fn in (("embedding_fwd", rows), ("embedding_bwd", rows_bwd), ("conv1d_fwd", conv), ("conv1d_bwd", conv_bwd),
+                     ("scan_fwd", scan), ("scan_bwd", scan_bwd)):
+        monkeypatch.setattr(F, name, fn)
+
+
+def calls():
+    g = torch.Generator().manual_seed(1)
+    r = lambda *s: torch.randn(*s, generator=g)  # noqa: E731
+    tok = torch.randint(0, 7, (2, 9), generator=g)
+    one = r(2, 5, 9), r(2, 5, 9), -r(5, 4).abs(), r(2, 4, 9), r(2, 4, 9)
+    return {"embedding": (lambda w: ssm.embedding(tok, w, scale=2.0), (r(7, 5),)),
+            "embedding, channels first": (lambda w: ssm.embedding(tok, w, channels_first=True), (r(7, 5),)),
+            "conv": (lambda *a: ssm.causal_conv1d(*a)[0], (r(2, 5, 9), r(5, 4), r(5), r(2, 5, 3))),
+            "scan": (lambda u, d: ssm.selective_scan(u, d, *one[2:])[0], one[:2])}
+
+
+@pytest.mark.parametrize("name", list(calls()))
+@pytest.mark.parametrize("how", ["backward", "grad", "grad of one"])
+def test_a_gradient_of_a_gradient_is_refused(plain, name, how):
+    """Not left out in silence: a gradient penalty through these operators would miss their terms."""
+    f, ins = calls()[name]
+    ins = [t.requires_grad_(True) for t in ins]
+    out = f(*ins)
+    loss = (out * out).sum() + sum((t ** 3).sum() for t in ins)  # (another way from the gradients to the inputs)
+    grads = torch.autograd.grad(loss, ins, create_graph=True)
+    penalty = sum((g * g).sum() for g in grads)
+    with pytest.raises(RuntimeError, match="cannot be differentiated again"):
+        penalty.backward() if how == "backward" else torch.autograd.grad(penalty, ins if how == "grad" else ins[:1])
+
+
+@pytest.mark.parametrize("name", ["conv", "scan"])
+def test_a_gradient_that_depends_on_the_inputs_alone(plain, name):
+    """The output's gradient is a constant; that of the inputs still depends on them."""
+    f, ins = calls()[name]
+    ins = [t.requires_grad_(True) for t in ins]
+    grads = torch.autograd.grad(f(*ins).sum() + sum((t ** 3).sum() for t in ins), ins, create_graph=True)
+    with pytest.raises(RuntimeError, match="cannot be differentiated again"):
+        torch.autograd.grad(sum((g * g).sum() for g in grads), ins)
+
+
+def test_the_embedding_is_linear(plain):
+    """With a constant output gradient the table's is a constant too, and a graph through it goes on."""
+    f, (w,) = calls()["embedding"]
+    w.requires_grad_(True)
+    (g,) = torch.autograd.grad(f(w).sum() + (w ** 3).sum(), [w], create_graph=True)
+    (h,) = torch.autograd.grad(g.sum(), [w])
+    assert torch.allclose(h, 6 * w)
+
+
+@pytest.mark.parametrize("name", list(calls()))
+def test_first_gradients_as_before(plain, name):
+    f, ins = calls()[name]
+    ins = [t.requires_grad_(True) for t in ins]
+    f(*ins).sum().backward()
+    assert all(t.grad is not None and t.grad.shape == t.shape for t in ins)
