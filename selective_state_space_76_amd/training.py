@@ -16,6 +16,7 @@ import math
 
 import numpy as np
 import torch
+from torch.autograd.graph import increment_version
 
 from ._lib import (SSM_BF16, SSM_F32, _check, _empty, _expect, _hand_out, _io_dtype, _nonempty, _ptr, load,
                    ssm_adamw_config, ssm_embed_shape)
@@ -321,6 +322,8 @@ class AdamW:
                                   _address(st.get("exp_avg_base")), _address(st.get("exp_avg_sq_base")),
                                   _address(st.get("master")), _address(clip), s))
         self.step_count += 1
+        # a graph that has kept a parameter for its backward pass must be refused from now on
+        increment_version([p for p, h in zip(self.params, have) if h])
         self._used_on(stream)
         _hand_out(stream, clip)
         return norm

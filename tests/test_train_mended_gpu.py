@@ -3,7 +3,7 @@ import numpy as np
 import pytest
 import torch
 
-from selective_state_space_76_amd import embedding_bwd
+from selective_state_space_76_amd import AdamW, embedding_bwd
 from tests.test_embedding_gpu import bwd_check, tokens_of
 
 pytestmark = pytest.mark.gpu
@@ -40,3 +40,12 @@ def test_adding_leaves_the_rows_of_other_tokens_alone(cf, V, gt):
         assert torch.equal(got.view(bits)[~named], dw.view(bits)[~named])
         occurs = torch.isin(torch.arange(V), tok)
         assert (got[occurs] != 0).all()
+
+
+def test_a_step_behind_a_kept_graph():
+    p = torch.ones(300, device=DEV, requires_grad=True)
+    loss = (p * p).sum()
+    loss.backward(retain_graph=True)
+    AdamW([p]).step()
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        loss.backward()

@@ -1,11 +1,13 @@
 """The training operators without a GPU: what a call must refuse, plan or pass on."""
 import ctypes
+from types import SimpleNamespace
 
 import numpy as np
 import pytest
 import torch
 
 from selective_state_space_76_amd import _lib as L
+from selective_state_space_76_amd import training as T
 from tests.test_train_host import cfg, fake, rows
 
 OVERLAP, LAUNCH = 8, 7
@@ -52,3 +54,45 @@ def test_embedding_gradient_workspace_of_many_short_rows(B, Ln, V, E, io):
     dout = B * Ln * E * (2 if io else 4)
     need = L.load().ssm_embedding_bwd_workspace_size(ctypes.byref(s))
     assert 0 < need <= 1.5 * dout + 32 * B * Ln + (8 << 20)
+
+
+class Library:
+    """Every size is 4096 bytes, every call succeeds and does nothing."""
+
+    def __getattr__(self, name):
+        return lambda *args: 4096 if name.endswith("_size") else 0
+
+
+@pytest.fixture
+def unplugged(monkeypatch):
+    """The binding on CPU tensors, without the library."""
+    for m in (L, T):
+        monkeypatch.setattr(m, "load", Library)
+        monkeypatch.setattr(m, "_ptr", lambda t: None)
+        monkeypatch.setattr(m, "_stream", lambda stream, device: 0)
+    monkeypatch.setattr(T, "_address", lambda t: None)
+    empty = torch.empty
+    monkeypatch.setattr(torch, "empty", lambda *a, device=None, **k: empty(*a, **k))
+
+    def make(params, **k):
+        opt = T.AdamW(params, **k)
+        opt.device = SimpleNamespace(index=-1)
+        return opt
+
+    return make
+
+
+@pytest.mark.parametrize("clip", [None, 1.0])
+def test_a_step_is_an_in_place_change(unplugged, clip):
+    """A graph built before the step must not be run on the changed weights in silence."""
+    p, q = (torch.ones(300, requires_grad=True) for _ in range(2))
+    opt = unplugged([p, q], max_grad_norm=clip)
+    loss = (p * p).sum()
+    other = (q * q).sum()
+    p.grad = torch.ones(300)
+    opt.step()
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        loss.backward()
+    other.backward()  # without a gradient it was left out, and is what it was
+    opt.step([torch.ones(300)] * 2)
+    assert (p._version, q._version) == (2, 1)
