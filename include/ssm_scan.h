@@ -390,7 +390,9 @@ ssm_status ssm_grad_norm(const ssm_adamw_tensor* tensors, int64_t count, double 
  *       (c + K) << 20 (a sign bit, 8 exponent bits and 3 mantissa bits); code 0 stands for zero.  m has a
  *       sign in bit 7 and c in bits 0-6, v has c in 8 bits.  A block's base puts its largest
  *       element at the largest code, the others are rounded stochastically, and a v that is not zero
- *       is not rounded to zero.
+ *       is not rounded to zero.  In a block with elements that are not finite the base is stored as its
+ *       complement (-1 - K): there the largest code stands for infinity (a NaN is held as one: its param
+ *       is a NaN already) and the block's largest finite element is put at the code below it.
  *   exp_avg_base, exp_avg_sq_base : the blocks' K, int16, element offset / 128 onwards; 8-bit only
  *   master : fp32 weights of all bf16 tensors at their offsets (the step works on these and writes
  *       their rounded values to param), or NULL: then a bf16 param is itself rounded stochastically.

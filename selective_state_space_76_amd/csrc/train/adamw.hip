@@ -23,6 +23,9 @@
 // rounds up with the odds of the part cut off, which keeps the expected state exact.  A v > 0 is
 // never rounded to zero: a zero under a nonzero m would divide by eps alone.  m below its smallest code
 // becomes that code with the odds that keep its mean, else zero.
+// A block in which a gradient, or a square of one, was not finite keeps the complement of K, a negative number: there
+// the largest code stands for infinity, a NaN too, and the largest of the others has the code below.  So the neighbours
+// of such an element go on as if it were not there, as they do with fp32 states.
 #include <type_traits>
 
 #include "../ssm_device.h"
@@ -120,7 +123,12 @@ __device__ __forceinline__ int find(const Table& t, uint32_t block) {
   return lo;
 }
 
-__device__ __forceinline__ uint32_t code_bits(uint32_t c, uint32_t K) { return c ? (c + K) << 20 : 0u; }
+constexpr uint32_t kInf = 0x7f800000u;
+// what code c of a block with base K stands for; `top`: the largest code
+__device__ __forceinline__ uint32_t code_bits(uint32_t c, uint32_t K, uint32_t top) {
+  const bool odd = (int32_t)K < 0;
+  return !c ? 0u : odd && c == top ? kInf : (c + (odd ? ~K : K)) << 20;
+}
 // bit 7 of each byte is clear where the byte's low 7 bits (8 bits) are zero
 __device__ __forceinline__ uint32_t marks7(uint32_t w) { return (w | 0x80808080u) - 0x01010101u; }
 __device__ __forceinline__ uint32_t marks8(uint32_t w) { return marks7(w & 0x7f7f7f7fu) | w; }
@@ -208,6 +216,13 @@ __global__ __launch_bounds__(256) void adamw_kernel(AdamTable t, AdamParams a) {
           if (!((x.vc[e >> 2] >> (8 * (e & 3))) & 255u)) vb[e] = 0u;
         }
       }
+      if (__builtin_expect((int32_t)(x.mk | x.vk) < 0, 0)) {  // blocks that hold infinities
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+          mb[e] = code_bits((x.mc[e >> 2] >> (8 * (e & 3))) & 127u, x.mk, 127u);
+          vb[e] = code_bits((x.vc[e >> 2] >> (8 * (e & 3))) & 255u, x.vk, 255u);
+        }
+      }
 #pragma unroll
       for (int e = 0; e < V; ++e) {
         m[e] = __uint_as_float(mb[e] | ((x.mc[e >> 2] << (24 - 8 * (e & 3))) & 0x80000000u));
@@ -260,25 +275,53 @@ __global__ __launch_bounds__(256) void adamw_kernel(AdamTable t, AdamParams a) {
         am = am > x ? am : x;
         av = av > y ? av : y;
       }
-      const uint32_t mk = block_base(row_max(am), 127u), vk = block_base(row_max(av), 255u);
-      const uint32_t least = (mk + 1) << 20, m0 = 8u - (mk << 20), v0 = 8u - (vk << 20);
-      uint32_t mc[8], vc[8];
-      bool under = false;
-#pragma unroll
-      for (int e = 0; e < V; ++e) {
-        const uint32_t x = __float_as_uint(m[e]) & 0x7fffffffu, y = __float_as_uint(v[e]);
-        const uint32_t rm = (h[e] & 0xffffu) << 4, rv = (h[e] >> 16) << 4;
-        mc[e] = (uint32_t)clamp_code((int32_t)(x + rm + m0) >> 20, 0, 127);
-        vc[e] = (uint32_t)clamp_code((int32_t)(y + rv + v0) >> 20, (int32_t)(y < 1u ? y : 1u), 255);
-        under |= x - 1u < least - 1u;  // 0 < x < least
-      }
-      if (under) {  // below the smallest code: that code or zero
+      am = row_max(am);
+      av = row_max(av);
+      uint32_t mc[8], vc[8], mk, vk;
+      auto encode = [&](int32_t top_m, int32_t top_v) {
+        mk = block_base(am, (uint32_t)top_m);
+        vk = block_base(av, (uint32_t)top_v);
+        const uint32_t least = (mk + 1) << 20, m0 = 8u - (mk << 20), v0 = 8u - (vk << 20);
+        bool under = false;
 #pragma unroll
         for (int e = 0; e < V; ++e) {
-          const uint32_t x = __float_as_uint(m[e]) & 0x7fffffffu;
-          const bool up = __uint_as_float(x) > __uint_as_float(least) * ((float)(h[e] & 0xffffu) * 0x1p-16f + 0x1p-17f);
-          if (x < least) mc[e] = up ? 1u : 0u;
+          const uint32_t x = __float_as_uint(m[e]) & 0x7fffffffu, y = __float_as_uint(v[e]);
+          const uint32_t rm = (h[e] & 0xffffu) << 4, rv = (h[e] >> 16) << 4;
+          mc[e] = (uint32_t)clamp_code((int32_t)(x + rm + m0) >> 20, 0, top_m);
+          vc[e] = (uint32_t)clamp_code((int32_t)(y + rv + v0) >> 20, (int32_t)(y < 1u ? y : 1u), top_v);
+          under |= x - 1u < least - 1u;  // 0 < x < least
         }
+        if (under) {  // below the smallest code: that code or zero
+#pragma unroll
+          for (int e = 0; e < V; ++e) {
+            const uint32_t x = __float_as_uint(m[e]) & 0x7fffffffu;
+            const bool up =
+                __uint_as_float(x) > __uint_as_float(least) * ((float)(h[e] & 0xffffu) * 0x1p-16f + 0x1p-17f);
+            if (x < least) mc[e] = up ? 1u : 0u;
+          }
+        }
+      };
+      if (__builtin_expect(am < kInf && av < kInf, 1)) {  // the same in all lanes of a block
+        encode(127, 255);
+      } else {  // what is not finite gets the largest code, and the base goes by the other elements
+        const bool odd_m = am >= kInf, odd_v = av >= kInf;
+        am = av = 0;
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+          const uint32_t x = __float_as_uint(m[e]) & 0x7fffffffu, y = __float_as_uint(v[e]) & 0x7fffffffu;
+          if (x < kInf) am = am > x ? am : x;
+          if (y < kInf) av = av > y ? av : y;
+        }
+        am = row_max(am);
+        av = row_max(av);
+        encode(odd_m ? 126 : 127, odd_v ? 254 : 255);
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+          if ((__float_as_uint(m[e]) & 0x7fffffffu) >= kInf) mc[e] = 127u;
+          if ((__float_as_uint(v[e]) & 0x7fffffffu) >= kInf) vc[e] = 255u;
+        }
+        if (odd_m) mk = ~mk;
+        if (odd_v) vk = ~vk;
       }
       u32x2 mw = pack_codes(mc);
 #pragma unroll
@@ -416,7 +459,7 @@ __global__ __launch_bounds__(256) void state_values_kernel(int64_t n, const uint
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       const uint32_t c = w[e >> 2] >> (8 * (e & 3));
-      x[e] = code_bits(c & 127u, K) | ((c << 24) & 0x80000000u);
+      x[e] = code_bits(c & 127u, K, 127u) | ((c << 24) & 0x80000000u);
     }
     store_high<8>(mo + i, 8, x);
   }
@@ -424,7 +467,7 @@ __global__ __launch_bounds__(256) void state_values_kernel(int64_t n, const uint
     const u32x2 w = load_codes(v + i, 8);
     const uint32_t K = (uint32_t)(int32_t)vb[i / kAdamBlock];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) x[e] = code_bits((w[e >> 2] >> (8 * (e & 3))) & 255u, K);
+    for (int e = 0; e < 8; ++e) x[e] = code_bits((w[e >> 2] >> (8 * (e & 3))) & 255u, K, 255u);
     store_high<8>(vo + i, 8, x);
   }
 }
