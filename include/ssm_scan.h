@@ -404,6 +404,26 @@ ssm_status ssm_adamw_step(const ssm_adamw_config* config, const ssm_adamw_tensor
                           void* exp_avg, void* exp_avg_sq, int16_t* exp_avg_base, int16_t* exp_avg_sq_base,
                           float* master, const float* clip, struct ihipStream_t* stream);
 
+/* What a clipped step counts and keeps on the device, 32 bytes: only `step` is the caller's to set (the
+ * steps already made, 0 for a new optimizer), and to read after the stream's work is done. */
+typedef struct ssm_adamw_progress {
+  int64_t step;
+  uint32_t internal[6];
+} ssm_adamw_progress;
+
+/* ssm_grad_norm and ssm_adamw_step in one call, with the number of the step on the device: a step whose
+ * norm is not finite changes nothing and is not counted, and the call may be captured in a graph, each
+ * replay of which is the next step (with the settings and addresses of the capture).
+ *   config   : its `step` is not used
+ *   progress : on the device, 16-byte aligned; read and written
+ *   norm     : one float on the device, the norm before clipping
+ *   workspace: required, at least ssm_grad_norm_workspace_size() bytes
+ * Everything else as in the two calls; all checks come before the first launch. */
+ssm_status ssm_adamw_clipped_step(const ssm_adamw_config* config, const ssm_adamw_tensor* tensors, int64_t count,
+                                  double max_norm, void* exp_avg, void* exp_avg_sq, int16_t* exp_avg_base,
+                                  int16_t* exp_avg_sq_base, float* master, ssm_adamw_progress* progress, float* norm,
+                                  void* workspace, size_t workspace_bytes, struct ihipStream_t* stream);
+
 /* The values that 8-bit states stand for, exactly, in bf16: `numel` codes (a multiple of
  * SSM_ADAMW_BLOCK), numel / 128 bases each.  m_values and v_values : [numel] bf16; NULL means not wanted. */
 ssm_status ssm_adamw_state_values(int64_t numel, const void* exp_avg, const void* exp_avg_sq,

@@ -53,7 +53,7 @@ EXPORTS = ("ssm_abi_version", "ssm_status_str", "ssm_scan_workspace_size", "ssm_
            "ssm_state_update", "ssm_scan_bwd_workspace_size", "ssm_scan_bwd", "ssm_scan_bwd_saved_workspace_size",
            "ssm_scan_bwd_saved", "ssm_conv1d_fwd", "ssm_conv1d_update",
            "ssm_conv1d_bwd_workspace_size", "ssm_conv1d_bwd", "ssm_embedding_fwd", "ssm_embedding_bwd_workspace_size",
-           "ssm_embedding_bwd", "ssm_grad_norm_workspace_size", "ssm_grad_norm", "ssm_adamw_step",
+           "ssm_embedding_bwd", "ssm_grad_norm_workspace_size", "ssm_grad_norm", "ssm_adamw_step", "ssm_adamw_clipped_step",
            "ssm_adamw_state_values")
 
 
@@ -110,6 +110,9 @@ def load() -> ctypes.CDLL:
     lib.ssm_grad_norm.restype = ctypes.c_int
     lib.ssm_adamw_step.argtypes = [ctypes.POINTER(ssm_adamw_config), vp, i64] + [vp] * 7
     lib.ssm_adamw_step.restype = ctypes.c_int
+    lib.ssm_adamw_clipped_step.argtypes = ([ctypes.POINTER(ssm_adamw_config), vp, i64, ctypes.c_double] + [vp] * 8
+                                           + [ctypes.c_size_t, vp])
+    lib.ssm_adamw_clipped_step.restype = ctypes.c_int
     lib.ssm_adamw_state_values.argtypes = [i64] + [vp] * 7
     lib.ssm_adamw_state_values.restype = ctypes.c_int
     if lib.ssm_abi_version() != ABI_VERSION:

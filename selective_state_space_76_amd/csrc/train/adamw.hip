@@ -181,16 +181,22 @@ template <bool PB, bool GB, bool MW, bool S8>
 __global__ __launch_bounds__(256) void adamw_kernel(AdamTable t, AdamParams a) {
 #pragma clang fp contract(off)  // every product and sum of the states rounds once: the codes depend on their bits
   constexpr int V = S8 ? 8 : 4;
-  float clip = 1.0f;
-  if (a.clip) {
-    clip = a.clip[1];
-    if (clip != clip) return;  // the gradients' norm is not finite: nothing changes
-  }
   const int k = find(t, blockIdx.x);
+  float clip = 1.0f, isb = a.isb, size = a.step;
+  uint32_t key = t.key[k];
+  if (a.progress) {
+    const AdamProgress now = *a.progress;
+    clip = now.factor;
+    isb = now.isb;
+    size = now.size;
+    key = mix32(now.key + key);
+  } else if (a.clip) {
+    clip = a.clip[1];
+  }
+  if (clip != clip) return;  // the gradients' norm is not finite: nothing changes
   const int64_t n = t.n[k], off = t.off[k];
   // the wave's first element
   const int64_t base = (int64_t)(blockIdx.x - t.first[k]) * kAdamChunk + (threadIdx.x & ~63) * V;
-  const uint32_t key = t.key[k];
 #pragma unroll 1
   for (int it = 0; it < kAdamChunk / (256 * V); ++it) {
     const int64_t w0 = base + it * (256 * V);
@@ -249,8 +255,8 @@ __global__ __launch_bounds__(256) void adamw_kernel(AdamTable t, AdamParams a) {
       const float ge = g[e] * clip;
       m[e] = m[e] * a.b1 + ge * a.c1;
       v[e] = v[e] * a.b2 + ge * a.c2 * ge;
-      const float den = __builtin_fmaf(__builtin_amdgcn_sqrtf(v[e]), a.isb, a.eps);
-      p[e] = __builtin_fmaf(-(m[e] * a.step), rcp_(den), p[e] * a.decay);
+      const float den = __builtin_fmaf(__builtin_amdgcn_sqrtf(v[e]), isb, a.eps);
+      p[e] = __builtin_fmaf(-(m[e] * size), rcp_(den), p[e] * a.decay);
       if constexpr (PB) {
         if constexpr (MW) {
           pb[e] = (uint32_t)__builtin_bit_cast(uint16_t, (__bf16)p[e]) << 16;
@@ -382,8 +388,32 @@ __global__ __launch_bounds__(256) void norm_part_kernel(NormTable t, double* par
   if (threadIdx.x == 0) part[blockIdx.x] = sm[0];
 }
 
-// The sum of a workgroup's 1024 lanes in a fixed tree, and from it the result.
-__device__ __forceinline__ void finish_norm(double s, double* sm, double max_norm, float* result) {
+// x^n by squaring: within n units of the last place of 1, which 1 - x^n is then right to
+__device__ __forceinline__ double power(double x, int64_t n) {
+  double r = 1.0;
+  for (; n > 0; n >>= 1) {
+    if (n & 1) r *= x;
+    x *= x;
+  }
+  return r;
+}
+
+// What the next step takes, by the first wave while it waits for its gradients.
+struct Next {
+  AdamProgress p;
+  __device__ __forceinline__ explicit Next(const AdamAdvance& a) {
+    if (!a.progress || threadIdx.x >= 64) return;
+    p.step = a.progress->step + 1;
+    p.size = (float)(a.lr / (1.0 - power(a.b1, p.step)));
+    p.isb = (float)(1.0 / sqrt(1.0 - power(a.b2, p.step)));
+    p.key = mix32(a.seed + (uint32_t)p.step);
+  }
+};
+
+// The sum of a workgroup's 1024 lanes in a fixed tree, and from it the result: result[0] the norm and result[1] the
+// factor, or with progress the norm alone.
+__device__ __forceinline__ void finish_norm(double s, double* sm, double max_norm, float* result, const AdamAdvance& adv,
+                                            const Next& next) {
   sm[threadIdx.x] = s;
   __syncthreads();
   for (int h = 512; h > 0; h >>= 1) {
@@ -394,14 +424,26 @@ __device__ __forceinline__ void finish_norm(double s, double* sm, double max_nor
     const double norm = sqrt(sm[0]);
     const float out = (float)norm;
     const bool finite = (__float_as_uint(out) & 0x7f800000u) != 0x7f800000u;
+    const float factor = !finite ? __uint_as_float(0x7fc00000u) : norm > max_norm ? (float)(max_norm / norm) : 1.0f;
     result[0] = out;
-    result[1] = !finite ? __uint_as_float(0x7fc00000u) : norm > max_norm ? (float)(max_norm / norm) : 1.0f;
+    if (!adv.progress) {
+      result[1] = factor;
+    } else if (finite) {
+      adv.progress->step = next.p.step;
+      adv.progress->factor = factor;
+      adv.progress->size = next.p.size;
+      adv.progress->isb = next.p.isb;
+      adv.progress->key = next.p.key;
+    } else {
+      adv.progress->factor = factor;  // and the step is not counted
+    }
   }
 }
 
-__global__ __launch_bounds__(1024) void norm_join_kernel(const double* part, int64_t n, double max_norm,
-                                                         float* result) {
+__global__ __launch_bounds__(1024) void norm_join_kernel(const double* part, int64_t n, double max_norm, float* result,
+                                                         AdamAdvance adv) {
   __shared__ double sm[1024];
+  const Next next(adv);
   double s = 0.0;
   int64_t i = threadIdx.x;
   for (; i + 7 * 1024 < n; i += 8 * 1024) {
@@ -412,7 +454,7 @@ __global__ __launch_bounds__(1024) void norm_join_kernel(const double* part, int
     for (int e = 0; e < 8; ++e) s += x[e];
   }
   for (; i < n; i += 1024) s += part[i];
-  finish_norm(s, sm, max_norm, result);
+  finish_norm(s, sm, max_norm, result, adv, next);
 }
 
 template <bool GB>
@@ -435,15 +477,16 @@ __device__ __forceinline__ double chunk_squares(const void* g, int64_t base, int
 
 // Few and small tensors: one workgroup, a wave per chunk, and no second launch.
 __global__ __launch_bounds__(1024) void norm_small_kernel(SmallNormTable t, uint32_t chunks, double max_norm,
-                                                          float* result) {
+                                                          float* result, AdamAdvance adv) {
   __shared__ double sm[1024];
+  const Next next(adv);
   double s = 0.0;
   for (uint32_t c = threadIdx.x >> 6; c < chunks; c += 16) {
     const int k = find(t, c);
     const int64_t base = (int64_t)(c - t.first[k]) * kSmallChunk;
     s += t.bf16[k] ? chunk_squares<true>(t.g[k], base, t.n[k]) : chunk_squares<false>(t.g[k], base, t.n[k]);
   }
-  finish_norm(s, sm, max_norm, result);
+  finish_norm(s, sm, max_norm, result, adv, next);
 }
 
 // (c + K) << 20 has its set bits in the upper half: the value in bf16 is (c + K) << 4, exactly
@@ -472,11 +515,13 @@ __global__ __launch_bounds__(256) void state_values_kernel(int64_t n, const uint
   }
 }
 
+uint32_t adam_seed(uint64_t seed) {
+  const uint32_t x = mix32((uint32_t)seed);
+  return seed >> 32 ? mix32(x + (uint32_t)(seed >> 32)) : x;
+}
+
 uint32_t adam_key(uint64_t seed, int64_t step, int64_t tensor) {
-  uint32_t x = mix32((uint32_t)seed);
-  if (seed >> 32) x = mix32(x + (uint32_t)(seed >> 32));
-  x = mix32(x + (uint32_t)step);
-  return mix32(x + (uint32_t)tensor);
+  return mix32(mix32(adam_seed(seed) + (uint32_t)step) + (uint32_t)tensor);
 }
 
 hipError_t launch_adamw(const AdamTable& t, const AdamParams& p, int kind, uint32_t blocks, hipStream_t s) {
@@ -505,13 +550,15 @@ hipError_t launch_norm_part(const NormTable& t, double* part, bool bf16, uint32_
   return hipGetLastError();
 }
 
-hipError_t launch_norm_small(const SmallNormTable& t, uint32_t chunks, double max_norm, float* result, hipStream_t s) {
-  hipLaunchKernelGGL(norm_small_kernel, dim3(1), dim3(1024), 0, s, t, chunks, max_norm, result);
+hipError_t launch_norm_small(const SmallNormTable& t, uint32_t chunks, double max_norm, float* result,
+                             const AdamAdvance& adv, hipStream_t s) {
+  hipLaunchKernelGGL(norm_small_kernel, dim3(1), dim3(1024), 0, s, t, chunks, max_norm, result, adv);
   return hipGetLastError();
 }
 
-hipError_t launch_norm_join(const double* part, int64_t n, double max_norm, float* result, hipStream_t s) {
-  hipLaunchKernelGGL(norm_join_kernel, dim3(1), dim3(1024), 0, s, part, n, max_norm, result);
+hipError_t launch_norm_join(const double* part, int64_t n, double max_norm, float* result, const AdamAdvance& adv,
+                            hipStream_t s) {
+  hipLaunchKernelGGL(norm_join_kernel, dim3(1), dim3(1024), 0, s, part, n, max_norm, result, adv);
   return hipGetLastError();
 }
 

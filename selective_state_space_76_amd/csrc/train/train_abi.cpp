@@ -223,10 +223,13 @@ bool params_clash(const ssm_adamw_tensor* t, int64_t count) {
   for (int64_t b = 0; b < count; b += kBlock) {
     const int64_t n = count - b < kBlock ? count - b : kBlock;
     for (int64_t i = 0; i < n; ++i) r[i] = param(b + i);
-    std::sort(r, r + n, [](const Range& x, const Range& y) { return x.lo < y.lo; });
+    auto before = [](const Range& x, const Range& y) { return x.lo < y.lo; };
+    if (!std::is_sorted(r, r + n, before)) std::sort(r, r + n, before);
     for (int64_t i = 1; i < n; ++i)
       if (overlaps(r[i - 1], r[i])) return true;
-    auto hit = [&](Range q) {  // the first that ends behind q's beginning: the only one before those behind q
+    auto hit = [&](Range q) {
+      if (q.hi <= r[0].lo || q.lo >= r[n - 1].hi) return false;
+      // the first that ends behind q's beginning: the only one before those behind q
       const Range* f = std::partition_point(r, r + n, [&](const Range& x) { return x.hi <= q.lo; });
       return f < r + n && overlaps(*f, q);
     };
@@ -265,6 +268,122 @@ hipError_t in_tables(const ssm_adamw_tensor* t, int64_t count, int64_t chunk, Ta
   return hipSuccess;
 }
 
+// (after check_tensors) what the norm's calls ask for; the result takes `result_bytes`
+ssm_status check_norm(const ssm_adamw_tensor* tensors, int64_t count, double max_norm, float* result,
+                      int64_t result_bytes, void* workspace, size_t workspace_bytes) {
+  if (!result || !workspace) return SSM_ERR_NULL;
+  if (!(max_norm > 0)) return SSM_ERR_UNSUPPORTED;
+  if (misaligned(workspace) || (reinterpret_cast<uintptr_t>(result) & 3u)) return SSM_ERR_ALIGN;
+  const size_t need = ssm_grad_norm_workspace_size(tensors, count);
+  if (workspace_bytes < need) return SSM_ERR_WORKSPACE;
+  const Range outs[] = {span(result, result_bytes), span(workspace, (int64_t)need)};
+  if (overlaps(outs[0], outs[1])) return SSM_ERR_OVERLAP;
+  for (int64_t k = 0; k < count; ++k) {
+    const Range g = span(tensors[k].grad, tensors[k].numel * dtype_size(tensors[k].grad_dtype));
+    if (overlaps(outs[0], g) || overlaps(outs[1], g)) return SSM_ERR_OVERLAP;
+  }
+  return SSM_OK;
+}
+
+ssm_status launch_norm(const ssm_adamw_tensor* tensors, int64_t count, double max_norm, float* result, void* workspace,
+                       const ssm::AdamAdvance& adv, hipStream_t st) {
+  int64_t chunks = 0;
+  for (int64_t k = 0; k < count && chunks <= ssm::kSmallChunks; ++k)
+    chunks += chunks_of(tensors[k].numel, ssm::kSmallChunk);
+  if (count <= ssm::kSmallTensors && chunks <= ssm::kSmallChunks) {
+    ssm::SmallNormTable t;
+    uint32_t first = 0;
+    for (int k = 0; k < (int)count; ++k) {
+      t.g[k] = tensors[k].grad;
+      t.n[k] = tensors[k].numel;
+      t.first[k] = first;
+      t.bf16[k] = tensors[k].grad_dtype == SSM_BF16;
+      first += (uint32_t)chunks_of(tensors[k].numel, ssm::kSmallChunk);
+    }
+    t.count = (int)count;
+    return launch_status(ssm::launch_norm_small(t, first, max_norm, result, adv, st));
+  }
+  double* part = static_cast<double*>(workspace);
+  int64_t done = 0;
+  for (int b = 0; b < 2; ++b) {
+    const hipError_t e = in_tables<ssm::NormTable, ssm::kNormTensors>(
+        tensors, count, ssm::kNormChunk,
+        [&](const ssm_adamw_tensor& t) { return (t.grad_dtype == SSM_BF16) == (b == 1); },
+        [](ssm::NormTable&, int, int64_t) {},
+        [&](const ssm::NormTable& tab, uint32_t blocks) {
+          const hipError_t r = ssm::launch_norm_part(tab, part + done, b == 1, blocks, st);
+          done += blocks;
+          return r;
+        });
+    if (e != hipSuccess) return SSM_ERR_LAUNCH;
+  }
+  return launch_status(ssm::launch_norm_join(part, done, max_norm, result, adv, st));
+}
+
+// what both step calls ask for, but for the step's number; `given`: what the step reads besides, `given_bytes` of it.
+// *a gets the buffers and the settings.
+ssm_status check_step(const ssm_adamw_config* c, const ssm_adamw_tensor* tensors, int64_t count, void* exp_avg,
+                      void* exp_avg_sq, int16_t* exp_avg_base, int16_t* exp_avg_sq_base, float* master,
+                      const void* given, int64_t given_bytes, ssm::AdamParams* a) {
+  if (c->flags || (c->state_bits != 32 && c->state_bits != 8)) return SSM_ERR_UNSUPPORTED;
+  if (!isfinite(c->lr) || !isfinite(c->weight_decay) || !finite_in(c->beta1, 0, 1) || !finite_in(c->beta2, 0, 1) ||
+      c->beta1 == 1 || c->beta2 == 1 || !finite_in(c->eps, 1e-30, 1e30))
+    return SSM_ERR_UNSUPPORTED;
+  int64_t elems;
+  const ssm_status rc = check_tensors(tensors, count, false, &elems);
+  if (rc != SSM_OK) return rc;
+  const bool s8 = c->state_bits == 8;
+  if (!exp_avg || !exp_avg_sq || (s8 && (!exp_avg_base || !exp_avg_sq_base))) return SSM_ERR_NULL;
+  if (!s8) exp_avg_base = exp_avg_sq_base = nullptr;
+  const void* ptrs[] = {exp_avg, exp_avg_sq, exp_avg_base, exp_avg_sq_base, master};
+  for (const void* q : ptrs)
+    if (misaligned(q)) return SSM_ERR_ALIGN;
+  if (reinterpret_cast<uintptr_t>(given) & 3u) return SSM_ERR_ALIGN;
+  const int64_t nb = elems / SSM_ADAMW_BLOCK;
+  const Range outs[] = {span(exp_avg, elems * (s8 ? 1 : 4)), span(exp_avg_sq, elems * (s8 ? 1 : 4)),
+                        span(exp_avg_base, nb * 2), span(exp_avg_sq_base, nb * 2), span(master, elems * 4)};
+  const Range ins[] = {span(given, given_bytes)};
+  if (any_overlap(outs, 5, ins, 1)) return SSM_ERR_OVERLAP;
+  for (int64_t k = 0; k < count; ++k) {
+    const Range p = span(tensors[k].param, tensors[k].numel * dtype_size(tensors[k].param_dtype));
+    const Range g = span(tensors[k].grad, tensors[k].numel * dtype_size(tensors[k].grad_dtype));
+    if (overlaps(p, ins[0])) return SSM_ERR_OVERLAP;
+    for (const Range& o : outs)
+      if (overlaps(o, p) || overlaps(o, g)) return SSM_ERR_OVERLAP;
+  }
+  if (params_clash(tensors, count)) return SSM_ERR_OVERLAP;
+
+  memset(a, 0, sizeof(*a));
+  a->m = exp_avg; a->v = exp_avg_sq; a->mb = exp_avg_base; a->vb = exp_avg_sq_base; a->master = master;
+  a->b1 = (float)c->beta1; a->c1 = (float)(1 - c->beta1);
+  a->b2 = (float)c->beta2; a->c2 = (float)(1 - c->beta2);
+  a->eps = (float)c->eps;
+  a->decay = (float)(1 - c->lr * c->weight_decay);
+  return SSM_OK;
+}
+
+ssm_status launch_step(const ssm_adamw_config* c, const ssm_adamw_tensor* tensors, int64_t count,
+                       const ssm::AdamParams& a, hipStream_t st) {
+  for (int kind = 0; kind < 8; ++kind) {  // bit 0 bf16 params, bit 1 bf16 gradients, bit 2 masters
+    const hipError_t e = in_tables<ssm::AdamTable, ssm::kAdamTensors>(
+        tensors, count, ssm::kAdamChunk,
+        [&](const ssm_adamw_tensor& t) {
+          const bool pb = t.param_dtype == SSM_BF16;
+          return kind == (pb ? 1 : 0) + (t.grad_dtype == SSM_BF16 ? 2 : 0) + (pb && a.master ? 4 : 0);
+        },
+        [&](ssm::AdamTable& tab, int i, int64_t k) {
+          tab.p[i] = tensors[k].param;
+          tab.off[i] = tensors[k].offset;
+          tab.key[i] = a.progress ? (uint32_t)k : ssm::adam_key(c->seed, c->step, k);
+        },
+        [&](const ssm::AdamTable& tab, uint32_t blocks) {
+          return ssm::launch_adamw(tab, a, kind + (c->state_bits == 8 ? 8 : 0), blocks, st);
+        });
+    if (e != hipSuccess) return SSM_ERR_LAUNCH;
+  }
+  return SSM_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -284,111 +403,64 @@ ssm_status ssm_grad_norm(const ssm_adamw_tensor* tensors, int64_t count, double 
   int64_t elems;
   const ssm_status rc = check_tensors(tensors, count, true, &elems);
   if (rc != SSM_OK) return rc;
-  if (!result || !workspace) return SSM_ERR_NULL;
-  if (!(max_norm > 0)) return SSM_ERR_UNSUPPORTED;
-  if (misaligned(workspace) || (reinterpret_cast<uintptr_t>(result) & 3u)) return SSM_ERR_ALIGN;
-  const size_t need = ssm_grad_norm_workspace_size(tensors, count);
-  if (workspace_bytes < need) return SSM_ERR_WORKSPACE;
-  const Range outs[] = {span(result, 8), span(workspace, (int64_t)need)};
-  if (overlaps(outs[0], outs[1])) return SSM_ERR_OVERLAP;
-  for (int64_t k = 0; k < count; ++k) {
-    const Range g = span(tensors[k].grad, tensors[k].numel * dtype_size(tensors[k].grad_dtype));
-    if (overlaps(outs[0], g) || overlaps(outs[1], g)) return SSM_ERR_OVERLAP;
-  }
-  hipStream_t st = reinterpret_cast<hipStream_t>(stream);
-  int64_t chunks = 0;
-  for (int64_t k = 0; k < count && chunks <= ssm::kSmallChunks; ++k)
-    chunks += chunks_of(tensors[k].numel, ssm::kSmallChunk);
-  if (count <= ssm::kSmallTensors && chunks <= ssm::kSmallChunks) {
-    ssm::SmallNormTable t;
-    uint32_t first = 0;
-    for (int k = 0; k < (int)count; ++k) {
-      t.g[k] = tensors[k].grad;
-      t.n[k] = tensors[k].numel;
-      t.first[k] = first;
-      t.bf16[k] = tensors[k].grad_dtype == SSM_BF16;
-      first += (uint32_t)chunks_of(tensors[k].numel, ssm::kSmallChunk);
-    }
-    t.count = (int)count;
-    return launch_status(ssm::launch_norm_small(t, first, max_norm, result, st));
-  }
-  double* part = static_cast<double*>(workspace);
-  int64_t done = 0;
-  for (int b = 0; b < 2; ++b) {
-    const hipError_t e = in_tables<ssm::NormTable, ssm::kNormTensors>(
-        tensors, count, ssm::kNormChunk,
-        [&](const ssm_adamw_tensor& t) { return (t.grad_dtype == SSM_BF16) == (b == 1); },
-        [](ssm::NormTable&, int, int64_t) {},
-        [&](const ssm::NormTable& tab, uint32_t blocks) {
-          const hipError_t r = ssm::launch_norm_part(tab, part + done, b == 1, blocks, st);
-          done += blocks;
-          return r;
-        });
-    if (e != hipSuccess) return SSM_ERR_LAUNCH;
-  }
-  return launch_status(ssm::launch_norm_join(part, done, max_norm, result, st));
+  const ssm_status rn = check_norm(tensors, count, max_norm, result, 8, workspace, workspace_bytes);
+  if (rn != SSM_OK) return rn;
+  return launch_norm(tensors, count, max_norm, result, workspace, ssm::AdamAdvance{},
+                     reinterpret_cast<hipStream_t>(stream));
 }
 
 ssm_status ssm_adamw_step(const ssm_adamw_config* c, const ssm_adamw_tensor* tensors, int64_t count, void* exp_avg,
                           void* exp_avg_sq, int16_t* exp_avg_base, int16_t* exp_avg_sq_base, float* master,
                           const float* clip, struct ihipStream_t* stream) {
   if (!c) return SSM_ERR_NULL;
-  if (c->flags || (c->state_bits != 32 && c->state_bits != 8)) return SSM_ERR_UNSUPPORTED;
-  if (!isfinite(c->lr) || !isfinite(c->weight_decay) || !finite_in(c->beta1, 0, 1) || !finite_in(c->beta2, 0, 1) ||
-      c->beta1 == 1 || c->beta2 == 1 || !finite_in(c->eps, 1e-30, 1e30) || c->step < 1)
-    return SSM_ERR_UNSUPPORTED;
-  int64_t elems;
-  const ssm_status rc = check_tensors(tensors, count, false, &elems);
-  if (rc != SSM_OK) return rc;
-  const bool s8 = c->state_bits == 8;
-  if (!exp_avg || !exp_avg_sq || (s8 && (!exp_avg_base || !exp_avg_sq_base))) return SSM_ERR_NULL;
-  if (!s8) exp_avg_base = exp_avg_sq_base = nullptr;
-  const void* ptrs[] = {exp_avg, exp_avg_sq, exp_avg_base, exp_avg_sq_base, master};
-  for (const void* q : ptrs)
-    if (misaligned(q)) return SSM_ERR_ALIGN;
-  if (reinterpret_cast<uintptr_t>(clip) & 3u) return SSM_ERR_ALIGN;
-  const int64_t nb = elems / SSM_ADAMW_BLOCK;
-  const Range outs[] = {span(exp_avg, elems * (s8 ? 1 : 4)), span(exp_avg_sq, elems * (s8 ? 1 : 4)),
-                        span(exp_avg_base, nb * 2), span(exp_avg_sq_base, nb * 2), span(master, elems * 4)};
-  const Range ins[] = {span(clip, 8)};
-  if (any_overlap(outs, 5, ins, 1)) return SSM_ERR_OVERLAP;
-  for (int64_t k = 0; k < count; ++k) {
-    const Range p = span(tensors[k].param, tensors[k].numel * dtype_size(tensors[k].param_dtype));
-    const Range g = span(tensors[k].grad, tensors[k].numel * dtype_size(tensors[k].grad_dtype));
-    if (overlaps(p, ins[0])) return SSM_ERR_OVERLAP;
-    for (const Range& o : outs)
-      if (overlaps(o, p) || overlaps(o, g)) return SSM_ERR_OVERLAP;
-  }
-  if (params_clash(tensors, count)) return SSM_ERR_OVERLAP;
-
+  if (c->step < 1) return SSM_ERR_UNSUPPORTED;
   ssm::AdamParams a;
-  memset(&a, 0, sizeof(a));
-  a.m = exp_avg; a.v = exp_avg_sq; a.mb = exp_avg_base; a.vb = exp_avg_sq_base; a.master = master; a.clip = clip;
-  a.b1 = (float)c->beta1; a.c1 = (float)(1 - c->beta1);
-  a.b2 = (float)c->beta2; a.c2 = (float)(1 - c->beta2);
-  a.eps = (float)c->eps;
+  const ssm_status rc = check_step(c, tensors, count, exp_avg, exp_avg_sq, exp_avg_base, exp_avg_sq_base, master, clip,
+                                   8, &a);
+  if (rc != SSM_OK) return rc;
+  a.clip = clip;
   a.isb = (float)(1 / sqrt(1 - pow(c->beta2, (double)c->step)));
   a.step = (float)(c->lr / (1 - pow(c->beta1, (double)c->step)));
-  a.decay = (float)(1 - c->lr * c->weight_decay);
-  hipStream_t st = reinterpret_cast<hipStream_t>(stream);
-  for (int kind = 0; kind < 8; ++kind) {  // bit 0 bf16 params, bit 1 bf16 gradients, bit 2 masters
-    const hipError_t e = in_tables<ssm::AdamTable, ssm::kAdamTensors>(
-        tensors, count, ssm::kAdamChunk,
-        [&](const ssm_adamw_tensor& t) {
-          const bool pb = t.param_dtype == SSM_BF16;
-          return kind == (pb ? 1 : 0) + (t.grad_dtype == SSM_BF16 ? 2 : 0) + (pb && master ? 4 : 0);
-        },
-        [&](ssm::AdamTable& tab, int i, int64_t k) {
-          tab.p[i] = tensors[k].param;
-          tab.off[i] = tensors[k].offset;
-          tab.key[i] = ssm::adam_key(c->seed, c->step, k);
-        },
-        [&](const ssm::AdamTable& tab, uint32_t blocks) {
-          return ssm::launch_adamw(tab, a, kind + (s8 ? 8 : 0), blocks, st);
-        });
-    if (e != hipSuccess) return SSM_ERR_LAUNCH;
+  return launch_step(c, tensors, count, a, reinterpret_cast<hipStream_t>(stream));
+}
+
+ssm_status ssm_adamw_clipped_step(const ssm_adamw_config* c, const ssm_adamw_tensor* tensors, int64_t count,
+                                  double max_norm, void* exp_avg, void* exp_avg_sq, int16_t* exp_avg_base,
+                                  int16_t* exp_avg_sq_base, float* master, ssm_adamw_progress* progress, float* norm,
+                                  void* workspace, size_t workspace_bytes, struct ihipStream_t* stream) {
+  static_assert(sizeof(ssm::AdamProgress) == sizeof(ssm_adamw_progress), "one struct in two places");
+  if (!c || !progress) return SSM_ERR_NULL;
+  ssm::AdamParams a;
+  ssm_status rc = check_step(c, tensors, count, exp_avg, exp_avg_sq, exp_avg_base, exp_avg_sq_base, master, progress,
+                             (int64_t)sizeof(*progress), &a);
+  if (rc != SSM_OK) return rc;
+  rc = check_norm(tensors, count, max_norm, norm, 4, workspace, workspace_bytes);
+  if (rc != SSM_OK) return rc;
+  if (misaligned(progress)) return SSM_ERR_ALIGN;
+  const int64_t bytes = (int64_t)ssm_grad_norm_workspace_size(tensors, count);
+  const Range own[] = {span(norm, 4), span(workspace, bytes), span(progress, (int64_t)sizeof(*progress))};
+  if (any_overlap(own, 3, nullptr, 0)) return SSM_ERR_OVERLAP;
+  const int64_t elems = tensors[count - 1].offset + chunks_of(tensors[count - 1].numel, SSM_ADAMW_BLOCK) * SSM_ADAMW_BLOCK;
+  const int64_t es = c->state_bits == 8 ? 1 : 4, nb = elems / SSM_ADAMW_BLOCK * 2;
+  const Range states[] = {span(a.m, elems * es), span(a.v, elems * es), span(a.mb, nb), span(a.vb, nb),
+                          span(a.master, elems * 4)};
+  for (int i = 0; i < 2; ++i) {
+    for (const Range& q : states)
+      if (overlaps(own[i], q)) return SSM_ERR_OVERLAP;
+    for (int64_t k = 0; k < count; ++k)
+      if (overlaps(own[i], span(tensors[k].param, tensors[k].numel * dtype_size(tensors[k].param_dtype))))
+        return SSM_ERR_OVERLAP;
   }
-  return SSM_OK;
+  for (int64_t k = 0; k < count; ++k)
+    if (overlaps(own[2], span(tensors[k].grad, tensors[k].numel * dtype_size(tensors[k].grad_dtype))))
+      return SSM_ERR_OVERLAP;
+
+  a.progress = reinterpret_cast<ssm::AdamProgress*>(progress);
+  const ssm::AdamAdvance adv{reinterpret_cast<ssm::AdamProgress*>(progress), c->lr, c->beta1, c->beta2,
+                             ssm::adam_seed(c->seed)};
+  hipStream_t st = reinterpret_cast<hipStream_t>(stream);
+  rc = launch_norm(tensors, count, max_norm, norm, workspace, adv, st);
+  return rc != SSM_OK ? rc : launch_step(c, tensors, count, a, st);
 }
 
 ssm_status ssm_adamw_state_values(int64_t numel, const void* exp_avg, const void* exp_avg_sq,

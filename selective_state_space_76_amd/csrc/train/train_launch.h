@@ -62,6 +62,21 @@ struct SmallNormTable {
   int count;
 };
 
+// A clipped step's numbers, on the device: the last kernel of the norm counts the step and writes them, where the norm
+// is finite; the step's own kernels read them.  (struct ssm_adamw_progress.)
+struct AdamProgress {
+  int64_t step;             // steps made
+  float factor;             // of the gradients; NaN: nothing changes
+  float size, isb;          // lr / (1 - b1^step), 1 / sqrt(1 - b2^step)
+  uint32_t key;             // hash of seed and step
+  uint32_t unused[2];
+};
+struct AdamAdvance {
+  AdamProgress* progress;   // null: the norm alone
+  double lr, b1, b2;
+  uint32_t seed;            // hashed
+};
+
 struct AdamParams {
   void* m;
   void* v;
@@ -69,16 +84,20 @@ struct AdamParams {
   int16_t* vb;
   float* master;
   const float* clip;   // {norm, factor} or null
+  const AdamProgress* progress;  // or null: then clip and what follows; with it a table's keys are the tensors' numbers
   float b1, c1, b2, c2, eps, isb, step, decay;
 };
 
 // of a tensor: a hash of the seed, the step and its place in the list
 uint32_t adam_key(uint64_t seed, int64_t step, int64_t tensor);
+uint32_t adam_seed(uint64_t seed);  // its part that is of the seed
 // kind: bit 0 bf16 params, bit 1 bf16 gradients, bit 2 master weights, bit 3 8-bit states
 hipError_t launch_adamw(const AdamTable& t, const AdamParams& p, int kind, uint32_t blocks, hipStream_t s);
 hipError_t launch_norm_part(const NormTable& t, double* part, bool bf16, uint32_t blocks, hipStream_t s);
-hipError_t launch_norm_small(const SmallNormTable& t, uint32_t chunks, double max_norm, float* result, hipStream_t s);
-hipError_t launch_norm_join(const double* part, int64_t n, double max_norm, float* result, hipStream_t s);
+hipError_t launch_norm_small(const SmallNormTable& t, uint32_t chunks, double max_norm, float* result,
+                             const AdamAdvance& adv, hipStream_t s);
+hipError_t launch_norm_join(const double* part, int64_t n, double max_norm, float* result, const AdamAdvance& adv,
+                            hipStream_t s);
 hipError_t launch_state_values(int64_t n, const void* m, const void* v, const int16_t* mb, const int16_t* vb,
                                void* mo, void* vo, hipStream_t s);
 

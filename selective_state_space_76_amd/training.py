@@ -195,7 +195,7 @@ class AdamW:
     master_weights: fp32 copies of the bf16 parameters, on which the step works; without them a bf16 parameter is
         rounded stochastically (to nearest, updates under half a unit would be lost).
     max_grad_norm: scale the gradients so that their norm over all tensors is at most this; a step whose
-        norm is not finite changes nothing.
+        norm is not finite changes nothing and is not counted.
     seed: of the stochastic rounding (a hash of seed, step, tensor and element: the same on every run).
     (The number of the step is an argument of the kernels: a step captured in a graph repeats its bias correction and
     random numbers with every replay.)
@@ -212,7 +212,7 @@ class AdamW:
             raise ValueError("state_bits must be 8 or 32, got %r" % (state_bits,))
         self.lr, self.betas, self.eps, self.weight_decay = lr, tuple(betas), eps, weight_decay
         self.state_bits, self.max_grad_norm = state_bits, max_grad_norm
-        self.seed, self.step_count = int(seed), int(step)
+        self.seed = int(seed)
         self.device = self.params[0].device
         for p in self.params:
             _io_dtype(p)
@@ -244,6 +244,11 @@ class AdamW:
         if set(given) - set(want):
             raise ValueError("state: %s not expected here" % ", ".join(sorted(set(given) - set(want))))
         self.state = {}
+        # With max_grad_norm the device counts the steps, which of them it leaves out is known only there; else _count.
+        self._progress = torch.zeros(4, dtype=torch.int64, device=self.device)  # struct ssm_adamw_progress
+        self._count = int(step)
+        if max_grad_norm is not None:
+            self._count_on_device(None)
         for k, (size, dt) in want.items():
             t = given.get(k)
             if t is None:
@@ -254,6 +259,19 @@ class AdamW:
             _expect(t, (size,), dt, k, self.device)
             _ptr(t)
             self.state[k] = t
+
+    @property
+    def step_count(self):
+        """The number of steps made.  With max_grad_norm this waits for the GPU."""
+        if self._count is not None:
+            return self._count
+        torch.cuda.synchronize(self.device)
+        return int(self._progress[0])
+
+    def _count_on_device(self, stream):
+        with torch.cuda.stream(stream):
+            self._progress[:1].fill_(self._count)
+        self._count = None
 
     def state_dict(self):
         """The state tensors and the number of steps made: AdamW(params, **settings, **state_dict) goes on from here."""
@@ -271,9 +289,8 @@ class AdamW:
 
     def _used_on(self, stream):
         """The states were made on the stream that was current at construction; the allocator has to know of this one."""
-        if stream is not None:
-            for t in self.state.values():
-                t.record_stream(stream)
+        for t in (self._progress, *self.state.values()):
+            t.record_stream(stream)
 
     def step(self, grads=None, *, stream=None):
         """One step with the gradients given (fp32 or bf16, the parameters' shapes), by default each parameter's
@@ -306,26 +323,31 @@ class AdamW:
                 and (self.max_grad_norm is None or self.max_grad_norm > 0)):
             raise ValueError("lr %r, betas %r, eps %r, weight_decay %r, max_grad_norm %r: out of range"
                              % (self.lr, self.betas, self.eps, self.weight_decay, self.max_grad_norm))
-        rows, count = table.ctypes.data, len(table)
-        s, norm, clip = _stream(stream, self.device), None, None
-        if self.max_grad_norm is not None:
-            need = int(lib.ssm_grad_norm_workspace_size(rows, count))
-            clip = _empty(2, torch.float32, self.device, stream)
-            workspace = _empty(need, torch.uint8, self.device, stream)
-            _check(lib.ssm_grad_norm(rows, count, float(self.max_grad_norm), _address(clip), _address(workspace), need,
-                                     s))
-            norm = clip[0]
-        cfg = ssm_adamw_config(self.lr, self.betas[0], self.betas[1], self.eps, self.weight_decay, self.step_count + 1,
+        rows, count, s, st, norm = table.ctypes.data, len(table), _stream(stream, self.device), self.state, None
+        get = st.get
+        states = (_address(st["exp_avg"]), _address(st["exp_avg_sq"]), _address(get("exp_avg_base")),
+                  _address(get("exp_avg_sq_base")), _address(get("master")))
+        cfg = ssm_adamw_config(self.lr, self.betas[0], self.betas[1], self.eps, self.weight_decay, 0,
                                self.seed & (2 ** 64 - 1), self.state_bits, 0)
-        st = self.state
-        _check(lib.ssm_adamw_step(ctypes.byref(cfg), rows, count, _address(st["exp_avg"]), _address(st["exp_avg_sq"]),
-                                  _address(st.get("exp_avg_base")), _address(st.get("exp_avg_sq_base")),
-                                  _address(st.get("master")), _address(clip), s))
-        self.step_count += 1
+        if self.max_grad_norm is not None:
+            if self._count is not None:
+                self._count_on_device(stream)
+            norm = _empty((), torch.float32, self.device, stream)
+            need = int(lib.ssm_grad_norm_workspace_size(rows, count))
+            workspace = _empty(need, torch.uint8, self.device, stream)
+            _check(lib.ssm_adamw_clipped_step(ctypes.byref(cfg), rows, count, float(self.max_grad_norm), *states,
+                                              _address(self._progress), _address(norm), _address(workspace), need, s))
+        else:
+            if self._count is None:
+                self._count = self.step_count
+            cfg.step = self._count + 1
+            _check(lib.ssm_adamw_step(ctypes.byref(cfg), rows, count, *states, None, s))
+            self._count += 1
         # a graph that has kept a parameter for its backward pass must be refused from now on
-        increment_version([p for p, h in zip(self.params, have) if h])
-        self._used_on(stream)
-        _hand_out(stream, clip)
+        increment_version(self.params if all(have) else [p for p, h in zip(self.params, have) if h])
+        if stream is not None:
+            self._used_on(stream)
+            _hand_out(stream, norm)
         return norm
 
     def state_values(self, *, stream=None):
@@ -339,6 +361,7 @@ class AdamW:
         _check(load().ssm_adamw_state_values(self.numel, _address(st["exp_avg"]), _address(st["exp_avg_sq"]),
                                              _address(st["exp_avg_base"]), _address(st["exp_avg_sq_base"]), _address(m),
                                              _address(v), _stream(stream, self.device)))
-        self._used_on(stream)
-        _hand_out(stream, m, v)
+        if stream is not None:
+            self._used_on(stream)
+            _hand_out(stream, m, v)
         return m, v

@@ -125,3 +125,73 @@ def test_8bit_neighbours_of_an_infinite_gradient(pt, gt, bad):
             tol = tol + np.exp2(np.floor(np.log2(np.maximum(np.abs(ref), 1e-30))) - 7) * 1.01
         assert (np.abs(f64(p) - ref)[~lost] <= tol[~lost]).all()
         assert np.array_equal(np.isnan(f64(p)), np.isnan(f64(exact.params[0])))
+
+
+SIZES = [(1,), (127,), (129,), (5, 7, 3), (8193,), (40, 1007)]
+
+
+def set_of(dtypes, seed, mul):
+    g = torch.Generator().manual_seed(seed)
+    return [(torch.randn(s, generator=g) * mul).to(dtypes[k % len(dtypes)]).to(DEV) for k, s in enumerate(SIZES)]
+
+
+def same(a, b):
+    return (a.step_count == b.step_count and all(torch.equal(x, y) for x, y in zip(a.params, b.params))
+            and all(torch.equal(a.state[k], b.state[k]) for k in a.state))
+
+
+@pytest.mark.parametrize("bits,master", [(32, True), (32, False), (8, True), (8, False)])
+@pytest.mark.parametrize("many", [False, True], ids=["one launch of the norm", "several"])
+def test_a_skipped_step_is_not_counted(bits, master, many):
+    """A run that meets gradients that are not finite goes on as one that never saw them, from its first step on."""
+    params = set_of([BF16, F32], 1, 0.1)
+    if many:
+        params.append(torch.randn(300000, generator=torch.Generator().manual_seed(9)).to(DEV))
+    k = dict(lr=3e-3, betas=(0.9, 0.99), weight_decay=0.1, state_bits=bits, master_weights=master, max_grad_norm=1.0, seed=3)
+    a, b = AdamW([p.clone() for p in params], **k), AdamW([p.clone() for p in params], **k)
+    for s, bad in enumerate((float("inf"), None, float("nan"), None, None)):
+        print("case: adamw, skipped steps", bits, master, many, bad, flush=True)
+        g = [torch.randn(p.shape, generator=torch.Generator().manual_seed(50 * s + i)).to(p.dtype).to(DEV)
+             for i, p in enumerate(params)]
+        if bad is not None:
+            g[-1].view(-1)[77] = bad
+            assert not torch.isfinite(a.step(g))
+            continue
+        assert torch.isfinite(a.step(g)) and torch.isfinite(b.step(g))
+        assert same(a, b)
+    assert a.step_count == 3 and a.state_dict()["step"] == 3
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_counting_on_either_side_is_the_same(bits):
+    """A limit that no norm reaches: the states are those of steps without one, bit for bit, the parameters but for the
+    last bit of the step's size; and the limit may come and go."""
+    params = set_of([F32], 2, 0.1)
+    k = dict(lr=3e-3, betas=(0.9, 0.99), weight_decay=0.1, state_bits=bits, seed=(5 << 32) + 3, step=1000)
+    a, b, c = (AdamW([p.clone() for p in params], max_grad_norm=n, **k) for n in (None, float("inf"), None))
+    for s in range(4):
+        print("case: adamw, counted on the host and on the device", bits, s, flush=True)
+        g = set_of([F32, BF16], 60 + s, 0.01)
+        c.max_grad_norm = float("inf") if s % 2 else None
+        for opt in (a, b, c):
+            opt.step(g)
+        for opt in (b, c):
+            assert opt.step_count == a.step_count == 1001 + s
+            assert all(torch.equal(opt.state[k], a.state[k]) for k in a.state)
+            for p, q in zip(opt.params, a.params):  # (1 + s) updates of up to lr, each right to a few units
+                assert ((p - q).abs() <= (1 + s) * (4 * 2.0 ** -24 * 3e-3 * 10 + 2.0 ** -24 * q.abs())).all()
+
+
+@pytest.mark.parametrize("step", [0, 1, 9, 999, 123456, (1 << 31) + 5])
+def test_the_step_size_from_the_device(step):
+    """One step with known moments, far into a run."""
+    b1, b2, lr = 0.9, 0.9995, 0.25
+    p = torch.zeros(256, device=DEV)
+    m, v = torch.full((256,), 0.5, device=DEV), torch.full((256,), 0.25, device=DEV)
+    opt = AdamW([p], lr=lr, betas=(b1, b2), eps=1e-8, weight_decay=0.0, max_grad_norm=1e9, step=step,
+                state={"exp_avg": m, "exp_avg_sq": v})
+    opt.step([torch.full((256,), 0.5, device=DEV)])
+    want = -lr * 0.5 / -np.expm1((step + 1) * np.log(b1)) / (0.5 / np.sqrt(-np.expm1((step + 1) * np.log(b2))) + 1e-8)
+    # moments, root, reciprocal, products and the two factors: some units each
+    assert np.abs(f64(p) / want - 1).max() <= 16 * 2.0 ** -24
+    assert opt.step_count == step + 1

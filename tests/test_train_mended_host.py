@@ -96,3 +96,53 @@ def test_a_step_is_an_in_place_change(unplugged, clip):
     other.backward()  # without a gradient it was left out, and is what it was
     opt.step([torch.ones(300)] * 2)
     assert (p._version, q._version) == (2, 1)
+
+
+def clipped(t=None, c=None, max_norm=1.0, count=None, m=fake(1), v=fake(2), mb=None, vb=None, master=None, progress=fake(3),
+            norm=fake(4), work=fake(5), ws=1 << 20):
+    t = rows({}, {}) if t is None else t
+    return L.load().ssm_adamw_clipped_step(ctypes.byref(c or cfg()), t.ctypes.data, len(t) if count is None else count,
+                                           max_norm, m, v, mb, vb, master, progress, norm, work, ws, None)
+
+
+def test_clipped_step_refusals():
+    good = rows({}, {})
+    assert L.load().ssm_adamw_clipped_step(None, good.ctypes.data, 2, 1.0, fake(1), fake(2), None, None, None, fake(3),
+                                           fake(4), fake(5), 1 << 20, None) == 1
+    for k in ("m", "v", "progress", "norm", "work"):
+        assert clipped(**{k: None}) == 1, k
+    assert clipped(c=cfg(state_bits=8)) == 1 and clipped(rows(dict(grad=0))) == 1 and clipped(rows(dict(param=0))) == 1
+    assert clipped(count=0) == 2 and clipped(rows(dict(numel=0))) == 2 and clipped(rows({}, dict(offset=256))) == 2
+    assert clipped(rows(dict(param_dtype=2))) == 3 and clipped(rows(dict(grad_dtype=-1))) == 3
+    for k in ("m", "v", "master", "progress", "work"):
+        assert clipped(**{k: fake(6, 8)}) == 4, k
+    assert clipped(norm=fake(4, 2)) == 4 and clipped(rows(dict(grad=fake(11).value + 8))) == 4
+    for bad in (dict(state_bits=16), dict(flags=1), dict(lr=float("nan")), dict(beta1=1.0), dict(eps=0.0)):
+        assert clipped(c=cfg(**bad)) == 5, bad
+    assert clipped(max_norm=0.0) == 5 and clipped(max_norm=float("nan")) == 5
+    need = L.load().ssm_grad_norm_workspace_size(good.ctypes.data, 2)
+    assert clipped(ws=need - 1) == 6
+    for k, off in (("progress", 16), ("norm", 4), ("work", 16)):
+        for at in (1, 2, 10, 11, 12):  # the states, a param, its gradient, the next param
+            assert clipped(**{k: fake(at, off)}) == OVERLAP, (k, at)
+        assert clipped(**{k: fake(6, off), "master": fake(6)}) == OVERLAP
+    assert clipped(norm=fake(3, 28)) == OVERLAP and clipped(norm=fake(5, 12)) == OVERLAP
+    assert clipped(progress=fake(5)) == OVERLAP and clipped(rows(dict(grad=fake(10).value))) == OVERLAP
+
+
+def test_where_the_step_is_counted(unplugged):
+    """On the host without max_grad_norm; with it the host does not know, and what it knew is passed on once."""
+    p, g = [torch.ones(300)], [torch.ones(300)]
+    opt = unplugged(p, step=7)
+    opt.step(g)
+    assert opt._count == 8 == opt.step_count
+    opt.max_grad_norm = 1.0
+    opt.step(g)
+    assert opt._count is None and int(opt._progress[0]) == 8  # (the library, which counts it, is not there)
+    opt = unplugged(p, step=7, max_grad_norm=1.0)
+    assert opt._count is None and int(opt._progress[0]) == 7
+    opt._progress[0] = 5  # two of its steps were left out
+    opt.max_grad_norm = None
+    opt._count = 5  # (read from the device, for which there has to be one)
+    opt.step(g)
+    assert opt.step_count == 6
