@@ -181,19 +181,19 @@ template <bool PB, bool GB, bool MW, bool S8>
 __global__ __launch_bounds__(256) void adamw_kernel(AdamTable t, AdamParams a) {
 #pragma clang fp contract(off)  // every product and sum of the states rounds once: the codes depend on their bits
   constexpr int V = S8 ? 8 : 4;
-  const int k = find(t, blockIdx.x);
   float clip = 1.0f, isb = a.isb, size = a.step;
-  uint32_t key = t.key[k];
-  if (a.progress) {
-    const AdamProgress now = *a.progress;
-    clip = now.factor;
-    isb = now.isb;
-    size = now.size;
-    key = mix32(now.key + key);
+  uint32_t now = 0;
+  if (a.progress) {  // (under way while the tensor is looked for)
+    clip = a.progress->factor;
+    isb = a.progress->isb;
+    size = a.progress->size;
+    now = a.progress->key;
   } else if (a.clip) {
     clip = a.clip[1];
   }
+  const int k = find(t, blockIdx.x);
   if (clip != clip) return;  // the gradients' norm is not finite: nothing changes
+  const uint32_t key = a.progress ? mix32(now + t.key[k]) : t.key[k];
   const int64_t n = t.n[k], off = t.off[k];
   // the wave's first element
   const int64_t base = (int64_t)(blockIdx.x - t.first[k]) * kAdamChunk + (threadIdx.x & ~63) * V;

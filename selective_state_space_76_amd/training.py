@@ -52,6 +52,13 @@ def _stream(stream, device):
     return torch._C._cuda_getCurrentRawStream(device.index) if stream is None else stream.cuda_stream
 
 
+def _capturing(stream):
+    if stream is None:
+        return torch.cuda.is_current_stream_capturing()
+    with torch.cuda.stream(stream):
+        return torch.cuda.is_current_stream_capturing()
+
+
 def _workspace(workspace, need, device, stream):
     """The caller's workspace, or one made here."""
     if workspace is None:
@@ -197,8 +204,9 @@ class AdamW:
     max_grad_norm: scale the gradients so that their norm over all tensors is at most this; a step whose
         norm is not finite changes nothing and is not counted.
     seed: of the stochastic rounding (a hash of seed, step, tensor and element: the same on every run).
-    (The number of the step is an argument of the kernels: a step captured in a graph repeats its bias correction and
-    random numbers with every replay.)
+    A step may be captured in a graph where max_grad_norm is set (math.inf where nothing is to be clipped): every replay
+    is then the next step, with the addresses, lr and other settings of the capture.  Without it the number of the
+    step is an argument of the kernels, which every replay would repeat, and a capture is refused.
     state, step: state_dict()'s tensors to go on from (taken over, not copied), and the steps already made.
 
     The states of all tensors are flat buffers: tensor k's begin at offsets[k], a multiple of 128."""
@@ -331,6 +339,9 @@ class AdamW:
                                self.seed & (2 ** 64 - 1), self.state_bits, 0)
         if self.max_grad_norm is not None:
             if self._count is not None:
+                if _capturing(stream):
+                    raise RuntimeError("the steps so far were counted on the host: make one step with max_grad_norm "
+                                       "before the capture")
                 self._count_on_device(stream)
             norm = _empty((), torch.float32, self.device, stream)
             need = int(lib.ssm_grad_norm_workspace_size(rows, count))
@@ -338,6 +349,9 @@ class AdamW:
             _check(lib.ssm_adamw_clipped_step(ctypes.byref(cfg), rows, count, float(self.max_grad_norm), *states,
                                               _address(self._progress), _address(norm), _address(workspace), need, s))
         else:
+            if _capturing(stream):
+                raise RuntimeError("without max_grad_norm every replay would repeat this step's number: set it "
+                                   "(math.inf: no clipping) for steps in a graph")
             if self._count is None:
                 self._count = self.step_count
             cfg.step = self._count + 1

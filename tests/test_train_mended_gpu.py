@@ -195,3 +195,55 @@ def test_the_step_size_from_the_device(step):
     # moments, root, reciprocal, products and the two factors: some units each
     assert np.abs(f64(p) / want - 1).max() <= 16 * 2.0 ** -24
     assert opt.step_count == step + 1
+
+
+@pytest.mark.parametrize("bits,master", [(32, True), (32, False), (8, True), (8, False)])
+@pytest.mark.parametrize("clip", [1.0, float("inf")])
+def test_replays_of_a_captured_step(bits, master, clip):
+    """Ten replays are ten steps: bias corrections, random numbers, a skipped one among them, and the norms."""
+    params = set_of([BF16, F32], 3, 0.1)
+    k = dict(lr=3e-3, betas=(0.9, 0.99), weight_decay=0.1, state_bits=bits, master_weights=master, max_grad_norm=clip, seed=8)
+    a, b = AdamW([p.clone() for p in params], **k), AdamW([p.clone() for p in params], **k)
+    fixed = [torch.zeros_like(p) for p in params]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        norm = a.step(fixed)
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    assert a.step_count == 0  # a capture runs nothing
+    for s in range(10):
+        print("replay", bits, master, clip, s, flush=True)
+        g = set_of([BF16, F32], 80 + s, 1.0)
+        if s == 4:
+            g[1][3] = float("inf")
+        for x, y in zip(fixed, g):
+            x.copy_(y)
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        want = b.step(g)
+        assert torch.equal(norm, want) and same(a, b), s
+    assert a.step_count == 9
+    a.step(g), b.step(g)  # and on without the graph
+    assert same(a, b)
+
+
+def test_refused_captures():
+    p, g = [torch.zeros(300, device=DEV)], [torch.ones(300, device=DEV)]
+    opt = AdamW(p)
+    graph, side = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    x = torch.zeros(10, device=DEV)
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph, stream=side):
+        x.add_(1)
+        with pytest.raises(RuntimeError, match="repeat this step's number"):
+            opt.step(g)
+        opt.max_grad_norm = 1.0
+        with pytest.raises(RuntimeError, match="before the capture"):
+            opt.step(g)
+    torch.cuda.synchronize()
+    assert opt.step_count == 0
+    opt.step(g)
+    assert opt.step_count == 1 and bool((p[0] != 0).all())

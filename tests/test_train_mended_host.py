@@ -71,6 +71,7 @@ def unplugged(monkeypatch):
         monkeypatch.setattr(m, "_ptr", lambda t: None)
         monkeypatch.setattr(m, "_stream", lambda stream, device: 0)
     monkeypatch.setattr(T, "_address", lambda t: None)
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: False)
     empty = torch.empty
     monkeypatch.setattr(torch, "empty", lambda *a, device=None, **k: empty(*a, **k))
 
@@ -146,3 +147,16 @@ def test_where_the_step_is_counted(unplugged):
     opt._count = 5  # (read from the device, for which there has to be one)
     opt.step(g)
     assert opt.step_count == 6
+
+
+def test_a_capture_that_would_repeat_a_step_is_refused(unplugged, monkeypatch):
+    p, g = [torch.ones(300)], [torch.ones(300)]
+    opt, clips = unplugged(p), unplugged(p, max_grad_norm=1.0)
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: True)
+    with pytest.raises(RuntimeError, match="repeat this step's number"):
+        opt.step(g)
+    opt.max_grad_norm = 1.0
+    with pytest.raises(RuntimeError, match="before the capture"):
+        opt.step(g)
+    assert opt.step_count == 0 and p[0]._version == 0
+    clips.step(g)
