@@ -13,6 +13,7 @@ from __future__ import annotations
 
 import ctypes
 import math
+import operator
 
 import numpy as np
 import torch
@@ -27,6 +28,7 @@ SSM_FLAG_CHANNELS_FIRST = 1
 SSM_FLAG_ACCUMULATE = 2
 ADAMW_BLOCK = 128
 _KIND = {torch.float32: SSM_F32, torch.bfloat16: SSM_BF16}
+_dtype = operator.attrgetter("dtype")
 _INDEX = {torch.int32: SSM_I32, torch.int64: SSM_I64}
 
 
@@ -240,6 +242,7 @@ class AdamW:
         self.offsets = (np.cumsum(room) - room).tolist()
         self.numel = int(room.sum())
         self._table = np.zeros(len(n), _TENSOR)
+        self._rows = self._table.ctypes.data
         self._table["numel"], self._table["offset"] = n, self.offsets
         self._table["param_dtype"] = [_io_dtype(p) for p in self.params]
         want = {"exp_avg": (self.numel, torch.float32 if state_bits == 32 else torch.uint8)}
@@ -287,7 +290,7 @@ class AdamW:
 
     def _checked(self, tensors, what):
         """Their addresses; every call looks at shape, device and layout anew (and the caller at the types)."""
-        if [t.shape for t in tensors] != self._shapes:
+        if list(map(torch.Tensor.size, tensors)) != self._shapes:
             raise ValueError("%s: shapes differ from the parameters' at construction" % what)
         if set(map(torch.Tensor.get_device, tensors)) != {self.device.index}:
             raise ValueError("%s: expected tensors on %s" % (what, self.device))
@@ -308,14 +311,14 @@ class AdamW:
         grads = [p.grad for p in self.params] if grads is None else list(grads)
         if len(grads) != len(self.params):
             raise ValueError("%d gradients for %d parameters" % (len(grads), len(self.params)))
-        table = self._table
-        if [p.dtype for p in self.params] != self._dtypes:
+        table, rows = self._table, self._rows
+        if list(map(_dtype, self.params)) != self._dtypes:
             raise TypeError("a parameter's dtype has changed")
         table["param"] = self._checked(self.params, "params")
         have = [g is not None for g in grads]
         if all(have):
             table["grad"] = self._checked(grads, "grads")
-            dtypes = [g.dtype for g in grads]
+            dtypes = list(map(_dtype, grads))
             if dtypes != self._grad_dtypes:
                 table["grad_dtype"] = [_io_dtype(g) for g in grads]
                 self._grad_dtypes = dtypes
@@ -323,6 +326,7 @@ class AdamW:
             if not any(have):
                 return None
             table = table[have].copy()
+            rows = table.ctypes.data
             grads = [p if g is None else g for p, g in zip(self.params, grads)]
             table["grad"] = np.array(self._checked(grads, "grads"), np.uint64)[have]
             table["grad_dtype"] = np.array([_io_dtype(g) for g in grads])[have]
@@ -331,7 +335,7 @@ class AdamW:
                 and (self.max_grad_norm is None or self.max_grad_norm > 0)):
             raise ValueError("lr %r, betas %r, eps %r, weight_decay %r, max_grad_norm %r: out of range"
                              % (self.lr, self.betas, self.eps, self.weight_decay, self.max_grad_norm))
-        rows, count, s, st, norm = table.ctypes.data, len(table), _stream(stream, self.device), self.state, None
+        count, s, st, norm = len(table), _stream(stream, self.device), self.state, None
         get = st.get
         states = (_address(st["exp_avg"]), _address(st["exp_avg_sq"]), _address(get("exp_avg_base")),
                   _address(get("exp_avg_sq_base")), _address(get("master")))
