@@ -51,6 +51,13 @@ def _first_order(backward):
     return run
 
 
+def _dense(grad, dtype):
+    """An output's gradient as the kernels take it: contiguous, from a multiple of 16 bytes on.  It may come as a view
+    into a larger one, behind a concatenation for instance."""
+    g = grad.to(dtype).contiguous()
+    return g if g.data_ptr() % 16 == 0 else g.clone()
+
+
 class SelectiveScanFn(torch.autograd.Function):
     @staticmethod
     def forward(ctx, u, delta, A, B, C, D, z, delta_bias, initial_state, zoh, reverse):
@@ -70,8 +77,8 @@ class SelectiveScanFn(torch.autograd.Function):
     @_first_order
     def backward(ctx, dout, dfinal):
         u, delta, A, B, C, D, z, delta_bias, initial_state, ck = ctx.saved_tensors
-        dout = torch.zeros_like(u) if dout is None else dout.to(u.dtype).contiguous()
-        dfinal = None if dfinal is None else dfinal.float().contiguous()
+        dout = torch.zeros_like(u) if dout is None else _dense(dout, u.dtype)
+        dfinal = None if dfinal is None else _dense(dfinal, torch.float32)
         g = scan_bwd(u, delta, A, B, C, D, z, delta_bias, initial_state, dout=dout, dfinal_state=dfinal,
                      zoh=ctx.zoh, reverse=ctx.reverse, checkpoints=ck)
         need = ctx.needs_input_grad
@@ -103,8 +110,8 @@ class CausalConv1dFn(torch.autograd.Function):
     @_first_order
     def backward(ctx, dout, dfinal):
         x, weight, bias, initial_state = ctx.saved_tensors
-        dout = torch.zeros_like(x) if dout is None else dout.to(x.dtype).contiguous()
-        dfinal = None if dfinal is None else dfinal.to(x.dtype).contiguous()
+        dout = torch.zeros_like(x) if dout is None else _dense(dout, x.dtype)
+        dfinal = None if dfinal is None else _dense(dfinal, x.dtype)
         g = conv1d_bwd(x, weight, bias, initial_state, dout=dout, dfinal_state=dfinal)
         need = ctx.needs_input_grad
         # (an output without a gradient comes as None)
@@ -131,7 +138,8 @@ class EmbeddingFn(torch.autograd.Function):
     def backward(ctx, dout):
         (tokens,) = ctx.saved_tensors
         rows, dtype, scale, channels_first = ctx.table
-        dw = embedding_bwd(tokens, dout.contiguous(), rows, scale=scale, channels_first=channels_first, dtype=dtype)
+        dw = embedding_bwd(tokens, _dense(dout, dout.dtype), rows, scale=scale, channels_first=channels_first,
+                           dtype=dtype)
         return None, dw, None, None, None
 
 

@@ -37,9 +37,17 @@ def plain(monkeypatch):
         return dict({n: None for n in ("dA", "dB", "dC", "dD", "dz", "ddelta_bias", "dinitial_state")}, du=dout * delta,
                     ddelta=dout * u)
 
+    def checked(fn):
+        def call(*a, **k):
+            for t in (*a, *k.values()):
+                if isinstance(t, torch.Tensor) and t.numel():
+                    assert t.is_contiguous() and t.data_ptr() % 16 == 0, "SSM_ERR_ALIGN"
+            return fn(*a, **k)
+        return call
+
     for name, fn in (("embedding_fwd", rows), ("embedding_bwd", rows_bwd), ("conv1d_fwd", conv), ("conv1d_bwd", conv_bwd),
                      ("scan_fwd", scan), ("scan_bwd", scan_bwd)):
-        monkeypatch.setattr(F, name, fn)
+        monkeypatch.setattr(F, name, checked(fn))
 
 
 def calls():
@@ -92,3 +100,26 @@ def test_first_gradients_as_before(plain, name):
     ins = [t.requires_grad_(True) for t in ins]
     f(*ins).sum().backward()
     assert all(t.grad is not None and t.grad.shape == t.shape for t in ins)
+
+
+@pytest.mark.parametrize("name", list(calls()))
+@pytest.mark.parametrize("width", [1, 2, 3, 4])
+def test_gradients_that_are_views(plain, name, width):
+    """Behind a concatenation they begin anywhere."""
+    f, ins = calls()[name]
+    ins = [t.requires_grad_(True) for t in ins]
+    weight = torch.arange(1.0, 1 + width + f(*ins).numel())
+    (torch.cat([torch.ones(width), f(*ins).reshape(-1)]) * weight).sum().backward()
+    got = [t.grad.clone() for t in ins]
+    for t in ins:
+        t.grad = None
+    (f(*ins).reshape(-1) * weight[width:].clone()).sum().backward()
+    assert all(torch.equal(a, t.grad) for a, t in zip(got, ins))
+
+
+def test_gradients_of_final_states_that_are_views(plain):
+    for f, ins in ((ssm.causal_conv1d, calls()["conv"][1]),):
+        ins = [t.requires_grad_(True) for t in ins]
+        u, last = f(*ins)
+        (torch.cat([torch.ones(3), last.reshape(-1)]) ** 2).sum().backward()
+        assert torch.isfinite(ins[0].grad).all()

@@ -3,7 +3,7 @@ import numpy as np
 import pytest
 import torch
 
-from selective_state_space_76_amd import AdamW, embedding_bwd
+from selective_state_space_76_amd import AdamW, causal_conv1d, embedding, embedding_bwd, selective_scan
 from tests.test_embedding_gpu import bwd_check, tokens_of
 from tests.train_ref import adamw64, decode, encode, f64, moments32, random_bits
 
@@ -247,3 +247,30 @@ def test_refused_captures():
     assert opt.step_count == 0
     opt.step(g)
     assert opt.step_count == 1 and bool((p[0] != 0).all())
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
+def test_gradients_that_are_views(dtype):
+    """Behind a concatenation of odd width the outputs' gradients begin off 16 bytes."""
+    g = torch.Generator(device=DEV).manual_seed(7)
+    r = lambda *s: torch.randn(*s, generator=g, device=DEV)  # noqa: E731
+    tok = torch.randint(0, 50, (1, 33), generator=g, device=DEV)
+    table, x, w, b = r(50, 24).to(dtype), r(1, 24, 33).to(dtype), r(24, 4), r(24)
+    u, delta, A, B, C = r(1, 24, 33).to(dtype), r(1, 24, 33).to(dtype), -r(24, 8).abs(), *(r(1, 8, 33).to(dtype) for _ in "BC")
+    for f, ins in ((lambda t: embedding(tok, t), (table,)), (lambda t: embedding(tok, t, channels_first=True), (table,)),
+                   (lambda *a: causal_conv1d(*a)[0], (x, w, b)), (lambda *a: selective_scan(*a)[0], (u, delta, A, B, C))):
+        ins = [t.detach().requires_grad_(True) for t in ins]
+        out = f(*ins)
+        wide = torch.randn(out.shape[0], out.shape[1], out.shape[2] + 1, generator=g, device=DEV).to(dtype)
+        torch.cat([torch.ones_like(out[..., :1]), out], -1).backward(wide)
+        got = [t.grad.clone() for t in ins]
+        flat = wide[..., 1:].contiguous()
+        for whole in (False, True):  # dout itself as a view into a larger buffer
+            for t in ins:
+                t.grad = None
+            if whole:
+                buf = torch.empty(flat.numel() + 1, dtype=dtype, device=DEV)
+                flat = buf[1:].view(flat.shape).copy_(flat)
+                assert flat.data_ptr() % 16
+            f(*ins).backward(flat)
+            assert all(torch.equal(a, t.grad) for a, t in zip(got, ins))
