@@ -19,7 +19,7 @@ import numpy as np
 import torch
 from torch.autograd.graph import increment_version
 
-from ._lib import (SSM_BF16, SSM_F32, _check, _empty, _expect, _hand_out, _io_dtype, _nonempty, _ptr, load,
+from ._lib import (SSM_BF16, SSM_F32, SSMError, _check, _empty, _expect, _hand_out, _io_dtype, _nonempty, _ptr, load,
                    ssm_adamw_config, ssm_embed_shape)
 
 SSM_I32 = 0
@@ -42,6 +42,11 @@ def _address(t):
     if not isinstance(t, torch.Tensor) or not t.is_cuda or not t.is_contiguous():
         _ptr(t)
     return t.data_ptr()
+
+
+def _aligned(t, name):
+    if t.data_ptr() % 16:
+        raise SSMError(4, "%s does not begin at a multiple of 16 bytes" % name)
 
 
 def _want(t, shape, dtype, name, device):
@@ -198,8 +203,8 @@ _TENSOR = np.dtype([("param", "u8"), ("grad", "u8"), ("numel", "i8"), ("offset",
 class AdamW:
     """AdamW over many tensors at once, in place, with decoupled weight decay and bias-corrected moments.
 
-    params: fp32 or bf16 tensors on one GPU, contiguous.  lr, betas, eps, weight_decay and max_grad_norm are
-    attributes that may be changed between steps.
+    params: fp32 or bf16 tensors on one GPU, contiguous, from multiples of 16 bytes on (and so the gradients).  lr, betas,
+    eps, weight_decay and max_grad_norm are attributes that may be changed between steps.
     state_bits: 32 (fp32 moments) or 8 (one byte per element and an int16 per 128; see include/ssm_scan.h).
     master_weights: fp32 copies of the bf16 parameters, on which the step works; without them a bf16 parameter is
         rounded stochastically (to nearest, updates under half a unit would be lost).
@@ -227,6 +232,7 @@ class AdamW:
         for p in self.params:
             _io_dtype(p)
             _ptr(p)
+            _aligned(p, "a parameter")
             if p.numel() < 1:
                 raise ValueError("empty parameter")
             if p.device != self.device:
@@ -269,6 +275,7 @@ class AdamW:
                         t[o:o + p.numel()].copy_(p.detach().reshape(-1))
             _expect(t, (size,), dt, k, self.device)
             _ptr(t)
+            _aligned(t, k)
             self.state[k] = t
 
     @property

@@ -160,3 +160,11 @@ def test_a_capture_that_would_repeat_a_step_is_refused(unplugged, monkeypatch):
         opt.step(g)
     assert opt.step_count == 0 and p[0]._version == 0
     clips.step(g)
+
+
+def test_alignment_is_looked_at_when_the_optimizer_is_made(unplugged):
+    with pytest.raises(L.SSMError, match="ALIGN.*a parameter"):
+        unplugged([torch.zeros(64), torch.zeros(65)[1:]])
+    with pytest.raises(L.SSMError, match="ALIGN.*exp_avg_sq"):
+        unplugged([torch.zeros(128)], state={"exp_avg_sq": torch.zeros(129)[1:]})
+    unplugged([torch.zeros(64), torch.zeros(68)[4:]])
