@@ -262,10 +262,10 @@ __global__ __launch_bounds__(256) void adamw_kernel(AdamTable t, AdamParams a) {
           pb[e] = (uint32_t)__builtin_bit_cast(uint16_t, (__bf16)p[e]) << 16;
         } else {
           const uint32_t b = __float_as_uint(p[e]);
-          // What is not finite stays so: the lower half of an infinity is zero, and that of a NaN too where
-          // every input came in bf16; with fp32 gradients it may not be.
+          // What is not finite stays so.  The lower half of an infinity is zero, and that of a NaN where every input
+          // came in bf16 or codes; from fp32 gradients or states it may be all ones.
           const uint32_t r = (h[e] * 0x3C6EF373u) >> 16;
-          pb[e] = b + (GB || __builtin_isfinite(p[e]) ? r : 0u);
+          pb[e] = b + ((GB && S8) || __builtin_isfinite(p[e]) ? r : 0u);
         }
       }
     }

@@ -274,3 +274,17 @@ def test_gradients_that_are_views(dtype):
                 assert flat.data_ptr() % 16
             f(*ins).backward(flat)
             assert all(torch.equal(a, t.grad) for a, t in zip(got, ins))
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+@pytest.mark.parametrize("nan", [-1, 0x7FFFFFFF, 0x7FC00000])
+def test_a_nan_stays_a_nan(bits, nan):
+    """Whatever its lower bits: rounding a bf16 parameter at random must not carry them into a number."""
+    n = 4096
+    p = torch.ones(n, dtype=BF16, device=DEV)
+    opt = AdamW([p], state_bits=bits, master_weights=False)
+    opt.step([torch.full((n,), nan, dtype=torch.int32, device=DEV).view(F32)])
+    assert torch.isnan(p).all()
+    for _ in range(3):
+        opt.step([torch.ones(n, dtype=BF16, device=DEV)])
+        assert torch.isnan(p).all()
