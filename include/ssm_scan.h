@@ -327,7 +327,8 @@ typedef struct ssm_embed_shape {
 } ssm_embed_shape;
 
 /* Embedding: out[b,t,:] = scale * weight[tokens[b,t],:], rounded once to io_dtype.
- *   tokens : [B, L];  weight : [V, E];  out : [B, L, E], or [B, E, L] with SSM_FLAG_CHANNELS_FIRST
+ *   tokens : [B, L], aligned to their own size;  weight : [V, E];
+ *   out    : [B, L, E], or [B, E, L] with SSM_FLAG_CHANNELS_FIRST
  * A token outside [0, V) (a padding mark such as -1) gives zeros. */
 ssm_status ssm_embedding_fwd(const ssm_embed_shape* shape, const void* tokens, const void* weight,
                              float scale, void* out, struct ihipStream_t* stream);

@@ -137,6 +137,11 @@ ssm_status embed_check(const ssm_embed_shape* s, uint32_t flags, ssm::EmbedParam
   return SSM_OK;
 }
 
+// tokens are read one at a time: a row of a batch of odd length will do
+bool tokens_misaligned(const ssm::EmbedParams& p, const void* tokens) {
+  return (reinterpret_cast<uintptr_t>(tokens) & (p.i64 ? 7u : 3u)) != 0;
+}
+
 }  // namespace
 
 extern "C" {
@@ -148,7 +153,7 @@ ssm_status ssm_embedding_fwd(const ssm_embed_shape* shape, const void* tokens, c
   if (rc != SSM_OK) return rc;
   if (!tokens || !weight || !out) return SSM_ERR_NULL;
   if (!isfinite(scale)) return SSM_ERR_UNSUPPORTED;
-  if (misaligned(tokens) || misaligned(weight) || misaligned(out)) return SSM_ERR_ALIGN;
+  if (tokens_misaligned(p, tokens) || misaligned(weight) || misaligned(out)) return SSM_ERR_ALIGN;
   const Range ins[] = {span(tokens, p.T * (p.i64 ? 8 : 4)),
                        span(weight, p.V * p.E * dtype_size(shape->table_dtype))};
   const Range outs[] = {span(out, p.T * p.E * dtype_size(shape->io_dtype))};
@@ -174,7 +179,7 @@ ssm_status ssm_embedding_bwd(const ssm_embed_shape* shape, const void* tokens, c
   if (rc != SSM_OK) return rc;
   if (!tokens || !dout || !dweight || !workspace) return SSM_ERR_NULL;
   if (!isfinite(scale)) return SSM_ERR_UNSUPPORTED;
-  if (misaligned(tokens) || misaligned(dout) || misaligned(dweight) || misaligned(workspace)) return SSM_ERR_ALIGN;
+  if (tokens_misaligned(p, tokens) || misaligned(dout) || misaligned(dweight) || misaligned(workspace)) return SSM_ERR_ALIGN;
   ssm::EmbedBwdPlan pl;
   ssm::plan_embed_bwd(p.Bsz, p.L, p.V, p.E, dtype_size(shape->table_dtype), shape->io_dtype == SSM_BF16, p.cf, p.add,
                       &pl);

@@ -3,7 +3,7 @@ import numpy as np
 import pytest
 import torch
 
-from selective_state_space_76_amd import AdamW, causal_conv1d, embedding, embedding_bwd, selective_scan
+from selective_state_space_76_amd import AdamW, causal_conv1d, embedding, embedding_bwd, embedding_fwd, selective_scan
 from tests.test_embedding_gpu import bwd_check, tokens_of
 from tests.train_ref import adamw64, decode, encode, f64, moments32, random_bits
 
@@ -288,3 +288,25 @@ def test_a_nan_stays_a_nan(bits, nan):
     for _ in range(3):
         opt.step([torch.ones(n, dtype=BF16, device=DEV)])
         assert torch.isnan(p).all()
+
+
+@pytest.mark.parametrize("cf", [False, True], ids=["ble", "bel"])
+@pytest.mark.parametrize("V", [5, 300])
+@pytest.mark.parametrize("index", [torch.int32, torch.int64])
+def test_micro_batches_of_odd_length(cf, V, index):
+    """Rows of a batch, one call each: their tokens begin anywhere."""
+    B, L, E = 5, 509, 40
+    tok = torch.randint(-1, V, (B, L), generator=torch.Generator().manual_seed(V)).to(index).to(DEV)
+    table = torch.randn(V, E, generator=torch.Generator().manual_seed(1)).to(DEV)
+    whole = embedding_fwd(tok, table, channels_first=cf)
+    dout = torch.randn(whole.shape, generator=torch.Generator().manual_seed(2)).to(DEV)
+    total = torch.zeros(V, E, device=DEV)
+    for b in range(B):
+        assert torch.equal(embedding_fwd(tok[b:b + 1], table, channels_first=cf), whole[b:b + 1])
+        d = dout[b:b + 1].clone()
+        one = embedding_bwd(tok[b:b + 1], d, V, channels_first=cf)
+        assert torch.equal(one, embedding_bwd(tok[b:b + 1].clone(), d, V, channels_first=cf))
+        embedding_bwd(tok[b:b + 1], d, V, channels_first=cf, dweight=total, accumulate=True)
+    want = embedding_bwd(tok, dout, V, channels_first=cf)
+    n = torch.bincount(tok[tok >= 0].long(), minlength=V)[:, None].to(DEV)
+    assert ((total - want).abs() <= (n + 5) * 2.0 ** -23 * n * 5).all()

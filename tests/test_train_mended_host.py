@@ -168,3 +168,15 @@ def test_alignment_is_looked_at_when_the_optimizer_is_made(unplugged):
     with pytest.raises(L.SSMError, match="ALIGN.*exp_avg_sq"):
         unplugged([torch.zeros(128)], state={"exp_avg_sq": torch.zeros(129)[1:]})
     unplugged([torch.zeros(64), torch.zeros(68)[4:]])
+
+
+@pytest.mark.skipif(torch.cuda.is_available(), reason="a call that is not refused would run on made-up addresses")
+@pytest.mark.parametrize("index,size", [(0, 4), (1, 8)], ids=["int32", "int64"])
+def test_tokens_need_their_own_alignment_only(index, size):
+    """A micro-batch is a row of a batch: with an odd length it begins off 16 bytes."""
+    s = L.ssm_embed_shape(batch=1, seqlen=509, rows=1000, dim=64, index_dtype=index, table_dtype=0, io_dtype=1, flags=0)
+    lib = L.load()
+    for off in range(0, 16, 2):
+        want = LAUNCH if off % size == 0 else 4
+        assert lib.ssm_embedding_fwd(ctypes.byref(s), fake(1, off), fake(2), 1.0, fake(3), None) == want
+        assert lib.ssm_embedding_bwd(ctypes.byref(s), fake(1, off), fake(2), 1.0, fake(3), fake(4), 1 << 30, None) == want
