@@ -493,7 +493,7 @@ __global__ __launch_bounds__(1024) void norm_small_kernel(SmallNormTable t, uint
 __global__ __launch_bounds__(256) void state_values_kernel(int64_t n, const uint8_t* m, const uint8_t* v,
                                                            const int16_t* mb, const int16_t* vb, bf16_t* mo,
                                                            bf16_t* vo) {
-  const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 8;
+  const int64_t i = ((int64_t)block_id() * 256 + threadIdx.x) * 8;
   if (i >= n) return;
   uint32_t x[8];
   if (mo) {
@@ -564,7 +564,7 @@ hipError_t launch_norm_join(const double* part, int64_t n, double max_norm, floa
 
 hipError_t launch_state_values(int64_t n, const void* m, const void* v, const int16_t* mb, const int16_t* vb,
                                void* mo, void* vo, hipStream_t s) {
-  hipLaunchKernelGGL(state_values_kernel, dim3((unsigned)((n / 8 + 255) / 256)), dim3(256), 0, s, n,
+  hipLaunchKernelGGL(state_values_kernel, grid_of((n / 8 + 255) / 256), dim3(256), 0, s, n,
                      static_cast<const uint8_t*>(m), static_cast<const uint8_t*>(v), mb, vb,
                      static_cast<bf16_t*>(mo), static_cast<bf16_t*>(vo));
   return hipGetLastError();

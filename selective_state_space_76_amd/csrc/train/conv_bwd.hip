@@ -21,6 +21,7 @@
 // 219 us with pieces that begin where the row does; 37 and 150 with aligned ones, 32-bit positions and DPP shifts;
 // 30 for the first once whole rows took the initial state's gradient from registers.
 #include "../ssm_device.h"
+#include "train_device.h"
 #include "train_launch.h"
 
 namespace ssm {
@@ -123,7 +124,7 @@ __global__ __launch_bounds__(256, LN == 64 ? 5 : 4) void conv_bwd_kernel(ConvBwd
   constexpr int SEG = LN * V * P;
   const int lane = threadIdx.x % LN;
   // row segment; their number fits 31 bits, so the divisions take 32
-  uint32_t unit = blockIdx.x * (256 / LN) + threadIdx.x / LN;
+  uint32_t unit = block_id() * (256 / LN) + threadIdx.x / LN;
   if constexpr (LN == 64) unit = (uint32_t)__builtin_amdgcn_readfirstlane((int)unit);  // scalar from here on
   const bool live = unit < p.units;
   unit = live ? unit : 0;
@@ -302,7 +303,7 @@ __global__ __launch_bounds__(256, LN == 64 ? 5 : 4) void conv_bwd_kernel(ConvBwd
 __global__ __launch_bounds__(256) void conv_bwd_join_kernel(const float* part, int64_t count, int64_t Dm, int K,
                                                             float* dw, float* db) {
   const int64_t n = Dm * (K + 1);
-  const int64_t i = (int64_t)blockIdx.x * 64 + (threadIdx.x & 63);
+  const int64_t i = (int64_t)block_id() * 64 + (threadIdx.x & 63);
   const int64_t per = (count + 3) / 4;
   const int64_t k0 = (threadIdx.x >> 6) * per, k1 = k0 + per < count ? k0 + per : count;
   float s = 0.0f;
@@ -343,9 +344,9 @@ namespace {
 template <typename IO, int K>
 void launch_k(const ConvBwdParams& p, hipStream_t s) {
   if (p.lanes == 16)
-    hipLaunchKernelGGL((conv_bwd_kernel<IO, K, 16>), dim3((p.units + 15) / 16), dim3(256), 0, s, p);
+    hipLaunchKernelGGL((conv_bwd_kernel<IO, K, 16>), grid_of((p.units + 15) / 16), dim3(256), 0, s, p);
   else
-    hipLaunchKernelGGL((conv_bwd_kernel<IO, K, 64>), dim3((p.units + 3) / 4), dim3(256), 0, s, p);
+    hipLaunchKernelGGL((conv_bwd_kernel<IO, K, 64>), grid_of((p.units + 3) / 4), dim3(256), 0, s, p);
 }
 
 template <typename IO>
@@ -365,7 +366,7 @@ hipError_t launch_conv_bwd(const ConvBwdParams& p, bool bf16, hipStream_t s) {
   else launch_io<float>(p, s);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || p.Bsz * p.S == 1) return e;
-  hipLaunchKernelGGL(conv_bwd_join_kernel, dim3((unsigned)((p.Dm * (p.K + 1) + 63) / 64)), dim3(256), 0, s, p.part,
+  hipLaunchKernelGGL(conv_bwd_join_kernel, grid_of((p.Dm * (p.K + 1) + 63) / 64), dim3(256), 0, s, p.part,
                      p.Bsz * p.S, p.Dm, p.K, p.dw, p.db);
   return hipGetLastError();
 }

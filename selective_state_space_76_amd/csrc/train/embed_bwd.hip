@@ -37,7 +37,7 @@ struct SortParams {
   uint32_t* pos_out;
   uint32_t* hist;         // [tiles][digits]
   char* fill;             // bytes to clear meanwhile (the sort leaves most of the chip idle)
-  int64_t fill_bytes;
+  int64_t fill_bytes, fill_blocks;
   int64_t n, V, tiles;
   int i64, shift, bits, passes;
 };
@@ -46,17 +46,19 @@ __device__ __forceinline__ uint32_t key_at(const SortParams& p, int64_t i) {
   return p.tokens ? (uint32_t)token_at(p.tokens, p.i64, i, p.V) : p.key_in[i];
 }
 
-constexpr int64_t kFill = 16384;  // bytes per workgroup
+constexpr int64_t kFill = 16384;                       // bytes per workgroup,
+constexpr int64_t kFillBlocks = int64_t(1) << 20;  // up to 16 GiB; then again that far on
 
 // clears piece `block` of the bytes to fill
 __device__ __forceinline__ void fill_piece(const SortParams& p, int64_t block, int threads) {
-  const int64_t lo = block * kFill;
-  const int64_t hi = lo + kFill < p.fill_bytes ? lo + kFill : p.fill_bytes;
-  int64_t i = lo + threadIdx.x * 16;
-  for (; i + 16 <= hi; i += threads * 16)
-    __builtin_nontemporal_store(u32x4a{0u, 0u, 0u, 0u}, reinterpret_cast<u32x4a*>(p.fill + i));
-  if (i < hi)  // the last elements, fewer than 16 bytes
-    for (; i < hi; i += 2) *reinterpret_cast<uint16_t*>(p.fill + i) = 0;
+  for (int64_t lo = block * kFill; lo < p.fill_bytes; lo += p.fill_blocks * kFill) {
+    const int64_t hi = lo + kFill < p.fill_bytes ? lo + kFill : p.fill_bytes;
+    int64_t i = lo + threadIdx.x * 16;
+    for (; i + 16 <= hi; i += threads * 16)
+      __builtin_nontemporal_store(u32x4a{0u, 0u, 0u, 0u}, reinterpret_cast<u32x4a*>(p.fill + i));
+    if (i < hi)  // the last elements, fewer than 16 bytes
+      for (; i < hi; i += 2) *reinterpret_cast<uint16_t*>(p.fill + i) = 0;
+  }
 }
 
 // Exclusive sum over up to 256 digits, by one wave: 4 per lane.
@@ -564,15 +566,16 @@ __global__ __launch_bounds__(256) void embed_join_kernel(SumParams p) {
 
 // [B,E,L] to [B,L,E]: a tile of 64 columns x 128 positions through LDS, in pairs of neighbouring columns
 template <typename IO>
-__global__ __launch_bounds__(256) void embed_turn_kernel(const IO* in, IO* out, int64_t E, int64_t L) {
+__global__ __launch_bounds__(256) void embed_turn_kernel(const IO* in, IO* out, int64_t Bsz, int64_t E, int64_t L) {
   constexpr int V = 16 / (int)sizeof(IO);
   constexpr int TT = 128, TE = 64;
   constexpr int LD = TE + V;  // elements between positions in LDS
   __shared__ __align__(16) IO sm[TT * LD];
   const int64_t tiles_t = (L + TT - 1) / TT, tiles_e = (E + TE - 1) / TE;
-  const int64_t blk = blockIdx.x;
+  const int64_t blk = block_id();
   const int64_t te = blk % tiles_e, rest = blk / tiles_e;
   const int64_t tt = rest % tiles_t, b = rest / tiles_t;
+  if (b >= Bsz) return;
   const int64_t t0 = tt * TT, e0 = te * TE;
   const int64_t nt = L - t0, ne = E - e0;
   constexpr int PPR = TT / 8;  // 8 positions per lane
@@ -642,8 +645,8 @@ hipError_t launch_io(const EmbedParams& e, const EmbedBwdPlan& pl, const SortPar
   if (pl.transpose) {
     const int64_t blocks = e.Bsz * ((e.L + 127) / 128) * ((e.E + 63) / 64);
     IO* rows = reinterpret_cast<IO*>(ws + pl.rows);
-    hipLaunchKernelGGL((embed_turn_kernel<IO>), dim3((unsigned)blocks), dim3(256), 0, s,
-                       static_cast<const IO*>(e.dout), rows, e.E, e.L);
+    hipLaunchKernelGGL((embed_turn_kernel<IO>), grid_of(blocks), dim3(256), 0, s,
+                       static_cast<const IO*>(e.dout), rows, e.Bsz, e.E, e.L);
     p.dout = rows;
   }
   if (pl.once) return launch_once<IO, OT>(sp, p, s);
@@ -658,7 +661,9 @@ hipError_t with_fill(SortParams& sp, int64_t* left, double share, F&& go) {
   int64_t bytes = (int64_t)(*left * share) / kFill * kFill;
   if (share >= 1.0) bytes = *left;
   sp.fill_bytes = bytes;
-  go((unsigned)((bytes + kFill - 1) / kFill));
+  sp.fill_blocks = (bytes + kFill - 1) / kFill;
+  if (sp.fill_blocks > kFillBlocks) sp.fill_blocks = kFillBlocks;
+  go((unsigned)sp.fill_blocks);
   sp.fill += bytes;
   *left -= bytes;
   return hipGetLastError();

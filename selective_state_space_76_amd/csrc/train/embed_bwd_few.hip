@@ -74,7 +74,8 @@ __global__ __launch_bounds__(256) void embed_few_kernel(FewParams p) {
   __shared__ __align__(16) u32x4a tile[4][16][64];  // per wave: 16 channels; piece c of channel k lies at c ^ k
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int n = lane & 15, g = lane >> 4;
-  const int64_t grp = blockIdx.x % p.groups, seg = blockIdx.x / p.groups;
+  const int64_t grp = block_id() % p.groups, seg = block_id() / p.groups;
+  if (seg >= p.segs) return;
   const int64_t b = seg / p.segs_row, t0 = (seg - b * p.segs_row) * p.seg;
   const int64_t e0 = grp * 64;
   const IO* base = static_cast<const IO*>(p.dout) + (b * p.E + e0) * p.L;
@@ -177,7 +178,7 @@ __global__ __launch_bounds__(256) void embed_few_kernel(FewParams p) {
 template <typename OT>
 __global__ __launch_bounds__(256) void embed_few_join_kernel(FewParams p) {
   const int64_t n = p.V * p.E;
-  const int64_t i = (int64_t)blockIdx.x * 64 + (threadIdx.x & 63);
+  const int64_t i = (int64_t)block_id() * 64 + (threadIdx.x & 63);
   const int64_t per = (p.segs + 3) / 4;
   const int64_t k0 = (threadIdx.x >> 6) * per, k1 = k0 + per < p.segs ? k0 + per : p.segs;
   float s = 0.0f;
@@ -234,11 +235,11 @@ namespace {
 
 template <typename IO>
 hipError_t launch_few(const FewParams& p, bool table_bf16, hipStream_t s) {
-  const dim3 grid((unsigned)(p.segs * p.groups));
+  const dim3 grid = grid_of(p.segs * p.groups);
   if (p.V <= 16) hipLaunchKernelGGL((embed_few_kernel<IO, 1>), grid, dim3(256), 0, s, p);
   else if (p.V <= 32) hipLaunchKernelGGL((embed_few_kernel<IO, 2>), grid, dim3(256), 0, s, p);
   else if constexpr (sizeof(IO) == 2) hipLaunchKernelGGL((embed_few_kernel<IO, 4>), grid, dim3(256), 0, s, p);
-  const dim3 jgrid((unsigned)((p.V * p.E + 63) / 64));
+  const dim3 jgrid = grid_of((p.V * p.E + 63) / 64);
   if (table_bf16) hipLaunchKernelGGL(embed_few_join_kernel<bf16_t>, jgrid, dim3(256), 0, s, p);
   else hipLaunchKernelGGL(embed_few_join_kernel<float>, jgrid, dim3(256), 0, s, p);
   return hipGetLastError();

@@ -18,7 +18,7 @@ template <typename WT, typename IO>
 __global__ __launch_bounds__(256) void embed_rows_kernel(EmbedParams p) {
   constexpr int V = 16 / (int)sizeof(IO);
   const int64_t total = p.T * p.E;
-  const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * V;  // the piece's first element
+  const int64_t i = ((int64_t)block_id() * 256 + threadIdx.x) * V;  // the piece's first element
   if (i >= total) return;
   int64_t t, e;
   if (total <= 0xffffffffll) {
@@ -73,8 +73,9 @@ __global__ __launch_bounds__(256) void embed_cols_kernel(EmbedParams p) {
   constexpr int LD = kT + EX + V;  // elements between columns in LDS, whole 16-byte pieces
   __shared__ __align__(16) IO sm[kE * LD];
   const int64_t tiles_t = p.tiles, tiles_e = (p.E + kE - 1) / kE;
-  const int64_t te = blockIdx.x % tiles_e, rest = blockIdx.x / tiles_e;
+  const int64_t blk = block_id(), te = blk % tiles_e, rest = blk / tiles_e;
   const int64_t tt = rest % tiles_t, b = rest / tiles_t;
+  if (b >= p.Bsz) return;
   const int64_t t0 = tt * kT, e0 = te * kE;
   const int64_t ne = p.E - e0;
   constexpr int CPR = kE / 8, RPP = 256 / CPR * 2;  // pieces of 8 columns, positions per pass
@@ -153,15 +154,15 @@ hipError_t launch(const EmbedParams& p, hipStream_t s) {
     EmbedParams q = p;
     q.tiles = Tile<IO, false>::along(p.L);
     const int64_t blocks = p.Bsz * q.tiles * ((p.E + Tile<IO, false>::E - 1) / Tile<IO, false>::E);
-    hipLaunchKernelGGL((embed_cols_kernel<WT, IO, false>), dim3((unsigned)blocks), dim3(256), 0, s, q);
+    hipLaunchKernelGGL((embed_cols_kernel<WT, IO, false>), grid_of(blocks), dim3(256), 0, s, q);
   } else if (p.cf) {
     EmbedParams q = p;
     q.tiles = Tile<IO, true>::along(p.L);
     const int64_t blocks = p.Bsz * q.tiles * ((p.E + Tile<IO, true>::E - 1) / Tile<IO, true>::E);
-    hipLaunchKernelGGL((embed_cols_kernel<WT, IO, true>), dim3((unsigned)blocks), dim3(256), 0, s, q);
+    hipLaunchKernelGGL((embed_cols_kernel<WT, IO, true>), grid_of(blocks), dim3(256), 0, s, q);
   } else {
     const int64_t pieces = (p.T * p.E + V - 1) / V;
-    hipLaunchKernelGGL((embed_rows_kernel<WT, IO>), dim3((unsigned)((pieces + 255) / 256)), dim3(256), 0, s, p);
+    hipLaunchKernelGGL((embed_rows_kernel<WT, IO>), grid_of((pieces + 255) / 256), dim3(256), 0, s, p);
   }
   return hipGetLastError();
 }

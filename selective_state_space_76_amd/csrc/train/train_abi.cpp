@@ -15,6 +15,7 @@ namespace {
 constexpr int64_t kMaxSize = int64_t(1) << 40;
 constexpr int64_t kMaxElems = int64_t(1) << 61;
 constexpr int64_t kMaxGrid = (int64_t(1) << 31) - 1;
+constexpr int64_t kMaxBlocks = (int64_t(1) << 24) - 1;  // of 256 threads, in a launch of one dimension
 
 struct Range {
   uintptr_t lo, hi;  // [lo, hi)
@@ -125,7 +126,7 @@ ssm_status embed_check(const ssm_embed_shape* s, uint32_t flags, ssm::EmbedParam
   if (!mul_ok(s->batch, s->seqlen, &n) || n > kMaxGrid) return SSM_ERR_SHAPE;
   if (s->rows >= kMaxGrid || s->dim > kMaxSize) return SSM_ERR_SHAPE;
   if (!mul_ok(n, s->dim, &te) || !mul_ok(s->rows, s->dim, &ve)) return SSM_ERR_SHAPE;
-  if (ve > (int64_t(1) << 42)) return SSM_ERR_SHAPE;  // cleared in pieces of 16 KiB, one workgroup each
+  if (ve > (int64_t(1) << 42)) return SSM_ERR_SHAPE;  // more than any memory holds
   // every kernel's grid: at most one workgroup per position and 64 columns, or per 256 pieces of 16 bytes
   int64_t blocks;
   if (!mul_ok(n, (s->dim + 63) / 64, &blocks) || blocks > kMaxGrid) return SSM_ERR_SHAPE;
@@ -256,7 +257,7 @@ hipError_t in_tables(const ssm_adamw_tensor* t, int64_t count, int64_t chunk, Ta
   for (int64_t k = 0; k <= count; ++k) {
     const bool here = k < count && take(t[k]);
     const int64_t more = here ? chunks_of(t[k].numel, chunk) : 0;
-    if (tab.count && (k == count || (here && (tab.count == kRoom || blocks + more > kMaxGrid)))) {
+    if (tab.count && (k == count || (here && (tab.count == kRoom || blocks + more > kMaxBlocks)))) {
       const hipError_t e = go(tab, (uint32_t)blocks);
       if (e != hipSuccess) return e;
       tab.count = 0;

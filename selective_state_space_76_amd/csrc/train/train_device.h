@@ -4,10 +4,14 @@
 #include <stdint.h>
 
 #include "../ssm_device.h"
+#include "train_launch.h"
 
 namespace ssm {
 
 typedef uint32_t u32x4a __attribute__((ext_vector_type(4)));
+
+// the workgroup's number in a grid_of() grid (a second row of which there is only behind a full one)
+__device__ __forceinline__ uint32_t block_id() { return blockIdx.y * (uint32_t)kGridX + blockIdx.x; }
 
 // 16 bytes that begin at any element
 template <typename IO> struct Unaligned;

@@ -6,6 +6,14 @@
 
 namespace ssm {
 
+// A launch takes fewer than 2^32 threads in x; workgroups beyond kGridX go on in y.  A kernel knows its workgroup by
+// block_id() (train_device.h); the last row of y may hold some past the last one.
+constexpr int64_t kGridX = int64_t(1) << 22;
+inline dim3 grid_of(int64_t blocks) {
+  const int64_t x = blocks < kGridX ? blocks : kGridX;
+  return dim3((unsigned)x, (unsigned)((blocks + x - 1) / x));
+}
+
 // ---- gradients of conv1d + SiLU (conv_bwd.hip)
 struct ConvBwdParams {
   const void* x;        // [B,D,L]
