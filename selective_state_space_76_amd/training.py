@@ -248,7 +248,6 @@ class AdamW:
         self.offsets = (np.cumsum(room) - room).tolist()
         self.numel = int(room.sum())
         self._table = np.zeros(len(n), _TENSOR)
-        self._rows = self._table.ctypes.data
         self._table["numel"], self._table["offset"] = n, self.offsets
         self._table["param_dtype"] = [_io_dtype(p) for p in self.params]
         want = {"exp_avg": (self.numel, torch.float32 if state_bits == 32 else torch.uint8)}
@@ -318,7 +317,7 @@ class AdamW:
         grads = [p.grad for p in self.params] if grads is None else list(grads)
         if len(grads) != len(self.params):
             raise ValueError("%d gradients for %d parameters" % (len(grads), len(self.params)))
-        table, rows = self._table, self._rows
+        table = self._table
         if list(map(_dtype, self.params)) != self._dtypes:
             raise TypeError("a parameter's dtype has changed")
         table["param"] = self._checked(self.params, "params")
@@ -333,7 +332,6 @@ class AdamW:
             if not any(have):
                 return None
             table = table[have].copy()
-            rows = table.ctypes.data
             grads = [p if g is None else g for p, g in zip(self.params, grads)]
             table["grad"] = np.array(self._checked(grads, "grads"), np.uint64)[have]
             table["grad_dtype"] = np.array([_io_dtype(g) for g in grads])[have]
@@ -342,7 +340,8 @@ class AdamW:
                 and (self.max_grad_norm is None or self.max_grad_norm > 0)):
             raise ValueError("lr %r, betas %r, eps %r, weight_decay %r, max_grad_norm %r: out of range"
                              % (self.lr, self.betas, self.eps, self.weight_decay, self.max_grad_norm))
-        count, s, st, norm = len(table), _stream(stream, self.device), self.state, None
+        rows, count = ctypes.addressof(ctypes.c_char.from_buffer(table)), len(table)
+        s, st, norm = _stream(stream, self.device), self.state, None
         get = st.get
         states = (_address(st["exp_avg"]), _address(st["exp_avg_sq"]), _address(get("exp_avg_base")),
                   _address(get("exp_avg_sq_base")), _address(get("master")))

@@ -1,4 +1,5 @@
 """The training operators without a GPU: what a call must refuse, plan or pass on."""
+import copy
 import ctypes
 from types import SimpleNamespace
 
@@ -180,3 +181,21 @@ def test_tokens_need_their_own_alignment_only(index, size):
         want = LAUNCH if off % size == 0 else 4
         assert lib.ssm_embedding_fwd(ctypes.byref(s), fake(1, off), fake(2), 1.0, fake(3), None) == want
         assert lib.ssm_embedding_bwd(ctypes.byref(s), fake(1, off), fake(2), 1.0, fake(3), fake(4), 1 << 30, None) == want
+
+
+def test_a_copied_optimizer_has_a_table_of_its_own(unplugged, monkeypatch):
+    seen = []
+
+    class Looks(Library):
+        def __getattr__(self, name):
+            if name == "ssm_adamw_step":
+                return lambda cfg, rows, count, *a: seen.append((rows, ctypes.c_uint64.from_address(rows).value)) or 0
+            return Library.__getattr__(self, name)
+
+    monkeypatch.setattr(T, "load", Looks)
+    opt = unplugged([torch.ones(300)])
+    twin = copy.deepcopy(opt)
+    for o in (opt, twin):
+        o.step([torch.ones(300)])
+        assert seen[-1] == (o._table.ctypes.data, o.params[0].data_ptr())
+    assert seen[0][0] != seen[1][0]
