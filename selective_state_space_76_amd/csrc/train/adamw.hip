@@ -7,12 +7,13 @@
 // table in memory to fill, keep or wait for).  A workgroup owns one chunk of kAdamChunk elements of one
 // tensor, found by bisection over the first workgroup of each tensor; a lane owns V consecutive elements
 // (4 with fp32 states, 8 with 8-bit ones, so that every stream is read in 8- or 16-byte pieces).
-// With fp32 states the step is bound by HBM: every byte is touched once, at 5.8 TB/s (a copy reaches 5.2, a plain
-// sum 6.0): 127 M bf16 weights with masters 0.66 ms.  With 8-bit states the instructions (about 70 an
+// With fp32 states the step is bound by HBM: it touches every byte once, at 5.2 TB/s (a copy reaches 5.2, a plain
+// sum 6.0): 127 M bf16 weights with masters 0.68 ms.  With 8-bit states the instructions (about 70 an
 // element, three of them 32-bit integer products for the random numbers) take nearly as long as the 10 bytes:
-// 311 M bf16 weights 0.59 ms, 5.3 TB/s (0.79 ms with 87 instructions).  Loading the next piece before
+// 311 M bf16 weights 0.60 ms, 5.2 TB/s (0.79 ms with 87 instructions).  Loading the next piece before
 // the present one is worked on gained nothing with either.
-// The gradients' norm comes first and reads them once more: 127 M in bf16 44 us, 5.8 TB/s.
+// The gradients' norm comes first and reads them once more: 127 M in bf16 44 us, 5.8 TB/s.  Its last kernel also counts
+// the step and writes what depends on the step's number (AdamProgress), so that neither is a matter of the host.
 //
 // 8-bit states.  A positive float's bit pattern is an increasing integer, and its top 12 bits a number
 // of 4 significant bits.  A block of 128 elements (16 lanes of 8) keeps K, the largest element's top

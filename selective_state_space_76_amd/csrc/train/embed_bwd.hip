@@ -19,7 +19,7 @@
 // Tokens outside the table sort as V, behind all others, and are left out.
 //
 // Bound by HBM, which the launches reach in part: 8 x 2048 tokens of width 768 into 50000 rows (25 MB read, 154 MB
-// cleared or written) take 48 us, of which 30 are the sort's four launches with the clearing (5.1 TB/s), 11 the sums
+// cleared or written) take 47 us, of which 30 are the sort's four launches with the clearing (5.1 TB/s), 11 the sums
 // and 6 the join.  262144 x 1024 in bf16: 148 us (sort 33, sums 105 at 5.1 TB/s, join 10).
 #include "../ssm_device.h"
 #include "train_device.h"
