@@ -431,6 +431,125 @@ ssm_status ssm_adamw_state_values(int64_t numel, const void* exp_avg, const void
                                   const int16_t* exp_avg_base, const int16_t* exp_avg_sq_base,
                                   void* m_values, void* v_values, struct ihipStream_t* stream);
 
+/* ------------------------------------------------------------------ the residual block around a recurrence
+ *
+ * What stands before and behind the scan (or the gated recurrence below) in a model: the sum of the stream with a
+ * branch, dropout of that branch, the norm of the sum.  Conventions as above: device pointers, 16-byte aligned bases,
+ * host-side checks before any launch, asynchronous on `stream`, no allocation, sums in fp32 in a fixed order (bitwise
+ * reproducible). */
+
+/* A dropout mask, which is never stored.  The elements of a tensor are numbered in memory order; elements 8 j .. 8 j + 7
+ * take the four 32-bit words that Philox4x32 with ten rounds (Salmon, Moraes, Dror, Shaw: Parallel random numbers: as
+ * easy as 1, 2, 3; SC 2011) gives for the counter (j, call) (64 bits each, low words first) and the key `seed`: 16 bits
+ * each, the low half of a word first.  With T = 65536 p rounded to the nearest integer, an element is kept where its 16
+ * bits are T or more, and is then multiplied by 65536 / (65536 - T); the others are zero, whatever they were. */
+typedef struct ssm_dropout {
+  double p;                     /* in [0, 1] */
+  uint64_t seed;
+  const int64_t* device_seed;   /* a seed on the device instead (8-byte aligned; read when the kernels run, so that
+                                   the replays of a graph may take new ones), or NULL */
+  uint64_t call;                /* tells the calls under one seed apart */
+} ssm_dropout;
+
+/* out = residual + dropout(x), rounded once to out_dtype.  x : [numel] x_dtype; residual : [numel] out_dtype, NULL means
+ * zero.  The gradient of x is the same call on the output's gradient without a residual. */
+ssm_status ssm_dropout_fwd(int64_t numel, int32_t x_dtype, int32_t out_dtype, const void* x, const void* residual,
+                           const ssm_dropout* drop, void* out, struct ihipStream_t* stream);
+
+#define SSM_FLAG_RMS 4u /* ssm_norm_shape.flags: RMS norm (the mean is not taken out) */
+
+typedef struct ssm_norm_shape {
+  int64_t batch;        /* B >= 1 */
+  int64_t seqlen;       /* L >= 1; B * L below 2^31 */
+  int64_t dim;          /* E in [1, 2^30], what is normalised over */
+  int32_t x_dtype;      /* ssm_dtype of x and out (backward: dout and dx) */
+  int32_t hidden_dtype; /* ssm_dtype of residual and hidden: SSM_F32, or x_dtype */
+  uint32_t flags;       /* SSM_FLAG_CHANNELS_FIRST: [B, E, L] instead of [B, L, E]; SSM_FLAG_RMS */
+} ssm_norm_shape;
+
+/* The norm of a sum:
+ *   s = residual + dropout(x);  m = mean of s over E (RMS: 0);  f = 1 / sqrt(mean of (s - m)^2 + eps)
+ *   out = (s - m) f weight + bias;  hidden = s
+ * both outputs rounded once (out is made from the unrounded s).
+ *   x, out            : [B, L, E] or [B, E, L], x_dtype
+ *   residual, hidden  : as x, hidden_dtype; NULL: zero, not written
+ *   weight, bias      : [E] fp32, NULL means one, zero
+ *   eps               : finite, not negative
+ *   drop              : NULL means no dropout
+ *   stats             : [2, B * L] fp32: all m, then all f; NULL means not written */
+ssm_status ssm_layer_norm_fwd(const ssm_norm_shape* shape, const void* x, const float* weight, const float* bias,
+                              const void* residual, double eps, const ssm_dropout* drop, void* out, void* hidden,
+                              float* stats, struct ihipStream_t* stream);
+
+/* Bytes of device workspace ssm_layer_norm_bwd needs for dweight and dbias (0 for an invalid shape). */
+size_t ssm_layer_norm_bwd_workspace_size(const ssm_norm_shape* shape);
+
+/* Gradients of ssm_layer_norm_fwd from its hidden (x itself where there was neither residual nor dropout) and stats.  With
+ * xh = (hidden - m) f and g = dout weight:
+ *   ds = f (g - mean(g) - xh mean(g xh)) + dhidden   (RMS: without mean(g))
+ *   dresidual = ds;  dx = dropout(ds);  dweight = sum over B and L of dout xh;  dbias = sum over B and L of dout
+ *   dout, dx            : x_dtype;  hidden, dhidden (gradient of hidden, NULL means zero), dresidual : hidden_dtype
+ *   drop                : that of the forward call
+ *   dx, dresidual       : NULL means not written (one of them is required)
+ *   dweight, dbias      : [E] fp32, NULL means not computed
+ *   workspace           : required with dweight or dbias, at least ssm_layer_norm_bwd_workspace_size() bytes */
+ssm_status ssm_layer_norm_bwd(const ssm_norm_shape* shape, const void* dout, const void* hidden, const float* weight,
+                              const float* stats, const void* dhidden, const ssm_dropout* drop, void* dx, void* dresidual,
+                              float* dweight, float* dbias, void* workspace, size_t workspace_bytes,
+                              struct ihipStream_t* stream);
+
+typedef struct ssm_recurrence_shape {
+  int64_t batch;    /* B >= 1 */
+  int64_t dim;      /* D >= 1; B * D below 2^31 */
+  int64_t seqlen;   /* L >= 1 */
+  int32_t io_dtype; /* ssm_dtype of x, r, i, z, out and their gradients */
+  uint32_t flags;   /* SSM_FLAG_REVERSE: from t = L-1 down to 0 */
+} ssm_recurrence_shape;
+
+/* A gated linear recurrence, one state per channel:
+ *   a[t] = exp(-decay[d] sigmoid(r[b,d,t] + r_bias[d]))
+ *   h[t] = a[t] h[t-1] + sqrt(1 - a[t]^2) sigmoid(i[b,d,t] + i_bias[d]) x[b,d,t]
+ *   out[b,d,t] = h[t] silu(z[b,d,t])
+ *   x, r, i, z, out : [B, D, L] io_dtype; z NULL means no gate (out = h)
+ *   decay           : [D] fp32, not negative (a channel with a negative decay gives NaN)
+ *   r_bias, i_bias  : [D] fp32, NULL means zero
+ *   initial_state   : [B, D] fp32, NULL means zero;  final_state : [B, D] fp32, NULL means not written
+ *   checkpoints     : [B, D, ssm_recurrence_checkpoints()] fp32 for ssm_recurrence_bwd, NULL means not written.  With C =
+ *                     512 (fp32: 256) and m = (b D + d) L mod 8 (fp32: mod 4; reverse: -(b D + d + 1) L), number k is
+ *                     the state after min(L, max(0, C k - m)) steps.
+ *   workspace       : at least ssm_recurrence_workspace_size() bytes (0: NULL will do) */
+int64_t ssm_recurrence_checkpoints(const ssm_recurrence_shape* shape);
+size_t ssm_recurrence_workspace_size(const ssm_recurrence_shape* shape);
+ssm_status ssm_recurrence_fwd(const ssm_recurrence_shape* shape, const void* x, const void* r, const void* i,
+                              const float* decay, const float* r_bias, const float* i_bias, const void* z,
+                              const float* initial_state, void* out, float* final_state, float* checkpoints,
+                              void* workspace, size_t workspace_bytes, struct ihipStream_t* stream);
+
+/* Bytes of device workspace ssm_recurrence_bwd needs (0 for an invalid shape), with the checkpoints given (saved != 0) or
+ * without. */
+size_t ssm_recurrence_bwd_workspace_size(const ssm_recurrence_shape* shape, int32_t saved);
+
+/* Gradients of ssm_recurrence_fwd, from its inputs.
+ *   dout                   : [B, D, L] io_dtype;  dfinal_state : [B, D] fp32, NULL means zero
+ *   checkpoints            : what the forward call wrote for the same inputs; NULL: they are made again
+ *   dx, dr, di             : [B, D, L] io_dtype;  dz : the same, required with z, else ignored
+ *   ddecay                 : [D] fp32;  dr_bias, di_bias : [D] fp32, NULL means not computed
+ *   dinitial_state         : [B, D] fp32, NULL means not written
+ *   workspace              : required, at least ssm_recurrence_bwd_workspace_size() bytes
+ * The root has no finite slope at a = 1: 1 / sqrt(1 - a^2) is taken at 1 - a^2 = 2^-100 where that is less.  With a decay
+ * of zero ddecay is then a large number that stands for an infinite one; every other gradient is exact there. */
+ssm_status ssm_recurrence_bwd(const ssm_recurrence_shape* shape, const void* x, const void* r, const void* i,
+                              const float* decay, const float* r_bias, const float* i_bias, const void* z,
+                              const float* initial_state, const void* dout, const float* dfinal_state,
+                              const float* checkpoints, void* dx, void* dr, void* di, void* dz, float* ddecay,
+                              float* dr_bias, float* di_bias, float* dinitial_state, void* workspace,
+                              size_t workspace_bytes, struct ihipStream_t* stream);
+
+/* One generation step of the recurrence: state [B, D] fp32, read and written; x, r, i, z, out : [B, D] io_dtype. */
+ssm_status ssm_recurrence_update(int64_t batch, int64_t dim, int32_t io_dtype, float* state, const void* x, const void* r,
+                                 const void* i, const float* decay, const float* r_bias, const float* i_bias,
+                                 const void* z, void* out, struct ihipStream_t* stream);
+
 #ifdef __cplusplus
 }
 #endif

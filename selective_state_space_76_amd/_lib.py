@@ -41,6 +41,21 @@ class ssm_embed_shape(ctypes.Structure):
                 ("io_dtype", ctypes.c_int32), ("flags", ctypes.c_uint32)]
 
 
+class ssm_dropout(ctypes.Structure):
+    _fields_ = [("p", ctypes.c_double), ("seed", ctypes.c_uint64), ("device_seed", ctypes.c_void_p),
+                ("call", ctypes.c_uint64)]
+
+
+class ssm_norm_shape(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int64), ("seqlen", ctypes.c_int64), ("dim", ctypes.c_int64),
+                ("x_dtype", ctypes.c_int32), ("hidden_dtype", ctypes.c_int32), ("flags", ctypes.c_uint32)]
+
+
+class ssm_recurrence_shape(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int64), ("dim", ctypes.c_int64), ("seqlen", ctypes.c_int64),
+                ("io_dtype", ctypes.c_int32), ("flags", ctypes.c_uint32)]
+
+
 class ssm_adamw_config(ctypes.Structure):
     _fields_ = [("lr", ctypes.c_double), ("beta1", ctypes.c_double), ("beta2", ctypes.c_double),
                 ("eps", ctypes.c_double), ("weight_decay", ctypes.c_double), ("step", ctypes.c_int64),
@@ -54,7 +69,9 @@ EXPORTS = ("ssm_abi_version", "ssm_status_str", "ssm_scan_workspace_size", "ssm_
            "ssm_scan_bwd_saved", "ssm_conv1d_fwd", "ssm_conv1d_update",
            "ssm_conv1d_bwd_workspace_size", "ssm_conv1d_bwd", "ssm_embedding_fwd", "ssm_embedding_bwd_workspace_size",
            "ssm_embedding_bwd", "ssm_grad_norm_workspace_size", "ssm_grad_norm", "ssm_adamw_step", "ssm_adamw_clipped_step",
-           "ssm_adamw_state_values")
+           "ssm_adamw_state_values", "ssm_dropout_fwd", "ssm_layer_norm_fwd", "ssm_layer_norm_bwd_workspace_size",
+           "ssm_layer_norm_bwd", "ssm_recurrence_checkpoints", "ssm_recurrence_workspace_size", "ssm_recurrence_fwd",
+           "ssm_recurrence_bwd_workspace_size", "ssm_recurrence_bwd", "ssm_recurrence_update")
 
 
 def load() -> ctypes.CDLL:
@@ -115,6 +132,27 @@ def load() -> ctypes.CDLL:
     lib.ssm_adamw_clipped_step.restype = ctypes.c_int
     lib.ssm_adamw_state_values.argtypes = [i64] + [vp] * 7
     lib.ssm_adamw_state_values.restype = ctypes.c_int
+    sz, norm, recur = ctypes.c_size_t, ctypes.POINTER(ssm_norm_shape), ctypes.POINTER(ssm_recurrence_shape)
+    lib.ssm_dropout_fwd.argtypes = [i64, i32, i32, vp, vp, ctypes.POINTER(ssm_dropout), vp, vp]
+    lib.ssm_dropout_fwd.restype = ctypes.c_int
+    lib.ssm_layer_norm_fwd.argtypes = [norm, vp, vp, vp, vp, ctypes.c_double, ctypes.POINTER(ssm_dropout)] + [vp] * 4
+    lib.ssm_layer_norm_fwd.restype = ctypes.c_int
+    lib.ssm_layer_norm_bwd_workspace_size.argtypes = [norm]
+    lib.ssm_layer_norm_bwd_workspace_size.restype = sz
+    lib.ssm_layer_norm_bwd.argtypes = [norm] + [vp] * 5 + [ctypes.POINTER(ssm_dropout)] + [vp] * 5 + [sz, vp]
+    lib.ssm_layer_norm_bwd.restype = ctypes.c_int
+    lib.ssm_recurrence_checkpoints.argtypes = [recur]
+    lib.ssm_recurrence_checkpoints.restype = i64
+    lib.ssm_recurrence_workspace_size.argtypes = [recur]
+    lib.ssm_recurrence_workspace_size.restype = sz
+    lib.ssm_recurrence_fwd.argtypes = [recur] + [vp] * 12 + [sz, vp]
+    lib.ssm_recurrence_fwd.restype = ctypes.c_int
+    lib.ssm_recurrence_bwd_workspace_size.argtypes = [recur, i32]
+    lib.ssm_recurrence_bwd_workspace_size.restype = sz
+    lib.ssm_recurrence_bwd.argtypes = [recur] + [vp] * 20 + [sz, vp]
+    lib.ssm_recurrence_bwd.restype = ctypes.c_int
+    lib.ssm_recurrence_update.argtypes = [i64, i64, i32] + [vp] * 9 + [vp]
+    lib.ssm_recurrence_update.restype = ctypes.c_int
     if lib.ssm_abi_version() != ABI_VERSION:
         raise ImportError("libssmscan.so ABI version %d, binding expects %d" % (lib.ssm_abi_version(), ABI_VERSION))
     _lib = lib

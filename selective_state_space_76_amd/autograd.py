@@ -1,4 +1,4 @@
-"""torch.autograd binding of the scan, the conv and the embedding.  The scan: forward through ssm_scan_fwd_save
+"""torch.autograd binding of the scan, the conv, the embedding and the residual block's operators.  The scan: forward through ssm_scan_fwd_save
 (the outputs plus the block checkpoints), backward through ssm_scan_bwd_saved.
 
     from selective_state_space_76_amd import selective_scan
@@ -18,7 +18,9 @@ import functools
 
 import torch
 
-from ._lib import checkpoints_shape, conv1d_fwd, scan_bwd, scan_fwd
+from ._lib import _io_dtype, checkpoints_shape, conv1d_fwd, scan_bwd, scan_fwd
+from .block import (dropout_bwd, dropout_fwd, layer_norm_bwd, layer_norm_fwd, recurrence_bwd, recurrence_checkpoints_shape,
+                    recurrence_fwd)
 from .training import conv1d_bwd, embedding_bwd, embedding_fwd
 
 
@@ -31,7 +33,7 @@ class _NoSecond(torch.autograd.Function):
 
     @staticmethod
     def backward(ctx, *grads):
-        raise RuntimeError("the gradients of the scan, the conv and the embedding cannot be differentiated again")
+        raise RuntimeError("the gradients of this package's operators cannot be differentiated again")
 
 
 def _first_order(backward):
@@ -146,3 +148,98 @@ class EmbeddingFn(torch.autograd.Function):
 def embedding(tokens, weight, *, scale=1.0, dtype=None, channels_first=False):
     """Differentiable embedding_fwd; the gradient comes in weight's dtype, summed in fp32 and rounded once."""
     return EmbeddingFn.apply(tokens, weight, scale, dtype, channels_first)
+
+
+def _seeds(seed):
+    """(what is kept for the backward pass as a tensor, as a number)."""
+    return (seed, None) if isinstance(seed, torch.Tensor) else (None, seed)
+
+
+class LayerNormFn(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, weight, bias, residual, seed, eps, rms, channels_first, p, call):
+        out, hidden, stats = layer_norm_fwd(x, weight, bias, residual, eps=eps, rms=rms, channels_first=channels_first, p=p,
+                                            seed=seed, call=call)
+        ctx.set_materialize_grads(False)
+        ctx.x_dtype = x.dtype
+        ctx.set = dict(rms=rms, channels_first=channels_first, p=p, call=call, residual=residual is not None,
+                       bias=bias is not None)
+        tensor, ctx.seed = _seeds(seed)
+        ctx.save_for_backward(hidden, weight, stats, tensor)
+        return (out,) if hidden is x else (out, hidden)
+
+    @staticmethod
+    @_first_order
+    def backward(ctx, dout, dhidden=None):
+        hidden, weight, stats, seed = ctx.saved_tensors
+        seed = ctx.seed if seed is None else seed
+        # (x's dtype is hidden's unless a residual in fp32 was added; an output without a gradient comes as None)
+        dout = None if dout is None else _dense(dout, dout.dtype)
+        dhidden = None if dhidden is None else _dense(dhidden, hidden.dtype)
+        if dout is None:
+            dout = torch.zeros(hidden.shape, dtype=ctx.x_dtype, device=hidden.device)
+        g = layer_norm_bwd(dout, hidden, weight, stats, dhidden=dhidden, seed=seed, **ctx.set)
+        need = ctx.needs_input_grad
+        return (g["dx"] if need[0] else None, g["dweight"] if need[1] else None, g["dbias"] if need[2] else None,
+                g["dresidual"] if need[3] else None, None, None, None, None, None, None)
+
+
+def layer_norm(x, weight=None, bias=None, residual=None, *, eps=1e-5, rms=False, channels_first=False, p=0.0, seed=None,
+               call=0):
+    """Differentiable layer_norm_fwd.  Returns out, or (out, hidden) where there is a residual or dropout; hidden may go
+    on as the residual of the next block, and its gradient is added on the way back."""
+    got = LayerNormFn.apply(x, weight, bias, residual, seed, eps, rms, channels_first, p, call)
+    return got if len(got) > 1 else got[0]
+
+
+class DropoutFn(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, residual, seed, p, call):
+        tensor, ctx.seed = _seeds(seed)
+        ctx.save_for_backward(tensor)
+        ctx.set = (p, call, x.dtype)
+        return dropout_fwd(x, p, seed, call=call, residual=residual)
+
+    @staticmethod
+    @_first_order
+    def backward(ctx, dout):
+        (seed,) = ctx.saved_tensors
+        p, call, dtype = ctx.set
+        dx = None
+        if ctx.needs_input_grad[0]:
+            dx = dropout_bwd(_dense(dout, dout.dtype), p, ctx.seed if seed is None else seed, call=call, dtype=dtype)
+        return dx, dout if ctx.needs_input_grad[1] else None, None, None, None
+
+
+def dropout(x, p, seed, *, call=0, residual=None):
+    """Differentiable dropout_fwd: residual + dropout(x)."""
+    return DropoutFn.apply(x, residual, seed, p, call)
+
+
+class GatedRecurrenceFn(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, r, i, decay, r_bias, i_bias, z, initial_state, reverse):
+        ck = None
+        if any(ctx.needs_input_grad[:8]):
+            ck = torch.empty(recurrence_checkpoints_shape(*x.shape, _io_dtype(x)), dtype=torch.float32, device=x.device)
+        out, last = recurrence_fwd(x, r, i, decay, r_bias, i_bias, z, initial_state, reverse=reverse, checkpoints=ck)
+        ctx.set_materialize_grads(False)
+        ctx.save_for_backward(x, r, i, decay, r_bias, i_bias, z, initial_state, ck)
+        ctx.reverse = reverse
+        return out, last
+
+    @staticmethod
+    @_first_order
+    def backward(ctx, dout, dlast):
+        *ins, ck = ctx.saved_tensors
+        dout = torch.zeros_like(ins[0]) if dout is None else _dense(dout, ins[0].dtype)
+        dlast = None if dlast is None else _dense(dlast, torch.float32)
+        g = recurrence_bwd(*ins, dout=dout, dfinal_state=dlast, reverse=ctx.reverse, checkpoints=ck)
+        names = ("dx", "dr", "di", "ddecay", "dr_bias", "di_bias", "dz", "dinitial_state")
+        return tuple(g[k] if need and t is not None else None
+                     for k, t, need in zip(names, ins, ctx.needs_input_grad)) + (None,)
+
+
+def gated_recurrence(x, r, i, decay, r_bias=None, i_bias=None, z=None, initial_state=None, *, reverse=False):
+    """Differentiable recurrence_fwd: (out [B,D,L], final_state [B,D] fp32), with gradients of every tensor given."""
+    return GatedRecurrenceFn.apply(x, r, i, decay, r_bias, i_bias, z, initial_state, reverse)

@@ -1,0 +1,113 @@
+// block_launch.h -- internal interface between the residual block's C entry points (block_abi.cpp) and their
+// gfx950 kernels: layer norm, dropout, the gated linear recurrence.  Not installed; not part of the public ABI.
+#pragma once
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "../train/train_launch.h"
+
+namespace ssm {
+
+// ---- dropout (block_device.h, dropout.hip): what a kernel needs to know of a mask
+struct DropParams {
+  const int64_t* device_seed;  // the seed on the device, or null: then `seed`
+  uint64_t seed, call;
+  uint32_t below;              // elements whose 16 bits are below this are dropped; 0: no dropout
+  float scale;                 // of the others
+};
+
+struct DropoutParams {
+  const void* x;
+  const void* residual;  // or null
+  void* out;
+  int64_t n;
+  DropParams drop;
+};
+hipError_t launch_dropout(const DropoutParams& p, bool x_bf16, bool out_bf16, hipStream_t s);
+
+// ---- layer norm (norm_rows.hip: [rows, E]; norm_cols.hip: [B, E, L])
+struct NormParams {
+  const void* x;         // forward; backward: dout
+  const void* residual;  // forward, or null; backward: hidden
+  const float* weight;   // or null (ones)
+  const float* bias;     // forward, or null
+  void* out;             // forward; backward: dx, or null
+  void* hidden;          // forward, or null; backward: dresidual, or null
+  const void* dhidden;   // backward, or null
+  float* stats;          // [2][rows]: means and factors; forward: or null
+  float* part;           // backward: [blocks][2][E] partial sums of dweight and dbias, or null
+  float* dweight;        // backward, or null
+  float* dbias;
+  int64_t rows, E, B, L;
+  int64_t blocks;        // backward: workgroups, each with its partial sums
+  float eps, inv_e;
+  int rms;
+  DropParams drop;
+};
+// kind: bit 0 bf16 x, bit 1 bf16 hidden
+hipError_t launch_norm_rows(const NormParams& p, int kind, hipStream_t s);
+hipError_t launch_norm_cols(const NormParams& p, int kind, hipStream_t s);
+int64_t norm_rows_bwd_blocks(int64_t rows, int64_t E);
+int64_t norm_cols_bwd_blocks(int64_t B, int64_t L, int64_t E, int kind);
+hipError_t launch_norm_rows_bwd(const NormParams& p, int kind, hipStream_t s);
+hipError_t launch_norm_cols_bwd(const NormParams& p, int kind, hipStream_t s);
+// dweight and dbias from p.blocks partial sums
+hipError_t launch_norm_join(const NormParams& p, hipStream_t s);
+
+// ---- gated linear recurrence (recur_fwd.hip, recur_bwd.hip)
+struct RecurPlan {
+  int lanes = 64;       // lanes per row: 16 or 64
+  int waves = 1;        // waves that share a row: 1 or 4
+  int64_t S = 1;        // segments of a row
+  int64_t blocks = 0;   // blocks of 64 pieces in a row, each with a checkpoint
+  int64_t tiles = 0;    // turns of a row's team
+  int64_t per = 0;      // tiles in a segment
+};
+RecurPlan recur_plan(int64_t B, int64_t D, int64_t L, bool bf16);
+
+struct RecurParams {
+  const void* x;      // [B,D,L]
+  const void* r;
+  const void* i;
+  const void* z;      // or null
+  const float* decay; // [D]
+  const float* rb;    // [D] or null (zeros)
+  const float* ib;
+  const float* init;  // [B,D] or null (zeros)
+  void* out;          // forward; null: checkpoints only
+  float* last;        // [B,D] or null
+  float* ckpt;        // [B,D,blocks]: written by the forward pass (or null), read by the backward
+  float* seg;         // [S][B*D][2]: what a segment makes of the state that enters it, S > 1
+  // backward
+  const void* dout;
+  const float* dlast; // [B,D] or null (zeros)
+  void* dx;
+  void* dr;
+  void* di;
+  void* dz;           // with z
+  float* dinit;       // [B,D] or null
+  float* part;        // [B*S*waves][3][D]
+  float* ddecay;      // [D]
+  float* drb;         // or null
+  float* dib;
+  int64_t B, D, L;
+  RecurPlan plan;
+};
+hipError_t launch_recur_fwd(const RecurParams& p, bool bf16, bool reverse, hipStream_t s);
+hipError_t launch_recur_bwd(const RecurParams& p, bool bf16, bool reverse, hipStream_t s);
+
+struct RecurStepParams {
+  float* state;       // [B,D]
+  const void* x;      // [B,D]
+  const void* r;
+  const void* i;
+  const void* z;      // or null
+  const float* decay;
+  const float* rb;
+  const float* ib;
+  void* out;
+  int64_t n, D;
+};
+hipError_t launch_recur_step(const RecurStepParams& p, bool bf16, hipStream_t s);
+
+}  // namespace ssm

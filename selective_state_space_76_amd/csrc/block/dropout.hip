@@ -1,0 +1,35 @@
+// dropout.hip -- out = residual + dropout(x), and (without a residual) the gradient, which is the same mask on dout.
+//
+// The mask is made from the elements' numbers (block_device.h) and never stored.  Bound by HBM: x and the residual are
+// read once, the output is written once.  A lane owns 8 aligned elements, one counter of the generator.
+#include "block_device.h"
+
+namespace ssm {
+
+template <typename XT, typename OT>
+__global__ __launch_bounds__(256) void dropout_kernel(DropoutParams p) {
+  const int64_t i = ((int64_t)block_id() * 256 + threadIdx.x) * 8;
+  if (i >= p.n) return;
+  const int n = p.n - i < 8 ? (int)(p.n - i) : 8;
+  float x[8], r[8];
+  load_n<XT, 8, true>(static_cast<const XT*>(p.x) + i, n, x);
+  if (p.residual) load_n<OT, 8, true>(static_cast<const OT*>(p.residual) + i, n, r);
+  const Drop drop(p.drop);
+  if (drop.any()) drop.apply(drop.kept((uint64_t)i), x);
+  if (p.residual) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[e] += r[e];
+  }
+  store_n<OT, 8>(static_cast<OT*>(p.out) + i, n, x);
+}
+
+hipError_t launch_dropout(const DropoutParams& p, bool x_bf16, bool out_bf16, hipStream_t s) {
+  const dim3 grid = grid_of(((p.n + 7) / 8 + 255) / 256), block(256);
+  if (x_bf16 && out_bf16) hipLaunchKernelGGL((dropout_kernel<bf16_t, bf16_t>), grid, block, 0, s, p);
+  else if (x_bf16) hipLaunchKernelGGL((dropout_kernel<bf16_t, float>), grid, block, 0, s, p);
+  else if (out_bf16) hipLaunchKernelGGL((dropout_kernel<float, bf16_t>), grid, block, 0, s, p);
+  else hipLaunchKernelGGL((dropout_kernel<float, float>), grid, block, 0, s, p);
+  return hipGetLastError();
+}
+
+}  // namespace ssm

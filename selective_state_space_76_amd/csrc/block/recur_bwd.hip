@@ -1,0 +1,256 @@
+// recur_bwd.hip -- gradients of the gated linear recurrence (recur_fwd.hip).
+//
+//   G[t] = dout silu(z) + F[t+1],  F[t] = a[t] G[t]  (F behind the last step: the final state's gradient)
+//   dx = G q sig(i);  di = G q x sig(i) (1 - sig(i));  dz = dout h silu'(z);  d(initial state) = F[0]
+//   dla = G (a h[t-1] - sig(i) x a^2 / q);  dr = -decay dla sig(r) (1 - sig(r));  ddecay = -sum dla sig(r)
+//   drb = sum dr;  dib = sum di
+//
+// Bound by HBM: x, r, i, dout (and z) are read once, their gradients written once (14 or 18 bytes a step in bf16).  The
+// states are made again from the checkpoints of the forward pass, one for every 64 pieces, so that a wave needs no
+// other's; the adjoint F is an affine recurrence against time, walked as the forward pass walks the states (teams of
+// waves through LDS, segments for few rows).  ddecay and the biases' gradients are summed per wave and joined by a
+// second kernel in a fixed order.
+#include "recur_device.h"
+
+namespace ssm {
+
+// MAPS: the segments' maps of the adjoint
+template <typename IO, int LN, int W, bool REV, bool MAPS>
+__global__ __launch_bounds__(256) void recur_bwd_kernel(RecurParams p) {
+  constexpr int V = 16 / (int)sizeof(IO);
+  constexpr int UNITS = 256 / (LN * W);
+  constexpr int TURN = LN * W * V;
+  __shared__ float sm[2][W][2];
+  const int lane = threadIdx.x % LN, w = W > 1 ? threadIdx.x / 64 : 0;
+  const int64_t S = MAPS ? p.plan.S - 1 : p.plan.S;
+  const int64_t rows = p.B * p.D;
+  int64_t unit = (int64_t)block_id() * UNITS + (W > 1 ? 0 : threadIdx.x / LN);
+  if (unit >= rows * S) return;
+  if (W > 1 || LN == 64) unit = __builtin_amdgcn_readfirstlane((int)unit);
+  const int64_t row = unit / S, seg = unit - row * S + (MAPS ? 1 : 0);  // (the first segment's map is not needed)
+  const int64_t b = row / p.D, d = row - b * p.D;
+  const Row<IO, REV> line(row, p.L);
+  const Channel ch(p.decay, p.rb, p.ib, d);
+  const float decay = p.decay[d];
+  const int64_t k0 = seg * p.plan.per, k1 = k0 + p.plan.per < p.plan.tiles ? k0 + p.plan.per : p.plan.tiles;
+
+  float carry = 0.0f, whole = 1.0f;
+  if (!MAPS) {
+    carry = p.dlast ? p.dlast[row] : 0.0f;
+    if (p.plan.S > 1) {  // the segments behind, one a lane
+      const int l = threadIdx.x & 63;
+      float A = 1.0f, B = 0.0f;
+      if (l > seg && l < p.plan.S) {
+        A = p.seg[(l * rows + row) * 2];
+        B = p.seg[(l * rows + row) * 2 + 1];
+      }
+      scan_down<64>(A, B);
+      carry = __builtin_fmaf(lane_of(A, 0), carry, lane_of(B, 0));
+    }
+  }
+
+  const u32x4a none = {0u, 0u, 0u, 0u};
+  u32x4a xn = none, rn = none, in = none, zn = none, gn = none;
+  float hn = 0.0f;
+  auto load = [&](int64_t tile) {
+    const int64_t s = tile * TURN + (w * LN + lane) * V, at = line.at(s);
+    const int lo = line.lo(s), hi = line.hi(s);
+    rn = load_slots<IO, REV>(p.r, at, lo, hi);
+    gn = load_slots<IO, REV>(p.dout, at, lo, hi);
+    if (p.z) zn = load_slots<IO, REV>(p.z, at, lo, hi);
+    if (!MAPS) {
+      xn = load_slots<IO, REV>(p.x, at, lo, hi);
+      in = load_slots<IO, REV>(p.i, at, lo, hi);
+      const int64_t block = LN == 64 ? tile * W + w : 0;
+      hn = p.ckpt[row * p.plan.blocks + (block < p.plan.blocks ? block : p.plan.blocks - 1)];
+    }
+  };
+  float sd = 0.0f, sr = 0.0f, si = 0.0f;
+  float state = 0.0f;  // LN = 16: the state that enters the first tile; the others' by walking up first
+  if (k0 < k1) load(k1 - 1);
+  for (int64_t tile = k1 - 1; tile >= k0; --tile) {
+    const u32x4a xq = xn, rq = rn, iq = in, zq = zn, gq = gn;
+    state = hn;
+    if (tile > k0) load(tile - 1);
+    const int64_t s = tile * TURN + (w * LN + lane) * V;
+    const int lo = line.lo(s), hi = line.hi(s);
+    float a[V], v[V], g[V], sig[V], sgi[V], wq[V], hb[V];
+    float A = 1.0f, B = 0.0f, FA = 1.0f, FB = 0.0f;
+#pragma unroll
+    for (int e = 0; e < V; ++e) {
+      const Gates q(slot<IO, REV>(rq, e), slot<IO, REV>(iq, e), ch);
+      a[e] = q.a;
+      sig[e] = q.sr;
+      sgi[e] = q.si;
+      wq[e] = q.w;
+      v[e] = __builtin_amdgcn_sqrtf(q.w) * q.si * slot<IO, REV>(xq, e);
+      g[e] = slot<IO, REV>(gq, e);
+      if (p.z) g[e] *= silu_(slot<IO, REV>(zq, e));
+      if (e < lo || e >= hi) {
+        a[e] = 1.0f;
+        v[e] = g[e] = 0.0f;
+      }
+      A *= a[e];
+      B = __builtin_fmaf(a[e], B, v[e]);
+    }
+#pragma unroll
+    for (int e = V - 1; e >= 0; --e) {
+      FB = a[e] * (g[e] + FB);
+      FA *= a[e];
+    }
+    scan_down<LN>(FA, FB);
+    const float ta = end_lane<LN, false>(FA), tb = end_lane<LN, false>(FB);
+    float behind = carry;
+    if constexpr (W == 1) {
+      carry = __builtin_fmaf(ta, carry, tb);
+      whole *= ta;
+    } else {
+      float (*q)[2] = sm[tile & 1];
+      if ((threadIdx.x & 63) == 0) {
+        q[w][0] = ta;
+        q[w][1] = tb;
+      }
+      __syncthreads();
+#pragma unroll
+      for (int k = W - 1; k >= 0; --k) {
+        if (k == w) behind = carry;
+        carry = __builtin_fmaf(q[k][0], carry, q[k][1]);
+        whole *= q[k][0];
+      }
+    }
+    if (MAPS) continue;
+
+    // the states: hb before each step
+    if (LN == 16 && tile > 0) {  // up to here from the row's beginning (at most three turns of 16 pieces)
+      for (int64_t k = 0; k < tile; ++k) {
+        const int64_t sk = k * TURN + lane * V, at = line.at(sk);
+        const int lk = line.lo(sk), hk = line.hi(sk);
+        const u32x4a x0 = load_slots<IO, REV>(p.x, at, lk, hk), r0 = load_slots<IO, REV>(p.r, at, lk, hk);
+        const u32x4a i0 = load_slots<IO, REV>(p.i, at, lk, hk);
+        float UA = 1.0f, UB = 0.0f;
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+          if (e < lk || e >= hk) continue;
+          const Gates q(slot<IO, REV>(r0, e), slot<IO, REV>(i0, e), ch);
+          UA *= q.a;
+          UB = __builtin_fmaf(q.a, UB, __builtin_amdgcn_sqrtf(q.w) * q.si * slot<IO, REV>(x0, e));
+        }
+        scan_up<LN>(UA, UB);
+        state = __builtin_fmaf(end_lane<LN, true>(UA), state, end_lane<LN, true>(UB));
+      }
+    }
+    scan_up<LN>(A, B);
+    float h = __builtin_fmaf(lane_before<LN>(A, 1.0f), state, lane_before<LN>(B, 0.0f));
+#pragma unroll
+    for (int e = 0; e < V; ++e) {
+      hb[e] = h;
+      h = __builtin_fmaf(a[e], h, v[e]);
+    }
+    // the adjoint, and with it the gradients
+    float F = __builtin_fmaf(lane_behind<LN>(FA, 1.0f), behind, lane_behind<LN>(FB, 0.0f));
+    float dx[V], dr[V], di[V], dz[V];
+#pragma unroll
+    for (int e = V - 1; e >= 0; --e) {
+      const bool step = e >= lo && e < hi;
+      const float G = g[e] + F;
+      F = a[e] * G;
+      const float x = slot<IO, REV>(xq, e);
+      // 1 / q; where a is 1 to the last bit (sig(r) under 2^-100 / decay) what it meets below is zero
+      const float rq1 = __builtin_amdgcn_rsqf(fmaxf(wq[e], 7.888609e-31f)), q = wq[e] * rq1;
+      const float gs = G * sgi[e];
+      dx[e] = gs * q;
+      di[e] = gs * q * x * (1.0f - sgi[e]);
+      float dla = __builtin_fmaf(G * a[e], hb[e], -gs * x * (a[e] * a[e] * rq1));
+      dla = step ? dla : 0.0f;
+      const float dls = -dla * sig[e];
+      dr[e] = dls * decay * (1.0f - sig[e]);
+      sd += dls;
+      sr += dr[e];
+      si += step ? di[e] : 0.0f;
+      if (p.z) {
+        const float z = slot<IO, REV>(zq, e), s1 = sigmoid_(z), hh = __builtin_fmaf(a[e], hb[e], v[e]);
+        dz[e] = slot<IO, REV>(gq, e) * hh * (s1 * __builtin_fmaf(z, 1.0f - s1, 1.0f));
+      }
+    }
+    const int64_t at = line.at(s);
+    store_slots<IO, REV>(p.dx, at, lo, hi, dx);
+    store_slots<IO, REV>(p.dr, at, lo, hi, dr);
+    store_slots<IO, REV>(p.di, at, lo, hi, di);
+    if (p.z) store_slots<IO, REV>(p.dz, at, lo, hi, dz);
+  }
+  if (MAPS) {
+    if (lane == 0 && w == 0) {
+      p.seg[(seg * rows + row) * 2] = whole;
+      p.seg[(seg * rows + row) * 2 + 1] = carry;
+    }
+    return;
+  }
+  if (p.dinit && seg == 0 && lane == 0 && w == 0) p.dinit[row] = carry;
+  sd = sum_lanes<LN>(sd);
+  sr = sum_lanes<LN>(sr);
+  si = sum_lanes<LN>(si);
+  if (lane == 0) {
+    float* o = p.part + ((b * p.plan.S + seg) * W + w) * 3 * p.D + d;
+    o[0] = sd;
+    o[p.D] = sr;
+    o[2 * p.D] = si;
+  }
+}
+
+// ddecay and the biases' gradients from the waves' sums: 64 outputs per workgroup, the sums split over 4 waves,
+// each in order, then the waves' in order.
+__global__ __launch_bounds__(256) void recur_join_kernel(RecurParams p) {
+  const int64_t n = 3 * p.D, count = p.B * p.plan.S * p.plan.waves;
+  const int64_t i = (int64_t)block_id() * 64 + (threadIdx.x & 63);
+  const int64_t per = (count + 3) / 4;
+  const int64_t k0 = (threadIdx.x >> 6) * per, k1 = k0 + per < count ? k0 + per : count;
+  float s = 0.0f;
+  if (i < n) {
+    int64_t k = k0;
+    for (; k + 8 <= k1; k += 8) {
+      float v[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] = p.part[(k + e) * n + i];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) s += v[e];
+    }
+    for (; k < k1; ++k) s += p.part[k * n + i];
+  }
+  __shared__ float sm[256];
+  sm[threadIdx.x] = s;
+  __syncthreads();
+  if (threadIdx.x < 64 && i < n) {
+    s = sm[threadIdx.x] + sm[threadIdx.x + 64] + sm[threadIdx.x + 128] + sm[threadIdx.x + 192];
+    float* out = i < p.D ? p.ddecay : i < 2 * p.D ? p.drb : p.dib;
+    if (out) out[i % p.D] = s;
+  }
+}
+
+namespace {
+
+template <typename IO, bool REV>
+void go(const RecurParams& p, hipStream_t s) {
+  const int64_t rows = p.B * p.D;
+  if (p.plan.lanes == 16) {
+    hipLaunchKernelGGL((recur_bwd_kernel<IO, 16, 1, REV, false>), grid_of((rows + 15) / 16), dim3(256), 0, s, p);
+  } else if (p.plan.waves == 1) {
+    hipLaunchKernelGGL((recur_bwd_kernel<IO, 64, 1, REV, false>), grid_of((rows + 3) / 4), dim3(256), 0, s, p);
+  } else {
+    if (p.plan.S > 1)
+      hipLaunchKernelGGL((recur_bwd_kernel<IO, 64, 4, REV, true>), grid_of(rows * (p.plan.S - 1)), dim3(256), 0, s, p);
+    hipLaunchKernelGGL((recur_bwd_kernel<IO, 64, 4, REV, false>), grid_of(rows * p.plan.S), dim3(256), 0, s, p);
+  }
+}
+
+}  // namespace
+
+hipError_t launch_recur_bwd(const RecurParams& p, bool bf16, bool reverse, hipStream_t s) {
+  if (bf16) reverse ? go<bf16_t, true>(p, s) : go<bf16_t, false>(p, s);
+  else reverse ? go<float, true>(p, s) : go<float, false>(p, s);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL(recur_join_kernel, grid_of((3 * p.D + 63) / 64), dim3(256), 0, s, p);
+  return hipGetLastError();
+}
+
+}  // namespace ssm

@@ -1,0 +1,241 @@
+// recur_fwd.hip -- the gated linear recurrence over a sequence, and one step of it.
+//
+// Bound by HBM: x, r, i (and z) are read once, out is written once (8 or 10 bytes a step in bf16).  A step is an affine
+// map of the state; a lane composes those of its V steps, the wave those of its lanes (DPP), and the state that enters
+// the wave's 64 pieces then gives all states.  Rows are walked in turns of W * 64 pieces by a team of W waves, whose
+// maps go through LDS, so that the sequence is read once however long it is; the next turn's pieces are loaded before
+// the present one's arithmetic.  Where there are too few rows even for that, a row is cut into S segments and the first
+// launch makes each segment's map (reading x, r and i once more).
+#include "recur_device.h"
+
+namespace ssm {
+
+namespace {
+
+// The map of all of the team's lanes before this one's piece (A, B: the lane's own map before, the map of the lanes of
+// its wave before it after), and the state that enters the wave; carry: the state that enters the team, then leaves it.
+template <int LN, int W>
+__device__ __forceinline__ float enter_up(float& A, float& B, float& carry, float (*sm)[2], int w) {
+  scan_up<LN>(A, B);
+  const float ta = end_lane<LN, true>(A), tb = end_lane<LN, true>(B);
+  A = lane_before<LN>(A, 1.0f);
+  B = lane_before<LN>(B, 0.0f);
+  float in = carry;
+  if constexpr (W == 1) {
+    carry = __builtin_fmaf(ta, carry, tb);
+  } else {
+    if ((threadIdx.x & 63) == 0) {
+      sm[w][0] = ta;
+      sm[w][1] = tb;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < W; ++k) {
+      if (k == w) in = carry;
+      carry = __builtin_fmaf(sm[k][0], carry, sm[k][1]);
+    }
+  }
+  return in;
+}
+
+}  // namespace
+
+// MAPS: the segments' maps instead of the outputs
+template <typename IO, int LN, int W, bool REV, bool MAPS>
+__global__ __launch_bounds__(256) void recur_fwd_kernel(RecurParams p) {
+  constexpr int V = 16 / (int)sizeof(IO);
+  constexpr int UNITS = 256 / (LN * W);  // row segments per workgroup
+  constexpr int TURN = LN * W * V;       // slots
+  __shared__ float sm[2][W][2];
+  const int lane = threadIdx.x % LN, w = W > 1 ? threadIdx.x / 64 : 0;
+  const int64_t S = MAPS ? p.plan.S - 1 : p.plan.S;
+  const int64_t rows = p.B * p.D;
+  int64_t unit = (int64_t)block_id() * UNITS + (W > 1 ? 0 : threadIdx.x / LN);
+  const bool live = unit < rows * S;
+  if (W > 1 || LN == 64) {
+    if (!live) return;
+    unit = __builtin_amdgcn_readfirstlane((int)unit);
+  } else if (!live) {
+    return;
+  }
+  const int64_t row = unit / S, seg = unit - row * S, d = row % p.D;
+  const Row<IO, REV> line(row, p.L);
+  const Channel ch(p.decay, p.rb, p.ib, d);
+  const int64_t k0 = seg * p.plan.per, k1 = k0 + p.plan.per < p.plan.tiles ? k0 + p.plan.per : p.plan.tiles;
+
+  float carry = 0.0f, whole = 1.0f;
+  if (!MAPS) {
+    carry = p.init ? p.init[row] : 0.0f;
+    if (p.plan.S > 1) {  // the segments before, one a lane
+      const int l = threadIdx.x & 63;
+      float A = 1.0f, B = 0.0f;
+      if (l < seg) {
+        A = p.seg[(l * rows + row) * 2];
+        B = p.seg[(l * rows + row) * 2 + 1];
+      }
+      scan_up<64>(A, B);
+      carry = __builtin_fmaf(lane_of(A, 63), carry, lane_of(B, 63));
+    }
+  }
+
+  u32x4a xq, rq, iq, zq = {0u, 0u, 0u, 0u}, xn, rn, in, zn = {0u, 0u, 0u, 0u};
+  auto load = [&](int64_t tile) {
+    const int64_t s = tile * TURN + (w * LN + lane) * V, at = line.at(s);
+    const int lo = line.lo(s), hi = line.hi(s);
+    xn = load_slots<IO, REV>(p.x, at, lo, hi);
+    rn = load_slots<IO, REV>(p.r, at, lo, hi);
+    in = load_slots<IO, REV>(p.i, at, lo, hi);
+    if (!MAPS && p.z && p.out) zn = load_slots<IO, REV>(p.z, at, lo, hi);
+  };
+  if (k0 < k1) load(k0);
+  for (int64_t tile = k0; tile < k1; ++tile) {
+    xq = xn;
+    rq = rn;
+    iq = in;
+    zq = zn;
+    if (tile + 1 < k1) load(tile + 1);
+    const int64_t s = tile * TURN + (w * LN + lane) * V;
+    const int lo = line.lo(s), hi = line.hi(s);
+    float a[V], v[V];
+    float A = 1.0f, B = 0.0f;
+#pragma unroll
+    for (int e = 0; e < V; ++e) {
+      const Gates g(slot<IO, REV>(rq, e), slot<IO, REV>(iq, e), ch);
+      a[e] = g.a;
+      v[e] = __builtin_amdgcn_sqrtf(g.w) * g.si * slot<IO, REV>(xq, e);
+      if (e < lo || e >= hi) {
+        a[e] = 1.0f;
+        v[e] = 0.0f;
+      }
+      A *= a[e];
+      B = __builtin_fmaf(a[e], B, v[e]);
+    }
+    if (MAPS) {  // (the team's map, built up in `whole` and `carry`)
+      scan_up<LN>(A, B);
+      const float ta = end_lane<LN, true>(A), tb = end_lane<LN, true>(B);
+      if constexpr (W == 1) {
+        carry = __builtin_fmaf(ta, carry, tb);
+        whole *= ta;
+      } else {
+        float (*q)[2] = sm[tile & 1];
+        if ((threadIdx.x & 63) == 0) {
+          q[w][0] = ta;
+          q[w][1] = tb;
+        }
+        __syncthreads();
+#pragma unroll
+        for (int k = 0; k < W; ++k) {
+          carry = __builtin_fmaf(q[k][0], carry, q[k][1]);
+          whole *= q[k][0];
+        }
+      }
+      continue;
+    }
+    const float enter = enter_up<LN, W>(A, B, carry, sm[tile & 1], w);
+    const int64_t block = LN == 64 ? tile * W + w : tile;
+    if (p.ckpt && lane == 0 && block < p.plan.blocks && (LN == 64 || tile == 0)) p.ckpt[row * p.plan.blocks + block] = enter;
+    if (!p.out) continue;
+    float h = __builtin_fmaf(A, enter, B), o[V];
+#pragma unroll
+    for (int e = 0; e < V; ++e) {
+      h = __builtin_fmaf(a[e], h, v[e]);
+      o[e] = p.z ? h * silu_(slot<IO, REV>(zq, e)) : h;
+    }
+    store_slots<IO, REV>(p.out, line.at(s), lo, hi, o);
+  }
+  if (MAPS) {
+    if (lane == 0 && w == 0) {
+      p.seg[(seg * rows + row) * 2] = whole;
+      p.seg[(seg * rows + row) * 2 + 1] = carry;
+    }
+  } else if (p.last && seg == S - 1 && lane == 0 && w == 0) {
+    p.last[row] = carry;
+  }
+}
+
+// One step: the same gates, the state updated in place.  A lane owns V consecutive elements of [B, D].
+template <typename IO>
+__global__ __launch_bounds__(256) void recur_step_kernel(RecurStepParams p) {
+  constexpr int V = 16 / (int)sizeof(IO);
+  const int64_t at = ((int64_t)block_id() * 256 + threadIdx.x) * V;
+  if (at >= p.n) return;
+  const int n = p.n - at < V ? (int)(p.n - at) : V;
+  float x[V], r[V], i[V], z[V], h[V], o[V];
+  load_n<IO, V>(static_cast<const IO*>(p.x) + at, n, x);
+  load_n<IO, V>(static_cast<const IO*>(p.r) + at, n, r);
+  load_n<IO, V>(static_cast<const IO*>(p.i) + at, n, i);
+  if (p.z) load_n<IO, V>(static_cast<const IO*>(p.z) + at, n, z);
+  load_n<float, V>(p.state + at, n, h);
+  int64_t d = at % p.D;
+#pragma unroll
+  for (int e = 0; e < V; ++e) {
+    const Channel ch(p.decay, p.rb, p.ib, d);
+    const Gates g(r[e], i[e], ch);
+    h[e] = __builtin_fmaf(g.a, h[e], __builtin_amdgcn_sqrtf(g.w) * g.si * x[e]);
+    o[e] = p.z ? h[e] * silu_(z[e]) : h[e];
+    if (++d == p.D) d = 0;
+  }
+  store_n<float, V>(p.state + at, n, h);
+  store_n<IO, V>(static_cast<IO*>(p.out) + at, n, o);
+}
+
+// Short rows (up to two pieces a lane of 16) take 16 lanes each.  Longer ones take a wave; where there are fewer rows
+// than two waves for each of the 1024 SIMDs, four waves, if the row gives each of them a piece; and where that is still
+// too few, segments, up to 64 (a lane each for their maps), of two turns and more.
+RecurPlan recur_plan(int64_t B, int64_t D, int64_t L, bool bf16) {
+  const int64_t V = bf16 ? 8 : 4, rows = B * D;
+  RecurPlan pl;
+  pl.blocks = (L + V - 1 + 64 * V - 1) / (64 * V);
+  if (L <= 32 * V) {
+    pl.lanes = 16;
+  } else if (rows < 2048 && pl.blocks >= 4) {
+    pl.waves = 4;
+  }
+  const int64_t turn = pl.lanes * pl.waves * V;
+  pl.tiles = (L + V - 1 + turn - 1) / turn;
+  pl.per = pl.tiles;
+  if (pl.waves == 4 && rows < 512) {
+    int64_t S = (511 + rows) / rows;
+    if (S > pl.tiles / 2) S = pl.tiles / 2;
+    if (S > 64) S = 64;
+    if (S > 1) {
+      pl.per = (pl.tiles + S - 1) / S;
+      pl.S = (pl.tiles + pl.per - 1) / pl.per;
+    }
+  }
+  return pl;
+}
+
+namespace {
+
+template <typename IO, bool REV>
+void go(const RecurParams& p, hipStream_t s) {
+  const int64_t rows = p.B * p.D;
+  if (p.plan.lanes == 16) {
+    hipLaunchKernelGGL((recur_fwd_kernel<IO, 16, 1, REV, false>), grid_of((rows + 15) / 16), dim3(256), 0, s, p);
+  } else if (p.plan.waves == 1) {
+    hipLaunchKernelGGL((recur_fwd_kernel<IO, 64, 1, REV, false>), grid_of((rows + 3) / 4), dim3(256), 0, s, p);
+  } else {
+    if (p.plan.S > 1)
+      hipLaunchKernelGGL((recur_fwd_kernel<IO, 64, 4, REV, true>), grid_of(rows * (p.plan.S - 1)), dim3(256), 0, s, p);
+    hipLaunchKernelGGL((recur_fwd_kernel<IO, 64, 4, REV, false>), grid_of(rows * p.plan.S), dim3(256), 0, s, p);
+  }
+}
+
+}  // namespace
+
+hipError_t launch_recur_fwd(const RecurParams& p, bool bf16, bool reverse, hipStream_t s) {
+  if (bf16) reverse ? go<bf16_t, true>(p, s) : go<bf16_t, false>(p, s);
+  else reverse ? go<float, true>(p, s) : go<float, false>(p, s);
+  return hipGetLastError();
+}
+
+hipError_t launch_recur_step(const RecurStepParams& p, bool bf16, hipStream_t s) {
+  const int V = bf16 ? 8 : 4;
+  const dim3 grid = grid_of(((p.n + V - 1) / V + 255) / 256);
+  if (bf16) hipLaunchKernelGGL(recur_step_kernel<bf16_t>, grid, dim3(256), 0, s, p);
+  else hipLaunchKernelGGL(recur_step_kernel<float>, grid, dim3(256), 0, s, p);
+  return hipGetLastError();
+}
+
+}  // namespace ssm

@@ -90,24 +90,6 @@ __device__ __forceinline__ uint32_t of_lane(uint32_t v) {
   else return (uint32_t)__builtin_amdgcn_mov_dpp((int)v, LAST ? 0x15f : 0x150, 0xf, 0xf, true);
 }
 
-// sum over the group's lanes: rotations within rows of 16, then the four rows
-template <int LN>
-__device__ __forceinline__ float sum_lanes(float v) {
-  auto step = [&](auto ctrl) {
-    v += __uint_as_float(
-        (uint32_t)__builtin_amdgcn_mov_dpp((int)__float_as_uint(v), decltype(ctrl)::value, 0xf, 0xf, true));
-  };
-  step(IC<0x128>{});  // row_ror:8
-  step(IC<0x124>{});
-  step(IC<0x122>{});
-  step(IC<0x121>{});
-  if constexpr (LN == 64) {
-    auto row = [&](int l) { return __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(v), l)); };
-    v = (row(0) + row(16)) + (row(32) + row(48));
-  }
-  return v;
-}
-
 __device__ __forceinline__ float silu_slope(float a) {
   const float s = rcp_(1.0f + exp2_(-a * kLog2e));
   return s * __builtin_fmaf(a, 1.0f - s, 1.0f);

@@ -8,49 +8,12 @@
 #include <algorithm>
 
 #include "../../../include/ssm_scan.h"
+#include "abi_checks.h"
 #include "train_launch.h"
 
+using namespace ssm::abi;
+
 namespace {
-
-constexpr int64_t kMaxSize = int64_t(1) << 40;
-constexpr int64_t kMaxElems = int64_t(1) << 61;
-constexpr int64_t kMaxGrid = (int64_t(1) << 31) - 1;
-constexpr int64_t kMaxBlocks = (int64_t(1) << 24) - 1;  // of 256 threads, in a launch of one dimension
-
-struct Range {
-  uintptr_t lo, hi;  // [lo, hi)
-};
-
-Range span(const void* p, int64_t bytes) {
-  const uintptr_t a = reinterpret_cast<uintptr_t>(p);
-  return Range{a, p ? a + static_cast<uintptr_t>(bytes) : a};
-}
-
-bool overlaps(Range a, Range b) { return a.lo < b.hi && b.lo < a.hi; }
-
-bool misaligned(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) != 0; }
-
-bool mul_ok(int64_t a, int64_t b, int64_t* out) {
-  if (a <= 0 || b <= 0 || a > kMaxElems / b) return false;
-  *out = a * b;
-  return true;
-}
-
-bool dtype_ok(int32_t t) { return t == SSM_F32 || t == SSM_BF16; }
-int64_t dtype_size(int32_t t) { return t == SSM_BF16 ? 2 : 4; }
-
-ssm_status launch_status(hipError_t e) { return e == hipSuccess ? SSM_OK : SSM_ERR_LAUNCH; }
-
-// any of the outputs over an input or another output
-bool any_overlap(const Range* outs, size_t nout, const Range* ins, size_t nin) {
-  for (size_t i = 0; i < nout; ++i) {
-    for (size_t j = 0; j < nin; ++j)
-      if (overlaps(outs[i], ins[j])) return true;
-    for (size_t j = i + 1; j < nout; ++j)
-      if (overlaps(outs[i], outs[j])) return true;
-  }
-  return false;
-}
 
 struct ConvPlan {
   int64_t bd, bdl, S;

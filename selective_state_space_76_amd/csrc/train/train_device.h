@@ -1,4 +1,4 @@
-// train_device.h -- what the training operators' kernels share: pieces of rows at any alignment, and tokens.
+// train_device.h -- what the training operators' kernels share: pieces of rows at any alignment, tokens, sums over lanes.
 #pragma once
 #include <hip/hip_runtime.h>
 #include <stdint.h>
@@ -123,6 +123,24 @@ __device__ __forceinline__ void store_n(IO* p, int n, const float (&x)[N]) {
     for (int i = 0; i < N; ++i)
       if (i < n) store_io(p + i, x[i]);
   }
+}
+
+// sum over the lanes of a group of 16 or 64: rotations within rows of 16, then the four rows
+template <int LN>
+__device__ __forceinline__ float sum_lanes(float v) {
+  auto step = [&](auto ctrl) {
+    v += __uint_as_float(
+        (uint32_t)__builtin_amdgcn_mov_dpp((int)__float_as_uint(v), decltype(ctrl)::value, 0xf, 0xf, true));
+  };
+  step(IC<0x128>{});  // row_ror:8
+  step(IC<0x124>{});
+  step(IC<0x122>{});
+  step(IC<0x121>{});
+  if constexpr (LN == 64) {
+    auto row = [&](int l) { return __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(v), l)); };
+    v = (row(0) + row(16)) + (row(32) + row(48));
+  }
+  return v;
 }
 
 }  // namespace ssm
