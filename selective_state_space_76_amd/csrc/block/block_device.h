@@ -59,12 +59,14 @@ struct Drop {
         v[k] = w[k];
         v[4 + k] = next[k];
       }
+      // moved down by `at` halves: by masks, so that the words stay in registers
+      const uint32_t four = at & 4 ? ~0u : 0u, two = at & 2 ? ~0u : 0u, one = at & 1 ? ~0u : 0u;
 #pragma unroll
-      for (int k = 0; k < 6; ++k) v[k] = at & 4 ? v[k + 2] : v[k];  // (v[6] and v[7] are not looked at from here on)
+      for (int k = 0; k < 6; ++k) v[k] = (v[k + 2] & four) | (v[k] & ~four);  // (v[6], v[7]: not looked at from here on)
 #pragma unroll
-      for (int k = 0; k < 5; ++k) v[k] = at & 2 ? v[k + 1] : v[k];
+      for (int k = 0; k < 5; ++k) v[k] = (v[k + 1] & two) | (v[k] & ~two);
 #pragma unroll
-      for (int k = 0; k < 4; ++k) w[k] = at & 1 ? v[k] >> 16 | v[k + 1] << 16 : v[k];
+      for (int k = 0; k < 4; ++k) w[k] = ((v[k] >> 16 | v[k + 1] << 16) & one) | (v[k] & ~one);
     }
     uint32_t m = 0;
 #pragma unroll
@@ -77,5 +79,75 @@ struct Drop {
     for (int e = 0; e < 8; ++e) x[e] = kept >> e & 1u ? x[e] * scale : 0.0f;
   }
 };
+
+// What of a piece of 8 exists: its elements lo .. hi - 1.
+struct Part {
+  int lo, hi;
+  // of n elements, the 8 from i on
+  __device__ __forceinline__ Part(int64_t i, int64_t n)
+      : lo(i < 0 ? (int)-i : 0), hi(n - i >= 8 ? 8 : n - i > 0 ? (int)(n - i) : 0) {}
+  __device__ __forceinline__ Part() : lo(0), hi(0) {}
+  __device__ __forceinline__ bool whole() const { return hi - lo == 8; }
+  __device__ __forceinline__ bool any() const { return lo < hi; }
+  __device__ __forceinline__ bool has(int k) const { return k >= lo && k < hi; }
+};
+
+// 8 elements as they lie in memory, from any element on.  Loads of several pieces are to be in flight together, so
+// a piece begins as zeros, full() asks for all 8 where it may and does not wait, and part() reads what is left of one
+// that goes over the end of its tensor, when all others have been asked for.
+template <typename IO>
+struct Piece {
+  static constexpr int Q = (int)sizeof(IO) / 2;  // 16-byte words
+  u32x4a w[Q];
+  __device__ __forceinline__ void full(const IO* p, bool may) {
+#pragma unroll
+    for (int k = 0; k < Q; ++k) w[k] = u32x4a{0u, 0u, 0u, 0u};
+    if (may) {
+#pragma unroll
+      for (int k = 0; k < Q; ++k) {
+        const auto* a = reinterpret_cast<const typename Unaligned<IO>::type*>(p) + k;
+        // (of two words of one line the first must not drop it)
+        const auto q = Q == 1 ? __builtin_nontemporal_load(a) : *a;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[k][i] = q[i];
+      }
+    }
+  }
+  // the elements lo .. hi - 1 (one at least) of the piece at p, in one go: the others repeat the nearest
+  __device__ __forceinline__ void part(const IO* p, const Part& r) {
+    IO v[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = p[e < r.lo ? r.lo : e < r.hi ? e : r.hi - 1];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      if constexpr (Q == 1) w[0][e >> 1] = (e & 1 ? w[0][e >> 1] & 0xffffu : 0u) | (uint32_t)v[e] << (16 * (e & 1));
+      else w[e >> 2][e & 3] = __float_as_uint(v[e]);
+    }
+  }
+  // zeros for what does not exist
+  __device__ __forceinline__ void cut(const Part& r) {
+#pragma unroll
+    for (int k = 0; k < 4 * Q; ++k) {
+      if constexpr (Q == 1)
+        w[0][k] &= (r.has(2 * k) ? 0xffffu : 0u) | (r.has(2 * k + 1) ? 0xffff0000u : 0u);
+      else w[k >> 2][k & 3] = r.has(k) ? w[k >> 2][k & 3] : 0u;
+    }
+  }
+  __device__ __forceinline__ float at(int e) const {
+    if constexpr (Q == 1) return __uint_as_float(e & 1 ? w[0][e >> 1] & 0xffff0000u : w[0][e >> 1] << 16);
+    else return __uint_as_float(w[e >> 2][e & 3]);
+  }
+};
+
+template <typename IO>
+__device__ __forceinline__ void store_part(IO* p, const Part& r, const float (&x)[8]) {
+  if (r.whole()) {
+    store_n<IO, 8>(p, 8, x);
+  } else if (r.any()) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (r.has(e)) store_io(p + e, x[e]);
+  }
+}
 
 }  // namespace ssm

@@ -6,268 +6,401 @@
 //   ds = r (g - mean(g) - xh mean(g xh)) + dhidden (RMS: without mean(g));  dresidual = ds;  dx = dropout(ds)
 //   dw = sum over rows of dout xh;  db = sum over rows of dout
 //
-// Bound by HBM: every stream is read once and written once.  LN lanes (16, 64 or a workgroup) hold a row in registers,
-// P pieces of 8 elements each, so that the variance is a second pass over registers (about the mean, no cancellation).
-// out is made from the unrounded sum; the hidden that is kept for the backward pass is rounded to its type.
-// Rows too long for the registers go through memory again for each pass.
+// Bound by HBM: every stream is read once and written once.  A row's team (16, 32 or 64 lanes, or a workgroup of as many
+// waves as it takes) holds the row in registers, 8 elements a lane, so that the variance is a second pass over registers
+// (about the mean, no cancellation).  out is made from the unrounded sum; the hidden that is kept for the backward
+// pass is rounded to its type.  Where E is no multiple of 8 a row's pieces begin up to 7 elements before it, at a
+// multiple of 16 bytes (16384 x 767 in bf16 with a residual: 27.7 us; with pieces that begin where the row does 38.7).
+// Longer rows than a workgroup holds go through memory again for each pass.
+//
+// A lane holds one piece, two above 4096 elements: a row's loads are then all in flight at once, few instructions stand
+// between them and the stores, and what a call of few rows takes is one pass through a short kernel (256 x 2560: 3.5 us;
+// 6 pieces a lane, one wave a row: 12).  16384 x 768 in bf16 into a stream in fp32, with dropout (151 MB): 31 us, 4.9
+// TB/s (16 lanes a row, 6 pieces each: 39; two pieces 33); 16384 x 2048, bf16 with a residual: 45.6 us, 5.9 TB/s; 16384 x
+// 8176: 110 us, 4.9 TB/s (one piece a lane 131).  Rows in turn with the next one's loads under way take twice the
+// registers and gave 33, 49 and 141.
+//
+// Backward: 16384 x 768 as above: 39 us with the join of the sums, 5.1 TB/s; 16384 x 2048: 46.
 #include "block_device.h"
 
 namespace ssm {
 
 namespace {
 
-// sum over the LN lanes of a row's team, in all of them; sm: a float for each wave (LN = 256), used in turn
-template <int LN>
-__device__ __forceinline__ float sum_team(float v, float* sm) {
-  if constexpr (LN <= 64) {
-    return sum_lanes<LN>(v);
+// Lanes of a row's team with `each` pieces a lane; 0: rows that no team holds.
+int team_of(int64_t E, int each = 1) {
+  const int64_t n = (E + (E % 8 ? 7 : 0) + 7) / 8;
+  if (n <= 64) return n <= 16 ? 16 : n <= 32 ? 32 : 64;
+  const int64_t lanes = (n + each * 64 - 1) / (each * 64) * 64;
+  return lanes <= 1024 ? (int)lanes : 0;
+}
+constexpr int64_t kTwo = 4096;  // elements from which on a lane holds two pieces (forward)
+constexpr int kLong = 256;      // lanes of a row that no team holds
+
+// (a, b) summed over the team's lanes, in all of them; TEAM 0: the workgroup; sm: two floats for each of 16 waves
+template <int TEAM>
+__device__ __forceinline__ void sum_team(float& a, float& b, float (*sm)[2]) {
+  if constexpr (TEAM == 16 || TEAM == 64) {
+    a = sum_lanes<TEAM>(a);
+    b = sum_lanes<TEAM>(b);
+  } else if constexpr (TEAM == 32) {
+    a = sum_lanes<16>(a);
+    b = sum_lanes<16>(b);
+    a += __shfl_xor(a, 16);
+    b += __shfl_xor(b, 16);
   } else {
-    v = sum_lanes<64>(v);
-    if ((threadIdx.x & 63) == 0) sm[threadIdx.x >> 6] = v;
+    a = sum_lanes<64>(a);
+    b = sum_lanes<64>(b);
+    if ((threadIdx.x & 63) == 0) {
+      sm[threadIdx.x >> 6][0] = a;
+      sm[threadIdx.x >> 6][1] = b;
+    }
     __syncthreads();
-    return (sm[0] + sm[1]) + (sm[2] + sm[3]);
+    const int k = threadIdx.x & 15;
+    const bool wave = k < (int)(blockDim.x >> 6);
+    a = sum_lanes<16>(wave ? sm[k][0] : 0.0f);
+    b = sum_lanes<16>(wave ? sm[k][1] : 0.0f);
   }
 }
-
-template <int N> __device__ __forceinline__ float sum8(const float (&x)[N]) {
-  float s = 0.0f;
-#pragma unroll
-  for (int e = 0; e < N; ++e) s += x[e];
-  return s;
+template <int TEAM> __device__ __forceinline__ float sum_team(float a, float (*sm)[2]) {
+  float none = 0.0f;
+  sum_team<TEAM>(a, none, sm);
+  return a;
 }
-
-__device__ __forceinline__ int in_piece(int64_t left) { return left >= 8 ? 8 : left > 0 ? (int)left : 0; }
 
 }  // namespace
 
-// One row of LN lanes; P = 0: any number of pieces, read again for every pass.
-template <typename XT, typename HT, int LN, int P>
-__global__ __launch_bounds__(256) void norm_rows_kernel(NormParams p) {
-  constexpr int R = 256 / LN;
-  __shared__ float sm[8];
-  const int lane = threadIdx.x % LN;
-  const int64_t row = (int64_t)block_id() * R + threadIdx.x / LN;
+// A row each, P pieces a lane.  ODD: E is no multiple of 8.
+template <typename XT, typename HT, int TEAM, int P, bool ODD>
+__global__ __launch_bounds__(TEAM ? 256 : 1024) void norm_rows_kernel(NormParams p) {
+  constexpr int R = TEAM ? 256 / (TEAM ? TEAM : 1) : 1;
+  __shared__ float sm[2][16][2];
+  const int LN = TEAM ? TEAM : blockDim.x;
+  const int lane = TEAM ? threadIdx.x % (TEAM ? TEAM : 1) : threadIdx.x, team = TEAM ? threadIdx.x / (TEAM ? TEAM : 1) : 0;
+  const int64_t row = (int64_t)block_id() * R + team;
   if (row >= p.rows) return;
-  const int64_t base = row * p.E;
+  const int64_t E = p.E, total = p.rows * E, base = row * E;
+  const Drop drop(p.drop);
+  const int before = ODD ? (int)(base % 8) : 0;
+  auto at = [&](int k) { return (int64_t)((k * LN + lane) * 8 - before); };
+  auto held = [&](int k) {
+    Part n(at(k), E);
+    if (!ODD) n.hi = n.hi ? 8 : 0, n.lo = 0;
+    return n;
+  };
+  Piece<XT> a[P];
+  Piece<HT> b[P];
+  Piece<float> w[P], c[P];  // the columns' weights and biases
+#pragma unroll
+  for (int k = 0; k < P; ++k) {
+    const int64_t e = at(k);
+    const bool may = held(k).any() && (!ODD || base + e + 8 <= total);
+    a[k].full(static_cast<const XT*>(p.x) + base + e, may);
+    if (p.residual) b[k].full(static_cast<const HT*>(p.residual) + base + e, may);
+  }
+#pragma unroll
+  for (int k = 0; k < P; ++k) {
+    const Part n = held(k);
+    if (p.weight) w[k].full(p.weight + at(k), n.whole());
+    if (p.bias) c[k].full(p.bias + at(k), n.whole());
+  }
+  float s[P][8], m = 0.0f, v = 0.0f;  // what is normalised (zeros outside the row)
+#pragma unroll
+  for (int k = 0; k < P; ++k) {
+    if constexpr (ODD) {
+      const Part n = held(k);
+      const int64_t e = at(k);
+      if (n.any() && !n.whole()) {
+        if (p.weight) w[k].part(p.weight + e, n);
+        if (p.bias) c[k].part(p.bias + e, n);
+        if (base + e + 8 > total) {  // the tensor's end
+          a[k].part(static_cast<const XT*>(p.x) + base + e, n);
+          if (p.residual) b[k].part(static_cast<const HT*>(p.residual) + base + e, n);
+        }
+        a[k].cut(n);
+        if (p.residual) b[k].cut(n);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) s[k][i] = a[k].at(i);
+    if (drop.any()) drop.apply(drop.kept((uint64_t)(base + at(k))), s[k]);
+    if (p.residual) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) s[k][i] += b[k].at(i);
+    }
+    if (p.hidden) store_part(static_cast<HT*>(p.hidden) + base + at(k), held(k), s[k]);
+  }
+  if (!p.rms) {
+#pragma unroll
+    for (int k = 0; k < P; ++k)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) m += s[k][i];
+    m = sum_team<TEAM>(m, sm[0]) * p.inv_e;
+  }
+#pragma unroll
+  for (int k = 0; k < P; ++k) {
+    const Part n = held(k);
+    float q = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      float d = s[k][i] - m;
+      if (ODD) d = n.has(i) ? d : 0.0f;
+      q = __builtin_fmaf(d, d, q);
+    }
+    v += n.any() ? q : 0.0f;
+  }
+  const float r = 1.0f / sqrtf(sum_team<TEAM>(v, sm[1]) * p.inv_e + p.eps);
+#pragma unroll
+  for (int k = 0; k < P; ++k) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) s[k][i] = (s[k][i] - m) * r;
+    if (p.weight) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) s[k][i] *= w[k].at(i);
+    }
+    if (p.bias) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) s[k][i] += c[k].at(i);
+    }
+    store_part(static_cast<XT*>(p.out) + base + at(k), held(k), s[k]);
+  }
+  if (p.stats && lane == 0) {
+    p.stats[row] = m;
+    p.stats[p.rows + row] = r;
+  }
+}
+
+// A row of any length by a workgroup, 8 elements a lane at a time, read again for every pass
+template <typename XT, typename HT>
+__global__ __launch_bounds__(kLong) void norm_long_kernel(NormParams p) {
+  __shared__ float sm[2][16][2];
+  const int64_t row = block_id(), E = p.E, base = row * E;
+  if (row >= p.rows) return;
   const XT* x = static_cast<const XT*>(p.x) + base;
   const HT* res = p.residual ? static_cast<const HT*>(p.residual) + base : nullptr;
   const Drop drop(p.drop);
-  auto fetch = [&](int64_t e, int n, float (&s)[8]) {  // the sum that is normalised
-    load_n<XT, 8>(x + e, n, s);
-    float q[8];
-    if (res) load_n<HT, 8>(res + e, n, q);
+  float s[8], m = 0.0f, v = 0.0f;
+  auto take = [&](int64_t e, const Part& n) {
+    Piece<XT> a;
+    Piece<HT> b;
+    a.full(x + e, n.whole());
+    if (res) b.full(res + e, n.whole());
+    if (!n.whole()) {
+      a.part(x + e, n);
+      a.cut(n);
+      if (res) {
+        b.part(res + e, n);
+        b.cut(n);
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < 8; ++k) s[k] = a.at(k);
     if (drop.any()) drop.apply(drop.kept((uint64_t)(base + e)), s);
     if (res) {
 #pragma unroll
-      for (int k = 0; k < 8; ++k) s[k] += q[k];
+      for (int k = 0; k < 8; ++k) s[k] += b.at(k);
     }
   };
-  auto finish = [&](int64_t e, int n, float (&s)[8], float m, float r) {
+  const int64_t e0 = threadIdx.x * 8;
+  for (int64_t e = e0; e < E; e += kLong * 8) {
+    const Part n(e, E);
+    take(e, n);
+    if (p.hidden) store_part(static_cast<HT*>(p.hidden) + base + e, n, s);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) m += s[k];
+  }
+  m = p.rms ? 0.0f : sum_team<0>(m, sm[0]) * p.inv_e;
+  for (int64_t e = e0; e < E; e += kLong * 8) {
+    const Part n(e, E);
+    take(e, n);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const float d = n.has(k) ? s[k] - m : 0.0f;
+      v = __builtin_fmaf(d, d, v);
+    }
+  }
+  const float r = 1.0f / sqrtf(sum_team<0>(v, sm[1]) * p.inv_e + p.eps);
+  for (int64_t e = e0; e < E; e += kLong * 8) {
+    const Part n(e, E);
+    take(e, n);
     float w[8];
 #pragma unroll
     for (int k = 0; k < 8; ++k) s[k] = (s[k] - m) * r;
     if (p.weight) {
-      load_n<float, 8>(p.weight + e, n, w);
+      load_n<float, 8>(p.weight + e, n.hi, w);
 #pragma unroll
       for (int k = 0; k < 8; ++k) s[k] *= w[k];
     }
     if (p.bias) {
-      load_n<float, 8>(p.bias + e, n, w);
+      load_n<float, 8>(p.bias + e, n.hi, w);
 #pragma unroll
       for (int k = 0; k < 8; ++k) s[k] += w[k];
     }
-    store_n<XT, 8>(static_cast<XT*>(p.out) + base + e, n, s);
-  };
-  auto spread = [&](const float (&s)[8], int n, float m) {  // sum of squares about m
-    float v = 0.0f;
+    store_part(static_cast<XT*>(p.out) + base + e, n, s);
+  }
+  if (p.stats && threadIdx.x == 0) {
+    p.stats[row] = m;
+    p.stats[p.rows + row] = r;
+  }
+}
+
+// Rows in turn (p.blocks workgroups); dw and db of the lane's columns are added up over the team's rows in registers,
+// then over the workgroup's teams in LDS, and go to memory as the workgroup's partial sums.  ODD: a team's rows are
+// 8 k apart, so that they all begin alike and a lane keeps its columns.
+template <typename XT, typename HT, int TEAM, bool ODD>
+__global__ __launch_bounds__(TEAM ? 256 : 1024) void norm_rows_bwd_kernel(NormParams p) {
+  constexpr int R = TEAM ? 256 / (TEAM ? TEAM : 1) : 1;
+  __shared__ float sm[2][16][2];
+  __shared__ float acc[R > 1 ? 256 * 8 : 1];
+  const int lane = TEAM ? threadIdx.x % (TEAM ? TEAM : 1) : threadIdx.x, team = TEAM ? threadIdx.x / (TEAM ? TEAM : 1) : 0;
+  const int64_t E = p.E, total = p.rows * E;
+  const XT* dout = static_cast<const XT*>(p.x);
+  const HT* hidden = static_cast<const HT*>(p.residual);
+  const HT* dhidden = static_cast<const HT*>(p.dhidden);
+  const Drop drop(p.drop);
+  const int64_t first = (int64_t)block_id() * R + team;
+  const int64_t e = lane * 8 - (ODD ? (int)(first * E % 8) : 0);
+  Part n(e, E);
+  if (!ODD) n.hi = n.hi ? 8 : 0, n.lo = 0;
+  Piece<float> w;
+  if (p.weight) {
+    w.full(p.weight + e, n.whole());
+    if (ODD && n.any() && !n.whole()) w.part(p.weight + e, n);
+  } else {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) w.w[k >> 2][k & 3] = 0x3f800000u;
+  }
+  float dw[8], db[8];
+#pragma unroll
+  for (int k = 0; k < 8; ++k) dw[k] = db[k] = 0.0f;
+  int turn = 0;
+  for (int64_t row = first; row < p.rows; row += p.blocks * R, turn ^= 1) {
+    const int64_t at = row * E + e;
+    const bool end = ODD && at + 8 > total, may = n.any() && !end;
+    Piece<XT> a;
+    Piece<HT> b, q;
+    a.full(dout + at, may);
+    b.full(hidden + at, may);
+    if (dhidden) q.full(dhidden + at, may);
+    const float m = p.stats[row], r = p.stats[p.rows + row];
+    if constexpr (ODD) {
+      if (n.any() && !n.whole()) {
+        if (end) {
+          a.part(dout + at, n);
+          b.part(hidden + at, n);
+          if (dhidden) q.part(dhidden + at, n);
+        }
+        a.cut(n);
+        b.cut(n);
+      }
+    }
+    float g[8], h[8], c1 = 0.0f, c2 = 0.0f;
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
-      const float d = k < n ? s[k] - m : 0.0f;
-      v = __builtin_fmaf(d, d, v);
+      const float d = a.at(k);  // (zero outside the row)
+      h[k] = (b.at(k) - m) * r;
+      dw[k] = __builtin_fmaf(d, h[k], dw[k]);
+      db[k] += d;
+      g[k] = d * w.at(k);
+      c1 += g[k];
+      c2 = __builtin_fmaf(g[k], h[k], c2);
     }
-    return v;
-  };
-  float m = 0.0f, v = 0.0f;
-  if constexpr (P > 0) {
-    float s[P][8];
-    int n[P];
+    sum_team<TEAM>(c1, c2, sm[turn]);  // (the other half may still be read)
+    c1 = p.rms ? 0.0f : c1 * p.inv_e;
+    c2 *= p.inv_e;
 #pragma unroll
-    for (int k = 0; k < P; ++k) {
-      const int64_t e = (int64_t)(k * LN + lane) * 8;
-      n[k] = in_piece(p.E - e);
-      fetch(e, n[k], s[k]);
-      m += sum8(s[k]);
-    }
-    if (p.hidden) {
+    for (int k = 0; k < 8; ++k) g[k] = r * (g[k] - c1 - h[k] * c2);
+    if (dhidden) {
 #pragma unroll
-      for (int k = 0; k < P; ++k)
-        store_n<HT, 8>(static_cast<HT*>(p.hidden) + base + (int64_t)(k * LN + lane) * 8, n[k], s[k]);
+      for (int k = 0; k < 8; ++k) g[k] += q.at(k);
     }
-    m = p.rms ? 0.0f : sum_team<LN>(m, sm) * p.inv_e;
+    if (p.hidden) store_part(static_cast<HT*>(p.hidden) + at, n, g);
+    if (p.out) {
+      if (drop.any()) drop.apply(drop.kept((uint64_t)at), g);
+      store_part(static_cast<XT*>(p.out) + at, n, g);
+    }
+  }
+  if (!p.part) return;
+  float* part = p.part + (int64_t)block_id() * 2 * E;
 #pragma unroll
-    for (int k = 0; k < P; ++k) v += spread(s[k], n[k], m);
-    v = sum_team<LN>(v, sm + 4) * p.inv_e;
-    const float r = 1.0f / sqrtf(v + p.eps);
+  for (int which = 0; which < 2; ++which) {
+    if constexpr (R > 1) {
+      __syncthreads();
 #pragma unroll
-    for (int k = 0; k < P; ++k) finish((int64_t)(k * LN + lane) * 8, n[k], s[k], m, r);
-    if (p.stats && lane == 0) {
-      p.stats[row] = m;
-      p.stats[p.rows + row] = r;
-    }
-  } else {
-    float s[8];
-    for (int64_t e = lane * 8; e < p.E; e += LN * 8) {
-      const int n = in_piece(p.E - e);
-      fetch(e, n, s);
-      if (p.hidden) store_n<HT, 8>(static_cast<HT*>(p.hidden) + base + e, n, s);
-      m += sum8(s);
-    }
-    m = p.rms ? 0.0f : sum_team<LN>(m, sm) * p.inv_e;
-    for (int64_t e = lane * 8; e < p.E; e += LN * 8) {
-      const int n = in_piece(p.E - e);
-      fetch(e, n, s);
-      v += spread(s, n, m);
-    }
-    v = sum_team<LN>(v, sm + 4) * p.inv_e;
-    const float r = 1.0f / sqrtf(v + p.eps);
-    for (int64_t e = lane * 8; e < p.E; e += LN * 8) {
-      const int n = in_piece(p.E - e);
-      fetch(e, n, s);
-      finish(e, n, s, m, r);
-    }
-    if (p.stats && lane == 0) {
-      p.stats[row] = m;
-      p.stats[p.rows + row] = r;
+      for (int k = 0; k < 8; ++k) acc[threadIdx.x * 8 + k] = which ? db[k] : dw[k];
+      __syncthreads();
+      for (int c = threadIdx.x; c < E; c += 256) {
+        float s = 0.0f;
+#pragma unroll
+        for (int t = 0; t < R; ++t)
+          s += acc[t * TEAM * 8 + c + (ODD ? (int)(((int64_t)block_id() * R + t) * E % 8) : 0)];
+        part[which * E + c] = s;
+      }
+    } else {
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        if (n.has(k)) part[which * E + e + k] = which ? db[k] : dw[k];
     }
   }
 }
 
-// Rows in turn (p.blocks workgroups of 256 / LN teams); dw and db of the lane's columns are added up over the team's
-// rows in registers, then over the workgroup's teams in LDS, and go to memory as the workgroup's partial sums.
-// P = 0: any number of pieces, read twice; dw and db are then summed by norm_sums_kernel.
-template <typename XT, typename HT, int LN, int P>
-__global__ __launch_bounds__(256) void norm_rows_bwd_kernel(NormParams p) {
-  constexpr int R = 256 / LN, PA = P > 0 ? P : 1;
-  __shared__ float sm[8];
-  __shared__ float acc[P > 0 && R > 1 ? 256 * PA * 8 : 1];
-  const int lane = threadIdx.x % LN, team = threadIdx.x / LN;
-  const HT* hidden = static_cast<const HT*>(p.residual);
+// The gradients of a row of any length by a workgroup, read twice; dw and db are summed by norm_sums_kernel.
+template <typename XT, typename HT>
+__global__ __launch_bounds__(kLong) void norm_long_bwd_kernel(NormParams p) {
+  __shared__ float sm[16][2];
+  const int64_t row = block_id(), E = p.E, base = row * E;
+  if (row >= p.rows) return;
   const Drop drop(p.drop);
-  float dw[PA][8], db[PA][8];
-#pragma unroll
-  for (int k = 0; k < PA; ++k)
-#pragma unroll
-    for (int e = 0; e < 8; ++e) dw[k][e] = db[k][e] = 0.0f;
-  // one piece: xh and g in place of what was read
-  auto fetch = [&](int64_t base, int64_t e, int n, float m, float r, float (&d)[8], float (&h)[8], float (&w)[8]) {
-    load_n<XT, 8>(static_cast<const XT*>(p.x) + base + e, n, d);
-    load_n<HT, 8>(hidden + base + e, n, h);
+  const float m = p.stats[row], r = p.stats[p.rows + row];
+  float g[8], h[8];
+  Piece<HT> q;
+  auto take = [&](int64_t e, const Part& n) {
+    Piece<XT> a;
+    Piece<HT> b;
+    const int64_t at = base + e;
+    a.full(static_cast<const XT*>(p.x) + at, n.whole());
+    b.full(static_cast<const HT*>(p.residual) + at, n.whole());
+    if (p.dhidden) q.full(static_cast<const HT*>(p.dhidden) + at, n.whole());
+    if (!n.whole()) {
+      a.part(static_cast<const XT*>(p.x) + at, n);
+      b.part(static_cast<const HT*>(p.residual) + at, n);
+      if (p.dhidden) q.part(static_cast<const HT*>(p.dhidden) + at, n);
+      a.cut(n);
+    }
     if (p.weight) {
-      load_n<float, 8>(p.weight + e, n, w);
+      load_n<float, 8>(p.weight + e, n.hi, g);
     } else {
 #pragma unroll
-      for (int k = 0; k < 8; ++k) w[k] = 1.0f;
+      for (int k = 0; k < 8; ++k) g[k] = 1.0f;
     }
 #pragma unroll
-    for (int k = 0; k < 8; ++k) h[k] = (h[k] - m) * r;
+    for (int k = 0; k < 8; ++k) {
+      h[k] = (b.at(k) - m) * r;
+      g[k] *= a.at(k);
+    }
   };
-  auto finish = [&](int64_t base, int64_t e, int n, float r, float c1, float c2, float (&g)[8], const float (&h)[8]) {
-    float q[8];
-    if (p.dhidden) load_n<HT, 8>(static_cast<const HT*>(p.dhidden) + base + e, n, q);
+  float c1 = 0.0f, c2 = 0.0f;
+  for (int64_t e = threadIdx.x * 8; e < E; e += kLong * 8) {
+    const Part n(e, E);
+    take(e, n);
 #pragma unroll
-    for (int k = 0; k < 8; ++k) g[k] = r * (g[k] - c1 - h[k] * c2);
-    if (p.dhidden) {
-#pragma unroll
-      for (int k = 0; k < 8; ++k) g[k] += q[k];
+    for (int k = 0; k < 8; ++k) {
+      c1 += g[k];
+      c2 = n.has(k) ? __builtin_fmaf(g[k], h[k], c2) : c2;
     }
-    if (p.hidden) store_n<HT, 8>(static_cast<HT*>(p.hidden) + base + e, n, g);
+  }
+  sum_team<0>(c1, c2, sm);
+  c1 = p.rms ? 0.0f : c1 * p.inv_e;
+  c2 *= p.inv_e;
+  for (int64_t e = threadIdx.x * 8; e < E; e += kLong * 8) {
+    const Part n(e, E);
+    take(e, n);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) g[k] = r * (g[k] - c1 - h[k] * c2) + (p.dhidden ? q.at(k) : 0.0f);
+    if (p.hidden) store_part(static_cast<HT*>(p.hidden) + base + e, n, g);
     if (p.out) {
       if (drop.any()) drop.apply(drop.kept((uint64_t)(base + e)), g);
-      store_n<XT, 8>(static_cast<XT*>(p.out) + base + e, n, g);
-    }
-  };
-  for (int64_t row0 = (int64_t)block_id() * R; row0 < p.rows; row0 += p.blocks * R) {
-    const int64_t row = row0 + team;
-    if (LN < 256 && row >= p.rows) break;
-    const int64_t base = row * p.E;
-    const float m = p.stats[row], r = p.stats[p.rows + row];
-    float c1 = 0.0f, c2 = 0.0f;
-    if constexpr (P > 0) {
-      float g[P][8], h[P][8];
-#pragma unroll
-      for (int k = 0; k < P; ++k) {
-        const int64_t e = (int64_t)(k * LN + lane) * 8;
-        const int n = in_piece(p.E - e);
-        float w[8];
-        fetch(base, e, n, m, r, g[k], h[k], w);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          if (i >= n) g[k][i] = h[k][i] = 0.0f;
-          dw[k][i] = __builtin_fmaf(g[k][i], h[k][i], dw[k][i]);
-          db[k][i] += g[k][i];
-          g[k][i] *= w[i];
-          c1 += g[k][i];
-          c2 = __builtin_fmaf(g[k][i], h[k][i], c2);
-        }
-      }
-      c1 = p.rms ? 0.0f : sum_team<LN>(c1, sm) * p.inv_e;
-      c2 = sum_team<LN>(c2, sm + 4) * p.inv_e;
-#pragma unroll
-      for (int k = 0; k < P; ++k) {
-        const int64_t e = (int64_t)(k * LN + lane) * 8;
-        finish(base, e, in_piece(p.E - e), r, c1, c2, g[k], h[k]);
-      }
-    } else {
-      float g[8], h[8], w[8];
-      for (int64_t e = lane * 8; e < p.E; e += LN * 8) {
-        const int n = in_piece(p.E - e);
-        fetch(base, e, n, m, r, g, h, w);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          if (i >= n) g[i] = h[i] = 0.0f;
-          c1 = __builtin_fmaf(g[i], w[i], c1);
-          c2 = __builtin_fmaf(g[i] * w[i], h[i], c2);
-        }
-      }
-      c1 = p.rms ? 0.0f : sum_team<LN>(c1, sm) * p.inv_e;
-      c2 = sum_team<LN>(c2, sm + 4) * p.inv_e;
-      for (int64_t e = lane * 8; e < p.E; e += LN * 8) {
-        const int n = in_piece(p.E - e);
-        fetch(base, e, n, m, r, g, h, w);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) g[i] *= w[i];
-        finish(base, e, n, r, c1, c2, g, h);
-      }
-    }
-    if constexpr (LN > 64) __syncthreads();  // sm is written again in the next row
-  }
-  if constexpr (P > 0) {
-    if (!p.part) return;
-    float* part = p.part + (int64_t)block_id() * 2 * p.E;
-#pragma unroll
-    for (int which = 0; which < 2; ++which) {
-      if constexpr (R > 1) {
-        __syncthreads();
-#pragma unroll
-        for (int k = 0; k < P; ++k)
-#pragma unroll
-          for (int i = 0; i < 8; ++i) acc[(team * P * LN + k * LN + lane) * 8 + i] = which ? db[k][i] : dw[k][i];
-        __syncthreads();
-        for (int c = threadIdx.x; c < P * LN * 8 && c < p.E; c += 256) {
-          float s = 0.0f;
-          for (int t = 0; t < R; ++t) s += acc[t * P * LN * 8 + c];
-          part[which * p.E + c] = s;
-        }
-      } else {
-#pragma unroll
-        for (int k = 0; k < P; ++k) {
-          const int64_t e = (int64_t)(k * LN + lane) * 8;
-          const int n = in_piece(p.E - e);
-#pragma unroll
-          for (int i = 0; i < 8; ++i)
-            if (i < n) part[which * p.E + e + i] = which ? db[k][i] : dw[k][i];
-        }
-      }
+      store_part(static_cast<XT*>(p.out) + base + e, n, g);
     }
   }
 }
@@ -326,71 +459,67 @@ __global__ __launch_bounds__(1024) void norm_join_kernel(NormParams p) {
 
 namespace {
 
-template <typename XT, typename HT, int LN, int P>
-void go(const NormParams& p, hipStream_t s) {
-  hipLaunchKernelGGL((norm_rows_kernel<XT, HT, LN, P>), grid_of((p.rows + 256 / LN - 1) / (256 / LN)), dim3(256), 0, s, p);
+template <typename XT, typename HT, int TEAM, int P>
+void go(const NormParams& p, int lanes, hipStream_t s) {
+  constexpr int R = TEAM ? 256 / (TEAM ? TEAM : 1) : 1;
+  const dim3 grid = grid_of((p.rows + R - 1) / R), block(TEAM ? 256 : lanes);
+  if (p.E % 8) hipLaunchKernelGGL((norm_rows_kernel<XT, HT, TEAM, P, true>), grid, block, 0, s, p);
+  else hipLaunchKernelGGL((norm_rows_kernel<XT, HT, TEAM, P, false>), grid, block, 0, s, p);
 }
 
 template <typename XT, typename HT>
 void fwd(const NormParams& p, hipStream_t s) {
-  const int64_t n = (p.E + 7) / 8;
-  if (n <= 128) {
-    if (n <= 16) return go<XT, HT, 16, 1>(p, s);
-    if (n <= 32) return go<XT, HT, 16, 2>(p, s);
-    if (n <= 64) return go<XT, HT, 16, 4>(p, s);
-    if (n <= 96) return go<XT, HT, 16, 6>(p, s);
-    return go<XT, HT, 16, 8>(p, s);
+  const int lanes = team_of(p.E, p.E > kTwo ? 2 : 1);
+  switch (lanes) {
+    case 0:
+      hipLaunchKernelGGL((norm_long_kernel<XT, HT>), grid_of(p.rows), dim3(kLong), 0, s, p);
+      return;
+    case 16: return go<XT, HT, 16, 1>(p, lanes, s);
+    case 32: return go<XT, HT, 32, 1>(p, lanes, s);
+    case 64: return go<XT, HT, 64, 1>(p, lanes, s);
+    default: return p.E > kTwo ? go<XT, HT, 0, 2>(p, lanes, s) : go<XT, HT, 0, 1>(p, lanes, s);
   }
-  if (n <= 512) {
-    if (n <= 256) return go<XT, HT, 64, 4>(p, s);
-    if (n <= 384) return go<XT, HT, 64, 6>(p, s);
-    return go<XT, HT, 64, 8>(p, s);
-  }
-  if (n <= 2048) {
-    if (n <= 1024) return go<XT, HT, 256, 4>(p, s);
-    return go<XT, HT, 256, 8>(p, s);
-  }
-  go<XT, HT, 256, 0>(p, s);
 }
 
-// lanes of a row's team in the backward pass, whose sums take a register per column besides; and its pieces
-int bwd_lanes(int64_t E) { return E <= 256 ? 16 : E <= 2048 ? 64 : 256; }
-constexpr int64_t kBwdLongest = 8192;
-
-template <typename XT, typename HT, int LN, int P>
-void go_bwd(const NormParams& p, hipStream_t s) {
-  hipLaunchKernelGGL((norm_rows_bwd_kernel<XT, HT, LN, P>), grid_of(p.blocks), dim3(256), 0, s, p);
+template <typename XT, typename HT, int TEAM>
+void go_bwd(const NormParams& p, int lanes, hipStream_t s) {
+  const dim3 grid = grid_of(p.blocks), block(TEAM ? 256 : lanes);
+  if (p.E % 8) hipLaunchKernelGGL((norm_rows_bwd_kernel<XT, HT, TEAM, true>), grid, block, 0, s, p);
+  else hipLaunchKernelGGL((norm_rows_bwd_kernel<XT, HT, TEAM, false>), grid, block, 0, s, p);
 }
 
 template <typename XT, typename HT>
 void bwd(const NormParams& p, hipStream_t s) {
-  const int64_t n = (p.E + 7) / 8;
-  if (p.E > kBwdLongest) {
-    NormParams q = p;
-    q.part = nullptr;
-    q.blocks = p.rows;
-    go_bwd<XT, HT, 256, 0>(q, s);
-    if (p.part)
-      hipLaunchKernelGGL((norm_sums_kernel<XT, HT>), grid_of((p.E + 255) / 256 * p.blocks), dim3(256), 0, s, p);
-    return;
-  }
-  switch (bwd_lanes(p.E)) {
-    case 16: return n <= 16 ? go_bwd<XT, HT, 16, 1>(p, s) : go_bwd<XT, HT, 16, 2>(p, s);
-    case 64:
-      if (n <= 64) return go_bwd<XT, HT, 64, 1>(p, s);
-      if (n <= 128) return go_bwd<XT, HT, 64, 2>(p, s);
-      return go_bwd<XT, HT, 64, 4>(p, s);
-    default:
-      return n <= 512 ? go_bwd<XT, HT, 256, 2>(p, s) : go_bwd<XT, HT, 256, 4>(p, s);
+  const int lanes = team_of(p.E);
+  switch (lanes) {
+    case 0:
+      hipLaunchKernelGGL((norm_long_bwd_kernel<XT, HT>), grid_of(p.rows), dim3(kLong), 0, s, p);
+      if (p.part)
+        hipLaunchKernelGGL((norm_sums_kernel<XT, HT>), grid_of((p.E + 255) / 256 * p.blocks), dim3(256), 0, s, p);
+      return;
+    case 16: return go_bwd<XT, HT, 16>(p, lanes, s);
+    case 32: return go_bwd<XT, HT, 32>(p, lanes, s);
+    case 64: return go_bwd<XT, HT, 64>(p, lanes, s);
+    default: return go_bwd<XT, HT, 0>(p, lanes, s);
   }
 }
 
 }  // namespace
 
+// Workgroups of the backward pass, each of which leaves a partial sum of dw and db: about 16 waves a compute unit, the
+// same number on each (16384 x 5000, 10 waves a row: 84 us with 512, 117 and 100 with 256 and 768), and where the
+// rows are fewer, up to 12 rows in turn rather than more sums (16384 x 768: 39 us with 1366, 41.6 with 2048, 51 with
+// 4096), but 512 at least.  A multiple of 8 where E is none.
 int64_t norm_rows_bwd_blocks(int64_t rows, int64_t E) {
-  if (E > kBwdLongest) return rows < 64 ? rows : 64;
-  const int64_t R = 256 / bwd_lanes(E), all = (rows + R - 1) / R;
-  return all < 768 ? all : 768;
+  const int lanes = team_of(E);
+  if (!lanes) return rows < 64 ? rows : 64;
+  const int64_t waves = lanes <= 64 ? 4 : lanes / 64, R = lanes <= 64 ? 256 / lanes : 1;
+  const int64_t each = (16 + waves - 1) / waves < 24 / waves ? (16 + waves - 1) / waves : 24 / waves;
+  const int64_t all = (rows + R - 1) / R, most = 256 * each;
+  int64_t turns = (all + 511) / 512 < 12 ? (all + 511) / 512 : 12;
+  if (turns < (all + most - 1) / most) turns = (all + most - 1) / most;
+  const int64_t n = (all + turns - 1) / turns;
+  return E % 8 ? (n + 7) / 8 * 8 : n;
 }
 
 hipError_t launch_norm_rows(const NormParams& p, int kind, hipStream_t s) {
