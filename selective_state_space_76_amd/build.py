@@ -17,13 +17,15 @@ SOURCES = [os.path.join(CSRC, f) for f in (
     "scan_cl.hip", "ssm_kernels.hip", "conv_kernels.hip", "scan_bwd.hip", "scan_bwd_zoh.hip", "ssm_abi.cpp",
     "train/conv_bwd.hip", "train/embed_fwd.hip", "train/embed_bwd.hip", "train/embed_bwd_few.hip",
     "train/adamw.hip", "train/train_abi.cpp",
-    "block/norm_rows.hip", "block/norm_cols.hip", "block/dropout.hip", "block/recur_fwd.hip", "block/recur_bwd.hip",
+    "block/norm_rows.hip", "block/norm_cols_bf16.hip", "block/norm_cols_mixed.hip", "block/norm_cols_f32.hip",
+    "block/dropout.hip", "block/recur_fwd.hip", "block/recur_bwd.hip",
     "block/block_abi.cpp")]
 HEADERS = [os.path.join(CSRC, "ssm_launch.h"), os.path.join(CSRC, "ssm_device.h"),
            os.path.join(CSRC, "scan_bwd_kernel.h"),
            os.path.join(CSRC, "train", "train_launch.h"), os.path.join(CSRC, "train", "train_device.h"),
            os.path.join(CSRC, "train", "abi_checks.h"), os.path.join(CSRC, "block", "block_launch.h"),
-           os.path.join(CSRC, "block", "block_device.h"), os.path.join(CSRC, "block", "recur_device.h"),
+           os.path.join(CSRC, "block", "block_device.h"), os.path.join(CSRC, "block", "norm_cols_kernel.h"),
+           os.path.join(CSRC, "block", "recur_device.h"),
            os.path.join(ROOT, "include", "ssm_scan.h")]
 ARCH = "gfx950"
 

@@ -133,6 +133,20 @@ struct Piece {
       else w[k >> 2][k & 3] = r.has(k) ? w[k >> 2][k & 3] : 0u;
     }
   }
+  // zeros where the bit is not set
+  __device__ __forceinline__ void keep(uint32_t kept) {
+#pragma unroll
+    for (int k = 0; k < 4 * Q; ++k) {
+      if constexpr (Q == 1)
+        w[0][k] &= (kept >> (2 * k) & 1u ? 0xffffu : 0u) | (kept >> (2 * k + 1) & 1u ? 0xffff0000u : 0u);
+      else w[k >> 2][k & 3] = kept >> k & 1u ? w[k >> 2][k & 3] : 0u;
+    }
+  }
+  // Keeps the compiler from holding what it has made of the piece (twice the registers) for a later pass.
+  __device__ __forceinline__ void forget() {
+#pragma unroll
+    for (int k = 0; k < Q; ++k) asm volatile("" : "+v"(w[k]));
+  }
   __device__ __forceinline__ float at(int e) const {
     if constexpr (Q == 1) return __uint_as_float(e & 1 ? w[0][e >> 1] & 0xffff0000u : w[0][e >> 1] << 16);
     else return __uint_as_float(w[e >> 2][e & 3]);

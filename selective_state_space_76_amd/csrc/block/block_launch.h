@@ -25,7 +25,7 @@ struct DropoutParams {
 };
 hipError_t launch_dropout(const DropoutParams& p, bool x_bf16, bool out_bf16, hipStream_t s);
 
-// ---- layer norm (norm_rows.hip: [rows, E]; norm_cols.hip: [B, E, L])
+// ---- layer norm (norm_rows.hip: [rows, E]; norm_cols_kernel.h: [B, E, L])
 struct NormParams {
   const void* x;         // forward; backward: dout
   const void* residual;  // forward, or null; backward: hidden
@@ -46,11 +46,35 @@ struct NormParams {
 };
 // kind: bit 0 bf16 x, bit 1 bf16 hidden
 hipError_t launch_norm_rows(const NormParams& p, int kind, hipStream_t s);
-hipError_t launch_norm_cols(const NormParams& p, int kind, hipStream_t s);
+hipError_t launch_norm_cols_bf16(const NormParams& p, hipStream_t s);  // x and hidden
+hipError_t launch_norm_cols_mixed(const NormParams& p, hipStream_t s);  // x in bf16, hidden in fp32
+hipError_t launch_norm_cols_f32(const NormParams& p, hipStream_t s);
+hipError_t launch_norm_cols_bwd_bf16(const NormParams& p, hipStream_t s);
+hipError_t launch_norm_cols_bwd_mixed(const NormParams& p, hipStream_t s);
+hipError_t launch_norm_cols_bwd_f32(const NormParams& p, hipStream_t s);
+inline hipError_t launch_norm_cols(const NormParams& p, int kind, hipStream_t s) {
+  return kind == 3 ? launch_norm_cols_bf16(p, s) : kind == 1 ? launch_norm_cols_mixed(p, s) : launch_norm_cols_f32(p, s);
+}
+inline hipError_t launch_norm_cols_bwd(const NormParams& p, int kind, hipStream_t s) {
+  return kind == 3 ? launch_norm_cols_bwd_bf16(p, s) : kind == 1 ? launch_norm_cols_bwd_mixed(p, s)
+                                                                 : launch_norm_cols_bwd_f32(p, s);
+}
 int64_t norm_rows_bwd_blocks(int64_t rows, int64_t E);
-int64_t norm_cols_bwd_blocks(int64_t B, int64_t L, int64_t E, int kind);
+// Positions of a tile of the backward pass over [B, E, L], and its workgroups: two for each compute unit, more where there
+// are tiles, each with a partial sum of dw and db.  Wide tiles as in the forward pass, where there are enough of them
+// (2^17 positions x 1024 channels: 246 us with 256 positions, 266 with 128, 304 with 64; 4 x 4096 x 2048: 71 us with
+// 64, 92 with 128).
+constexpr int64_t kFewTiles = 128;  // of 64 positions: then they are cut to 16, lines shared through the caches
+inline int norm_cols_bwd_tile(int64_t B, int64_t L) {
+  auto tiles = [&](int64_t T) { return B * ((L + T - 1) / T); };
+  if (L % 8) return tiles(128) >= 256 ? 128 : 64;
+  return tiles(256) >= 512 ? 256 : tiles(128) >= 256 ? 128 : tiles(64) >= kFewTiles ? 64 : 16;
+}
+inline int64_t norm_cols_bwd_blocks(int64_t B, int64_t L) {
+  const int64_t T = norm_cols_bwd_tile(B, L), tiles = B * ((L + T - 1) / T);
+  return tiles < 1024 ? tiles : 1024;
+}
 hipError_t launch_norm_rows_bwd(const NormParams& p, int kind, hipStream_t s);
-hipError_t launch_norm_cols_bwd(const NormParams& p, int kind, hipStream_t s);
 // dweight and dbias from p.blocks partial sums
 hipError_t launch_norm_join(const NormParams& p, hipStream_t s);
 

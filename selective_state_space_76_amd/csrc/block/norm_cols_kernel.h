@@ -1,0 +1,462 @@
+// norm_cols_kernel.h -- the layer norm of norm_rows.hip over the channels of [B, E, L], the layout of the conv and the
+// scan; compiled by norm_cols_{bf16,mixed,f32}.hip.
+//
+// A workgroup owns T = LP * 8 consecutive positions of one batch row and all of their channels: LP lanes hold a channel's
+// positions, 8 each, and the NT / LP groups of lanes take the channels in turn, C of them at a time.  A position's sums go
+// over the groups: within a wave by exchanges that leave each lane one position, over the waves through LDS.  KEEP: C
+// channels a group are all there are, and stay in registers as they came from memory; otherwise they are read again
+// for every pass.
+#pragma once
+#include "block_device.h"
+
+namespace ssm {
+
+namespace {
+
+// v[k] summed over all lanes of the workgroup that have the same positions; sm: (NT / 64 + 1) * LP * 8 floats
+template <int NT, int LP>
+__device__ __forceinline__ void sum_groups(float (&v)[8], float* sm) {
+  constexpr int T = LP * 8, NW = NT / 64;
+  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+  // halves of the positions are exchanged with the lane 32, 16 and 8 away: its bits 5, 4 and 3 name what is left
+  float* to = sm + w * T + (lane % LP) * 8 + (lane >> 5) * 4;
+  float a[4], b[2], c;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const float keep = lane & 32 ? v[k + 4] : v[k], send = lane & 32 ? v[k] : v[k + 4];
+    a[k] = keep + __shfl_xor(send, 32);
+  }
+  if constexpr (LP == 32) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) to[k] = a[k];
+  } else {
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const float keep = lane & 16 ? a[k + 2] : a[k], send = lane & 16 ? a[k] : a[k + 2];
+      b[k] = keep + __shfl_xor(send, 16);
+    }
+    to += (lane >> 4 & 1) * 2;
+    if constexpr (LP == 16) {
+      to[0] = b[0];
+      to[1] = b[1];
+    } else {
+      const float keep = lane & 8 ? b[1] : b[0], send = lane & 8 ? b[0] : b[1];
+      c = keep + __shfl_xor(send, 8);
+#pragma unroll
+      for (int m = 4; m >= LP; m /= 2) c += __shfl_xor(c, m);
+      to[lane >> 3 & 1] = c;  // (lanes of the same position: the same sum)
+    }
+  }
+  __syncthreads();
+  if (threadIdx.x < T) {
+    float s = 0.0f;
+#pragma unroll
+    for (int i = 0; i < NW; ++i) s += sm[i * T + threadIdx.x];
+    sm[NW * T + threadIdx.x] = s;
+  }
+  __syncthreads();
+#pragma unroll
+  for (int k = 0; k < 8; ++k) v[k] = sm[NW * T + (threadIdx.x % LP) * 8 + k];
+}
+
+// sum over the LP lanes that hold a channel's positions
+template <int LP> __device__ __forceinline__ float sum_positions(float v) {
+#pragma unroll
+  for (int m = 1; m < LP; m *= 2) v += __shfl_xor(v, m);
+  return v;
+}
+
+// Where rows do not begin with a line, neighbouring tiles write parts of one: put together by the cache.
+template <typename IO>
+__device__ __forceinline__ void store_cols(IO* p, int n, const float (&x)[8], bool lines) {
+  if (lines || n < 8) return store_n<IO, 8>(p, n, x);
+#pragma unroll
+  for (int k = 0; k < (int)sizeof(IO) / 2; ++k) {
+    typename Unaligned<IO>::type q;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if constexpr (sizeof(IO) == 2)
+        q[i] = (uint32_t)__builtin_bit_cast(uint16_t, (__bf16)x[2 * i]) |
+               (uint32_t)__builtin_bit_cast(uint16_t, (__bf16)x[2 * i + 1]) << 16;
+      else
+        q[i] = __float_as_uint(x[k * 4 + i]);
+    }
+    *(reinterpret_cast<typename Unaligned<IO>::type*>(p) + k) = q;
+  }
+}
+
+}  // namespace
+
+// On this architecture a wave that waits for a load waits for the stores that it issued before, too.  So nothing is
+// loaded behind a store that it does not follow from: weights come with the pieces, and where pieces are read again, the
+// next ones are asked for before the present ones are stored.
+
+// C channels of a lane: NG apart, from channel e on
+template <typename XT, typename HT, bool RES, int C>
+struct Chunk {
+  Piece<XT> x[C];  // zeros where dropped
+  Piece<HT> q[RES ? C : 1];
+  float w[C], c[C];
+};
+
+// RES: there is a residual.  DROP: there is dropout (not with KEEP: the masks of all channels at once would take more
+// registers than there are).  ODD: L is no multiple of 8.
+template <typename XT, typename HT, bool RES, bool DROP, bool ODD, int NT, int LP, int C, bool KEEP>
+__global__ __launch_bounds__(NT) void norm_cols_kernel(NormParams p) {
+  constexpr int NG = NT / LP, T = LP * 8;
+  __shared__ float sm[(NT / 64 + 1) * T];
+  const int pl = threadIdx.x % LP, cg = threadIdx.x / LP, E = (int)p.E;
+  const int64_t tiles = (p.L + T - 1) / T, blk = block_id();
+  const int64_t b = blk / tiles, t = blk % tiles * T + pl * 8, total = p.rows * p.E, step = NG * p.L;
+  if (b >= p.B) return;
+  const int n = p.L - t >= 8 ? 8 : !ODD || p.L <= t ? 0 : (int)(p.L - t);
+  const int64_t base = b * p.E * p.L + t;
+  const bool lines = !ODD && p.L % 64 == 0;
+  static_assert(!(DROP && KEEP), "");
+  const Drop drop(p.drop);
+  typedef Chunk<XT, HT, RES, C> Ch;
+  // f(c, e, where it lies) for the lane's channels e from e0 on.  Where they lie is worked out again by every pass: kept
+  // from one to the next it would take two registers a channel.
+  auto channels = [&](int e0, auto f) {
+    int e = e0 + cg;
+    asm volatile("" : "+v"(e));
+    int64_t at = base + e * p.L;
+#pragma unroll
+    for (int c = 0; c < C; ++c, e += NG, at += step) f(c, e, at);
+  };
+  auto fetch = [&](Ch& k, int e0, bool side) {  // (positions behind the last one: whatever is there)
+    channels(e0, [&](int c, int e, int64_t at) {
+      const bool may = e < E && n > 0 && (!ODD || at + 8 <= total);
+      k.x[c].full(static_cast<const XT*>(p.x) + at, may);
+      if (RES) k.q[RES ? c : 0].full(static_cast<const HT*>(p.residual) + at, may);
+    });
+    if (side) {
+#pragma unroll
+      for (int c = 0; c < C; ++c) {
+        const int e = e0 + cg + c * NG, i = e < E ? e : 0;
+        k.w[c] = p.weight ? p.weight[i] : 1.0f;
+        k.c[c] = p.bias ? p.bias[i] : 0.0f;
+      }
+    }
+    if (ODD)
+      channels(e0, [&](int c, int e, int64_t at) {
+        if (e < E && n > 0 && at + 8 > total) {  // the tensor's end
+          Part r;
+          r.hi = n;
+          k.x[c].part(static_cast<const XT*>(p.x) + at, r);
+          if (RES) k.q[RES ? c : 0].part(static_cast<const HT*>(p.residual) + at, r);
+        }
+      });
+    if (DROP)
+      channels(e0, [&](int c, int, int64_t at) {
+        k.x[c].keep(drop.kept((uint64_t)at));
+        __builtin_amdgcn_sched_barrier(0);
+      });
+  };
+  auto sum = [&](const Ch& k, int c, float (&s)[8]) {  // what is normalised
+#pragma unroll
+    for (int i = 0; i < 8; ++i) s[i] = DROP ? k.x[c].at(i) * drop.scale : k.x[c].at(i);
+    if (RES) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) s[i] += k.q[RES ? c : 0].at(i);
+    }
+  };
+  // f(chunk, e0) for all channels
+  Ch kept;
+  if (KEEP) fetch(kept, 0, true);
+  auto pass = [&](bool side, auto f) {
+    if constexpr (KEEP) {
+      f(kept, 0);
+#pragma unroll
+      for (int c = 0; c < C; ++c) {
+        kept.x[c].forget();
+        if (RES) kept.q[RES ? c : 0].forget();
+      }
+    } else {
+      Ch next;
+      fetch(next, 0, side);
+      for (int e0 = 0; e0 < E; e0 += C * NG) {
+        const Ch now = next;
+        if (e0 + C * NG < E) fetch(next, e0 + C * NG, side);
+        f(now, e0);
+      }
+    }
+  };
+  auto keep = [&](const Ch& k, int e0) {
+    channels(e0, [&](int c, int e, int64_t at) {
+      float s[8];
+      sum(k, c, s);
+      if (e < E) store_cols(static_cast<HT*>(p.hidden) + at, n, s, lines);
+    });
+  };
+  float m[8], r[8];
+#pragma unroll
+  for (int k = 0; k < 8; ++k) m[k] = r[k] = 0.0f;
+  if constexpr (KEEP) {
+    if (p.hidden) pass(false, keep);
+    if (!p.rms) {
+      pass(false, [&](const Ch& k, int) {
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+          float s[8];
+          sum(k, c, s);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) m[i] += s[i];  // (zero for a channel that is not there)
+        }
+      });
+      sum_groups<NT, LP>(m, sm);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) m[k] *= p.inv_e;
+    }
+    pass(false, [&](const Ch& k, int) {
+#pragma unroll
+      for (int c = 0; c < C; ++c) {
+        float s[8];
+        sum(k, c, s);
+        if (cg + c * NG < E) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const float d = s[i] - m[i];
+            r[i] = __builtin_fmaf(d, d, r[i]);
+          }
+        }
+      }
+    });
+  } else {
+    // One pass: the lane's own mean and its squares about that, kept up to date channel by channel; the lanes' means
+    // then differ from the whole mean by what is added to the squares.
+    float mine[8], count = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) mine[i] = 0.0f;
+    pass(false, [&](const Ch& k, int e0) {
+#pragma unroll
+      for (int c = 0; c < C; ++c) {
+        if (e0 + cg + c * NG < E) {
+          float s[8];
+          sum(k, c, s);
+          count += 1.0f;
+          const float share = p.rms ? 0.0f : rcp_(count);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const float d = s[i] - mine[i];
+            mine[i] = __builtin_fmaf(d, share, mine[i]);
+            r[i] = __builtin_fmaf(d, s[i] - mine[i], r[i]);
+          }
+        }
+      }
+      if (p.hidden) keep(k, e0);
+    });
+    if (!p.rms) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) m[i] = mine[i] * count;
+      sum_groups<NT, LP>(m, sm);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        m[i] *= p.inv_e;
+        const float d = mine[i] - m[i];
+        r[i] = __builtin_fmaf(d * count, d, r[i]);
+      }
+    }
+  }
+  sum_groups<NT, LP>(r, sm);
+#pragma unroll
+  for (int k = 0; k < 8; ++k) r[k] = 1.0f / sqrtf(r[k] * p.inv_e + p.eps);
+  pass(true, [&](const Ch& k, int e0) {
+    channels(e0, [&](int c, int e, int64_t at) {
+      if (e >= E) return;
+      float s[8];
+      sum(k, c, s);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) s[i] = __builtin_fmaf((s[i] - m[i]) * r[i], k.w[c], k.c[c]);
+      store_cols(static_cast<XT*>(p.out) + at, n, s, lines);
+      __builtin_amdgcn_sched_barrier(0);  // a channel at a time: all together would take several times the registers
+    });
+  });
+  if (p.stats && cg == 0) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      if (k < n) {
+        p.stats[b * p.L + t + k] = m[k];
+        p.stats[p.rows + b * p.L + t + k] = r[k];
+      }
+  }
+}
+
+// Tiles in turn, everything read twice.  The lanes that own a channel add every tile's dw and db to the workgroup's
+// partial sums, which no other lane touches.
+template <typename XT, typename HT, bool ODD, int NT, int LP, int C>
+__global__ __launch_bounds__(NT) void norm_cols_bwd_kernel(NormParams p) {
+  constexpr int NG = NT / LP, T = LP * 8;
+  __shared__ float sm[(NT / 64 + 1) * T];
+  const int pl = threadIdx.x % LP, cg = threadIdx.x / LP, E = (int)p.E;
+  const int64_t tiles = (p.L + T - 1) / T, total = p.rows * p.E, step = NG * p.L;
+  const bool lines = !ODD && p.L % 64 == 0;
+  const Drop drop(p.drop);
+  float* part = p.part ? p.part + (int64_t)block_id() * 2 * p.E : nullptr;
+  struct Ch {
+    Piece<XT> d[C];
+    Piece<HT> h[C], q[C];
+    float w[C];
+  };
+  bool first = true;
+  for (int64_t tile = block_id(); tile < p.B * tiles; tile += p.blocks) {
+    const int64_t b = tile / tiles, t = tile % tiles * T + pl * 8;
+    const int n = p.L - t >= 8 ? 8 : !ODD || p.L <= t ? 0 : (int)(p.L - t);
+    const int64_t base = b * p.E * p.L + t;
+    Part real;
+    real.hi = n;
+    auto channels = [&](int e0, auto f) {
+      int e = e0 + cg;
+      asm volatile("" : "+v"(e));
+      int64_t at = base + e * p.L;
+#pragma unroll
+      for (int c = 0; c < C; ++c, e += NG, at += step) f(c, e, at);
+    };
+    auto fetch = [&](Ch& k, int e0, bool third) {
+      channels(e0, [&](int c, int e, int64_t at) {
+        const bool may = e < E && n > 0 && (!ODD || at + 8 <= total);
+        k.d[c].full(static_cast<const XT*>(p.x) + at, may);
+        k.h[c].full(static_cast<const HT*>(p.residual) + at, may);
+        if (third && p.dhidden) k.q[c].full(static_cast<const HT*>(p.dhidden) + at, may);
+        k.w[c] = p.weight ? p.weight[e < E ? e : 0] : 1.0f;
+      });
+      if (ODD)
+        channels(e0, [&](int c, int e, int64_t at) {
+          if (e < E && n > 0 && at + 8 > total) {
+            k.d[c].part(static_cast<const XT*>(p.x) + at, real);
+            k.h[c].part(static_cast<const HT*>(p.residual) + at, real);
+            if (third && p.dhidden) k.q[c].part(static_cast<const HT*>(p.dhidden) + at, real);
+          }
+          k.d[c].cut(real);  // (what lies behind the last position takes no part in dw and db)
+          k.h[c].cut(real);
+        });
+    };
+    float m[8], r[8], c1[8], c2[8];
+    load_n<float, 8>(p.stats + b * p.L + t, n, m);
+    load_n<float, 8>(p.stats + p.rows + b * p.L + t, n, r);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) c1[k] = c2[k] = 0.0f;
+    auto pass = [&](bool third, auto f) {
+      Ch next;
+      fetch(next, 0, third);
+      for (int e0 = 0; e0 < E; e0 += C * NG) {
+        const Ch now = next;
+        if (e0 + C * NG < E) fetch(next, e0 + C * NG, third);
+        f(now, e0);
+      }
+    };
+    pass(false, [&](const Ch& k, int e0) {
+      channels(e0, [&](int c, int e, int64_t) {
+        float dw = 0.0f, db = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {  // (d is 0 for a channel that is not there, r behind the last position)
+          const float g = k.d[c].at(i), x = (k.h[c].at(i) - m[i]) * r[i];
+          dw = __builtin_fmaf(g, x, dw);
+          db += g;
+          c1[i] = __builtin_fmaf(g, k.w[c], c1[i]);
+          c2[i] = __builtin_fmaf(g * k.w[c], x, c2[i]);
+        }
+        if (part) {
+          dw = sum_positions<LP>(dw);
+          db = sum_positions<LP>(db);
+          if (pl == 0 && e < E) {
+            part[e] = first ? dw : part[e] + dw;
+            part[E + e] = first ? db : part[E + e] + db;
+          }
+        }
+        __builtin_amdgcn_sched_barrier(0);
+      });
+    });
+    if (!p.rms) sum_groups<NT, LP>(c1, sm);
+    sum_groups<NT, LP>(c2, sm);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      c1[k] = p.rms ? 0.0f : c1[k] * p.inv_e;
+      c2[k] *= p.inv_e;
+    }
+    pass(true, [&](const Ch& k, int e0) {
+      channels(e0, [&](int c, int e, int64_t at) {
+        if (e >= E) return;
+        float g[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float x = (k.h[c].at(i) - m[i]) * r[i];
+          g[i] = r[i] * (k.d[c].at(i) * k.w[c] - c1[i] - x * c2[i]);
+        }
+        if (p.dhidden) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) g[i] += k.q[c].at(i);
+        }
+        if (p.hidden) store_cols(static_cast<HT*>(p.hidden) + at, n, g, lines);
+        if (p.out) {
+          if (drop.any()) drop.apply(drop.kept((uint64_t)at), g);
+          store_cols(static_cast<XT*>(p.out) + at, n, g, lines);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+      });
+    });
+    first = false;
+  }
+}
+
+namespace {
+
+// Channels that a lane keeps: of 512 lanes they fill 128 registers each.
+template <typename XT, typename HT, bool RES> constexpr int kept_channels() {
+  constexpr int regs = 2 * (int)sizeof(XT) + (RES ? 2 * (int)sizeof(HT) : 0);  // of one
+  return regs <= 4 ? 32 : regs <= 8 ? 16 : 8;
+}
+
+template <typename XT, typename HT, bool RES, bool DROP, bool ODD, int NT, int LP, int C, bool KEEP>
+void go(const NormParams& p, hipStream_t s) {
+  hipLaunchKernelGGL((norm_cols_kernel<XT, HT, RES, DROP, ODD, NT, LP, C, KEEP>),
+                     grid_of(p.B * ((p.L + LP * 8 - 1) / (LP * 8))), dim3(NT), 0, s, p);
+}
+
+// Everything read again for each pass.
+template <typename XT, typename HT, bool RES, bool DROP>
+void again(const NormParams& p, bool wide, hipStream_t s) {
+  if (p.L % 8) return go<XT, HT, RES, DROP, true, 512, 16, 2, false>(p, s);
+  if (p.B * ((p.L + 63) / 64) < kFewTiles) return go<XT, HT, RES, DROP, false, 1024, 2, 2, false>(p, s);
+  wide ? go<XT, HT, RES, DROP, false, 512, 32, 2, false>(p, s) : go<XT, HT, RES, DROP, false, 1024, 8, 2, false>(p, s);
+}
+
+// Wide tiles read and write longer pieces of the rows, which lie far apart (2^17 positions x 1024 channels in bf16: 125
+// us with 64 positions, 114 with 128; 2^18 x 512: 122, 112, and 105 with 256), but hold fewer channels and leave compute
+// units idle where there are few of them.
+template <typename XT, typename HT, bool RES>
+void fwd(const NormParams& p, hipStream_t s) {
+  constexpr int C = kept_channels<XT, HT, RES>();
+  const bool wide = p.B * ((p.L + 127) / 128) >= 512;
+  if (p.drop.below) return again<XT, HT, RES, true>(p, wide, s);
+  if (p.L % 8) {
+    if (p.E <= 16 * (C / 4)) return go<XT, HT, RES, false, true, 256, 16, C / 4, true>(p, s);
+    if (p.E <= 64 * (C / 4)) return go<XT, HT, RES, false, true, 512, 8, C / 4, true>(p, s);
+    return again<XT, HT, RES, false>(p, wide, s);
+  }
+  if (p.E <= 16 * (C / 4)) return go<XT, HT, RES, false, false, 256, 16, C / 4, true>(p, s);
+  if (wide && p.E <= 32 * (C / 4)) return go<XT, HT, RES, false, false, 512, 16, C / 4, true>(p, s);
+  if (p.E <= 64 * (C / 4)) return go<XT, HT, RES, false, false, 512, 8, C / 4, true>(p, s);
+  if (wide && p.E <= 32 * C) return go<XT, HT, RES, false, false, 512, 16, C, true>(p, s);
+  if (p.E <= 64 * C) return go<XT, HT, RES, false, false, 512, 8, C, true>(p, s);
+  again<XT, HT, RES, false>(p, wide, s);
+}
+
+template <typename XT, typename HT, bool ODD, int NT, int LP, int C>
+void go_bwd(const NormParams& p, hipStream_t s) {
+  hipLaunchKernelGGL((norm_cols_bwd_kernel<XT, HT, ODD, NT, LP, C>), grid_of(p.blocks), dim3(NT), 0, s, p);
+}
+
+template <typename XT, typename HT>
+void bwd(const NormParams& p, hipStream_t s) {
+  const int T = norm_cols_bwd_tile(p.B, p.L);
+  if (p.L % 8) return T > 64 ? go_bwd<XT, HT, true, 512, 16, 2>(p, s) : go_bwd<XT, HT, true, 1024, 8, 1>(p, s);
+  if (T == 256) return go_bwd<XT, HT, false, 512, 32, 2>(p, s);
+  if (T == 128) return go_bwd<XT, HT, false, 512, 16, 2>(p, s);
+  if (T == 16) return go_bwd<XT, HT, false, 1024, 2, 2>(p, s);
+  go_bwd<XT, HT, false, 1024, 8, 1>(p, s);
+}
+
+}  // namespace
+
+}  // namespace ssm
