@@ -23,10 +23,29 @@ import torch
 
 from ._lib import (SSM_BF16, SSM_FLAG_REVERSE, _check, _empty, _expect, _hand_out, _io_dtype, _nonempty, _ptr, load,
                    ssm_dropout, ssm_norm_shape, ssm_recurrence_shape)
-from .training import (SSM_FLAG_CHANNELS_FIRST, _KIND, _address, _capturing, _stream, _want, _workspace)
+from .training import SSM_FLAG_CHANNELS_FIRST, _KIND, _address, _capturing, _stream, _workspace
 
 SSM_FLAG_RMS = 4
 _NONE = 0xFFFFFFFFFFFFFFFF
+
+
+# Every tensor of a call is checked and turned into its address in one go.
+
+def _arg(t, shape, dtype, name, device):
+    """The address of a tensor that has to look like this (None for None); an error says what does not."""
+    if t is None:
+        return None
+    if t.shape != shape or t.dtype != dtype or t.device != device or not t.is_contiguous():
+        _expect(t, shape, dtype, name, device)
+        _ptr(t)
+    return t.data_ptr()
+
+
+def _like(t, dtype, stream):
+    """An uninitialised tensor of t's shape; torch's quicker call where the dtype and the stream allow it."""
+    if stream is None and dtype == t.dtype:
+        return torch.empty_like(t, memory_format=torch.contiguous_format)
+    return _empty(t.shape, dtype, t.device, stream)
 
 
 def _mask(p, seed, call, device, stream, fresh):
@@ -46,10 +65,6 @@ def _mask(p, seed, call, device, stream, fresh):
     if fresh and _capturing(stream):
         raise RuntimeError("every replay would repeat this call's mask: give the seed as a tensor on the device")
     return ssm_dropout(p, seed & _NONE, None, call & _NONE)
-
-
-def _ref(struct):
-    return None if struct is None else ctypes.byref(struct)
 
 
 def dropout_fwd(x, p, seed, *, call=0, residual=None, out=None, stream=None):
@@ -74,14 +89,13 @@ def _dropout(x, mask, residual, dtype, out, stream):
     kinds = _KIND.get(x.dtype), _KIND.get(dtype)
     if None in kinds:
         raise TypeError("streams must be float32 or bfloat16, got %s" % (x.dtype if kinds[0] is None else dtype))
-    _want(residual, x.shape, dtype, "residual", device)
+    px, pr = _address(x), _arg(residual, x.shape, dtype, "residual", device)
     if out is None:
-        out = made = _empty(x.shape, dtype, device, stream)
-    else:
-        _want(out, x.shape, dtype, "out", device)
-    _check(load().ssm_dropout_fwd(n, *kinds, _address(x), _address(residual), ctypes.byref(mask), _address(out),
+        out = made = _like(x, dtype, stream)
+    _check(load().ssm_dropout_fwd(n, *kinds, px, pr, mask, _arg(out, x.shape, dtype, "out", device),
                                   _stream(stream, device)))
-    _hand_out(stream, made)
+    if stream is not None:
+        _hand_out(stream, made)
     return out
 
 
@@ -119,47 +133,43 @@ def layer_norm_fwd(x, weight=None, bias=None, residual=None, *, eps=1e-5, rms=Fa
     itself where there is no dropout either), stats [2, rows] in fp32: the means (rms: zeros) and the factors
     1 / sqrt(variance + eps), for layer_norm_bwd; stats=False: not wanted.
     p, seed, call: dropout of x, as in dropout_fwd."""
-    device, f32, shape = x.device, torch.float32, x.shape
-    hdt = x.dtype if residual is None else residual.dtype
-    sh, rows, E = _norm_shape(shape, x.dtype, hdt, rms, channels_first)
-    mask = _mask(p, seed, call, device, stream, True)
-    _want(residual, shape, hdt, "residual", device)
-    _want(weight, (E,), f32, "weight", device)
-    _want(bias, (E,), f32, "bias", device)
-    made = []
+    device, f32, shape, xdt = x.device, torch.float32, x.shape, x.dtype
+    hdt = xdt if residual is None else residual.dtype
+    sh, rows, E = _norm_shape(shape, xdt, hdt, rms, channels_first)
+    mask = _mask(p, seed, call, device, stream, True) if p else None
+    pr = _arg(residual, shape, hdt, "residual", device)
+    pw, pb = _arg(weight, (E,), f32, "weight", device), _arg(bias, (E,), f32, "bias", device)
+    plain = residual is None and mask is None
+    if plain and hidden is not None:
+        raise ValueError("hidden: without a residual and dropout it is x itself")
+    px, made = _address(x), []
     if out is None:
-        out = _empty(shape, x.dtype, device, stream)
+        out = _like(x, xdt, stream)
         made.append(out)
+    po = _arg(out, shape, xdt, "out", device)
+    if plain:
+        ph, hidden = None, x
     else:
-        _want(out, shape, x.dtype, "out", device)
-    if residual is None and mask is None:
-        if hidden is not None:
-            raise ValueError("hidden: without a residual and dropout it is x itself")
-        kept, hidden = None, x
-    elif hidden is None:
-        kept = hidden = _empty(shape, hdt, device, stream)
-        made.append(hidden)
-    else:
-        _want(hidden, shape, hdt, "hidden", device)
-        kept = hidden
+        if hidden is None:
+            hidden = _like(x if residual is None else residual, hdt, stream)
+            made.append(hidden)
+        ph = _arg(hidden, shape, hdt, "hidden", device)
     if stats is None:
         stats = _empty((2, rows), f32, device, stream)
         made.append(stats)
     elif stats is False:
         stats = None
-    else:
-        _want(stats, (2, rows), f32, "stats", device)
-    _check(load().ssm_layer_norm_fwd(ctypes.byref(sh), _address(x), _address(weight), _address(bias), _address(residual),
-                                     eps, _ref(mask), _address(out), _address(kept), _address(stats),
+    _check(load().ssm_layer_norm_fwd(sh, px, pw, pb, pr, eps, mask, po, ph, _arg(stats, (2, rows), f32, "stats", device),
                                      _stream(stream, device)))
-    _hand_out(stream, *made)
+    if stream is not None:
+        _hand_out(stream, *made)
     return out, hidden, stats
 
 
 def layer_norm_bwd_workspace_size(dout, *, hidden_dtype=None, channels_first=False) -> int:
     """Workspace bytes of layer_norm_bwd."""
     sh, _, _ = _norm_shape(dout.shape, dout.dtype, hidden_dtype or dout.dtype, False, channels_first)
-    return int(load().ssm_layer_norm_bwd_workspace_size(ctypes.byref(sh)))
+    return int(load().ssm_layer_norm_bwd_workspace_size(sh))
 
 
 def layer_norm_bwd(dout, hidden, weight, stats, *, dhidden=None, rms=False, channels_first=False, p=0.0, seed=None, call=0,
@@ -172,32 +182,29 @@ def layer_norm_bwd(dout, hidden, weight, stats, *, dhidden=None, rms=False, chan
     if x_dtype is not None and x_dtype != dout.dtype:
         raise TypeError("dout: expected x's dtype %s, got %s" % (x_dtype, dout.dtype))
     sh, rows, E = _norm_shape(shape, dout.dtype, hdt, rms, channels_first)
-    mask = _mask(p, seed, call, device, stream, False)
-    _want(hidden, shape, hdt, "hidden", device)
-    _want(dhidden, shape, hdt, "dhidden", device)
-    _want(weight, (E,), f32, "weight", device)
-    _want(stats, (2, rows), f32, "stats", device)
+    mask = _mask(p, seed, call, device, stream, False) if p else None
+    ph, pdh = _arg(hidden, shape, hdt, "hidden", device), _arg(dhidden, shape, hdt, "dhidden", device)
+    pw, ps = _arg(weight, (E,), f32, "weight", device), _arg(stats, (2, rows), f32, "stats", device)
     one = residual and mask is None and hdt == dout.dtype
-    g, made = dict(grads) if grads else {}, []
+    g, made, to = dict(grads) if grads else {}, [], []
     for k, wanted, shp, dt in (("dx", not one, shape, dout.dtype), ("dresidual", residual, shape, hdt),
                                ("dweight", weight is not None, (E,), f32), ("dbias", bias, (E,), f32)):
+        t = g.get(k)
         if not wanted:
-            if g.get(k) is not None and not (k == "dx" and g[k] is g.get("dresidual")):
+            if t is not None and not (k == "dx" and t is g.get("dresidual")):
                 raise ValueError("grads: %s is not computed here" % k)
-            g[k] = None
-        elif g.get(k) is None:
-            g[k] = _empty(shp, dt, device, stream)
-            made.append(g[k])
-        else:
-            _want(g[k], shp, dt, k, device)
-    lib, ws_bytes = load(), 0
-    if g["dweight"] is not None or g["dbias"] is not None:
-        workspace, ws_bytes = _workspace(workspace, lib.ssm_layer_norm_bwd_workspace_size(ctypes.byref(sh)), device, stream)
-    _check(lib.ssm_layer_norm_bwd(ctypes.byref(sh), _address(dout), _address(hidden), _address(weight), _address(stats),
-                                  _address(dhidden), _ref(mask), _address(g["dx"]), _address(g["dresidual"]),
-                                  _address(g["dweight"]), _address(g["dbias"]), _address(workspace), ws_bytes,
-                                  _stream(stream, device)))
-    _hand_out(stream, *made)
+            g[k] = t = None
+        elif t is None:
+            g[k] = t = _empty(shp, dt, device, stream) if k[1] in "wb" else _like(dout if k == "dx" else hidden, dt, stream)
+            made.append(t)
+        to.append(_arg(t, shp, dt, k, device))
+    pd, lib, ws_bytes, pws = _address(dout), load(), 0, None
+    if to[2] is not None or to[3] is not None:
+        workspace, ws_bytes = _workspace(workspace, lib.ssm_layer_norm_bwd_workspace_size(sh), device, stream)
+        pws = _address(workspace)
+    _check(lib.ssm_layer_norm_bwd(sh, pd, ph, pw, ps, pdh, mask, *to, pws, ws_bytes, _stream(stream, device)))
+    if stream is not None:
+        _hand_out(stream, *made)
     if one:
         g["dx"] = g["dresidual"]
     return g
@@ -210,6 +217,15 @@ def _recurrence_shape(x, reverse):
     if B < 1 or D < 1 or L < 1:
         _nonempty(batch=B, dim=D, seqlen=L)
     return ssm_recurrence_shape(B, D, L, _io_dtype(x), SSM_FLAG_REVERSE if reverse else 0), B, D
+
+
+def _recurrence_args(x, r, i, decay, r_bias, i_bias, z, state, full, ends, device):
+    """The addresses of a call's inputs, in the order of the C entry points."""
+    dt, f32, D = x.dtype, torch.float32, (ends[1],)
+    others = (_arg(r, full, dt, "r", device), _arg(i, full, dt, "i", device), _arg(decay, D, f32, "decay", device),
+              _arg(r_bias, D, f32, "r_bias", device), _arg(i_bias, D, f32, "i_bias", device),
+              _arg(z, full, dt, "z", device), _arg(state, ends, f32, "initial_state", device))
+    return (_address(x), *others)
 
 
 def recurrence_checkpoints_shape(batch, dim, seqlen, io_dtype=SSM_BF16):
@@ -238,33 +254,28 @@ def recurrence_fwd(x, r, i, decay, r_bias=None, i_bias=None, z=None, initial_sta
     checkpoints: an fp32 tensor of recurrence_checkpoints_shape(...) to write for recurrence_bwd."""
     lib = load()
     sh, B, D = _recurrence_shape(x, reverse)
-    device, dt, f32, full, made = x.device, x.dtype, torch.float32, x.shape, []
-    for t, shp, d, name in ((r, full, dt, "r"), (i, full, dt, "i"), (z, full, dt, "z"), (decay, (D,), f32, "decay"),
-                            (r_bias, (D,), f32, "r_bias"), (i_bias, (D,), f32, "i_bias"),
-                            (initial_state, (B, D), f32, "initial_state")):
-        _want(t, shp, d, name, device)
+    device, made = x.device, []
+    ins = _recurrence_args(x, r, i, decay, r_bias, i_bias, z, initial_state, x.shape, (B, D), device)
     if out is None:
-        out = _empty(full, dt, device, stream)
+        out = _like(x, x.dtype, stream)
         made.append(out)
-    else:
-        _want(out, full, dt, "out", device)
     if final_state is True:
-        final_state = _empty((B, D), f32, device, stream)
+        final_state = _empty((B, D), torch.float32, device, stream)
         made.append(final_state)
     elif final_state is False:
         final_state = None
-    else:
-        _want(final_state, (B, D), f32, "final_state", device)
+    pc = None
     if checkpoints is not None:
-        _want(checkpoints, (B, D, lib.ssm_recurrence_checkpoints(ctypes.byref(sh))), f32, "checkpoints", device)
-    need, ws_bytes = lib.ssm_recurrence_workspace_size(ctypes.byref(sh)), 0
+        pc = _arg(checkpoints, (B, D, lib.ssm_recurrence_checkpoints(sh)), torch.float32, "checkpoints", device)
+    need, ws_bytes, pws = lib.ssm_recurrence_workspace_size(sh), 0, None
     if need or workspace is not None:
         workspace, ws_bytes = _workspace(workspace, need, device, stream)
-    _check(lib.ssm_recurrence_fwd(ctypes.byref(sh), _address(x), _address(r), _address(i), _address(decay),
-                                  _address(r_bias), _address(i_bias), _address(z), _address(initial_state), _address(out),
-                                  _address(final_state), _address(checkpoints), _address(workspace), ws_bytes,
+        pws = _address(workspace)
+    _check(lib.ssm_recurrence_fwd(sh, *ins, _arg(out, x.shape, x.dtype, "out", device),
+                                  _arg(final_state, (B, D), torch.float32, "final_state", device), pc, pws, ws_bytes,
                                   _stream(stream, device)))
-    _hand_out(stream, *made)
+    if stream is not None:
+        _hand_out(stream, *made)
     return out, final_state
 
 
@@ -278,32 +289,26 @@ def recurrence_bwd(x, r, i, decay, r_bias=None, i_bias=None, z=None, initial_sta
     lib = load()
     sh, B, D = _recurrence_shape(x, reverse)
     device, dt, f32, full = x.device, x.dtype, torch.float32, x.shape
-    for t, shp, d, name in ((r, full, dt, "r"), (i, full, dt, "i"), (z, full, dt, "z"), (decay, (D,), f32, "decay"),
-                            (r_bias, (D,), f32, "r_bias"), (i_bias, (D,), f32, "i_bias"),
-                            (initial_state, (B, D), f32, "initial_state"), (dout, full, dt, "dout"),
-                            (dfinal_state, (B, D), f32, "dfinal_state")):
-        _want(t, shp, d, name, device)
+    pd, pl = _arg(dout, full, dt, "dout", device), _arg(dfinal_state, (B, D), f32, "dfinal_state", device)
+    pc = None
     if checkpoints is not None:
-        _want(checkpoints, (B, D, lib.ssm_recurrence_checkpoints(ctypes.byref(sh))), f32, "checkpoints", device)
-    g, made = dict(grads) if grads else {}, []
+        pc = _arg(checkpoints, (B, D, lib.ssm_recurrence_checkpoints(sh)), f32, "checkpoints", device)
+    ins = _recurrence_args(x, r, i, decay, r_bias, i_bias, z, initial_state, full, (B, D), device)
+    g, made, to = dict(grads) if grads else {}, [], []
     for k, shp, d in (("dx", full, dt), ("dr", full, dt), ("di", full, dt), ("dz", full, dt), ("ddecay", (D,), f32),
                       ("dr_bias", (D,), f32), ("di_bias", (D,), f32), ("dinitial_state", (B, D), f32)):
+        t = g.get(k)
         if k == "dz" and z is None:
-            g[k] = None
-        elif g.get(k) is None:
-            g[k] = _empty(shp, d, device, stream)
-            made.append(g[k])
-        else:
-            _want(g[k], shp, d, k, device)
-    need = lib.ssm_recurrence_bwd_workspace_size(ctypes.byref(sh), 0 if checkpoints is None else 1)
+            g[k] = t = None
+        elif t is None:
+            g[k] = t = _like(x, dt, stream) if shp is full else _empty(shp, d, device, stream)
+            made.append(t)
+        to.append(_arg(t, shp, d, k, device))
+    need = lib.ssm_recurrence_bwd_workspace_size(sh, 0 if pc is None else 1)
     workspace, ws_bytes = _workspace(workspace, need, device, stream)
-    _check(lib.ssm_recurrence_bwd(ctypes.byref(sh), _address(x), _address(r), _address(i), _address(decay),
-                                  _address(r_bias), _address(i_bias), _address(z), _address(initial_state), _address(dout),
-                                  _address(dfinal_state), _address(checkpoints), _address(g["dx"]), _address(g["dr"]),
-                                  _address(g["di"]), _address(g["dz"]), _address(g["ddecay"]), _address(g["dr_bias"]),
-                                  _address(g["di_bias"]), _address(g["dinitial_state"]), _address(workspace), ws_bytes,
-                                  _stream(stream, device)))
-    _hand_out(stream, *made)
+    _check(lib.ssm_recurrence_bwd(sh, *ins, pd, pl, pc, *to, _address(workspace), ws_bytes, _stream(stream, device)))
+    if stream is not None:
+        _hand_out(stream, *made)
     return g
 
 
@@ -315,16 +320,13 @@ def recurrence_update(state, x, r, i, decay, r_bias=None, i_bias=None, z=None, *
     B, D = size = x.shape
     if B < 1 or D < 1:
         _nonempty(batch=B, dim=D)
-    io, device, dt, f32, made = _io_dtype(x), x.device, x.dtype, torch.float32, None
-    for t, shp, d, name in ((state, size, f32, "state"), (r, size, dt, "r"), (i, size, dt, "i"), (z, size, dt, "z"),
-                            (decay, (D,), f32, "decay"), (r_bias, (D,), f32, "r_bias"), (i_bias, (D,), f32, "i_bias")):
-        _want(t, shp, d, name, device)
+    io, device, dt, made = _io_dtype(x), x.device, x.dtype, None
+    ps = _arg(state, size, torch.float32, "state", device)
+    ins = _recurrence_args(x, r, i, decay, r_bias, i_bias, z, None, size, size, device)
     if out is None:
-        out = made = _empty(size, dt, device, stream)
-    else:
-        _want(out, size, dt, "out", device)
-    _check(load().ssm_recurrence_update(B, D, io, _address(state), _address(x), _address(r), _address(i), _address(decay),
-                                        _address(r_bias), _address(i_bias), _address(z), _address(out),
-                                        _stream(stream, device)))
-    _hand_out(stream, made)
+        out = made = _like(x, dt, stream)
+    _check(load().ssm_recurrence_update(B, D, io, ps, *ins[:7],
+                                        _arg(out, size, dt, "out", device), _stream(stream, device)))
+    if stream is not None:
+        _hand_out(stream, made)
     return out

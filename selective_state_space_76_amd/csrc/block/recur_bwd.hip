@@ -14,14 +14,14 @@
 
 namespace ssm {
 
-// MAPS: the segments' maps of the adjoint
-template <typename IO, int LN, int W, bool REV, bool MAPS>
-__global__ __launch_bounds__(256) void recur_bwd_kernel(RecurParams p) {
+// Z: there is a gate.  MAPS: the segments' maps of the adjoint.
+template <typename IO, int LN, int W, bool REV, bool Z, bool MAPS>
+__global__ __launch_bounds__(W > 4 ? W * 64 : 256, Z || LN == 16 ? 3 : 4) void recur_bwd_kernel(RecurParams p) {
   constexpr int V = 16 / (int)sizeof(IO);
-  constexpr int UNITS = 256 / (LN * W);
+  constexpr int UNITS = W > 4 ? 1 : 256 / (LN * W);
   constexpr int TURN = LN * W * V;
   __shared__ float sm[2][W][2];
-  const int lane = threadIdx.x % LN, w = W > 1 ? threadIdx.x / 64 : 0;
+  const int lane = threadIdx.x % LN, w = W > 1 ? __builtin_amdgcn_readfirstlane(threadIdx.x / 64) : 0;
   const int64_t S = MAPS ? p.plan.S - 1 : p.plan.S;
   const int64_t rows = p.B * p.D;
   int64_t unit = (int64_t)block_id() * UNITS + (W > 1 ? 0 : threadIdx.x / LN);
@@ -55,12 +55,13 @@ __global__ __launch_bounds__(256) void recur_bwd_kernel(RecurParams p) {
   auto load = [&](int64_t tile) {
     const int64_t s = tile * TURN + (w * LN + lane) * V, at = line.at(s);
     const int lo = line.lo(s), hi = line.hi(s);
-    rn = load_slots<IO, REV>(p.r, at, lo, hi);
-    gn = load_slots<IO, REV>(p.dout, at, lo, hi);
-    if (p.z) zn = load_slots<IO, REV>(p.z, at, lo, hi);
+    const bool edge = line.edge(tile * TURN, TURN);
+    rn = load_slots<IO, REV>(p.r, at, lo, hi, edge);
+    gn = load_slots<IO, REV>(p.dout, at, lo, hi, edge);
+    if (Z) zn = load_slots<IO, REV>(p.z, at, lo, hi, edge);
     if (!MAPS) {
-      xn = load_slots<IO, REV>(p.x, at, lo, hi);
-      in = load_slots<IO, REV>(p.i, at, lo, hi);
+      xn = load_slots<IO, REV>(p.x, at, lo, hi, edge);
+      in = load_slots<IO, REV>(p.i, at, lo, hi, edge);
       const int64_t block = LN == 64 ? tile * W + w : 0;
       hn = p.ckpt[row * p.plan.blocks + (block < p.plan.blocks ? block : p.plan.blocks - 1)];
     }
@@ -69,35 +70,47 @@ __global__ __launch_bounds__(256) void recur_bwd_kernel(RecurParams p) {
   float state = 0.0f;  // LN = 16: the state that enters the first tile; the others' by walking up first
   if (k0 < k1) load(k1 - 1);
   for (int64_t tile = k1 - 1; tile >= k0; --tile) {
-    const u32x4a xq = xn, rq = rn, iq = in, zq = zn, gq = gn;
+    const u32x4a xq = xn, rq = rn, uq = in, zq = zn, gq = gn;
     state = hn;
     if (tile > k0) load(tile - 1);
     const int64_t s = tile * TURN + (w * LN + lane) * V;
     const int lo = line.lo(s), hi = line.hi(s);
-    float a[V], v[V], g[V], sig[V], sgi[V], wq[V], hb[V];
-    float A = 1.0f, B = 0.0f, FA = 1.0f, FB = 0.0f;
+    const bool edge = line.edge(tile * TURN, TURN);
+    float a[V], v[V], g[V], sig[V], sgi[V], q[V], iq[V], sz[V];
 #pragma unroll
     for (int e = 0; e < V; ++e) {
-      const Gates q(slot<IO, REV>(rq, e), slot<IO, REV>(iq, e), ch);
-      a[e] = q.a;
-      sig[e] = q.sr;
-      sgi[e] = q.si;
-      wq[e] = q.w;
-      v[e] = __builtin_amdgcn_sqrtf(q.w) * q.si * slot<IO, REV>(xq, e);
+      const Gates k(slot<IO, REV>(rq, e), slot<IO, REV>(uq, e), ch);
+      a[e] = k.a;
+      sig[e] = k.sr;
+      sgi[e] = k.si;
+      q[e] = k.q;
+      iq[e] = k.iq;
+      v[e] = k.q * k.si * slot<IO, REV>(xq, e);
       g[e] = slot<IO, REV>(gq, e);
-      if (p.z) g[e] *= silu_(slot<IO, REV>(zq, e));
-      if (e < lo || e >= hi) {
-        a[e] = 1.0f;
-        v[e] = g[e] = 0.0f;
+      if (Z) {
+        const float z = slot<IO, REV>(zq, e);
+        sz[e] = sigmoid_(z);
+        g[e] *= z * sz[e];
       }
+    }
+    if (edge) {  // the identity where there is no step, and nothing that would add to the sums
+#pragma unroll
+      for (int e = 0; e < V; ++e) {
+        const bool step = e >= lo && e < hi;
+        a[e] = step ? a[e] : 1.0f;
+        v[e] = step ? v[e] : 0.0f;
+        g[e] = step ? g[e] : 0.0f;
+      }
+    }
+    float A = a[0], B = v[0], FA = 1.0f, FB = 0.0f;
+#pragma unroll
+    for (int e = 1; e < V; ++e) {
       A *= a[e];
       B = __builtin_fmaf(a[e], B, v[e]);
     }
 #pragma unroll
-    for (int e = V - 1; e >= 0; --e) {
-      FB = a[e] * (g[e] + FB);
-      FA *= a[e];
-    }
+    for (int e = V - 1; e >= 0; --e) FB = a[e] * (g[e] + FB);
+    FA = A;
     scan_down<LN>(FA, FB);
     const float ta = end_lane<LN, false>(FA), tb = end_lane<LN, false>(FB);
     float behind = carry;
@@ -105,17 +118,17 @@ __global__ __launch_bounds__(256) void recur_bwd_kernel(RecurParams p) {
       carry = __builtin_fmaf(ta, carry, tb);
       whole *= ta;
     } else {
-      float (*q)[2] = sm[tile & 1];
+      float (*to)[2] = sm[tile & 1];
       if ((threadIdx.x & 63) == 0) {
-        q[w][0] = ta;
-        q[w][1] = tb;
+        to[w][0] = ta;
+        to[w][1] = tb;
       }
       __syncthreads();
 #pragma unroll
       for (int k = W - 1; k >= 0; --k) {
         if (k == w) behind = carry;
-        carry = __builtin_fmaf(q[k][0], carry, q[k][1]);
-        whole *= q[k][0];
+        carry = __builtin_fmaf(to[k][0], carry, to[k][1]);
+        whole *= to[k][0];
       }
     }
     if (MAPS) continue;
@@ -125,15 +138,15 @@ __global__ __launch_bounds__(256) void recur_bwd_kernel(RecurParams p) {
       for (int64_t k = 0; k < tile; ++k) {
         const int64_t sk = k * TURN + lane * V, at = line.at(sk);
         const int lk = line.lo(sk), hk = line.hi(sk);
-        const u32x4a x0 = load_slots<IO, REV>(p.x, at, lk, hk), r0 = load_slots<IO, REV>(p.r, at, lk, hk);
-        const u32x4a i0 = load_slots<IO, REV>(p.i, at, lk, hk);
+        const u32x4a x0 = load_slots<IO, REV>(p.x, at, lk, hk, true), r0 = load_slots<IO, REV>(p.r, at, lk, hk, true);
+        const u32x4a i0 = load_slots<IO, REV>(p.i, at, lk, hk, true);
         float UA = 1.0f, UB = 0.0f;
 #pragma unroll
         for (int e = 0; e < V; ++e) {
           if (e < lk || e >= hk) continue;
-          const Gates q(slot<IO, REV>(r0, e), slot<IO, REV>(i0, e), ch);
-          UA *= q.a;
-          UB = __builtin_fmaf(q.a, UB, __builtin_amdgcn_sqrtf(q.w) * q.si * slot<IO, REV>(x0, e));
+          const Gates k(slot<IO, REV>(r0, e), slot<IO, REV>(i0, e), ch);
+          UA *= k.a;
+          UB = __builtin_fmaf(k.a, UB, k.q * k.si * slot<IO, REV>(x0, e));
         }
         scan_up<LN>(UA, UB);
         state = __builtin_fmaf(end_lane<LN, true>(UA), state, end_lane<LN, true>(UB));
@@ -141,42 +154,46 @@ __global__ __launch_bounds__(256) void recur_bwd_kernel(RecurParams p) {
     }
     scan_up<LN>(A, B);
     float h = __builtin_fmaf(lane_before<LN>(A, 1.0f), state, lane_before<LN>(B, 0.0f));
+    const int64_t at = line.at(s);
+    float hb[V], o[V];
 #pragma unroll
     for (int e = 0; e < V; ++e) {
       hb[e] = h;
       h = __builtin_fmaf(a[e], h, v[e]);
-    }
-    // the adjoint, and with it the gradients
-    float F = __builtin_fmaf(lane_behind<LN>(FA, 1.0f), behind, lane_behind<LN>(FB, 0.0f));
-    float dx[V], dr[V], di[V], dz[V];
-#pragma unroll
-    for (int e = V - 1; e >= 0; --e) {
-      const bool step = e >= lo && e < hi;
-      const float G = g[e] + F;
-      F = a[e] * G;
-      const float x = slot<IO, REV>(xq, e);
-      // 1 / q; where a is 1 to the last bit (sig(r) under 2^-100 / decay) what it meets below is zero
-      const float rq1 = __builtin_amdgcn_rsqf(fmaxf(wq[e], 7.888609e-31f)), q = wq[e] * rq1;
-      const float gs = G * sgi[e];
-      dx[e] = gs * q;
-      di[e] = gs * q * x * (1.0f - sgi[e]);
-      float dla = __builtin_fmaf(G * a[e], hb[e], -gs * x * (a[e] * a[e] * rq1));
-      dla = step ? dla : 0.0f;
-      const float dls = -dla * sig[e];
-      dr[e] = dls * decay * (1.0f - sig[e]);
-      sd += dls;
-      sr += dr[e];
-      si += step ? di[e] : 0.0f;
-      if (p.z) {
-        const float z = slot<IO, REV>(zq, e), s1 = sigmoid_(z), hh = __builtin_fmaf(a[e], hb[e], v[e]);
-        dz[e] = slot<IO, REV>(gq, e) * hh * (s1 * __builtin_fmaf(z, 1.0f - s1, 1.0f));
+      if (Z) {
+        const float z = slot<IO, REV>(zq, e);
+        o[e] = slot<IO, REV>(gq, e) * h * (sz[e] * __builtin_fmaf(z, 1.0f - sz[e], 1.0f));
       }
     }
-    const int64_t at = line.at(s);
-    store_slots<IO, REV>(p.dx, at, lo, hi, dx);
-    store_slots<IO, REV>(p.dr, at, lo, hi, dr);
-    store_slots<IO, REV>(p.di, at, lo, hi, di);
-    if (p.z) store_slots<IO, REV>(p.dz, at, lo, hi, dz);
+    if (Z) store_slots<IO, REV>(p.dz, at, lo, hi, edge, o);
+    // the adjoint: G in g's place
+    float F = __builtin_fmaf(lane_behind<LN>(FA, 1.0f), behind, lane_behind<LN>(FB, 0.0f));
+#pragma unroll
+    for (int e = V - 1; e >= 0; --e) {
+      g[e] += F;
+      F = a[e] * g[e];
+    }
+    if (edge) {
+#pragma unroll
+      for (int e = 0; e < V; ++e) g[e] = e >= lo && e < hi ? g[e] : 0.0f;
+    }
+    // (gradients with respect to what the sigmoids take; where a is 1 to the last bit, with sig(r) under 2^-100 / decay,
+    // what 1 / q meets is zero)
+#pragma unroll
+    for (int e = 0; e < V; ++e) {
+      const float gs = g[e] * sgi[e], x = slot<IO, REV>(xq, e);
+      const float dla = __builtin_fmaf(g[e] * a[e], hb[e], -gs * x * (a[e] * a[e] * iq[e]));
+      const float dls = -dla * sig[e];
+      sd += dls;
+      hb[e] = dls * decay * (1.0f - sig[e]);
+      sr += hb[e];
+      o[e] = gs * q[e];
+      g[e] = o[e] * x * (1.0f - sgi[e]);
+      si += g[e];
+    }
+    store_slots<IO, REV>(p.dx, at, lo, hi, edge, o);
+    store_slots<IO, REV>(p.dr, at, lo, hi, edge, hb);
+    store_slots<IO, REV>(p.di, at, lo, hi, edge, g);
   }
   if (MAPS) {
     if (lane == 0 && w == 0) {
@@ -228,25 +245,32 @@ __global__ __launch_bounds__(256) void recur_join_kernel(RecurParams p) {
 
 namespace {
 
-template <typename IO, bool REV>
+template <typename IO, bool REV, bool Z>
 void go(const RecurParams& p, hipStream_t s) {
   const int64_t rows = p.B * p.D;
   if (p.plan.lanes == 16) {
-    hipLaunchKernelGGL((recur_bwd_kernel<IO, 16, 1, REV, false>), grid_of((rows + 15) / 16), dim3(256), 0, s, p);
+    hipLaunchKernelGGL((recur_bwd_kernel<IO, 16, 1, REV, Z, false>), grid_of((rows + 15) / 16), dim3(256), 0, s, p);
   } else if (p.plan.waves == 1) {
-    hipLaunchKernelGGL((recur_bwd_kernel<IO, 64, 1, REV, false>), grid_of((rows + 3) / 4), dim3(256), 0, s, p);
+    hipLaunchKernelGGL((recur_bwd_kernel<IO, 64, 1, REV, Z, false>), grid_of((rows + 3) / 4), dim3(256), 0, s, p);
+  } else if (p.plan.waves == 8) {
+    hipLaunchKernelGGL((recur_bwd_kernel<IO, 64, 8, REV, Z, false>), grid_of(rows), dim3(512), 0, s, p);
   } else {
     if (p.plan.S > 1)
-      hipLaunchKernelGGL((recur_bwd_kernel<IO, 64, 4, REV, true>), grid_of(rows * (p.plan.S - 1)), dim3(256), 0, s, p);
-    hipLaunchKernelGGL((recur_bwd_kernel<IO, 64, 4, REV, false>), grid_of(rows * p.plan.S), dim3(256), 0, s, p);
+      hipLaunchKernelGGL((recur_bwd_kernel<IO, 64, 4, REV, Z, true>), grid_of(rows * (p.plan.S - 1)), dim3(256), 0, s, p);
+    hipLaunchKernelGGL((recur_bwd_kernel<IO, 64, 4, REV, Z, false>), grid_of(rows * p.plan.S), dim3(256), 0, s, p);
   }
+}
+
+template <typename IO>
+void any(const RecurParams& p, bool reverse, hipStream_t s) {
+  if (reverse) p.z ? go<IO, true, true>(p, s) : go<IO, true, false>(p, s);
+  else p.z ? go<IO, false, true>(p, s) : go<IO, false, false>(p, s);
 }
 
 }  // namespace
 
 hipError_t launch_recur_bwd(const RecurParams& p, bool bf16, bool reverse, hipStream_t s) {
-  if (bf16) reverse ? go<bf16_t, true>(p, s) : go<bf16_t, false>(p, s);
-  else reverse ? go<float, true>(p, s) : go<float, false>(p, s);
+  bf16 ? any<bf16_t>(p, reverse, s) : any<float>(p, reverse, s);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   hipLaunchKernelGGL(recur_join_kernel, grid_of((3 * p.D + 63) / 64), dim3(256), 0, s, p);

@@ -99,17 +99,20 @@ struct Row {
   }
   // element number of the piece that begins at slot s (a multiple of V)
   __device__ __forceinline__ int64_t at(int64_t s) const { return REV ? origin - s - V : origin + s; }
+  // whether slots s .. s + n - 1 are not all steps
+  __device__ __forceinline__ bool edge(int64_t s, int64_t n) const { return s < m || s + n > slots; }
   // its slots that are steps: lo .. hi - 1
   __device__ __forceinline__ int lo(int64_t s) const { return s >= m ? 0 : (int)(m - s < V ? m - s : V); }
   __device__ __forceinline__ int hi(int64_t s) const { return slots - s >= V ? V : slots > s ? (int)(slots - s) : 0; }
 };
 
-// 16 bytes of which the slots lo .. hi - 1 are read, the others zero
+// 16 bytes of which the slots lo .. hi - 1 are read, the others zero.  edge: there are others in this turn of the team
+// (the same in all its lanes).
 template <typename IO, bool REV>
-__device__ __forceinline__ u32x4a load_slots(const void* p, int64_t at, int lo, int hi) {
+__device__ __forceinline__ u32x4a load_slots(const void* p, int64_t at, int lo, int hi, bool edge) {
   constexpr int V = 16 / (int)sizeof(IO);
   const IO* q = static_cast<const IO*>(p) + at;
-  if (lo == 0 && hi == V) return __builtin_nontemporal_load(reinterpret_cast<const u32x4a*>(q));
+  if (!edge || (lo == 0 && hi == V)) return __builtin_nontemporal_load(reinterpret_cast<const u32x4a*>(q));
   u32x4a w = {0u, 0u, 0u, 0u};
 #pragma unroll
   for (int k = 0; k < V; ++k) {
@@ -131,9 +134,9 @@ __device__ __forceinline__ float slot(const u32x4a& w, int s) {
 }
 
 template <typename IO, bool REV, int V>
-__device__ __forceinline__ void store_slots(void* p, int64_t at, int lo, int hi, const float (&x)[V]) {
+__device__ __forceinline__ void store_slots(void* p, int64_t at, int lo, int hi, bool edge, const float (&x)[V]) {
   IO* q = static_cast<IO*>(p) + at;
-  if (lo == 0 && hi == V) {
+  if (!edge || (lo == 0 && hi == V)) {
     u32x4a w;
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
@@ -158,19 +161,18 @@ __device__ __forceinline__ void store_slots(void* p, int64_t at, int lo, int hi,
 
 __device__ __forceinline__ float sigmoid_(float x) { return rcp_(1.0f + exp2_(-x * kLog2e)); }
 
-// a channel's numbers: -log2(e) of the decay and the biases
+// a channel's numbers: -log2(e) of the decay (NaN for a negative one) and the biases
 struct Channel {
   float nd, rb, ib;
-  __device__ __forceinline__ Channel(const float* decay, const float* r_bias, const float* i_bias, int64_t d) {
-    nd = -kLog2e * decay[d];
-    rb = r_bias ? -kLog2e * r_bias[d] : 0.0f;
-    ib = i_bias ? -kLog2e * i_bias[d] : 0.0f;
-  }
+  __device__ __forceinline__ Channel(float decay, float r_bias, float i_bias)
+      : nd(decay >= 0.0f ? -kLog2e * decay : __builtin_nanf("")), rb(-kLog2e * r_bias), ib(-kLog2e * i_bias) {}
+  __device__ __forceinline__ Channel(const float* decay, const float* r_bias, const float* i_bias, int64_t d)
+      : Channel(decay[d], r_bias ? r_bias[d] : 0.0f, i_bias ? i_bias[d] : 0.0f) {}
 };
 
-// a step's gates; w = 1 - a^2
+// a step's gates; q = sqrt(1 - a^2), iq = 1 / q (of 2^-100 where 1 - a^2 is less)
 struct Gates {
-  float sr, si, a, w;
+  float sr, si, a, q, iq;
   // 1 - a^2 = 1 - e^-t with t = 2 decay sr: up to t = 1/4 from the series to t^6 (the next term is under 5e-8 of it), where
   // a^2 is near 1 and the difference would lose its bits; above it the difference, off by under 6e-7 of itself.
   __device__ __forceinline__ Gates(float r, float i, const Channel& c) {
@@ -184,7 +186,9 @@ struct Gates {
     s = __builtin_fmaf(t, s, 1.0f / 6);
     s = __builtin_fmaf(t, s, -0.5f);
     s = __builtin_fmaf(t, s, 1.0f);
-    w = t < 0.25f ? t * s : __builtin_fmaf(-a, a, 1.0f);
+    const float w = t < 0.25f ? t * s : __builtin_fmaf(-a, a, 1.0f);
+    iq = __builtin_amdgcn_rsqf(fmaxf(w, 7.888609e-31f));
+    q = w * iq;
   }
 };
 

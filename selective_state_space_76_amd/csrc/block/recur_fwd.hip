@@ -40,14 +40,14 @@ __device__ __forceinline__ float enter_up(float& A, float& B, float& carry, floa
 
 }  // namespace
 
-// MAPS: the segments' maps instead of the outputs
-template <typename IO, int LN, int W, bool REV, bool MAPS>
-__global__ __launch_bounds__(256) void recur_fwd_kernel(RecurParams p) {
+// Z: there is a gate.  MAPS: the segments' maps instead of the outputs.
+template <typename IO, int LN, int W, bool REV, bool Z, bool MAPS>
+__global__ __launch_bounds__(W > 4 ? W * 64 : 256) void recur_fwd_kernel(RecurParams p) {
   constexpr int V = 16 / (int)sizeof(IO);
-  constexpr int UNITS = 256 / (LN * W);  // row segments per workgroup
+  constexpr int UNITS = W > 4 ? 1 : 256 / (LN * W);  // row segments per workgroup
   constexpr int TURN = LN * W * V;       // slots
   __shared__ float sm[2][W][2];
-  const int lane = threadIdx.x % LN, w = W > 1 ? threadIdx.x / 64 : 0;
+  const int lane = threadIdx.x % LN, w = W > 1 ? __builtin_amdgcn_readfirstlane(threadIdx.x / 64) : 0;
   const int64_t S = MAPS ? p.plan.S - 1 : p.plan.S;
   const int64_t rows = p.B * p.D;
   int64_t unit = (int64_t)block_id() * UNITS + (W > 1 ? 0 : threadIdx.x / LN);
@@ -78,35 +78,42 @@ __global__ __launch_bounds__(256) void recur_fwd_kernel(RecurParams p) {
     }
   }
 
-  u32x4a xq, rq, iq, zq = {0u, 0u, 0u, 0u}, xn, rn, in, zn = {0u, 0u, 0u, 0u};
+  const u32x4a none = {0u, 0u, 0u, 0u};
+  u32x4a xn = none, rn = none, in = none, zn = none;
+  const bool gate = Z && !MAPS && p.out;
   auto load = [&](int64_t tile) {
     const int64_t s = tile * TURN + (w * LN + lane) * V, at = line.at(s);
     const int lo = line.lo(s), hi = line.hi(s);
-    xn = load_slots<IO, REV>(p.x, at, lo, hi);
-    rn = load_slots<IO, REV>(p.r, at, lo, hi);
-    in = load_slots<IO, REV>(p.i, at, lo, hi);
-    if (!MAPS && p.z && p.out) zn = load_slots<IO, REV>(p.z, at, lo, hi);
+    const bool edge = line.edge(tile * TURN, TURN);
+    xn = load_slots<IO, REV>(p.x, at, lo, hi, edge);
+    rn = load_slots<IO, REV>(p.r, at, lo, hi, edge);
+    in = load_slots<IO, REV>(p.i, at, lo, hi, edge);
+    if (gate) zn = load_slots<IO, REV>(p.z, at, lo, hi, edge);
   };
   if (k0 < k1) load(k0);
   for (int64_t tile = k0; tile < k1; ++tile) {
-    xq = xn;
-    rq = rn;
-    iq = in;
-    zq = zn;
+    const u32x4a xq = xn, rq = rn, iq = in, zq = zn;
     if (tile + 1 < k1) load(tile + 1);
     const int64_t s = tile * TURN + (w * LN + lane) * V;
     const int lo = line.lo(s), hi = line.hi(s);
+    const bool edge = line.edge(tile * TURN, TURN);
     float a[V], v[V];
-    float A = 1.0f, B = 0.0f;
 #pragma unroll
     for (int e = 0; e < V; ++e) {
       const Gates g(slot<IO, REV>(rq, e), slot<IO, REV>(iq, e), ch);
       a[e] = g.a;
-      v[e] = __builtin_amdgcn_sqrtf(g.w) * g.si * slot<IO, REV>(xq, e);
-      if (e < lo || e >= hi) {
-        a[e] = 1.0f;
-        v[e] = 0.0f;
+      v[e] = g.q * g.si * slot<IO, REV>(xq, e);
+    }
+    if (edge) {
+#pragma unroll
+      for (int e = 0; e < V; ++e) {
+        a[e] = e < lo || e >= hi ? 1.0f : a[e];
+        v[e] = e < lo || e >= hi ? 0.0f : v[e];
       }
+    }
+    float A = a[0], B = v[0];
+#pragma unroll
+    for (int e = 1; e < V; ++e) {
       A *= a[e];
       B = __builtin_fmaf(a[e], B, v[e]);
     }
@@ -139,9 +146,9 @@ __global__ __launch_bounds__(256) void recur_fwd_kernel(RecurParams p) {
 #pragma unroll
     for (int e = 0; e < V; ++e) {
       h = __builtin_fmaf(a[e], h, v[e]);
-      o[e] = p.z ? h * silu_(slot<IO, REV>(zq, e)) : h;
+      o[e] = Z ? h * silu_(slot<IO, REV>(zq, e)) : h;
     }
-    store_slots<IO, REV>(p.out, line.at(s), lo, hi, o);
+    store_slots<IO, REV>(p.out, line.at(s), lo, hi, edge, o);
   }
   if (MAPS) {
     if (lane == 0 && w == 0) {
@@ -153,49 +160,68 @@ __global__ __launch_bounds__(256) void recur_fwd_kernel(RecurParams p) {
   }
 }
 
-// One step: the same gates, the state updated in place.  A lane owns V consecutive elements of [B, D].
-template <typename IO>
+// One step: the same gates, the state updated in place.  A lane owns 4 consecutive elements of [B, D].  EVEN: they are of
+// one row, so that the channels' numbers come in one piece each (256 x 5120: 12.9 us with a load for each).
+template <typename IO, bool EVEN>
 __global__ __launch_bounds__(256) void recur_step_kernel(RecurStepParams p) {
-  constexpr int V = 16 / (int)sizeof(IO);
-  const int64_t at = ((int64_t)block_id() * 256 + threadIdx.x) * V;
+  const int64_t at = ((int64_t)block_id() * 256 + threadIdx.x) * 4;
   if (at >= p.n) return;
-  const int n = p.n - at < V ? (int)(p.n - at) : V;
-  float x[V], r[V], i[V], z[V], h[V], o[V];
-  load_n<IO, V>(static_cast<const IO*>(p.x) + at, n, x);
-  load_n<IO, V>(static_cast<const IO*>(p.r) + at, n, r);
-  load_n<IO, V>(static_cast<const IO*>(p.i) + at, n, i);
-  if (p.z) load_n<IO, V>(static_cast<const IO*>(p.z) + at, n, z);
-  load_n<float, V>(p.state + at, n, h);
-  int64_t d = at % p.D;
+  const int n = EVEN || p.n - at >= 4 ? 4 : (int)(p.n - at);
+  float x[4], r[4], i[4], z[4], h[4], o[4], c[3][4];
+  load_n<IO, 4>(static_cast<const IO*>(p.r) + at, n, r);
+  load_n<IO, 4>(static_cast<const IO*>(p.i) + at, n, i);
+  load_n<IO, 4>(static_cast<const IO*>(p.x) + at, n, x);
+  if (p.z) load_n<IO, 4>(static_cast<const IO*>(p.z) + at, n, z);
+  load_n<float, 4>(p.state + at, n, h);
+  int64_t d = p.n <= 0xffffffffll ? (uint32_t)at % (uint32_t)p.D : at % p.D;
+  if (EVEN) {
+    const float* const of[] = {p.decay, p.rb, p.ib};
 #pragma unroll
-  for (int e = 0; e < V; ++e) {
-    const Channel ch(p.decay, p.rb, p.ib, d);
-    const Gates g(r[e], i[e], ch);
-    h[e] = __builtin_fmaf(g.a, h[e], __builtin_amdgcn_sqrtf(g.w) * g.si * x[e]);
-    o[e] = p.z ? h[e] * silu_(z[e]) : h[e];
-    if (++d == p.D) d = 0;
+    for (int k = 0; k < 3; ++k) {
+      if (of[k]) {
+        load_n<float, 4>(of[k] + d, 4, c[k]);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) c[k][e] = 0.0f;
+      }
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      c[0][e] = p.decay[d];
+      c[1][e] = p.rb ? p.rb[d] : 0.0f;
+      c[2][e] = p.ib ? p.ib[d] : 0.0f;
+      if (++d == p.D) d = 0;
+    }
   }
-  store_n<float, V>(p.state + at, n, h);
-  store_n<IO, V>(static_cast<IO*>(p.out) + at, n, o);
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const Gates g(r[e], i[e], Channel(c[0][e], c[1][e], c[2][e]));
+    h[e] = __builtin_fmaf(g.a, h[e], g.q * g.si * x[e]);
+    o[e] = p.z ? h[e] * silu_(z[e]) : h[e];
+  }
+  store_n<float, 4>(p.state + at, n, h);
+  store_n<IO, 4>(static_cast<IO*>(p.out) + at, n, o);
 }
 
-// Short rows (up to two pieces a lane of 16) take 16 lanes each.  Longer ones take a wave; where there are fewer rows
-// than two waves for each of the 1024 SIMDs, four waves, if the row gives each of them a piece; and where that is still
-// too few, segments, up to 64 (a lane each for their maps), of two turns and more.
+// Short rows (up to two pieces a lane of 16) take 16 lanes each, longer ones a wave: a row at a time costs least where
+// there are rows for every SIMD (8 x 1536 x 2048: 57 us, 77 with four waves a row).  Fewer rows take four or eight waves
+// each, if they are long enough for several turns (1 x 2048 x 65536: 264 us, 248 with four, 228 with eight; 2 x 1536 x
+// 8192: 54, 63, 83) or there is no other way to fill the card; and where that is still too few, segments, up to 64
+// (a lane each for their maps), of two turns and more.
 RecurPlan recur_plan(int64_t B, int64_t D, int64_t L, bool bf16) {
   const int64_t V = bf16 ? 8 : 4, rows = B * D;
   RecurPlan pl;
   pl.blocks = (L + V - 1 + 64 * V - 1) / (64 * V);
-  if (L <= 32 * V) {
-    pl.lanes = 16;
-  } else if (rows < 2048 && pl.blocks >= 4) {
-    pl.waves = 4;
-  }
+  if (L <= 32 * V) pl.lanes = 16;
+  else if (rows < 256) pl.waves = pl.blocks >= 4 ? 4 : 1;
+  else if ((rows < 1024 && pl.blocks >= 8) || (rows <= 2048 && pl.blocks >= 64)) pl.waves = 8;
+  else if ((rows < 2048 && pl.blocks >= 4) || (rows < 4096 && pl.blocks >= 32)) pl.waves = 4;
   const int64_t turn = pl.lanes * pl.waves * V;
   pl.tiles = (L + V - 1 + turn - 1) / turn;
   pl.per = pl.tiles;
-  if (pl.waves == 4 && rows < 512) {
-    int64_t S = (511 + rows) / rows;
+  if (pl.waves == 4 && rows < 256) {
+    int64_t S = (1023 + rows) / rows;
     if (S > pl.tiles / 2) S = pl.tiles / 2;
     if (S > 64) S = 64;
     if (S > 1) {
@@ -208,33 +234,44 @@ RecurPlan recur_plan(int64_t B, int64_t D, int64_t L, bool bf16) {
 
 namespace {
 
-template <typename IO, bool REV>
+template <typename IO, bool REV, bool Z>
 void go(const RecurParams& p, hipStream_t s) {
   const int64_t rows = p.B * p.D;
   if (p.plan.lanes == 16) {
-    hipLaunchKernelGGL((recur_fwd_kernel<IO, 16, 1, REV, false>), grid_of((rows + 15) / 16), dim3(256), 0, s, p);
+    hipLaunchKernelGGL((recur_fwd_kernel<IO, 16, 1, REV, Z, false>), grid_of((rows + 15) / 16), dim3(256), 0, s, p);
   } else if (p.plan.waves == 1) {
-    hipLaunchKernelGGL((recur_fwd_kernel<IO, 64, 1, REV, false>), grid_of((rows + 3) / 4), dim3(256), 0, s, p);
+    hipLaunchKernelGGL((recur_fwd_kernel<IO, 64, 1, REV, Z, false>), grid_of((rows + 3) / 4), dim3(256), 0, s, p);
+  } else if (p.plan.waves == 8) {
+    hipLaunchKernelGGL((recur_fwd_kernel<IO, 64, 8, REV, Z, false>), grid_of(rows), dim3(512), 0, s, p);
   } else {
     if (p.plan.S > 1)
-      hipLaunchKernelGGL((recur_fwd_kernel<IO, 64, 4, REV, true>), grid_of(rows * (p.plan.S - 1)), dim3(256), 0, s, p);
-    hipLaunchKernelGGL((recur_fwd_kernel<IO, 64, 4, REV, false>), grid_of(rows * p.plan.S), dim3(256), 0, s, p);
+      hipLaunchKernelGGL((recur_fwd_kernel<IO, 64, 4, REV, false, true>), grid_of(rows * (p.plan.S - 1)), dim3(256), 0, s, p);
+    hipLaunchKernelGGL((recur_fwd_kernel<IO, 64, 4, REV, Z, false>), grid_of(rows * p.plan.S), dim3(256), 0, s, p);
   }
+}
+
+template <typename IO>
+void any(const RecurParams& p, bool reverse, hipStream_t s) {
+  if (reverse) p.z ? go<IO, true, true>(p, s) : go<IO, true, false>(p, s);
+  else p.z ? go<IO, false, true>(p, s) : go<IO, false, false>(p, s);
+}
+
+template <typename IO>
+void step(const RecurStepParams& p, hipStream_t s) {
+  const dim3 grid = grid_of(((p.n + 3) / 4 + 255) / 256);
+  if (p.D % 4) hipLaunchKernelGGL((recur_step_kernel<IO, false>), grid, dim3(256), 0, s, p);
+  else hipLaunchKernelGGL((recur_step_kernel<IO, true>), grid, dim3(256), 0, s, p);
 }
 
 }  // namespace
 
 hipError_t launch_recur_fwd(const RecurParams& p, bool bf16, bool reverse, hipStream_t s) {
-  if (bf16) reverse ? go<bf16_t, true>(p, s) : go<bf16_t, false>(p, s);
-  else reverse ? go<float, true>(p, s) : go<float, false>(p, s);
+  bf16 ? any<bf16_t>(p, reverse, s) : any<float>(p, reverse, s);
   return hipGetLastError();
 }
 
 hipError_t launch_recur_step(const RecurStepParams& p, bool bf16, hipStream_t s) {
-  const int V = bf16 ? 8 : 4;
-  const dim3 grid = grid_of(((p.n + V - 1) / V + 255) / 256);
-  if (bf16) hipLaunchKernelGGL(recur_step_kernel<bf16_t>, grid, dim3(256), 0, s, p);
-  else hipLaunchKernelGGL(recur_step_kernel<float>, grid, dim3(256), 0, s, p);
+  bf16 ? step<bf16_t>(p, s) : step<float>(p, s);
   return hipGetLastError();
 }
 

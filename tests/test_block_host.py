@@ -276,11 +276,13 @@ def test_buffers_belong_to_the_stream_of_the_call(monkeypatch, name):
         return t
 
     monkeypatch.setattr(torch, "empty", allocate)
+    monkeypatch.setattr(torch, "empty_like", lambda t, **k: allocate(t.shape, dtype=t.dtype))
     monkeypatch.setattr(torch.cuda, "stream", on)
     monkeypatch.setattr(torch.cuda, "current_stream", lambda *a: r.current)
     monkeypatch.setattr(torch.Tensor, "record_stream", lambda t, s: r.told.append((s, t.data_ptr())))
     monkeypatch.setattr(K, "load", Library)
     monkeypatch.setattr(K, "_address", lambda t: None)
+    monkeypatch.setattr(K, "_arg", lambda *a: None if a[0] is None else 0)
     monkeypatch.setattr(K, "_capturing", lambda stream: False)
     monkeypatch.setattr(K, "_stream", lambda stream, device: 0)
     side = SimpleNamespace(cuda_stream=7, device="cuda:0")
