@@ -63,7 +63,7 @@ ssm_status norm_check(const ssm_norm_shape* s, NormSizes* z, ssm::NormParams* p)
 bool norm_cols(const ssm_norm_shape* s) { return (s->flags & SSM_FLAG_CHANNELS_FIRST) && s->seqlen > 1; }
 
 int64_t norm_bwd_blocks(const ssm_norm_shape* s, const NormSizes& z) {
-  return norm_cols(s) ? ssm::norm_cols_bwd_blocks(s->batch, s->seqlen)
+  return norm_cols(s) ? ssm::norm_cols_bwd_blocks(s->batch, s->dim, s->seqlen, z.kind, s->flags & SSM_FLAG_RMS)
                       : ssm::norm_rows_bwd_blocks(z.rows, s->dim);
 }
 

@@ -99,7 +99,8 @@ template <typename IO>
 struct Piece {
   static constexpr int Q = (int)sizeof(IO) / 2;  // 16-byte words
   u32x4a w[Q];
-  __device__ __forceinline__ void full(const IO* p, bool may) {
+  // again: it is to be read again (and is left to the caches)
+  __device__ __forceinline__ void full(const IO* p, bool may, bool again = false) {
 #pragma unroll
     for (int k = 0; k < Q; ++k) w[k] = u32x4a{0u, 0u, 0u, 0u};
     if (may) {
@@ -107,7 +108,7 @@ struct Piece {
       for (int k = 0; k < Q; ++k) {
         const auto* a = reinterpret_cast<const typename Unaligned<IO>::type*>(p) + k;
         // (of two words of one line the first must not drop it)
-        const auto q = Q == 1 ? __builtin_nontemporal_load(a) : *a;
+        const auto q = Q == 1 && !again ? __builtin_nontemporal_load(a) : *a;
 #pragma unroll
         for (int i = 0; i < 4; ++i) w[k][i] = q[i];
       }

@@ -60,19 +60,30 @@ inline hipError_t launch_norm_cols_bwd(const NormParams& p, int kind, hipStream_
                                                                  : launch_norm_cols_bwd_f32(p, s);
 }
 int64_t norm_rows_bwd_blocks(int64_t rows, int64_t E);
-// Positions of a tile of the backward pass over [B, E, L], and its workgroups: two for each compute unit, more where there
-// are tiles, each with a partial sum of dw and db.  Wide tiles as in the forward pass, where there are enough of them
-// (2^17 positions x 1024 channels: 246 us with 256 positions, 266 with 128, 304 with 64; 4 x 4096 x 2048: 71 us with
-// 64, 92 with 128).
+// The backward pass over [B, E, L]: a workgroup and a partial sum of dw and db for each tile.
 constexpr int64_t kFewTiles = 128;  // of 64 positions: then they are cut to 16, lines shared through the caches
-inline int norm_cols_bwd_tile(int64_t B, int64_t L) {
-  auto tiles = [&](int64_t T) { return B * ((L + T - 1) / T); };
-  if (L % 8) return tiles(128) >= 256 ? 128 : 64;
-  return tiles(256) >= 512 ? 256 : tiles(128) >= 256 ? 128 : tiles(64) >= kFewTiles ? 64 : 16;
+// Channels up to which a tile of 64 positions keeps dout between its two passes, as far as 128 registers go.
+constexpr int norm_cols_bwd_kept(bool x16, bool h16, bool rms) {
+  return 128 * (!x16 ? (rms ? 8 : 6) : !h16 ? 8 : rms ? 16 : 12);
 }
-inline int64_t norm_cols_bwd_blocks(int64_t B, int64_t L) {
-  const int64_t T = norm_cols_bwd_tile(B, L), tiles = B * ((L + T - 1) / T);
-  return tiles < 1024 ? tiles : 1024;
+struct NormTile {
+  int T;      // positions
+  bool keep;  // dout is kept
+};
+// Kept dout spares a reading, but takes 128 channels at least to fill its lanes (RMS norm, bf16, with the carried
+// gradient; 2^17 positions x 1024 channels: 226 us, read twice 258 in tiles of 64 positions, 262 in tiles of 256; 2^17 x
+// 2048: 420, 556 and 528; 16384 x 2048: 60 and 66; 2^20 x 64: 169, 188 and 115).  Read twice, wide tiles are better
+// where there are enough of them (2^15 x 4096: 262 us with 128 positions, 319 with 64, 361 with 256).
+inline NormTile norm_cols_bwd_tile(int64_t B, int64_t E, int64_t L, int kind, bool rms) {
+  auto tiles = [&](int64_t T) { return B * ((L + T - 1) / T); };
+  if (L % 8) return {tiles(128) >= 256 ? 128 : 64, false};
+  if (tiles(64) < kFewTiles) return {16, false};
+  if (E > 128 && E <= norm_cols_bwd_kept(kind & 1, kind & 2, rms)) return {64, true};
+  return {tiles(256) >= 512 ? 256 : tiles(128) >= 256 ? 128 : 64, false};
+}
+inline int64_t norm_cols_bwd_blocks(int64_t B, int64_t E, int64_t L, int kind, bool rms) {
+  const int T = norm_cols_bwd_tile(B, E, L, kind, rms).T;
+  return B * ((L + T - 1) / T);
 }
 hipError_t launch_norm_rows_bwd(const NormParams& p, int kind, hipStream_t s);
 // dweight and dbias from p.blocks partial sums

@@ -61,10 +61,21 @@ __device__ __forceinline__ void sum_groups(float (&v)[8], float* sm) {
 
 // sum over the LP lanes that hold a channel's positions
 template <int LP> __device__ __forceinline__ float sum_positions(float v) {
-#pragma unroll
-  for (int m = 1; m < LP; m *= 2) v += __shfl_xor(v, m);
+  auto step = [&](auto ctrl) {
+    v += __uint_as_float(
+        (uint32_t)__builtin_amdgcn_mov_dpp((int)__float_as_uint(v), decltype(ctrl)::value, 0xf, 0xf, true));
+  };
+  step(IC<0xb1>{});                             // quad_perm [1,0,3,2]
+  if constexpr (LP >= 4) step(IC<0x4e>{});      // quad_perm [2,3,0,1]
+  if constexpr (LP >= 8) step(IC<0x141>{});     // row_half_mirror
+  if constexpr (LP >= 16) step(IC<0x140>{});    // row_mirror
+  if constexpr (LP >= 32) v += __shfl_xor(v, 16);
   return v;
 }
+
+// The sum is to be taken here: the compiler would put the additions off to where the sum is used, behind all channels, and
+// keep all of their terms until then.
+__device__ __forceinline__ void here(float& v) { asm volatile("" : "+v"(v)); }
 
 // Where rows do not begin with a line, neighbouring tiles write parts of one: put together by the cache.
 template <typename IO>
@@ -127,8 +138,8 @@ __global__ __launch_bounds__(NT) void norm_cols_kernel(NormParams p) {
   auto fetch = [&](Ch& k, int e0, bool side) {  // (positions behind the last one: whatever is there)
     channels(e0, [&](int c, int e, int64_t at) {
       const bool may = e < E && n > 0 && (!ODD || at + 8 <= total);
-      k.x[c].full(static_cast<const XT*>(p.x) + at, may);
-      if (RES) k.q[RES ? c : 0].full(static_cast<const HT*>(p.residual) + at, may);
+      k.x[c].full(static_cast<const XT*>(p.x) + at, may, !KEEP && !side);
+      if (RES) k.q[RES ? c : 0].full(static_cast<const HT*>(p.residual) + at, may, !KEEP && !side);
     });
     if (side) {
 #pragma unroll
@@ -201,7 +212,10 @@ __global__ __launch_bounds__(NT) void norm_cols_kernel(NormParams p) {
           float s[8];
           sum(k, c, s);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) m[i] += s[i];  // (zero for a channel that is not there)
+          for (int i = 0; i < 8; ++i) {
+            m[i] += s[i];  // (zero for a channel that is not there)
+            here(m[i]);
+          }
         }
       });
       sum_groups<NT, LP>(m, sm);
@@ -218,6 +232,7 @@ __global__ __launch_bounds__(NT) void norm_cols_kernel(NormParams p) {
           for (int i = 0; i < 8; ++i) {
             const float d = s[i] - m[i];
             r[i] = __builtin_fmaf(d, d, r[i]);
+            here(r[i]);
           }
         }
       }
@@ -282,120 +297,226 @@ __global__ __launch_bounds__(NT) void norm_cols_kernel(NormParams p) {
   }
 }
 
-// Tiles in turn, everything read twice.  The lanes that own a channel add every tile's dw and db to the workgroup's
-// partial sums, which no other lane touches.
+// A tile each, everything read twice.  The tile's dw and db are a partial sum of its own.
 template <typename XT, typename HT, bool ODD, int NT, int LP, int C>
 __global__ __launch_bounds__(NT) void norm_cols_bwd_kernel(NormParams p) {
   constexpr int NG = NT / LP, T = LP * 8;
   __shared__ float sm[(NT / 64 + 1) * T];
   const int pl = threadIdx.x % LP, cg = threadIdx.x / LP, E = (int)p.E;
-  const int64_t tiles = (p.L + T - 1) / T, total = p.rows * p.E, step = NG * p.L;
+  const int64_t tiles = (p.L + T - 1) / T, total = p.rows * p.E, step = NG * p.L, tile = block_id();
+  if (tile >= p.blocks) return;
   const bool lines = !ODD && p.L % 64 == 0;
   const Drop drop(p.drop);
-  float* part = p.part ? p.part + (int64_t)block_id() * 2 * p.E : nullptr;
+  float* part = p.part ? p.part + tile * 2 * p.E : nullptr;
   struct Ch {
     Piece<XT> d[C];
     Piece<HT> h[C], q[C];
     float w[C];
   };
-  bool first = true;
-  for (int64_t tile = block_id(); tile < p.B * tiles; tile += p.blocks) {
-    const int64_t b = tile / tiles, t = tile % tiles * T + pl * 8;
-    const int n = p.L - t >= 8 ? 8 : !ODD || p.L <= t ? 0 : (int)(p.L - t);
-    const int64_t base = b * p.E * p.L + t;
-    Part real;
-    real.hi = n;
-    auto channels = [&](int e0, auto f) {
-      int e = e0 + cg;
-      asm volatile("" : "+v"(e));
-      int64_t at = base + e * p.L;
+  const int64_t b = tile / tiles, t = tile % tiles * T + pl * 8;
+  const int n = p.L - t >= 8 ? 8 : !ODD || p.L <= t ? 0 : (int)(p.L - t);
+  const int64_t base = b * p.E * p.L + t;
+  Part real;
+  real.hi = n;
+  auto channels = [&](int e0, auto f) {
+    int e = e0 + cg;
+    asm volatile("" : "+v"(e));
+    int64_t at = base + e * p.L;
 #pragma unroll
-      for (int c = 0; c < C; ++c, e += NG, at += step) f(c, e, at);
-    };
-    auto fetch = [&](Ch& k, int e0, bool third) {
-      channels(e0, [&](int c, int e, int64_t at) {
-        const bool may = e < E && n > 0 && (!ODD || at + 8 <= total);
-        k.d[c].full(static_cast<const XT*>(p.x) + at, may);
-        k.h[c].full(static_cast<const HT*>(p.residual) + at, may);
-        if (third && p.dhidden) k.q[c].full(static_cast<const HT*>(p.dhidden) + at, may);
-        k.w[c] = p.weight ? p.weight[e < E ? e : 0] : 1.0f;
-      });
-      if (ODD)
-        channels(e0, [&](int c, int e, int64_t at) {
-          if (e < E && n > 0 && at + 8 > total) {
-            k.d[c].part(static_cast<const XT*>(p.x) + at, real);
-            k.h[c].part(static_cast<const HT*>(p.residual) + at, real);
-            if (third && p.dhidden) k.q[c].part(static_cast<const HT*>(p.dhidden) + at, real);
-          }
-          k.d[c].cut(real);  // (what lies behind the last position takes no part in dw and db)
-          k.h[c].cut(real);
-        });
-    };
-    float m[8], r[8], c1[8], c2[8];
-    load_n<float, 8>(p.stats + b * p.L + t, n, m);
-    load_n<float, 8>(p.stats + p.rows + b * p.L + t, n, r);
-#pragma unroll
-    for (int k = 0; k < 8; ++k) c1[k] = c2[k] = 0.0f;
-    auto pass = [&](bool third, auto f) {
-      Ch next;
-      fetch(next, 0, third);
-      for (int e0 = 0; e0 < E; e0 += C * NG) {
-        const Ch now = next;
-        if (e0 + C * NG < E) fetch(next, e0 + C * NG, third);
-        f(now, e0);
-      }
-    };
-    pass(false, [&](const Ch& k, int e0) {
-      channels(e0, [&](int c, int e, int64_t) {
-        float dw = 0.0f, db = 0.0f;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {  // (d is 0 for a channel that is not there, r behind the last position)
-          const float g = k.d[c].at(i), x = (k.h[c].at(i) - m[i]) * r[i];
-          dw = __builtin_fmaf(g, x, dw);
-          db += g;
-          c1[i] = __builtin_fmaf(g, k.w[c], c1[i]);
-          c2[i] = __builtin_fmaf(g * k.w[c], x, c2[i]);
-        }
-        if (part) {
-          dw = sum_positions<LP>(dw);
-          db = sum_positions<LP>(db);
-          if (pl == 0 && e < E) {
-            part[e] = first ? dw : part[e] + dw;
-            part[E + e] = first ? db : part[E + e] + db;
-          }
-        }
-        __builtin_amdgcn_sched_barrier(0);
-      });
+    for (int c = 0; c < C; ++c, e += NG, at += step) f(c, e, at);
+  };
+  auto fetch = [&](Ch& k, int e0, bool third) {
+    channels(e0, [&](int c, int e, int64_t at) {
+      const bool may = e < E && n > 0 && (!ODD || at + 8 <= total), again = LP < 32 && !third;
+      k.d[c].full(static_cast<const XT*>(p.x) + at, may, again);
+      k.h[c].full(static_cast<const HT*>(p.residual) + at, may, again);
+      if (third && p.dhidden) k.q[c].full(static_cast<const HT*>(p.dhidden) + at, may);
+      k.w[c] = p.weight ? p.weight[e < E ? e : 0] : 1.0f;
     });
-    if (!p.rms) sum_groups<NT, LP>(c1, sm);
-    sum_groups<NT, LP>(c2, sm);
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      c1[k] = p.rms ? 0.0f : c1[k] * p.inv_e;
-      c2[k] *= p.inv_e;
+    if (ODD)
+      channels(e0, [&](int c, int e, int64_t at) {
+        if (e < E && n > 0 && at + 8 > total) {
+          k.d[c].part(static_cast<const XT*>(p.x) + at, real);
+          k.h[c].part(static_cast<const HT*>(p.residual) + at, real);
+          if (third && p.dhidden) k.q[c].part(static_cast<const HT*>(p.dhidden) + at, real);
+        }
+        k.d[c].cut(real);  // (what lies behind the last position takes no part in dw and db)
+        k.h[c].cut(real);
+      });
+  };
+  // f(channels, e0) for all channels
+  auto pass = [&](bool third, auto f) {
+    Ch next;
+    fetch(next, 0, third);
+    for (int e0 = 0; e0 < E; e0 += C * NG) {
+      const Ch now = next;
+      if (e0 + C * NG < E) fetch(next, e0 + C * NG, third);
+      f(now, e0);
     }
-    pass(true, [&](const Ch& k, int e0) {
-      channels(e0, [&](int c, int e, int64_t at) {
-        if (e >= E) return;
-        float g[8];
+  };
+  float m[8], r[8], c1[8], c2[8];
+  load_n<float, 8>(p.stats + b * p.L + t, n, m);
+  load_n<float, 8>(p.stats + p.rows + b * p.L + t, n, r);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float x = (k.h[c].at(i) - m[i]) * r[i];
-          g[i] = r[i] * (k.d[c].at(i) * k.w[c] - c1[i] - x * c2[i]);
-        }
-        if (p.dhidden) {
+  for (int k = 0; k < 8; ++k) c1[k] = c2[k] = 0.0f;
+  pass(false, [&](const Ch& k, int e0) {
+    channels(e0, [&](int c, int e, int64_t) {
+      float dw = 0.0f, db = 0.0f;
 #pragma unroll
-          for (int i = 0; i < 8; ++i) g[i] += k.q[c].at(i);
+      for (int i = 0; i < 8; ++i) {  // (d is 0 for a channel that is not there, r behind the last position)
+        const float g = k.d[c].at(i), x = (k.h[c].at(i) - m[i]) * r[i];
+        dw = __builtin_fmaf(g, x, dw);
+        db += g;
+        c1[i] = __builtin_fmaf(g, k.w[c], c1[i]);
+        c2[i] = __builtin_fmaf(g * k.w[c], x, c2[i]);
+      }
+      if (part) {
+        dw = sum_positions<LP>(dw);
+        db = sum_positions<LP>(db);
+        if (pl == 0 && e < E) {
+          part[e] = dw;
+          part[E + e] = db;
         }
-        if (p.hidden) store_cols(static_cast<HT*>(p.hidden) + at, n, g, lines);
-        if (p.out) {
-          if (drop.any()) drop.apply(drop.kept((uint64_t)at), g);
-          store_cols(static_cast<XT*>(p.out) + at, n, g, lines);
-        }
-        __builtin_amdgcn_sched_barrier(0);
-      });
+      }
+      __builtin_amdgcn_sched_barrier(0);
     });
-    first = false;
+  });
+  if (!p.rms) sum_groups<NT, LP>(c1, sm);
+  sum_groups<NT, LP>(c2, sm);
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    c1[k] = p.rms ? 0.0f : c1[k] * p.inv_e;
+    c2[k] *= p.inv_e;
+  }
+  pass(true, [&](const Ch& k, int e0) {
+    channels(e0, [&](int c, int e, int64_t at) {
+      if (e >= E) return;
+      float g[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float x = (k.h[c].at(i) - m[i]) * r[i];
+        g[i] = r[i] * (k.d[c].at(i) * k.w[c] - c1[i] - x * c2[i]);
+      }
+      if (p.dhidden) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) g[i] += k.q[c].at(i);
+      }
+      if (p.hidden) store_cols(static_cast<HT*>(p.hidden) + at, n, g, lines);
+      if (p.out) {
+        if (drop.any()) drop.apply(drop.kept((uint64_t)at), g);
+        store_cols(static_cast<XT*>(p.out) + at, n, g, lines);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    });
+  });
+}
+
+// The same for tiles of 64 positions by 1024 lanes that keep dout of C channels each, all there are; hidden is read again
+// (parts of it kept in LDS gained nothing).  RMS is the template's for its registers: C = 16 fits them, and not with m
+// and c1 beside them.
+template <typename XT, typename HT, bool RMS, int C>
+__global__ __launch_bounds__(1024) void norm_cols_bwd_keep_kernel(NormParams p) {
+  constexpr int NT = 1024, LP = 8, NG = NT / LP, T = LP * 8;
+  __shared__ float sm[(NT / 64 + 1) * T];
+  const int pl = threadIdx.x % LP, cg = threadIdx.x / LP, E = (int)p.E;
+  const int64_t tiles = (p.L + T - 1) / T, step = NG * p.L, tile = block_id();
+  if (tile >= p.blocks) return;
+  const bool lines = p.L % 64 == 0;
+  const Drop drop(p.drop);
+  float* part = p.part ? p.part + tile * 2 * p.E : nullptr;
+  const int64_t b = tile / tiles, t = tile % tiles * T + pl * 8;
+  const bool in = t < p.L;
+  const int64_t base = b * p.E * p.L + t;
+  Piece<XT> d[C];
+  Piece<HT> h[2];
+  float w[2];
+  int e0 = cg;
+  asm volatile("" : "+v"(e0));
+  int64_t at0 = base + e0 * p.L;
+  auto side = [&](int e) { return p.weight ? p.weight[e < E ? e : 0] : 1.0f; };
+  auto hidden = [&](int c, bool again) {
+    h[c & 1].full(static_cast<const HT*>(p.residual) + at0 + c * step, in && e0 + c * NG < E, again);
+  };
+#pragma unroll
+  for (int c = 0; c < C; ++c) d[c].full(static_cast<const XT*>(p.x) + at0 + c * step, in && e0 + c * NG < E);
+  hidden(0, true);
+  w[0] = side(e0);
+  float m[8], r[8], c1[8], c2[8];
+  if (!RMS) load_n<float, 8>(p.stats + b * p.L + t, in ? 8 : 0, m);
+  load_n<float, 8>(p.stats + p.rows + b * p.L + t, in ? 8 : 0, r);
+#pragma unroll
+  for (int k = 0; k < 8; ++k) c1[k] = c2[k] = 0.0f;
+#pragma unroll
+  for (int c = 0; c < C; ++c) {
+    if (c + 1 < C) {
+      hidden(c + 1, true);
+      w[(c + 1) & 1] = side(e0 + (c + 1) * NG);
+    }
+    const Piece<HT>& now = h[c & 1];
+    float dw = 0.0f, db = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float g = d[c].at(i), x = (RMS ? now.at(i) : now.at(i) - m[i]) * r[i], gw = g * w[c & 1];
+      dw = __builtin_fmaf(g, x, dw);
+      db += g;
+      if (!RMS) c1[i] += gw;
+      c2[i] = __builtin_fmaf(gw, x, c2[i]);
+      if (!RMS) here(c1[i]);
+      here(c2[i]);
+    }
+    if (part) {
+      dw = sum_positions<LP>(dw);
+      db = sum_positions<LP>(db);
+      const int e = e0 + c * NG;
+      if (pl == 0 && e < E) {
+        part[e] = dw;
+        part[E + e] = db;
+      }
+    }
+    __builtin_amdgcn_sched_barrier(0);
+  }
+#pragma unroll
+  for (int c = 0; c < C; ++c) d[c].forget();
+  // the second pass asks for its first pieces before the sums
+  Piece<HT> q[2];
+  e0 = cg;
+  asm volatile("" : "+v"(e0));
+  at0 = base + e0 * p.L;
+  auto second = [&](int c) {
+    const bool may = in && e0 + c * NG < E;
+    if (p.dhidden) q[c & 1].full(static_cast<const HT*>(p.dhidden) + at0 + c * step, may);
+    hidden(c, false);
+    w[c & 1] = side(e0 + c * NG);
+  };
+  second(0);
+  if (!RMS) sum_groups<NT, LP>(c1, sm);
+  sum_groups<NT, LP>(c2, sm);
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    c1[k] *= p.inv_e;
+    c2[k] *= p.inv_e * r[k];
+  }
+#pragma unroll
+  for (int c = 0; c < C; ++c) {
+    if (c + 1 < C) second(c + 1);
+    const int e = e0 + c * NG;
+    const Piece<HT>& now = h[c & 1];
+    float g[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      g[i] = d[c].at(i) * w[c & 1] - (RMS ? now.at(i) : now.at(i) - m[i]) * c2[i];
+      g[i] = r[i] * (RMS ? g[i] : g[i] - c1[i]);
+      if (p.dhidden) g[i] += q[c & 1].at(i);
+    }
+    const int64_t at = at0 + c * step;
+    if (in && e < E) {
+      if (p.hidden) store_cols(static_cast<HT*>(p.hidden) + at, 8, g, lines);
+      if (p.out) {
+        if (drop.any()) drop.apply(drop.kept((uint64_t)at), g);
+        store_cols(static_cast<XT*>(p.out) + at, 8, g, lines);
+      }
+    }
+    __builtin_amdgcn_sched_barrier(0);
   }
 }
 
@@ -447,14 +568,28 @@ void go_bwd(const NormParams& p, hipStream_t s) {
   hipLaunchKernelGGL((norm_cols_bwd_kernel<XT, HT, ODD, NT, LP, C>), grid_of(p.blocks), dim3(NT), 0, s, p);
 }
 
+template <typename XT, typename HT, bool RMS>
+void keep_bwd(const NormParams& p, hipStream_t s) {
+  constexpr int most = norm_cols_bwd_kept(sizeof(XT) == 2, sizeof(HT) == 2, RMS) / 128;
+  auto go = [&](auto c) {
+    if constexpr (decltype(c)::value <= most)
+      hipLaunchKernelGGL((norm_cols_bwd_keep_kernel<XT, HT, RMS, decltype(c)::value>), grid_of(p.blocks), dim3(1024), 0,
+                         s, p);
+  };
+  const int64_t c = (p.E + 127) / 128;
+  c <= 2 ? go(IC<2>()) : c <= 4 ? go(IC<4>()) : c <= 8 && c <= most ? go(IC<(most < 8 ? most : 8)>()) : go(IC<most>());
+}
+
 template <typename XT, typename HT>
 void bwd(const NormParams& p, hipStream_t s) {
-  const int T = norm_cols_bwd_tile(p.B, p.L);
-  if (p.L % 8) return T > 64 ? go_bwd<XT, HT, true, 512, 16, 2>(p, s) : go_bwd<XT, HT, true, 1024, 8, 1>(p, s);
-  if (T == 256) return go_bwd<XT, HT, false, 512, 32, 2>(p, s);
-  if (T == 128) return go_bwd<XT, HT, false, 512, 16, 2>(p, s);
-  if (T == 16) return go_bwd<XT, HT, false, 1024, 2, 2>(p, s);
-  go_bwd<XT, HT, false, 1024, 8, 1>(p, s);
+  const int kind = (sizeof(XT) == 2 ? 1 : 0) + (sizeof(HT) == 2 ? 2 : 0);
+  const NormTile tile = norm_cols_bwd_tile(p.B, p.E, p.L, kind, p.rms);
+  if (tile.keep) return p.rms ? keep_bwd<XT, HT, true>(p, s) : keep_bwd<XT, HT, false>(p, s);
+  if (p.L % 8) return tile.T > 64 ? go_bwd<XT, HT, true, 512, 16, 2>(p, s) : go_bwd<XT, HT, true, 512, 8, 2>(p, s);
+  if (tile.T == 256) return go_bwd<XT, HT, false, 512, 32, 2>(p, s);
+  if (tile.T == 128) return go_bwd<XT, HT, false, 512, 16, 2>(p, s);
+  if (tile.T == 16) return go_bwd<XT, HT, false, 1024, 2, 2>(p, s);
+  go_bwd<XT, HT, false, 512, 8, 2>(p, s);
 }
 
 }  // namespace

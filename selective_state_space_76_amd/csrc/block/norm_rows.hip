@@ -422,38 +422,46 @@ __global__ __launch_bounds__(256) void norm_sums_kernel(NormParams p) {
   p.part[first * 2 * p.E + p.E + e] = db;
 }
 
-// dw and db from the partial sums: 64 columns per workgroup, the partial sums split over 16 waves, each in order,
-// then the waves' sums in order.
-__global__ __launch_bounds__(1024) void norm_join_kernel(NormParams p) {
-  __shared__ float sm[1024];
-  const int64_t cols = (p.E + 63) / 64;
+// dw and db from the partial sums: 16 columns per workgroup, the partial sums split over 64 groups of lanes, each in
+// order, then the groups' sums in order (1366 sums of 768 columns: 7.2 us with 64 columns and 16 groups).  Every `step`th
+// of them, `many` to a workgroup, which leaves their sum in the place of the first; the last call's single one writes dw
+// and db.
+__global__ __launch_bounds__(1024) void norm_join_kernel(NormParams p, int64_t step, int64_t many) {
+  __shared__ float sm[1024], sn[256];
+  const int64_t cols = (p.E + 15) / 16, n = (p.blocks + step - 1) / step;
   const int64_t blk = block_id();
-  const int64_t which = blk / cols;
-  if (which > 1) return;
-  const int64_t c = blk % cols * 64 + (threadIdx.x & 63);
-  const int64_t per = (p.blocks + 15) / 16;
-  const int64_t k0 = (threadIdx.x >> 6) * per, k1 = k0 + per < p.blocks ? k0 + per : p.blocks;
-  const float* q = p.part + which * p.E + c;
+  const int64_t which = blk / cols % 2, first = blk / (2 * cols) * many;
+  if (first >= n) return;
+  const int64_t here = n - first < many ? n - first : many;
+  const int64_t c = blk % cols * 16 + (threadIdx.x & 15);
+  const int64_t per = (here + 63) / 64, row = step * 2 * p.E;
+  const int64_t k0 = (threadIdx.x >> 4) * per, k1 = k0 + per < here ? k0 + per : here;
+  float* q = p.part + first * row + which * p.E + c;
   float s = 0.0f;
   if (c < p.E) {
     int64_t k = k0;
     for (; k + 8 <= k1; k += 8) {
       float v[8];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] = q[(k + e) * 2 * p.E];
+      for (int e = 0; e < 8; ++e) v[e] = q[(k + e) * row];
 #pragma unroll
       for (int e = 0; e < 8; ++e) s += v[e];
     }
-    for (; k < k1; ++k) s += q[k * 2 * p.E];
+    for (; k < k1; ++k) s += q[k * row];
   }
   sm[threadIdx.x] = s;
   __syncthreads();
-  float* out = which ? p.dbias : p.dweight;
-  if (threadIdx.x < 64 && c < p.E && out) {
+  if (threadIdx.x < 256) {
+    const int at = (threadIdx.x >> 4) * 64 + (threadIdx.x & 15);
+    sn[threadIdx.x] = (sm[at] + sm[at + 16]) + (sm[at + 32] + sm[at + 48]);
+  }
+  __syncthreads();
+  float* out = many < n ? q : which ? p.dbias : p.dweight;
+  if (threadIdx.x < 16 && c < p.E && out) {
     s = 0.0f;
 #pragma unroll
-    for (int t = 0; t < 16; ++t) s += sm[t * 64 + threadIdx.x];
-    out[c] = s;
+    for (int t = 0; t < 16; ++t) s += sn[t * 16 + threadIdx.x];
+    out[many < n ? 0 : c] = s;
   }
 }
 
@@ -537,7 +545,13 @@ hipError_t launch_norm_rows_bwd(const NormParams& p, int kind, hipStream_t s) {
 }
 
 hipError_t launch_norm_join(const NormParams& p, hipStream_t s) {
-  hipLaunchKernelGGL(norm_join_kernel, grid_of((p.E + 63) / 64 * 2), dim3(1024), 0, s, p);
+  // in one go while a lane's share is short
+  for (int64_t n = p.blocks, step = 1, many; n; step *= many) {
+    many = n <= 4096 ? n : 512;
+    const int64_t groups = (n + many - 1) / many;
+    hipLaunchKernelGGL(norm_join_kernel, grid_of((p.E + 15) / 16 * 2 * groups), dim3(1024), 0, s, p, step, many);
+    n = groups > 1 ? groups : 0;
+  }
   return hipGetLastError();
 }
 

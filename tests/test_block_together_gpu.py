@@ -255,6 +255,50 @@ def test_norm_over_channels_of_long_sequences(xt, ht, B, E, L):
             assert bool(((got["dbias"].double() - d.double().sum((0, 2))).abs() <= lim).all())
 
 
+# on either side of the channels that the gradients' tiles of 64 positions keep, ends inside a tile; partial sums of more
+# tiles than are joined in one go
+KEPT = [(1, 130, 8192), (2, 256, 4104), (1, 257, 8200), (1, 520, 8192), (1, 769, 8192), (3, 1024, 2752), (1, 1100, 8192),
+        (1, 1536, 8200), (1, 1537, 8192), (1, 2048, 8192), (1, 2049, 8192), (1, 8, (1 << 21) + 8)]
+
+
+@pytest.mark.parametrize("rms", [False, True], ids=["layer", "rms"])
+@pytest.mark.parametrize("xt,ht", [(F32, F32), (BF16, BF16), (BF16, F32)], ids=["f32", "bf16", "bf16-f32"])
+@pytest.mark.parametrize("B,E,L", KEPT)
+def test_norm_gradients_over_channels(xt, ht, rms, B, E, L):
+    """Against 64-bit torch on the GPU; bounds as in the test above, dropout adds the rounding of a product."""
+    print("case: norm gradients over channels", xt, ht, rms, B, E, L, flush=True)
+    g = torch.Generator(device=DEV).manual_seed(E + L)
+    d, h, dh = randn(g, B, E, L, dtype=xt), randn(g, B, E, L, dtype=ht), randn(g, B, E, L, dtype=ht)
+    w = 1 + 0.1 * randn(g, E)
+    _, m, f = norm64(h.double(), w.double(), None, rms, 1)
+    stats = torch.stack([m.reshape(-1), f.reshape(-1)]).float()
+    st = stats.double().view(2, B, 1, L)
+    xh = (h.double() - st[0]) * st[1]
+    gw = d.double() * w.double().view(-1, 1)
+    ds = gw - xh * (gw * xh).mean(1, keepdim=True)
+    ds = st[1] * (ds if rms else ds - gw.mean(1, keepdim=True))
+
+    def near(got, ref):
+        eps = 0.0 if got.dtype == F32 else torch.finfo(BF16).eps / 2
+        return bool(((got.double() - ref).abs() <= 1e-5 * ref.abs().max() + eps * (1 + 2 ** -6) * ref.abs()).all())
+
+    kw = dict(rms=rms, channels_first=True)
+    if xt == ht:
+        got = ssm.layer_norm_bwd(d, h, w, stats, residual=False, bias=True, **kw)
+        assert near(got["dx"], ds)
+    p = 0.2
+    more = ssm.layer_norm_bwd(d, h, w, stats, dhidden=dh, p=p, seed=9, call=2, residual=True, bias=True, **kw)
+    ds = ds + dh.double()
+    mask = ssm.dropout_fwd(torch.ones(B, E, L, device=DEV), p, seed=9, call=2)
+    assert near(more["dresidual"], ds) and near(more["dx"], ds * mask.double())
+    lim = 1300 * R.U * (d.double() * xh).abs().sum((0, 2)) + 1e-30
+    assert bool(((more["dweight"].double() - (d.double() * xh).sum((0, 2))).abs() <= lim).all())
+    lim = 1300 * R.U * d.double().abs().sum((0, 2))
+    assert bool(((more["dbias"].double() - d.double().sum((0, 2))).abs() <= lim).all())
+    if xt == ht:
+        assert torch.equal(got["dweight"], more["dweight"]) and torch.equal(got["dbias"], more["dbias"])
+
+
 @pytest.mark.parametrize("dtype,tol", [(F32, 1e-4), (BF16, 2e-2)], ids=["f32", "bf16"])
 @pytest.mark.parametrize("B,D,L", [(1, 300, 9000), (2, 1000, 33000), (1, 3000, 20000), (8, 600, 2048)])
 @pytest.mark.parametrize("reverse", [False, True], ids=["forward", "reverse"])
