@@ -166,9 +166,9 @@ def layer_norm_fwd(x, weight=None, bias=None, residual=None, *, eps=1e-5, rms=Fa
     return out, hidden, stats
 
 
-def layer_norm_bwd_workspace_size(dout, *, hidden_dtype=None, channels_first=False) -> int:
+def layer_norm_bwd_workspace_size(dout, *, hidden_dtype=None, rms=False, channels_first=False) -> int:
     """Workspace bytes of layer_norm_bwd."""
-    sh, _, _ = _norm_shape(dout.shape, dout.dtype, hidden_dtype or dout.dtype, False, channels_first)
+    sh, _, _ = _norm_shape(dout.shape, dout.dtype, hidden_dtype or dout.dtype, rms, channels_first)
     return int(load().ssm_layer_norm_bwd_workspace_size(sh))
 
 

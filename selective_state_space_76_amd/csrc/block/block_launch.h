@@ -70,15 +70,15 @@ struct NormTile {
   int T;      // positions
   bool keep;  // dout is kept
 };
-// Kept dout spares a reading, but takes 128 channels at least to fill its lanes (RMS norm, bf16, with the carried
-// gradient; 2^17 positions x 1024 channels: 226 us, read twice 258 in tiles of 64 positions, 262 in tiles of 256; 2^17 x
-// 2048: 420, 556 and 528; 16384 x 2048: 60 and 66; 2^20 x 64: 169, 188 and 115).  Read twice, wide tiles are better
-// where there are enough of them (2^15 x 4096: 262 us with 128 positions, 319 with 64, 361 with 256).
+// Kept dout spares a reading, but takes 128 channels to fill its lanes (RMS norm in bf16 with the stream's own gradient;
+// 2^17 positions x 1024 channels: 263 us, read twice 312 in tiles of 64 positions, 323 in tiles of 256; 2^17 x 2048:
+// 562, 712 and 643; 16384 x 2048: 67 and 78; 2^19 x 128: 114, 145 and 129; 2^20 x 64: 173, 220 and 138).  Read twice, wide
+// tiles are better where there are enough of them (2^15 x 4096: 317 us with 128 positions, 375 with 64, 404 with 256).
 inline NormTile norm_cols_bwd_tile(int64_t B, int64_t E, int64_t L, int kind, bool rms) {
   auto tiles = [&](int64_t T) { return B * ((L + T - 1) / T); };
   if (L % 8) return {tiles(128) >= 256 ? 128 : 64, false};
   if (tiles(64) < kFewTiles) return {16, false};
-  if (E > 128 && E <= norm_cols_bwd_kept(kind & 1, kind & 2, rms)) return {64, true};
+  if (E >= 128 && E <= norm_cols_bwd_kept(kind & 1, kind & 2, rms)) return {64, true};
   return {tiles(256) >= 512 ? 256 : tiles(128) >= 256 ? 128 : 64, false};
 }
 inline int64_t norm_cols_bwd_blocks(int64_t B, int64_t E, int64_t L, int kind, bool rms) {

@@ -411,13 +411,16 @@ __global__ __launch_bounds__(NT) void norm_cols_bwd_kernel(NormParams p) {
   });
 }
 
-// The same for tiles of 64 positions by 1024 lanes that keep dout of C channels each, all there are; hidden is read again
-// (parts of it kept in LDS gained nothing).  RMS is the template's for its registers: C = 16 fits them, and not with m
-// and c1 beside them.
+// The same for tiles of 64 positions by 1024 lanes that keep what they can of C channels each, all there are: dout in
+// registers, hidden of the first HL in LDS (up to 128 KB; each lane its own pieces), the others' is read again (2^17
+// positions x 1024 channels, RMS norm in bf16: 262 us, with all of hidden read again 279; 16384 x 2048: 66.5 and 70).
+// RMS is the template's for its registers: C = 16 fits them, and not with m and c1 beside them.
 template <typename XT, typename HT, bool RMS, int C>
 __global__ __launch_bounds__(1024) void norm_cols_bwd_keep_kernel(NormParams p) {
-  constexpr int NT = 1024, LP = 8, NG = NT / LP, T = LP * 8;
+  constexpr int NT = 1024, LP = 8, NG = NT / LP, T = LP * 8, QH = (int)sizeof(HT) / 2;
+  constexpr int HL = C < 16 / (int)sizeof(HT) ? C : 16 / (int)sizeof(HT);
   __shared__ float sm[(NT / 64 + 1) * T];
+  __shared__ u32x4a own[HL * QH][NT];
   const int pl = threadIdx.x % LP, cg = threadIdx.x / LP, E = (int)p.E;
   const int64_t tiles = (p.L + T - 1) / T, step = NG * p.L, tile = block_id();
   if (tile >= p.blocks) return;
@@ -439,7 +442,7 @@ __global__ __launch_bounds__(1024) void norm_cols_bwd_keep_kernel(NormParams p) 
   };
 #pragma unroll
   for (int c = 0; c < C; ++c) d[c].full(static_cast<const XT*>(p.x) + at0 + c * step, in && e0 + c * NG < E);
-  hidden(0, true);
+  hidden(0, 0 >= HL);
   w[0] = side(e0);
   float m[8], r[8], c1[8], c2[8];
   if (!RMS) load_n<float, 8>(p.stats + b * p.L + t, in ? 8 : 0, m);
@@ -449,7 +452,7 @@ __global__ __launch_bounds__(1024) void norm_cols_bwd_keep_kernel(NormParams p) 
 #pragma unroll
   for (int c = 0; c < C; ++c) {
     if (c + 1 < C) {
-      hidden(c + 1, true);
+      hidden(c + 1, c + 1 >= HL);
       w[(c + 1) & 1] = side(e0 + (c + 1) * NG);
     }
     const Piece<HT>& now = h[c & 1];
@@ -463,6 +466,10 @@ __global__ __launch_bounds__(1024) void norm_cols_bwd_keep_kernel(NormParams p) 
       c2[i] = __builtin_fmaf(gw, x, c2[i]);
       if (!RMS) here(c1[i]);
       here(c2[i]);
+    }
+    if (c < HL) {
+#pragma unroll
+      for (int q = 0; q < QH; ++q) own[(c < HL ? c : 0) * QH + q][threadIdx.x] = now.w[q];
     }
     if (part) {
       dw = sum_positions<LP>(dw);
@@ -485,7 +492,7 @@ __global__ __launch_bounds__(1024) void norm_cols_bwd_keep_kernel(NormParams p) 
   auto second = [&](int c) {
     const bool may = in && e0 + c * NG < E;
     if (p.dhidden) q[c & 1].full(static_cast<const HT*>(p.dhidden) + at0 + c * step, may);
-    hidden(c, false);
+    if (c >= HL) hidden(c, false);
     w[c & 1] = side(e0 + c * NG);
   };
   second(0);
@@ -500,7 +507,11 @@ __global__ __launch_bounds__(1024) void norm_cols_bwd_keep_kernel(NormParams p) 
   for (int c = 0; c < C; ++c) {
     if (c + 1 < C) second(c + 1);
     const int e = e0 + c * NG;
-    const Piece<HT>& now = h[c & 1];
+    Piece<HT> now = h[c & 1];
+    if (c < HL) {
+#pragma unroll
+      for (int k = 0; k < QH; ++k) now.w[k] = own[(c < HL ? c : 0) * QH + k][threadIdx.x];
+    }
     float g[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {

@@ -301,6 +301,24 @@ def test_same_bits_again_on_another_stream_and_into_given_buffers(cf):
     assert torch.equal(out, layer_norm_fwd(d["x"], d["weight"], d["bias"], d["residual"], **kw)[0])
 
 
+@pytest.mark.parametrize("rms", [False, True], ids=["layer", "rms"])
+@pytest.mark.parametrize("E", [700, 1000, 1100])
+def test_given_workspace_of_the_size_that_is_named(rms, E):
+    """Over channels in fp32, where the two norms keep different numbers of them between their passes."""
+    print("case: workspace of the norm's gradients", rms, E, flush=True)
+    g = torch.Generator(device=DEV).manual_seed(E)
+    d, h = torch.randn(1, E, 8192, generator=g, device=DEV), torch.randn(1, E, 8192, generator=g, device=DEV)
+    w = torch.ones(E, device=DEV)
+    stats = layer_norm_fwd(h, w, rms=rms, channels_first=True)[2]
+    n = layer_norm_bwd_workspace_size(d, rms=rms, channels_first=True)
+    ws = torch.zeros(n + 256, dtype=torch.uint8, device=DEV)
+    ws[n:] = 77
+    got = layer_norm_bwd(d, h, w, stats, rms=rms, channels_first=True, workspace=ws[:n])
+    ref = layer_norm_bwd(d, h, w, stats, rms=rms, channels_first=True)
+    torch.cuda.synchronize()
+    assert all(torch.equal(got[k], ref[k]) for k in ("dx", "dweight", "dbias")) and bool((ws[n:] == 77).all())
+
+
 @pytest.mark.parametrize("cf", [False, True], ids=["rows", "cols"])
 def test_more_than_2_31_elements(cf):
     """The last rows lie behind element 2^31."""
