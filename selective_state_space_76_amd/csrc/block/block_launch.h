@@ -126,6 +126,7 @@ struct RecurParams {
   float* drb;         // or null
   float* dib;
   int64_t B, D, L;
+  bool whole;         // backward: a team has all of a channel and joins its sums itself
   RecurPlan plan;
 };
 hipError_t launch_recur_fwd(const RecurParams& p, bool bf16, bool reverse, hipStream_t s);

@@ -108,6 +108,18 @@ def test_rows(dtype, reverse, B, D, L):
     same(g, check_bwd(i, None, reverse))
 
 
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("B", [1, 2, 5, 9])
+@pytest.mark.parametrize("L", [40, 700, 4500])
+def test_batches(dtype, B, L):
+    """The sums over the batch: a channel's one row, and several."""
+    print("case: recurrence batches", dtype, B, L, flush=True)
+    i = make(B, 9 if L < 4500 else 256, L, dtype, seed=B + L, gate=B % 2 == 1)
+    _, _, ck = check_fwd(i, B % 3 == 0)
+    g = check_bwd(i, ck, B % 3 == 0)
+    same(g, check_bwd(i, None, B % 3 == 0))
+
+
 def test_the_variants_are_all_reached():
     """By the sizes of the tests above: segments (a workspace), none."""
     assert recurrence_workspace_size(1, 3, 9001) and recurrence_workspace_size(2, 7, 12345, 0)
