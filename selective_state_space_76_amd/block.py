@@ -32,7 +32,8 @@ _NONE = 0xFFFFFFFFFFFFFFFF
 # Every tensor of a call is checked and turned into its address in one go.
 
 def _arg(t, shape, dtype, name, device):
-    """The address of a tensor that has to look like this (None for None); an error says what does not."""
+    """The address of a tensor that has to look like this (None for None); an error says what does not.  (Tensors that the
+    call made itself are not looked at again.)"""
     if t is None:
         return None
     if t.shape != shape or t.dtype != dtype or t.device != device or not t.is_contiguous():
@@ -92,8 +93,10 @@ def _dropout(x, mask, residual, dtype, out, stream):
     px, pr = _address(x), _arg(residual, x.shape, dtype, "residual", device)
     if out is None:
         out = made = _like(x, dtype, stream)
-    _check(load().ssm_dropout_fwd(n, *kinds, px, pr, mask, _arg(out, x.shape, dtype, "out", device),
-                                  _stream(stream, device)))
+        po = out.data_ptr()
+    else:
+        po = _arg(out, x.shape, dtype, "out", device)
+    _check(load().ssm_dropout_fwd(n, *kinds, px, pr, mask, po, _stream(stream, device)))
     if stream is not None:
         _hand_out(stream, made)
     return out
@@ -146,21 +149,25 @@ def layer_norm_fwd(x, weight=None, bias=None, residual=None, *, eps=1e-5, rms=Fa
     if out is None:
         out = _like(x, xdt, stream)
         made.append(out)
-    po = _arg(out, shape, xdt, "out", device)
+        po = out.data_ptr()
+    else:
+        po = _arg(out, shape, xdt, "out", device)
     if plain:
         ph, hidden = None, x
+    elif hidden is None:
+        hidden = _like(x if residual is None else residual, hdt, stream)
+        made.append(hidden)
+        ph = hidden.data_ptr()
     else:
-        if hidden is None:
-            hidden = _like(x if residual is None else residual, hdt, stream)
-            made.append(hidden)
         ph = _arg(hidden, shape, hdt, "hidden", device)
     if stats is None:
         stats = _empty((2, rows), f32, device, stream)
         made.append(stats)
-    elif stats is False:
-        stats = None
-    _check(load().ssm_layer_norm_fwd(sh, px, pw, pb, pr, eps, mask, po, ph, _arg(stats, (2, rows), f32, "stats", device),
-                                     _stream(stream, device)))
+        pst = stats.data_ptr()
+    else:
+        stats = None if stats is False else stats
+        pst = _arg(stats, (2, rows), f32, "stats", device)
+    _check(load().ssm_layer_norm_fwd(sh, px, pw, pb, pr, eps, mask, po, ph, pst, _stream(stream, device)))
     if stream is not None:
         _hand_out(stream, *made)
     return out, hidden, stats
@@ -193,11 +200,14 @@ def layer_norm_bwd(dout, hidden, weight, stats, *, dhidden=None, rms=False, chan
         if not wanted:
             if t is not None and not (k == "dx" and t is g.get("dresidual")):
                 raise ValueError("grads: %s is not computed here" % k)
-            g[k] = t = None
+            g[k] = None
+            to.append(None)
         elif t is None:
             g[k] = t = _empty(shp, dt, device, stream) if k[1] in "wb" else _like(dout if k == "dx" else hidden, dt, stream)
             made.append(t)
-        to.append(_arg(t, shp, dt, k, device))
+            to.append(t.data_ptr())
+        else:
+            to.append(_arg(t, shp, dt, k, device))
     pd, lib, ws_bytes, pws = _address(dout), load(), 0, None
     if to[2] is not None or to[3] is not None:
         workspace, ws_bytes = _workspace(workspace, lib.ssm_layer_norm_bwd_workspace_size(sh), device, stream)
@@ -259,11 +269,16 @@ def recurrence_fwd(x, r, i, decay, r_bias=None, i_bias=None, z=None, initial_sta
     if out is None:
         out = _like(x, x.dtype, stream)
         made.append(out)
+        po = out.data_ptr()
+    else:
+        po = _arg(out, x.shape, x.dtype, "out", device)
     if final_state is True:
         final_state = _empty((B, D), torch.float32, device, stream)
         made.append(final_state)
-    elif final_state is False:
-        final_state = None
+        pf = final_state.data_ptr()
+    else:
+        final_state = None if final_state is False else final_state
+        pf = _arg(final_state, (B, D), torch.float32, "final_state", device)
     pc = None
     if checkpoints is not None:
         pc = _arg(checkpoints, (B, D, lib.ssm_recurrence_checkpoints(sh)), torch.float32, "checkpoints", device)
@@ -271,9 +286,7 @@ def recurrence_fwd(x, r, i, decay, r_bias=None, i_bias=None, z=None, initial_sta
     if need or workspace is not None:
         workspace, ws_bytes = _workspace(workspace, need, device, stream)
         pws = _address(workspace)
-    _check(lib.ssm_recurrence_fwd(sh, *ins, _arg(out, x.shape, x.dtype, "out", device),
-                                  _arg(final_state, (B, D), torch.float32, "final_state", device), pc, pws, ws_bytes,
-                                  _stream(stream, device)))
+    _check(lib.ssm_recurrence_fwd(sh, *ins, po, pf, pc, pws, ws_bytes, _stream(stream, device)))
     if stream is not None:
         _hand_out(stream, *made)
     return out, final_state
@@ -299,11 +312,14 @@ def recurrence_bwd(x, r, i, decay, r_bias=None, i_bias=None, z=None, initial_sta
                       ("dr_bias", (D,), f32), ("di_bias", (D,), f32), ("dinitial_state", (B, D), f32)):
         t = g.get(k)
         if k == "dz" and z is None:
-            g[k] = t = None
+            g[k] = None
+            to.append(None)
         elif t is None:
             g[k] = t = _like(x, dt, stream) if shp is full else _empty(shp, d, device, stream)
             made.append(t)
-        to.append(_arg(t, shp, d, k, device))
+            to.append(t.data_ptr())
+        else:
+            to.append(_arg(t, shp, d, k, device))
     need = lib.ssm_recurrence_bwd_workspace_size(sh, 0 if pc is None else 1)
     workspace, ws_bytes = _workspace(workspace, need, device, stream)
     _check(lib.ssm_recurrence_bwd(sh, *ins, pd, pl, pc, *to, _address(workspace), ws_bytes, _stream(stream, device)))
@@ -325,8 +341,10 @@ def recurrence_update(state, x, r, i, decay, r_bias=None, i_bias=None, z=None, *
     ins = _recurrence_args(x, r, i, decay, r_bias, i_bias, z, None, size, size, device)
     if out is None:
         out = made = _like(x, dt, stream)
-    _check(load().ssm_recurrence_update(B, D, io, ps, *ins[:7],
-                                        _arg(out, size, dt, "out", device), _stream(stream, device)))
+        po = out.data_ptr()
+    else:
+        po = _arg(out, size, dt, "out", device)
+    _check(load().ssm_recurrence_update(B, D, io, ps, *ins[:7], po, _stream(stream, device)))
     if stream is not None:
         _hand_out(stream, made)
     return out
