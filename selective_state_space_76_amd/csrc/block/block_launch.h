@@ -76,8 +76,8 @@ struct NormTile {
 // tiles are better where there are enough of them (2^15 x 4096: 317 us with 128 positions, 375 with 64, 404 with 256).
 inline NormTile norm_cols_bwd_tile(int64_t B, int64_t E, int64_t L, int kind, bool rms) {
   auto tiles = [&](int64_t T) { return B * ((L + T - 1) / T); };
-  if (L % 8) return {tiles(128) >= 256 ? 128 : 64, false};
   if (tiles(64) < kFewTiles) return {16, false};
+  if (L % 8) return {tiles(128) >= 256 ? 128 : 64, false};
   if (E >= 128 && E <= norm_cols_bwd_kept(kind & 1, kind & 2, rms)) return {64, true};
   return {tiles(256) >= 512 ? 256 : tiles(128) >= 256 ? 128 : 64, false};
 }

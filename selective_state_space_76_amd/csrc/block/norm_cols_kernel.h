@@ -59,6 +59,13 @@ __device__ __forceinline__ void sum_groups(float (&v)[8], float* sm) {
   for (int k = 0; k < 8; ++k) v[k] = sm[NW * T + (threadIdx.x % LP) * 8 + k];
 }
 
+// The workgroup's tile of `count`, or -1.  Where tiles share lines an XCD's tiles are neighbours, so that its L2 has a
+// line once (4 x 2048 x 4095, gradients: 128 us in order, 88 so; 2^17 x 1024, which shares none: 119 and 132).
+__device__ __forceinline__ int64_t tile_id(int64_t count, bool lines) {
+  const uint32_t blk = block_id();
+  return blk >= count ? -1 : lines ? (int64_t)blk : xcd_remap((int)blk, (int)count);
+}
+
 // sum over the LP lanes that hold a channel's positions
 template <int LP> __device__ __forceinline__ float sum_positions(float v) {
   auto step = [&](auto ctrl) {
@@ -115,14 +122,15 @@ struct Chunk {
 template <typename XT, typename HT, bool RES, bool DROP, bool ODD, int NT, int LP, int C, bool KEEP>
 __global__ __launch_bounds__(NT) void norm_cols_kernel(NormParams p) {
   constexpr int NG = NT / LP, T = LP * 8;
+  constexpr bool SHARED = ODD || LP < 8;  // neighbouring tiles share lines
   __shared__ float sm[(NT / 64 + 1) * T];
   const int pl = threadIdx.x % LP, cg = threadIdx.x / LP, E = (int)p.E;
-  const int64_t tiles = (p.L + T - 1) / T, blk = block_id();
+  const bool lines = !SHARED && p.L % 64 == 0;  // tiles are whole lines
+  const int64_t tiles = (p.L + T - 1) / T, blk = tile_id(p.B * tiles, lines);
+  if (blk < 0) return;
   const int64_t b = blk / tiles, t = blk % tiles * T + pl * 8, total = p.rows * p.E, step = NG * p.L;
-  if (b >= p.B) return;
   const int n = p.L - t >= 8 ? 8 : !ODD || p.L <= t ? 0 : (int)(p.L - t);
   const int64_t base = b * p.E * p.L + t;
-  const bool lines = !ODD && p.L % 64 == 0;
   static_assert(!(DROP && KEEP), "");
   const Drop drop(p.drop);
   typedef Chunk<XT, HT, RES, C> Ch;
@@ -138,8 +146,8 @@ __global__ __launch_bounds__(NT) void norm_cols_kernel(NormParams p) {
   auto fetch = [&](Ch& k, int e0, bool side) {  // (positions behind the last one: whatever is there)
     channels(e0, [&](int c, int e, int64_t at) {
       const bool may = e < E && n > 0 && (!ODD || at + 8 <= total);
-      k.x[c].full(static_cast<const XT*>(p.x) + at, may, !KEEP && !side);
-      if (RES) k.q[RES ? c : 0].full(static_cast<const HT*>(p.residual) + at, may, !KEEP && !side);
+      k.x[c].full(static_cast<const XT*>(p.x) + at, may, SHARED || (!KEEP && !side));
+      if (RES) k.q[RES ? c : 0].full(static_cast<const HT*>(p.residual) + at, may, SHARED || (!KEEP && !side));
     });
     if (side) {
 #pragma unroll
@@ -301,11 +309,12 @@ __global__ __launch_bounds__(NT) void norm_cols_kernel(NormParams p) {
 template <typename XT, typename HT, bool ODD, int NT, int LP, int C>
 __global__ __launch_bounds__(NT) void norm_cols_bwd_kernel(NormParams p) {
   constexpr int NG = NT / LP, T = LP * 8;
+  constexpr bool SHARED = ODD || LP < 8;  // neighbouring tiles share lines
   __shared__ float sm[(NT / 64 + 1) * T];
   const int pl = threadIdx.x % LP, cg = threadIdx.x / LP, E = (int)p.E;
-  const int64_t tiles = (p.L + T - 1) / T, total = p.rows * p.E, step = NG * p.L, tile = block_id();
-  if (tile >= p.blocks) return;
-  const bool lines = !ODD && p.L % 64 == 0;
+  const bool lines = !SHARED && p.L % 64 == 0;
+  const int64_t tiles = (p.L + T - 1) / T, total = p.rows * p.E, step = NG * p.L, tile = tile_id(p.blocks, lines);
+  if (tile < 0) return;
   const Drop drop(p.drop);
   float* part = p.part ? p.part + tile * 2 * p.E : nullptr;
   struct Ch {
@@ -327,10 +336,10 @@ __global__ __launch_bounds__(NT) void norm_cols_bwd_kernel(NormParams p) {
   };
   auto fetch = [&](Ch& k, int e0, bool third) {
     channels(e0, [&](int c, int e, int64_t at) {
-      const bool may = e < E && n > 0 && (!ODD || at + 8 <= total), again = LP < 32 && !third;
+      const bool may = e < E && n > 0 && (!ODD || at + 8 <= total), again = SHARED || (LP < 32 && !third);
       k.d[c].full(static_cast<const XT*>(p.x) + at, may, again);
       k.h[c].full(static_cast<const HT*>(p.residual) + at, may, again);
-      if (third && p.dhidden) k.q[c].full(static_cast<const HT*>(p.dhidden) + at, may);
+      if (third && p.dhidden) k.q[c].full(static_cast<const HT*>(p.dhidden) + at, may, SHARED);
       k.w[c] = p.weight ? p.weight[e < E ? e : 0] : 1.0f;
     });
     if (ODD)
@@ -422,9 +431,9 @@ __global__ __launch_bounds__(1024) void norm_cols_bwd_keep_kernel(NormParams p) 
   __shared__ float sm[(NT / 64 + 1) * T];
   __shared__ u32x4a own[HL * QH][NT];
   const int pl = threadIdx.x % LP, cg = threadIdx.x / LP, E = (int)p.E;
-  const int64_t tiles = (p.L + T - 1) / T, step = NG * p.L, tile = block_id();
-  if (tile >= p.blocks) return;
   const bool lines = p.L % 64 == 0;
+  const int64_t tiles = (p.L + T - 1) / T, step = NG * p.L, tile = tile_id(p.blocks, lines);
+  if (tile < 0) return;
   const Drop drop(p.drop);
   float* part = p.part ? p.part + tile * 2 * p.E : nullptr;
   const int64_t b = tile / tiles, t = tile % tiles * T + pl * 8;
@@ -546,32 +555,35 @@ void go(const NormParams& p, hipStream_t s) {
 }
 
 // Everything read again for each pass.
-template <typename XT, typename HT, bool RES, bool DROP>
+template <typename XT, typename HT, bool RES, bool DROP, bool ODD>
 void again(const NormParams& p, bool wide, hipStream_t s) {
-  if (p.L % 8) return go<XT, HT, RES, DROP, true, 512, 16, 2, false>(p, s);
-  if (p.B * ((p.L + 63) / 64) < kFewTiles) return go<XT, HT, RES, DROP, false, 1024, 2, 2, false>(p, s);
-  wide ? go<XT, HT, RES, DROP, false, 512, 32, 2, false>(p, s) : go<XT, HT, RES, DROP, false, 1024, 8, 2, false>(p, s);
+  wide ? go<XT, HT, RES, DROP, ODD, 512, 32, 2, false>(p, s) : go<XT, HT, RES, DROP, ODD, 1024, 8, 2, false>(p, s);
 }
 
 // Wide tiles read and write longer pieces of the rows, which lie far apart (2^17 positions x 1024 channels in bf16: 125
 // us with 64 positions, 114 with 128; 2^18 x 512: 122, 112, and 105 with 256), but hold fewer channels and leave compute
-// units idle where there are few of them.
-template <typename XT, typename HT, bool RES>
-void fwd(const NormParams& p, hipStream_t s) {
+// units idle where there are few of them.  With few tiles of 64 positions they are cut to 16, and what is kept gains
+// nothing then (8 x 512 positions x 768 channels with a residual: 9.8 us, kept 9.8, 64 positions and kept 14.6).
+template <typename XT, typename HT, bool RES, bool ODD>
+void fwd_of(const NormParams& p, hipStream_t s) {
   constexpr int C = kept_channels<XT, HT, RES>();
   const bool wide = p.B * ((p.L + 127) / 128) >= 512;
-  if (p.drop.below) return again<XT, HT, RES, true>(p, wide, s);
-  if (p.L % 8) {
-    if (p.E <= 16 * (C / 4)) return go<XT, HT, RES, false, true, 256, 16, C / 4, true>(p, s);
-    if (p.E <= 64 * (C / 4)) return go<XT, HT, RES, false, true, 512, 8, C / 4, true>(p, s);
-    return again<XT, HT, RES, false>(p, wide, s);
+  if (p.B * ((p.L + 63) / 64) < kFewTiles) {
+    if (p.drop.below) return go<XT, HT, RES, true, ODD, 512, 2, 2, false>(p, s);
+    return go<XT, HT, RES, false, ODD, 512, 2, 2, false>(p, s);
   }
-  if (p.E <= 16 * (C / 4)) return go<XT, HT, RES, false, false, 256, 16, C / 4, true>(p, s);
-  if (wide && p.E <= 32 * (C / 4)) return go<XT, HT, RES, false, false, 512, 16, C / 4, true>(p, s);
-  if (p.E <= 64 * (C / 4)) return go<XT, HT, RES, false, false, 512, 8, C / 4, true>(p, s);
-  if (wide && p.E <= 32 * C) return go<XT, HT, RES, false, false, 512, 16, C, true>(p, s);
-  if (p.E <= 64 * C) return go<XT, HT, RES, false, false, 512, 8, C, true>(p, s);
-  again<XT, HT, RES, false>(p, wide, s);
+  if (p.drop.below) return again<XT, HT, RES, true, ODD>(p, wide, s);
+  if (p.E <= 16 * (C / 4)) return go<XT, HT, RES, false, ODD, 256, 16, C / 4, true>(p, s);
+  if (wide && p.E <= 32 * (C / 4)) return go<XT, HT, RES, false, ODD, 512, 16, C / 4, true>(p, s);
+  if (p.E <= 64 * (C / 4)) return go<XT, HT, RES, false, ODD, 512, 8, C / 4, true>(p, s);
+  if (wide && p.E <= 32 * C) return go<XT, HT, RES, false, ODD, 512, 16, C, true>(p, s);
+  if (p.E <= 64 * C) return go<XT, HT, RES, false, ODD, 512, 8, C, true>(p, s);
+  again<XT, HT, RES, false, ODD>(p, wide, s);
+}
+
+template <typename XT, typename HT, bool RES>
+void fwd(const NormParams& p, hipStream_t s) {
+  p.L % 8 ? fwd_of<XT, HT, RES, true>(p, s) : fwd_of<XT, HT, RES, false>(p, s);
 }
 
 template <typename XT, typename HT, bool ODD, int NT, int LP, int C>
@@ -596,7 +608,10 @@ void bwd(const NormParams& p, hipStream_t s) {
   const int kind = (sizeof(XT) == 2 ? 1 : 0) + (sizeof(HT) == 2 ? 2 : 0);
   const NormTile tile = norm_cols_bwd_tile(p.B, p.E, p.L, kind, p.rms);
   if (tile.keep) return p.rms ? keep_bwd<XT, HT, true>(p, s) : keep_bwd<XT, HT, false>(p, s);
-  if (p.L % 8) return tile.T > 64 ? go_bwd<XT, HT, true, 512, 16, 2>(p, s) : go_bwd<XT, HT, true, 512, 8, 2>(p, s);
+  if (p.L % 8) {
+    if (tile.T == 16) return go_bwd<XT, HT, true, 512, 2, 2>(p, s);
+    return tile.T > 64 ? go_bwd<XT, HT, true, 512, 16, 2>(p, s) : go_bwd<XT, HT, true, 512, 8, 2>(p, s);
+  }
   if (tile.T == 256) return go_bwd<XT, HT, false, 512, 32, 2>(p, s);
   if (tile.T == 128) return go_bwd<XT, HT, false, 512, 16, 2>(p, s);
   if (tile.T == 16) return go_bwd<XT, HT, false, 1024, 2, 2>(p, s);

@@ -255,6 +255,46 @@ def test_norm_over_channels_of_long_sequences(xt, ht, B, E, L):
             assert bool(((got["dbias"].double() - d.double().sum((0, 2))).abs() <= lim).all())
 
 
+@pytest.mark.parametrize("p", [0.0, 0.2], ids=["whole", "dropped"])
+@pytest.mark.parametrize("xt,ht", [(F32, F32), (BF16, BF16), (BF16, F32)], ids=["f32", "bf16", "bf16-f32"])
+@pytest.mark.parametrize("E", [40, 100, 200, 400, 900, 1100])
+@pytest.mark.parametrize("L", [301, 8197, 65541])
+def test_norm_over_channels_of_odd_lengths(xt, ht, E, L, p):
+    """Rows that begin anywhere, in every form of the forward pass and of the gradients; bounds as above."""
+    print("case: norm over channels, odd", xt, ht, E, L, p, flush=True)
+    g = torch.Generator(device=DEV).manual_seed(E + L)
+    x, r, d, dh = (randn(g, 1, E, L, dtype=t) for t in (xt, ht, xt, ht))
+    w, b = 1 + 0.1 * randn(g, E), randn(g, E)
+    mask = ssm.dropout_fwd(torch.ones(1, E, L, device=DEV), p, seed=9) if p else torch.ones(1, E, L, device=DEV)
+
+    def near(got, ref):
+        eps = 0.0 if got.dtype == F32 else torch.finfo(BF16).eps / 2
+        return bool(((got.double() - ref).abs() <= 1e-5 * ref.abs().max() + eps * (1 + 2 ** -6) * ref.abs()).all())
+
+    rms = E % 200 == 0
+    kw = dict(rms=rms, channels_first=True, p=p, seed=9)
+    out, hidden, stats = ssm.layer_norm_fwd(x, w, b, r, **kw)
+    s = x.double() * mask.double() + r.double()
+    ref, m, f = norm64(s, w.double(), b.double(), rms, 1)
+    assert near(out, ref) and near(hidden, s)
+    assert near(stats[0], m.reshape(-1)) and near(stats[1], f.reshape(-1))
+    if not p:  # alone
+        out, same, _ = ssm.layer_norm_fwd(x, w, b, **kw)
+        assert same is x and near(out, norm64(x.double(), w.double(), b.double(), rms, 1)[0])
+    del ref, out
+    got = ssm.layer_norm_bwd(d, hidden, w, stats, dhidden=dh, residual=True, **kw)
+    st = stats.double().view(2, 1, 1, L)
+    xh = (hidden.double() - st[0]) * st[1]
+    gw = d.double() * w.double().view(-1, 1)
+    ds = gw - xh * (gw * xh).mean(1, keepdim=True)
+    ds = st[1] * (ds if rms else ds - gw.mean(1, keepdim=True)) + dh.double()
+    assert near(got["dx"], ds * mask.double()) and near(got["dresidual"], ds)
+    lim = 1300 * R.U * (d.double() * xh).abs().sum((0, 2)) + 1e-30
+    assert bool(((got["dweight"].double() - (d.double() * xh).sum((0, 2))).abs() <= lim).all())
+    lim = 1300 * R.U * d.double().abs().sum((0, 2))
+    assert bool(((got["dbias"].double() - d.double().sum((0, 2))).abs() <= lim).all())
+
+
 # on either side of the channels that the gradients' tiles of 64 positions keep, ends inside a tile; partial sums of more
 # tiles than are joined in one go
 KEPT = [(1, 130, 8192), (2, 256, 4104), (1, 257, 8200), (1, 520, 8192), (1, 769, 8192), (3, 1024, 2752), (1, 1100, 8192),
