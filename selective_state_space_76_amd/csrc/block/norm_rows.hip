@@ -429,9 +429,10 @@ __global__ __launch_bounds__(256) void norm_sums_kernel(NormParams p) {
 __global__ __launch_bounds__(1024) void norm_join_kernel(NormParams p, int64_t step, int64_t many) {
   __shared__ float sm[1024], sn[256];
   const int64_t cols = (p.E + 15) / 16, n = (p.blocks + step - 1) / step;
-  const int64_t blk = block_id();
+  const int64_t count = 2 * cols * ((n + many - 1) / many);
+  if (block_id() >= count) return;
+  const int64_t blk = xcd_remap((int)block_id(), (int)count);  // (neighbours read the same lines)
   const int64_t which = blk / cols % 2, first = blk / (2 * cols) * many;
-  if (first >= n) return;
   const int64_t here = n - first < many ? n - first : many;
   const int64_t c = blk % cols * 16 + (threadIdx.x & 15);
   const int64_t per = (here + 63) / 64, row = step * 2 * p.E;
