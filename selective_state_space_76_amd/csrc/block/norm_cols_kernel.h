@@ -305,6 +305,124 @@ __global__ __launch_bounds__(NT) void norm_cols_kernel(NormParams p) {
   }
 }
 
+// The same with a residual for tiles of 64 positions by 1024 lanes that keep what they can of C channels each, all there
+// are: x in registers (what is dropped is zero there), the residual of the first HL in LDS (up to 128 KB; each lane
+// its own pieces), the others' is read again.
+template <typename XT, typename HT, int C>
+__global__ __launch_bounds__(1024) void norm_cols_keep_kernel(NormParams p) {
+  constexpr int NT = 1024, LP = 8, NG = NT / LP, T = LP * 8, QH = (int)sizeof(HT) / 2;
+  constexpr int HL = C < 16 / (int)sizeof(HT) ? C : 16 / (int)sizeof(HT);
+  __shared__ float sm[(NT / 64 + 1) * T];
+  __shared__ u32x4a own[HL * QH][NT];
+  const int pl = threadIdx.x % LP, cg = threadIdx.x / LP, E = (int)p.E;
+  const bool lines = p.L % 64 == 0;
+  const int64_t tiles = (p.L + T - 1) / T, step = NG * p.L, tile = tile_id(p.B * tiles, lines);
+  if (tile < 0) return;
+  const Drop drop(p.drop);
+  const float scale = drop.any() ? drop.scale : 1.0f;
+  const int64_t b = tile / tiles, t = tile % tiles * T + pl * 8;
+  const bool in = t < p.L;
+  const int64_t base = b * p.E * p.L + t;
+  Piece<XT> x[C];
+  Piece<HT> q[2];
+  int e0 = cg;
+  asm volatile("" : "+v"(e0));
+  int64_t at0 = base + e0 * p.L;
+  auto other = [&](int c, bool again) {
+    q[c & 1].full(static_cast<const HT*>(p.residual) + at0 + c * step, in && e0 + c * NG < E, again);
+  };
+  auto sum = [&](int c, const Piece<HT>& o, float (&s)[8]) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) s[i] = __builtin_fmaf(x[c].at(i), scale, o.at(i));
+  };
+#pragma unroll
+  for (int c = 0; c < C; ++c) x[c].full(static_cast<const XT*>(p.x) + at0 + c * step, in && e0 + c * NG < E);
+  other(0, 0 >= HL);
+  float m[8], r[8], count = 0.0f;
+#pragma unroll
+  for (int k = 0; k < 8; ++k) m[k] = r[k] = 0.0f;
+#pragma unroll
+  for (int c = 0; c < C; ++c) {
+    if (c + 1 < C) other(c + 1, c + 1 >= HL);
+    const Piece<HT>& now = q[c & 1];
+    const int64_t at = at0 + c * step;
+    if (drop.any()) x[c].keep(drop.kept((uint64_t)at));
+    float s[8];
+    sum(c, now, s);
+    if (e0 + c * NG < E) {
+      count += 1.0f;
+      const float share = p.rms ? 0.0f : rcp_(count);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float d = s[i] - m[i];
+        m[i] = __builtin_fmaf(d, share, m[i]);
+        r[i] = __builtin_fmaf(d, s[i] - m[i], r[i]);
+        here(m[i]);
+        here(r[i]);
+      }
+      if (in && p.hidden) store_cols(static_cast<HT*>(p.hidden) + at, 8, s, lines);
+    }
+    if (c < HL) {
+#pragma unroll
+      for (int k = 0; k < QH; ++k) own[(c < HL ? c : 0) * QH + k][threadIdx.x] = now.w[k];
+    }
+    __builtin_amdgcn_sched_barrier(0);
+  }
+#pragma unroll
+  for (int c = 0; c < C; ++c) x[c].forget();
+  e0 = cg;
+  asm volatile("" : "+v"(e0));
+  at0 = base + e0 * p.L;
+  float w[2], o[2];
+  auto second = [&](int c) {
+    if (c >= HL) other(c, false);
+    const int e = e0 + c * NG < E ? e0 + c * NG : 0;
+    w[c & 1] = p.weight ? p.weight[e] : 1.0f;
+    o[c & 1] = p.bias ? p.bias[e] : 0.0f;
+  };
+  second(0);
+  if (!p.rms) {
+    float mine[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      mine[i] = m[i];
+      m[i] *= count;
+    }
+    sum_groups<NT, LP>(m, sm);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      m[i] *= p.inv_e;
+      const float d = mine[i] - m[i];
+      r[i] = __builtin_fmaf(d * count, d, r[i]);
+    }
+  }
+  sum_groups<NT, LP>(r, sm);
+#pragma unroll
+  for (int k = 0; k < 8; ++k) r[k] = 1.0f / sqrtf(r[k] * p.inv_e + p.eps);
+#pragma unroll
+  for (int c = 0; c < C; ++c) {
+    if (c + 1 < C) second(c + 1);
+    Piece<HT> now = q[c & 1];
+    if (c < HL) {
+#pragma unroll
+      for (int k = 0; k < QH; ++k) now.w[k] = own[(c < HL ? c : 0) * QH + k][threadIdx.x];
+    }
+    float s[8];
+    sum(c, now, s);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) s[i] = __builtin_fmaf((s[i] - m[i]) * r[i], w[c & 1], o[c & 1]);
+    if (in && e0 + c * NG < E) store_cols(static_cast<XT*>(p.out) + at0 + c * step, 8, s, lines);
+    __builtin_amdgcn_sched_barrier(0);
+  }
+  if (p.stats && cg == 0 && in) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      p.stats[b * p.L + t + k] = m[k];
+      p.stats[p.rows + b * p.L + t + k] = r[k];
+    }
+  }
+}
+
 // A tile each, everything read twice.  The tile's dw and db are a partial sum of its own.
 template <typename XT, typename HT, bool ODD, int NT, int LP, int C>
 __global__ __launch_bounds__(NT) void norm_cols_bwd_kernel(NormParams p) {
@@ -560,6 +678,21 @@ void again(const NormParams& p, bool wide, hipStream_t s) {
   wide ? go<XT, HT, RES, DROP, ODD, 512, 32, 2, false>(p, s) : go<XT, HT, RES, DROP, ODD, 1024, 8, 2, false>(p, s);
 }
 
+// With a residual, channels that do not fit the registers: x alone does (4 x 4096 positions x 2048 channels in bf16: 75
+// us, everything read again 81; 2^17 x 2048: 521 and 625; 2^18 x 512 with dropout: 281 and 308; 8 x 2048 x 768 with
+// dropout into fp32: 40 and 45).
+template <typename XT> constexpr int keep_most() { return sizeof(XT) == 2 ? 16 : 8; }
+
+template <typename XT, typename HT>
+void keep_fwd(const NormParams& p, hipStream_t s) {
+  auto go = [&](auto c) {
+    hipLaunchKernelGGL((norm_cols_keep_kernel<XT, HT, decltype(c)::value>), grid_of(p.B * ((p.L + 63) / 64)), dim3(1024),
+                       0, s, p);
+  };
+  const int64_t c = (p.E + 127) / 128;
+  c <= 2 ? go(IC<2>()) : c <= 4 ? go(IC<4>()) : c <= 8 ? go(IC<8>()) : go(IC<keep_most<XT>()>());
+}
+
 // Wide tiles read and write longer pieces of the rows, which lie far apart (2^17 positions x 1024 channels in bf16: 125
 // us with 64 positions, 114 with 128; 2^18 x 512: 122, 112, and 105 with 256), but hold fewer channels and leave compute
 // units idle where there are few of them.  With few tiles of 64 positions they are cut to 16, and what is kept gains
@@ -571,6 +704,9 @@ void fwd_of(const NormParams& p, hipStream_t s) {
   if (p.B * ((p.L + 63) / 64) < kFewTiles) {
     if (p.drop.below) return go<XT, HT, RES, true, ODD, 512, 2, 2, false>(p, s);
     return go<XT, HT, RES, false, ODD, 512, 2, 2, false>(p, s);
+  }
+  if constexpr (RES && !ODD) {
+    if (p.E >= 128 && p.E <= 128 * keep_most<XT>() && (p.drop.below || p.E > 64 * C)) return keep_fwd<XT, HT>(p, s);
   }
   if (p.drop.below) return again<XT, HT, RES, true, ODD>(p, wide, s);
   if (p.E <= 16 * (C / 4)) return go<XT, HT, RES, false, ODD, 256, 16, C / 4, true>(p, s);

@@ -255,13 +255,17 @@ def test_norm_over_channels_of_long_sequences(xt, ht, B, E, L):
             assert bool(((got["dbias"].double() - d.double().sum((0, 2))).abs() <= lim).all())
 
 
+ODD_AND_KEPT = ([(E, L) for E in (40, 100, 200, 400, 900, 1100) for L in (301, 8197, 65541)]
+                + [(E, L) for E in (128, 250, 257, 512, 600, 1024, 1300, 2048, 2049) for L in (8192, 8200)])
+
+
 @pytest.mark.parametrize("p", [0.0, 0.2], ids=["whole", "dropped"])
 @pytest.mark.parametrize("xt,ht", [(F32, F32), (BF16, BF16), (BF16, F32)], ids=["f32", "bf16", "bf16-f32"])
-@pytest.mark.parametrize("E", [40, 100, 200, 400, 900, 1100])
-@pytest.mark.parametrize("L", [301, 8197, 65541])
-def test_norm_over_channels_of_odd_lengths(xt, ht, E, L, p):
-    """Rows that begin anywhere, in every form of the forward pass and of the gradients; bounds as above."""
-    print("case: norm over channels, odd", xt, ht, E, L, p, flush=True)
+@pytest.mark.parametrize("E,L", ODD_AND_KEPT)
+def test_norm_over_channels_and_its_gradients(xt, ht, E, L, p):
+    """Rows that begin anywhere, in every form of the forward pass and of the gradients, and with x kept and the residual
+    in part; bounds as above."""
+    print("case: norm over channels and gradients", xt, ht, E, L, p, flush=True)
     g = torch.Generator(device=DEV).manual_seed(E + L)
     x, r, d, dh = (randn(g, 1, E, L, dtype=t) for t in (xt, ht, xt, ht))
     w, b = 1 + 0.1 * randn(g, E), randn(g, E)
