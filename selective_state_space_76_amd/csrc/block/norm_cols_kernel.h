@@ -6,6 +6,10 @@
 // over the groups: within a wave by exchanges that leave each lane one position, over the waves through LDS.  KEEP: C
 // channels a group are all there are, and stay in registers as they came from memory; otherwise they are read again
 // for every pass.
+//
+// Bound by HBM: 2^17 positions x 1024 channels in bf16, RMS norm: 113-119 us by the box, 4.5-4.7 TB/s (a copy 104).  The
+// gradients of 4 x 4096 x 2048 with a residual and the stream's own gradient: 63 us, and 5 for the join of the tiles'
+// sums, 4.85 TB/s with what is read twice.
 #pragma once
 #include "block_device.h"
 
