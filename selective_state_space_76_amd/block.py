@@ -18,6 +18,7 @@ include/ssm_scan.h for the formulas and layouts), and nothing falls back to anyt
 from __future__ import annotations
 
 import ctypes
+from operator import index
 
 import torch
 
@@ -62,10 +63,10 @@ def _mask(p, seed, call, device, stream, fresh):
             raise TypeError("seed: expected an int or one int64 on the device, got %s of %d" % (seed.dtype, seed.numel()))
         if seed.device != device:
             _expect(seed, seed.shape, seed.dtype, "seed", device)
-        return ssm_dropout(p, 0, _ptr(seed), call & _NONE)
+        return ssm_dropout(p, 0, _ptr(seed), index(call) & _NONE)
     if fresh and _capturing(stream):
         raise RuntimeError("every replay would repeat this call's mask: give the seed as a tensor on the device")
-    return ssm_dropout(p, seed & _NONE, None, call & _NONE)
+    return ssm_dropout(p, index(seed) & _NONE, None, index(call) & _NONE)  # (numpy's integers, too)
 
 
 def dropout_fwd(x, p, seed, *, call=0, residual=None, out=None, stream=None):

@@ -237,6 +237,16 @@ def test_a_mask_that_replays_would_repeat_is_refused(monkeypatch):
     assert K._mask(0.0, None, 0, x.device, None, True) is None
 
 
+def test_seeds_are_integers_of_any_kind():
+    """numpy's, too, and negative ones: the same 64 bits; nothing that is no integer."""
+    for seed, call in ((-5, 3), (2 ** 63 + 1, 2 ** 64 - 1), (np.int64(-5), np.int32(3)), (np.uint64(2 ** 63 + 1), np.int64(-1))):
+        m = K._mask(0.5, seed, call, torch.device("cpu"), None, False)
+        assert (m.seed, m.call) == (int(seed) % 2 ** 64, int(call) % 2 ** 64)
+    for seed in (1.5, "7"):
+        with pytest.raises(TypeError):
+            K._mask(0.5, seed, 0, torch.device("cpu"), None, False)
+
+
 class Library:
     """Every size is 4096 bytes, every call succeeds."""
 
