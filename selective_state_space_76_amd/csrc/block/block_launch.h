@@ -60,8 +60,13 @@ inline hipError_t launch_norm_cols_bwd(const NormParams& p, int kind, hipStream_
                                                                  : launch_norm_cols_bwd_f32(p, s);
 }
 int64_t norm_rows_bwd_blocks(int64_t rows, int64_t E);
-// The backward pass over [B, E, L]: a workgroup and a partial sum of dw and db for each tile.
-constexpr int64_t kFewTiles = 128;  // of 64 positions: then they are cut to 16, lines shared through the caches
+// Over [B, E, L]: tiles of 16 positions, lines shared through the caches, where there are few of 64, or where rows are so
+// short that most lanes of those would have none (4096 x 768 x 8 in bf16 with a residual: 71 us, 187 in tiles of 64; but
+// few channels leave more lanes without any: 65536 x 16 x 8: 355 and 186).
+inline bool norm_cols_narrow(int64_t B, int64_t E, int64_t L) {
+  return B * ((L + 63) / 64) < 128 || (L <= 32 && E >= 256);
+}
+// The backward pass there: a workgroup and a partial sum of dw and db for each tile.
 // Channels up to which a tile of 64 positions keeps dout between its two passes, as far as 128 registers go.
 constexpr int norm_cols_bwd_kept(bool x16, bool h16, bool rms) {
   return 128 * (!x16 ? (rms ? 8 : 6) : !h16 ? 8 : rms ? 16 : 12);
@@ -76,10 +81,10 @@ struct NormTile {
 // tiles are better where there are enough of them (2^15 x 4096: 317 us with 128 positions, 375 with 64, 404 with 256).
 inline NormTile norm_cols_bwd_tile(int64_t B, int64_t E, int64_t L, int kind, bool rms) {
   auto tiles = [&](int64_t T) { return B * ((L + T - 1) / T); };
-  if (tiles(64) < kFewTiles) return {16, false};
-  if (L % 8) return {tiles(128) >= 256 ? 128 : 64, false};
+  if (norm_cols_narrow(B, E, L)) return {16, false};
+  if (L % 8) return {L >= 128 && tiles(128) >= 256 ? 128 : 64, false};
   if (E >= 128 && E <= norm_cols_bwd_kept(kind & 1, kind & 2, rms)) return {64, true};
-  return {tiles(256) >= 512 ? 256 : tiles(128) >= 256 ? 128 : 64, false};
+  return {L >= 256 && tiles(256) >= 512 ? 256 : L >= 128 && tiles(128) >= 256 ? 128 : 64, false};
 }
 inline int64_t norm_cols_bwd_blocks(int64_t B, int64_t E, int64_t L, int kind, bool rms) {
   const int T = norm_cols_bwd_tile(B, E, L, kind, rms).T;

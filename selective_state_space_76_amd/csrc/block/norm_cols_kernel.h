@@ -679,7 +679,7 @@ void go(const NormParams& p, hipStream_t s) {
 // Everything read again for each pass.
 template <typename XT, typename HT, bool RES, bool DROP, bool ODD>
 void again(const NormParams& p, bool wide, hipStream_t s) {
-  wide ? go<XT, HT, RES, DROP, ODD, 512, 32, 2, false>(p, s) : go<XT, HT, RES, DROP, ODD, 1024, 8, 2, false>(p, s);
+  wide && p.L >= 256 ? go<XT, HT, RES, DROP, ODD, 512, 32, 2, false>(p, s) : go<XT, HT, RES, DROP, ODD, 512, 8, 2, false>(p, s);
 }
 
 // With a residual, channels that do not fit the registers: x alone does (4 x 4096 positions x 2048 channels in bf16: 75
@@ -704,8 +704,8 @@ void keep_fwd(const NormParams& p, hipStream_t s) {
 template <typename XT, typename HT, bool RES, bool ODD>
 void fwd_of(const NormParams& p, hipStream_t s) {
   constexpr int C = kept_channels<XT, HT, RES>();
-  const bool wide = p.B * ((p.L + 127) / 128) >= 512;
-  if (p.B * ((p.L + 63) / 64) < kFewTiles) {
+  const bool wide = p.L >= 128 && p.B * ((p.L + 127) / 128) >= 512;
+  if (norm_cols_narrow(p.B, p.E, p.L)) {
     if (p.drop.below) return go<XT, HT, RES, true, ODD, 512, 2, 2, false>(p, s);
     return go<XT, HT, RES, false, ODD, 512, 2, 2, false>(p, s);
   }
@@ -754,7 +754,7 @@ void bwd(const NormParams& p, hipStream_t s) {
   }
   if (tile.T == 256) return go_bwd<XT, HT, false, 512, 32, 2>(p, s);
   if (tile.T == 128) return go_bwd<XT, HT, false, 512, 16, 2>(p, s);
-  if (tile.T == 16) return go_bwd<XT, HT, false, 1024, 2, 2>(p, s);
+  if (tile.T == 16) return go_bwd<XT, HT, false, 512, 2, 2>(p, s);
   go_bwd<XT, HT, false, 512, 8, 2>(p, s);
 }
 
