@@ -96,7 +96,7 @@ hipError_t launch_norm_join(const NormParams& p, hipStream_t s);
 
 // ---- gated linear recurrence (recur_fwd.hip, recur_bwd.hip)
 struct RecurPlan {
-  int lanes = 64;       // lanes per row: 16 or 64
+  int lanes = 64;       // lanes per row: 1, 4, 16, 32 or 64
   int waves = 1;        // waves that share a row: 1, 4 or 8
   int64_t S = 1;        // segments of a row
   int64_t blocks = 0;   // blocks of 64 pieces in a row, each with a checkpoint

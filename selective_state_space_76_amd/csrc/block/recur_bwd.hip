@@ -18,14 +18,14 @@ namespace ssm {
 
 // Z: there is a gate.  MAPS: the segments' maps of the adjoint.
 template <typename IO, int LN, int W, bool REV, bool Z, bool MAPS>
-__global__ __launch_bounds__(W > 4 ? W * 64 : 256, Z || LN == 16 ? 3 : 4) void recur_bwd_kernel(RecurParams p) {
+__global__ __launch_bounds__(W > 4 ? W * 64 : 256, Z || LN < 64 ? 3 : 4) void recur_bwd_kernel(RecurParams p) {
   constexpr int V = 16 / (int)sizeof(IO);
   constexpr int UNITS = W > 4 ? 1 : 256 / (LN * W);
   constexpr int TURN = LN * W * V;
   __shared__ float sm[2][W][2];
   const int lane = threadIdx.x % LN, w = W > 1 ? __builtin_amdgcn_readfirstlane(threadIdx.x / 64) : 0;
   const int64_t S = MAPS ? p.plan.S - 1 : p.plan.S;
-  const int64_t rows = p.B * p.D;
+  const int64_t rows = p.B * p.D, total = rows * p.L;
   int64_t unit = (int64_t)block_id() * UNITS + (W > 1 ? 0 : threadIdx.x / LN);
   if (unit >= rows * S) return;
   if (W > 1 || LN == 64) unit = __builtin_amdgcn_readfirstlane((int)unit);
@@ -58,23 +58,23 @@ __global__ __launch_bounds__(W > 4 ? W * 64 : 256, Z || LN == 16 ? 3 : 4) void r
     const int64_t s = tile * TURN + (w * LN + lane) * V, at = line.at(s);
     const int lo = line.lo(s), hi = line.hi(s);
     const bool edge = line.edge(tile * TURN, TURN);
-    rn = load_slots<IO, REV>(p.r, at, lo, hi, edge);
-    gn = load_slots<IO, REV>(p.dout, at, lo, hi, edge);
-    if (Z) zn = load_slots<IO, REV>(p.z, at, lo, hi, edge);
+    rn = load_slots<IO, REV>(p.r, at, lo, hi, edge, total);
+    gn = load_slots<IO, REV>(p.dout, at, lo, hi, edge, total);
+    if (Z) zn = load_slots<IO, REV>(p.z, at, lo, hi, edge, total);
     if (!MAPS) {
-      xn = load_slots<IO, REV>(p.x, at, lo, hi, edge);
-      in = load_slots<IO, REV>(p.i, at, lo, hi, edge);
-      const int64_t block = LN == 64 ? tile * W + w : 0;
+      xn = load_slots<IO, REV>(p.x, at, lo, hi, edge, total);
+      in = load_slots<IO, REV>(p.i, at, lo, hi, edge, total);
+      const int64_t block = tile * W + w;
       hn = p.ckpt[row * p.plan.blocks + (block < p.plan.blocks ? block : p.plan.blocks - 1)];
     }
   };
   float sd = 0.0f, sr = 0.0f, si = 0.0f;
-  float state = 0.0f;  // LN = 16: the state that enters the first tile; the others' by walking up first
+  float state = 0.0f;
   if (k0 < k1) load(k1 - 1);
   for (int64_t tile = k1 - 1; tile >= k0; --tile) {
     const u32x4a xq = xn, rq = rn, uq = in, zq = zn, gq = gn;
     state = hn;
-    if (tile > k0) load(tile - 1);
+    if (LN == 64 && tile > k0) load(tile - 1);
     const int64_t s = tile * TURN + (w * LN + lane) * V;
     const int lo = line.lo(s), hi = line.hi(s);
     const bool edge = line.edge(tile * TURN, TURN);
@@ -136,24 +136,6 @@ __global__ __launch_bounds__(W > 4 ? W * 64 : 256, Z || LN == 16 ? 3 : 4) void r
     if (MAPS) continue;
 
     // the states: hb before each step
-    if (LN == 16 && tile > 0) {  // up to here from the row's beginning (at most three turns of 16 pieces)
-      for (int64_t k = 0; k < tile; ++k) {
-        const int64_t sk = k * TURN + lane * V, at = line.at(sk);
-        const int lk = line.lo(sk), hk = line.hi(sk);
-        const u32x4a x0 = load_slots<IO, REV>(p.x, at, lk, hk, true), r0 = load_slots<IO, REV>(p.r, at, lk, hk, true);
-        const u32x4a i0 = load_slots<IO, REV>(p.i, at, lk, hk, true);
-        float UA = 1.0f, UB = 0.0f;
-#pragma unroll
-        for (int e = 0; e < V; ++e) {
-          if (e < lk || e >= hk) continue;
-          const Gates k(slot<IO, REV>(r0, e), slot<IO, REV>(i0, e), ch);
-          UA *= k.a;
-          UB = __builtin_fmaf(k.a, UB, k.q * k.si * slot<IO, REV>(x0, e));
-        }
-        scan_up<LN>(UA, UB);
-        state = __builtin_fmaf(end_lane<LN, true>(UA), state, end_lane<LN, true>(UB));
-      }
-    }
     scan_up<LN>(A, B);
     float h = __builtin_fmaf(lane_before<LN>(A, 1.0f), state, lane_before<LN>(B, 0.0f));
     const int64_t at = line.at(s);
@@ -196,6 +178,7 @@ __global__ __launch_bounds__(W > 4 ? W * 64 : 256, Z || LN == 16 ? 3 : 4) void r
     store_slots<IO, REV>(p.dx, at, lo, hi, edge, o);
     store_slots<IO, REV>(p.dr, at, lo, hi, edge, hb);
     store_slots<IO, REV>(p.di, at, lo, hi, edge, g);
+    if (LN < 64) break;  // (rows of fewer lanes are one turn)
   }
   if (MAPS) {
     if (lane == 0 && w == 0) {
@@ -205,9 +188,9 @@ __global__ __launch_bounds__(W > 4 ? W * 64 : 256, Z || LN == 16 ? 3 : 4) void r
     return;
   }
   if (p.dinit && seg == 0 && lane == 0 && w == 0) p.dinit[row] = carry;
-  sd = sum_lanes<LN>(sd);
-  sr = sum_lanes<LN>(sr);
-  si = sum_lanes<LN>(si);
+  sd = sum_group<LN>(sd);
+  sr = sum_group<LN>(sr);
+  si = sum_group<LN>(si);
   if (p.whole) {
     if constexpr (W > 1) {
       __shared__ float all[W][3];
@@ -273,8 +256,12 @@ namespace {
 template <typename IO, bool REV, bool Z>
 void go(const RecurParams& p, hipStream_t s) {
   const int64_t rows = p.B * p.D;
-  if (p.plan.lanes == 16) {
-    hipLaunchKernelGGL((recur_bwd_kernel<IO, 16, 1, REV, Z, false>), grid_of((rows + 15) / 16), dim3(256), 0, s, p);
+  auto few = [&](auto lanes) {
+    constexpr int LN = decltype(lanes)::value, ROWS = 256 / LN;
+    hipLaunchKernelGGL((recur_bwd_kernel<IO, LN, 1, REV, Z, false>), grid_of((rows + ROWS - 1) / ROWS), dim3(256), 0, s, p);
+  };
+  if (p.plan.lanes < 64) {
+    p.plan.lanes == 1 ? few(IC<1>()) : p.plan.lanes == 4 ? few(IC<4>()) : p.plan.lanes == 16 ? few(IC<16>()) : few(IC<32>());
   } else if (p.plan.waves == 1) {
     hipLaunchKernelGGL((recur_bwd_kernel<IO, 64, 1, REV, Z, false>), grid_of((rows + 3) / 4), dim3(256), 0, s, p);
   } else if (p.plan.waves == 8) {

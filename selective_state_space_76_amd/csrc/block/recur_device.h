@@ -23,9 +23,30 @@ __device__ __forceinline__ float lane_of(float v, int l) {
   return __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(v), l));
 }
 
+// Groups of LN = 1, 4, 16, 32 or 64 lanes.
+
+// the same of a lane of the quad, CTRL, or `other` where that lane is not of the group
+template <int CTRL>
+__device__ __forceinline__ float quad_or(float v, float other, bool has) {
+  const float q = __uint_as_float((uint32_t)__builtin_amdgcn_mov_dpp((int)__float_as_uint(v), CTRL, 0xf, 0xf, true));
+  return has ? q : other;
+}
+
 // The lane's map after those of the lanes before it.
 template <int LN>
 __device__ __forceinline__ void scan_up(float& A, float& B) {
+  if constexpr (LN == 1) return;
+  if constexpr (LN == 4) {
+    auto quad = [&](auto ctrl, int by) {
+      const bool has = (int)(threadIdx.x & 3) >= by;
+      const float a = quad_or<decltype(ctrl)::value>(A, 1.0f, has), b = quad_or<decltype(ctrl)::value>(B, 0.0f, has);
+      B = __builtin_fmaf(A, b, B);
+      A *= a;
+    };
+    quad(IC<0x90>{}, 1);  // [0,0,1,2]
+    quad(IC<0x40>{}, 2);  // [0,0,0,1]
+    return;
+  }
   auto step = [&](auto ctrl, auto rows) {
     const float a = dpp_or<decltype(ctrl)::value, decltype(rows)::value>(A, 1.0f);
     const float b = dpp_or<decltype(ctrl)::value, decltype(rows)::value>(B, 0.0f);
@@ -36,15 +57,25 @@ __device__ __forceinline__ void scan_up(float& A, float& B) {
   step(IC<0x112>{}, IC<0xf>{});
   step(IC<0x114>{}, IC<0xf>{});
   step(IC<0x118>{}, IC<0xf>{});
-  if constexpr (LN == 64) {
-    step(IC<0x142>{}, IC<0xa>{});  // row_bcast:15 into rows 1 and 3
-    step(IC<0x143>{}, IC<0xc>{});  // row_bcast:31 into rows 2 and 3
-  }
+  if constexpr (LN >= 32) step(IC<0x142>{}, IC<0xa>{});  // row_bcast:15 into rows 1 and 3
+  if constexpr (LN == 64) step(IC<0x143>{}, IC<0xc>{});  // row_bcast:31 into rows 2 and 3
 }
 
 // The lane's map after those of the lanes behind it.
 template <int LN>
 __device__ __forceinline__ void scan_down(float& A, float& B) {
+  if constexpr (LN == 1) return;
+  if constexpr (LN == 4) {
+    auto quad = [&](auto ctrl, int by) {
+      const bool has = (int)(threadIdx.x & 3) + by < 4;
+      const float a = quad_or<decltype(ctrl)::value>(A, 1.0f, has), b = quad_or<decltype(ctrl)::value>(B, 0.0f, has);
+      B = __builtin_fmaf(A, b, B);
+      A *= a;
+    };
+    quad(IC<0xf9>{}, 1);  // [1,2,3,3]
+    quad(IC<0xfe>{}, 2);  // [2,3,3,3]
+    return;
+  }
   auto step = [&](auto ctrl) {
     const float a = dpp_or<decltype(ctrl)::value, 0xf>(A, 1.0f);
     const float b = dpp_or<decltype(ctrl)::value, 0xf>(B, 0.0f);
@@ -55,7 +86,14 @@ __device__ __forceinline__ void scan_down(float& A, float& B) {
   step(IC<0x102>{});
   step(IC<0x104>{});
   step(IC<0x108>{});
-  if constexpr (LN == 64) {  // the rows behind: their first lanes hold their whole maps
+  if constexpr (LN == 32) {  // the row behind: its first lane holds its whole map
+    const float a3 = lane_of(A, 48), b3 = lane_of(B, 48), a1 = lane_of(A, 16), b1 = lane_of(B, 16);
+    const int row = (threadIdx.x & 63) >> 4;
+    const float a = row == 0 ? a1 : row == 2 ? a3 : 1.0f, b = row == 0 ? b1 : row == 2 ? b3 : 0.0f;
+    B = __builtin_fmaf(A, b, B);
+    A *= a;
+  }
+  if constexpr (LN == 64) {  // the rows behind
     const float a3 = lane_of(A, 48), b3 = lane_of(B, 48);
     const float a2 = lane_of(A, 32), b2 = lane_of(B, 32);
     const float a1 = lane_of(A, 16), b1 = lane_of(B, 16);
@@ -71,15 +109,46 @@ __device__ __forceinline__ void scan_down(float& A, float& B) {
 
 // the value of the lane before (behind) in the group of LN; the first (last) gets `end`
 template <int LN> __device__ __forceinline__ float lane_before(float v, float end) {
-  return dpp_or<LN == 64 ? 0x138 : 0x111, 0xf>(v, end);
+  if constexpr (LN == 1) return end;
+  else if constexpr (LN == 4) return quad_or<0x90>(v, end, threadIdx.x & 3);
+  else if constexpr (LN == 16) return dpp_or<0x111, 0xf>(v, end);
+  else {
+    const float q = dpp_or<0x138, 0xf>(v, end);
+    return LN == 64 || (threadIdx.x & 31) ? q : end;
+  }
 }
 template <int LN> __device__ __forceinline__ float lane_behind(float v, float end) {
-  return dpp_or<LN == 64 ? 0x130 : 0x101, 0xf>(v, end);
+  if constexpr (LN == 1) return end;
+  else if constexpr (LN == 4) return quad_or<0xf9>(v, end, (threadIdx.x & 3) < 3);
+  else if constexpr (LN == 16) return dpp_or<0x101, 0xf>(v, end);
+  else {
+    const float q = dpp_or<0x130, 0xf>(v, end);
+    return LN == 64 || (threadIdx.x & 31) < 31 ? q : end;
+  }
 }
 // the group's first or last lane's value, in all of its lanes
 template <int LN, bool LAST> __device__ __forceinline__ float end_lane(float v) {
-  if constexpr (LN == 64) return lane_of(v, LAST ? 63 : 0);
-  else return __uint_as_float((uint32_t)__builtin_amdgcn_mov_dpp((int)__float_as_uint(v), LAST ? 0x15f : 0x150, 0xf, 0xf, true));
+  if constexpr (LN == 1) return v;
+  else if constexpr (LN == 4) return quad_or<LAST ? 0xff : 0x00>(v, 0.0f, true);
+  else if constexpr (LN == 16) return __uint_as_float((uint32_t)__builtin_amdgcn_mov_dpp((int)__float_as_uint(v), LAST ? 0x15f : 0x150, 0xf, 0xf, true));
+  else if constexpr (LN == 32) {
+    const float a = lane_of(v, LAST ? 31 : 0), b = lane_of(v, LAST ? 63 : 32);
+    return threadIdx.x & 32 ? b : a;
+  }
+  else return lane_of(v, LAST ? 63 : 0);
+}
+// summed over the group, in its first lane
+template <int LN> __device__ __forceinline__ float sum_group(float v) {
+  if constexpr (LN == 1) return v;
+  else if constexpr (LN == 4) {
+    v += quad_or<0xb1>(v, 0.0f, true);
+    return v + quad_or<0x4e>(v, 0.0f, true);
+  }
+  else if constexpr (LN == 32) {
+    v = sum_lanes<16>(v);
+    return v + __shfl_xor(v, 16);
+  }
+  else return sum_lanes<LN>(v);
 }
 
 // ---------------------------------------------------------------- pieces
@@ -107,19 +176,32 @@ struct Row {
 };
 
 // 16 bytes of which the slots lo .. hi - 1 are read, the others zero.  edge: there are others in this turn of the team
-// (the same in all its lanes).
+// (the same in all its lanes).  What lies there belongs to the neighbouring rows, or to nothing behind the tensor's end
+// (total), and only there the elements are read one by one (8 x 1536 x 2047: 63 us, 78 with
+// every such piece read so; its gradients 120 and 157).
 template <typename IO, bool REV>
-__device__ __forceinline__ u32x4a load_slots(const void* p, int64_t at, int lo, int hi, bool edge) {
+__device__ __forceinline__ u32x4a load_slots(const void* p, int64_t at, int lo, int hi, bool edge, int64_t total) {
   constexpr int V = 16 / (int)sizeof(IO);
   const IO* q = static_cast<const IO*>(p) + at;
-  if (!edge || (lo == 0 && hi == V)) return __builtin_nontemporal_load(reinterpret_cast<const u32x4a*>(q));
+  if (!edge) return __builtin_nontemporal_load(reinterpret_cast<const u32x4a*>(q));
   u32x4a w = {0u, 0u, 0u, 0u};
+  if (lo >= hi) return w;
+  const int first = REV ? V - hi : lo, last = REV ? V - lo : hi;  // in the order of memory
+  if (at + V <= total) {
+    w = *reinterpret_cast<const u32x4a*>(q);
 #pragma unroll
-  for (int k = 0; k < V; ++k) {
-    const int s = REV ? V - 1 - k : k;
-    if (s >= lo && s < hi) {
-      if constexpr (V == 8) w[k >> 1] |= (uint32_t)q[k] << (16 * (k & 1));
-      else w[k] = __float_as_uint(q[k]);
+    for (int k = 0; k < 4; ++k) {
+      if constexpr (V == 8)
+        w[k] &= (2 * k >= first && 2 * k < last ? 0xffffu : 0u) | (2 * k + 1 >= first && 2 * k + 1 < last ? 0xffff0000u : 0u);
+      else w[k] = k >= first && k < last ? w[k] : 0u;
+    }
+  } else {
+#pragma unroll
+    for (int k = 0; k < V; ++k) {
+      if (k >= first && k < last) {
+        if constexpr (V == 8) w[k >> 1] |= (uint32_t)q[k] << (16 * (k & 1));
+        else w[k] = __float_as_uint(q[k]);
+      }
     }
   }
   return w;

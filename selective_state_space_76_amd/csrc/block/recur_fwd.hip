@@ -52,7 +52,7 @@ __global__ __launch_bounds__(W > 4 ? W * 64 : 256) void recur_fwd_kernel(RecurPa
   __shared__ float sm[2][W][2];
   const int lane = threadIdx.x % LN, w = W > 1 ? __builtin_amdgcn_readfirstlane(threadIdx.x / 64) : 0;
   const int64_t S = MAPS ? p.plan.S - 1 : p.plan.S;
-  const int64_t rows = p.B * p.D;
+  const int64_t rows = p.B * p.D, total = rows * p.L;
   int64_t unit = (int64_t)block_id() * UNITS + (W > 1 ? 0 : threadIdx.x / LN);
   const bool live = unit < rows * S;
   if (W > 1 || LN == 64) {
@@ -88,15 +88,15 @@ __global__ __launch_bounds__(W > 4 ? W * 64 : 256) void recur_fwd_kernel(RecurPa
     const int64_t s = tile * TURN + (w * LN + lane) * V, at = line.at(s);
     const int lo = line.lo(s), hi = line.hi(s);
     const bool edge = line.edge(tile * TURN, TURN);
-    xn = load_slots<IO, REV>(p.x, at, lo, hi, edge);
-    rn = load_slots<IO, REV>(p.r, at, lo, hi, edge);
-    in = load_slots<IO, REV>(p.i, at, lo, hi, edge);
-    if (gate) zn = load_slots<IO, REV>(p.z, at, lo, hi, edge);
+    xn = load_slots<IO, REV>(p.x, at, lo, hi, edge, total);
+    rn = load_slots<IO, REV>(p.r, at, lo, hi, edge, total);
+    in = load_slots<IO, REV>(p.i, at, lo, hi, edge, total);
+    if (gate) zn = load_slots<IO, REV>(p.z, at, lo, hi, edge, total);
   };
   if (k0 < k1) load(k0);
   for (int64_t tile = k0; tile < k1; ++tile) {
     const u32x4a xq = xn, rq = rn, iq = in, zq = zn;
-    if (tile + 1 < k1) load(tile + 1);
+    if (LN == 64 && tile + 1 < k1) load(tile + 1);
     const int64_t s = tile * TURN + (w * LN + lane) * V;
     const int lo = line.lo(s), hi = line.hi(s);
     const bool edge = line.edge(tile * TURN, TURN);
@@ -142,8 +142,8 @@ __global__ __launch_bounds__(W > 4 ? W * 64 : 256) void recur_fwd_kernel(RecurPa
       continue;
     }
     const float enter = enter_up<LN, W>(A, B, carry, sm[tile & 1], w);
-    const int64_t block = LN == 64 ? tile * W + w : tile;
-    if (p.ckpt && lane == 0 && block < p.plan.blocks && (LN == 64 || tile == 0)) p.ckpt[row * p.plan.blocks + block] = enter;
+    const int64_t block = tile * W + w;
+    if (p.ckpt && lane == 0 && block < p.plan.blocks) p.ckpt[row * p.plan.blocks + block] = enter;
     if (!p.out) continue;
     float h = __builtin_fmaf(A, enter, B), o[V];
 #pragma unroll
@@ -152,6 +152,7 @@ __global__ __launch_bounds__(W > 4 ? W * 64 : 256) void recur_fwd_kernel(RecurPa
       o[e] = Z ? h * silu_(slot<IO, REV>(zq, e)) : h;
     }
     store_slots<IO, REV>(p.out, line.at(s), lo, hi, edge, o);
+    if (LN < 64) break;  // (rows of fewer lanes are one turn)
   }
   if (MAPS) {
     if (lane == 0 && w == 0) {
@@ -207,21 +208,23 @@ __global__ __launch_bounds__(256) void recur_step_kernel(RecurStepParams p) {
   store_n<IO, 4>(static_cast<IO*>(p.out) + at, n, o);
 }
 
-// Short rows (up to two pieces a lane of 16) take 16 lanes each, longer ones a wave: a row at a time costs least where
-// there are rows for every SIMD (8 x 1536 x 2048: 57 us, 77 with four waves a row).  Fewer rows take four or eight waves
-// each, if they are long enough for several turns (1 x 2048 x 65536: 264 us, 248 with four, 228 with eight; 2 x 1536 x
-// 8192: 54, 63, 83) or there is no other way to fill the card; and where that is still too few, segments, up to 64
-// (a lane each for their maps), of two turns and more.
+// Short rows take the 1, 4, 16 or 32 lanes that hold all of their pieces (256 x 2560 x 8 in bf16: 15 us, 214 with 16
+// lanes; 64 x 1536 x 256: 62, 77 with 16 lanes twice), longer ones a wave: a row at a time costs least where there are rows
+// for every SIMD (8 x 1536 x 2048: 57 us, 77 with four waves a row).  Fewer rows take four or eight waves each, if they are
+// long enough for several turns (1 x 2048 x 65536: 264 us, 248 with four, 228 with eight; 2 x 1536 x 8192: 54, 63, 83)
+// or there is no other way to fill the card; and where that is still too few, segments, up to 64 (a lane each for their
+// maps), of two turns and more.
 RecurPlan recur_plan(int64_t B, int64_t D, int64_t L, bool bf16) {
   const int64_t V = bf16 ? 8 : 4, rows = B * D;
   RecurPlan pl;
   pl.blocks = (L + V - 1 + 64 * V - 1) / (64 * V);
-  if (L <= 32 * V) pl.lanes = 16;
+  const int64_t most = L % V ? (L + 2 * V - 2) / V : L / V;  // pieces of a row that begins anywhere
+  if (most <= 32) pl.lanes = most <= 1 ? 1 : most <= 4 ? 4 : most <= 16 ? 16 : 32;
   else if (rows < 256) pl.waves = pl.blocks >= 4 ? 4 : 1;
   else if ((rows < 1024 && pl.blocks >= 8) || (rows <= 2048 && pl.blocks >= 64)) pl.waves = 8;
   else if ((rows < 2048 && pl.blocks >= 4) || (rows < 4096 && pl.blocks >= 32)) pl.waves = 4;
   const int64_t turn = pl.lanes * pl.waves * V;
-  pl.tiles = (L + V - 1 + turn - 1) / turn;
+  pl.tiles = pl.lanes < 64 ? 1 : (L + V - 1 + turn - 1) / turn;
   pl.per = pl.tiles;
   if (pl.waves == 4 && rows < 256) {
     int64_t S = (1023 + rows) / rows;
@@ -240,8 +243,12 @@ namespace {
 template <typename IO, bool REV, bool Z>
 void go(const RecurParams& p, hipStream_t s) {
   const int64_t rows = p.B * p.D;
-  if (p.plan.lanes == 16) {
-    hipLaunchKernelGGL((recur_fwd_kernel<IO, 16, 1, REV, Z, false>), grid_of((rows + 15) / 16), dim3(256), 0, s, p);
+  auto few = [&](auto lanes) {
+    constexpr int LN = decltype(lanes)::value, ROWS = 256 / LN;
+    hipLaunchKernelGGL((recur_fwd_kernel<IO, LN, 1, REV, Z, false>), grid_of((rows + ROWS - 1) / ROWS), dim3(256), 0, s, p);
+  };
+  if (p.plan.lanes < 64) {
+    p.plan.lanes == 1 ? few(IC<1>()) : p.plan.lanes == 4 ? few(IC<4>()) : p.plan.lanes == 16 ? few(IC<16>()) : few(IC<32>());
   } else if (p.plan.waves == 1) {
     hipLaunchKernelGGL((recur_fwd_kernel<IO, 64, 1, REV, Z, false>), grid_of((rows + 3) / 4), dim3(256), 0, s, p);
   } else if (p.plan.waves == 8) {

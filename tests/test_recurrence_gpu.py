@@ -120,6 +120,43 @@ def test_batches(dtype, B, L):
     same(g, check_bwd(i, None, B % 3 == 0))
 
 
+SHORT = [(3, 700, 8), (5, 300, 1), (3, 333, 13), (2, 600, 30), (3, 100, 200), (4, 90, 32), (2, 130, 255), (2, 300, 4)]
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("reverse", [False, True], ids=["forward", "reverse"])
+@pytest.mark.parametrize("B,D,L", SHORT)
+def test_short_rows(dtype, reverse, B, D, L):
+    """Several rows to a wave, of 1, 4, 16 and 32 lanes."""
+    print("case: recurrence short rows", dtype, reverse, B, D, L, flush=True)
+    i = make(B, D, L, dtype, seed=B + D + L, gate=D % 4 != 0)
+    _, _, ck = check_fwd(i, reverse)
+    g = check_bwd(i, ck, reverse)
+    same(g, check_bwd(i, None, reverse))
+
+
+@pytest.mark.parametrize("reverse", [False, True], ids=["forward", "reverse"])
+@pytest.mark.parametrize("L", [3, 8, 9, 27, 101, 255, 700])
+def test_nan_stays_in_its_row_where_rows_share_pieces(reverse, L):
+    print("case: recurrence, a row of NaN", reverse, L, flush=True)
+    i = make(2, 9, L, BF16, seed=L)
+    sick = {k: None if v is None else v.clone() for k, v in i.items()}
+    for k in ("x", "r", "i", "z", "dout"):
+        sick[k][1, 4] = float("nan")
+    got = []
+    for case in (i, sick):
+        d = gpu(case)
+        ck = torch.zeros(recurrence_checkpoints_shape(2, 9, L, 1), device=DEV)
+        out, last = recurrence_fwd(*[d[k] for k in ARGS], reverse=reverse, checkpoints=ck)
+        g = recurrence_bwd(*[d[k] for k in ARGS], dout=d["dout"], dfinal_state=d["dlast"], reverse=reverse, checkpoints=ck)
+        got.append([out, last, g["dx"], g["dr"], g["di"], g["dz"], g["dinitial_state"], g["ddecay"], g["dr_bias"], g["di_bias"]])
+    torch.cuda.synchronize()
+    for a, b in zip(*got):
+        keep = torch.ones(a.shape[:2] if a.dim() > 1 else a.shape, dtype=torch.bool, device=DEV)
+        keep[(1, 4) if a.dim() > 1 else 4] = False
+        assert torch.equal(a[keep], b[keep]) and bool(torch.isnan(b[~keep]).any())
+
+
 def test_the_variants_are_all_reached():
     """By the sizes of the tests above: segments (a workspace), none."""
     assert recurrence_workspace_size(1, 3, 9001) and recurrence_workspace_size(2, 7, 12345, 0)
