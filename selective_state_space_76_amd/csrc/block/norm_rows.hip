@@ -35,7 +35,7 @@ int team_of(int64_t E, int each = 1) {
   return lanes <= 1024 ? (int)lanes : 0;
 }
 constexpr int64_t kTwo = 4096;  // elements from which on a lane holds two pieces (forward)
-constexpr int kLong = 256;      // lanes of a row that no team holds
+constexpr int kLong = 1024;     // lanes of a row that no team holds (16 x 200000: 84 us, 250 with 256)
 
 // (a, b) summed over the team's lanes, in all of them; TEAM 0: the workgroup; sm: two floats for each of 16 waves
 template <int TEAM>
@@ -422,21 +422,22 @@ __global__ __launch_bounds__(256) void norm_sums_kernel(NormParams p) {
   p.part[first * 2 * p.E + p.E + e] = db;
 }
 
-// dw and db from the partial sums: 16 columns per workgroup, the partial sums split over 64 groups of lanes, each in
-// order, then the groups' sums in order (1366 sums of 768 columns: 6.5 us).  Every `step`th
+// dw and db from the partial sums: COLS columns per workgroup, the partial sums split over 1024 / COLS groups of lanes, each
+// in order, then the groups' sums in order (1366 sums of 768 columns, 16 at a time: 6 us).  Every `step`th
 // of them, `many` to a workgroup, which leaves their sum in the place of the first; the last call's single one writes dw
 // and db.
+template <int COLS>
 __global__ __launch_bounds__(1024) void norm_join_kernel(NormParams p, int64_t step, int64_t many) {
   __shared__ float sm[1024], sn[256];
-  const int64_t cols = (p.E + 15) / 16, n = (p.blocks + step - 1) / step;
+  const int64_t cols = (p.E + COLS - 1) / COLS, n = (p.blocks + step - 1) / step;
   const int64_t count = 2 * cols * ((n + many - 1) / many);
   if (block_id() >= count) return;
   const int64_t blk = xcd_remap((int)block_id(), (int)count);  // (neighbours read the same lines)
   const int64_t which = blk / cols % 2, first = blk / (2 * cols) * many;
   const int64_t here = n - first < many ? n - first : many;
-  const int64_t c = blk % cols * 16 + (threadIdx.x & 15);
-  const int64_t per = (here + 63) / 64, row = step * 2 * p.E;
-  const int64_t k0 = (threadIdx.x >> 4) * per, k1 = k0 + per < here ? k0 + per : here;
+  const int64_t c = blk % cols * COLS + threadIdx.x % COLS;
+  const int64_t per = (here + 1024 / COLS - 1) / (1024 / COLS), row = step * 2 * p.E;
+  const int64_t k0 = threadIdx.x / COLS * per, k1 = k0 + per < here ? k0 + per : here;
   float* q = p.part + first * row + which * p.E + c;
   float s = 0.0f;
   if (c < p.E) {
@@ -451,15 +452,15 @@ __global__ __launch_bounds__(1024) void norm_join_kernel(NormParams p, int64_t s
   sm[threadIdx.x] = s;
   __syncthreads();
   if (threadIdx.x < 256) {
-    const int at = (threadIdx.x >> 4) * 64 + (threadIdx.x & 15);
-    sn[threadIdx.x] = (sm[at] + sm[at + 16]) + (sm[at + 32] + sm[at + 48]);
+    const int at = threadIdx.x / COLS * 4 * COLS + threadIdx.x % COLS;
+    sn[threadIdx.x] = (sm[at] + sm[at + COLS]) + (sm[at + 2 * COLS] + sm[at + 3 * COLS]);
   }
   __syncthreads();
   float* out = many < n ? q : which ? p.dbias : p.dweight;
-  if (threadIdx.x < 16 && c < p.E && out) {
+  if (threadIdx.x < COLS && c < p.E && out) {
     s = 0.0f;
 #pragma unroll
-    for (int t = 0; t < 16; ++t) s += sn[t * 16 + threadIdx.x];
+    for (int t = 0; t < 256 / COLS; ++t) s += sn[t * COLS + threadIdx.x];
     out[many < n ? 0 : c] = s;
   }
 }
@@ -548,7 +549,11 @@ hipError_t launch_norm_join(const NormParams& p, hipStream_t s) {
   for (int64_t n = p.blocks, step = 1, many; n; step *= many) {
     many = n <= 4096 ? n : 512;
     const int64_t groups = (n + many - 1) / many;
-    hipLaunchKernelGGL(norm_join_kernel, grid_of((p.E + 15) / 16 * 2 * groups), dim3(1024), 0, s, p, step, many);
+    if (many <= 64)  // (of few sums 256 columns leave no lane without one: 64 x 100000, gradients: 83
+    // us, 153 with 16)
+      hipLaunchKernelGGL(norm_join_kernel<256>, grid_of((p.E + 255) / 256 * 2 * groups), dim3(1024), 0, s, p, step, many);
+    else
+      hipLaunchKernelGGL(norm_join_kernel<16>, grid_of((p.E + 15) / 16 * 2 * groups), dim3(1024), 0, s, p, step, many);
     n = groups > 1 ? groups : 0;
   }
   return hipGetLastError();
