@@ -10,7 +10,7 @@
 // other's; the adjoint F is an affine recurrence against time, walked as the forward pass walks the states (teams of
 // waves through LDS, segments for few rows).  ddecay and the biases' gradients are summed per wave and joined by a
 // second kernel in a fixed order, or at once where a channel is one team's (1 x 509 x 262147: 401 -> 391 us).
-// 8 x 1536 x 2048: 100 us a call, 18 bytes a step, 4.5 TB/s; workgroups of 8 waves instead of 4 take 112, and 123 where
+// 8 x 1536 x 2048: 98 us a call, 18 bytes a step, 4.6 TB/s; workgroups of 8 waves instead of 4 take 112, and 123 where
 // they are the rows of a channel, whose sums then need no second kernel.
 #include "recur_device.h"
 

@@ -7,7 +7,7 @@
 // the present one's arithmetic.  Where there are too few rows even for that, a row is cut into S segments and the first
 // launch makes each segment's map (reading x, r and i once more).
 //
-// 8 x 1536 x 2048 in bf16 with a gate, a wave a row: 57 us a call, 4.5 TB/s; 1 x 1024 x 2^20, 8
+// 8 x 1536 x 2048 in bf16 with a gate, a wave a row: 56 us a call, 4.5 TB/s; 1 x 1024 x 2^20, 8
 // waves a row: 1.75 ms, 4.9 TB/s.
 #include "recur_device.h"
 
