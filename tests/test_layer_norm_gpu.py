@@ -346,3 +346,21 @@ def test_more_than_2_31_elements(cf):
     ref = np.where(keep.reshape(n, 64), ds, 0) * f
     scale = f64(stats[1, -n:])[:, None] * 4 * (np.abs(rows * f64(w)) + np.abs(rows) * 5)
     assert (np.abs(dx - ref) <= half(BF16) * np.abs(ref) + 200 * U * scale).all()
+
+
+def test_gradients_of_2_30_columns():
+    """A row of all the elements that a row may have: the join of the sums takes 2^32 threads and more."""
+    print("case: norm gradients of 2^30 columns", flush=True)
+    E, g = 1 << 30, torch.Generator(device=DEV).manual_seed(6)
+    d, h = (torch.empty(1, E, dtype=BF16, device=DEV).normal_(generator=g) for _ in range(2))
+    w = torch.ones(E, device=DEV)
+    stats = torch.tensor([[0.25], [0.5]], device=DEV)
+    got = layer_norm_bwd(d, h, w, stats)
+    torch.cuda.synchronize()
+    for lo in (0, (1 << 29) - 50, E - 100):
+        s = slice(lo, lo + 100)
+        dd, hh = f64(d[0, s]), f64(h[0, s])
+        want = dd * (hh - 0.25) * 0.5
+        assert np.array_equal(f64(got["dbias"][s]), dd)
+        # a difference, a product with 1/2 (exact), a product
+        assert (np.abs(f64(got["dweight"][s]) - want) <= 3 * U * (np.abs(dd) * (np.abs(hh) + 0.25))).all()
