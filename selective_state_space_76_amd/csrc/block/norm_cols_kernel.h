@@ -679,7 +679,8 @@ void go(const NormParams& p, hipStream_t s) {
 // Everything read again for each pass.
 template <typename XT, typename HT, bool RES, bool DROP, bool ODD>
 void again(const NormParams& p, bool wide, hipStream_t s) {
-  wide && p.L >= 256 ? go<XT, HT, RES, DROP, ODD, 512, 32, 2, false>(p, s) : go<XT, HT, RES, DROP, ODD, 512, 8, 2, false>(p, s);
+  wide && p.L >= 256 ? go<XT, HT, RES, DROP, ODD, 512, 32, 2, false>(p, s)
+                     : go<XT, HT, RES, DROP, ODD, 512, 8, 2, false>(p, s);
 }
 
 // With a residual, channels that do not fit the registers: x alone does (4 x 4096 positions x 2048 channels in bf16: 75

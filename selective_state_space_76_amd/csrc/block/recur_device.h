@@ -25,7 +25,7 @@ __device__ __forceinline__ float lane_of(float v, int l) {
 
 // Groups of LN = 1, 4, 16, 32 or 64 lanes.
 
-// the same of a lane of the quad, CTRL, or `other` where that lane is not of the group
+// the value of the lane that CTRL names, or `other` where that lane is not of the group
 template <int CTRL>
 __device__ __forceinline__ float quad_or(float v, float other, bool has) {
   const float q = __uint_as_float((uint32_t)__builtin_amdgcn_mov_dpp((int)__float_as_uint(v), CTRL, 0xf, 0xf, true));
@@ -130,7 +130,7 @@ template <int LN> __device__ __forceinline__ float lane_behind(float v, float en
 template <int LN, bool LAST> __device__ __forceinline__ float end_lane(float v) {
   if constexpr (LN == 1) return v;
   else if constexpr (LN == 4) return quad_or<LAST ? 0xff : 0x00>(v, 0.0f, true);
-  else if constexpr (LN == 16) return __uint_as_float((uint32_t)__builtin_amdgcn_mov_dpp((int)__float_as_uint(v), LAST ? 0x15f : 0x150, 0xf, 0xf, true));
+  else if constexpr (LN == 16) return quad_or<LAST ? 0x15f : 0x150>(v, 0.0f, true);  // (row_newbcast)
   else if constexpr (LN == 32) {
     const float a = lane_of(v, LAST ? 31 : 0), b = lane_of(v, LAST ? 63 : 32);
     return threadIdx.x & 32 ? b : a;
