@@ -170,7 +170,8 @@ __global__ __launch_bounds__(TEAM ? 256 : 1024) void norm_rows_kernel(NormParams
   }
 }
 
-// A row of any length by a workgroup, 8 elements a lane at a time, read again for every pass
+// A row of any length by a workgroup, 8 elements a lane at a time, read again for every pass.  A lane's share is up to 2^20
+// elements: each piece is summed by itself, the pieces' sums are compensated (constant rows of 2^24: (s - m) r was 0.06).
 template <typename XT, typename HT>
 __global__ __launch_bounds__(kLong) void norm_long_kernel(NormParams p) {
   __shared__ float sm[2][16][2];
@@ -179,7 +180,8 @@ __global__ __launch_bounds__(kLong) void norm_long_kernel(NormParams p) {
   const XT* x = static_cast<const XT*>(p.x) + base;
   const HT* res = p.residual ? static_cast<const HT*>(p.residual) + base : nullptr;
   const Drop drop(p.drop);
-  float s[8], m = 0.0f, v = 0.0f;
+  float s[8];
+  LongSum sum, squares;
   auto take = [&](int64_t e, const Part& n) {
     Piece<XT> a;
     Piece<HT> b;
@@ -206,20 +208,21 @@ __global__ __launch_bounds__(kLong) void norm_long_kernel(NormParams p) {
     const Part n(e, E);
     take(e, n);
     if (p.hidden) store_part(static_cast<HT*>(p.hidden) + base + e, n, s);
-#pragma unroll
-    for (int k = 0; k < 8; ++k) m += s[k];
+    sum.add(((s[0] + s[1]) + (s[2] + s[3])) + ((s[4] + s[5]) + (s[6] + s[7])));
   }
-  m = p.rms ? 0.0f : sum_team<0>(m, sm[0]) * p.inv_e;
+  const float m = p.rms ? 0.0f : sum_team<0>(sum.value(), sm[0]) * p.inv_e;
   for (int64_t e = e0; e < E; e += kLong * 8) {
     const Part n(e, E);
     take(e, n);
+    float v = 0.0f;
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
       const float d = n.has(k) ? s[k] - m : 0.0f;
       v = __builtin_fmaf(d, d, v);
     }
+    squares.add(v);
   }
-  const float r = 1.0f / sqrtf(sum_team<0>(v, sm[1]) * p.inv_e + p.eps);
+  const float r = 1.0f / sqrtf(sum_team<0>(squares.value(), sm[1]) * p.inv_e + p.eps);
   for (int64_t e = e0; e < E; e += kLong * 8) {
     const Part n(e, E);
     take(e, n);
@@ -379,16 +382,20 @@ __global__ __launch_bounds__(kLong) void norm_long_bwd_kernel(NormParams p) {
       g[k] *= a.at(k);
     }
   };
-  float c1 = 0.0f, c2 = 0.0f;
+  LongSum s1, s2;
   for (int64_t e = threadIdx.x * 8; e < E; e += kLong * 8) {
     const Part n(e, E);
     take(e, n);
+    float a = 0.0f, b = 0.0f;
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
-      c1 += g[k];
-      c2 = n.has(k) ? __builtin_fmaf(g[k], h[k], c2) : c2;
+      a += g[k];
+      b = n.has(k) ? __builtin_fmaf(g[k], h[k], b) : b;
     }
+    s1.add(a);
+    s2.add(b);
   }
+  float c1 = s1.value(), c2 = s2.value();
   sum_team<0>(c1, c2, sm);
   c1 = p.rms ? 0.0f : c1 * p.inv_e;
   c2 *= p.inv_e;

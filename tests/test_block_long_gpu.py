@@ -1,0 +1,118 @@
+"""Sums of very many terms in the residual block's operators (GPU): rows of millions of elements, gradients over millions
+of rows.  What an addition rounds away must not add up with the number of terms, which it does where all have one sign.
+
+Tolerances.  u = 2^-24.  A compensated sum is off by 2 u of the sum of magnitudes, whatever their number; its terms here
+are sums of up to 128 numbers (128 u; of squares or products 129 u), lanes and waves or tiles are 20 more additions.  N u
+times the sum of magnitudes with N = 160, then.  The mean takes two more roundings."""
+import pytest
+import torch
+
+from selective_state_space_76_amd import layer_norm_bwd, layer_norm_fwd
+from tests import block_ref as R
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+F32, BF16 = torch.float32, torch.bfloat16
+U, N = R.U, 160
+TYPES = [(F32, F32), (BF16, BF16), (BF16, F32)]
+IDS = ["f32", "bf16", "bf16-f32"]
+
+
+def half(dtype):
+    return torch.finfo(dtype).eps / 2 if dtype != F32 else U
+
+
+def rows64(t, cf):
+    """[rows, E] in 64 bits, on the device."""
+    return (t.transpose(1, 2).reshape(-1, t.shape[1]) if cf else t.reshape(-1, t.shape[-1])).double()
+
+
+def worst(got, want, lim):
+    return float(((got - want).abs() / (lim + 1e-37)).max())
+
+
+def values(kind, shape, xt, seed, cf):
+    """One value everywhere; numbers far from zero; a row whose level changes half way."""
+    g = torch.Generator(device=DEV).manual_seed(seed)
+    if kind == "constant":
+        return torch.full(shape, 1.1, dtype=xt, device=DEV)
+    x = torch.empty(shape, dtype=F32, device=DEV).normal_(generator=g)
+    if kind == "far":
+        return x.add_(50).to(xt)
+    E = shape[1] if cf else shape[-1]
+    half_way = x[:, E // 2:] if cf else x[..., E // 2:]
+    half_way.add_(0.25)
+    return x.add_(1).to(xt)
+
+
+def check_fwd(x, rms, cf, eps=1e-5):
+    """(over channels: the first and the last batch row)."""
+    out, _, stats = layer_norm_fwd(x, rms=rms, channels_first=cf, eps=eps)
+    if cf and x.shape[0] > 2:
+        stats = stats.view(2, x.shape[0], -1)[:, [0, -1]].flatten(1)
+        x, out = x[[0, -1]], out[[0, -1]]
+    s = rows64(x, cf)
+    m = torch.zeros_like(s[:, 0]) if rms else s.mean(1)
+    mag = s.abs().mean(1)
+    em = (0 if rms else N + 2) * U * mag
+    d = s - m[:, None]
+    var = d.square().mean(1)
+    f = (var + eps).rsqrt()
+    ev = 2 * (em * d.abs().mean(1)) + em ** 2 + (N + 6) * U * var
+    ef = (ev / (2 * (var + eps)) + 4 * U) * f
+    assert worst(stats[0].double(), m, em + U * m.abs()) <= 1 and worst(stats[1].double(), f, ef + U * f) <= 1
+    want = d * f[:, None]
+    lim = (em[:, None] + U * d.abs()) * f[:, None] + d.abs() * ef[:, None] + (4 * U + half(x.dtype) * (1 + 2 ** -6)) * want.abs()
+    got = rows64(out, cf)
+    assert worst(got, want, lim) <= 1, worst(got, want, lim)
+
+
+def check_bwd(dout, hidden, rms, cf):
+    """The factors and means that go in are near those of hidden, not equal to them."""
+    rows = hidden.numel() // hidden.shape[1 if cf else -1]
+    stats = torch.tensor([0.0 if rms else 1.125, 0.9], device=DEV)[:, None].repeat(1, rows)
+    got = layer_norm_bwd(dout, hidden, None, stats, rms=rms, channels_first=cf, bias=False,
+                         residual=hidden.dtype != dout.dtype)["dx"]
+    if cf and dout.shape[0] > 2:
+        dout, hidden, got = (t[[0, -1]] for t in (dout, hidden, got))
+    s = rows64(hidden, cf)
+    m, f = stats[:, :s.shape[0]].double()
+    g = rows64(dout, cf)
+    xh = (s - m[:, None]) * f[:, None]
+    exh = 2 * U * xh.abs() + U * (s.abs() + m.abs()[:, None]) * f[:, None]
+    c1 = 0.0 * m[:, None] if rms else g.mean(1, keepdim=True)
+    c2 = (g * xh).mean(1, keepdim=True)
+    want = f[:, None] * (g - c1 - xh * c2)
+    a1 = 0.0 if rms else g.abs().mean(1, keepdim=True)
+    a2 = (g * xh).abs().mean(1, keepdim=True)
+    lim = f[:, None] * ((N + 3) * U * a1 + xh.abs() * ((N + 4) * U * a2 + (g.abs() * exh).mean(1, keepdim=True)) + exh * a2
+                        + 4 * U * (g.abs() + a1 + xh.abs() * a2)) + (U + half(dout.dtype) * (1 + 2 ** -6)) * want.abs()
+    assert worst(rows64(got, cf), want, lim) <= 1, worst(rows64(got, cf), want, lim)
+
+
+@pytest.mark.parametrize("rms", [False, True], ids=["layer", "rms"])
+@pytest.mark.parametrize("kind", ["constant", "far", "two levels"])
+@pytest.mark.parametrize("E", [1 << 20, (1 << 24) + 5])
+def test_very_long_rows(E, kind, rms):
+    for types in TYPES[:2]:
+        print("case: very long rows", E, kind, rms, types, flush=True)
+        check_fwd(values(kind, (2, E), types[0], E + rms, False), rms, False)
+
+
+@pytest.mark.parametrize("rms", [False, True], ids=["layer", "rms"])
+@pytest.mark.parametrize("E", [1 << 20, (1 << 24) + 5])
+def test_gradients_of_very_long_rows(E, rms):
+    for xt, ht in TYPES:
+        for kind in ("constant", "two levels"):
+            print("case: gradients of very long rows", E, kind, rms, xt, ht, flush=True)
+            check_bwd(values(kind, (2, E), xt, E + 1, False), values("two levels", (2, E), ht, E + 2, False), rms, False)
+
+
+@pytest.mark.parametrize("shape,cf", [((2, 40001), False)])
+def test_an_infinite_sum_stays_infinite(shape, cf):
+    """The factor is then zero, and so is what is finite in that row, as in short ones."""
+    x = torch.ones(shape, device=DEV)
+    (x[0, 11] if cf else x[0])[7] = float("inf")
+    out, _, stats = layer_norm_fwd(x, rms=True, channels_first=cf)
+    rows, k = rows64(out, cf), 7 if cf else 0
+    assert stats[1, k] == 0 and stats[1, k - 1] > 0.9 and torch.isnan(rows[k]).sum() == 1 and rows[k].nansum() == 0
