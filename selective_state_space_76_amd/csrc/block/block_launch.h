@@ -66,6 +66,9 @@ int64_t norm_rows_bwd_blocks(int64_t rows, int64_t E);
 inline bool norm_cols_narrow(int64_t B, int64_t E, int64_t L) {
   return B * ((L + 63) / 64) < 128 || (L <= 32 && E >= 256);
 }
+// With more channels than these, tiles of 16 or 64 positions whose lanes add up blocks of 128 channels (a lane has up to
+// 2^24 of them); with as many, a lane's share is 1024 at the most.
+constexpr int64_t kManyChannels = 16384;
 // The backward pass there: a workgroup and a partial sum of dw and db for each tile.
 // Channels up to which a tile of 64 positions keeps dout between its two passes, as far as 128 registers go.
 constexpr int norm_cols_bwd_kept(bool x16, bool h16, bool rms) {
@@ -82,6 +85,7 @@ struct NormTile {
 inline NormTile norm_cols_bwd_tile(int64_t B, int64_t E, int64_t L, int kind, bool rms) {
   auto tiles = [&](int64_t T) { return B * ((L + T - 1) / T); };
   if (norm_cols_narrow(B, E, L)) return {16, false};
+  if (E > kManyChannels) return {64, false};
   if (L % 8) return {L >= 128 && tiles(128) >= 256 ? 128 : 64, false};
   if (E >= 128 && E <= norm_cols_bwd_kept(kind & 1, kind & 2, rms)) return {64, true};
   return {L >= 256 && tiles(256) >= 512 ? 256 : L >= 128 && tiles(128) >= 256 ? 128 : 64, false};

@@ -109,6 +109,9 @@ __device__ __forceinline__ void store_cols(IO* p, int n, const float (&x)[8], bo
 
 }  // namespace
 
+// Of very many channels, the turns whose sums are taken by themselves and then compensated.
+constexpr int kBlock = 64;
+
 // On this architecture a wave that waits for a load waits for the stores that it issued before, too.  So nothing is
 // loaded behind a store that it does not follow from: weights come with the pieces, and where pieces are read again, the
 // next ones are asked for before the present ones are stored.
@@ -122,8 +125,8 @@ struct Chunk {
 };
 
 // RES: there is a residual.  DROP: there is dropout (not with KEEP: the masks of all channels at once would take more
-// registers than there are).  ODD: L is no multiple of 8.
-template <typename XT, typename HT, bool RES, bool DROP, bool ODD, int NT, int LP, int C, bool KEEP>
+// registers than there are).  ODD: L is no multiple of 8.  MANY: more than kManyChannels, not with KEEP.
+template <typename XT, typename HT, bool RES, bool DROP, bool ODD, int NT, int LP, int C, bool KEEP, bool MANY>
 __global__ __launch_bounds__(NT) void norm_cols_kernel(NormParams p) {
   constexpr int NG = NT / LP, T = LP * 8;
   constexpr bool SHARED = ODD || LP < 8;  // neighbouring tiles share lines
@@ -251,8 +254,22 @@ __global__ __launch_bounds__(NT) void norm_cols_kernel(NormParams p) {
     });
   } else {
     // One pass: the lane's own mean and its squares about that, kept up to date channel by channel; the lanes' means
-    // then differ from the whole mean by what is added to the squares.
-    float mine[8], count = 0.0f;
+    // then differ from the whole mean by what is added to the squares.  MANY: kBlock turns at a time, each block's
+    // numbers then put to those of the blocks before it.
+    float mine[8], count = 0.0f, before = 0.0f;
+    LongSum mean[MANY ? 8 : 1], squares[MANY ? 8 : 1];
+    auto fold = [&] {
+      before += count;
+      const float share = count > 0.0f ? count / before : 0.0f;
+#pragma unroll
+      for (int i = 0; i < (MANY ? 8 : 0); ++i) {
+        const float d = p.rms ? 0.0f : (mine[i] - mean[i].s) - mean[i].c;
+        mean[i].add(d * share);
+        squares[i].add(__builtin_fmaf(d * share * (before - count), d, r[i]));
+        mine[i] = r[i] = 0.0f;
+      }
+      count = 0.0f;
+    };
 #pragma unroll
     for (int i = 0; i < 8; ++i) mine[i] = 0.0f;
     pass(false, [&](const Ch& k, int e0) {
@@ -272,7 +289,17 @@ __global__ __launch_bounds__(NT) void norm_cols_kernel(NormParams p) {
         }
       }
       if (p.hidden) keep(k, e0);
+      if (MANY && e0 / (C * NG) % kBlock == kBlock - 1) fold();
     });
+    if constexpr (MANY) {
+      fold();
+      count = before;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        mine[i] = mean[i].value();
+        r[i] = squares[i].value();
+      }
+    }
     if (!p.rms) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) m[i] = mine[i] * count;
@@ -428,7 +455,7 @@ __global__ __launch_bounds__(1024) void norm_cols_keep_kernel(NormParams p) {
 }
 
 // A tile each, everything read twice.  The tile's dw and db are a partial sum of its own.
-template <typename XT, typename HT, bool ODD, int NT, int LP, int C>
+template <typename XT, typename HT, bool ODD, int NT, int LP, int C, bool MANY>
 __global__ __launch_bounds__(NT) void norm_cols_bwd_kernel(NormParams p) {
   constexpr int NG = NT / LP, T = LP * 8;
   constexpr bool SHARED = ODD || LP < 8;  // neighbouring tiles share lines
@@ -490,7 +517,16 @@ __global__ __launch_bounds__(NT) void norm_cols_bwd_kernel(NormParams p) {
   load_n<float, 8>(p.stats + p.rows + b * p.L + t, n, r);
 #pragma unroll
   for (int k = 0; k < 8; ++k) c1[k] = c2[k] = 0.0f;
+  LongSum s1[MANY ? 8 : 1], s2[MANY ? 8 : 1];
   pass(false, [&](const Ch& k, int e0) {
+    if (MANY && e0 / (C * NG) % kBlock == 0) {  // the sums of the block of channels before
+#pragma unroll
+      for (int i = 0; i < (MANY ? 8 : 0); ++i) {
+        s1[i].add(c1[i]);
+        s2[i].add(c2[i]);
+        c1[i] = c2[i] = 0.0f;
+      }
+    }
     channels(e0, [&](int c, int e, int64_t) {
       float dw = 0.0f, db = 0.0f;
 #pragma unroll
@@ -512,6 +548,13 @@ __global__ __launch_bounds__(NT) void norm_cols_bwd_kernel(NormParams p) {
       __builtin_amdgcn_sched_barrier(0);
     });
   });
+  if constexpr (MANY) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      c1[i] += s1[i].value();
+      c2[i] += s2[i].value();
+    }
+  }
   if (!p.rms) sum_groups<NT, LP>(c1, sm);
   sum_groups<NT, LP>(c2, sm);
 #pragma unroll
@@ -670,17 +713,21 @@ template <typename XT, typename HT, bool RES> constexpr int kept_channels() {
   return regs <= 4 ? 32 : regs <= 8 ? 16 : 8;
 }
 
-template <typename XT, typename HT, bool RES, bool DROP, bool ODD, int NT, int LP, int C, bool KEEP>
+template <typename XT, typename HT, bool RES, bool DROP, bool ODD, int NT, int LP, int C, bool KEEP, bool MANY = false>
 void go(const NormParams& p, hipStream_t s) {
-  hipLaunchKernelGGL((norm_cols_kernel<XT, HT, RES, DROP, ODD, NT, LP, C, KEEP>),
+  hipLaunchKernelGGL((norm_cols_kernel<XT, HT, RES, DROP, ODD, NT, LP, C, KEEP, MANY>),
                      grid_of(p.B * ((p.L + LP * 8 - 1) / (LP * 8))), dim3(NT), 0, s, p);
 }
 
-// Everything read again for each pass.
+// Everything read again for each pass, in tiles of T = 16, 64 or 256 positions (of very many channels, 16 or 64).
 template <typename XT, typename HT, bool RES, bool DROP, bool ODD>
-void again(const NormParams& p, bool wide, hipStream_t s) {
-  wide && p.L >= 256 ? go<XT, HT, RES, DROP, ODD, 512, 32, 2, false>(p, s)
-                     : go<XT, HT, RES, DROP, ODD, 512, 8, 2, false>(p, s);
+void again(const NormParams& p, int T, hipStream_t s) {
+  if (p.E > kManyChannels)
+    T == 16 ? go<XT, HT, RES, DROP, ODD, 512, 2, 2, false, true>(p, s)
+            : go<XT, HT, RES, DROP, ODD, 512, 8, 2, false, true>(p, s);
+  else if (T == 16) go<XT, HT, RES, DROP, ODD, 512, 2, 2, false>(p, s);
+  else if (T == 64) go<XT, HT, RES, DROP, ODD, 512, 8, 2, false>(p, s);
+  else go<XT, HT, RES, DROP, ODD, 512, 32, 2, false>(p, s);
 }
 
 // With a residual, channels that do not fit the registers: x alone does (4 x 4096 positions x 2048 channels in bf16: 75
@@ -706,20 +753,21 @@ template <typename XT, typename HT, bool RES, bool ODD>
 void fwd_of(const NormParams& p, hipStream_t s) {
   constexpr int C = kept_channels<XT, HT, RES>();
   const bool wide = p.L >= 128 && p.B * ((p.L + 127) / 128) >= 512;
-  if (norm_cols_narrow(p.B, p.E, p.L)) {
-    if (p.drop.below) return go<XT, HT, RES, true, ODD, 512, 2, 2, false>(p, s);
-    return go<XT, HT, RES, false, ODD, 512, 2, 2, false>(p, s);
+  const int T = norm_cols_narrow(p.B, p.E, p.L) ? 16 : wide && p.L >= 256 ? 256 : 64;  // of what is read again
+  if (T == 16) {
+    if (p.drop.below) return again<XT, HT, RES, true, ODD>(p, T, s);
+    return again<XT, HT, RES, false, ODD>(p, T, s);
   }
   if constexpr (RES && !ODD) {
     if (p.E >= 128 && p.E <= 128 * keep_most<XT>() && (p.drop.below || p.E > 64 * C)) return keep_fwd<XT, HT>(p, s);
   }
-  if (p.drop.below) return again<XT, HT, RES, true, ODD>(p, wide, s);
+  if (p.drop.below) return again<XT, HT, RES, true, ODD>(p, T, s);
   if (p.E <= 16 * (C / 4)) return go<XT, HT, RES, false, ODD, 256, 16, C / 4, true>(p, s);
   if (wide && p.E <= 32 * (C / 4)) return go<XT, HT, RES, false, ODD, 512, 16, C / 4, true>(p, s);
   if (p.E <= 64 * (C / 4)) return go<XT, HT, RES, false, ODD, 512, 8, C / 4, true>(p, s);
   if (wide && p.E <= 32 * C) return go<XT, HT, RES, false, ODD, 512, 16, C, true>(p, s);
   if (p.E <= 64 * C) return go<XT, HT, RES, false, ODD, 512, 8, C, true>(p, s);
-  again<XT, HT, RES, false, ODD>(p, wide, s);
+  again<XT, HT, RES, false, ODD>(p, T, s);
 }
 
 template <typename XT, typename HT, bool RES>
@@ -727,9 +775,9 @@ void fwd(const NormParams& p, hipStream_t s) {
   p.L % 8 ? fwd_of<XT, HT, RES, true>(p, s) : fwd_of<XT, HT, RES, false>(p, s);
 }
 
-template <typename XT, typename HT, bool ODD, int NT, int LP, int C>
+template <typename XT, typename HT, bool ODD, int NT, int LP, int C, bool MANY = false>
 void go_bwd(const NormParams& p, hipStream_t s) {
-  hipLaunchKernelGGL((norm_cols_bwd_kernel<XT, HT, ODD, NT, LP, C>), grid_of(p.blocks), dim3(NT), 0, s, p);
+  hipLaunchKernelGGL((norm_cols_bwd_kernel<XT, HT, ODD, NT, LP, C, MANY>), grid_of(p.blocks), dim3(NT), 0, s, p);
 }
 
 template <typename XT, typename HT, bool RMS>
@@ -749,6 +797,10 @@ void bwd(const NormParams& p, hipStream_t s) {
   const int kind = (sizeof(XT) == 2 ? 1 : 0) + (sizeof(HT) == 2 ? 2 : 0);
   const NormTile tile = norm_cols_bwd_tile(p.B, p.E, p.L, kind, p.rms);
   if (tile.keep) return p.rms ? keep_bwd<XT, HT, true>(p, s) : keep_bwd<XT, HT, false>(p, s);
+  if (p.E > kManyChannels) {
+    if (p.L % 8) return tile.T == 16 ? go_bwd<XT, HT, true, 512, 2, 2, true>(p, s) : go_bwd<XT, HT, true, 512, 8, 2, true>(p, s);
+    return tile.T == 16 ? go_bwd<XT, HT, false, 512, 2, 2, true>(p, s) : go_bwd<XT, HT, false, 512, 8, 2, true>(p, s);
+  }
   if (p.L % 8) {
     if (tile.T == 16) return go_bwd<XT, HT, true, 512, 2, 2>(p, s);
     return tile.T > 64 ? go_bwd<XT, HT, true, 512, 16, 2>(p, s) : go_bwd<XT, HT, true, 512, 8, 2>(p, s);

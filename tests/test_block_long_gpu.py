@@ -7,7 +7,7 @@ times the sum of magnitudes with N = 160, then.  The mean takes two more roundin
 import pytest
 import torch
 
-from selective_state_space_76_amd import layer_norm_bwd, layer_norm_fwd
+from selective_state_space_76_amd import dropout_bwd, dropout_fwd, layer_norm_bwd, layer_norm_fwd
 from tests import block_ref as R
 
 pytestmark = pytest.mark.gpu
@@ -116,3 +116,52 @@ def test_an_infinite_sum_stays_infinite(shape, cf):
     out, _, stats = layer_norm_fwd(x, rms=True, channels_first=cf)
     rows, k = rows64(out, cf), 7 if cf else 0
     assert stats[1, k] == 0 and stats[1, k - 1] > 0.9 and torch.isnan(rows[k]).sum() == 1 and rows[k].nansum() == 0
+
+
+# over channels: tiles of 16 positions, odd lengths, tiles of 64 positions
+CHANNELS = [(1, 1 << 22, 16), (1, (1 << 22) + 3, 5), (128, 1 << 18, 64)]
+
+
+@pytest.mark.parametrize("rms", [False, True], ids=["layer", "rms"])
+@pytest.mark.parametrize("kind", ["constant", "far", "two levels"])
+@pytest.mark.parametrize("shape", CHANNELS)
+def test_very_many_channels(shape, kind, rms):
+    for types in TYPES[:2]:
+        print("case: very many channels", shape, kind, rms, types, flush=True)
+        check_fwd(values(kind, shape, types[0], 7 + rms, True), rms, True)
+
+
+@pytest.mark.parametrize("rms", [False, True], ids=["layer", "rms"])
+@pytest.mark.parametrize("shape", CHANNELS)
+def test_gradients_of_very_many_channels(shape, rms):
+    for xt, ht in TYPES:
+        for kind in ("constant", "two levels"):
+            print("case: gradients of very many channels", shape, kind, rms, xt, ht, flush=True)
+            check_bwd(values(kind, shape, xt, 8, True), values("two levels", shape, ht, 9, True), rms, True)
+
+
+@pytest.mark.parametrize("rms", [False, True], ids=["layer", "rms"])
+@pytest.mark.parametrize("xt", [F32, BF16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("shape", [(128, 17000, 64), (128, 17000, 61), (2, 17000, 40), (2, 17001, 5)])
+def test_many_channels_with_residual_and_dropout(shape, xt, rms):
+    """Into an fp32 stream: the sum against 64 bits, out against the norm of that sum, dx against dropout of dresidual."""
+    print("case: many channels with residual and dropout", shape, xt, rms, flush=True)
+    g = torch.Generator(device=DEV).manual_seed(3)
+    rnd = lambda *s: torch.empty(s, device=DEV).normal_(generator=g)  # noqa: E731
+    x, res, w = rnd(*shape).to(xt), rnd(*shape), 1 + 0.1 * rnd(shape[1])
+    kw = dict(rms=rms, channels_first=True)
+    drop = dict(p=0.25, seed=11, call=2)
+    out, hidden, stats = layer_norm_fwd(x, w, None, res, **kw, **drop)
+    kept = dropout_fwd(torch.ones(shape, device=DEV), 0.25, 11, call=2)
+    s = x.double() * kept + res
+    assert bool(((hidden - s).abs() <= 3 * U * (s.abs() + res.abs())).all())  # (a product and a sum, the stream's rounding)
+    want, _, again = layer_norm_fwd(hidden, w, None, **kw)
+    assert bool(((out.double() - want).abs() <= 8 * U * (1 + want.abs()) + half(xt) * want.abs() * (1 + 2 ** -6)).all())
+    assert bool(((stats - again).abs() <= 8 * U).all())
+    check_fwd(hidden, rms, True)
+    dout, dh = rnd(*shape).to(xt), rnd(*shape)
+    got = layer_norm_bwd(dout, hidden, w, stats, dhidden=dh, residual=True, bias=False, **kw, **drop)
+    plain = layer_norm_bwd(dout, hidden, w, stats, dhidden=torch.zeros_like(dh), residual=True, bias=False, **kw)["dresidual"]
+    assert bool(((got["dresidual"].double() - (plain.double() + dh)).abs() <= 4 * U * (plain.abs() + dh.abs())).all())
+    assert torch.equal(got["dx"], dropout_bwd(got["dresidual"], 0.25, 11, call=2, dtype=xt))
+    check_bwd(dout, hidden, rms, True)
