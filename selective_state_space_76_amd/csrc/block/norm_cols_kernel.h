@@ -88,6 +88,18 @@ template <int LP> __device__ __forceinline__ float sum_positions(float v) {
 // keep all of their terms until then.
 __device__ __forceinline__ void here(float& v) { asm volatile("" : "+v"(v)); }
 
+// A channel's numbers join a lane's means and its squares about them; share: 1 / the channels so far.  RMS norm: the
+// means are zero (by a mask: an infinite number times a share of zero would make the sum NaN, and it is infinite).
+__device__ __forceinline__ void one_more(const float (&s)[8], float share, int rms, float (&mean)[8], float (&squares)[8]) {
+  const uint32_t some = rms ? 0u : ~0u;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float d = s[i] - mean[i];
+    mean[i] = __uint_as_float(__float_as_uint(__builtin_fmaf(d, share, mean[i])) & some);
+    squares[i] = __builtin_fmaf(d, s[i] - mean[i], squares[i]);
+  }
+}
+
 // Where rows do not begin with a line, neighbouring tiles write parts of one: put together by the cache.
 template <typename IO>
 __device__ __forceinline__ void store_cols(IO* p, int n, const float (&x)[8], bool lines) {
@@ -279,13 +291,7 @@ __global__ __launch_bounds__(NT) void norm_cols_kernel(NormParams p) {
           float s[8];
           sum(k, c, s);
           count += 1.0f;
-          const float share = p.rms ? 0.0f : rcp_(count);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const float d = s[i] - mine[i];
-            mine[i] = __builtin_fmaf(d, share, mine[i]);
-            r[i] = __builtin_fmaf(d, s[i] - mine[i], r[i]);
-          }
+          one_more(s, rcp_(count), p.rms, mine, r);
         }
       }
       if (p.hidden) keep(k, e0);
@@ -382,12 +388,9 @@ __global__ __launch_bounds__(1024) void norm_cols_keep_kernel(NormParams p) {
     sum(c, now, s);
     if (e0 + c * NG < E) {
       count += 1.0f;
-      const float share = p.rms ? 0.0f : rcp_(count);
+      one_more(s, rcp_(count), p.rms, m, r);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const float d = s[i] - m[i];
-        m[i] = __builtin_fmaf(d, share, m[i]);
-        r[i] = __builtin_fmaf(d, s[i] - m[i], r[i]);
         here(m[i]);
         here(r[i]);
       }
