@@ -40,6 +40,7 @@ struct NormParams {
   float* dbias;
   int64_t rows, E, B, L;
   int64_t blocks;        // backward: workgroups, each with its partial sums
+  int64_t from, to;      // backward, rows of a launch
   float eps, inv_e;
   int rms;
   DropParams drop;

@@ -801,8 +801,9 @@ void bwd(const NormParams& p, hipStream_t s) {
   const NormTile tile = norm_cols_bwd_tile(p.B, p.E, p.L, kind, p.rms);
   if (tile.keep) return p.rms ? keep_bwd<XT, HT, true>(p, s) : keep_bwd<XT, HT, false>(p, s);
   if (p.E > kManyChannels) {
-    if (p.L % 8) return tile.T == 16 ? go_bwd<XT, HT, true, 512, 2, 2, true>(p, s) : go_bwd<XT, HT, true, 512, 8, 2, true>(p, s);
-    return tile.T == 16 ? go_bwd<XT, HT, false, 512, 2, 2, true>(p, s) : go_bwd<XT, HT, false, 512, 8, 2, true>(p, s);
+    if (tile.T == 16)
+      return p.L % 8 ? go_bwd<XT, HT, true, 512, 2, 2, true>(p, s) : go_bwd<XT, HT, false, 512, 2, 2, true>(p, s);
+    return p.L % 8 ? go_bwd<XT, HT, true, 512, 8, 2, true>(p, s) : go_bwd<XT, HT, false, 512, 8, 2, true>(p, s);
   }
   if (p.L % 8) {
     if (tile.T == 16) return go_bwd<XT, HT, true, 512, 2, 2>(p, s);

@@ -36,6 +36,7 @@ int team_of(int64_t E, int each = 1) {
 }
 constexpr int64_t kTwo = 4096;  // elements from which on a lane holds two pieces (forward)
 constexpr int kLong = 1024;     // lanes of a row that no team holds (16 x 200000: 84 us, 250 with 256)
+constexpr int kTurns = 256;     // rows in turn of a team in the backward pass
 
 // (a, b) summed over the team's lanes, in all of them; TEAM 0: the workgroup; sm: two floats for each of 16 waves
 template <int TEAM>
@@ -247,9 +248,9 @@ __global__ __launch_bounds__(kLong) void norm_long_kernel(NormParams p) {
   }
 }
 
-// Rows in turn (p.blocks workgroups); dw and db of the lane's columns are added up over the team's rows in registers,
-// then over the workgroup's teams in LDS, and go to memory as the workgroup's partial sums.  ODD: a team's rows are
-// 8 k apart, so that they all begin alike and a lane keeps its columns.
+// Rows p.from .. p.to - 1 in turn (p.blocks workgroups); dw and db of the lane's columns are added up over the team's rows in
+// registers, then over the workgroup's teams in LDS, and go to memory as the workgroup's partial sums.  ODD: a team's
+// rows are 8 k apart, so that they all begin alike and a lane keeps its columns.
 template <typename XT, typename HT, int TEAM, bool ODD>
 __global__ __launch_bounds__(TEAM ? 256 : 1024) void norm_rows_bwd_kernel(NormParams p) {
   constexpr int R = TEAM ? 256 / (TEAM ? TEAM : 1) : 1;
@@ -261,7 +262,7 @@ __global__ __launch_bounds__(TEAM ? 256 : 1024) void norm_rows_bwd_kernel(NormPa
   const HT* hidden = static_cast<const HT*>(p.residual);
   const HT* dhidden = static_cast<const HT*>(p.dhidden);
   const Drop drop(p.drop);
-  const int64_t first = (int64_t)block_id() * R + team;
+  const int64_t first = p.from + (int64_t)block_id() * R + team;
   const int64_t e = lane * 8 - (ODD ? (int)(first * E % 8) : 0);
   Part n(e, E);
   if (!ODD) n.hi = n.hi ? 8 : 0, n.lo = 0;
@@ -277,7 +278,7 @@ __global__ __launch_bounds__(TEAM ? 256 : 1024) void norm_rows_bwd_kernel(NormPa
 #pragma unroll
   for (int k = 0; k < 8; ++k) dw[k] = db[k] = 0.0f;
   int turn = 0;
-  for (int64_t row = first; row < p.rows; row += p.blocks * R, turn ^= 1) {
+  for (int64_t row = first; row < p.to; row += p.blocks * R, turn ^= 1) {
     const int64_t at = row * E + e;
     const bool end = ODD && at + 8 > total, may = n.any() && !end;
     Piece<XT> a;
@@ -336,7 +337,7 @@ __global__ __launch_bounds__(TEAM ? 256 : 1024) void norm_rows_bwd_kernel(NormPa
         float s = 0.0f;
 #pragma unroll
         for (int t = 0; t < R; ++t)
-          s += acc[t * TEAM * 8 + c + (ODD ? (int)(((int64_t)block_id() * R + t) * E % 8) : 0)];
+          s += acc[t * TEAM * 8 + c + (ODD ? (int)((p.from + (int64_t)block_id() * R + t) * E % 8) : 0)];
         part[which * E + c] = s;
       }
     } else {
@@ -496,11 +497,41 @@ void fwd(const NormParams& p, hipStream_t s) {
   }
 }
 
+// Workgroups of the backward pass, each of which leaves a partial sum of dw and db: about 16 waves a compute unit, the
+// same number on each (16384 x 5000, 10 waves a row: 84 us with 512, 117 and 100 with 256 and 768), and where the
+// rows are fewer, up to 12 rows in turn rather than more sums (16384 x 768: 39 us with 1366, 41.6 with 2048, 51 with
+// 4096), but 512 at least.  A multiple of 8 where E is none.  A plain sum over rows in turn is off by up to their number of
+// half steps: of very many rows, each launch takes kTurns (more workgroups instead, of which not all are resident at
+// once: 2^20 x 768 1058 us, 961 so).  Rows that no team holds: groups of rows in one launch.
+struct BwdPlan {
+  int64_t groups, launches;
+};
+BwdPlan bwd_plan(int64_t rows, int64_t E) {
+  const int lanes = team_of(E);
+  if (!lanes) return {rows < 64 ? rows : rows <= 64 * kTurns ? 64 : (rows + kTurns - 1) / kTurns, 1};
+  const int64_t waves = lanes <= 64 ? 4 : lanes / 64, R = lanes <= 64 ? 256 / lanes : 1;
+  const int64_t each = (16 + waves - 1) / waves < 24 / waves ? (16 + waves - 1) / waves : 24 / waves;
+  const int64_t all = (rows + R - 1) / R, most = 256 * each;
+  int64_t turns = (all + 511) / 512 < 12 ? (all + 511) / 512 : 12;
+  if (turns < (all + most - 1) / most) turns = (all + most - 1) / most;
+  const int64_t n = (all + turns - 1) / turns;
+  return {E % 8 ? (n + 7) / 8 * 8 : n, (turns + kTurns - 1) / kTurns};
+}
+
 template <typename XT, typename HT, int TEAM>
 void go_bwd(const NormParams& p, int lanes, hipStream_t s) {
-  const dim3 grid = grid_of(p.blocks), block(TEAM ? 256 : lanes);
-  if (p.E % 8) hipLaunchKernelGGL((norm_rows_bwd_kernel<XT, HT, TEAM, true>), grid, block, 0, s, p);
-  else hipLaunchKernelGGL((norm_rows_bwd_kernel<XT, HT, TEAM, false>), grid, block, 0, s, p);
+  const BwdPlan plan = bwd_plan(p.rows, p.E);
+  const dim3 grid = grid_of(plan.groups), block(TEAM ? 256 : lanes);
+  const int64_t step = kTurns * plan.groups * (TEAM ? 256 / (TEAM ? TEAM : 1) : 1);
+  NormParams q = p;
+  q.blocks = plan.groups;
+  for (int64_t k = 0; k < plan.launches; ++k) {
+    q.from = k * step;
+    q.to = q.from + step < p.rows ? q.from + step : p.rows;
+    q.part = p.part ? p.part + k * plan.groups * 2 * p.E : nullptr;
+    if (p.E % 8) hipLaunchKernelGGL((norm_rows_bwd_kernel<XT, HT, TEAM, true>), grid, block, 0, s, q);
+    else hipLaunchKernelGGL((norm_rows_bwd_kernel<XT, HT, TEAM, false>), grid, block, 0, s, q);
+  }
 }
 
 template <typename XT, typename HT>
@@ -521,20 +552,9 @@ void bwd(const NormParams& p, hipStream_t s) {
 
 }  // namespace
 
-// Workgroups of the backward pass, each of which leaves a partial sum of dw and db: about 16 waves a compute unit, the
-// same number on each (16384 x 5000, 10 waves a row: 84 us with 512, 117 and 100 with 256 and 768), and where the
-// rows are fewer, up to 12 rows in turn rather than more sums (16384 x 768: 39 us with 1366, 41.6 with 2048, 51 with
-// 4096), but 512 at least.  A multiple of 8 where E is none.
 int64_t norm_rows_bwd_blocks(int64_t rows, int64_t E) {
-  const int lanes = team_of(E);
-  if (!lanes) return rows < 64 ? rows : 64;
-  const int64_t waves = lanes <= 64 ? 4 : lanes / 64, R = lanes <= 64 ? 256 / lanes : 1;
-  const int64_t each = (16 + waves - 1) / waves < 24 / waves ? (16 + waves - 1) / waves : 24 / waves;
-  const int64_t all = (rows + R - 1) / R, most = 256 * each;
-  int64_t turns = (all + 511) / 512 < 12 ? (all + 511) / 512 : 12;
-  if (turns < (all + most - 1) / most) turns = (all + most - 1) / most;
-  const int64_t n = (all + turns - 1) / turns;
-  return E % 8 ? (n + 7) / 8 * 8 : n;
+  const BwdPlan plan = bwd_plan(rows, E);
+  return plan.groups * plan.launches;
 }
 
 hipError_t launch_norm_rows(const NormParams& p, int kind, hipStream_t s) {

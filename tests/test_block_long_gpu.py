@@ -165,3 +165,20 @@ def test_many_channels_with_residual_and_dropout(shape, xt, rms):
     assert bool(((got["dresidual"].double() - (plain.double() + dh)).abs() <= 4 * U * (plain.abs() + dh.abs())).all())
     assert torch.equal(got["dx"], dropout_bwd(got["dresidual"], 0.25, 11, call=2, dtype=xt))
     check_bwd(dout, hidden, rms, True)
+
+
+@pytest.mark.parametrize("rows,E", [(1 << 28, 8), ((1 << 28) - 3, 7), (1 << 22, 768), (1 << 20, 8200)])
+def test_weight_gradients_of_very_many_rows(rows, E):
+    """All rows alike: the sums are the rows' number times one of them (256 rows in turn, 64 sums a lane of the joins, of
+    which there are two, and 20 more additions: 500 u)."""
+    print("case: weight gradients of very many rows", rows, E, flush=True)
+    dout, hidden = (torch.full((rows, E), v, dtype=BF16, device=DEV) for v in (1.1, 0.7))
+    stats = torch.empty(2, rows, device=DEV)
+    stats[0], stats[1] = 0, 1
+    got = layer_norm_bwd(dout, hidden, torch.ones(E, device=DEV), stats, rms=True)
+    d, h = float(dout[0, 0]), float(hidden[0, 0])
+    for k, one in (("dweight", d * h), ("dbias", d)):
+        assert float((got[k].double() / (rows * one) - 1).abs().max()) <= 500 * U, k
+    one = float(got["dx"][0, 0])
+    assert one != 0 and float(got["dx"].min()) >= min(one * (1 + 2 ** -7), one * (1 - 2 ** -7))
+    assert float(got["dx"].max()) <= max(one * (1 + 2 ** -7), one * (1 - 2 ** -7))
