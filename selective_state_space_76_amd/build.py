@@ -18,7 +18,7 @@ SOURCES = [os.path.join(CSRC, f) for f in (
     "train/conv_bwd.hip", "train/embed_fwd.hip", "train/embed_bwd.hip", "train/embed_bwd_few.hip",
     "train/adamw.hip", "train/train_abi.cpp",
     "block/norm_rows.hip", "block/norm_cols_bf16.hip", "block/norm_cols_mixed.hip", "block/norm_cols_f32.hip",
-    "block/dropout.hip", "block/recur_fwd.hip", "block/recur_bwd.hip",
+    "block/dropout.hip", "block/recur_fwd.hip", "block/recur_bwd.hip", "block/join.hip",
     "block/block_abi.cpp")]
 HEADERS = [os.path.join(CSRC, "ssm_launch.h"), os.path.join(CSRC, "ssm_device.h"),
            os.path.join(CSRC, "scan_bwd_kernel.h"),

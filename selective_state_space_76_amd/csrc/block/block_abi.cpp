@@ -130,7 +130,8 @@ ssm_status ssm_layer_norm_bwd(const ssm_norm_shape* shape, const void* dout, con
   p.blocks = norm_bwd_blocks(shape, z);
   hipStream_t st = reinterpret_cast<hipStream_t>(stream);
   rc = launch_status(norm_cols(shape) ? ssm::launch_norm_cols_bwd(p, z.kind, st) : ssm::launch_norm_rows_bwd(p, z.kind, st));
-  return rc != SSM_OK || !sums ? rc : launch_status(ssm::launch_norm_join(p, st));
+  if (rc != SSM_OK || !sums) return rc;
+  return launch_status(ssm::launch_join({p.part, p.blocks, p.E, 2, {dweight, dbias, nullptr}}, st));
 }
 
 ssm_status ssm_dropout_fwd(int64_t numel, int32_t x_dtype, int32_t out_dtype, const void* x, const void* residual,

@@ -96,8 +96,15 @@ inline int64_t norm_cols_bwd_blocks(int64_t B, int64_t E, int64_t L, int kind, b
   return B * ((L + T - 1) / T);
 }
 hipError_t launch_norm_rows_bwd(const NormParams& p, int kind, hipStream_t s);
-// dweight and dbias from p.blocks partial sums
-hipError_t launch_norm_join(const NormParams& p, hipStream_t s);
+
+// ---- the sums of partial sums (join.hip); part is overwritten where there are more than 4096
+struct JoinParams {
+  float* part;      // [count][kinds][E]
+  int64_t count, E;
+  int kinds;        // 2 or 3
+  float* out[3];    // [E] each, or null
+};
+hipError_t launch_join(const JoinParams& p, hipStream_t s);
 
 // ---- gated linear recurrence (recur_fwd.hip, recur_bwd.hip)
 struct RecurPlan {

@@ -430,49 +430,6 @@ __global__ __launch_bounds__(256) void norm_sums_kernel(NormParams p) {
   p.part[first * 2 * p.E + p.E + e] = db;
 }
 
-// dw and db from the partial sums: COLS columns per workgroup, the partial sums split over 1024 / COLS groups of lanes, each
-// in order, then the groups' sums in order (1366 sums of 768 columns, 16 at a time: 6 us).  Every `step`th
-// of them, `many` to a workgroup, which leaves their sum in the place of the first; the last call's single one writes dw
-// and db.
-template <int COLS>
-__global__ __launch_bounds__(1024) void norm_join_kernel(NormParams p, int64_t step, int64_t many) {
-  __shared__ float sm[1024], sn[256];
-  const int64_t cols = (p.E + COLS - 1) / COLS, n = (p.blocks + step - 1) / step;
-  const int64_t count = 2 * cols * ((n + many - 1) / many);
-  if (block_id() >= count) return;
-  const int64_t blk = xcd_remap((int)block_id(), (int)count);  // (neighbours read the same lines)
-  const int64_t which = blk / cols % 2, first = blk / (2 * cols) * many;
-  const int64_t here = n - first < many ? n - first : many;
-  const int64_t c = blk % cols * COLS + threadIdx.x % COLS;
-  const int64_t per = (here + 1024 / COLS - 1) / (1024 / COLS), row = step * 2 * p.E;
-  const int64_t k0 = threadIdx.x / COLS * per, k1 = k0 + per < here ? k0 + per : here;
-  float* q = p.part + first * row + which * p.E + c;
-  float s = 0.0f;
-  if (c < p.E) {
-    for (int64_t k = k0; k < k1; k += 8) {  // (the last few at once, too: one by one they were half of the time)
-      float v[8];
-#pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] = k + e < k1 ? q[(k + e) * row] : 0.0f;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) s += v[e];
-    }
-  }
-  sm[threadIdx.x] = s;
-  __syncthreads();
-  if (threadIdx.x < 256) {
-    const int at = threadIdx.x / COLS * 4 * COLS + threadIdx.x % COLS;
-    sn[threadIdx.x] = (sm[at] + sm[at + COLS]) + (sm[at + 2 * COLS] + sm[at + 3 * COLS]);
-  }
-  __syncthreads();
-  float* out = many < n ? q : which ? p.dbias : p.dweight;
-  if (threadIdx.x < COLS && c < p.E && out) {
-    s = 0.0f;
-#pragma unroll
-    for (int t = 0; t < 256 / COLS; ++t) s += sn[t * COLS + threadIdx.x];
-    out[many < n ? 0 : c] = s;
-  }
-}
-
 namespace {
 
 template <typename XT, typename HT, int TEAM, int P>
@@ -568,21 +525,6 @@ hipError_t launch_norm_rows_bwd(const NormParams& p, int kind, hipStream_t s) {
   if (kind == 3) bwd<bf16_t, bf16_t>(p, s);
   else if (kind == 1) bwd<bf16_t, float>(p, s);
   else bwd<float, float>(p, s);
-  return hipGetLastError();
-}
-
-hipError_t launch_norm_join(const NormParams& p, hipStream_t s) {
-  // in one go while a lane's share is short
-  for (int64_t n = p.blocks, step = 1, many; n; step *= many) {
-    many = n <= 4096 ? n : 512;
-    const int64_t groups = (n + many - 1) / many;
-    // (of few sums, 256 columns at a time leave fewer lanes without one: 64 x 100000, gradients: 83 us, 153 with 16)
-    if (many <= 64)
-      hipLaunchKernelGGL(norm_join_kernel<256>, grid_of((p.E + 255) / 256 * 2 * groups), dim3(1024), 0, s, p, step, many);
-    else
-      hipLaunchKernelGGL(norm_join_kernel<16>, grid_of((p.E + 15) / 16 * 2 * groups), dim3(1024), 0, s, p, step, many);
-    n = groups > 1 ? groups : 0;
-  }
   return hipGetLastError();
 }
 

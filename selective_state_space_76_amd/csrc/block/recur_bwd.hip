@@ -222,35 +222,6 @@ __global__ __launch_bounds__(W > 4 ? W * 64 : 256, Z || LN < 64 ? 3 : 4) void re
   }
 }
 
-// ddecay and the biases' gradients from the waves' sums: 64 outputs per workgroup, the sums split over 4 waves,
-// each in order, then the waves' in order.
-__global__ __launch_bounds__(256) void recur_join_kernel(RecurParams p) {
-  const int64_t n = 3 * p.D, count = p.B * p.plan.S * p.plan.waves;
-  const int64_t i = (int64_t)block_id() * 64 + (threadIdx.x & 63);
-  const int64_t per = (count + 3) / 4;
-  const int64_t k0 = (threadIdx.x >> 6) * per, k1 = k0 + per < count ? k0 + per : count;
-  float s = 0.0f;
-  if (i < n) {
-    int64_t k = k0;
-    for (; k + 8 <= k1; k += 8) {
-      float v[8];
-#pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] = p.part[(k + e) * n + i];
-#pragma unroll
-      for (int e = 0; e < 8; ++e) s += v[e];
-    }
-    for (; k < k1; ++k) s += p.part[k * n + i];
-  }
-  __shared__ float sm[256];
-  sm[threadIdx.x] = s;
-  __syncthreads();
-  if (threadIdx.x < 64 && i < n) {
-    s = sm[threadIdx.x] + sm[threadIdx.x + 64] + sm[threadIdx.x + 128] + sm[threadIdx.x + 192];
-    float* out = i < p.D ? p.ddecay : i < 2 * p.D ? p.drb : p.dib;
-    if (out) out[i % p.D] = s;
-  }
-}
-
 namespace {
 
 template <typename IO, bool REV, bool Z>
@@ -287,8 +258,7 @@ hipError_t launch_recur_bwd(const RecurParams& q, bool bf16, bool reverse, hipSt
   bf16 ? any<bf16_t>(p, reverse, s) : any<float>(p, reverse, s);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || p.whole) return e;
-  hipLaunchKernelGGL(recur_join_kernel, grid_of((3 * p.D + 63) / 64), dim3(256), 0, s, p);
-  return hipGetLastError();
+  return launch_join({p.part, p.B * p.plan.S * p.plan.waves, p.D, 3, {p.ddecay, p.drb, p.dib}}, s);
 }
 
 }  // namespace ssm
