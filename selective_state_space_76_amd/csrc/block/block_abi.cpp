@@ -180,7 +180,7 @@ ssm_status recur_check(const ssm_recurrence_shape* s, RecurSizes* z) {
   z->plan = ssm::recur_plan(s->batch, s->dim, s->seqlen, z->bf16);
   z->ckpt = z->bd * z->plan.blocks * 4;
   z->seg = z->plan.S > 1 ? z->bd * z->plan.S * 8 : 0;
-  z->part = z->bd * z->plan.S * z->plan.waves * 12;
+  z->part = z->bd * z->plan.S * z->plan.waves * z->plan.parts * 12;
   return SSM_OK;
 }
 

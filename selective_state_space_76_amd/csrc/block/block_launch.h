@@ -114,6 +114,8 @@ struct RecurPlan {
   int64_t blocks = 0;   // blocks of 64 pieces in a row, each with a checkpoint
   int64_t tiles = 0;    // turns of a row's team
   int64_t per = 0;      // tiles in a segment
+  int chain = 0;        // backward: turns that a lane adds up before they become a partial sum
+  int parts = 1;        // such sums of a segment
 };
 RecurPlan recur_plan(int64_t B, int64_t D, int64_t L, bool bf16);
 
@@ -138,7 +140,7 @@ struct RecurParams {
   void* di;
   void* dz;           // with z
   float* dinit;       // [B,D] or null
-  float* part;        // [B*S*waves][3][D]
+  float* part;        // [B*S*waves*parts][3][D]
   float* ddecay;      // [D]
   float* drb;         // or null
   float* dib;

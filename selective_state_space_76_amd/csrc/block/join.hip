@@ -1,5 +1,5 @@
-// join.hip -- sums over rows or batches (dweight and dbias of a norm; ddecay and the biases' gradients of a recurrence) from the
-// partial sums that the workgroups of their backward passes leave.
+// join.hip -- sums over rows or batches (dweight and dbias of a norm; ddecay and the biases' gradients of a recurrence) from
+// the partial sums that the workgroups of their backward passes leave.
 //
 // COLS columns per workgroup, the partial sums split over NT / COLS groups of lanes, each in order, then the groups' sums
 // in order (1366 sums of 768 columns, 16 at a time: 6 us).  Up to 4096 of them in one go: 64 a lane; more in levels of 512:

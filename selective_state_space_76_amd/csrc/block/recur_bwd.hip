@@ -16,9 +16,11 @@
 
 namespace ssm {
 
-// Z: there is a gate.  MAPS: the segments' maps of the adjoint.
-template <typename IO, int LN, int W, bool REV, bool Z, bool MAPS>
-__global__ __launch_bounds__(W > 4 ? W * 64 : 256, Z || LN < 64 ? 3 : 4) void recur_bwd_kernel(RecurParams p) {
+// Z: there is a gate.  MAPS: the segments' maps of the adjoint.  PARTS: a segment leaves several partial sums (apart from the
+// others for its registers: 1 x 509 x 262147 394 us, 405 with it).
+template <typename IO, int LN, int W, bool REV, bool Z, bool MAPS, bool PARTS = false>
+__global__ __launch_bounds__(W > 4 ? W * 64 : 256, Z || (REV && PARTS) || LN < 64 ? 3 : 4)
+void recur_bwd_kernel(RecurParams p) {
   constexpr int V = 16 / (int)sizeof(IO);
   constexpr int UNITS = W > 4 ? 1 : 256 / (LN * W);
   constexpr int TURN = LN * W * V;
@@ -68,7 +70,11 @@ __global__ __launch_bounds__(W > 4 ? W * 64 : 256, Z || LN < 64 ? 3 : 4) void re
       hn = p.ckpt[row * p.plan.blocks + (block < p.plan.blocks ? block : p.plan.blocks - 1)];
     }
   };
+  // The lane's sums, of p.plan.chain turns at the most: then they become a partial sum (a plain chain of 2^14 terms of one
+  // sign was off by 5e-5; compensated in registers or LDS the sums cost long rows up to 9 and 28%).
   float sd = 0.0f, sr = 0.0f, si = 0.0f;
+  int left = p.plan.chain, parts = 0;
+  auto part = [&] { return p.part + (((b * p.plan.S + seg) * W + w) * (PARTS ? p.plan.parts : 1) + parts) * 3 * p.D + d; };
   float state = 0.0f;
   if (k0 < k1) load(k1 - 1);
   for (int64_t tile = k1 - 1; tile >= k0; --tile) {
@@ -163,22 +169,40 @@ __global__ __launch_bounds__(W > 4 ? W * 64 : 256, Z || LN < 64 ? 3 : 4) void re
     }
     // (gradients with respect to what the sigmoids take; where a is 1 to the last bit, with sig(r) under 2^-100 / decay,
     // what 1 / q meets is zero)
+    float td = 0.0f, tr = 0.0f, ti = 0.0f;  // the turn's
 #pragma unroll
     for (int e = 0; e < V; ++e) {
       const float gs = g[e] * sgi[e], x = slot<IO, REV>(xq, e);
       const float dla = __builtin_fmaf(g[e] * a[e], hb[e], -gs * x * (a[e] * a[e] * iq[e]));
       const float dls = -dla * sig[e];
-      sd += dls;
+      td += dls;
       hb[e] = dls * decay * (1.0f - sig[e]);
-      sr += hb[e];
+      tr += hb[e];
       o[e] = gs * q[e];
       g[e] = o[e] * x * (1.0f - sgi[e]);
-      si += g[e];
+      ti += g[e];
     }
+    sd += td;
+    sr += tr;
+    si += ti;
     store_slots<IO, REV>(p.dx, at, lo, hi, edge, o);
     store_slots<IO, REV>(p.dr, at, lo, hi, edge, hb);
     store_slots<IO, REV>(p.di, at, lo, hi, edge, g);
     if (LN < 64) break;  // (rows of fewer lanes are one turn)
+    if (PARTS && --left == 0 && tile > k0) {
+      sd = sum_group<LN>(sd);
+      sr = sum_group<LN>(sr);
+      si = sum_group<LN>(si);
+      if (lane == 0) {
+        float* o = part();
+        o[0] = sd;
+        o[p.D] = sr;
+        o[2 * p.D] = si;
+      }
+      sd = sr = si = 0.0f;
+      left = p.plan.chain;
+      ++parts;
+    }
   }
   if (MAPS) {
     if (lane == 0 && w == 0) {
@@ -215,14 +239,28 @@ __global__ __launch_bounds__(W > 4 ? W * 64 : 256, Z || LN < 64 ? 3 : 4) void re
       if (p.dib) p.dib[d] = si;
     }
   } else if (lane == 0) {
-    float* o = p.part + ((b * p.plan.S + seg) * W + w) * 3 * p.D + d;
-    o[0] = sd;
-    o[p.D] = sr;
-    o[2 * p.D] = si;
+    for (; parts < (PARTS ? p.plan.parts : 1); ++parts) {  // (a last segment may have fewer turns)
+      float* o = part();
+      o[0] = sd;
+      o[p.D] = sr;
+      o[2 * p.D] = si;
+      sd = sr = si = 0.0f;
+    }
   }
 }
 
 namespace {
+
+template <typename IO, bool REV, bool Z, bool PARTS>
+void waves(const RecurParams& p, hipStream_t s) {
+  const int64_t rows = p.B * p.D;
+  if (p.plan.waves == 1)
+    hipLaunchKernelGGL((recur_bwd_kernel<IO, 64, 1, REV, Z, false, PARTS>), grid_of((rows + 3) / 4), dim3(256), 0, s, p);
+  else if (p.plan.waves == 8)
+    hipLaunchKernelGGL((recur_bwd_kernel<IO, 64, 8, REV, Z, false, PARTS>), grid_of(rows), dim3(512), 0, s, p);
+  else
+    hipLaunchKernelGGL((recur_bwd_kernel<IO, 64, 4, REV, Z, false, PARTS>), grid_of(rows * p.plan.S), dim3(256), 0, s, p);
+}
 
 template <typename IO, bool REV, bool Z>
 void go(const RecurParams& p, hipStream_t s) {
@@ -233,14 +271,10 @@ void go(const RecurParams& p, hipStream_t s) {
   };
   if (p.plan.lanes < 64) {
     p.plan.lanes == 1 ? few(IC<1>()) : p.plan.lanes == 4 ? few(IC<4>()) : p.plan.lanes == 16 ? few(IC<16>()) : few(IC<32>());
-  } else if (p.plan.waves == 1) {
-    hipLaunchKernelGGL((recur_bwd_kernel<IO, 64, 1, REV, Z, false>), grid_of((rows + 3) / 4), dim3(256), 0, s, p);
-  } else if (p.plan.waves == 8) {
-    hipLaunchKernelGGL((recur_bwd_kernel<IO, 64, 8, REV, Z, false>), grid_of(rows), dim3(512), 0, s, p);
   } else {
     if (p.plan.S > 1)
       hipLaunchKernelGGL((recur_bwd_kernel<IO, 64, 4, REV, Z, true>), grid_of(rows * (p.plan.S - 1)), dim3(256), 0, s, p);
-    hipLaunchKernelGGL((recur_bwd_kernel<IO, 64, 4, REV, Z, false>), grid_of(rows * p.plan.S), dim3(256), 0, s, p);
+    p.plan.parts > 1 ? waves<IO, REV, Z, true>(p, s) : waves<IO, REV, Z, false>(p, s);
   }
 }
 
@@ -254,11 +288,11 @@ void any(const RecurParams& p, bool reverse, hipStream_t s) {
 
 hipError_t launch_recur_bwd(const RecurParams& q, bool bf16, bool reverse, hipStream_t s) {
   RecurParams p = q;
-  p.whole = p.B == 1 && p.plan.S == 1;
+  p.whole = p.B == 1 && p.plan.S == 1 && p.plan.parts == 1;
   bf16 ? any<bf16_t>(p, reverse, s) : any<float>(p, reverse, s);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || p.whole) return e;
-  return launch_join({p.part, p.B * p.plan.S * p.plan.waves, p.D, 3, {p.ddecay, p.drb, p.dib}}, s);
+  return launch_join({p.part, p.B * p.plan.S * p.plan.waves * p.plan.parts, p.D, 3, {p.ddecay, p.drb, p.dib}}, s);
 }
 
 }  // namespace ssm

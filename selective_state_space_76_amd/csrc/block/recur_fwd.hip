@@ -235,6 +235,9 @@ RecurPlan recur_plan(int64_t B, int64_t D, int64_t L, bool bf16) {
       pl.S = (pl.tiles + pl.per - 1) / pl.per;
     }
   }
+  // 64 to 127 turns a partial sum
+  pl.parts = pl.per < 128 ? 1 : (int)(pl.per / 64);
+  pl.chain = (int)((pl.per + pl.parts - 1) / pl.parts);
   return pl;
 }
 

@@ -1,11 +1,11 @@
-"""The sums over the batch in the gradients of the gated linear recurrence (GPU): decay and biases, where very many
+"""The sums over batch and steps in the gradients of the gated linear recurrence (GPU): decay and biases, where very many
 terms of one sign are added."""
 import pytest
 import torch
 
-from selective_state_space_76_amd import recurrence_bwd
+from selective_state_space_76_amd import recurrence_bwd, recurrence_fwd
 from tests import block_ref as R
-from tests.gpu_util import rel_err, tol_for
+from tests.gpu_util import TOL_F32, rel_err, tol_for
 from tests.train_ref import f64
 
 pytestmark = pytest.mark.gpu
@@ -45,3 +45,54 @@ def test_large_batches(B, D, L, dtype):
     want = R.recurrence_grads(*[f64(t) for t in (x, r, i, decay, rb, ib)], None, None, f64(dout), None)
     for k in (*SUMS, "dx", "dr", "di"):
         assert rel_err(got[k], want[k]) <= tol_for(x), k
+
+
+@pytest.mark.parametrize("D,L", [(1, 1 << 28), (4096, 1 << 17)])
+def test_steps_alike(D, L):
+    """Long rows whose steps are all the same but for the first and the last hundred (the state forgets a third at each).  A
+    sum of any number of steps is off by 230 u (8 steps, 127 of those, lanes, 64 partial sums, 25 more); what a step adds is
+    taken from the difference between 4096 and 8192 of them, off by 40 u each (they take 8 turns), and so known to 120 u."""
+    print("case: sums of steps alike", D, L, flush=True)
+    a, b, got = alike(1, D, 4096), alike(1, D, 8192), alike(1, D, L)
+    for k in SUMS:
+        step = (b[k].double() - a[k].double()) / 4096
+        want = b[k].double() + (L - 8192) * step
+        assert float((got[k].double() / want - 1).abs().max()) <= 350 * U, k
+
+
+@pytest.mark.parametrize("reverse", [False, True], ids=["forward", "reverse"])
+@pytest.mark.parametrize("gate", [False, True], ids=["state", "gated"])
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("B,D", [(1, 300), (2, 1100), (1, 4099)])
+def test_long_rows_are_the_sum_of_their_pieces(B, D, dtype, gate, reverse):
+    """Teams of eight, four and one waves whose rows leave several partial sums: a row in one call, and in pieces that leave one
+    each, with the states and their gradients handed on."""
+    piece = (1 << (18 if dtype == BF16 else 17)) // (1 if D < 1000 else 2 if D < 4096 else 8)
+    L = 3 * piece + 4321
+    print("case: pieces of long rows", B, D, L, dtype, gate, reverse, flush=True)
+    g = torch.Generator(device=DEV).manual_seed(D)
+    rnd = lambda *s: torch.empty(s, device=DEV).normal_(generator=g)  # noqa: E731
+    x, r, i, dout, z = (rnd(B, D, L).to(dtype) for _ in range(5))
+    z = z if gate else None
+    decay, rb, ib = torch.exp(torch.rand(D, generator=g, device=DEV) * 3 - 3), rnd(D), rnd(D)
+    last, first = rnd(B, D), rnd(B, D)
+    whole = recurrence_bwd(x, r, i, decay, rb, ib, z, first, dout=dout, dfinal_state=last, reverse=reverse)
+    spans = [slice(k, min(k + piece, L)) for k in range(0, L, piece)]
+    if reverse:
+        spans.reverse()
+    cut = lambda t, s: None if t is None else t[..., s].contiguous()  # noqa: E731
+    states, h = [], first
+    for s in spans:
+        states.append(h)
+        h = recurrence_fwd(cut(x, s), cut(r, s), cut(i, s), decay, rb, ib, cut(z, s), h, reverse=reverse)[1]
+    sums, dh = {k: 0.0 for k in SUMS}, last
+    for s, h in reversed(list(zip(spans, states))):
+        got = recurrence_bwd(cut(x, s), cut(r, s), cut(i, s), decay, rb, ib, cut(z, s), h, dout=cut(dout, s),
+                             dfinal_state=dh, reverse=reverse)
+        dh = got["dinitial_state"]
+        for k in SUMS:
+            sums[k] = sums[k] + got[k].double()
+        assert rel_err(got["dx"][0, -1], whole["dx"][0, -1, s].double().cpu()) <= tol_for(x)
+    assert rel_err(dh, whole["dinitial_state"].double().cpu()) <= TOL_F32
+    for k in SUMS:
+        assert rel_err(whole[k], sums[k].cpu()) <= TOL_F32, k
