@@ -10,6 +10,7 @@ import ctypes
 import os
 
 import torch
+from torch.autograd.graph import increment_version
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libssmscan.so")
 
@@ -231,6 +232,14 @@ def _hand_out(stream, *tensors):
             t.record_stream(torch.cuda.current_stream(t.device))
 
 
+def _written(*tensors):
+    """The caller's own tensors that a call has written (None, True and False are none): autograd is told, so that an
+    operation that has kept one for its backward pass is refused and does not go on with other values."""
+    given = [t for t in tensors if isinstance(t, torch.Tensor)]
+    if given:
+        increment_version(given)
+
+
 def make_shape(batch, dim, dstate, seqlen, io_dtype, zoh=False, reverse=False) -> ssm_shape:
     flags = (SSM_FLAG_ZOH if zoh else 0) | (SSM_FLAG_REVERSE if reverse else 0)
     return ssm_shape(int(batch), int(dim), int(dstate), int(seqlen), int(io_dtype), flags)
@@ -264,7 +273,7 @@ def scan_fwd(u, delta, A, B, C, D=None, z=None, delta_bias=None, initial_state=N
     io = _io_dtype(u)
     device = u.device
     sh = make_shape(Bsz, Dm, N, L, io, zoh, reverse)
-    made = []  # tensors allocated here
+    given, made = (out, final_state, checkpoints), []  # the caller's tensors, those allocated here
     if out is None:
         out = _empty(u.shape, u.dtype, device, stream)
         made.append(out)
@@ -302,6 +311,7 @@ def scan_fwd(u, delta, A, B, C, D=None, z=None, delta_bias=None, initial_state=N
         _check(lib.ssm_scan_fwd_save(ctypes.byref(sh), _ptr(u), _ptr(delta), _ptr(A), _ptr(B), _ptr(C), _ptr(D),
                                      _ptr(z), _ptr(delta_bias), _ptr(initial_state), _ptr(out), _ptr(final_state),
                                      _ptr(checkpoints), _ptr(workspace), ws_bytes, _stream(stream, device)))
+    _written(*given)
     _hand_out(stream, *made)
     return out, final_state
 
@@ -334,6 +344,7 @@ def scan_fwd_noalloc(u, delta, A, B, C, D=None, z=None, delta_bias=None, initial
     _check(lib.ssm_scan_fwd_noalloc(ctypes.byref(sh), _ptr(u), _ptr(delta), _ptr(A), _ptr(B), _ptr(C), _ptr(D),
                                     _ptr(z), _ptr(delta_bias), _ptr(initial_state), _ptr(out), _ptr(final_state),
                                     _stream(stream, device)))
+    _written(out, final_state)
     return out, final_state
 
 
@@ -347,7 +358,7 @@ def state_update(state, u, delta, A, B, C, D=None, z=None, delta_bias=None, *, o
     _nonempty(batch=Bsz, dim=Dm, dstate=N)
     io = _io_dtype(u)
     device = u.device
-    made = []
+    given, made = (state, out), []
     if out is None:
         out = _empty(u.shape, u.dtype, device, stream)
         made.append(out)
@@ -360,6 +371,7 @@ def state_update(state, u, delta, A, B, C, D=None, z=None, delta_bias=None, *, o
     _check(lib.ssm_state_update(Bsz, Dm, N, io, SSM_FLAG_ZOH if zoh else 0, _ptr(state), _ptr(u), _ptr(delta),
                                 _ptr(A), _ptr(B), _ptr(C), _ptr(D), _ptr(z), _ptr(delta_bias), _ptr(out),
                                 _stream(stream, device)))
+    _written(*given)
     _hand_out(stream, *made)
     return out
 
@@ -426,6 +438,8 @@ def scan_bwd(u, delta, A, B, C, D=None, z=None, delta_bias=None, initial_state=N
     else:
         _check(lib.ssm_scan_bwd_saved(ctypes.byref(sh), *ins, _ptr(checkpoints), *outs, _ptr(workspace), ws_bytes,
                                       _stream(stream, device)))
+    if grads:
+        _written(*[g[k] for k in grads if k in shapes])
     _hand_out(stream, *made)
     return g
 
@@ -441,7 +455,7 @@ def conv1d_fwd(x, weight, bias=None, initial_state=None, *, out=None, final_stat
     _nonempty(batch=Bsz, dim=Dm, seqlen=L, width=K)
     io = _io_dtype(x)
     device = x.device
-    made = []
+    given, made = (out, final_state), []
     if out is None:
         out = _empty(x.shape, x.dtype, device, stream)
         made.append(out)
@@ -458,6 +472,7 @@ def conv1d_fwd(x, weight, bias=None, initial_state=None, *, out=None, final_stat
         _expect(t, shp, dt, name, device)
     _check(lib.ssm_conv1d_fwd(Bsz, Dm, L, K, io, _ptr(x), _ptr(weight), _ptr(bias), _ptr(initial_state),
                               _ptr(out), _ptr(final_state), _stream(stream, device)))
+    _written(*given)
     _hand_out(stream, *made)
     return out, final_state
 
@@ -471,7 +486,7 @@ def conv1d_update(conv_state, x, weight, bias=None, *, out=None, stream=None):
     _nonempty(batch=Bsz, dim=Dm, width=K)
     io = _io_dtype(x)
     device = x.device
-    made = []
+    given, made = (conv_state, out), []
     if out is None:
         out = _empty(x.shape, x.dtype, device, stream)
         made.append(out)
@@ -482,5 +497,6 @@ def conv1d_update(conv_state, x, weight, bias=None, *, out=None, stream=None):
         _expect(t, shp, dt, name, device)
     _check(lib.ssm_conv1d_update(Bsz, Dm, K, io, _ptr(conv_state), _ptr(x), _ptr(weight), _ptr(bias),
                                  _ptr(out), _stream(stream, device)))
+    _written(*given)
     _hand_out(stream, *made)
     return out

@@ -21,9 +21,10 @@ import ctypes
 from operator import index
 
 import torch
+from torch.autograd.graph import increment_version
 
-from ._lib import (SSM_BF16, SSM_FLAG_REVERSE, _check, _empty, _expect, _hand_out, _io_dtype, _nonempty, _ptr, load,
-                   ssm_dropout, ssm_norm_shape, ssm_recurrence_shape)
+from ._lib import (SSM_BF16, SSM_FLAG_REVERSE, _check, _empty, _expect, _hand_out, _io_dtype, _nonempty, _ptr, _written,
+                   load, ssm_dropout, ssm_norm_shape, ssm_recurrence_shape)
 from .training import SSM_FLAG_CHANNELS_FIRST, _KIND, _address, _capturing, _stream, _workspace
 
 SSM_FLAG_RMS = 4
@@ -98,6 +99,8 @@ def _dropout(x, mask, residual, dtype, out, stream):
     else:
         po = _arg(out, x.shape, dtype, "out", device)
     _check(load().ssm_dropout_fwd(n, *kinds, px, pr, mask, po, _stream(stream, device)))
+    if made is None:
+        _written(out)
     if stream is not None:
         _hand_out(stream, made)
     return out
@@ -146,13 +149,14 @@ def layer_norm_fwd(x, weight=None, bias=None, residual=None, *, eps=1e-5, rms=Fa
     plain = residual is None and mask is None
     if plain and hidden is not None:
         raise ValueError("hidden: without a residual and dropout it is x itself")
-    px, made = _address(x), []
+    px, given, made = _address(x), [], []
     if out is None:
         out = _like(x, xdt, stream)
         made.append(out)
         po = out.data_ptr()
     else:
         po = _arg(out, shape, xdt, "out", device)
+        given.append(out)
     if plain:
         ph, hidden = None, x
     elif hidden is None:
@@ -161,6 +165,7 @@ def layer_norm_fwd(x, weight=None, bias=None, residual=None, *, eps=1e-5, rms=Fa
         ph = hidden.data_ptr()
     else:
         ph = _arg(hidden, shape, hdt, "hidden", device)
+        given.append(hidden)
     if stats is None:
         stats = _empty((2, rows), f32, device, stream)
         made.append(stats)
@@ -168,7 +173,10 @@ def layer_norm_fwd(x, weight=None, bias=None, residual=None, *, eps=1e-5, rms=Fa
     else:
         stats = None if stats is False else stats
         pst = _arg(stats, (2, rows), f32, "stats", device)
+        given.append(stats)
     _check(load().ssm_layer_norm_fwd(sh, px, pw, pb, pr, eps, mask, po, ph, pst, _stream(stream, device)))
+    if given:
+        _written(*given)
     if stream is not None:
         _hand_out(stream, *made)
     return out, hidden, stats
@@ -214,6 +222,8 @@ def layer_norm_bwd(dout, hidden, weight, stats, *, dhidden=None, rms=False, chan
         workspace, ws_bytes = _workspace(workspace, lib.ssm_layer_norm_bwd_workspace_size(sh), device, stream)
         pws = _address(workspace)
     _check(lib.ssm_layer_norm_bwd(sh, pd, ph, pw, ps, pdh, mask, *to, pws, ws_bytes, _stream(stream, device)))
+    if grads:
+        _written(*[g[k] for k in grads if k in ("dx", "dresidual", "dweight", "dbias")])
     if stream is not None:
         _hand_out(stream, *made)
     if one:
@@ -265,7 +275,7 @@ def recurrence_fwd(x, r, i, decay, r_bias=None, i_bias=None, z=None, initial_sta
     checkpoints: an fp32 tensor of recurrence_checkpoints_shape(...) to write for recurrence_bwd."""
     lib = load()
     sh, B, D = _recurrence_shape(x, reverse)
-    device, made = x.device, []
+    device, given, made = x.device, (out, final_state, checkpoints), []
     ins = _recurrence_args(x, r, i, decay, r_bias, i_bias, z, initial_state, x.shape, (B, D), device)
     if out is None:
         out = _like(x, x.dtype, stream)
@@ -288,6 +298,7 @@ def recurrence_fwd(x, r, i, decay, r_bias=None, i_bias=None, z=None, initial_sta
         workspace, ws_bytes = _workspace(workspace, need, device, stream)
         pws = _address(workspace)
     _check(lib.ssm_recurrence_fwd(sh, *ins, po, pf, pc, pws, ws_bytes, _stream(stream, device)))
+    _written(*given)
     if stream is not None:
         _hand_out(stream, *made)
     return out, final_state
@@ -309,8 +320,9 @@ def recurrence_bwd(x, r, i, decay, r_bias=None, i_bias=None, z=None, initial_sta
         pc = _arg(checkpoints, (B, D, lib.ssm_recurrence_checkpoints(sh)), f32, "checkpoints", device)
     ins = _recurrence_args(x, r, i, decay, r_bias, i_bias, z, initial_state, full, (B, D), device)
     g, made, to = dict(grads) if grads else {}, [], []
-    for k, shp, d in (("dx", full, dt), ("dr", full, dt), ("di", full, dt), ("dz", full, dt), ("ddecay", (D,), f32),
-                      ("dr_bias", (D,), f32), ("di_bias", (D,), f32), ("dinitial_state", (B, D), f32)):
+    outs = (("dx", full, dt), ("dr", full, dt), ("di", full, dt), ("dz", full, dt), ("ddecay", (D,), f32),
+            ("dr_bias", (D,), f32), ("di_bias", (D,), f32), ("dinitial_state", (B, D), f32))
+    for k, shp, d in outs:
         t = g.get(k)
         if k == "dz" and z is None:
             g[k] = None
@@ -324,6 +336,8 @@ def recurrence_bwd(x, r, i, decay, r_bias=None, i_bias=None, z=None, initial_sta
     need = lib.ssm_recurrence_bwd_workspace_size(sh, 0 if pc is None else 1)
     workspace, ws_bytes = _workspace(workspace, need, device, stream)
     _check(lib.ssm_recurrence_bwd(sh, *ins, pd, pl, pc, *to, _address(workspace), ws_bytes, _stream(stream, device)))
+    if grads:
+        _written(*[g[k] for k, _, _ in outs if k in grads])
     if stream is not None:
         _hand_out(stream, *made)
     return g
@@ -346,6 +360,7 @@ def recurrence_update(state, x, r, i, decay, r_bias=None, i_bias=None, z=None, *
     else:
         po = _arg(out, size, dt, "out", device)
     _check(load().ssm_recurrence_update(B, D, io, ps, *ins[:7], po, _stream(stream, device)))
+    increment_version((state,) if made is not None else (state, out))  # (as _written(), in its cheapest form)
     if stream is not None:
         _hand_out(stream, made)
     return out

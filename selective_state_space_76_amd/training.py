@@ -22,8 +22,8 @@ import numpy as np
 import torch
 from torch.autograd.graph import increment_version
 
-from ._lib import (SSM_BF16, SSM_F32, SSMError, _check, _empty, _expect, _hand_out, _io_dtype, _nonempty, _ptr, load,
-                   ssm_adamw_config, ssm_embed_shape)
+from ._lib import (SSM_BF16, SSM_F32, SSMError, _check, _empty, _expect, _hand_out, _io_dtype, _nonempty, _ptr, _written,
+                   load, ssm_adamw_config, ssm_embed_shape)
 
 SSM_I32 = 0
 SSM_I64 = 1
@@ -114,6 +114,8 @@ def conv1d_bwd(x, weight, bias=None, initial_state=None, *, dout, dfinal_state=N
                               _address(initial_state), _address(dout), _address(dfinal_state), _address(g["dx"]),
                               _address(g["dweight"]), _address(g["dbias"]), _address(g["dinitial_state"]),
                               _address(workspace), ws_bytes, _stream(stream, device)))
+    if grads:
+        _written(*[g[k] for k in grads if k in ("dx", "dweight", "dbias", "dinitial_state")])
     _hand_out(stream, *made)
     return g
 
@@ -159,6 +161,8 @@ def embedding_fwd(tokens, weight, *, scale=1.0, dtype=None, channels_first=False
         _expect(weight, weight.shape, weight.dtype, "weight", device)
     _check(lib.ssm_embedding_fwd(ctypes.byref(sh), _address(tokens), _address(weight), scale, _address(out),
                                  _stream(stream, device)))
+    if made is None:
+        _written(out)
     _hand_out(stream, made)
     return out
 
@@ -194,6 +198,8 @@ def embedding_bwd(tokens, dout, rows, *, scale=1.0, channels_first=False, dtype=
     workspace, ws_bytes = _workspace(workspace, need, device, stream)
     _check(lib.ssm_embedding_bwd(ctypes.byref(sh), _address(tokens), _address(dout), scale, _address(dweight),
                                  _address(workspace), ws_bytes, _stream(stream, device)))
+    if made is None:
+        _written(dweight)
     _hand_out(stream, made)
     return dweight
 
