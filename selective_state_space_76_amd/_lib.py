@@ -165,6 +165,23 @@ def _check(status: int):
         raise SSMError(status, load().ssm_status_str(status).decode())
 
 
+def _current(device):
+    """Whether it is the current device (or none of the GPUs)."""
+    return device.index is None or device.index < 0 or device.index == torch._C._cuda_getDevice()
+
+
+def _launch(device, call, *args):
+    """The library's call, made while its tensors' device is the current one: the default stream has no number of its own,
+    and would be the current device's."""
+    if _current(device):
+        status = call(*args)
+    else:
+        with torch.cuda.device(device.index):
+            status = call(*args)
+    if status:
+        _check(status)
+
+
 def _io_dtype(t: torch.Tensor) -> int:
     if t.dtype == torch.float32:
         return SSM_F32
@@ -210,7 +227,14 @@ def _stream(stream, device):
     """The caller's stream, by default the current stream of the tensors' device."""
     if stream is None:
         stream = torch.cuda.current_stream(device)
+    else:
+        _of_device(stream, device)
     return ctypes.c_void_p(stream.cuda_stream)
+
+
+def _of_device(stream, device):
+    if getattr(device, "type", None) == "cuda" and stream.device != device:
+        raise ValueError("stream: expected one of %s, got one of %s" % (device, stream.device))
 
 
 def _empty(shape, dtype, device, stream):
@@ -304,13 +328,13 @@ def scan_fwd(u, delta, A, B, C, D=None, z=None, delta_bias=None, initial_state=N
     else:
         workspace = None
     if checkpoints is None:
-        _check(lib.ssm_scan_fwd(ctypes.byref(sh), _ptr(u), _ptr(delta), _ptr(A), _ptr(B), _ptr(C), _ptr(D),
-                                _ptr(z), _ptr(delta_bias), _ptr(initial_state), _ptr(out), _ptr(final_state),
-                                _ptr(workspace), ws_bytes, _stream(stream, device)))
+        _launch(device, lib.ssm_scan_fwd, ctypes.byref(sh), _ptr(u), _ptr(delta), _ptr(A), _ptr(B), _ptr(C), _ptr(D),
+                _ptr(z), _ptr(delta_bias), _ptr(initial_state), _ptr(out), _ptr(final_state), _ptr(workspace),
+                ws_bytes, _stream(stream, device))
     else:
-        _check(lib.ssm_scan_fwd_save(ctypes.byref(sh), _ptr(u), _ptr(delta), _ptr(A), _ptr(B), _ptr(C), _ptr(D),
-                                     _ptr(z), _ptr(delta_bias), _ptr(initial_state), _ptr(out), _ptr(final_state),
-                                     _ptr(checkpoints), _ptr(workspace), ws_bytes, _stream(stream, device)))
+        _launch(device, lib.ssm_scan_fwd_save, ctypes.byref(sh), _ptr(u), _ptr(delta), _ptr(A), _ptr(B), _ptr(C),
+                _ptr(D), _ptr(z), _ptr(delta_bias), _ptr(initial_state), _ptr(out), _ptr(final_state),
+                _ptr(checkpoints), _ptr(workspace), ws_bytes, _stream(stream, device))
     _written(*given)
     _hand_out(stream, *made)
     return out, final_state
@@ -341,9 +365,9 @@ def scan_fwd_noalloc(u, delta, A, B, C, D=None, z=None, delta_bias=None, initial
                              (out, (Bsz, Dm, L), u.dtype, "out"),
                              (final_state, (Bsz, Dm, N), f32, "final_state")):
         _expect(t, shp, dt, name, device)
-    _check(lib.ssm_scan_fwd_noalloc(ctypes.byref(sh), _ptr(u), _ptr(delta), _ptr(A), _ptr(B), _ptr(C), _ptr(D),
-                                    _ptr(z), _ptr(delta_bias), _ptr(initial_state), _ptr(out), _ptr(final_state),
-                                    _stream(stream, device)))
+    _launch(device, lib.ssm_scan_fwd_noalloc, ctypes.byref(sh), _ptr(u), _ptr(delta), _ptr(A), _ptr(B), _ptr(C),
+            _ptr(D), _ptr(z), _ptr(delta_bias), _ptr(initial_state), _ptr(out), _ptr(final_state),
+            _stream(stream, device))
     _written(out, final_state)
     return out, final_state
 
@@ -368,9 +392,9 @@ def state_update(state, u, delta, A, B, C, D=None, z=None, delta_bias=None, *, o
                              (D, (Dm,), f32, "D"), (z, (Bsz, Dm), u.dtype, "z"),
                              (delta_bias, (Dm,), f32, "delta_bias"), (out, (Bsz, Dm), u.dtype, "out")):
         _expect(t, shp, dt, name, device)
-    _check(lib.ssm_state_update(Bsz, Dm, N, io, SSM_FLAG_ZOH if zoh else 0, _ptr(state), _ptr(u), _ptr(delta),
-                                _ptr(A), _ptr(B), _ptr(C), _ptr(D), _ptr(z), _ptr(delta_bias), _ptr(out),
-                                _stream(stream, device)))
+    _launch(device, lib.ssm_state_update, Bsz, Dm, N, io, SSM_FLAG_ZOH if zoh else 0, _ptr(state), _ptr(u),
+            _ptr(delta), _ptr(A), _ptr(B), _ptr(C), _ptr(D), _ptr(z), _ptr(delta_bias), _ptr(out),
+            _stream(stream, device))
     _written(*given)
     _hand_out(stream, *made)
     return out
@@ -434,10 +458,11 @@ def scan_bwd(u, delta, A, B, C, D=None, z=None, delta_bias=None, initial_state=N
     ins = (_ptr(u), _ptr(delta), _ptr(A), _ptr(B), _ptr(C), _ptr(D), _ptr(z), _ptr(delta_bias),
            _ptr(initial_state), _ptr(dout), _ptr(dfinal_state))
     if checkpoints is None:
-        _check(lib.ssm_scan_bwd(ctypes.byref(sh), *ins, *outs, _ptr(workspace), ws_bytes, _stream(stream, device)))
+        _launch(device, lib.ssm_scan_bwd, ctypes.byref(sh), *ins, *outs, _ptr(workspace), ws_bytes,
+                _stream(stream, device))
     else:
-        _check(lib.ssm_scan_bwd_saved(ctypes.byref(sh), *ins, _ptr(checkpoints), *outs, _ptr(workspace), ws_bytes,
-                                      _stream(stream, device)))
+        _launch(device, lib.ssm_scan_bwd_saved, ctypes.byref(sh), *ins, _ptr(checkpoints), *outs, _ptr(workspace),
+                ws_bytes, _stream(stream, device))
     if grads:
         _written(*[g[k] for k in grads if k in shapes])
     _hand_out(stream, *made)
@@ -470,8 +495,8 @@ def conv1d_fwd(x, weight, bias=None, initial_state=None, *, out=None, final_stat
                              (out, (Bsz, Dm, L), x.dtype, "out"),
                              (final_state, (Bsz, Dm, K - 1), x.dtype, "final_state")):
         _expect(t, shp, dt, name, device)
-    _check(lib.ssm_conv1d_fwd(Bsz, Dm, L, K, io, _ptr(x), _ptr(weight), _ptr(bias), _ptr(initial_state),
-                              _ptr(out), _ptr(final_state), _stream(stream, device)))
+    _launch(device, lib.ssm_conv1d_fwd, Bsz, Dm, L, K, io, _ptr(x), _ptr(weight), _ptr(bias), _ptr(initial_state),
+            _ptr(out), _ptr(final_state), _stream(stream, device))
     _written(*given)
     _hand_out(stream, *made)
     return out, final_state
@@ -495,8 +520,8 @@ def conv1d_update(conv_state, x, weight, bias=None, *, out=None, stream=None):
                              (weight, (Dm, K), f32, "weight"), (bias, (Dm,), f32, "bias"),
                              (out, (Bsz, Dm), x.dtype, "out")):
         _expect(t, shp, dt, name, device)
-    _check(lib.ssm_conv1d_update(Bsz, Dm, K, io, _ptr(conv_state), _ptr(x), _ptr(weight), _ptr(bias),
-                                 _ptr(out), _stream(stream, device)))
+    _launch(device, lib.ssm_conv1d_update, Bsz, Dm, K, io, _ptr(conv_state), _ptr(x), _ptr(weight), _ptr(bias),
+            _ptr(out), _stream(stream, device))
     _written(*given)
     _hand_out(stream, *made)
     return out

@@ -23,9 +23,9 @@ from operator import index
 import torch
 from torch.autograd.graph import increment_version
 
-from ._lib import (SSM_BF16, SSM_FLAG_REVERSE, _check, _empty, _expect, _hand_out, _io_dtype, _nonempty, _ptr, _written,
+from ._lib import (SSM_BF16, SSM_FLAG_REVERSE, _empty, _expect, _hand_out, _io_dtype, _launch, _nonempty, _ptr, _written,
                    load, ssm_dropout, ssm_norm_shape, ssm_recurrence_shape)
-from .training import SSM_FLAG_CHANNELS_FIRST, _KIND, _address, _capturing, _stream, _workspace
+from .training import SSM_FLAG_CHANNELS_FIRST, _KIND, _address, _capturing, _queue, _stream, _workspace
 
 SSM_FLAG_RMS = 4
 _NONE = 0xFFFFFFFFFFFFFFFF
@@ -65,7 +65,7 @@ def _mask(p, seed, call, device, stream, fresh):
         if seed.device != device:
             _expect(seed, seed.shape, seed.dtype, "seed", device)
         return ssm_dropout(p, 0, _ptr(seed), index(call) & _NONE)
-    if fresh and _capturing(stream):
+    if fresh and _capturing(_queue(stream, device)):
         raise RuntimeError("every replay would repeat this call's mask: give the seed as a tensor on the device")
     return ssm_dropout(p, index(seed) & _NONE, None, index(call) & _NONE)  # (numpy's integers, too)
 
@@ -98,7 +98,7 @@ def _dropout(x, mask, residual, dtype, out, stream):
         po = out.data_ptr()
     else:
         po = _arg(out, x.shape, dtype, "out", device)
-    _check(load().ssm_dropout_fwd(n, *kinds, px, pr, mask, po, _stream(stream, device)))
+    _launch(device, load().ssm_dropout_fwd, n, *kinds, px, pr, mask, po, _stream(stream, device))
     if made is None:
         _written(out)
     if stream is not None:
@@ -174,7 +174,7 @@ def layer_norm_fwd(x, weight=None, bias=None, residual=None, *, eps=1e-5, rms=Fa
         stats = None if stats is False else stats
         pst = _arg(stats, (2, rows), f32, "stats", device)
         given.append(stats)
-    _check(load().ssm_layer_norm_fwd(sh, px, pw, pb, pr, eps, mask, po, ph, pst, _stream(stream, device)))
+    _launch(device, load().ssm_layer_norm_fwd, sh, px, pw, pb, pr, eps, mask, po, ph, pst, _stream(stream, device))
     if given:
         _written(*given)
     if stream is not None:
@@ -221,7 +221,8 @@ def layer_norm_bwd(dout, hidden, weight, stats, *, dhidden=None, rms=False, chan
     if to[2] is not None or to[3] is not None:
         workspace, ws_bytes = _workspace(workspace, lib.ssm_layer_norm_bwd_workspace_size(sh), device, stream)
         pws = _address(workspace)
-    _check(lib.ssm_layer_norm_bwd(sh, pd, ph, pw, ps, pdh, mask, *to, pws, ws_bytes, _stream(stream, device)))
+    _launch(device, lib.ssm_layer_norm_bwd, sh, pd, ph, pw, ps, pdh, mask, *to, pws, ws_bytes,
+            _stream(stream, device))
     if grads:
         _written(*[g[k] for k in grads if k in ("dx", "dresidual", "dweight", "dbias")])
     if stream is not None:
@@ -297,7 +298,7 @@ def recurrence_fwd(x, r, i, decay, r_bias=None, i_bias=None, z=None, initial_sta
     if need or workspace is not None:
         workspace, ws_bytes = _workspace(workspace, need, device, stream)
         pws = _address(workspace)
-    _check(lib.ssm_recurrence_fwd(sh, *ins, po, pf, pc, pws, ws_bytes, _stream(stream, device)))
+    _launch(device, lib.ssm_recurrence_fwd, sh, *ins, po, pf, pc, pws, ws_bytes, _stream(stream, device))
     _written(*given)
     if stream is not None:
         _hand_out(stream, *made)
@@ -335,7 +336,8 @@ def recurrence_bwd(x, r, i, decay, r_bias=None, i_bias=None, z=None, initial_sta
             to.append(_arg(t, shp, d, k, device))
     need = lib.ssm_recurrence_bwd_workspace_size(sh, 0 if pc is None else 1)
     workspace, ws_bytes = _workspace(workspace, need, device, stream)
-    _check(lib.ssm_recurrence_bwd(sh, *ins, pd, pl, pc, *to, _address(workspace), ws_bytes, _stream(stream, device)))
+    _launch(device, lib.ssm_recurrence_bwd, sh, *ins, pd, pl, pc, *to, _address(workspace), ws_bytes,
+            _stream(stream, device))
     if grads:
         _written(*[g[k] for k, _, _ in outs if k in grads])
     if stream is not None:
@@ -359,7 +361,7 @@ def recurrence_update(state, x, r, i, decay, r_bias=None, i_bias=None, z=None, *
         po = out.data_ptr()
     else:
         po = _arg(out, size, dt, "out", device)
-    _check(load().ssm_recurrence_update(B, D, io, ps, *ins[:7], po, _stream(stream, device)))
+    _launch(device, load().ssm_recurrence_update, B, D, io, ps, *ins[:7], po, _stream(stream, device))
     increment_version((state,) if made is not None else (state, out))  # (as _written(), in its cheapest form)
     if stream is not None:
         _hand_out(stream, made)

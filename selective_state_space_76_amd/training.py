@@ -22,8 +22,8 @@ import numpy as np
 import torch
 from torch.autograd.graph import increment_version
 
-from ._lib import (SSM_BF16, SSM_F32, SSMError, _check, _empty, _expect, _hand_out, _io_dtype, _nonempty, _ptr, _written,
-                   load, ssm_adamw_config, ssm_embed_shape)
+from ._lib import (SSM_BF16, SSM_F32, SSMError, _current, _empty, _expect, _hand_out, _io_dtype, _launch, _nonempty,
+                   _of_device, _ptr, _written, load, ssm_adamw_config, ssm_embed_shape)
 
 SSM_I32 = 0
 SSM_I64 = 1
@@ -59,7 +59,10 @@ def _want(t, shape, dtype, name, device):
 
 def _stream(stream, device):
     """The caller's stream, by default the current one of the tensors' device, as the number the library takes."""
-    return torch._C._cuda_getCurrentRawStream(device.index) if stream is None else stream.cuda_stream
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(device.index)
+    _of_device(stream, device)
+    return stream.cuda_stream
 
 
 def _capturing(stream):
@@ -67,6 +70,11 @@ def _capturing(stream):
         return torch.cuda.is_current_stream_capturing()
     with torch.cuda.stream(stream):
         return torch.cuda.is_current_stream_capturing()
+
+
+def _queue(stream, device):
+    """The stream to ask about: the caller's, or, of another device than the current one, that device's current one."""
+    return stream if stream is not None or _current(device) else torch.cuda.current_stream(device)
 
 
 def _workspace(workspace, need, device, stream):
@@ -110,10 +118,10 @@ def conv1d_bwd(x, weight, bias=None, initial_state=None, *, dout, dfinal_state=N
         else:
             _want(g[k], shp, dt, k, device)
     workspace, ws_bytes = _workspace(workspace, lib.ssm_conv1d_bwd_workspace_size(Bsz, Dm, L, K, io), device, stream)
-    _check(lib.ssm_conv1d_bwd(Bsz, Dm, L, K, io, _address(x), _address(weight), _address(bias),
-                              _address(initial_state), _address(dout), _address(dfinal_state), _address(g["dx"]),
-                              _address(g["dweight"]), _address(g["dbias"]), _address(g["dinitial_state"]),
-                              _address(workspace), ws_bytes, _stream(stream, device)))
+    _launch(device, lib.ssm_conv1d_bwd, Bsz, Dm, L, K, io, _address(x), _address(weight), _address(bias),
+            _address(initial_state), _address(dout), _address(dfinal_state), _address(g["dx"]),
+            _address(g["dweight"]), _address(g["dbias"]), _address(g["dinitial_state"]), _address(workspace),
+            ws_bytes, _stream(stream, device))
     if grads:
         _written(*[g[k] for k in grads if k in ("dx", "dweight", "dbias", "dinitial_state")])
     _hand_out(stream, *made)
@@ -159,8 +167,8 @@ def embedding_fwd(tokens, weight, *, scale=1.0, dtype=None, channels_first=False
         _want(out, shape, dtype, "out", device)
     if weight.device != device:
         _expect(weight, weight.shape, weight.dtype, "weight", device)
-    _check(lib.ssm_embedding_fwd(ctypes.byref(sh), _address(tokens), _address(weight), scale, _address(out),
-                                 _stream(stream, device)))
+    _launch(device, lib.ssm_embedding_fwd, ctypes.byref(sh), _address(tokens), _address(weight), scale, _address(out),
+            _stream(stream, device))
     if made is None:
         _written(out)
     _hand_out(stream, made)
@@ -196,8 +204,8 @@ def embedding_bwd(tokens, dout, rows, *, scale=1.0, channels_first=False, dtype=
     _want(dweight, (rows, dim), dtype, "dweight", device)
     need = int(lib.ssm_embedding_bwd_workspace_size(ctypes.byref(sh)))
     workspace, ws_bytes = _workspace(workspace, need, device, stream)
-    _check(lib.ssm_embedding_bwd(ctypes.byref(sh), _address(tokens), _address(dout), scale, _address(dweight),
-                                 _address(workspace), ws_bytes, _stream(stream, device)))
+    _launch(device, lib.ssm_embedding_bwd, ctypes.byref(sh), _address(tokens), _address(dout), scale,
+            _address(dweight), _address(workspace), ws_bytes, _stream(stream, device))
     if made is None:
         _written(dweight)
     _hand_out(stream, made)
@@ -358,23 +366,24 @@ class AdamW:
                                self.seed & (2 ** 64 - 1), self.state_bits, 0)
         if self.max_grad_norm is not None:
             if self._count is not None:
-                if _capturing(stream):
+                if _capturing(_queue(stream, self.device)):
                     raise RuntimeError("the steps so far were counted on the host: make one step with max_grad_norm "
                                        "before the capture")
                 self._count_on_device(stream)
             norm = _empty((), torch.float32, self.device, stream)
             need = int(lib.ssm_grad_norm_workspace_size(rows, count))
             workspace = _empty(need, torch.uint8, self.device, stream)
-            _check(lib.ssm_adamw_clipped_step(ctypes.byref(cfg), rows, count, float(self.max_grad_norm), *states,
-                                              _address(self._progress), _address(norm), _address(workspace), need, s))
+            _launch(self.device, lib.ssm_adamw_clipped_step, ctypes.byref(cfg), rows, count,
+                    float(self.max_grad_norm), *states, _address(self._progress), _address(norm), _address(workspace),
+                    need, s)
         else:
-            if _capturing(stream):
+            if _capturing(_queue(stream, self.device)):
                 raise RuntimeError("without max_grad_norm every replay would repeat this step's number: set it "
                                    "(math.inf: no clipping) for steps in a graph")
             if self._count is None:
                 self._count = self.step_count
             cfg.step = self._count + 1
-            _check(lib.ssm_adamw_step(ctypes.byref(cfg), rows, count, *states, None, s))
+            _launch(self.device, lib.ssm_adamw_step, ctypes.byref(cfg), rows, count, *states, None, s)
             self._count += 1
         # a graph that has kept a parameter for its backward pass must be refused from now on
         increment_version(self.params if all(have) else [p for p, h in zip(self.params, have) if h])
@@ -391,9 +400,9 @@ class AdamW:
             return st["exp_avg"], st["exp_avg_sq"]
         m = _empty(self.numel, torch.bfloat16, self.device, stream)
         v = _empty(self.numel, torch.bfloat16, self.device, stream)
-        _check(load().ssm_adamw_state_values(self.numel, _address(st["exp_avg"]), _address(st["exp_avg_sq"]),
-                                             _address(st["exp_avg_base"]), _address(st["exp_avg_sq_base"]), _address(m),
-                                             _address(v), _stream(stream, self.device)))
+        _launch(self.device, load().ssm_adamw_state_values, self.numel, _address(st["exp_avg"]),
+                _address(st["exp_avg_sq"]), _address(st["exp_avg_base"]), _address(st["exp_avg_sq_base"]),
+                _address(m), _address(v), _stream(stream, self.device))
         if stream is not None:
             self._used_on(stream)
             _hand_out(stream, m, v)
