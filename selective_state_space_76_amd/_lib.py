@@ -165,18 +165,14 @@ def _check(status: int):
         raise SSMError(status, load().ssm_status_str(status).decode())
 
 
-def _current(device):
-    """Whether it is the current device (or none of the GPUs)."""
-    return device.index is None or device.index < 0 or device.index == torch._C._cuda_getDevice()
-
-
 def _launch(device, call, *args):
     """The library's call, made while its tensors' device is the current one: the default stream has no number of its own,
     and would be the current device's."""
-    if _current(device):
+    index = device.index
+    if index is None or index < 0 or index == torch._C._cuda_getDevice():
         status = call(*args)
     else:
-        with torch.cuda.device(device.index):
+        with torch.cuda.device(index):
             status = call(*args)
     if status:
         _check(status)

@@ -21,7 +21,6 @@ import ctypes
 from operator import index
 
 import torch
-from torch.autograd.graph import increment_version
 
 from ._lib import (SSM_BF16, SSM_FLAG_REVERSE, _empty, _expect, _hand_out, _io_dtype, _launch, _nonempty, _ptr, _written,
                    load, ssm_dropout, ssm_norm_shape, ssm_recurrence_shape)
@@ -45,9 +44,10 @@ def _arg(t, shape, dtype, name, device):
 
 
 def _like(t, dtype, stream):
-    """An uninitialised tensor of t's shape; torch's quicker call where the dtype and the stream allow it."""
+    """An uninitialised tensor of t's shape; torch's quicker call where the dtype and the stream allow it.  (t is contiguous,
+    or its call is refused.)"""
     if stream is None and dtype == t.dtype:
-        return torch.empty_like(t, memory_format=torch.contiguous_format)
+        return torch.empty_like(t)
     return _empty(t.shape, dtype, t.device, stream)
 
 
@@ -59,13 +59,13 @@ def _mask(p, seed, call, device, stream, fresh):
         raise ValueError("p must be in [0, 1], got %r" % (p,))
     if seed is None:
         raise ValueError("dropout needs a seed")
-    if isinstance(seed, torch.Tensor):
+    if type(seed) is not int and isinstance(seed, torch.Tensor):
         if seed.dtype != torch.int64 or seed.numel() != 1:
             raise TypeError("seed: expected an int or one int64 on the device, got %s of %d" % (seed.dtype, seed.numel()))
         if seed.device != device:
             _expect(seed, seed.shape, seed.dtype, "seed", device)
         return ssm_dropout(p, 0, _ptr(seed), index(call) & _NONE)
-    if fresh and _capturing(_queue(stream, device)):
+    if fresh and _capturing(stream if device.index is None else _queue(stream, device.index)):
         raise RuntimeError("every replay would repeat this call's mask: give the seed as a tensor on the device")
     return ssm_dropout(p, index(seed) & _NONE, None, index(call) & _NONE)  # (numpy's integers, too)
 
@@ -89,16 +89,16 @@ def _dropout(x, mask, residual, dtype, out, stream):
     n, device, made = x.numel(), x.device, None
     if n < 1:
         _nonempty(numel=n)
-    kinds = _KIND.get(x.dtype), _KIND.get(dtype)
-    if None in kinds:
-        raise TypeError("streams must be float32 or bfloat16, got %s" % (x.dtype if kinds[0] is None else dtype))
-    px, pr = _address(x), _arg(residual, x.shape, dtype, "residual", device)
+    kx, ko = _KIND.get(x.dtype), _KIND.get(dtype)
+    if kx is None or ko is None:
+        raise TypeError("streams must be float32 or bfloat16, got %s" % (x.dtype if kx is None else dtype))
+    px, pr = _address(x), None if residual is None else _arg(residual, x.shape, dtype, "residual", device)
     if out is None:
         out = made = _like(x, dtype, stream)
         po = out.data_ptr()
     else:
         po = _arg(out, x.shape, dtype, "out", device)
-    _launch(device, load().ssm_dropout_fwd, n, *kinds, px, pr, mask, po, _stream(stream, device))
+    _launch(device, load().ssm_dropout_fwd, n, kx, ko, px, pr, mask, po, _stream(stream, device))
     if made is None:
         _written(out)
     if stream is not None:
@@ -353,16 +353,22 @@ def recurrence_update(state, x, r, i, decay, r_bias=None, i_bias=None, z=None, *
     B, D = size = x.shape
     if B < 1 or D < 1:
         _nonempty(batch=B, dim=D)
-    io, device, dt, made = _io_dtype(x), x.device, x.dtype, None
-    ps = _arg(state, size, torch.float32, "state", device)
-    ins = _recurrence_args(x, r, i, decay, r_bias, i_bias, z, None, size, size, device)
+    device, dt, f32, made = x.device, x.dtype, torch.float32, None
+    io = _KIND.get(dt)
+    if io is None:
+        _io_dtype(x)
+    ps = _arg(state, size, f32, "state", device)
+    ins = (_arg(r, size, dt, "r", device), _arg(i, size, dt, "i", device), _arg(decay, (D,), f32, "decay", device),
+           _arg(r_bias, (D,), f32, "r_bias", device), _arg(i_bias, (D,), f32, "i_bias", device),
+           _arg(z, size, dt, "z", device))
+    px = _address(x)
     if out is None:
         out = made = _like(x, dt, stream)
         po = out.data_ptr()
     else:
         po = _arg(out, size, dt, "out", device)
-    _launch(device, load().ssm_recurrence_update, B, D, io, ps, *ins[:7], po, _stream(stream, device))
-    increment_version((state,) if made is not None else (state, out))  # (as _written(), in its cheapest form)
+    _launch(device, load().ssm_recurrence_update, B, D, io, ps, px, *ins, po, _stream(stream, device))
+    torch._C._increment_version((state,) if made is not None else (state, out))  # (_written() in its cheapest form)
     if stream is not None:
         _hand_out(stream, made)
     return out

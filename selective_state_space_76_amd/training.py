@@ -22,7 +22,7 @@ import numpy as np
 import torch
 from torch.autograd.graph import increment_version
 
-from ._lib import (SSM_BF16, SSM_F32, SSMError, _current, _empty, _expect, _hand_out, _io_dtype, _launch, _nonempty,
+from ._lib import (SSM_BF16, SSM_F32, SSMError, _empty, _expect, _hand_out, _io_dtype, _launch, _nonempty,
                    _of_device, _ptr, _written, load, ssm_adamw_config, ssm_embed_shape)
 
 SSM_I32 = 0
@@ -72,9 +72,11 @@ def _capturing(stream):
         return torch.cuda.is_current_stream_capturing()
 
 
-def _queue(stream, device):
+def _queue(stream, index):
     """The stream to ask about: the caller's, or, of another device than the current one, that device's current one."""
-    return stream if stream is not None or _current(device) else torch.cuda.current_stream(device)
+    if stream is not None or index < 0 or index == torch._C._cuda_getDevice():
+        return stream
+    return torch.cuda.current_stream(index)
 
 
 def _workspace(workspace, need, device, stream):
@@ -366,7 +368,7 @@ class AdamW:
                                self.seed & (2 ** 64 - 1), self.state_bits, 0)
         if self.max_grad_norm is not None:
             if self._count is not None:
-                if _capturing(_queue(stream, self.device)):
+                if _capturing(_queue(stream, self.device.index)):
                     raise RuntimeError("the steps so far were counted on the host: make one step with max_grad_norm "
                                        "before the capture")
                 self._count_on_device(stream)
@@ -377,7 +379,7 @@ class AdamW:
                     float(self.max_grad_norm), *states, _address(self._progress), _address(norm), _address(workspace),
                     need, s)
         else:
-            if _capturing(_queue(stream, self.device)):
+            if _capturing(_queue(stream, self.device.index)):
                 raise RuntimeError("without max_grad_norm every replay would repeat this step's number: set it "
                                    "(math.inf: no clipping) for steps in a graph")
             if self._count is None:

@@ -46,7 +46,8 @@ def two(monkeypatch):
     monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: r.now, raising=False)
     monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda index: 0, raising=False)
     monkeypatch.setattr(torch.cuda, "device", on)
-    monkeypatch.setattr(torch.cuda, "current_stream", lambda d=None: SimpleNamespace(cuda_stream=0, device=d))
+    stream = lambda d=0: SimpleNamespace(cuda_stream=0, device=torch.device("cuda", d) if isinstance(d, int) else d)  # noqa: E731
+    monkeypatch.setattr(torch.cuda, "current_stream", stream)
     monkeypatch.setattr(torch.cuda, "stream", lambda s: contextlib.nullcontext() if s is None else on(s.device))
     monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: r.now == 1)  # only the second device's is
     monkeypatch.setattr(torch.Tensor, "record_stream", lambda t, s: None)
