@@ -11,7 +11,8 @@
 // (about the mean, no cancellation).  out is made from the unrounded sum; the hidden that is kept for the backward
 // pass is rounded to its type.  Where E is no multiple of 8 a row's pieces begin up to 7 elements before it, at a
 // multiple of 16 bytes (16384 x 767 in bf16 with a residual: 27.7 us; with pieces that begin where the row does 38.7).
-// Longer rows than a workgroup holds go through memory again for each pass.
+// Rows that a workgroup does not hold (forward more than 16384 elements, backward more than 8192, one piece a lane; 16377
+// and 8185 where E is no multiple of 8) go through memory again for each pass.
 //
 // A lane holds one piece, two above 4096 elements: a row's loads are then all in flight at once, few instructions stand
 // between them and the stores, and what a call of few rows takes is one pass through a short kernel (256 x 2560: 3.5 us;
@@ -21,6 +22,7 @@
 // registers and gave 33, 49 and 141.
 //
 // Backward: 16384 x 768 as above, with the stream's own gradient (201 MB): 39 us, 5.3 TB/s, and 6 for the join of the sums.
+// Odd widths over 512 keep up to 12 registers in scratch memory, the other forms none.
 #include "block_device.h"
 
 namespace ssm {
@@ -458,8 +460,8 @@ void fwd(const NormParams& p, hipStream_t s) {
 // same number on each (16384 x 5000, 10 waves a row: 84 us with 512, 117 and 100 with 256 and 768), and where the
 // rows are fewer, up to 12 rows in turn rather than more sums (16384 x 768: 39 us with 1366, 41.6 with 2048, 51 with
 // 4096), but 512 at least.  A multiple of 8 where E is none.  A plain sum over rows in turn is off by up to their number of
-// half steps: of very many rows, each launch takes kTurns (more workgroups instead, of which not all are resident at
-// once: 2^20 x 768 1058 us, 961 so).  Rows that no team holds: groups of rows in one launch.
+// half steps: of very many rows, each launch takes kTurns (2^20 x 768: 1.19 ms; more workgroups instead, of which not all
+// are resident at once, take a tenth more).  Rows that no team holds: groups of rows in one launch.
 struct BwdPlan {
   int64_t groups, launches;
 };

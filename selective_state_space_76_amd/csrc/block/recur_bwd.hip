@@ -8,16 +8,17 @@
 // Bound by HBM: x, r, i, dout (and z) are read once, their gradients written once (14 or 18 bytes a step in bf16).  The
 // states are made again from the checkpoints of the forward pass, one for every 64 pieces, so that a wave needs no
 // other's; the adjoint F is an affine recurrence against time, walked as the forward pass walks the states (teams of
-// waves through LDS, segments for few rows).  ddecay and the biases' gradients are summed per wave and joined by a
-// second kernel in a fixed order, or at once where a channel is one team's (1 x 509 x 262147: 401 -> 391 us).
+// waves through LDS, segments for few rows).  ddecay and the biases' gradients are summed per wave and joined in a fixed
+// order (join.hip), or at once where a channel is one team's (1 x 509 x 262147: 401 -> 391 us).
 // 8 x 1536 x 2048: 98 us a call, 18 bytes a step, 4.6 TB/s; workgroups of 8 waves instead of 4 take 112, and 123 where
 // they are the rows of a channel, whose sums then need no second kernel.
 #include "recur_device.h"
 
 namespace ssm {
 
-// Z: there is a gate.  MAPS: the segments' maps of the adjoint.  PARTS: a segment leaves several partial sums (apart from the
-// others for its registers: 1 x 509 x 262147 394 us, 405 with it).
+// Z: there is a gate.  MAPS: the segments' maps of the adjoint.  PARTS: a segment leaves several partial sums, of turns that
+// are summed by themselves (apart from the others for its registers: 1 x 509 x 262147 394 us, 405 with it; 1 x 100 x 200000
+// in reverse 136 and 147).
 template <typename IO, int LN, int W, bool REV, bool Z, bool MAPS, bool PARTS = false>
 __global__ __launch_bounds__(W > 4 ? W * 64 : 256, Z || (REV && PARTS) || LN < 64 ? 3 : 4)
 void recur_bwd_kernel(RecurParams p) {
@@ -70,8 +71,8 @@ void recur_bwd_kernel(RecurParams p) {
       hn = p.ckpt[row * p.plan.blocks + (block < p.plan.blocks ? block : p.plan.blocks - 1)];
     }
   };
-  // The lane's sums, of p.plan.chain turns at the most: then they become a partial sum (a plain chain of 2^14 terms of one
-  // sign was off by 5e-5; compensated in registers or LDS the sums cost long rows up to 9 and 28%).
+  // The lane's sums, of p.plan.chain turns (127 at the most): then they become a partial sum.  (A plain chain of 2^14 terms
+  // of one sign was off by 5e-5; compensated in registers or LDS the sums cost long rows up to 9 and 28%.)
   float sd = 0.0f, sr = 0.0f, si = 0.0f;
   int left = p.plan.chain, parts = 0;
   auto part = [&] { return p.part + (((b * p.plan.S + seg) * W + w) * (PARTS ? p.plan.parts : 1) + parts) * 3 * p.D + d; };
@@ -169,7 +170,7 @@ void recur_bwd_kernel(RecurParams p) {
     }
     // (gradients with respect to what the sigmoids take; where a is 1 to the last bit, with sig(r) under 2^-100 / decay,
     // what 1 / q meets is zero)
-    float td = 0.0f, tr = 0.0f, ti = 0.0f;  // the turn's
+    float td = PARTS ? 0.0f : sd, tr = PARTS ? 0.0f : sr, ti = PARTS ? 0.0f : si;  // the turn's
 #pragma unroll
     for (int e = 0; e < V; ++e) {
       const float gs = g[e] * sgi[e], x = slot<IO, REV>(xq, e);
@@ -182,9 +183,9 @@ void recur_bwd_kernel(RecurParams p) {
       g[e] = o[e] * x * (1.0f - sgi[e]);
       ti += g[e];
     }
-    sd += td;
-    sr += tr;
-    si += ti;
+    sd = PARTS ? sd + td : td;
+    sr = PARTS ? sr + tr : tr;
+    si = PARTS ? si + ti : ti;
     store_slots<IO, REV>(p.dx, at, lo, hi, edge, o);
     store_slots<IO, REV>(p.dr, at, lo, hi, edge, hb);
     store_slots<IO, REV>(p.di, at, lo, hi, edge, g);
