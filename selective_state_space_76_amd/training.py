@@ -6,8 +6,9 @@
     opt = AdamW(params, lr=1e-4, weight_decay=0.1, state_bits=8, max_grad_norm=1.0)
     opt.step()
 
-stream=: the kernels' stream, by default the current one.  To order it with the work that made the inputs (an AdamW
-included) and with what uses the outputs is the caller's part, as with every stream.
+stream=: the kernels' stream, by default the current one of the tensors' device; one of another device is refused.  To order
+it with the work that made the inputs (an AdamW included) and with what uses the outputs is the caller's part, as with
+every stream.
 
 As in _lib.py this is argument marshalling: the arithmetic runs in the library's HIP kernels (see
 include/ssm_scan.h for the formulas and layouts), and nothing falls back to anything else.
